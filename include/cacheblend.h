@@ -58,7 +58,7 @@ extern "C" {
 #define CB_ERR_SHAPE        2   /* sizes inconsistent with each other or the dims      */
 #define CB_ERR_DTYPE        3   /* unsupported element type                            */
 #define CB_ERR_WORKSPACE    4   /* workspace smaller than cb_workspace_bytes() asks    */
-#define CB_ERR_NONFINITE    5   /* NaN/Inf deviation score (reported by cb_sync)       */
+#define CB_ERR_NONFINITE    5   /* NaN/Inf score, cache row or logit (by cb_sync)      */
 #define CB_ERR_CUDA         6   /* a CUDA runtime/driver call failed                   */
 #define CB_ERR_TIMEOUT      7   /* cb_sync waited longer than its limit                */
 #define CB_ERR_UNSUPPORTED  8   /* a shape the kernels do not handle (see message)     */
@@ -204,6 +204,94 @@ int cb_rope_shift_q8(void* k_dst, void* v_dst, const uint8_t* k_codes, const uin
                      const float* v_zero, const int32_t* src_row, int64_t n_src_rows,
                      const int32_t* qrow, int32_t n_qrows, const int32_t* delta, int64_t n_rows,
                      const cb_dims* dims, const float* cos_sin, int32_t max_pos, void* stream);
+
+/* ---- 8-bit KV cache of an answer in progress ---------------------------------------- */
+
+/* A layer's KV cache in 8 bits, one fp32 scale per block of `block` rows and KV head (K and V
+ * each): value = code * scale, codes in [-127, 127].  Unlike the chunk store above it grows
+ * row by row and is read by attention directly.  The caller owns the buffers; sequence s,
+ * KV head h, row i sits at ((s * Hkv + h) * capacity + i) * head_dim (head-major: a head's
+ * rows are contiguous), its scale at (s * Hkv + h) * (capacity / block) + i / block.
+ * A row index counts the rows a sequence holds; after an eviction it is no longer the token's
+ * position (keys keep the rotation they were stored with). */
+typedef struct {
+    int8_t* k_codes;    /* [n_seq, Hkv, capacity, head_dim], 16-byte aligned (all four)     */
+    int8_t* v_codes;
+    float*  k_scale;    /* [n_seq, Hkv, capacity / block]                                   */
+    float*  v_scale;
+    int64_t capacity;   /* rows per sequence and head: a multiple of block, below 2^31      */
+    int32_t n_seq;      /* 1..65535                                                         */
+    int32_t block;      /* 16, 32, 64 or 128                                                */
+} cb_kv8_cache;
+
+/* Appends rows to every sequence: new row j of sequence s becomes cache row start[s] + j.
+ *   k, v  : [n_seq, n_rows, Hkv hd] of dims->dtype (k already rotated)
+ *   start : [n_seq] int32, the rows the sequence already holds; -1: the sequence is idle
+ *   count : [n_seq] int32 new rows per sequence in [0, n_rows], or NULL (n_rows each); the
+ *           rows of k and v past it are not read
+ * A block that held no row gets scale max(amax / 127, 1e-8) (fp32 division, amax over the
+ * new rows of that block and head).  A block that already holds rows keeps its scale unless
+ * the new rows need a larger one; then its older codes c become the integer nearest to
+ * c * old / new.  A new code is the integer nearest to x / scale (ties to even; the nearest
+ * integer is decided exactly, without a rounding of the quotient).  Rows from
+ * start[s] + n on count as unused: their codes are left as they were, the scale of the block
+ * they share with the last new row is not.
+ * Rows past the capacity are not stored and, like a start below -1 or a count outside
+ * [0, n_rows], reported by cb_sync (CB_ERR_DEVICE).  A non-finite value is stored as 0 and
+ * reported (CB_ERR_NONFINITE).  Two calls on one cache must be ordered by their stream. */
+int cb_kv8_append(const void* k, const void* v, int32_t n_rows, const int32_t* start,
+                  const int32_t* count, const cb_kv8_cache* cache, const cb_dims* dims,
+                  void* stream);
+
+/* Reads rows back as values (code * scale, one fp32 product, rounded to dims->dtype): output
+ * row j of sequence s is cache row start[s] + j.
+ *   start, count : as in cb_kv8_append
+ *   k_out, v_out : [n_seq, n_rows, Hkv hd] of dims->dtype; either may be NULL.  Rows past
+ *                  count[s], of idle sequences and past the capacity are left as they were
+ *                  (the last is reported). */
+int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* count,
+                int32_t n_rows, const cb_dims* dims, void* k_out, void* v_out, void* stream);
+
+/* Device workspace (bytes) of cb_kv8_attention at these sizes (may be 0).  Host-only. */
+int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q,
+                           int32_t with_weights, size_t* out_host);
+
+/* Attention of n_q queries per sequence over the 8-bit cache, for single tokens (n_q = 1) as
+ * for the selected rows of a blend:
+ *   out[s, j, h] = sum_{i <= last[s, j]} p_i v[i],  p = softmax_i(q[s, j, h] . k[i] / sqrt(hd)),
+ * k, v of KV head h / (H / Hkv).
+ *   q, out : [n_seq, n_q, H hd] of dims->dtype
+ *   last   : [n_seq, n_q] int32, the last cache row each query sees (a token appended at row
+ *            r sees itself: last = r); -1: none, its output row is 0 (padding).  A value
+ *            outside [-1, capacity) is reported by cb_sync and counts as -1.
+ *   weights: [n_seq, Hkv, capacity] fp32 or NULL; every row's entry grows by the sum of its p
+ *            over the sequence's queries and the query heads of its KV head (the account that
+ *            cb_kv8_evict goes by).  Rows no query sees are left as they were.
+ * Queries need no order, but launches of many queries run faster when last ascends.
+ * The results are the same from run to run (no floating-point atomics).
+ * head_dim 32, 64, 128 or 256. */
+int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_kv8_cache* cache,
+                     const cb_dims* dims, void* out, float* weights, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/* Eviction by accumulated attention weight, per sequence and KV head: of the rows
+ * [0, len[s]) it keeps the first n_sink, the last n_recent and the heaviest of the others
+ * (ties to the lower row), n_keep in all; with len[s] <= n_keep, every row.  The kept rows
+ * move in ascending order to rows 0, 1, ... of dst, where each block is coded afresh as by
+ * cb_kv8_append into an empty cache.
+ *   len         : [n_seq] int32 in [0, src->capacity] (others are reported and clamped)
+ *   weights     : [n_seq, Hkv, src->capacity] fp32 as cb_kv8_attention accumulates them.  A NaN
+ *                 or negative weight among [0, len) ranks as 0, infinity highest; all three
+ *                 are reported (CB_ERR_NONFINITE).
+ *   dst         : same n_seq and block, n_keep <= dst->capacity, no buffer shared with src
+ *   dst_len     : [n_seq] int32, min(len[s], n_keep)
+ *   dst_weights : [n_seq, Hkv, dst->capacity] fp32 or NULL: the kept rows' weights, then 0
+ *   kept        : [n_seq, Hkv, n_keep] int32: the source row of each kept row, then -1
+ * Needs n_keep >= 1 and n_sink + n_recent <= n_keep.  dims gives Hkv and head_dim. */
+int cb_kv8_evict(const cb_kv8_cache* src, const int32_t* len, const float* weights,
+                 int32_t n_keep, int32_t n_sink, int32_t n_recent, const cb_kv8_cache* dst,
+                 int32_t* dst_len, float* dst_weights, int32_t* kept, const cb_dims* dims,
+                 void* stream);
 
 /* ---- HKVD selection ----------------------------------------------------------------- */
 
@@ -437,6 +525,41 @@ int cb_lmhead_argmax(const void* h, const void* final_norm, const void* w_lm,
                      const cb_dims* dims, float* logits, int32_t* token, void* ws,
                      size_t ws_bytes, void* stream);
 
+/* The rules on the logits of one batch of answers; NULL pointers switch a rule off. */
+typedef struct {
+    const int32_t*  history;      /* [n_rows, history_ld] token ids, prompt then answer       */
+    const int32_t*  history_len;  /* [n_rows] ids held, in [0, history_ld]                    */
+    const int32_t*  prompt_len;   /* [n_rows] how many of them are the prompt's, in
+                                   * [0, history_len]; NULL: none                             */
+    const float*    repetition;   /* [n_rows] > 0: divides a positive logit of an id in the
+                                   * history, multiplies another                              */
+    const float*    presence;     /* [n_rows] taken off once for an id in the answer          */
+    const float*    frequency;    /* [n_rows] taken off for each time it is in the answer     */
+    const int32_t*  bias_id;      /* [n_rows, n_bias] ids, -1: unused entry                   */
+    const float*    bias;         /* [n_rows, n_bias] added; an id listed twice gets both,
+                                   * added up in list order                                   */
+    const uint32_t* mask;         /* [n_rows, mask_ld] bit i % 32 of word i / 32: id i allowed */
+    int64_t         history_ld;
+    int64_t         mask_ld;      /* >= ceil(vocab / 32)                                      */
+    int32_t         n_bias;       /* at most 4096                                             */
+} cb_logit_rules;
+
+/* The rules on the logits before the next token, and that token:
+ *   x > 0 ? x / repetition : x * repetition   if the id is in the history,
+ *   x - (frequency * count + presence)        if it is count > 0 times in the answer,
+ *   x + bias,                                 then -inf where the mask does not allow the id;
+ * fp32 arithmetic, rounded once to `dtype`.
+ *   logits, out : [n_rows, vocab] of `dtype` (CB_F32 or CB_BF16); out may be logits itself or
+ *                 NULL
+ *   token       : [n_rows] int32 or NULL: the lowest id with the largest value of out; -1 if
+ *                 none is above -inf.  A NaN where the mask allows it is never chosen and is
+ *                 reported by cb_sync (CB_ERR_NONFINITE); one that is masked is not.
+ * History and bias ids outside [0, vocab) are skipped and reported (CB_ERR_DEVICE; bias id -1
+ * is not), lengths outside their range clamped and reported; a repetition that is not a
+ * positive finite number counts as 1 and is reported (CB_ERR_NONFINITE). */
+int cb_logits_process(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype,
+                      const cb_logit_rules* rules, void* out, int32_t* token, void* stream);
+
 /* ---- layer-ahead loading ------------------------------------------------------------ */
 
 /* Starts the copy of one layer's cached chunk KV from pinned host memory to the device on
@@ -471,6 +594,11 @@ int cb_stream_wait(void* stream, void* event);
 #define CB_PROF_ARGMAX     9
 #define CB_PROF_ROPE_TABLE 10
 #define CB_PROF_QUANT      11
+#define CB_PROF_KV8_APPEND 12   /* 8-bit cache: append                                      */
+#define CB_PROF_KV8_READ   13
+#define CB_PROF_KV8_ATTN   14   /* aux: 0 attention, 1 weights of many queries             */
+#define CB_PROF_KV8_EVICT  15   /* aux: 0 selection, 1 move                                */
+#define CB_PROF_LOGITS     16
 
 typedef struct {
     int32_t kind;      /* CB_PROF_*                                                     */

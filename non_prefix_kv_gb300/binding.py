@@ -49,8 +49,24 @@ class cb_prof_record(C.Structure):
                 ("flops", C.c_double), ("bytes", C.c_double), ("ms", C.c_float), ("span_ms", C.c_float)]
 
 
+class cb_kv8_cache(C.Structure):
+    """A layer's 8-bit KV cache (see cacheblend.h); made by kv8_cache(), which also keeps the
+    tensors alive and their head count and width for the checks."""
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("capacity", C.c_int64), ("n_seq", C.c_int32), ("block", C.c_int32)]
+
+
+class cb_logit_rules(C.Structure):
+    """The rules of cb_logits_process (see cacheblend.h); made by logit_rules()."""
+    _fields_ = [("history", C.c_void_p), ("history_len", C.c_void_p), ("prompt_len", C.c_void_p),
+                ("repetition", C.c_void_p), ("presence", C.c_void_p), ("frequency", C.c_void_p),
+                ("bias_id", C.c_void_p), ("bias", C.c_void_p), ("mask", C.c_void_p), ("history_ld", C.c_int64),
+                ("mask_ld", C.c_int64), ("n_bias", C.c_int32)]
+
+
 PROF_KINDS = {0: "rope_shift", 1: "copy_rows", 2: "rmsnorm", 3: "gemm", 4: "attention", 5: "deviation",
-              6: "topk", 7: "index", 8: "lmhead_gemv", 9: "argmax", 10: "rope_table", 11: "kv_quantize"}
+              6: "topk", 7: "index", 8: "lmhead_gemv", 9: "argmax", 10: "rope_table", 11: "kv_quantize", 12: "kv8_append",
+              13: "kv8_read", 14: "kv8_attention", 15: "kv8_evict", 16: "logits"}
 
 _P = C.c_void_p
 _I32 = C.c_int32
@@ -96,6 +112,13 @@ _PROTOS = {
     "cb_io_error_message": (C.c_char_p, []),
     "cb_rope_shift_q8": (C.c_int, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _I32, _P, _I64,
                                    C.POINTER(cb_dims), _P, _I32, _P]),
+    "cb_kv8_append": (C.c_int, [_P, _P, _I32, _P, _P, C.POINTER(cb_kv8_cache), C.POINTER(cb_dims), _P]),
+    "cb_kv8_read": (C.c_int, [C.POINTER(cb_kv8_cache), _P, _P, _I32, C.POINTER(cb_dims), _P, _P, _P]),
+    "cb_kv8_workspace_bytes": (C.c_int, [C.POINTER(cb_dims), _I32, _I64, _I32, _I32, C.POINTER(_SZ)]),
+    "cb_kv8_attention": (C.c_int, [_P, _P, _I32, C.POINTER(cb_kv8_cache), C.POINTER(cb_dims), _P, _P, _P, _SZ, _P]),
+    "cb_kv8_evict": (C.c_int, [C.POINTER(cb_kv8_cache), _P, _P, _I32, _I32, _I32, C.POINTER(cb_kv8_cache), _P, _P, _P,
+                               C.POINTER(cb_dims), _P]),
+    "cb_logits_process": (C.c_int, [_P, _I32, _I32, _I32, C.POINTER(cb_logit_rules), _P, _P, _P]),
     "cb_prefetch_layer": (C.c_int, [_P, _P, _SZ, _P, _P]),
     "cb_stream_wait": (C.c_int, [_P, _P]),
     "cb_kernel_launch_count": (_I64, []),
@@ -396,3 +419,118 @@ def cb_prefetch_layer(dev_dst, pinned_src, nbytes: int, side_stream, done_event)
 
 def cb_stream_wait(stream, event):
     _check("cb_stream_wait", lib().cb_stream_wait(_stream(stream), _event(event)))
+
+
+# ---- 8-bit KV cache of an answer in progress, rules on the logits ---------------------------
+def _buf(what: str, t, dtype: str, n: Optional[int] = None) -> Optional[int]:
+    """The address of a buffer.  A tensor must be contiguous, on the current CUDA device, of
+    the element type and hold n elements; raw pointers pass unchecked."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype is not getattr(torch, dtype):
+        raise ValueError(f"{what}: {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: not contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{what}: {tuple(t.shape)} holds {t.numel()} elements, expected {n}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+_ROW_DTYPE = {CB_F32: "float32", CB_BF16: "bfloat16"}
+
+
+def kv8_cache(k_codes, v_codes, k_scale, v_scale, block: int) -> cb_kv8_cache:
+    """The handle of a cache in these tensors: codes [n_seq, Hkv, capacity, head_dim] int8,
+    scales [n_seq, Hkv, capacity / block] float32."""
+    n_seq, hkv, cap, hd = k_codes.shape
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block {block} is not 16, 32, 64 or 128")
+    ns = n_seq * hkv * (cap // block)
+    c = cb_kv8_cache(_buf("k_codes", k_codes, "int8"), _buf("v_codes", v_codes, "int8", k_codes.numel()),
+                     _buf("k_scale", k_scale, "float32", ns), _buf("v_scale", v_scale, "float32", ns), cap, n_seq, block)
+    c.hkv, c.hd, c.tensors = hkv, hd, (k_codes, v_codes, k_scale, v_scale)
+    return c
+
+
+def _kv8(cache: cb_kv8_cache, dims: cb_dims):
+    if cache.hkv != dims.n_kv_heads or cache.hd != dims.head_dim:
+        raise ValueError(f"cache of {cache.hkv} heads of {cache.hd}, dims of {dims.n_kv_heads} heads of {dims.head_dim}")
+    return C.byref(cache)
+
+
+def cb_kv8_append(k, v, n_rows: int, start, count, cache: cb_kv8_cache, dims: cb_dims, stream=None):
+    dt, n = _ROW_DTYPE[dims.dtype], cache.n_seq * n_rows * cache.hkv * cache.hd
+    _check("cb_kv8_append", lib().cb_kv8_append(
+        _buf("k", k, dt, n), _buf("v", v, dt, n), n_rows, _buf("start", start, "int32", cache.n_seq),
+        _buf("count", count, "int32", cache.n_seq), _kv8(cache, dims), C.byref(dims), _stream(stream)))
+
+
+def cb_kv8_read(cache: cb_kv8_cache, start, count, n_rows: int, dims: cb_dims, k_out, v_out, stream=None):
+    dt, n = _ROW_DTYPE[dims.dtype], cache.n_seq * n_rows * cache.hkv * cache.hd
+    _check("cb_kv8_read", lib().cb_kv8_read(
+        _kv8(cache, dims), _buf("start", start, "int32", cache.n_seq), _buf("count", count, "int32", cache.n_seq),
+        n_rows, C.byref(dims), _buf("k_out", k_out, dt, n), _buf("v_out", v_out, dt, n), _stream(stream)))
+
+
+def cb_kv8_workspace_bytes(dims: cb_dims, n_seq: int, capacity: int, n_q: int, with_weights: bool = False) -> int:
+    out = _SZ(0)
+    _check("cb_kv8_workspace_bytes", lib().cb_kv8_workspace_bytes(C.byref(dims), n_seq, capacity, n_q,
+                                                                  1 if with_weights else 0, C.byref(out)))
+    return int(out.value)
+
+
+def cb_kv8_attention(q, last, n_q: int, cache: cb_kv8_cache, dims: cb_dims, out, weights=None, ws=None, stream=None):
+    dt, n = _ROW_DTYPE[dims.dtype], cache.n_seq * n_q * dims.n_heads * dims.head_dim
+    _check("cb_kv8_attention", lib().cb_kv8_attention(
+        _buf("q", q, dt, n), _buf("last", last, "int32", cache.n_seq * n_q), n_q, _kv8(cache, dims), C.byref(dims),
+        _buf("out", out, dt, n), _buf("weights", weights, "float32", cache.n_seq * cache.hkv * cache.capacity),
+        _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def cb_kv8_evict(src: cb_kv8_cache, length, weights, n_keep: int, n_sink: int, n_recent: int, dst: cb_kv8_cache,
+                 dst_len, dst_weights, kept, dims: cb_dims, stream=None):
+    heads = src.n_seq * src.hkv
+    _check("cb_kv8_evict", lib().cb_kv8_evict(
+        _kv8(src, dims), _buf("length", length, "int32", src.n_seq),
+        _buf("weights", weights, "float32", heads * src.capacity), n_keep, n_sink, n_recent, _kv8(dst, dims),
+        _buf("dst_len", dst_len, "int32", src.n_seq), _buf("dst_weights", dst_weights, "float32", heads * dst.capacity),
+        _buf("kept", kept, "int32", heads * n_keep), C.byref(dims), _stream(stream)))
+
+
+def logit_rules(history=None, history_len=None, prompt_len=None, repetition=None, presence=None, frequency=None,
+                bias_id=None, bias=None, mask=None) -> cb_logit_rules:
+    """The rules of one batch: history [n_rows, ld] int32 with its lengths, penalties [n_rows]
+    float32, bias_id / bias [n_rows, n_bias], mask [n_rows, words] (32 ids a word, int32).
+    None switches a rule off."""
+    rows = [t.shape[0] for t in (history, history_len, prompt_len, repetition, presence, frequency, bias_id, bias, mask)
+            if t is not None]
+    if rows and min(rows) != max(rows):
+        raise ValueError("the rules' tensors differ in their row count")
+    if bias is not None and (bias_id is None or bias.shape != bias_id.shape):
+        raise ValueError("bias and bias_id must have one shape")
+    r = cb_logit_rules(
+        _buf("history", history, "int32"), _buf("history_len", history_len, "int32"),
+        _buf("prompt_len", prompt_len, "int32"), _buf("repetition", repetition, "float32"),
+        _buf("presence", presence, "float32"), _buf("frequency", frequency, "float32"),
+        _buf("bias_id", bias_id, "int32"), _buf("bias", bias, "float32"), _buf("mask", mask, "int32"),
+        0 if history is None else history.shape[1], 0 if mask is None else mask.shape[1],
+        0 if bias_id is None else bias_id.shape[1])
+    r.n_rows = rows[0] if rows else None
+    r.tensors = (history, history_len, prompt_len, repetition, presence, frequency, bias_id, bias, mask)
+    return r
+
+
+def cb_logits_process(logits, rules: cb_logit_rules, out=None, token=None, stream=None):
+    """logits [n_rows, vocab] float32 or bfloat16; out (may be logits) and token as in the header."""
+    n, vocab = logits.shape
+    if rules.n_rows is not None and rules.n_rows != n:
+        raise ValueError(f"rules for {rules.n_rows} rows, logits of {n}")
+    dt = {v: k for k, v in _ROW_DTYPE.items()}.get(str(logits.dtype).split(".")[-1])
+    if dt is None:
+        raise ValueError(f"logits: {logits.dtype}, expected float32 or bfloat16")
+    _check("cb_logits_process", lib().cb_logits_process(
+        _buf("logits", logits, _ROW_DTYPE[dt]), n, vocab, dt, C.byref(rules), _buf("out", out, _ROW_DTYPE[dt], n * vocab),
+        _buf("token", token, "int32", n), _stream(stream)))

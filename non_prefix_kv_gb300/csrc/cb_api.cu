@@ -18,6 +18,26 @@
 namespace cb {
 uint32_t take_error_gemm_tc();
 uint32_t take_error_attn_tc();
+
+// 8-bit KV cache (cb_kv8.cu, cb_kv8_attn.cu) and logits (cb_logits.cu)
+cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, const int32_t* start,
+                              const int32_t* count, const cb_kv8_cache& c, int Hkv, int hd, cudaStream_t s);
+cudaError_t launch_kv8_read(int dt, const cb_kv8_cache& c, const int32_t* start, const int32_t* count, int n_rows,
+                            int Hkv, int hd, void* k_out, void* v_out, cudaStream_t s);
+cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const float* weights, int n_keep, int n_sink,
+                              int n_recent, int64_t dcap, int32_t* dst_len, float* dst_weights, int32_t* kept, int Hkv,
+                              cudaStream_t s);
+cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, const int32_t* dst_len, int n_keep,
+                            const int32_t* kept, int Hkv, int hd, cudaStream_t s);
+bool kv8_attn_supported(int hd);
+size_t kv8_attn_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, bool weights);
+bool kv8_attn_weights_apart(int G, int n_q);
+cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
+                            int hd, void* out, float* weights, void* ws, cudaStream_t s);
+cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
+                               int Hkv, int hd, float* weights, void* ws, cudaStream_t s);
+cudaError_t launch_logits(int dt, const void* logits, int n_rows, int vocab, const cb_logit_rules& r, void* out,
+                          int32_t* token, cudaStream_t s);
 }  // namespace cb
 
 using namespace cb;
@@ -470,7 +490,7 @@ const char* cb_status_string(int status) {
     case CB_ERR_SHAPE: return "inconsistent shape";
     case CB_ERR_DTYPE: return "unsupported dtype";
     case CB_ERR_WORKSPACE: return "workspace too small";
-    case CB_ERR_NONFINITE: return "non-finite deviation score";
+    case CB_ERR_NONFINITE: return "non-finite score, cache row, weight or logit";
     case CB_ERR_CUDA: return "CUDA error";
     case CB_ERR_TIMEOUT: return "timed out";
     case CB_ERR_UNSUPPORTED: return "unsupported shape";
@@ -499,8 +519,9 @@ int cb_sync(void* stream, double timeout_s) {
     nanosleep(&ts, nullptr);
   }
   const uint32_t bits = take_error_mem() | take_error_gemm() | take_error_gemm_tc() | take_error_attn() |
-                        take_error_attn_tc();
-  if (bits & ERRBIT_NONFINITE) return fail(CB_ERR_NONFINITE, "a deviation score was NaN/Inf");
+                        take_error_attn_tc() | take_error_kv8() | take_error_kv8_attn() | take_error_logits();
+  if (bits & ERRBIT_NONFINITE)
+    return fail(CB_ERR_NONFINITE, "a deviation score, cache row, weight or logit was NaN/Inf (or out of its range)");
   if (bits & ERRBIT_INDEX) return fail(CB_ERR_DEVICE, "a kernel met an out-of-range index");
   if (bits & ERRBIT_TIMEOUT) return fail(CB_ERR_DEVICE, "a kernel's bounded wait expired");
   return CB_OK;
@@ -1152,6 +1173,161 @@ int cb_linear(const void* x, const void* w, void* y, int32_t M, int32_t N, int32
   return CB_OK;
 }
 
+// ---- 8-bit KV cache of an answer in progress -----------------------------------------------
+namespace {
+
+int check_cache(const cb_kv8_cache* c, const cb_dims* d, const char* what) {
+  if (!c || !c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale)
+    return fail(CB_ERR_INVALID_ARG, "%s: cache pointer is NULL", what);
+  if (int st = check_al16({c->k_codes, c->v_codes, c->k_scale, c->v_scale}, what)) return st;
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
+    return fail(CB_ERR_UNSUPPORTED, "%s: block %d is not 16, 32, 64 or 128", what, c->block);
+  if (c->n_seq < 1 || c->n_seq > 65535) return fail(CB_ERR_SHAPE, "%s: n_seq %d outside [1, 65535]", what, c->n_seq);
+  if (c->capacity < c->block || c->capacity % c->block || c->capacity > INT32_MAX)
+    return fail(CB_ERR_SHAPE, "%s: capacity %lld is not a multiple of block below 2^31", what, (long long)c->capacity);
+  if (d->n_kv_heads > 65535) return fail(CB_ERR_UNSUPPORTED, "%s: more than 65535 KV heads", what);
+  return CB_OK;
+}
+
+// codes and scales of a cache as address ranges, for the check that two caches share none
+bool caches_overlap(const cb_kv8_cache* a, const cb_kv8_cache* b, const cb_dims* d) {
+  auto ranges = [&](const cb_kv8_cache* c, uintptr_t (*r)[2]) {
+    const size_t rows = (size_t)c->n_seq * d->n_kv_heads * (size_t)c->capacity;
+    const void* p[4] = {c->k_codes, c->v_codes, c->k_scale, c->v_scale};
+    for (int i = 0; i < 4; ++i) {
+      r[i][0] = reinterpret_cast<uintptr_t>(p[i]);
+      r[i][1] = r[i][0] + (i < 2 ? rows * d->head_dim : rows / c->block * 4);
+    }
+  };
+  uintptr_t x[4][2], y[4][2];
+  ranges(a, x);
+  ranges(b, y);
+  for (auto& i : x)
+    for (auto& j : y)
+      if (i[0] < j[1] && j[0] < i[1]) return true;
+  return false;
+}
+
+}  // namespace
+
+int cb_kv8_append(const void* k, const void* v, int32_t n_rows, const int32_t* start, const int32_t* count,
+                  const cb_kv8_cache* cache, const cb_dims* dims, void* stream) {
+  int st = check_dims(dims);
+  if (st || (st = check_cache(cache, dims, "kv8_append"))) return st;
+  if (n_rows < 0) return fail(CB_ERR_SHAPE, "n_rows < 0");
+  if (n_rows == 0) return CB_OK;
+  if (n_rows > cache->capacity) return fail(CB_ERR_SHAPE, "n_rows %d exceeds the capacity", n_rows);
+  if (!k || !v || !start) return fail(CB_ERR_INVALID_ARG, "kv8_append pointer is NULL");
+  if ((st = check_al16({k, v}, "kv8_append"))) return st;
+  const double W = 2.0 * dims->n_kv_heads * dims->head_dim, n = (double)cache->n_seq * n_rows;
+  CB_LAUNCH(CB_PROF_KV8_APPEND, 0, (int64_t)cache->n_seq * n_rows, (int64_t)W, 0, 0.0, n * W * (1.0 + esize(dims->dtype)),
+            S(stream), launch_kv8_append(dims->dtype, k, v, n_rows, start, count, *cache, dims->n_kv_heads,
+                                         dims->head_dim, S(stream)));
+  return CB_OK;
+}
+
+int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* count, int32_t n_rows,
+                const cb_dims* dims, void* k_out, void* v_out, void* stream) {
+  int st = check_dims(dims);
+  if (st || (st = check_cache(cache, dims, "kv8_read"))) return st;
+  if (n_rows < 0) return fail(CB_ERR_SHAPE, "n_rows < 0");
+  if (n_rows == 0 || (!k_out && !v_out)) return CB_OK;
+  if (!start) return fail(CB_ERR_INVALID_ARG, "kv8_read: start is NULL");
+  if ((st = check_al16({k_out, v_out}, "kv8_read"))) return st;
+  if ((int64_t)n_rows * dims->n_kv_heads * dims->head_dim / 8 > INT32_MAX)
+    return fail(CB_ERR_UNSUPPORTED, "kv8_read: more than 2^34 values of a sequence in one call");
+  const double W = (k_out && v_out ? 2.0 : 1.0) * dims->n_kv_heads * dims->head_dim, n = (double)cache->n_seq * n_rows;
+  CB_LAUNCH(CB_PROF_KV8_READ, 0, (int64_t)cache->n_seq * n_rows, (int64_t)W, 0, 0.0, n * W * (1.0 + esize(dims->dtype)),
+            S(stream), launch_kv8_read(dims->dtype, *cache, start, count, n_rows, dims->n_kv_heads, dims->head_dim,
+                                       k_out, v_out, S(stream)));
+  return CB_OK;
+}
+
+int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q, int32_t with_weights,
+                           size_t* out_host) {
+  int st = check_dims(dims);
+  if (st) return st;
+  if (!out_host || n_seq < 1 || capacity < 1 || n_q < 0) return fail(CB_ERR_INVALID_ARG, "workspace query arguments");
+  *out_host = kv8_attn_ws_bytes(n_seq, dims->n_kv_heads, dims->n_heads / dims->n_kv_heads, n_q, capacity,
+                                with_weights != 0);
+  return CB_OK;
+}
+
+int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_kv8_cache* cache, const cb_dims* dims,
+                     void* out, float* weights, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_dims(dims);
+  if (st || (st = check_cache(cache, dims, "kv8_attention"))) return st;
+  if (!kv8_attn_supported(dims->head_dim))
+    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: head_dim %d is not 32, 64, 128 or 256", dims->head_dim);
+  if (n_q < 0) return fail(CB_ERR_SHAPE, "n_q < 0");
+  if (n_q == 0) return CB_OK;
+  const int H = dims->n_heads, Hkv = dims->n_kv_heads, hd = dims->head_dim, G = H / Hkv;
+  if ((int64_t)n_q * G > (1 << 27)) return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
+  if (!q || !last || !out) return fail(CB_ERR_INVALID_ARG, "kv8_attention pointer is NULL");
+  if ((st = check_al16({q, out, weights, ws}, "kv8_attention"))) return st;
+  const size_t need = kv8_attn_ws_bytes(cache->n_seq, Hkv, G, n_q, cache->capacity, weights != nullptr);
+  if (need && (!ws || ws_bytes < need)) return fail(CB_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
+  const int64_t m = (int64_t)cache->n_seq * n_q;
+  CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),
+            launch_kv8_attn(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
+  if (weights && kv8_attn_weights_apart(G, n_q))
+    CB_LAUNCH(CB_PROF_KV8_ATTN, 1, m, cache->capacity, H, 0.0, 0.0, S(stream),
+              launch_kv8_weights(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, weights, ws, S(stream)));
+  return CB_OK;
+}
+
+int cb_kv8_evict(const cb_kv8_cache* src, const int32_t* len, const float* weights, int32_t n_keep, int32_t n_sink,
+                 int32_t n_recent, const cb_kv8_cache* dst, int32_t* dst_len, float* dst_weights, int32_t* kept,
+                 const cb_dims* dims, void* stream) {
+  int st = check_dims(dims);
+  if (st || (st = check_cache(src, dims, "kv8_evict src")) || (st = check_cache(dst, dims, "kv8_evict dst"))) return st;
+  if (src->n_seq != dst->n_seq || src->block != dst->block)
+    return fail(CB_ERR_SHAPE, "kv8_evict: src and dst differ in n_seq or block");
+  if (n_keep < 1 || n_keep > dst->capacity) return fail(CB_ERR_SHAPE, "n_keep %d outside [1, dst capacity]", n_keep);
+  if (n_sink < 0 || n_recent < 0 || (int64_t)n_sink + n_recent > n_keep)
+    return fail(CB_ERR_SHAPE, "need n_sink, n_recent >= 0 and n_sink + n_recent <= n_keep");
+  if (!len || !weights || !dst_len || !kept) return fail(CB_ERR_INVALID_ARG, "kv8_evict pointer is NULL");
+  if ((st = check_al16({weights, dst_weights, kept}, "kv8_evict"))) return st;
+  if (caches_overlap(src, dst, dims)) return fail(CB_ERR_INVALID_ARG, "kv8_evict: src and dst share memory");
+  if (len == dst_len || weights == dst_weights)
+    return fail(CB_ERR_INVALID_ARG, "kv8_evict: dst_len and dst_weights must not be the source's");
+  const int Hkv = dims->n_kv_heads, hd = dims->head_dim;
+  const int64_t heads = (int64_t)src->n_seq * Hkv;
+  CB_LAUNCH(CB_PROF_KV8_EVICT, 0, heads, src->capacity, n_keep, 0.0, (double)heads * (4.0 * src->capacity + 8.0 * n_keep),
+            S(stream), launch_kv8_select(*src, len, weights, n_keep, n_sink, n_recent, dst->capacity, dst_len,
+                                         dst_weights, kept, Hkv, S(stream)));
+  CB_LAUNCH(CB_PROF_KV8_EVICT, 1, heads, n_keep, hd, 0.0, 4.0 * heads * n_keep * hd, S(stream),
+            launch_kv8_move(*src, *dst, dst_len, n_keep, kept, Hkv, hd, S(stream)));
+  return CB_OK;
+}
+
+int cb_logits_process(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype, const cb_logit_rules* rules,
+                      void* out, int32_t* token, void* stream) {
+  if (dtype != CB_F32 && dtype != CB_BF16) return fail(CB_ERR_DTYPE, "dtype %d", dtype);
+  if (n_rows < 0 || n_rows > 65535 || vocab < 1) return fail(CB_ERR_SHAPE, "need 0 <= n_rows <= 65535, vocab >= 1");
+  if (vocab > INT32_MAX - 65536) return fail(CB_ERR_UNSUPPORTED, "vocab %d is too large", vocab);
+  if (!rules) return fail(CB_ERR_INVALID_ARG, "rules is NULL");
+  const cb_logit_rules& r = *rules;
+  if (r.n_bias < 0 || r.n_bias > 4096) return fail(CB_ERR_SHAPE, "n_bias %d outside [0, 4096]", r.n_bias);
+  if (n_rows == 0 || (!out && !token)) return CB_OK;
+  if (!logits) return fail(CB_ERR_INVALID_ARG, "logits is NULL");
+  if (r.history && (!r.history_len || r.history_ld < 0 || r.history_ld > INT32_MAX))
+    return fail(CB_ERR_INVALID_ARG, "history needs history_len and 0 <= history_ld < 2^31");
+  if (!r.history && (r.history_len || r.prompt_len || r.repetition || r.presence || r.frequency))
+    return fail(CB_ERR_INVALID_ARG, "lengths and penalties need a history");
+  if (r.n_bias > 0 && (!r.bias_id || !r.bias)) return fail(CB_ERR_INVALID_ARG, "n_bias > 0 needs bias_id and bias");
+  if (r.mask && r.mask_ld < (vocab + 31) / 32) return fail(CB_ERR_SHAPE, "mask_ld shorter than ceil(vocab / 32)");
+  if (int st = check_al16({logits, out}, "logits_process")) return st;
+  const char* a = static_cast<const char*>(logits);
+  const char* b = static_cast<const char*>(out);
+  const size_t bytes = (size_t)n_rows * vocab * esize(dtype);
+  if (out && out != logits && a < b + bytes && b < a + bytes)
+    return fail(CB_ERR_INVALID_ARG, "out overlaps logits without being the same buffer");
+  CB_LAUNCH(CB_PROF_LOGITS, 0, n_rows, vocab, 0, 0.0, (double)bytes * (out ? 2.0 : 1.0), S(stream),
+            launch_logits(dtype, logits, n_rows, vocab, r, out, token, S(stream)));
+  return CB_OK;
+}
+
 int cb_prefetch_layer(void* dev_dst, const void* pinned_src, size_t bytes, void* side_stream, void* done_event) {
   if (bytes > 0 && (!dev_dst || !pinned_src)) return fail(CB_ERR_INVALID_ARG, "prefetch pointer is NULL");
   if (!done_event) return fail(CB_ERR_INVALID_ARG, "done_event is NULL");
@@ -1182,6 +1358,9 @@ void cb_shutdown(void) {
   reset_mem_caches();
   reset_gemm_tc_caches();
   reset_attn_tc_caches();
+  reset_kv8_caches();
+  reset_kv8_attn_caches();
+  reset_logits_caches();
   ProfState& P = g_prof;
   bool failed = false;
   for (cudaEvent_t e : P.ev) failed = cudaEventDestroy(e) != cudaSuccess || failed;

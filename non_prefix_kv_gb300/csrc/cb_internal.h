@@ -189,4 +189,13 @@ cudaError_t launch_attention(int dt, const void* q, const int32_t* q_pos, int M,
                              int hd, void* out, void* ws, size_t ws_bytes, cudaStream_t s);
 uint32_t take_error_attn();
 
+// ---- error words of the 8-bit cache and logits kernels, and their per-device caches ------
+// (the launchers take cb_kv8_cache / cb_logit_rules and are declared where they are called)
+uint32_t take_error_kv8();
+uint32_t take_error_kv8_attn();
+uint32_t take_error_logits();
+void reset_kv8_caches();
+void reset_kv8_attn_caches();
+void reset_logits_caches();
+
 }  // namespace cb

@@ -1,0 +1,258 @@
+// The rules on a batch's logits before the next token (penalties for repeated ids, biases, a
+// grammar's mask) and that token, in one pass over the logits.
+//
+// HBM-bound: a row reads and writes vocab elements and reads its mask bits and history once
+// per CTA.  One cluster of CTAs per row, each owning a slice of the vocabulary: it counts the
+// row's history ids that fall into its slice in shared memory (integers, so the order of the
+// atomics does not matter), adds up the biases there in list order, then streams the slice
+// through the rules.  The slices' best (value, id) keys meet in the cluster's shared memory,
+// so there is no second launch and no workspace.
+#include <math.h>
+
+#include <mutex>
+
+#include "../../include/cacheblend.h"
+#include "cb_common.cuh"
+#include "cb_internal.h"
+#include "cb_tc.cuh"
+
+namespace cb {
+
+static __device__ uint32_t g_err_logits;
+
+uint32_t take_error_logits() {
+  uint32_t v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_logits, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
+  cudaMemcpyToSymbol(g_err_logits, &z, sizeof(z));
+  return v;
+}
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kChunk = 8192;                 // ids a CTA holds counts and biases of at once
+constexpr uint32_t kSeen = 0x80000000u;      // in the history (the low bits: times in the answer)
+
+// larger value first, then the lower id; 0 only for "nothing"
+__device__ __forceinline__ unsigned long long token_key(float v, int id) {
+  const uint32_t u = __float_as_uint(v + 0.0f);   // -0 counts as +0
+  const uint32_t o = (u >> 31) ? ~u : (u | 0x80000000u);
+  return ((unsigned long long)o << 32) | (uint32_t)~id;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, int32_t* __restrict__ token, int vocab,
+                                                     int slice, bool vec, const cb_logit_rules r) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int E = 16 / sizeof(T);          // elements of a 16-byte access
+  extern __shared__ __align__(16) uint32_t smem[];
+  uint32_t* cnt = smem;                      // [kChunk]
+  float* bias = reinterpret_cast<float*>(smem + kChunk);
+  __shared__ unsigned long long s_best[kThreads / 32];
+  __shared__ unsigned long long s_key;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x, row = blockIdx.y;
+  const bool report = rank == 0 && tid == 0;
+  const T* x = logits + (int64_t)row * vocab;
+  T* y = out ? out + (int64_t)row * vocab : nullptr;
+  const bool hist = r.history != nullptr, biased = r.n_bias > 0;
+
+  int len = 0, plen = 0;
+  if (hist) {
+    const int64_t l = r.history_len[row], p = r.prompt_len ? r.prompt_len[row] : 0;
+    len = (int)(l < 0 ? 0 : (l > r.history_ld ? r.history_ld : l));
+    plen = (int)(p < 0 ? 0 : (p > len ? len : p));
+    if (report && (len != l || plen != p)) atomicOr(&g_err_logits, ERRBIT_INDEX);
+  }
+  float rep = r.repetition ? r.repetition[row] : 1.0f;
+  if (!(rep > 0.0f) || isinf(rep)) {
+    if (report) atomicOr(&g_err_logits, ERRBIT_NONFINITE);
+    rep = 1.0f;
+  }
+  const float pres = r.presence ? r.presence[row] : 0.0f, freq = r.frequency ? r.frequency[row] : 0.0f;
+  const uint32_t* mask = r.mask ? r.mask + (int64_t)row * r.mask_ld : nullptr;
+  const int s0 = rank * slice, s1 = min(vocab, s0 + slice);
+  unsigned long long best = 0;
+  bool bad_id = false, bad_x = false;
+
+  for (int c0 = s0; c0 < s1; c0 += kChunk) {
+    const int n = min(kChunk, s1 - c0);
+    if (hist || biased) {
+      for (int i = tid; i < n; i += kThreads) {
+        if (hist) cnt[i] = 0;
+        if (biased) bias[i] = 0.f;
+      }
+      __syncthreads();
+    }
+    if (hist) {
+      const int32_t* ids = r.history + (int64_t)row * r.history_ld;
+      for (int i = tid; i < len; i += kThreads) {
+        const int id = ids[i];
+        if (id < 0 || id >= vocab) {
+          bad_id = true;
+          continue;
+        }
+        const int k = id - c0;
+        if (k < 0 || k >= n) continue;
+        if (i >= plen) atomicAdd(&cnt[k], 1u);
+        atomicOr(&cnt[k], kSeen);
+      }
+    }
+    if (biased && warp == 0) {
+      // 32 entries at a time; the first lane of each id adds that id's entries in list order
+      const int32_t* bid = r.bias_id + (int64_t)row * r.n_bias;
+      const float* bv = r.bias + (int64_t)row * r.n_bias;
+      for (int i = 0; i < r.n_bias; i += 32) {
+        int id = -1;
+        float v = 0.f;
+        if (i + lane < r.n_bias) {
+          id = bid[i + lane];
+          v = bv[i + lane];
+          if (id < -1 || id >= vocab) {
+            bad_id = true;
+            id = -1;
+          }
+        }
+        const int k = id - c0;
+        const bool in = id >= 0 && k >= 0 && k < n;
+        const unsigned same = __match_any_sync(0xffffffffu, in ? k : -1 - lane);
+        const bool first = in && lane == __ffs(same) - 1;
+        float sum = first ? bias[k] : 0.f;
+#pragma unroll
+        for (int l = 0; l < 32; ++l) {
+          const float w = __shfl_sync(0xffffffffu, v, l);
+          if ((same >> l) & 1) sum += w;
+        }
+        if (first) bias[k] = sum;
+        __syncwarp();
+      }
+    }
+    if (hist || biased) __syncthreads();
+
+    auto rule = [&](float v, int i, uint32_t open) -> float {     // id c0 + i
+      if (hist) {
+        const uint32_t c = cnt[i];
+        if (c) {
+          v = v > 0.f ? v / rep : v * rep;
+          const uint32_t k = c & ~kSeen;
+          if (k) v -= freq * (float)k + pres;
+        }
+      }
+      if (biased) v += bias[i];
+      return open & 1 ? v : -INFINITY;
+    };
+    auto take = [&](float v, int i) {                              // v as it is returned
+      if (v != v) {
+        bad_x = true;
+        return;
+      }
+      const unsigned long long k = token_key(v, c0 + i);
+      best = k > best ? k : best;
+    };
+    if (vec) {
+      for (int i = tid * E; i < n; i += kThreads * E) {
+        T e[E];
+        *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(x + c0 + i);
+        const uint32_t open = mask ? mask[(c0 + i) >> 5] >> ((c0 + i) & 31) : 0xffffffffu;
+#pragma unroll
+        for (int q = 0; q < E; ++q) {
+          e[q] = from_f<T>(rule(to_f(e[q]), i + q, open >> q));
+          take(to_f(e[q]), i + q);
+        }
+        if (y) *reinterpret_cast<uint4*>(y + c0 + i) = *reinterpret_cast<const uint4*>(e);
+      }
+    } else {
+      for (int i = tid; i < n; i += kThreads) {
+        const uint32_t open = mask ? mask[(c0 + i) >> 5] >> ((c0 + i) & 31) : 1u;
+        const T v = from_f<T>(rule(to_f(x[c0 + i]), i, open));
+        take(to_f(v), i);
+        if (y) y[c0 + i] = v;
+      }
+    }
+    __syncthreads();                       // the counts are used up before the next chunk's
+  }
+  if (bad_id) atomicOr(&g_err_logits, ERRBIT_INDEX);
+  if (bad_x) atomicOr(&g_err_logits, ERRBIT_NONFINITE);
+  if (!token) return;                      // uniform over the cluster
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
+    best = k > best ? k : best;
+  }
+  if (lane == 0) s_best[warp] = best;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kThreads / 32; ++w) best = s_best[w] > best ? s_best[w] : best;
+    s_key = best;
+  }
+  tc::cluster_sync();
+  if (rank == 0 && tid == 0) {
+    for (int c = 1; c < (int)gridDim.x; ++c) {
+      unsigned long long k;
+      asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(tc::mapa_shared(tc::smem_u32(&s_key), c)));
+      best = k > best ? k : best;
+    }
+    // only a value above -inf is chosen
+    const bool any = (uint32_t)(best >> 32) > ~0xff800000u;
+    token[row] = any ? (int32_t)~(uint32_t)best : -1;
+  }
+  tc::cluster_sync();                      // the key was read before its CTA ends
+}
+
+std::mutex g_logits_mu;
+uint32_t g_logits_attr[64];
+
+template <typename T>
+cudaError_t launch_t(const void* logits, int n_rows, int vocab, const cb_logit_rules& r, void* out, int32_t* token,
+                     cudaStream_t s) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr uint32_t bit = sizeof(T) == 4 ? 1u : 2u;
+  constexpr int smem = kChunk * 8;
+  {
+    std::lock_guard<std::mutex> g(g_logits_mu);
+    if (dev < 0 || dev >= 64 || !(g_logits_attr[dev] & bit)) {
+      e = cudaFuncSetAttribute(k_logits<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      if (dev >= 0 && dev < 64) g_logits_attr[dev] |= bit;
+    }
+  }
+  int nc = 8;
+  while (nc > 1 && (int64_t)nc * 512 > vocab) nc /= 2;
+  const int slice = ((vocab + nc - 1) / nc + 63) & ~63;
+  const uintptr_t al = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out);
+  const bool vec = (int64_t)vocab * sizeof(T) % 16 == 0 && al % 16 == 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(nc, n_rows);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = r.history || r.n_bias > 0 ? smem : 0;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = nc;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_logits<T>, static_cast<const T*>(logits), static_cast<T*>(out), token, vocab, slice,
+                            vec, r);
+}
+
+}  // namespace
+
+void reset_logits_caches() {
+  std::lock_guard<std::mutex> g(g_logits_mu);
+  for (int i = 0; i < 64; ++i) g_logits_attr[i] = 0;
+}
+
+cudaError_t launch_logits(int dt, const void* logits, int n_rows, int vocab, const cb_logit_rules& r, void* out,
+                          int32_t* token, cudaStream_t s) {
+  if (dt == DT_BF16) return launch_t<bf16>(logits, n_rows, vocab, r, out, token, s);
+  return launch_t<float>(logits, n_rows, vocab, r, out, token, s);
+}
+
+}  // namespace cb
