@@ -527,7 +527,8 @@ int cb_lmhead_argmax(const void* h, const void* final_norm, const void* w_lm,
 
 /* The rules on the logits of one batch of answers; NULL pointers switch a rule off. */
 typedef struct {
-    const int32_t*  history;      /* [n_rows, history_ld] token ids, prompt then answer       */
+    const int32_t*  history;      /* [n_rows, history_ld] token ids, prompt then answer; NULL
+                                   * (with history_ld 0): none, the penalties have no effect  */
     const int32_t*  history_len;  /* [n_rows] ids held, in [0, history_ld]                    */
     const int32_t*  prompt_len;   /* [n_rows] how many of them are the prompt's, in
                                    * [0, history_len]; NULL: none                             */

@@ -511,6 +511,8 @@ def logit_rules(history=None, history_len=None, prompt_len=None, repetition=None
         raise ValueError("the rules' tensors differ in their row count")
     if bias is not None and (bias_id is None or bias.shape != bias_id.shape):
         raise ValueError("bias and bias_id must have one shape")
+    if history is None and any(t is not None for t in (history_len, prompt_len, repetition, presence, frequency)):
+        raise ValueError("lengths and penalties need a history")
     r = cb_logit_rules(
         _buf("history", history, "int32"), _buf("history_len", history_len, "int32"),
         _buf("prompt_len", prompt_len, "int32"), _buf("repetition", repetition, "float32"),

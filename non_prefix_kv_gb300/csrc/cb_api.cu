@@ -1313,8 +1313,7 @@ int cb_logits_process(const void* logits, int32_t n_rows, int32_t vocab, int32_t
   if (!logits) return fail(CB_ERR_INVALID_ARG, "logits is NULL");
   if (r.history && (!r.history_len || r.history_ld < 0 || r.history_ld > INT32_MAX))
     return fail(CB_ERR_INVALID_ARG, "history needs history_len and 0 <= history_ld < 2^31");
-  if (!r.history && (r.history_len || r.prompt_len || r.repetition || r.presence || r.frequency))
-    return fail(CB_ERR_INVALID_ARG, "lengths and penalties need a history");
+  if (!r.history && r.history_ld != 0) return fail(CB_ERR_INVALID_ARG, "history is NULL with history_ld != 0");
   if (r.n_bias > 0 && (!r.bias_id || !r.bias)) return fail(CB_ERR_INVALID_ARG, "n_bias > 0 needs bias_id and bias");
   if (r.mask && r.mask_ld < (vocab + 31) / 32) return fail(CB_ERR_SHAPE, "mask_ld shorter than ceil(vocab / 32)");
   if (int st = check_al16({logits, out}, "logits_process")) return st;

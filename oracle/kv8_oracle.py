@@ -57,12 +57,14 @@ def values(codes, scale, block):
 
 def attention(c, q, last):
     """q: [n_seq, n_q, H, hd], last: [n_seq, n_q].  Returns out [n_seq, n_q, H, hd], the weights
-    [n_seq, Hkv, cap], sum_i p_i |v_i| (same shape as out) and, per query, the largest
-    sum_c |q_c k_c| / sqrt(hd) over the keys it sees (the scale of a score's rounding)."""
+    [n_seq, Hkv, cap], sum_i p_i |v_i| (same shape as out) and, per query, two figures that
+    roundings scale with: the largest sum_c |q_c k_c| / sqrt(hd) over the keys it sees, and the
+    largest p_i times the scale of v_i."""
     n_seq, nq, H, hd = q.shape
     hkv, cap = c["k"].shape[1:3]
     g = H // hkv
     out, mag, zmag = np.zeros(q.shape), np.zeros(q.shape), np.zeros((n_seq, nq, H))
+    top = np.zeros((n_seq, nq, H))
     w = np.zeros((n_seq, hkv, cap))
     for s in range(n_seq):
         for j in range(nq):
@@ -81,8 +83,9 @@ def attention(c, q, last):
                 out[s, j, h] = p @ V
                 mag[s, j, h] = p @ np.abs(V)
                 zmag[s, j, h] = (np.abs(K) @ np.abs(q[s, j, h])).max() / np.sqrt(hd)
+                top[s, j, h] = (p * np.repeat(np.maximum(c["vs"][s, kh, :nb], MIN_SCALE), c["block"])[:n]).max()
                 w[s, kh, :n] += p
-    return out, w, mag, zmag
+    return out, w, mag, zmag, top
 
 
 def evict(c, length, weights, n_keep, n_sink, n_recent, dst_cap):
