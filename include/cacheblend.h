@@ -597,7 +597,8 @@ int cb_stream_wait(void* stream, void* event);
 #define CB_PROF_QUANT      11
 #define CB_PROF_KV8_APPEND 12   /* 8-bit cache: append                                      */
 #define CB_PROF_KV8_READ   13
-#define CB_PROF_KV8_ATTN   14   /* aux: 0 attention, 1 weights of many queries             */
+#define CB_PROF_KV8_ATTN   14   /* aux: 0 attention, 1 weights of many queries, 2 both on
+                                 * the tensor cores (three launches at most, one record)  */
 #define CB_PROF_KV8_EVICT  15   /* aux: 0 selection, 1 move                                */
 #define CB_PROF_LOGITS     16
 

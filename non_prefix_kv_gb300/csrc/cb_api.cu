@@ -36,6 +36,10 @@ cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q,
                             int hd, void* out, float* weights, void* ws, cudaStream_t s);
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
                                int Hkv, int hd, float* weights, void* ws, cudaStream_t s);
+bool kv8_tc_taken(int dt, int hd, int G, int n_q);
+size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
+cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
+                          void* out, float* weights, void* ws, cudaStream_t s);
 cudaError_t launch_logits(int dt, const void* logits, int n_rows, int vocab, const cb_logit_rules& r, void* out,
                           int32_t* token, cudaStream_t s);
 }  // namespace cb
@@ -519,7 +523,8 @@ int cb_sync(void* stream, double timeout_s) {
     nanosleep(&ts, nullptr);
   }
   const uint32_t bits = take_error_mem() | take_error_gemm() | take_error_gemm_tc() | take_error_attn() |
-                        take_error_attn_tc() | take_error_kv8() | take_error_kv8_attn() | take_error_logits();
+                        take_error_attn_tc() | take_error_kv8() | take_error_kv8_attn() | take_error_kv8_tc() |
+                        take_error_logits();
   if (bits & ERRBIT_NONFINITE)
     return fail(CB_ERR_NONFINITE, "a deviation score, cache row, weight or logit was NaN/Inf (or out of its range)");
   if (bits & ERRBIT_INDEX) return fail(CB_ERR_DEVICE, "a kernel met an out-of-range index");
@@ -1243,13 +1248,22 @@ int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* 
   return CB_OK;
 }
 
+namespace {
+// scratch of an attention call: the tensor-core path's operands, or the small path's scores
+size_t kv8_ws(const cb_dims* d, int n_seq, int64_t cap, int n_q, bool weights) {
+  const int G = d->n_heads / d->n_kv_heads;
+  if (kv8_tc_taken(d->dtype, d->head_dim, G, n_q))
+    return kv8_tc_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
+  return kv8_attn_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, weights);
+}
+}  // namespace
+
 int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q, int32_t with_weights,
                            size_t* out_host) {
   int st = check_dims(dims);
   if (st) return st;
   if (!out_host || n_seq < 1 || capacity < 1 || n_q < 0) return fail(CB_ERR_INVALID_ARG, "workspace query arguments");
-  *out_host = kv8_attn_ws_bytes(n_seq, dims->n_kv_heads, dims->n_heads / dims->n_kv_heads, n_q, capacity,
-                                with_weights != 0);
+  *out_host = kv8_ws(dims, n_seq, capacity, n_q, with_weights != 0);
   return CB_OK;
 }
 
@@ -1265,9 +1279,15 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   if ((int64_t)n_q * G > (1 << 27)) return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
   if (!q || !last || !out) return fail(CB_ERR_INVALID_ARG, "kv8_attention pointer is NULL");
   if ((st = check_al16({q, out, weights, ws}, "kv8_attention"))) return st;
-  const size_t need = kv8_attn_ws_bytes(cache->n_seq, Hkv, G, n_q, cache->capacity, weights != nullptr);
+  const size_t need = kv8_ws(dims, cache->n_seq, cache->capacity, n_q, weights != nullptr);
   if (need && (!ws || ws_bytes < need)) return fail(CB_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
   const int64_t m = (int64_t)cache->n_seq * n_q;
+  if (kv8_tc_taken(dims->dtype, hd, G, n_q)) {
+    CB_LAUNCH(CB_PROF_KV8_ATTN, 2, m, cache->capacity, H, 0.0, 0.0, S(stream),
+              launch_kv8_tc(q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
+    g_launches.fetch_add(weights ? 2 : 1, std::memory_order_relaxed);
+    return CB_OK;
+  }
   CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),
             launch_kv8_attn(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
   if (weights && kv8_attn_weights_apart(G, n_q))
@@ -1359,6 +1379,7 @@ void cb_shutdown(void) {
   reset_attn_tc_caches();
   reset_kv8_caches();
   reset_kv8_attn_caches();
+  reset_kv8_tc_caches();
   reset_logits_caches();
   ProfState& P = g_prof;
   bool failed = false;

@@ -193,9 +193,11 @@ uint32_t take_error_attn();
 // (the launchers take cb_kv8_cache / cb_logit_rules and are declared where they are called)
 uint32_t take_error_kv8();
 uint32_t take_error_kv8_attn();
+uint32_t take_error_kv8_tc();
 uint32_t take_error_logits();
 void reset_kv8_caches();
 void reset_kv8_attn_caches();
+void reset_kv8_tc_caches();
 void reset_logits_caches();
 
 }  // namespace cb

@@ -12,8 +12,8 @@
 //
 // Rounding: q goes to fp16 after a division by a power of two per row (its 8 bf16 bits fit in
 // fp16's 11; an element 2^14 below the row's largest loses bits that are 2^-25 of that
-// largest), fp32 q as two such parts (22 bits).  2^(t - m) is rounded to fp16 (2^-12) beside
-// the rounding of the bf16 output (2^-9), for fp32 output split in two parts.  Sums, maxima
+// largest), fp32 q as two such parts (22 bits).  2^(t - m) is rounded to fp16 (2^-11) beside
+// the rounding of the bf16 output (2^-8), for fp32 output split in two parts.  Sums, maxima
 // and accumulators are fp32.
 #include <math.h>
 
@@ -75,17 +75,8 @@ __device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t p) {
   return pack_h2(a - f.x, b - f.y);
 }
 
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   tc::smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
-               : "memory");
-}
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
+using tc::bulk_load;
+using tc::ld_cluster;
 
 struct Kv8Attn {
   const void* q;
@@ -206,8 +197,9 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
       return (lane < L::NG ? ksc : vsc)[key >> p.lg];
     };
     float sc = scale_of(t0);
-    for (int j = t0; j < t1; ++j) {
-      const int u = j - t0, st = u % L::NST;
+    int u = 0;
+    for (; u < t1 - t0; ++u) {
+      const int j = t0 + u, st = u % L::NST;
       const float nxt = scale_of(j + 1);
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[st], ((u / L::NST) & 1) ^ 1));
       if (!ok) break;
@@ -231,6 +223,8 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
       __syncwarp();
     }
     if (!ok && lane == 0) atomicOr(&g_err_kv8_attn, ERRBIT_TIMEOUT);
+    // no copy is in flight when the CTA goes on, whoever gave up on what
+    for (int k = u > L::NST ? u - L::NST : 0; k < u; ++k) tc::mbar_wait(&full[k % L::NST], (k / L::NST) & 1);
   } else {
     // ------------------------------------------------------------------ consumer warps
     const bool upper = nrow > 8;                              // rows 8..15 exist
@@ -303,10 +297,7 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
     for (int j = t0; j < t1; ++j) {
       const int u = j - t0, st = u % L::NST;
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[st], (u / L::NST) & 1));
-      if (!ok) {       // give the copies in flight as long again before the memory is given up
-        tc::mbar_wait(&full[st], (u / L::NST) & 1);
-        break;
-      }
+      if (!ok) break;
       const uint8_t* sk = base + st * 2 * L::HALF;
       const float* sc = ssc + st * 3 * L::NG;
 #pragma unroll 1
@@ -558,9 +549,11 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
       for (int c = 0; c < n_split; ++c) {
         const float f = pf[c * ROWS + r];
         if (f == 0.f) continue;            // also a CTA without visible keys
-        const uint32_t a = tc::mapa_shared(om_a + 16 * i, c);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = fmaf(ld_cluster(a + 4 * q), f, o[q]);
+        const float4 v = tc::ld_cluster4(tc::mapa_shared(om_a + 16 * i, c));
+        o[0] = fmaf(v.x, f, o[0]);
+        o[1] = fmaf(v.y, f, o[1]);
+        o[2] = fmaf(v.z, f, o[2]);
+        o[3] = fmaf(v.w, f, o[3]);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[q] *= fm[r];

@@ -1,0 +1,847 @@
+// Attention of many query rows over the 8-bit block-scaled KV cache on the tensor cores (bf16,
+// head_dim 64 or 128), and the attention weight each cache row receives from them.
+//
+// The mathematics is cb_kv8_attn.cu's: the codes enter the matrix instructions exactly, K's
+// scale multiplies a score, V's scale sits in the exponent (t = z + log2 vs) and leaves the
+// row sum by a multiplication with 1 / vs.  Here
+//   S_j = Q C_K,j^T    tcgen05.mma, bf16 x bf16 (an 8-bit code is exact in bf16), into TMEM
+//   P_j = 2^(t - m)    softmax warps, fp16, back into TMEM
+//   O  += P_j C_V,j    tcgen05.mma, fp16 x fp16, P from TMEM
+// k_kv8_expand turns the codes into those two forms once per call, already in the swizzled
+// order the tensor cores read, so that a tile is one bulk copy and no tensor map is needed:
+// every key tile is read by n_q G / 128 CTAs, and converting it in each of them would cost
+// more issue slots than the softmax itself (26 instructions per 16 codes, against one pass
+// over 5 bytes per code).
+//
+// Rows of one KV head are packed into tiles: row r of a tile is query r / G, head r % G, so
+// a few queries of grouped heads fill a tile and a tile's rows share one narrow run of
+// positions.  Small grids split the keys over a cluster of CTAs, merged through distributed
+// shared memory.
+#include <math.h>
+
+#include <mutex>
+
+#include "cb_kv8.cuh"
+#include "cb_tc.cuh"
+
+namespace cb {
+
+static __device__ uint32_t g_err_kv8_tc;
+
+uint32_t take_error_kv8_tc() {
+  uint32_t v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_kv8_tc, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
+  cudaMemcpyToSymbol(g_err_kv8_tc, &z, sizeof(z));
+  return v;
+}
+
+namespace {
+
+using tc::f2_add;
+using tc::f2_fma;
+using tc::f2_pack;
+using tc::f2_unpack;
+using tc::fmax3;
+
+constexpr int BM = 128;              // query rows per tile
+constexpr int BN = 128;              // keys per tile
+constexpr int SLAB = 128 * 128;      // bytes of one [128 rows x 64 elements] swizzled slab
+constexpr int NSOFT = 8;             // softmax warps: two groups of one per TMEM lane quarter
+constexpr int THREADS = 32 * (2 + NSOFT);
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int NG = BN / 16;          // scale groups of a key tile
+constexpr float kPBias = 8.0f;       // as in cb_kv8_attn.cu: weights up to 2^8, 2^14 before m is raised
+constexpr float kLazy = 6.0f;
+
+struct Kv8Tc {
+  const bf16* q;
+  const int32_t* last;      // [n_seq, n_q]
+  bf16* out;
+  const uint8_t* kx;        // [n_seq * Hkv, tiles] key tiles in shared-memory order: bf16 codes
+  const uint8_t* vx;        // the same of V: fp16 codes
+  float* lse;               // [n_seq * Hkv, n_q * G] log2 of a row's sum, or null
+  float* weights;           // [n_seq, Hkv, capacity]
+  cb_kv8_cache c;
+  int n_q, H, Hkv, G, lg, tiles;
+  int qpt;                  // queries per tile: 128 / G
+  float scale_log2;
+};
+
+__device__ __forceinline__ int last_of(const Kv8Tc& p, int s, int j) {
+  const int l = p.last[(int64_t)s * p.n_q + j];
+  return l < -1 || l >= p.c.capacity ? -1 : l;
+}
+
+// ---- codes to matrix operands -------------------------------------------------------------
+// byte c of w as bf16 / fp16 pairs.  fp16: byte ^ 0x80 = c + 128, 0x6400 | u is 1024 + u.
+// bf16 (7 mantissa bits): 0x4300 | (c & 127) is 128 + (c & 127); from it 128 is taken, or 256
+// where the code is negative (0x4300 | (c & 128) is 128 or 256).
+__device__ __forceinline__ uint32_t pair_f16(uint32_t u, uint32_t sel) {
+  const uint32_t x = __byte_perm(u, 0x64646464u, sel);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pair_bf16(uint32_t w, uint32_t sel) {
+  const uint32_t x = __byte_perm(w, 0x43434343u, sel);
+  const uint32_t a = x & 0xff7fff7fu, b = x & 0xff80ff80u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// One CTA per (key tile, KV head, sequence): 128 rows of K and V codes to bf16 / fp16 in
+// 128-byte-swizzled slabs.  Tiles no query sees are skipped.
+template <int HD>
+__global__ void __launch_bounds__(256) k_kv8_expand(const Kv8Tc p) {
+  pdl_wait();
+  pdl_trigger();
+  const int tile = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
+  // some query sees the tile's first key?  (the newest rows usually come last)
+  bool need = false;
+  for (int j = p.n_q - 1 - (int)threadIdx.x; !need; j -= 256) {
+    const bool in = j >= 0 && last_of(p, s, j) >= tile * BN;
+    need = __syncthreads_or(in);
+    if (__syncthreads_and(j < 256)) break;
+  }
+  if (!need) return;
+  const int64_t head = (int64_t)s * p.Hkv + h, row0 = (int64_t)tile * BN;
+  const int64_t src = (head * p.c.capacity + row0) * HD, dst = (head * p.tiles + tile) * (int64_t)(BN * HD * 2);
+  constexpr int PER = HD / 16;             // pieces of 16 codes in a row
+#pragma unroll
+  for (int i = 0; i < BN * PER / 256; ++i) {
+    const int idx = i * 256 + threadIdx.x, row = idx / PER, piece = idx % PER;
+    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    if (row0 + row < p.c.capacity) {
+      k = *reinterpret_cast<const uint4*>(p.c.k_codes + src + row * HD + piece * 16);
+      v = *reinterpret_cast<const uint4*>(p.c.v_codes + src + row * HD + piece * 16);
+    }
+    const uint32_t kw[4] = {k.x, k.y, k.z, k.w}, vw[4] = {v.x, v.y, v.z, v.w};
+    uint8_t* kd = const_cast<uint8_t*>(p.kx) + dst + (piece >> 2) * SLAB + row * 128;
+    uint8_t* vd = const_cast<uint8_t*>(p.vx) + dst + (piece >> 2) * SLAB + row * 128;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int at = ((2 * (piece & 3) + c) ^ (row & 7)) * 16;
+      const uint32_t u0 = vw[2 * c] ^ 0x80808080u, u1 = vw[2 * c + 1] ^ 0x80808080u;
+      *reinterpret_cast<uint4*>(kd + at) =
+          make_uint4(pair_bf16(kw[2 * c], 0x4140), pair_bf16(kw[2 * c], 0x4342), pair_bf16(kw[2 * c + 1], 0x4140),
+                     pair_bf16(kw[2 * c + 1], 0x4342));
+      *reinterpret_cast<uint4*>(vd + at) =
+          make_uint4(pair_f16(u0, 0x4140), pair_f16(u0, 0x4342), pair_f16(u1, 0x4140), pair_f16(u1, 0x4342));
+    }
+  }
+}
+
+// ---- shared pieces --------------------------------------------------------------------------
+// Row r of the tile whose first query is j0 (may be negative: the first tile is cut short).
+struct Row {
+  int j, g;
+  bool on;
+};
+__device__ __forceinline__ Row row_of(const Kv8Tc& p, int j0, int r) {
+  Row x;
+  const int jl = r / p.G;
+  x.j = j0 + jl;
+  x.g = r - jl * p.G;
+  x.on = jl < p.qpt && x.j >= 0;
+  return x;
+}
+
+// Gathers a tile's query rows into swizzled slabs with 16-byte asynchronous copies (rows that
+// do not exist are zero); the caller waits for them and fences.
+template <int HD>
+__device__ __forceinline__ void gather_q(const Kv8Tc& p, int s, int h, int j0, uint8_t* dst, int tid, int n_thr) {
+  constexpr int PER = HD / 8;              // 16-byte pieces in a row
+  for (int i = tid; i < BM * PER; i += n_thr) {
+    const int r = i / PER, piece = i % PER;
+    const Row x = row_of(p, j0, r);
+    const bf16* src = p.q + (((int64_t)s * p.n_q + (x.on ? x.j : 0)) * p.H + (int64_t)h * p.G + (x.on ? x.g : 0)) * HD + piece * 8;
+    const uint32_t d = tc::smem_u32(dst + (piece >> 3) * SLAB + r * 128 + (((piece & 7) ^ (r & 7)) * 16));
+    const int bytes = x.on ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+  }
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// ---- attention ------------------------------------------------------------------------------
+template <int HD>
+struct Layout {
+  static constexpr int NSLAB = HD / 64;
+  static constexpr int T_BYTES = NSLAB * SLAB;               // a tile of Q, K or V
+  static constexpr int STAGES = HD == 128 ? 5 : 10;          // ring K_0, V_0, K_1, V_1, ...
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = T_BYTES;
+  static constexpr int OFF_X = OFF_KV + STAGES * T_BYTES;    // [2 groups][2][BM] row max, row sum
+  static constexpr int OFF_ML = OFF_X + 4 * BM * 4;          // [2][BM] the CTA's row max and sum, read by the cluster
+  static constexpr int OFF_SC = OFF_ML + 2 * BM * 4;         // [NSOFT][NG] float4 {ks, log2 vs, 1/vs, -}
+  static constexpr int OFF_BAR = OFF_SC + NSOFT * NG * 16;
+  static constexpr int BYTES = OFF_BAR + 256;
+  static constexpr int SMEM = BYTES + 1024;
+  static_assert((6 + 2 * STAGES) * 8 + 8 <= 256, "barriers exceed their region");
+  static_assert(BM * HD * 4 <= STAGES * T_BYTES, "the merge buffer exceeds the ring");
+  static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
+};
+constexpr uint32_t TM_O = 2 * BN;    // O_0 at column 256, O_1 right after it
+
+// A warp's scales of one key tile: lane l < NG loads group l's pair (1 past the visible keys:
+// the block may never have been written).
+struct Scales {
+  float k, v;
+};
+__device__ __forceinline__ Scales load_scales(const float* ks, const float* vs, int lg, int tile, int64_t nk, int lane) {
+  Scales r{1.0f, 1.0f};
+  const int64_t key = (int64_t)tile * BN + 16 * lane;
+  if (lane < NG && key < nk) {
+    r.k = ks[key >> lg];
+    r.v = vs[key >> lg];
+  }
+  return r;
+}
+
+// One key tile of a softmax group; a thread owns one row of S_g and O_g in TMEM.  sc: the
+// tile's scale groups in the warp's own shared memory.
+template <int HD>
+__device__ __forceinline__ bool softmax_tile(uint64_t* s_full_g, uint64_t* p_full_g, uint64_t* pv_done_g, uint32_t u,
+                                             int key0, int last, uint32_t tS, uint32_t tO, const float4* sc,
+                                             float& m_used, float& l, int lane) {
+  if (!__all_sync(0xffffffffu, tc::mbar_wait(s_full_g, u & 1))) return false;
+  const bool none = __all_sync(0xffffffffu, key0 > last);
+  const bool full_row = key0 + BN - 1 <= last;
+  float mt = -INFINITY;
+  if (!none) {
+    tc::tc_fence_after();
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t sr[64];
+      tc::tmem_ld32_nowait(tS + hf * 64, sr);
+      tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int gg = 0; gg < 4; ++gg) {
+        float a = -INFINITY, b = -INFINITY;
+        if (full_row) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            a = fmax3(a, __uint_as_float(sr[gg * 16 + i]), __uint_as_float(sr[gg * 16 + i + 1]));
+            b = fmax3(b, __uint_as_float(sr[gg * 16 + i + 2]), __uint_as_float(sr[gg * 16 + i + 3]));
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (key0 + hf * 64 + gg * 16 + i <= last) a = fmaxf(a, __uint_as_float(sr[gg * 16 + i]));
+        }
+        const float4 c = sc[hf * 4 + gg];
+        mt = fmaxf(mt, fmaf(fmaxf(a, b), c.x, c.y));
+      }
+    }
+  }
+  if (u == 0) {
+    m_used = mt;               // O_g is written, not added to, by this tile's P.V
+  } else {
+    const bool need = mt > m_used + kLazy;
+    if (__any_sync(0xffffffffu, need)) {
+      // O_g must be stable: the group's previous P.V has completed
+      if (!__all_sync(0xffffffffu, tc::mbar_wait(pv_done_g, (u - 1) & 1))) return false;
+      tc::tc_fence_after();
+      const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
+#pragma unroll 1
+      for (int c = 0; c < HD / 16; ++c) {
+        float o[16];
+        tc::tmem_ld16(tO + c * 16, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+        tc::tmem_st16(tO + c * 16, o);
+      }
+      l *= alpha;
+      if (need) m_used = mt;
+    }
+  }
+  const float off = kPBias - (m_used == -INFINITY ? 0.f : m_used);
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t sr[64];
+    if (!none) {
+      tc::tmem_ld32_nowait(tS + hf * 64, sr);
+      tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
+      tc::tmem_wait_ld();
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t pk[16];
+      if (none) {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) pk[w] = 0u;
+      } else {
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+          const float4 k = sc[hf * 4 + c * 2 + gg];
+          const uint64_t f2 = f2_pack(k.x, k.x), a2 = f2_pack(k.y + off, k.y + off);
+          uint64_t sum = 0ull;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            const int k0 = c * 32 + gg * 16 + 2 * w, key = key0 + hf * 64 + k0;
+            const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, a2));
+            float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
+            if (!full_row) {
+              p0 = key <= last ? p0 : 0.f;
+              p1 = key + 1 <= last ? p1 : 0.f;
+            }
+            sum = f2_add(sum, f2_pack(p0, p1));
+            const __half2 h2 = __floats2half2_rn(p0, p1);
+            pk[gg * 8 + w] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          const float2 sm = f2_unpack(sum);
+          l = fmaf(sm.x + sm.y, k.z, l);
+        }
+      }
+      tc::tmem_st16u_nowait(tS + hf * 32 + c * 16, pk);
+    }
+  }
+  tc::tmem_wait_st();
+  tc::tc_fence_before();
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(p_full_g);
+  return true;
+}
+
+// Two softmax groups take alternate key tiles (TMEM: S_0 | S_1 | O_0 | O_1), merged at the
+// end; a cluster's CTAs take consecutive runs of key tiles.  Warp roles: 0 = copies, 1 = TMEM
+// allocation and MMA issue, 2..9 = softmax; all gather Q first.
+template <int HD>
+__global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n_split) {
+  pdl_wait();
+  pdl_trigger();
+  using L = Layout<HD>;
+  constexpr int NST = L::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sQ = base + L::OFF_Q;
+  uint8_t* sKV = base + L::OFF_KV;
+  float* xm = reinterpret_cast<float*>(base + L::OFF_X);   // [2][BM] row max, then [2][BM] row sum
+  float* xl = xm + 2 * BM;
+  float* cm = reinterpret_cast<float*>(base + L::OFF_ML);  // [BM] max, [BM] sum
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
+  uint64_t* s_full = bars;         // [2] per group: S_g holds a tile's scores
+  uint64_t* p_full = bars + 2;     // [2] the group's four warps wrote P
+  uint64_t* pv_done = bars + 4;    // [2] P V into O_g completed
+  uint64_t* kv_full = bars + 6;    // [NST]
+  uint64_t* kv_empty = kv_full + NST;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + NST);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % n_split, h = blockIdx.x / n_split, s = blockIdx.z;
+  // tiles are cut from the end of the queries: the longest rows come first, and the tile that
+  // is cut short is the one with the lowest positions
+  const int j0 = p.n_q - (int)(blockIdx.y + 1) * p.qpt;
+  const int64_t head = (int64_t)s * p.Hkv + h;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_full[i], 4);
+      tc::mbar_init(&pv_done[i], 1);
+    }
+    for (int i = 0; i < NST; ++i) {
+      tc::mbar_init(&kv_full[i], 1);
+      tc::mbar_init(&kv_empty[i], 1);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  gather_q<HD>(p, s, h, j0, sQ, tid, THREADS);
+  // keys that some row of the tile sees
+  int mx = -1;
+  for (int i = tid; i < p.qpt; i += THREADS) {
+    const int j = j0 + i;
+    if (j >= 0) {
+      const int l = p.last[(int64_t)s * p.n_q + j];
+      if ((l < -1 || l >= p.c.capacity) && rank == 0) atomicOr(&g_err_kv8_tc, ERRBIT_INDEX);
+      mx = max(mx, last_of(p, s, j));
+    }
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  int* wm = reinterpret_cast<int*>(xm);
+  if (lane == 0) wm[warp] = mx;
+  cp_async_wait_all();
+  tc::fence_proxy_async_smem();
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) mx = max(mx, wm[w]);
+  __syncthreads();                 // wm's memory is the groups' row maxima later on
+  const int64_t nk = (int64_t)mx + 1;
+  const int all = (mx + BN) / BN;  // key tiles; 0 if no row sees a key
+  const int ta = (int)((int64_t)all * rank / n_split), T = (int)((int64_t)all * (rank + 1) / n_split) - ta;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ copies
+    if (lane == 0) {
+      const uint8_t* kx = p.kx + (head * p.tiles + ta) * (int64_t)L::T_BYTES;
+      const uint8_t* vx = p.vx + (head * p.tiles + ta) * (int64_t)L::T_BYTES;
+      int i = 0;
+      for (; i < 2 * T; ++i) {
+        const int st = i % NST;
+        if (!tc::mbar_wait(&kv_empty[st], ((i / NST) & 1) ^ 1)) {
+          atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+          break;
+        }
+        tc::mbar_expect_tx(&kv_full[st], L::T_BYTES);
+        tc::bulk_load(sKV + st * L::T_BYTES, ((i & 1) ? vx : kx) + (int64_t)(i >> 1) * L::T_BYTES, L::T_BYTES, &kv_full[st]);
+      }
+      // no copy is in flight when the CTA ends, whoever gave up on what
+      for (int k = i > NST ? i - NST : 0; k < i; ++k) tc::mbar_wait(&kv_full[k % NST], (k / NST) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issue
+    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN);
+    constexpr uint32_t idesc_o = tc::idesc_f16_f32(BM, HD, true);
+    const uint64_t kv_desc = tc::desc_sw128(tc::smem_u32(sKV));
+    const uint64_t v_desc = tc::desc_sw128_mn(tc::smem_u32(sKV), SLAB);
+    const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(sQ));
+    bool ok = true;
+    auto issue_s = [&](int jj) {
+      const int b = jj & 1, i = 2 * jj, st = i % NST;
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&kv_full[st], (i / NST) & 1) &&
+                                             (jj < 2 || tc::mbar_wait(&pv_done[b], ((jj - 2) >> 1) & 1)));
+      if (!ok) return;
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+        const uint64_t kd = kv_desc + (uint64_t)((st * L::T_BYTES) >> 4);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+          tc::mma_bf16(tmem + b * BN, q_desc + off, kd + off, idesc_s, k > 0);
+        }
+        tc::mma_commit(&s_full[b]);
+        tc::mma_commit(&kv_empty[st]);
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int jj) {
+      const int b = jj & 1, i = 2 * jj + 1, st = i % NST;
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&p_full[b], (jj >> 1) & 1) &&
+                                             tc::mbar_wait(&kv_full[st], (i / NST) & 1));
+      if (!ok) return;
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+        const uint64_t vd = v_desc + (uint64_t)((st * L::T_BYTES) >> 4);
+#pragma unroll
+        for (int k = 0; k < BN / 16; ++k)
+          tc::mma_bf16_ts(tmem + TM_O + b * HD, tmem + b * BN + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc_o,
+                          (jj >= 2 || k > 0) ? 1u : 0u);
+        tc::mma_commit(&pv_done[b]);
+        tc::mma_commit(&kv_empty[st]);
+      }
+      __syncwarp();
+    };
+    if (T > 0) issue_s(0);
+    if (T > 1) issue_s(1);
+    for (int jj = 0; ok && jj < T; ++jj) {
+      issue_pv(jj);
+      if (jj + 2 < T) issue_s(jj + 2);
+    }
+    if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+  } else {
+    // ------------------------------------------------------------------ softmax
+    const int grp = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const Row x = row_of(p, j0, r);
+    const int last = x.on ? last_of(p, s, x.j) : -1;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int64_t nblk = p.c.capacity >> p.lg;
+    const float* ks = p.c.k_scale + head * nblk;
+    const float* vs = p.c.v_scale + head * nblk;
+    float4* sc = reinterpret_cast<float4*>(base + L::OFF_SC) + (warp - 2) * NG;
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    int u = 0;
+    Scales nx = load_scales(ks, vs, p.lg, ta + grp, nk, lane);
+    for (int j = grp; j < T; j += 2, ++u) {
+      if (!ok) break;
+      __syncwarp();
+      if (lane < NG) {
+        const float v = fmaxf(nx.v, kKv8MinScale);
+        sc[lane] = make_float4(fmaxf(nx.k, kKv8MinScale) * p.scale_log2, log2f(v), 1.0f / v, 0.f);
+      }
+      nx = load_scales(ks, vs, p.lg, ta + j + 2, nk, lane);
+      __syncwarp();
+      ok = softmax_tile<HD>(&s_full[grp], &p_full[grp], &pv_done[grp], (uint32_t)u, (ta + j) * BN, last, trow + grp * BN,
+                            trow + TM_O + grp * HD, sc, m_used, l, lane);
+    }
+    // the group's last P.V, then both groups' row statistics meet in shared memory
+    const bool done = ok && (u == 0 || __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[grp], (u - 1) & 1)));
+    if (!done && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+    xm[grp * BM + r] = m_used;
+    xl[grp * BM + r] = l;
+    tc::tc_fence_before();
+    asm volatile("bar.sync 1, %0;" ::"n"(NSOFT * 32) : "memory");
+    tc::tc_fence_after();
+    const float ma = xm[r], mb = xm[BM + r], mm = fmaxf(ma, mb);
+    const float a0 = ma == -INFINITY ? 0.f : tc::ex2_approx(ma - mm);
+    const float a1 = mb == -INFINITY ? 0.f : tc::ex2_approx(mb - mm);
+    const float lt = xl[r] * a0 + xl[BM + r] * a1;
+    const float inv = lt > 0.f ? 1.0f / lt : 0.f;
+    if (grp == 0) {
+      if (n_split > 1) {
+        cm[r] = mm;
+        cm[BM + r] = lt;
+      } else if (p.lse && x.on) {
+        p.lse[head * p.n_q * p.G + (int64_t)x.j * p.G + x.g] = lt > 0.f ? mm - kPBias + log2f(lt) : INFINITY;
+      }
+    }
+    // group g finalises columns [g HD/2, (g + 1) HD/2); O_g was never written with fewer than
+    // g + 1 key tiles
+    float* om = reinterpret_cast<float*>(sKV) + r * HD;
+    bf16* orow = p.out + (((int64_t)s * p.n_q + (x.on ? x.j : 0)) * p.H + (int64_t)h * p.G + (x.on ? x.g : 0)) * HD;
+#pragma unroll 1
+    for (int c = 0; c < HD / 32; ++c) {
+      const int col = grp * (HD / 2) + c * 16;
+      float o0[16], o1[16];
+      if (T > 0) {
+        tc::tmem_ld16(trow + TM_O + col, o0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o0[i] = 0.f;
+      }
+      if (T > 1) {
+        tc::tmem_ld16(trow + TM_O + HD + col, o1);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o1[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o0[i] = o0[i] * a0 + o1[i] * a1;
+      if (n_split > 1) {
+        // 16-byte words rotated by the row, so that the rows of a warp spread over the banks
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(om + (((col >> 2) + i) ^ (r & 7)) * 4) =
+              make_float4(o0[4 * i], o0[4 * i + 1], o0[4 * i + 2], o0[4 * i + 3]);
+      } else if (x.on) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o0[i] *= inv;
+        st8(orow + col, o0);
+        st8(orow + col + 8, o0 + 8);
+      }
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (n_split > 1) {
+    // ------------------------------------------------------------------ merge of the cluster
+    tc::cluster_sync();
+    const uint32_t cm_a = tc::smem_u32(cm), om_a = tc::smem_u32(sKV);
+    const int per = BM / n_split, r0 = rank * per;        // this CTA's share of the rows
+    constexpr int W4 = HD / 4;
+    for (int i = tid; i < per * W4; i += THREADS) {
+      const int r = r0 + i / W4, w = i % W4;
+      const Row x = row_of(p, j0, r);
+      if (!x.on) continue;
+      float M = -INFINITY, sum = 0.f;
+      for (int c = 0; c < n_split; ++c) M = fmaxf(M, tc::ld_cluster(tc::mapa_shared(cm_a + 4 * r, c)));
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < n_split; ++c) {
+        const float mc = tc::ld_cluster(tc::mapa_shared(cm_a + 4 * r, c));
+        if (mc == -INFINITY) continue;
+        const float f = tc::ex2_approx(mc - M);
+        sum = fmaf(tc::ld_cluster(tc::mapa_shared(cm_a + 4 * (BM + r), c)), f, sum);
+        const float4 v = tc::ld_cluster4(tc::mapa_shared(om_a + 4 * (r * HD + (w ^ (r & 7)) * 4), c));
+        o[0] = fmaf(v.x, f, o[0]);
+        o[1] = fmaf(v.y, f, o[1]);
+        o[2] = fmaf(v.z, f, o[2]);
+        o[3] = fmaf(v.w, f, o[3]);
+      }
+      const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[q] *= inv;
+      st4(p.out + (((int64_t)s * p.n_q + x.j) * p.H + (int64_t)h * p.G + x.g) * HD + 4 * w, o);
+      if (p.lse && w == 0)
+        p.lse[head * p.n_q * p.G + (int64_t)x.j * p.G + x.g] = sum > 0.f ? M - kPBias + log2f(sum) : INFINITY;
+    }
+    tc::cluster_sync();            // the peers may still be reading this CTA's part
+  }
+  if (warp == 1) {
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// ---- weights --------------------------------------------------------------------------------
+// One CTA per (128 keys, KV head, sequence): S^T = C_K Q^T puts a key in each TMEM lane, so the
+// sum over the query rows stays inside a thread.  Row tiles go round four S buffers (TMEM 4 x
+// 128 columns); two softmax groups take alternate tiles, and their two sums per key meet at the
+// end.  Each Q tile is gathered by the softmax group that will read its scores, right after it
+// has finished the tile before.
+template <int HD>
+struct WLayout {
+  static constexpr int T_BYTES = HD / 64 * SLAB;
+  static constexpr int QS = 4;                                // Q tiles: two per group
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_Q = T_BYTES;
+  static constexpr int OFF_L = OFF_Q + QS * T_BYTES;          // [QS][BM] float2 {log2 sum, last}
+  static constexpr int OFF_X = OFF_L + QS * BM * 8;           // [BM] the second group's sums
+  static constexpr int OFF_BAR = OFF_X + BM * 4;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
+};
+
+template <int HD>
+__global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
+  pdl_wait();
+  pdl_trigger();
+  using L = WLayout<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* sK = base + L::OFF_K;
+  uint8_t* sQ = base + L::OFF_Q;
+  float2* sL = reinterpret_cast<float2*>(base + L::OFF_L);
+  float* sx = reinterpret_cast<float*>(base + L::OFF_X);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
+  uint64_t* q_full = k_full + 1;     // [QS] the group's four warps gathered a Q tile
+  uint64_t* s_full = q_full + L::QS; // [QS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + L::QS);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int key0 = blockIdx.x * BN, h = blockIdx.y, s = blockIdx.z;
+  const int64_t head = (int64_t)s * p.Hkv + h;
+  const int n_tiles = (p.n_q + p.qpt - 1) / p.qpt;
+  if (tid == 0) {
+    tc::mbar_init(k_full, 1);
+    for (int i = 0; i < L::QS; ++i) {
+      tc::mbar_init(&q_full[i], 4);
+      tc::mbar_init(&s_full[i], 1);
+    }
+    tc::fence_mbar_init();
+  }
+  // does any query see the first key?
+  bool need = false;
+  for (int j = p.n_q - 1 - tid; !need; j -= THREADS) {
+    need = __syncthreads_or(j >= 0 && last_of(p, s, j) >= key0);
+    if (__syncthreads_and(j < THREADS)) break;
+  }
+  if (!need) return;
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tc::mbar_expect_tx(k_full, L::T_BYTES);
+      tc::bulk_load(sK, p.kx + (head * p.tiles + blockIdx.x) * (int64_t)L::T_BYTES, L::T_BYTES, k_full);
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(BN, BM);
+    const uint64_t k_desc = tc::desc_sw128(tc::smem_u32(sK)), q_desc = tc::desc_sw128(tc::smem_u32(sQ));
+    bool ok = __all_sync(0xffffffffu, tc::mbar_wait(k_full, 0));
+    for (int y = 0; ok && y < n_tiles; ++y) {
+      // q_full also says that the group has read the scores this S buffer held four tiles ago
+      const int b = y % L::QS;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (y / L::QS) & 1));
+      if (!ok) break;
+      tc::tc_fence_after();
+      if (tc::elect_one()) {
+        const uint64_t qd = q_desc + (uint64_t)((b * L::T_BYTES) >> 4);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+          tc::mma_bf16(tmem + b * BM, k_desc + off, qd + off, idesc, k > 0);
+        }
+        tc::mma_commit(&s_full[b]);
+      }
+      __syncwarp();
+    }
+    if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+  } else {
+    const int grp = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const int gt = (warp - 2 - 4 * grp) * 32 + lane;       // thread of the group
+    const int key = key0 + r;
+    const bool live = key < p.c.capacity;
+    float f = 0.f;
+    if (live) f = fmaxf(p.c.k_scale[head * (p.c.capacity >> p.lg) + (key >> p.lg)], kKv8MinScale) * p.scale_log2;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const float* lse = p.lse + head * p.n_q * p.G;
+    // starts gathering Q tile y, with its rows' sums and bounds, into its buffer ...
+    auto gather = [&](int y) {
+      const int b = y % L::QS, j0 = p.n_q - (y + 1) * p.qpt;
+      gather_q<HD>(p, s, h, j0, sQ + b * L::T_BYTES, gt, 128);
+      const Row x = row_of(p, j0, gt);
+      float2 v = make_float2(INFINITY, __int_as_float(-1));
+      if (x.on) v = make_float2(lse[(int64_t)x.j * p.G + x.g], __int_as_float(last_of(p, s, x.j)));
+      sL[b * BM + gt] = v;
+    };
+    // ... and hands it to the tensor core
+    auto gathered = [&](int y) {
+      cp_async_wait_all();
+      tc::fence_proxy_async_smem();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full[y % L::QS]);
+    };
+    float sum = 0.f;
+    bool ok = true;
+    if (grp < n_tiles) {
+      gather(grp);
+      gathered(grp);
+    }
+    for (int y = grp; y < n_tiles; y += 2) {
+      const int b = y % L::QS;
+      // every warp of the group has gathered its part of tile y, and did so after reading the
+      // scores of tile y - 2: the buffers of tile y + 2, which are that tile's, are free
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (y / L::QS) & 1));
+      if (!ok) break;
+      if (y + 2 < n_tiles) gather(y + 2);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[b], (y / L::QS) & 1));
+      if (!ok) break;
+      tc::tc_fence_after();
+      const float2* lb = sL + b * BM;
+#pragma unroll 1
+      for (int c = 0; c < BM / 32; ++c) {
+        uint32_t sr[32];
+        tc::tmem_ld32_nowait(trow + b * BM + c * 32, sr);
+        tc::tmem_wait_ld();
+        float acc[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float2 v = lb[c * 32 + i];
+          const float e = tc::ex2_approx(fmaf(__uint_as_float(sr[i]), f, -v.x));
+          acc[i & 1] += key <= __float_as_int(v.y) ? e : 0.f;
+        }
+        sum += acc[0] + acc[1];
+      }
+      if (y + 2 < n_tiles) gathered(y + 2);
+    }
+    cp_async_wait_all();
+    if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+    if (grp == 1) sx[r] = sum;
+    asm volatile("bar.sync 3, %0;" ::"n"(NSOFT * 32) : "memory");
+    if (grp == 0 && live) {
+      sum += sx[r];
+      float* w = p.weights + head * p.c.capacity + key;
+      if (sum != 0.f) *w += sum;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// shared-memory limits set per device and kernel, and SM counts, guarded for calls from several threads
+std::mutex g_tc_mu;
+uint32_t g_tc_attr[64];
+int g_tc_sms[64];
+
+template <int HD>
+cudaError_t prepare_tc(int dev, int* sms) {
+  constexpr uint32_t bit = HD == 128 ? 1u : 2u;
+  std::lock_guard<std::mutex> g(g_tc_mu);
+  const bool cached = dev >= 0 && dev < 64;
+  if (!cached || !(g_tc_attr[dev] & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_kv8_weights_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WLayout<HD>::SMEM);
+    int n = 0;
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    *sms = n;
+    if (cached) {
+      g_tc_attr[dev] |= bit;
+      g_tc_sms[dev] = n;
+    }
+    return cudaSuccess;
+  }
+  *sms = g_tc_sms[dev];
+  return cudaSuccess;
+}
+
+template <int HD>
+cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (e = prepare_tc<HD>(dev, &sms)) != cudaSuccess) return e;
+  if ((e = launch_k(k_kv8_expand<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
+  const int q_tiles = (p.n_q + p.qpt - 1) / p.qpt;
+  // one CTA per SM: the keys are split while that gives more of them work
+  const int64_t units = (int64_t)q_tiles * p.Hkv * p.c.n_seq;
+  int ns = 1;
+  while (ns < 8 && units * ns * 2 <= sms && 2 * ns <= p.tiles) ns *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.Hkv * ns, q_tiles, p.c.n_seq);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Layout<HD>::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ns;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  if ((e = cudaLaunchKernelEx(&cfg, k_kv8_attn_tc<HD>, p, ns)) != cudaSuccess) return e;
+  if (!p.weights) return cudaSuccess;
+  return launch_k(k_kv8_weights_tc<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(THREADS), WLayout<HD>::SMEM, s, p);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+}  // namespace
+
+void reset_kv8_tc_caches() {
+  std::lock_guard<std::mutex> g(g_tc_mu);
+  for (int i = 0; i < 64; ++i) {
+    g_tc_attr[i] = 0;
+    g_tc_sms[i] = 0;
+  }
+}
+
+// Which launches take the tensor cores: bf16, head_dim 64 or 128, and enough query rows per KV
+// head.
+bool kv8_tc_taken(int dt, int hd, int G, int n_q) {
+  return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > 64 && (n_q + BM / G - 1) / (BM / G) <= 65535;
+}
+
+size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+  const size_t tiles = (size_t)n_seq * Hkv * ((cap + BN - 1) / BN) * BN * hd * 2;
+  return 2 * align256(tiles) + (weights ? align256((size_t)n_seq * Hkv * n_q * G * 4) : 0);
+}
+
+cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
+                          void* out, float* weights, void* ws, cudaStream_t s) {
+  Kv8Tc p{};
+  p.q = static_cast<const bf16*>(q);
+  p.last = last;
+  p.out = static_cast<bf16*>(out);
+  p.c = c;
+  p.n_q = n_q;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = H / Hkv;
+  p.lg = 31 - __builtin_clz((unsigned)c.block);
+  p.tiles = (int)((c.capacity + BN - 1) / BN);
+  p.qpt = BM / p.G;
+  p.scale_log2 = 1.4426950408889634f / sqrtf((float)hd);
+  const size_t tiles = (size_t)c.n_seq * Hkv * p.tiles * BN * hd * 2;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.kx = w;
+  p.vx = w + align256(tiles);
+  if (weights) {
+    p.lse = reinterpret_cast<float*>(w + 2 * align256(tiles));
+    p.weights = weights;
+  }
+  return hd == 128 ? launch_hd<128>(p, s) : launch_hd<64>(p, s);
+}
+
+}  // namespace cb
