@@ -30,8 +30,8 @@ cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const f
 cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, const int32_t* dst_len, int n_keep,
                             const int32_t* kept, int Hkv, int hd, cudaStream_t s);
 bool kv8_attn_supported(int hd);
-size_t kv8_attn_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, bool weights);
-bool kv8_attn_weights_apart(int G, int n_q);
+size_t kv8_attn_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
+bool kv8_attn_weights_apart(int hd, int G, int n_q);
 cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
                             int hd, void* out, float* weights, void* ws, cudaStream_t s);
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
@@ -1254,7 +1254,7 @@ size_t kv8_ws(const cb_dims* d, int n_seq, int64_t cap, int n_q, bool weights) {
   const int G = d->n_heads / d->n_kv_heads;
   if (kv8_tc_taken(d->dtype, d->head_dim, G, n_q))
     return kv8_tc_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
-  return kv8_attn_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, weights);
+  return kv8_attn_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
 }
 }  // namespace
 
@@ -1290,7 +1290,7 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   }
   CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),
             launch_kv8_attn(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
-  if (weights && kv8_attn_weights_apart(G, n_q))
+  if (weights && kv8_attn_weights_apart(hd, G, n_q))
     CB_LAUNCH(CB_PROF_KV8_ATTN, 1, m, cache->capacity, H, 0.0, 0.0, S(stream),
               launch_kv8_weights(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, weights, ws, S(stream)));
   return CB_OK;
