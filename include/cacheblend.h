@@ -219,7 +219,7 @@ typedef struct {
     int8_t* v_codes;
     float*  k_scale;    /* [n_seq, Hkv, capacity / block]                                   */
     float*  v_scale;
-    int64_t capacity;   /* rows per sequence and head: a multiple of block, below 2^31      */
+    int64_t capacity;   /* rows per sequence and head: a multiple of block, at most 2^30    */
     int32_t n_seq;      /* 1..65535                                                         */
     int32_t block;      /* 16, 32, 64 or 128                                                */
 } cb_kv8_cache;
@@ -252,7 +252,7 @@ int cb_kv8_append(const void* k, const void* v, int32_t n_rows, const int32_t* s
 int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* count,
                 int32_t n_rows, const cb_dims* dims, void* k_out, void* v_out, void* stream);
 
-/* Device workspace (bytes) of cb_kv8_attention at these sizes (may be 0).  Host-only. */
+/* Device workspace (bytes) of cb_kv8_attention at these sizes.  Host-only. */
 int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q,
                            int32_t with_weights, size_t* out_host);
 

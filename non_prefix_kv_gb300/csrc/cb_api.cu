@@ -30,8 +30,8 @@ cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const f
 cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, const int32_t* dst_len, int n_keep,
                             const int32_t* kept, int Hkv, int hd, cudaStream_t s);
 bool kv8_attn_supported(int hd);
-size_t kv8_attn_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
-bool kv8_attn_weights_apart(int hd, int G, int n_q);
+size_t kv8_attn_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
+bool kv8_attn_weights_apart(int dt, int hd, int G, int n_q);
 cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
                             int hd, void* out, float* weights, void* ws, cudaStream_t s);
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
@@ -1188,8 +1188,8 @@ int check_cache(const cb_kv8_cache* c, const cb_dims* d, const char* what) {
   if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
     return fail(CB_ERR_UNSUPPORTED, "%s: block %d is not 16, 32, 64 or 128", what, c->block);
   if (c->n_seq < 1 || c->n_seq > 65535) return fail(CB_ERR_SHAPE, "%s: n_seq %d outside [1, 65535]", what, c->n_seq);
-  if (c->capacity < c->block || c->capacity % c->block || c->capacity > INT32_MAX)
-    return fail(CB_ERR_SHAPE, "%s: capacity %lld is not a multiple of block below 2^31", what, (long long)c->capacity);
+  if (c->capacity < c->block || c->capacity % c->block || c->capacity > (1 << 30))
+    return fail(CB_ERR_SHAPE, "%s: capacity %lld is not a multiple of block up to 2^30", what, (long long)c->capacity);
   if (d->n_kv_heads > 65535) return fail(CB_ERR_UNSUPPORTED, "%s: more than 65535 KV heads", what);
   return CB_OK;
 }
@@ -1254,7 +1254,7 @@ size_t kv8_ws(const cb_dims* d, int n_seq, int64_t cap, int n_q, bool weights) {
   const int G = d->n_heads / d->n_kv_heads;
   if (kv8_tc_taken(d->dtype, d->head_dim, G, n_q))
     return kv8_tc_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
-  return kv8_attn_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
+  return kv8_attn_ws_bytes(d->dtype, n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
 }
 }  // namespace
 
@@ -1277,6 +1277,9 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   if (n_q == 0) return CB_OK;
   const int H = dims->n_heads, Hkv = dims->n_kv_heads, hd = dims->head_dim, G = H / Hkv;
   if ((int64_t)n_q * G > (1 << 27)) return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
+  // the line of work is counted in 32 bits: (row tile, sequence, head, 16 keys)
+  if ((double)(((int64_t)n_q * G + 7) / 8) * cache->n_seq * Hkv * ((double)cache->capacity / 16) > (double)INT32_MAX)
+    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: query rows, sequences, heads and capacity too many for one call");
   if (!q || !last || !out) return fail(CB_ERR_INVALID_ARG, "kv8_attention pointer is NULL");
   if ((st = check_al16({q, out, weights, ws}, "kv8_attention"))) return st;
   const size_t need = kv8_ws(dims, cache->n_seq, cache->capacity, n_q, weights != nullptr);
@@ -1290,7 +1293,9 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   }
   CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),
             launch_kv8_attn(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
-  if (weights && kv8_attn_weights_apart(hd, G, n_q))
+  const bool apart = kv8_attn_weights_apart(dims->dtype, hd, G, n_q);
+  g_launches.fetch_add(weights && !apart ? 2 : 1, std::memory_order_relaxed);    // the merge, and the account
+  if (weights && apart)
     CB_LAUNCH(CB_PROF_KV8_ATTN, 1, m, cache->capacity, H, 0.0, 0.0, S(stream),
               launch_kv8_weights(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, weights, ws, S(stream)));
   return CB_OK;

@@ -17,6 +17,7 @@
 // and accumulators are fp32.
 #include <math.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "cb_kv8.cuh"
@@ -40,7 +41,7 @@ constexpr int THREADS = 32 * WARPS;
 constexpr float kPBias = 8.0f;       // 2^(t - m) is held up to 2^8 ...
 constexpr float kLazy = 6.0f;        // ... and up to 2^14 before m is raised: fp16 ends at 2^16
 constexpr float kNone = -1e30f;      // m of a row that has seen no key
-constexpr int MAX_SPLIT = 8;         // CTAs of a cluster
+constexpr int MAX_WORKERS = 4096;    // warps of the largest grid (a workspace is sized without the device)
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -77,7 +78,6 @@ __device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t p) {
 }
 
 using tc::bulk_load;
-using tc::ld_cluster;
 
 // 8 x 8 transposition of fp16 pairs across the warp: thread (g, t) gives elements (g, 2t..2t+1)
 // and gets (2t..2t+1, g)
@@ -91,49 +91,38 @@ struct Kv8Attn {
   const void* q;
   const int32_t* last;      // [n_seq, n_q]
   void* out;
+  int32_t* plan;            // [entries + 1] steps before each (sequence, row tile), times Hkv
+  float* part;              // partial results, see slot()
   float* z;                 // [n_seq * Hkv, n_q * G, capacity] scores z_i for the weights, or null
-  float* lse;               // [n_seq, Hkv, n_q * G] log2 of a row's sum, or null
-  float* weights;           // [n_seq, Hkv, capacity] (with z), or null
+  float* lse;               // [n_seq * Hkv, n_q * G] log2 of a row's sum, or null
+  float* weights;           // [n_seq, Hkv, capacity], or null
   cb_kv8_cache c;
   int n_q, H, Hkv, G, lg;
+  int rt, row_tiles;        // query rows of a tile, tiles of a sequence
   float scale_log2;         // log2(e) / sqrt(hd)
 };
 
-// A stage holds KT keys, 16 KW per warp, so that its codes are 32 KB (64 KB at head_dim 256):
-// three stages and two CTAs per SM (one at 256) keep about 190 KB of loads in flight per SM.
+// A step is 16 KW keys: 4 KB of codes (8 KB at head_dim 256).  Each warp keeps three of them in
+// flight in its own shared memory: with 16 warps per SM (8 at 256) 192 KB of loads.
 template <int HD>
 struct Lay {
-  static constexpr int KW = HD < 128 ? 128 / HD : 1;               // groups of 16 keys per warp and stage
-  static constexpr int KT = 16 * WARPS * KW;
-  static constexpr int HALF = KT * HD;                             // K (or V) codes of a stage
+  static constexpr int KW = HD < 128 ? 128 / HD : 1;               // groups of 16 keys per step
+  static constexpr int KT = 16 * KW;
+  static constexpr int HALF = KT * HD;                             // K (or V) codes of a step
   static constexpr int NST = 3;
+  static constexpr int OFF_BAR = WARPS * NST * 2 * HALF;           // [WARPS][NST]
+  static constexpr int OFF_SUM = OFF_BAR + WARPS * NST * 8;        // [THREADS] steps before a thread's entries
+  static constexpr int BYTES = OFF_SUM + THREADS * 4 + 128;
 };
-// shared memory of a CTA with row tiles of RT rows
-template <int HD, int RT, bool QS, int NS>
-struct Smem {
-  using L = Lay<HD>;
-  static constexpr int OFF_ML = L::NST * 2 * L::HALF;              // [2][WARPS][RT] row max and sum per warp
-  static constexpr int OFF_CM = OFF_ML + 2 * WARPS * RT * 4;       // [RT] CTA max, [RT] CTA sum
-  static constexpr int OFF_FM = OFF_CM + 2 * RT * 4;               // [RT] 1 / sum over the cluster, [RT] log2 of it
-  static constexpr int OFF_LAST = OFF_FM + 2 * RT * 4;             // [RT]
-  static constexpr int OFF_BAR = OFF_LAST + RT * 4;
-  static constexpr int OFF_Q = (OFF_BAR + L::NST * 16 + 16 + 15) & ~15;   // fp16 q in fragment order (when not in registers)
-  static constexpr int BYTES = OFF_Q + (QS ? NS * RT * HD * 2 : 0) + 128;
-  static_assert(WARPS * RT * HD * 4 <= OFF_ML, "the merge buffer exceeds the stages");
-  static_assert(MAX_SPLIT <= WARPS, "the factors of a cluster's CTAs reuse the warps' figures");
-};
-// fp16 parts of q and of the weights; whether q's fragments go to shared memory (two parts, or
-// more than 32 registers)
+// fp16 parts of q and of the weights
 template <typename T>
 constexpr int parts() {
   return sizeof(T) == 4 ? 2 : 1;
 }
-template <int HD, int NT, typename T>
-constexpr bool q_in_smem() {
-  return parts<T>() == 2 || NT * (HD / 16) * 2 > 32;
+template <int HD, typename T>
+constexpr int ctas_per_sm() {
+  return HD == 256 ? 1 : 2;
 }
-template <int HD, int NT, typename T>
-using SmemOf = Smem<HD, 8 * NT, q_in_smem<HD, NT, T>(), parts<T>()>;
 
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, bool on, float* f) {
@@ -144,181 +133,242 @@ __device__ __forceinline__ void load4(const T* p, bool on, float* f) {
   }
 }
 
-// One cluster of CTAs per (8 NT query rows, KV head, sequence); its CTAs take consecutive runs
-// of the visible keys and are merged through distributed shared memory.  The products are
-// taken transposed, S^T = C_K Q^T and O^T = C_V^T P^T, with the keys (then the channels) as
-// the 16 rows of mma.m16n8k16 and the query rows as its 8 columns: the few rows of a single
-// token fill the instruction (with rows as M, one token of grouped heads leaves more than half
-// of the products, accumulators and conversions' consumers empty), and a thread's share of O
-// is HD / 4 NT registers, which lets 16 warps live on an SM and hide each other's latencies.
-// There is no producing warp: whichever warp is the last to finish a stage refills it.
-// Measured before (rows as M, 10 warps per SM): 32 sequences of up to 16384 rows, 8 heads of
-// 128, 205 us = 4.1 TB/s at an issue rate of 0.33 per scheduler.
+// Row r of entry e (sequence e / row_tiles, row tile e % row_tiles): the last cache row it sees,
+// -1 where the row does not exist or its bound is bad (reported if asked).
+__device__ __forceinline__ int row_last(const Kv8Attn& p, int e, int r, bool report) {
+  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * p.rt + r;
+  if (r >= p.rt || row >= p.n_q * p.G) return -1;
+  const int l = p.last[(int64_t)s * p.n_q + row / p.G];
+  if (l < -1 || l >= p.c.capacity) {
+    if (report) atomicOr(&g_err_kv8_attn, ERRBIT_INDEX);
+    return -1;
+  }
+  return l;
+}
+
+// The line of work: unit (entry e, KV head h) holds the steps of the entry's visible keys;
+// units follow one another by entry, then head, and the line is cut into equal runs, one per
+// worker (a warp).  A run may end inside a unit and hold several; each (worker, unit) pair
+// leaves one partial result.  Along the line either the worker or the unit goes up at every
+// new pair, so worker + unit numbers the pairs' slots without a gap wider than one.
+__device__ __forceinline__ int workers_of(int total, int workers) { return max(1, min(workers, total / 2)); }
+__device__ __forceinline__ float* slot(const Kv8Attn& p, int hd, int worker, int unit) {
+  const int rows = min(p.rt, p.n_q * p.G);
+  return p.part + ((int64_t)worker + unit) * (rows * hd + 2 * p.rt);     // [rt] max, [rt] sum, [rows][hd] O
+}
+
+// Single tokens are bound by the cache's bytes, and a grid of CTAs per (sequence, head) leaves
+// a third of them on the table: with 32 sequences of 9000..16384 rows and 8 heads (841 MB) it
+// took 167 us, though one full wave of equal CTAs ran at 0.96 of the copy rate (whole waves,
+// lengths that differ, and about 10 us of start, fill and merge per CTA).  So every warp of a
+// grid that fills the machine once takes an equal run of the line above, streams it through its
+// own stages, and meets no other warp; k_kv8_merge joins the partial results.
+//
+// The products are taken transposed, S^T = C_K Q^T and O^T = C_V^T P^T, with the keys (then the
+// channels) as the 16 rows of mma.m16n8k16 and the query rows as its 8 columns: the few rows of
+// a token fill the instruction, and a thread's share of O is HD / 4 NT registers, so that 16
+// warps fit on an SM.  (With rows as M and 10 warps: 205 us at an issue rate of 0.33.)
 template <int HD, int NT, typename T>
-__global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const Kv8Attn p, int n_split) {
+__global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(const Kv8Attn p) {
   pdl_wait();
   pdl_trigger();
   using L = Lay<HD>;
-  using M = SmemOf<HD, NT, T>;
   constexpr int NS = parts<T>();
-  constexpr bool QS = q_in_smem<HD, NT, T>();
   constexpr int KS = HD / 16;                    // k steps of a score; also channel tiles of O
   constexpr int RT = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((128 - (tc::smem_u32(smem_raw) & 127)) & 127);
-  float* ml = reinterpret_cast<float*>(base + M::OFF_ML);
-  float* cm = reinterpret_cast<float*>(base + M::OFF_CM);
-  float* fm = reinterpret_cast<float*>(base + M::OFF_FM);
-  int* slast = reinterpret_cast<int*>(base + M::OFF_LAST);
-  uint64_t* full = reinterpret_cast<uint64_t*>(base + M::OFF_BAR);
-  uint32_t* spent = reinterpret_cast<uint32_t*>(full + L::NST);    // [NST] warps that have finished a stage, so far
-  uint32_t* issued = spent + L::NST;                               // stages filled so far (valid once a wait has failed)
-  uint32_t* failed = issued + 1;
-  uint2* sq = reinterpret_cast<uint2*>(base + M::OFF_Q);
-
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int rank = blockIdx.x % n_split, rt = blockIdx.x / n_split, h = blockIdx.y, s = blockIdx.z;
-  const int R = p.n_q * p.G, row0 = rt * RT, nrow = min(RT, R - row0);
-  const int64_t cap = p.c.capacity, head = (int64_t)s * p.Hkv + h;
+  uint8_t* stages = base + warp * L::NST * 2 * L::HALF;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR) + warp * L::NST;
+  int* before = reinterpret_cast<int*>(base + L::OFF_SUM);
+  const int R = p.n_q * p.G, entries = p.c.n_seq * p.row_tiles;
+  const int64_t cap = p.c.capacity;
+  if (lane == 0)
+    for (int i = 0; i < L::NST; ++i) tc::mbar_init(&full[i], 1);
+  if (lane == 0) tc::fence_mbar_init();
 
-  if (tid < RT) {
-    int l = -1;
-    if (tid < nrow) {
-      l = p.last[(int64_t)s * p.n_q + (row0 + tid) / p.G];
-      if (l < -1 || l >= cap) {
-        atomicOr(&g_err_kv8_attn, ERRBIT_INDEX);
-        l = -1;
-      }
-    }
-    slast[tid] = l;
+  // ---- where this worker's run lies: thread i sums the steps of a contiguous share of the
+  // entries, a scan over the threads places them (the first CTA writes the plan for the merge)
+  auto steps_of = [&](int e, bool report) -> int {
+    int mx = -1;
+    for (int r = 0; r < RT; ++r) mx = max(mx, row_last(p, e, r, report));
+    return (mx + L::KT) / L::KT;
+  };
+  const int share = (entries + THREADS - 1) / THREADS, e0 = min(entries, tid * share), e1 = min(entries, e0 + share);
+  int own = 0;
+  for (int e = e0; e < e1; ++e) own += steps_of(e, blockIdx.x == 0) * p.Hkv;
+  int incl = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
-  if (tid == 0) {
-    for (int i = 0; i < L::NST; ++i) {
-      tc::mbar_init(&full[i], 1);
-      spent[i] = 0;
+  __shared__ int wsum[WARPS];
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) incl += wsum[w];
+    total += wsum[w];
+  }
+  before[tid] = incl - own;
+  if (blockIdx.x == 0) {
+    int at = incl - own;
+    for (int e = e0; e < e1; ++e) {
+      p.plan[e] = at;
+      at += steps_of(e, false) * p.Hkv;
     }
-    *failed = 0;
-    tc::fence_mbar_init();
+    if (tid == 0) p.plan[entries] = total;
   }
   __syncthreads();
-  int mx = -1, mn = 0x7fffffff;
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    mx = max(mx, slast[i]);
-    if (i < nrow) mn = min(mn, slast[i]);
-  }
-  const int64_t nk = (int64_t)mx + 1;                        // keys some row sees
-  const int tiles = (int)((nk + L::KT - 1) / L::KT);
-  const int t0 = (int)((int64_t)tiles * rank / n_split), t1 = (int)((int64_t)tiles * (rank + 1) / n_split);
+  // consecutive workers sit in different CTAs, so that few of them still spread over the SMs
+  const int n_work = workers_of(total, gridDim.x * WARPS), worker = warp * gridDim.x + blockIdx.x;
+  if (worker >= n_work) return;                  // no barrier of the CTA follows
+  const int a = (int)((int64_t)total * worker / n_work), b = (int)((int64_t)total * (worker + 1) / n_work);
+  if (a >= b) return;
 
-  float O[KS][NT][4];                            // channel tile, row tile: rows 2t, 2t + 1 of channels g, g + 8
-  float m_used[NT][2], l_sum[NT][2];             // of rows 8 n + 2t, 2t + 1 (l: this thread's keys)
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      m_used[n][c] = kNone;
-      l_sum[n][c] = 0.f;
-    }
-  bool ok = true;
-
-  const int64_t nblk = cap >> p.lg;
-  const float* ksc = p.c.k_scale + head * nblk;
-  const float* vsc = p.c.v_scale + head * nblk;
-  // fills stage u % NST with key tile t0 + u (one thread)
-  auto fill = [&](int u) {
-    const int st = u % L::NST;
-    const int64_t k0 = (int64_t)(t0 + u) * L::KT, at = (head * cap + k0) * HD;
-    const uint32_t bytes = (uint32_t)(cap - k0 < L::KT ? cap - k0 : L::KT) * HD;
-    *issued = u + 1;
-    tc::mbar_expect_tx(&full[st], 2 * bytes);
-    bulk_load(base + st * 2 * L::HALF, p.c.k_codes + at, bytes, &full[st]);
-    bulk_load(base + st * 2 * L::HALF + L::HALF, p.c.v_codes + at, bytes, &full[st]);
+  // steps of entry e, by the whole warp
+  auto warp_steps = [&](int e) -> int {
+    return (__reduce_max_sync(0xffffffffu, row_last(p, e, lane, false)) + L::KT) / L::KT;
   };
-  if (tid == 0)
-    for (int u = 0; u < L::NST && u < t1 - t0; ++u) fill(u);
-
+  struct Pos {
+    int e, h, k, n;       // entry, head, step of the unit, steps in a unit of the entry
+  };
+  auto to_entry = [&](Pos& x) {                  // skips entries without a step; stops at the last
+    while (x.e < entries && (x.n = warp_steps(x.e)) == 0) ++x.e;
+  };
+  auto advance = [&](Pos& x) {
+    if (++x.k < x.n) return;
+    x.k = 0;
+    if (++x.h < p.Hkv) return;
+    x.h = 0;
+    ++x.e;
+    to_entry(x);
+  };
+  Pos cur;
   {
+    // the last thread whose share starts at or before the run
+    int c = 0;
+    for (int i = lane; i < THREADS; i += 32)
+      if (before[i] <= a && i * share < entries) c = i;
+    c = __reduce_max_sync(0xffffffffu, c);
+    cur.e = c * share;
+    int left = a - before[c];
+    for (;; ++cur.e) {
+      cur.n = warp_steps(cur.e);
+      if (left < cur.n * p.Hkv) break;
+      left -= cur.n * p.Hkv;
+    }
+    cur.h = left / cur.n;
+    cur.k = left - cur.h * cur.n;
+  }
+  auto fill = [&](const Pos& x, int st) {
+    if (lane != 0) return;
+    const int64_t k0 = (int64_t)x.k * L::KT, at = (((int64_t)(x.e / p.row_tiles) * p.Hkv + x.h) * cap + k0) * HD;
+    const uint32_t bytes = (uint32_t)(cap - k0 < L::KT ? cap - k0 : L::KT) * HD;
+    tc::mbar_expect_tx(&full[st], 2 * bytes);
+    bulk_load(stages + st * 2 * L::HALF, p.c.k_codes + at, bytes, &full[st]);
+    bulk_load(stages + st * 2 * L::HALF + L::HALF, p.c.v_codes + at, bytes, &full[st]);
+  };
+  Pos pre = cur;                                 // the next step to load
+  int loaded = 0;
+  for (; loaded < L::NST && a + loaded < b; ++loaded) {
+    fill(pre, loaded);
+    if (a + loaded + 1 < b) advance(pre);
+  }
+
+  bool ok = true;
+  for (int i = a; ok && i < b;) {
+    // ------------------------------------------------------------------ a unit, or a part of one
+    const int s = cur.e / p.row_tiles, row0 = (cur.e - s * p.row_tiles) * RT, nrow = min(RT, R - row0), h = cur.h;
+    const int64_t head = (int64_t)s * p.Hkv + h;
+    const int my_last = row_last(p, cur.e, lane, false);
+    const int nk = __reduce_max_sync(0xffffffffu, my_last) + 1;       // keys some row sees
+    const int mn = __reduce_min_sync(0xffffffffu, lane < nrow ? my_last : 0x7fffffff);
+    const float* ksc = p.c.k_scale + head * (cap >> p.lg);
+    const float* vsc = p.c.v_scale + head * (cap >> p.lg);
+    // scales of the next 16 keys, loaded one group ahead (1 past the visible keys: their block
+    // may never have been written)
+    auto scales_of = [&](int key) -> float2 {
+      float2 r = make_float2(1.0f, 1.0f);
+      if (key < nk) {
+        r.x = ksc[key >> p.lg];
+        r.y = vsc[key >> p.lg];
+      }
+      return r;
+    };
+    float2 next = scales_of(cur.k * L::KT);
     // Q^T as the column operand: thread (g, t) holds row 8 n + g, channels [t HD/4, (t + 1) HD/4),
     // 4 per k step (the order of the channels inside a sum is free; K is read with the same one)
-    uint2 qb[QS ? 1 : NT][QS ? 1 : KS];
-    float rf_g[NT];                                           // score factor of row 8 n + g
-    {
-      const T* q = static_cast<const T*>(p.q);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int r = row0 + 8 * n + g;
-        const bool on = 8 * n + g < nrow;
-        const int j = on ? r / p.G : 0;
-        const T* qr = q + (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (on ? r - j * p.G : 0)) * HD + t * (HD / 4);
-        float amax = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          float f[4];
-          load4(qr + 4 * ks, on, f);
-          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        // 2^e <= amax < 2^(e + 1); both powers stay normal
-        int e = amax > 0.f ? ilogbf(amax) : 0;
-        e = e < -120 ? -120 : (e > 120 ? 120 : e);
-        const float down = ldexpf(1.0f, -e);
-        rf_g[n] = ldexpf(p.scale_log2, e);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          float f[4];
-          load4(qr + 4 * ks, on, f);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] *= down;
-          const uint2 a = make_uint2(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]));
-          if constexpr (QS) {
-            if (warp == 0) {
-              sq[(n * KS + ks) * 32 + lane] = a;
-              if constexpr (NS == 2)
-                sq[((NT + n) * KS + ks) * 32 + lane] = make_uint2(rest_h2(f[0], f[1], a.x), rest_h2(f[2], f[3], a.y));
-            }
-          } else {
-            qb[n][ks] = a;
-          }
-        }
-      }
-      if constexpr (QS) asm volatile("bar.sync 1, %0;" ::"n"(WARPS * 32) : "memory");
-    }
-    float rf[NT][2];                                          // of rows 8 n + 2t, 2t + 1
+    uint2 qb[NT][NS][KS];
+    float rf[NT][2];                             // score factor of rows 8 n + 2t, 2t + 1
     int lastr[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      const int r = row0 + 8 * n + g;
+      const bool on = 8 * n + g < nrow;
+      const int j = on ? r / p.G : 0;
+      const T* qr = static_cast<const T*>(p.q) +
+                    (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (on ? r - j * p.G : 0)) * HD + t * (HD / 4);
+      float amax = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        float f[4];
+        load4(qr + 4 * ks, on, f);
+        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      // 2^ex <= amax < 2^(ex + 1); both powers stay normal
+      int ex = amax > 0.f ? ilogbf(amax) : 0;
+      ex = ex < -120 ? -120 : (ex > 120 ? 120 : ex);
+      const float down = ldexpf(1.0f, -ex), up = ldexpf(p.scale_log2, ex);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        float f[4];
+        load4(qr + 4 * ks, on, f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) f[c] *= down;
+        qb[n][0][ks] = make_uint2(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]));
+        if constexpr (NS == 2)
+          qb[n][1][ks] = make_uint2(rest_h2(f[0], f[1], qb[n][0][ks].x), rest_h2(f[2], f[3], qb[n][0][ks].y));
+      }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        rf[n][c] = __shfl_sync(0xffffffffu, rf_g[n], (2 * t + c) * 4);
-        lastr[n][c] = slast[8 * n + 2 * t + c];
+        rf[n][c] = __shfl_sync(0xffffffffu, up, (2 * t + c) * 4);
+        lastr[n][c] = __shfl_sync(0xffffffffu, my_last, 8 * n + 2 * t + c);
       }
+    }
     float* z = p.z ? p.z + (head * R + row0) * cap : nullptr;
+    float O[KS][NT][4];                          // channel tile, row tile: rows 2t, 2t + 1 of channels g, g + 8
+    float m_used[NT][2], l_sum[NT][2];           // of rows 8 n + 2t, 2t + 1 (l: this thread's keys)
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int c = 0; c < 2; ++c) {
+        m_used[n][c] = kNone;
+        l_sum[n][c] = 0.f;
+      }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) O[i][n][c] = 0.f;
-
-    // scales of this warp's next 16 keys, loaded one step ahead (1 past the visible keys: their
-    // block may never have been written)
-    auto scales_of = [&](int64_t key) -> float2 {
-      return key < nk ? make_float2(ksc[key >> p.lg], vsc[key >> p.lg]) : make_float2(1.0f, 1.0f);
-    };
-    float2 next = scales_of((int64_t)t0 * L::KT + warp * L::KW * 16);
-    for (int j = t0; j < t1; ++j) {
-      const int u = j - t0, st = u % L::NST;
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) O[k][n][c] = 0.f;
+    }
+    const int end = min(b, i + cur.n - cur.k);   // line position after this unit's share
+    const int unit = cur.e * p.Hkv + h;
+    int k0 = cur.k * L::KT;
+    for (; i < end; ++i, k0 += L::KT) {
+      const int u = i - a, st = u % L::NST;
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[st], (u / L::NST) & 1));
       if (!ok) break;
-      const uint8_t* sk = base + st * 2 * L::HALF;
+      const uint8_t* sk = stages + st * 2 * L::HALF;
 #pragma unroll 1
       for (int w = 0; w < L::KW; ++w) {
-        const int grp = warp * L::KW + w;
-        const int64_t key0 = (int64_t)j * L::KT + grp * 16;
-        const float2 cur = next;
-        next = scales_of(w + 1 < L::KW ? key0 + 16 : key0 + L::KT - 16 * (L::KW - 1));
+        const int key0 = k0 + w * 16;
+        const float2 now = next;
+        next = scales_of(key0 + 16);
         if (key0 >= nk) continue;
         // ---- scores of 16 keys: thread (g, t) reads keys g and g + 8
         float S[NT][4];
@@ -326,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 4; ++c) S[n][c] = 0.f;
-        const uint8_t* kr = sk + (grp * 16 + g) * HD + t * (HD / 4);
+        const uint8_t* kr = sk + (w * 16 + g) * HD + t * (HD / 4);
         constexpr int KC = HD >= 64 ? 16 : 8;                 // bytes per load
 #pragma unroll
         for (int c0 = 0; c0 < HD / 4; c0 += KC) {
@@ -341,30 +391,22 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
             w1[0] = y.x; w1[1] = y.y;
           }
 #pragma unroll
-          for (int i = 0; i < KC / 4; ++i) {
-            const int ks = c0 / 4 + i;
-            uint32_t a[4];                                    // rows g, g + 8 of channels 4 ks .. + 1, then + 2 .. + 3
-            codes_to_h2(w0[i], a[0], a[2]);
-            codes_to_h2(w1[i], a[1], a[3]);
+          for (int q = 0; q < KC / 4; ++q) {
+            const int ks = c0 / 4 + q;
+            uint32_t x[4];                                    // rows g, g + 8 of channels 4 ks .. + 1, then + 2 .. + 3
+            codes_to_h2(w0[q], x[0], x[2]);
+            codes_to_h2(w1[q], x[1], x[3]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if constexpr (QS) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int part = 0; part < NS; ++part) {
-                  const uint2 b = sq[((part * NT + n) * KS + ks) * 32 + lane];
-                  mma_f16(S[n], a, b.x, b.y);
-                }
-              } else {
-                mma_f16(S[n], a, qb[n][ks].x, qb[n][ks].y);
-              }
-            }
+              for (int part = 0; part < NS; ++part) mma_f16(S[n], x, qb[n][part][ks].x, qb[n][part][ks].y);
           }
         }
         // ---- weights: element c of S[n] is key g + 8 (c / 2), row 8 n + 2t + c % 2
-        const float vs = fmaxf(cur.y, kKv8MinScale);
-        const float3 sc = make_float3(fmaxf(cur.x, kKv8MinScale), NS == 2 ? log2f(vs) : __log2f(vs), __frcp_rn(vs));   // ks, log2 vs, 1 / vs
+        const float vs = fmaxf(now.y, kKv8MinScale);
+        const float3 sc = make_float3(fmaxf(now.x, kKv8MinScale), NS == 2 ? log2f(vs) : __log2f(vs), __fdividef(1.0f, vs));
         const bool whole = key0 + 15 <= mn;                   // every row sees every key
-        float f[NT][2], add[NT][2], e[NT][4];
+        float f[NT][2], add[NT][2], ev[NT][4];
         bool up = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -376,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
           if (!whole) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if ((int)key0 + g + 8 * (c >> 1) > lastr[n][c & 1]) S[n][c] = -INFINITY;
+              if (key0 + g + 8 * (c >> 1) > lastr[n][c & 1]) S[n][c] = -INFINITY;
           }
           if (z) {
 #pragma unroll
@@ -385,10 +427,8 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
                 z[(8 * n + 2 * t + (c & 1)) * cap + key0 + g + 8 * (c >> 1)] = S[n][c] * f[n][c & 1];
           }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            e[n][c] = fmaf(S[n][c], f[n][c & 1], add[n][c & 1]);
-            up |= e[n][c] > kPBias + kLazy;
-          }
+          for (int c = 0; c < 4; ++c) ev[n][c] = fmaf(S[n][c], f[n][c & 1], add[n][c & 1]);
+          up |= fmaxf(fmaxf(ev[n][0], ev[n][1]), fmaxf(ev[n][2], ev[n][3])) > kPBias + kLazy;
         }
         // m is raised when a weight would leave fp16's range (and at a row's first key)
         if (__any_sync(0xffffffffu, up)) {
@@ -406,200 +446,227 @@ __global__ void __launch_bounds__(THREADS, HD == 256 ? 1 : 2) k_kv8_attn(const K
               if (raise) m_used[n][c] = tt;
               l_sum[n][c] *= al[c];
               add[n][c] = sc.y - m_used[n][c] + kPBias;
-              e[n][c] = fmaf(S[n][c], f[n][c], add[n][c]);
-              e[n][c + 2] = fmaf(S[n][c + 2], f[n][c], add[n][c]);
+              ev[n][c] = fmaf(S[n][c], f[n][c], add[n][c]);
+              ev[n][c + 2] = fmaf(S[n][c + 2], f[n][c], add[n][c]);
             }
 #pragma unroll
-            for (int i = 0; i < KS; ++i)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) O[i][n][c] *= al[c & 1];
+              for (int c = 0; c < 4; ++c) O[k][n][c] *= al[c & 1];
           }
         }
         uint32_t pb[NT][NS][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) e[n][c] = tc::ex2_approx(e[n][c]);
+          for (int c = 0; c < 4; ++c) ev[n][c] = tc::ex2_approx(ev[n][c]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t a = pack_h2(e[n][2 * k], e[n][2 * k + 1]);
-            pb[n][0][k] = transpose_h2(a);
-            if constexpr (NS == 2) pb[n][1][k] = transpose_h2(rest_h2(e[n][2 * k], e[n][2 * k + 1], a));
+            const uint32_t x = pack_h2(ev[n][2 * k], ev[n][2 * k + 1]);
+            pb[n][0][k] = transpose_h2(x);
+            if constexpr (NS == 2) pb[n][1][k] = transpose_h2(rest_h2(ev[n][2 * k], ev[n][2 * k + 1], x));
           }
 #pragma unroll
-          for (int c = 0; c < 2; ++c) l_sum[n][c] = fmaf(e[n][c] + e[n][c + 2], sc.z, l_sum[n][c]);
+          for (int c = 0; c < 2; ++c) l_sum[n][c] = fmaf(ev[n][c] + ev[n][c + 2], sc.z, l_sum[n][c]);
         }
         // ---- O^T += C_V^T P^T: this thread's V rows are keys 2t, 2t+1, 2t+8, 2t+9; rows g, g + 8
-        // of channel tile i stand for channels (HD/8) g + 2 i, + 1
-        const uint8_t* vr = sk + L::HALF + (grp * 16 + 2 * t) * HD + g * (HD / 8);
+        // of channel tile k stand for channels (HD/8) g + 2 k, + 1
+        const uint8_t* vr = sk + L::HALF + (w * 16 + 2 * t) * HD + g * (HD / 8);
         constexpr int VC = HD >= 128 ? 16 : HD / 8;           // bytes per load
 #pragma unroll
         for (int c0 = 0; c0 < HD / 8; c0 += VC) {
           uint32_t v[4][VC / 4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const uint8_t* a = vr + ((r & 1) + 8 * (r >> 1)) * HD + c0;
+            const uint8_t* at = vr + ((r & 1) + 8 * (r >> 1)) * HD + c0;
             if constexpr (VC == 16) {
-              const uint4 x = *reinterpret_cast<const uint4*>(a);
+              const uint4 x = *reinterpret_cast<const uint4*>(at);
               v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
             } else if constexpr (VC == 8) {
-              const uint2 x = *reinterpret_cast<const uint2*>(a);
+              const uint2 x = *reinterpret_cast<const uint2*>(at);
               v[r][0] = x.x; v[r][1] = x.y;
             } else {
-              v[r][0] = *reinterpret_cast<const uint32_t*>(a);
+              v[r][0] = *reinterpret_cast<const uint32_t*>(at);
             }
           }
 #pragma unroll
           for (int c = 0; c < VC / 4; ++c) {
-            const uint32_t a0[4] = {codes_pair<0>(v[0][c], v[1][c]), codes_pair<1>(v[0][c], v[1][c]),
+            const uint32_t x0[4] = {codes_pair<0>(v[0][c], v[1][c]), codes_pair<1>(v[0][c], v[1][c]),
                                     codes_pair<0>(v[2][c], v[3][c]), codes_pair<1>(v[2][c], v[3][c])};
-            const uint32_t a1[4] = {codes_pair<2>(v[0][c], v[1][c]), codes_pair<3>(v[0][c], v[1][c]),
+            const uint32_t x1[4] = {codes_pair<2>(v[0][c], v[1][c]), codes_pair<3>(v[0][c], v[1][c]),
                                     codes_pair<2>(v[2][c], v[3][c]), codes_pair<3>(v[2][c], v[3][c])};
-            const int i = c0 / 2 + 2 * c;
+            const int k = c0 / 2 + 2 * c;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int part = 0; part < NS; ++part) {
-                mma_f16(O[i][n], a0, pb[n][part][0], pb[n][part][1]);
-                mma_f16(O[i + 1][n], a1, pb[n][part][0], pb[n][part][1]);
+                mma_f16(O[k][n], x0, pb[n][part][0], pb[n][part][1]);
+                mma_f16(O[k + 1][n], x1, pb[n][part][0], pb[n][part][1]);
               }
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) {
-        // every warp's reads of the stage come before its count, the refill after the last one
-        uint32_t before;
-        asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(tc::smem_u32(&spent[st])) : "memory");
-        if (before == (uint32_t)(u / L::NST + 1) * WARPS - 1 && j + L::NST < t1) fill(u + L::NST);
+      __syncwarp();                              // every lane has read the stage: refill it
+      if (a + loaded < b) {
+        fill(pre, st);
+        ++loaded;
+        if (a + loaded < b) advance(pre);
       }
-      __syncwarp();
     }
-    if (!ok && lane == 0) {
-      atomicOr(&g_err_kv8_attn, ERRBIT_TIMEOUT);
-      *failed = 1;
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float l = l_sum[n][c];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (g == 0) {
-          ml[warp * RT + 8 * n + 2 * t + c] = m_used[n][c];
-          ml[(WARPS + warp) * RT + 8 * n + 2 * t + c] = l;
-        }
-      }
-  }
-  // ------------------------------------------------------------------ merge of the warps
-  // (after this barrier every stage has been consumed: the stages' memory is free)
-  __syncthreads();
-  if (*failed) {   // unless a wait gave up: then the copies in flight get as long again
-    if (tid == 0)
-      for (int k = *issued > L::NST ? (int)*issued - L::NST : 0; k < (int)*issued; ++k)
-        tc::mbar_wait(&full[k % L::NST], (k / L::NST) & 1);
-    __syncthreads();
-  }
-  float* om = reinterpret_cast<float*>(base);    // [WARPS][RT][HD]
-  {
+    if (!ok) break;
+    // ------------------------------------------------------------------ the partial result
+    float* dst = slot(p, HD, worker, unit);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = 8 * n + 2 * t + c;
-        float mm = kNone, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) mm = fmaxf(mm, ml[w * RT + r]);
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) sum = fmaf(ml[(WARPS + w) * RT + r], tc::ex2_approx(ml[w * RT + r] - mm), sum);
-        const float a = tc::ex2_approx(m_used[n][c] - mm);
-        if (warp == 0 && g == 0) {
-          cm[r] = mm;
-          cm[RT + r] = sum;
+        float l = l_sum[n][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) {
+          dst[r] = m_used[n][c];
+          dst[RT + r] = l;
         }
-        // this thread's channels of row r: (HD/8) g + 0 .. HD/8 - 1, rotated by the row's pair so
-        // that the four t of a store meet different banks
-        float* dst = om + (warp * RT + r) * HD;
+        if (r < nrow) {
+          float* o = dst + 2 * RT + r * HD + (HD / 8) * g;
 #pragma unroll
-        for (int i = 0; i < KS; i += 2) {
-          const int w4 = (HD / 32) * g + i / 2;               // 16-byte word of the row
-          *reinterpret_cast<float4*>(dst + ((w4 + 2 * r) & (HD / 4 - 1)) * 4) =
-              make_float4(O[i][n][c] * a, O[i][n][c + 2] * a, O[i + 1][n][c] * a, O[i + 1][n][c + 2] * a);
+          for (int k = 0; k < KS; k += 2)
+            *reinterpret_cast<float4*>(o + 2 * k) = make_float4(O[k][n][c], O[k][n][c + 2], O[k + 1][n][c], O[k + 1][n][c + 2]);
         }
       }
-  }
-  __syncthreads();
-  for (int i = tid; i < RT * HD / 4; i += THREADS) {
-    float4 x = reinterpret_cast<float4*>(om)[i];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) {
-      const float4 y = reinterpret_cast<float4*>(om)[w * (RT * HD / 4) + i];
-      x.x += y.x;
-      x.y += y.y;
-      x.z += y.z;
-      x.w += y.w;
-    }
-    reinterpret_cast<float4*>(om)[i] = x;
-  }
-  // ------------------------------------------------------------------ merge of the cluster
-  if (n_split > 1)
-    tc::cluster_sync();
-  else
-    __syncthreads();
-  const uint32_t cm_a = tc::smem_u32(cm), om_a = tc::smem_u32(om);
-  float* pf = ml;                          // [n_split][RT] factor of each CTA's part (the warps' figures are spent)
-  if (tid < RT) {
-    float mm = kNone, sum = 0.f;
-    for (int c = 0; c < n_split; ++c) mm = fmaxf(mm, ld_cluster(tc::mapa_shared(cm_a + 4 * tid, c)));
-    for (int c = 0; c < n_split; ++c) {
-      const float f = tc::ex2_approx(ld_cluster(tc::mapa_shared(cm_a + 4 * tid, c)) - mm);
-      pf[c * RT + tid] = f;
-      sum = fmaf(ld_cluster(tc::mapa_shared(cm_a + 4 * (RT + tid), c)), f, sum);
-    }
-    fm[tid] = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);   // a row that sees nothing is 0, a NaN stays one
-    // log2 of sum_i 2^z_i: the weights carry 2^(bias - m); a row that sees nothing weighs nothing
-    fm[RT + tid] = sum == 0.f ? INFINITY : mm - kPBias + log2f(sum);
-    if (p.lse && rank == 0 && tid < nrow) p.lse[head * R + row0 + tid] = fm[RT + tid];
-  }
-  __syncthreads();
-  {
-    // CTA `rank` writes an equal share of the tile's output
-    const int n4 = nrow * (HD / 4), per = (n4 + n_split - 1) / n_split;
-    T* out = static_cast<T*>(p.out);
-    for (int i = rank * per + tid; i < min(n4, (rank + 1) * per); i += THREADS) {
-      const int r = i / (HD / 4), w4 = i - r * (HD / 4);
-      const uint32_t at = om_a + 16 * (r * (HD / 4) + ((w4 + 2 * r) & (HD / 4 - 1)));
-      float o[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int c = 0; c < n_split; ++c) {
-        const float f = pf[c * RT + r];
-        const float4 v = tc::ld_cluster4(tc::mapa_shared(at, c));
-        o[0] = fmaf(v.x, f, o[0]);
-        o[1] = fmaf(v.y, f, o[1]);
-        o[2] = fmaf(v.z, f, o[2]);
-        o[3] = fmaf(v.w, f, o[3]);
+    cur.k = 0;
+    if (i < b) {                                 // the run goes on: the unit was finished
+      if (++cur.h == p.Hkv) {
+        cur.h = 0;
+        ++cur.e;
+        to_entry(cur);
       }
+    }
+  }
+  if (!ok) {
+    // report, and give the copies in flight as long again before the memory is given up
+    if (lane == 0) atomicOr(&g_err_kv8_attn, ERRBIT_TIMEOUT);
+    for (int k = loaded > L::NST ? loaded - L::NST : 0; k < loaded; ++k) tc::mbar_wait(&full[k % L::NST], (k / L::NST) & 1);
+  }
+}
+
+// Joins the partial results of one query row: the workers that touched its unit, their maxima,
+// the common maximum's factors, then the weighted sum of their O.  One CTA per (row, unit);
+// each group of HD / 4 threads takes every so-many-th worker.
+constexpr int MERGE_THREADS = 256;
+template <int HD, typename T>
+__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(const Kv8Attn p, int max_workers) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int C4 = HD / 4, NGRP = MERGE_THREADS / C4;
+  __shared__ float s_f[MAX_WORKERS];
+  __shared__ float4 s_o[MERGE_THREADS];
+  __shared__ float s_red[MERGE_THREADS / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.y, e = blockIdx.z * (gridDim.x / p.rt) + blockIdx.x / p.rt, r = blockIdx.x % p.rt;
+  const int entries = p.c.n_seq * p.row_tiles;
+  if (e >= entries) return;
+  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * p.rt + r, R = p.n_q * p.G;
+  if (row >= R) return;
+  const int start = p.plan[e], n = (p.plan[e + 1] - start) / p.Hkv, total = p.plan[entries];
+  const int64_t head = (int64_t)s * p.Hkv + h;
+  const int j = row / p.G;
+  T* out = static_cast<T*>(p.out) + (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (row - j * p.G)) * HD;
+  int w0 = 0, w1 = -1;                 // workers of the unit: the runs that meet [x0, x1)
+  if (n > 0) {
+    const int nw = workers_of(total, max_workers);
+    const int64_t x0 = start + (int64_t)h * n, x1 = x0 + n;
+    w0 = (int)(x0 * nw / total);
+    while (w0 > 0 && (int64_t)total * w0 / nw > x0) --w0;
+    while ((int64_t)total * (w0 + 1) / nw <= x0) ++w0;
+    w1 = (int)((x1 - 1) * nw / total);
+    while ((int64_t)total * w1 / nw > x1 - 1) --w1;
+    while ((int64_t)total * (w1 + 1) / nw <= x1 - 1) ++w1;
+  }
+  const int unit = e * p.Hkv + h, np = w1 - w0 + 1;
+  float mm = kNone;
+  for (int i = tid; i < np; i += MERGE_THREADS) {
+    const float m = slot(p, HD, w0 + i, unit)[r];
+    s_f[i] = m;
+    mm = fmaxf(mm, m);
+  }
+  mm = warp_max(mm);
+  if (lane == 0) s_red[warp] = mm;
+  __syncthreads();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) o[q] *= fm[r];
-      const int rr = row0 + r, j = rr / p.G;
-      st4(out + (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (rr - j * p.G)) * HD + 4 * w4, o);
-    }
+  for (int w = 0; w < MERGE_THREADS / 32; ++w) mm = fmaxf(mm, s_red[w]);
+  float sum = 0.f;
+  for (int i = tid; i < np; i += MERGE_THREADS) {
+    const float f = tc::ex2_approx(s_f[i] - mm);
+    s_f[i] = f;
+    sum = fmaf(slot(p, HD, w0 + i, unit)[p.rt + r], f, sum);
   }
-  // ------------------------------------------------------------------ the keys' weights
-  // (written back by the CTA that scored them: its own z, read after the barriers above)
-  if (p.weights) {
-    float* wr = p.weights + head * cap;
-    const float* z = p.z + head * R * cap;
-    const int64_t k1 = (int64_t)t1 * L::KT < nk ? (int64_t)t1 * L::KT : nk;
-    for (int64_t key = (int64_t)t0 * L::KT + tid; key < k1; key += THREADS) {
-      float sum = 0.f;
-      for (int r = 0; r < nrow; ++r)       // an unseen key's z is -inf
-        sum += tc::ex2_approx(z[r * cap + key] - fm[RT + r]);
-      wr[key] += sum;
-    }
+  sum = warp_sum(sum);
+  __syncthreads();
+  if (lane == 0) s_red[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < MERGE_THREADS / 32; ++w) sum += s_red[w];
+  // a row that sees nothing is 0 and weighs nothing; a NaN stays one
+  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+  if (p.lse && tid == 0) p.lse[head * R + row] = sum == 0.f ? INFINITY : mm - kPBias + log2f(sum);
+  const int c = tid % C4, grp = tid / C4;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = grp; i < np; i += NGRP) {
+    const float4 v = *reinterpret_cast<const float4*>(slot(p, HD, w0 + i, unit) + 2 * p.rt + r * HD + 4 * c);
+    const float f = s_f[i];
+    o.x = fmaf(v.x, f, o.x);
+    o.y = fmaf(v.y, f, o.y);
+    o.z = fmaf(v.z, f, o.z);
+    o.w = fmaf(v.w, f, o.w);
   }
-  if (n_split > 1) tc::cluster_sync();     // the peers may still be reading this CTA's part
+  s_o[tid] = o;
+  __syncthreads();
+  if (grp == 0) {
+    float a[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int k = 1; k < NGRP; ++k) {
+      const float4 v = s_o[k * C4 + c];
+      a[0] += v.x;
+      a[1] += v.y;
+      a[2] += v.z;
+      a[3] += v.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] *= inv;
+    st4(out + 4 * c, a);
+  }
+}
+
+// weights[key] += sum over the rows of 2^(z - log2 of the row's sum); four keys per thread
+__global__ void __launch_bounds__(256) k_kv8_account(const Kv8Attn p) {
+  pdl_wait();
+  pdl_trigger();
+  const int h = blockIdx.y, s = blockIdx.z, R = p.n_q * p.G;
+  const int64_t cap = p.c.capacity, head = (int64_t)s * p.Hkv + h;
+  int mx = -1;
+  for (int r = 0; r < R; r += p.G) mx = max(mx, row_last(p, s, r, false));
+  const int64_t key = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (key > mx) return;
+  const float* z = p.z + head * R * cap + key;
+  const float* lse = p.lse + head * R;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < R; ++r) {
+    const float4 v = *reinterpret_cast<const float4*>(z + r * cap);     // an unseen key's z is -inf
+    const float l = lse[r];
+    a[0] += tc::ex2_approx(v.x - l);
+    a[1] += tc::ex2_approx(v.y - l);
+    a[2] += tc::ex2_approx(v.z - l);
+    a[3] += tc::ex2_approx(v.w - l);
+  }
+  float* w = p.weights + head * cap + key;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (key + k <= mx) w[k] += a[k];
 }
 
 // The weights of more query rows than one tile holds: with log2 of every row's sum known, each
@@ -744,8 +811,7 @@ cudaError_t prepare_attn(int dev) {
   constexpr uint32_t bit = 1u << (h + (sizeof(T) == 4 ? 4 : 0) + (NT == 2 ? 8 : 0));
   std::lock_guard<std::mutex> g(g_kv8_mu);
   if (dev >= 0 && dev < 64 && (g_kv8_attr[dev] & bit)) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       SmemOf<HD, NT, T>::BYTES);
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<HD>::BYTES);
   if (e == cudaSuccess && dev >= 0 && dev < 64) g_kv8_attr[dev] |= bit;
   return e;
 }
@@ -762,8 +828,9 @@ int device_sms(int dev) {
   return n;
 }
 
-// rows of a tile of k_kv8_attn: 8 where they suffice (and at head_dim 256, for the registers)
-int tile_rows(int hd, int64_t R) { return hd == 256 || R <= 8 ? 8 : 16; }
+// rows of a tile of k_kv8_attn: 8 where they suffice, and where two parts of q or 256 channels
+// leave no registers for 16
+int tile_rows(int dt, int hd, int64_t R) { return dt == DT_F32 || hd == 256 || R <= 8 ? 8 : 16; }
 
 template <int HD, int NT, typename T>
 cudaError_t launch_attn_n(const Kv8Attn& p, cudaStream_t s) {
@@ -771,32 +838,22 @@ cudaError_t launch_attn_n(const Kv8Attn& p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = prepare_attn<HD, NT, T>(dev)) != cudaSuccess) return e;
-  const int64_t tiles = ((int64_t)p.n_q * p.G + 8 * NT - 1) / (8 * NT);
-  const int64_t units = tiles * p.Hkv * p.c.n_seq, kt = (p.c.capacity + Lay<HD>::KT - 1) / Lay<HD>::KT;
-  const int64_t want = 2 * (int64_t)device_sms(dev);
-  int ns = 1;
-  while (ns < MAX_SPLIT && units * ns < want && 2 * ns <= kt) ns *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * ns), p.Hkv, p.c.n_seq);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SmemOf<HD, NT, T>::BYTES;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ns;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, NT, T>, p, ns);
+  const int ctas = std::min(ctas_per_sm<HD, T>() * device_sms(dev), MAX_WORKERS / WARPS);
+  if ((e = launch_k(k_kv8_attn<HD, NT, T>, dim3(ctas), dim3(THREADS), Lay<HD>::BYTES, s, p)) != cudaSuccess) return e;
+  const int64_t entries = (int64_t)p.c.n_seq * p.row_tiles;
+  // grid.x: the rows of up to 2^16 entries, grid.z the rest
+  const int64_t per = std::min<int64_t>(entries, 1 << 16);
+  if ((e = launch_k(k_kv8_merge<HD, T>, dim3((unsigned)(per * p.rt), p.Hkv, (unsigned)((entries + per - 1) / per)),
+                    dim3(MERGE_THREADS), 0, s, p, ctas * WARPS)) != cudaSuccess)
+    return e;
+  if (!p.z) return cudaSuccess;
+  return launch_k(k_kv8_account, dim3((unsigned)((p.c.capacity + 1023) / 1024), p.Hkv, p.c.n_seq), dim3(256), 0, s, p);
 }
 
 template <int HD, typename T>
 cudaError_t launch_attn_t(const Kv8Attn& p, cudaStream_t s) {
-  if constexpr (HD < 256)
-    if (tile_rows(HD, (int64_t)p.n_q * p.G) == 16) return launch_attn_n<HD, 2, T>(p, s);
+  if constexpr (HD < 256 && sizeof(T) == 2)
+    if (p.rt == 16) return launch_attn_n<HD, 2, T>(p, s);
   return launch_attn_n<HD, 1, T>(p, s);
 }
 
@@ -818,21 +875,35 @@ void reset_kv8_attn_caches() {
 
 bool kv8_attn_supported(int hd) { return hd == 32 || hd == 64 || hd == 128 || hd == 256; }
 
-// whether the weights take a launch of their own: the rows do not fit in one tile
-bool kv8_attn_weights_apart(int hd, int G, int n_q) {
+// whether the weights of several row tiles are taken by a kernel of their own, from the row sums
+bool kv8_attn_weights_apart(int dt, int hd, int G, int n_q) {
   const int64_t R = (int64_t)n_q * G;
-  return R > tile_rows(hd, R);
+  return R > tile_rows(dt, hd, R);
 }
 
-// scratch for the weights: the scores of the rows, or log2 of every row's sum
-size_t kv8_attn_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
-  if (!weights) return 0;
-  const size_t R = (size_t)n_q * G;
-  return (size_t)n_seq * Hkv * 4 * R * (kv8_attn_weights_apart(hd, G, n_q) ? 1 : (size_t)cap);
+namespace {
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
+// the workspace: plan, partial results, and for the weights the row sums and (one tile) the scores
+struct WsOff {
+  size_t part, lse, z, bytes;
+};
+WsOff ws_of(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+  const size_t R = (size_t)n_q * G, rt = tile_rows(dt, hd, (int64_t)R), tiles = (R + rt - 1) / rt;
+  WsOff w;
+  w.part = up256(((size_t)n_seq * tiles + 1) * 4);
+  w.lse = w.part + up256(((size_t)n_seq * tiles * Hkv + MAX_WORKERS) * (std::min(rt, R) * hd + 2 * rt) * 4);
+  w.z = w.lse + (weights ? up256((size_t)n_seq * Hkv * R * 4) : 0);
+  w.bytes = w.z + (weights && !kv8_attn_weights_apart(dt, hd, G, n_q) ? (size_t)n_seq * Hkv * R * cap * 4 : 0);
+  return w;
+}
+}  // namespace
+
+size_t kv8_attn_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+  return ws_of(dt, n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
 }
 
-static Kv8Attn make_params(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
-                           void* out, float* weights, void* ws) {
+static Kv8Attn make_params(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
+                           int hd, void* out, float* weights, void* ws) {
   Kv8Attn p{};
   p.q = q;
   p.last = last;
@@ -844,13 +915,17 @@ static Kv8Attn make_params(const void* q, const int32_t* last, int n_q, const cb
   p.G = H / Hkv;
   p.lg = 31 - __builtin_clz((unsigned)c.block);
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)hd);
+  const int64_t R = (int64_t)n_q * p.G;
+  p.rt = tile_rows(dt, hd, R);
+  p.row_tiles = (int)((R + p.rt - 1) / p.rt);
+  const WsOff w = ws_of(dt, c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
+  char* b = static_cast<char*>(ws);
+  p.plan = reinterpret_cast<int32_t*>(b);
+  p.part = reinterpret_cast<float*>(b + w.part);
   if (weights) {
-    if (kv8_attn_weights_apart(hd, p.G, n_q)) {
-      p.lse = static_cast<float*>(ws);
-    } else {
-      p.z = static_cast<float*>(ws);
-      p.weights = weights;
-    }
+    p.lse = reinterpret_cast<float*>(b + w.lse);
+    p.weights = weights;
+    if (!kv8_attn_weights_apart(dt, hd, p.G, n_q)) p.z = reinterpret_cast<float*>(b + w.z);
   }
   return p;
 }
@@ -866,14 +941,13 @@ static Kv8Attn make_params(const void* q, const int32_t* last, int n_q, const cb
 
 cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
                             int hd, void* out, float* weights, void* ws, cudaStream_t s) {
-  const Kv8Attn p = make_params(q, last, n_q, c, H, Hkv, hd, out, weights, ws);
+  const Kv8Attn p = make_params(dt, q, last, n_q, c, H, Hkv, hd, out, weights, ws);
   CB_KV8_DISPATCH(launch_attn_t)
 }
 
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
                                int Hkv, int hd, float* weights, void* ws, cudaStream_t s) {
-  Kv8Attn p = make_params(q, last, n_q, c, H, Hkv, hd, nullptr, weights, ws);
-  p.weights = weights;
+  const Kv8Attn p = make_params(dt, q, last, n_q, c, H, Hkv, hd, nullptr, weights, ws);
   CB_KV8_DISPATCH(launch_weights_t)
 }
 

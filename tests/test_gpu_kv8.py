@@ -360,7 +360,8 @@ def test_attention_over_a_long_cache(B):
     q = torch.randn(n_seq, 1, 2, hd, device="cuda")
     last = dev_i32([[-1], [-1], [cap - 1]])
     out = torch.empty_like(q)
-    B.cb_kv8_attention(q, last, 1, c, dims, out)
+    ws = torch.empty(B.cb_kv8_workspace_bytes(dims, n_seq, cap, 1), dtype=torch.uint8, device="cuda")
+    B.cb_kv8_attention(q, last, 1, c, dims, out, None, ws)
     B.cb_sync(None)
     ref = 1.0 - 0.5 / cap
     # sums of 2^22 equal terms in fp32, joined tile by tile: at most 2^22 roundings of 2^-24
