@@ -552,93 +552,114 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
   }
 }
 
-// Joins the partial results of one query row: the workers that touched its unit, their maxima,
-// the common maximum's factors, then the weighted sum of their O.  One CTA per (row, unit);
-// each group of HD / 4 threads takes every so-many-th worker.
-constexpr int MERGE_THREADS = 256;
-template <int HD, typename T>
-__global__ void __launch_bounds__(MERGE_THREADS) k_kv8_merge(const Kv8Attn p, int max_workers) {
+// Joins the partial results of one query row: the workers whose runs meet its unit, their
+// maxima and sums, then the weighted sum of their O.  WPR warps per (row, unit), each taking
+// every WPR-th worker, 32 at a time (a lane per worker for the statistics, a lane per HD / 32
+// channels for O); with several warps their results meet in shared memory.
+constexpr int MERGE_WARPS = 8;
+template <int HD, int WPR, typename T>
+__global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p, int max_workers) {
   pdl_wait();
   pdl_trigger();
-  constexpr int C4 = HD / 4, NGRP = MERGE_THREADS / C4;
-  __shared__ float s_f[MAX_WORKERS];
-  __shared__ float4 s_o[MERGE_THREADS];
-  __shared__ float s_red[MERGE_THREADS / 32];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.y, e = blockIdx.z * (gridDim.x / p.rt) + blockIdx.x / p.rt, r = blockIdx.x % p.rt;
-  const int entries = p.c.n_seq * p.row_tiles;
-  if (e >= entries) return;
+  constexpr int PL = HD / 32;          // channels of a lane
+  __shared__ float s_o[WPR > 1 ? MERGE_WARPS : 1][HD];
+  __shared__ float s_m[MERGE_WARPS], s_l[MERGE_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const int rows = min(p.rt, p.n_q * p.G), entries = p.c.n_seq * p.row_tiles;
+  const int64_t item = (int64_t)blockIdx.x * (MERGE_WARPS / WPR) + warp / WPR;   // (entry, head, row of the tile)
+  const int64_t units = (int64_t)entries * p.Hkv;
+  if (item >= units * rows) return;    // whole CTAs when WPR = MERGE_WARPS
+  const int unit = (int)(item / rows), r = (int)(item - (int64_t)unit * rows), e = unit / p.Hkv, h = unit - e * p.Hkv;
   const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * p.rt + r, R = p.n_q * p.G;
-  if (row >= R) return;
   const int start = p.plan[e], n = (p.plan[e + 1] - start) / p.Hkv, total = p.plan[entries];
-  const int64_t head = (int64_t)s * p.Hkv + h;
-  const int j = row / p.G;
-  T* out = static_cast<T*>(p.out) + (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (row - j * p.G)) * HD;
-  int w0 = 0, w1 = -1;                 // workers of the unit: the runs that meet [x0, x1)
-  if (n > 0) {
+  int w0 = 0, np = 0;                  // the unit's workers: the runs that meet [x0, x1)
+  if (n > 0 && row < R) {
     const int nw = workers_of(total, max_workers);
-    const int64_t x0 = start + (int64_t)h * n, x1 = x0 + n;
+    const int64_t x0 = start + (int64_t)h * n, x1 = x0 + n - 1;
     w0 = (int)(x0 * nw / total);
-    while (w0 > 0 && (int64_t)total * w0 / nw > x0) --w0;
+    while ((int64_t)total * w0 / nw > x0) --w0;
     while ((int64_t)total * (w0 + 1) / nw <= x0) ++w0;
-    w1 = (int)((x1 - 1) * nw / total);
-    while ((int64_t)total * w1 / nw > x1 - 1) --w1;
-    while ((int64_t)total * (w1 + 1) / nw <= x1 - 1) ++w1;
+    int w1 = (int)(x1 * nw / total);
+    while ((int64_t)total * w1 / nw > x1) --w1;
+    while ((int64_t)total * (w1 + 1) / nw <= x1) ++w1;
+    np = w1 - w0 + 1;
   }
-  const int unit = e * p.Hkv + h, np = w1 - w0 + 1;
-  float mm = kNone;
-  for (int i = tid; i < np; i += MERGE_THREADS) {
-    const float m = slot(p, HD, w0 + i, unit)[r];
-    s_f[i] = m;
-    mm = fmaxf(mm, m);
-  }
-  mm = warp_max(mm);
-  if (lane == 0) s_red[warp] = mm;
-  __syncthreads();
+  float mm = kNone, sum = 0.f, o[PL];
 #pragma unroll
-  for (int w = 0; w < MERGE_THREADS / 32; ++w) mm = fmaxf(mm, s_red[w]);
-  float sum = 0.f;
-  for (int i = tid; i < np; i += MERGE_THREADS) {
-    const float f = tc::ex2_approx(s_f[i] - mm);
-    s_f[i] = f;
-    sum = fmaf(slot(p, HD, w0 + i, unit)[p.rt + r], f, sum);
-  }
-  sum = warp_sum(sum);
-  __syncthreads();
-  if (lane == 0) s_red[warp] = sum;
-  __syncthreads();
-  sum = 0.f;
+  for (int k = 0; k < PL; ++k) o[k] = 0.f;
+  for (int i0 = sub; i0 < np; i0 += 32 * WPR) {
+    const int mine = i0 + lane * WPR;
+    float m = kNone, l = 0.f;
+    if (mine < np) {
+      const float* src = slot(p, HD, w0 + mine, unit);
+      m = src[r];
+      l = src[p.rt + r];
+    }
+    const float top = fmaxf(mm, warp_max(m)), back = tc::ex2_approx(mm - top), f = tc::ex2_approx(m - top);
+    mm = top;
+    sum = fmaf(sum, back, warp_sum(l * f));
 #pragma unroll
-  for (int w = 0; w < MERGE_THREADS / 32; ++w) sum += s_red[w];
-  // a row that sees nothing is 0 and weighs nothing; a NaN stays one
-  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
-  if (p.lse && tid == 0) p.lse[head * R + row] = sum == 0.f ? INFINITY : mm - kPBias + log2f(sum);
-  const int c = tid % C4, grp = tid / C4;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = grp; i < np; i += NGRP) {
-    const float4 v = *reinterpret_cast<const float4*>(slot(p, HD, w0 + i, unit) + 2 * p.rt + r * HD + 4 * c);
-    const float f = s_f[i];
-    o.x = fmaf(v.x, f, o.x);
-    o.y = fmaf(v.y, f, o.y);
-    o.z = fmaf(v.z, f, o.z);
-    o.w = fmaf(v.w, f, o.w);
-  }
-  s_o[tid] = o;
-  __syncthreads();
-  if (grp == 0) {
-    float a[4] = {o.x, o.y, o.z, o.w};
+    for (int k = 0; k < PL; ++k) o[k] *= back;
+    const int cnt = min(32, (np - i0 + WPR - 1) / WPR);
+#pragma unroll 8
+    for (int i = 0; i < cnt; ++i) {
+      const float* src = slot(p, HD, w0 + i0 + i * WPR, unit) + 2 * p.rt + r * HD + lane * PL;
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      float v[PL];
+      if constexpr (PL >= 4) {
 #pragma unroll
-    for (int k = 1; k < NGRP; ++k) {
-      const float4 v = s_o[k * C4 + c];
-      a[0] += v.x;
-      a[1] += v.y;
-      a[2] += v.z;
-      a[3] += v.w;
+        for (int k = 0; k < PL; k += 4) ld4(src + k, v + k);
+      } else if constexpr (PL == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        v[0] = x.x;
+        v[1] = x.y;
+      } else {
+        v[0] = *src;
+      }
+#pragma unroll
+      for (int k = 0; k < PL; ++k) o[k] = fmaf(v[k], fi, o[k]);
+    }
+  }
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      s_m[warp] = mm;
+      s_l[warp] = sum;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) a[k] *= inv;
-    st4(out + 4 * c, a);
+    for (int k = 0; k < PL; ++k) s_o[warp][lane * PL + k] = o[k];
+    __syncthreads();
+    if (sub != 0) return;
+    float top = mm;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) top = fmaxf(top, s_m[w]);
+    const float f0 = tc::ex2_approx(mm - top);
+    sum *= f0;
+#pragma unroll
+    for (int k = 0; k < PL; ++k) o[k] *= f0;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      const float f = tc::ex2_approx(s_m[w] - top);
+      sum = fmaf(s_l[w], f, sum);
+#pragma unroll
+      for (int k = 0; k < PL; ++k) o[k] = fmaf(s_o[w][lane * PL + k], f, o[k]);
+    }
+    mm = top;
+  }
+  if (row >= R) return;
+  // a row that sees nothing is 0 and weighs nothing; a NaN stays one
+  const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+  const int64_t head = (int64_t)s * p.Hkv + h;
+  if (p.lse && lane == 0) p.lse[head * R + row] = sum == 0.f ? INFINITY : mm - kPBias + log2f(sum);
+  const int j = row / p.G;
+  T* out = static_cast<T*>(p.out) + (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (row - j * p.G)) * HD + lane * PL;
+#pragma unroll
+  for (int k = 0; k < PL; ++k) o[k] *= inv;
+  if constexpr (PL >= 4) {
+#pragma unroll
+    for (int k = 0; k < PL; k += 4) st4(out + k, o + k);
+  } else {
+#pragma unroll
+    for (int k = 0; k < PL; ++k) out[k] = from_f<T>(o[k]);
   }
 }
 
@@ -840,12 +861,15 @@ cudaError_t launch_attn_n(const Kv8Attn& p, cudaStream_t s) {
   if ((e = prepare_attn<HD, NT, T>(dev)) != cudaSuccess) return e;
   const int ctas = std::min(ctas_per_sm<HD, T>() * device_sms(dev), MAX_WORKERS / WARPS);
   if ((e = launch_k(k_kv8_attn<HD, NT, T>, dim3(ctas), dim3(THREADS), Lay<HD>::BYTES, s, p)) != cudaSuccess) return e;
-  const int64_t entries = (int64_t)p.c.n_seq * p.row_tiles;
-  // grid.x: the rows of up to 2^16 entries, grid.z the rest
-  const int64_t per = std::min<int64_t>(entries, 1 << 16);
-  if ((e = launch_k(k_kv8_merge<HD, T>, dim3((unsigned)(per * p.rt), p.Hkv, (unsigned)((entries + per - 1) / per)),
-                    dim3(MERGE_THREADS), 0, s, p, ctas * WARPS)) != cudaSuccess)
-    return e;
+  // a unit has about workers / units partial results: one warp joins up to two dozen, more go
+  // over a CTA's eight
+  const int64_t units = (int64_t)p.c.n_seq * p.row_tiles * p.Hkv, items = units * std::min(p.rt, p.n_q * p.G);
+  if (units * 24 >= ctas * WARPS)
+    e = launch_k(k_kv8_merge<HD, 1, T>, dim3((unsigned)((items + MERGE_WARPS - 1) / MERGE_WARPS)), dim3(32 * MERGE_WARPS), 0,
+                 s, p, ctas * WARPS);
+  else
+    e = launch_k(k_kv8_merge<HD, MERGE_WARPS, T>, dim3((unsigned)items), dim3(32 * MERGE_WARPS), 0, s, p, ctas * WARPS);
+  if (e != cudaSuccess) return e;
   if (!p.z) return cudaSuccess;
   return launch_k(k_kv8_account, dim3((unsigned)((p.c.capacity + 1023) / 1024), p.Hkv, p.c.n_seq), dim3(256), 0, s, p);
 }
