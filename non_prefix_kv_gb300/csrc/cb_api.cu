@@ -1190,7 +1190,7 @@ int check_cache(const cb_kv8_cache* c, const cb_dims* d, const char* what) {
   if (c->n_seq < 1 || c->n_seq > 65535) return fail(CB_ERR_SHAPE, "%s: n_seq %d outside [1, 65535]", what, c->n_seq);
   if (c->capacity < c->block || c->capacity % c->block || c->capacity > (1 << 30))
     return fail(CB_ERR_SHAPE, "%s: capacity %lld is not a multiple of block up to 2^30", what, (long long)c->capacity);
-  if (d->n_kv_heads > 65535) return fail(CB_ERR_UNSUPPORTED, "%s: more than 65535 KV heads", what);
+  if (d->n_kv_heads > 32767) return fail(CB_ERR_UNSUPPORTED, "%s: more than 32767 KV heads", what);
   return CB_OK;
 }
 
@@ -1239,8 +1239,6 @@ int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* 
   if (n_rows == 0 || (!k_out && !v_out)) return CB_OK;
   if (!start) return fail(CB_ERR_INVALID_ARG, "kv8_read: start is NULL");
   if ((st = check_al16({k_out, v_out}, "kv8_read"))) return st;
-  if ((int64_t)n_rows * dims->n_kv_heads * dims->head_dim / 8 > INT32_MAX)
-    return fail(CB_ERR_UNSUPPORTED, "kv8_read: more than 2^34 values of a sequence in one call");
   const double W = (k_out && v_out ? 2.0 : 1.0) * dims->n_kv_heads * dims->head_dim, n = (double)cache->n_seq * n_rows;
   CB_LAUNCH(CB_PROF_KV8_READ, 0, (int64_t)cache->n_seq * n_rows, (int64_t)W, 0, 0.0, n * W * (1.0 + esize(dims->dtype)),
             S(stream), launch_kv8_read(dims->dtype, *cache, start, count, n_rows, dims->n_kv_heads, dims->head_dim,

@@ -44,17 +44,63 @@ __device__ __forceinline__ bool kv8_rows(const int32_t* start, const int32_t* co
   return *a < *e;
 }
 
-// 16 consecutive elements as floats; a non-finite one counts as 0 and is noted
+// 16 consecutive elements as they were loaded, their largest magnitude as fp32 bits (above
+// 0x7f7fffff if one is not finite), and their values (not finite: 0)
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float* f, bool& bad) {
-  ld8(p, f);
-  ld8(p + 8, f + 8);
+struct Chunk;
+template <>
+struct Chunk<bf16> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const bf16* p) {
+    a = reinterpret_cast<const uint4*>(p)[0];
+    b = reinterpret_cast<const uint4*>(p)[1];
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&m) & 0x7fff7fffu;
+    return max(u << 16, u & 0xffff0000u);
+  }
+  __device__ __forceinline__ void values(float* f) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Chunk<float> {
+  uint4 w[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = max(max(max(m, w[i].x & 0x7fffffffu), max(w[i].y & 0x7fffffffu, w[i].z & 0x7fffffffu)), w[i].w & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ void values(float* f) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[4 * i] = __uint_as_float(w[i].x);
+      f[4 * i + 1] = __uint_as_float(w[i].y);
+      f[4 * i + 2] = __uint_as_float(w[i].z);
+      f[4 * i + 3] = __uint_as_float(w[i].w);
+    }
+  }
+};
+// not finite: 0
+__device__ __forceinline__ void zero_bad(float* f) {
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (!isfinite(f[i])) {
-      bad = true;
-      f[i] = 0.f;
-    }
+    if (!isfinite(f[i])) f[i] = 0.f;
 }
 
 // One CTA per (touched block, K or V, head, sequence); a thread owns NCH chunks of 16 channels
@@ -83,20 +129,34 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
   const float old = lo > 0 ? *scale : 0.f;
   const int per_row = hd >> 4;
   const T* src = (is_v ? v : k) + (((int64_t)s * n_rows + (r0 - a)) * Hkv + h) * hd;
-  float f[NCH][16];
-  float amax = 0.f;
+  Chunk<T> x[NCH];
+  uint32_t top = 0;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
-    if (row >= lo && row < hi) {
-      load16(src + (int64_t)row * Hkv * hd + col, f[i], bad);
+    if (row >= lo && row < hi) x[i].load(src + (int64_t)row * Hkv * hd + col);
+  }
 #pragma unroll
-      for (int q = 0; q < 16; ++q) amax = fmaxf(amax, fabsf(f[i][q]));
+  for (int i = 0; i < NCH; ++i) {
+    const int row = (threadIdx.x + i * blockDim.x) / per_row;
+    if (row >= lo && row < hi) {
+      uint32_t m = x[i].amax_bits();
+      if (m >= 0x7f800000u) {
+        bad = true;
+        float f[16];
+        x[i].values(f);
+        zero_bad(f);
+        float a = 0.f;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) a = fmaxf(a, fabsf(f[q]));
+        m = __float_as_uint(a);
+      }
+      top = max(top, m);
     }
   }
   if (bad) atomicOr(&g_err_kv8, ERRBIT_NONFINITE);
-  amax = kv8_block_max(amax, sh);
+  const float amax = kv8_block_max(__uint_as_float(top), sh);
   const float sc = fmaxf(fmaxf(__fdiv_rn(amax, 127.0f), kKv8MinScale), old);
   const float inv = 1.0f / sc;
   const bool grow = sc > old;
@@ -105,47 +165,66 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
     const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
     uint4* dst = reinterpret_cast<uint4*>(codes + (int64_t)row * hd + col);
     if (row >= lo && row < hi) {
-#pragma unroll
-      for (int q = 0; q < 16; ++q) f[i][q] = kv8_code(f[i][q], sc, inv);
-      *dst = kv8_pack16(f[i]);
+      float f[16];
+      x[i].values(f);
+      if (bad) zero_bad(f);
+      *dst = kv8_code16(f, sc, inv);
     } else if (row < lo && grow) {
       float g[16];
+      uint32_t q[16];
       kv8_unpack16(*dst, g);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) g[q] = kv8_recode(g[q], old, sc, inv);
-      *dst = kv8_pack16(g);
+      for (int c = 0; c < 16; ++c) q[c] = (uint32_t)(int)kv8_recode(g[c], old, sc, inv);
+      *dst = make_uint4(kv8_pack4(q[0], q[1], q[2], q[3]), kv8_pack4(q[4], q[5], q[6], q[7]),
+                        kv8_pack4(q[8], q[9], q[10], q[11]), kv8_pack4(q[12], q[13], q[14], q[15]));
     }
   }
   if (threadIdx.x == 0 && grow) *scale = sc;
 }
 
-// A thread turns 8 codes into 8 values: the codes of a warp's chunks are contiguous per head,
-// the values it writes are contiguous across heads.
+// A thread turns 8 codes into 8 values.  A CTA takes a run of rows of one head: the codes it
+// reads are contiguous, each row it writes is a contiguous run of hd values.
+constexpr int kReadUnroll = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv8_read(const cb_kv8_cache c, int lg, const int32_t* __restrict__ start,
                                                   const int32_t* __restrict__ count, int n_rows, int Hkv, int hd,
                                                   T* __restrict__ k_out, T* __restrict__ v_out) {
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.y;
-  const bool is_v = k_out == nullptr || blockIdx.z == 1;
+  const int s = blockIdx.z, h = blockIdx.y >= (unsigned)Hkv ? blockIdx.y - Hkv : blockIdx.y;
+  const bool is_v = k_out == nullptr || blockIdx.y >= (unsigned)Hkv;
   int64_t a, e;
-  if (!kv8_rows(start, count, n_rows, c.capacity, s, blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0, &a, &e))
+  if (!kv8_rows(start, count, n_rows, c.capacity, s, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0, &a, &e))
     return;
-  const unsigned idx = blockIdx.x * 256u + threadIdx.x;
-  const unsigned w8 = (unsigned)(Hkv * hd) >> 3, h8 = (unsigned)hd >> 3;
-  const unsigned row = idx / w8, rem = idx - row * w8, h = rem / h8, d = (rem - h * h8) << 3;
-  if (row >= (unsigned)(e - a)) return;
-  const int64_t head = (int64_t)s * Hkv + h, r = a + row;
-  const uint2 u = *reinterpret_cast<const uint2*>((is_v ? c.v_codes : c.k_codes) + (head * c.capacity + r) * hd + d);
-  const float sc = (is_v ? c.v_scale : c.k_scale)[head * (c.capacity >> lg) + (r >> lg)];
-  float f[8];
+  const int h8 = hd >> 3, per = 256 / h8;          // rows of one pass (hd 96 and the like leave threads idle)
+  const int tr = threadIdx.x / h8, d = (threadIdx.x - tr * h8) << 3;
+  const int64_t head = (int64_t)s * Hkv + h;
+  const int8_t* codes = (is_v ? c.v_codes : c.k_codes) + head * c.capacity * hd + d;
+  const float* scale = (is_v ? c.v_scale : c.k_scale) + head * (c.capacity >> lg);
+  T* out = (is_v ? v_out : k_out) + ((int64_t)s * n_rows * Hkv + h) * hd + d;
+  const int64_t row0 = (int64_t)blockIdx.x * per * kReadUnroll + tr;
+  uint2 u[kReadUnroll];
+  float sc[kReadUnroll];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    f[q] = (float)(int8_t)(u.x >> (8 * q)) * sc;
-    f[4 + q] = (float)(int8_t)(u.y >> (8 * q)) * sc;
+  for (int i = 0; i < kReadUnroll; ++i) {
+    const int64_t r = a + row0 + i * per;
+    if (tr < per && r < e) {
+      u[i] = *reinterpret_cast<const uint2*>(codes + r * hd);
+      sc[i] = scale[r >> lg];
+    }
   }
-  st8((is_v ? v_out : k_out) + ((int64_t)s * n_rows + row) * Hkv * hd + h * hd + d, f);
+#pragma unroll
+  for (int i = 0; i < kReadUnroll; ++i) {
+    const int64_t row = row0 + i * per;
+    if (tr < per && a + row < e) {
+      float f[8];
+      kv8_unpack4(u[i].x, f);
+      kv8_unpack4(u[i].y, f + 4);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], sc[i]);
+      st8(out + row * Hkv * hd, f);
+    }
+  }
 }
 
 // ---- eviction ---------------------------------------------------------------------------
@@ -305,20 +384,28 @@ __global__ void __launch_bounds__(1024) k_kv8_move(const cb_kv8_cache c, const c
   int8_t* out = (is_v ? d.v_codes : d.k_codes) + (head * d.capacity + r0) * hd;
   const int32_t* kr = kept + head * n_keep + r0;
   const int per_row = hd >> 4;
-  float f[NCH][16];
-  float amax = 0.f;
+  uint4 x[NCH];
+  float xs[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
     if (row < rows) {
       const int64_t r = kr[row];
-      const float sc = scale[r >> lg];
-      kv8_unpack16(*reinterpret_cast<const uint4*>(codes + r * hd + col), f[i]);
+      xs[i] = scale[r >> lg];
+      x[i] = *reinterpret_cast<const uint4*>(codes + r * hd + col);
+    }
+  }
+  float amax = 0.f;
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        f[i][q] = __fmul_rn(f[i][q], sc);
-        amax = fmaxf(amax, fabsf(f[i][q]));
-      }
+  for (int i = 0; i < NCH; ++i) {
+    const int row = (threadIdx.x + i * blockDim.x) / per_row;
+    if (row < rows) {
+      // the largest |code| times the scale is the largest |value|: products round monotonically
+      float f[16], m = 0.f;
+      kv8_unpack16(x[i], f);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) m = fmaxf(m, fabsf(f[q]));
+      amax = fmaxf(amax, __fmul_rn(m, xs[i]));
     }
   }
   amax = kv8_block_max(amax, sh);
@@ -328,9 +415,11 @@ __global__ void __launch_bounds__(1024) k_kv8_move(const cb_kv8_cache c, const c
   for (int i = 0; i < NCH; ++i) {
     const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
     if (row < rows) {
+      float f[16];
+      kv8_unpack16(x[i], f);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) f[i][q] = kv8_code(f[i][q], sc, inv);
-      *reinterpret_cast<uint4*>(out + (int64_t)row * hd + col) = kv8_pack16(f[i]);
+      for (int q = 0; q < 16; ++q) f[q] = __fmul_rn(f[q], xs[i]);
+      *reinterpret_cast<uint4*>(out + (int64_t)row * hd + col) = kv8_code16(f, sc, inv);
     }
   }
   if (threadIdx.x == 0) (is_v ? d.v_scale : d.k_scale)[head * (d.capacity >> lg) + b] = sc;
@@ -373,8 +462,8 @@ cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, 
 
 cudaError_t launch_kv8_read(int dt, const cb_kv8_cache& c, const int32_t* start, const int32_t* count, int n_rows,
                             int Hkv, int hd, void* k_out, void* v_out, cudaStream_t s) {
-  const int64_t items = (int64_t)n_rows * Hkv * hd / 8;
-  const dim3 grid((unsigned)((items + 255) / 256), c.n_seq, k_out && v_out ? 2 : 1);
+  const int per = 256 / (hd / 8) * kReadUnroll;
+  const dim3 grid((unsigned)(((int64_t)n_rows + per - 1) / per), k_out && v_out ? 2 * Hkv : Hkv, c.n_seq);
   const int lg = log2_of(c.block);
   if (dt == DT_BF16)
     return launch_k(k_kv8_read<bf16>, grid, dim3(256), 0, s, c, lg, start, count, n_rows, Hkv, hd,

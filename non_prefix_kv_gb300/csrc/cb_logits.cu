@@ -6,7 +6,8 @@
 // row's history ids that fall into its slice in shared memory (integers, so the order of the
 // atomics does not matter), adds up the biases there in list order, then streams the slice
 // through the rules.  The slices' best (value, id) keys meet in the cluster's shared memory,
-// so there is no second launch and no workspace.
+// so there is no second launch and no workspace.  Sixteen small CTAs per row (32 KB of shared
+// memory, 256 threads) let 64 rows of 64000 ids run as one wave.
 #include <math.h>
 
 #include <mutex>
@@ -29,9 +30,13 @@ uint32_t take_error_logits() {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kChunk = 8192;                 // ids a CTA holds counts and biases of at once
-constexpr uint32_t kSeen = 0x80000000u;      // in the history (the low bits: times in the answer)
+constexpr int kThreads = 256;
+constexpr int kChunk = 4096;                 // ids a CTA holds counts and biases of at once
+constexpr int kMaxBias = 4096;
+constexpr int kMaxCluster = 16;
+constexpr uint32_t kSeen = 0x80000000u;      // in the prompt (the low bits: times in the answer)
+constexpr uint32_t kNoBias = 0xffffffffu;    // bias word of an id without one (no sum is stored as this NaN)
+constexpr uint32_t kShared = 0x80000000u;    // on the way: more than one entry has this id
 
 // larger value first, then the lower id; 0 only for "nothing"
 __device__ __forceinline__ unsigned long long token_key(float v, int id) {
@@ -48,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, in
   constexpr int E = 16 / sizeof(T);          // elements of a 16-byte access
   extern __shared__ __align__(16) uint32_t smem[];
   uint32_t* cnt = smem;                      // [kChunk]
-  float* bias = reinterpret_cast<float*>(smem + kChunk);
+  uint32_t* bias = smem + kChunk;            // [kChunk] bits of the sum, or kNoBias
   __shared__ unsigned long long s_best[kThreads / 32];
   __shared__ unsigned long long s_key;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -81,51 +86,61 @@ __global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, in
     if (hist || biased) {
       for (int i = tid; i < n; i += kThreads) {
         if (hist) cnt[i] = 0;
-        if (biased) bias[i] = 0.f;
+        if (biased) bias[i] = kNoBias;
       }
       __syncthreads();
     }
     if (hist) {
       const int32_t* ids = r.history + (int64_t)row * r.history_ld;
+#pragma unroll 4
       for (int i = tid; i < len; i += kThreads) {
-        const int id = ids[i];
-        if (id < 0 || id >= vocab) {
+        const int id = ids[i], k = id - c0;
+        if (id < 0 || id >= vocab)
           bad_id = true;
-          continue;
+        else if (k >= 0 && k < n) {
+          if (i >= plen)
+            atomicAdd(&cnt[k], 1u);
+          else
+            atomicOr(&cnt[k], kSeen);
         }
-        const int k = id - c0;
-        if (k < 0 || k >= n) continue;
-        if (i >= plen) atomicAdd(&cnt[k], 1u);
-        atomicOr(&cnt[k], kSeen);
       }
     }
-    if (biased && warp == 0) {
-      // 32 entries at a time; the first lane of each id adds that id's entries in list order
+    if (biased) {
+      // The first entry of an id owns its word and adds the id's entries in list order: every
+      // entry puts its number in with a minimum, one that finds another there marks the word, and
+      // only the owner of a marked word looks through the rest of the list.
       const int32_t* bid = r.bias_id + (int64_t)row * r.n_bias;
       const float* bv = r.bias + (int64_t)row * r.n_bias;
-      for (int i = 0; i < r.n_bias; i += 32) {
-        int id = -1;
-        float v = 0.f;
-        if (i + lane < r.n_bias) {
-          id = bid[i + lane];
-          v = bv[i + lane];
-          if (id < -1 || id >= vocab) {
-            bad_id = true;
-            id = -1;
-          }
+      auto place = [&](int i) -> int {     // an entry's word in this chunk, or -1
+        const int id = bid[i];
+        if (id < -1 || id >= vocab) bad_id = true;
+        return id >= c0 && id - c0 < n ? id - c0 : -1;
+      };
+      for (int i = tid; i < r.n_bias; i += kThreads) {
+        const int k = place(i);
+        if (k >= 0) atomicMin(&bias[k], (uint32_t)i);
+      }
+      __syncthreads();
+      static_assert(kMaxBias / kThreads <= 32, "a thread's entries exceed a word");
+      uint32_t owned = 0;                  // bit j: this thread's j-th entry owns its word
+      for (int i = tid, j = 0; i < r.n_bias; i += kThreads, ++j) {
+        const int k = place(i);
+        if (k < 0) continue;
+        if ((bias[k] & ~kShared) == (uint32_t)i)
+          owned |= 1u << j;
+        else
+          atomicOr(&bias[k], kShared);
+      }
+      __syncthreads();
+      for (; owned; owned &= owned - 1) {
+        const int i = tid + (__ffs(owned) - 1) * kThreads, id = bid[i];
+        float sum = bv[i];
+        if (bias[id - c0] & kShared) {
+#pragma unroll 4
+          for (int k = i + 1; k < r.n_bias; ++k)
+            if (bid[k] == id) sum += bv[k];
         }
-        const int k = id - c0;
-        const bool in = id >= 0 && k >= 0 && k < n;
-        const unsigned same = __match_any_sync(0xffffffffu, in ? k : -1 - lane);
-        const bool first = in && lane == __ffs(same) - 1;
-        float sum = first ? bias[k] : 0.f;
-#pragma unroll
-        for (int l = 0; l < 32; ++l) {
-          const float w = __shfl_sync(0xffffffffu, v, l);
-          if ((same >> l) & 1) sum += w;
-        }
-        if (first) bias[k] = sum;
-        __syncwarp();
+        bias[id - c0] = sum != sum ? 0x7fffffffu : __float_as_uint(sum);
       }
     }
     if (hist || biased) __syncthreads();
@@ -133,13 +148,16 @@ __global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, in
     auto rule = [&](float v, int i, uint32_t open) -> float {     // id c0 + i
       if (hist) {
         const uint32_t c = cnt[i];
-        if (c) {
+        if (c) {                           // in the prompt or in the answer
           v = v > 0.f ? v / rep : v * rep;
           const uint32_t k = c & ~kSeen;
           if (k) v -= freq * (float)k + pres;
         }
       }
-      if (biased) v += bias[i];
+      if (biased) {
+        const uint32_t w = bias[i];
+        if (w != kNoBias) v += __uint_as_float(w);
+      }
       return open & 1 ? v : -INFINITY;
     };
     auto take = [&](float v, int i) {                              // v as it is returned
@@ -215,11 +233,12 @@ cudaError_t launch_t(const void* logits, int n_rows, int vocab, const cb_logit_r
     std::lock_guard<std::mutex> g(g_logits_mu);
     if (dev < 0 || dev >= 64 || !(g_logits_attr[dev] & bit)) {
       e = cudaFuncSetAttribute(k_logits<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(k_logits<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       if (dev >= 0 && dev < 64) g_logits_attr[dev] |= bit;
     }
   }
-  int nc = 8;
+  int nc = kMaxCluster;
   while (nc > 1 && (int64_t)nc * 512 > vocab) nc /= 2;
   const int slice = ((vocab + nc - 1) / nc + 63) & ~63;
   const uintptr_t al = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out);
