@@ -129,17 +129,19 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
   const float old = lo > 0 ? *scale : 0.f;
   const int per_row = hd >> 4;
   const T* src = (is_v ? v : k) + (((int64_t)s * n_rows + (r0 - a)) * Hkv + h) * hd;
+  // a thread's chunks lie whole rows apart
+  const int row0 = threadIdx.x / per_row, col = (threadIdx.x - row0 * per_row) << 4, step = block / NCH;
   Chunk<T> x[NCH];
   uint32_t top = 0;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
+    const int row = row0 + i * step;
     if (row >= lo && row < hi) x[i].load(src + (int64_t)row * Hkv * hd + col);
   }
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int row = (threadIdx.x + i * blockDim.x) / per_row;
+    const int row = row0 + i * step;
     if (row >= lo && row < hi) {
       uint32_t m = x[i].amax_bits();
       if (m >= 0x7f800000u) {
@@ -162,8 +164,8 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
   const bool grow = sc > old;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
-    uint4* dst = reinterpret_cast<uint4*>(codes + (int64_t)row * hd + col);
+    const int row = row0 + i * step;
+    uint4* dst = reinterpret_cast<uint4*>(codes + row * hd + col);
     if (row >= lo && row < hi) {
       float f[16];
       x[i].values(f);
@@ -182,13 +184,25 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
   if (threadIdx.x == 0 && grow) *scale = sc;
 }
 
-// A thread turns 8 codes into 8 values.  A CTA takes a run of rows of one head: the codes it
-// reads are contiguous, each row it writes is a contiguous run of hd values.
+// 8 consecutive values: one 32-byte store of floats where the buffer allows it
+__device__ __forceinline__ void put8(bf16* p, const float* f, bool) { st8(p, f); }
+__device__ __forceinline__ void put8(float* p, const float* f, bool al32) {
+  if (al32)
+    asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]),
+                 "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                 : "memory");
+  else
+    st8(p, f);
+}
+
+// A thread turns 16 codes into 16 values, a few rows of them at once.  A CTA takes a run of
+// rows of one head: the codes it reads are contiguous, each row it writes is a contiguous run
+// of hd values.
 constexpr int kReadUnroll = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv8_read(const cb_kv8_cache c, int lg, const int32_t* __restrict__ start,
                                                   const int32_t* __restrict__ count, int n_rows, int Hkv, int hd,
-                                                  T* __restrict__ k_out, T* __restrict__ v_out) {
+                                                  T* __restrict__ k_out, T* __restrict__ v_out, bool al32) {
   pdl_wait();
   pdl_trigger();
   const int s = blockIdx.z, h = blockIdx.y >= (unsigned)Hkv ? blockIdx.y - Hkv : blockIdx.y;
@@ -196,35 +210,32 @@ __global__ void __launch_bounds__(256) k_kv8_read(const cb_kv8_cache c, int lg, 
   int64_t a, e;
   if (!kv8_rows(start, count, n_rows, c.capacity, s, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0, &a, &e))
     return;
-  const int h8 = hd >> 3, per = 256 / h8;          // rows of one pass (hd 96 and the like leave threads idle)
-  const int tr = threadIdx.x / h8, d = (threadIdx.x - tr * h8) << 3;
-  const int64_t head = (int64_t)s * Hkv + h;
-  const int8_t* codes = (is_v ? c.v_codes : c.k_codes) + head * c.capacity * hd + d;
+  const int h16 = hd >> 4, per = 256 / h16;        // rows of one pass (hd 96 and the like leave threads idle)
+  const int tr = threadIdx.x / h16, d = (threadIdx.x - tr * h16) << 4;
+  const int64_t head = (int64_t)s * Hkv + h, row0 = (int64_t)blockIdx.x * per * kReadUnroll + tr;
+  const int8_t* codes = (is_v ? c.v_codes : c.k_codes) + (head * c.capacity + a + row0) * hd + d;
   const float* scale = (is_v ? c.v_scale : c.k_scale) + head * (c.capacity >> lg);
-  T* out = (is_v ? v_out : k_out) + ((int64_t)s * n_rows * Hkv + h) * hd + d;
-  const int64_t row0 = (int64_t)blockIdx.x * per * kReadUnroll + tr;
-  uint2 u[kReadUnroll];
+  T* out = (is_v ? v_out : k_out) + (((int64_t)s * n_rows + row0) * Hkv + h) * hd + d;
+  const int left = tr < per ? (int)(e - a - row0 < per * kReadUnroll ? e - a - row0 : per * kReadUnroll) : 0;   // rows from row0 on
+  uint4 u[kReadUnroll];
   float sc[kReadUnroll];
 #pragma unroll
-  for (int i = 0; i < kReadUnroll; ++i) {
-    const int64_t r = a + row0 + i * per;
-    if (tr < per && r < e) {
-      u[i] = *reinterpret_cast<const uint2*>(codes + r * hd);
-      sc[i] = scale[r >> lg];
+  for (int i = 0; i < kReadUnroll; ++i)
+    if (i * per < left) {
+      u[i] = *reinterpret_cast<const uint4*>(codes + i * per * hd);
+      sc[i] = scale[(a + row0 + i * per) >> lg];
     }
-  }
 #pragma unroll
-  for (int i = 0; i < kReadUnroll; ++i) {
-    const int64_t row = row0 + i * per;
-    if (tr < per && a + row < e) {
-      float f[8];
-      kv8_unpack4(u[i].x, f);
-      kv8_unpack4(u[i].y, f + 4);
+  for (int i = 0; i < kReadUnroll; ++i)
+    if (i * per < left) {
+      float f[16];
+      kv8_unpack16(u[i], f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = __fmul_rn(f[q], sc[i]);
-      st8(out + row * Hkv * hd, f);
+      for (int q = 0; q < 16; ++q) f[q] = __fmul_rn(f[q], sc[i]);
+      T* o = out + (int64_t)i * per * Hkv * hd;
+      put8(o, f, al32);
+      put8(o + 8, f + 8, al32);
     }
-  }
 }
 
 // ---- eviction ---------------------------------------------------------------------------
@@ -384,11 +395,12 @@ __global__ void __launch_bounds__(1024) k_kv8_move(const cb_kv8_cache c, const c
   int8_t* out = (is_v ? d.v_codes : d.k_codes) + (head * d.capacity + r0) * hd;
   const int32_t* kr = kept + head * n_keep + r0;
   const int per_row = hd >> 4;
+  const int row0 = threadIdx.x / per_row, col = (threadIdx.x - row0 * per_row) << 4, step = (1 << lg) / NCH;
   uint4 x[NCH];
-  float xs[NCH];
+  float f[NCH][16], xs[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
+    const int row = row0 + i * step;
     if (row < rows) {
       const int64_t r = kr[row];
       xs[i] = scale[r >> lg];
@@ -397,29 +409,25 @@ __global__ void __launch_bounds__(1024) k_kv8_move(const cb_kv8_cache c, const c
   }
   float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int row = (threadIdx.x + i * blockDim.x) / per_row;
-    if (row < rows) {
+  for (int i = 0; i < NCH; ++i)
+    if (row0 + i * step < rows) {
       // the largest |code| times the scale is the largest |value|: products round monotonically
-      float f[16], m = 0.f;
-      kv8_unpack16(x[i], f);
+      float m = 0.f;
+      kv8_unpack16(x[i], f[i]);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) m = fmaxf(m, fabsf(f[q]));
+      for (int q = 0; q < 16; ++q) m = fmaxf(m, fabsf(f[i][q]));
       amax = fmaxf(amax, __fmul_rn(m, xs[i]));
     }
-  }
   amax = kv8_block_max(amax, sh);
   const float sc = fmaxf(__fdiv_rn(amax, 127.0f), kKv8MinScale);
   const float inv = 1.0f / sc;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int ch = threadIdx.x + i * blockDim.x, row = ch / per_row, col = (ch - row * per_row) << 4;
+    const int row = row0 + i * step;
     if (row < rows) {
-      float f[16];
-      kv8_unpack16(x[i], f);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) f[q] = __fmul_rn(f[q], xs[i]);
-      *reinterpret_cast<uint4*>(out + (int64_t)row * hd + col) = kv8_code16(f, sc, inv);
+      for (int q = 0; q < 16; ++q) f[i][q] = __fmul_rn(f[i][q], xs[i]);
+      *reinterpret_cast<uint4*>(out + row * hd + col) = kv8_code16(f[i], sc, inv);
     }
   }
   if (threadIdx.x == 0) (is_v ? d.v_scale : d.k_scale)[head * (d.capacity >> lg) + b] = sc;
@@ -462,14 +470,15 @@ cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, 
 
 cudaError_t launch_kv8_read(int dt, const cb_kv8_cache& c, const int32_t* start, const int32_t* count, int n_rows,
                             int Hkv, int hd, void* k_out, void* v_out, cudaStream_t s) {
-  const int per = 256 / (hd / 8) * kReadUnroll;
+  const int per = 256 / (hd / 16) * kReadUnroll;
+  const bool al32 = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   const dim3 grid((unsigned)(((int64_t)n_rows + per - 1) / per), k_out && v_out ? 2 * Hkv : Hkv, c.n_seq);
   const int lg = log2_of(c.block);
   if (dt == DT_BF16)
     return launch_k(k_kv8_read<bf16>, grid, dim3(256), 0, s, c, lg, start, count, n_rows, Hkv, hd,
-                    static_cast<bf16*>(k_out), static_cast<bf16*>(v_out));
+                    static_cast<bf16*>(k_out), static_cast<bf16*>(v_out), al32);
   return launch_k(k_kv8_read<float>, grid, dim3(256), 0, s, c, lg, start, count, n_rows, Hkv, hd,
-                  static_cast<float*>(k_out), static_cast<float*>(v_out));
+                  static_cast<float*>(k_out), static_cast<float*>(v_out), al32);
 }
 
 cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const float* weights, int n_keep, int n_sink,

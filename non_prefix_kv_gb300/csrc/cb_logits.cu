@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, in
   const float pres = r.presence ? r.presence[row] : 0.0f, freq = r.frequency ? r.frequency[row] : 0.0f;
   const uint32_t* mask = r.mask ? r.mask + (int64_t)row * r.mask_ld : nullptr;
   const int s0 = rank * slice, s1 = min(vocab, s0 + slice);
-  unsigned long long best = 0;
+  float best_v = -INFINITY;
+  int best_i = -1;
   bool bad_id = false, bad_x = false;
 
   for (int c0 = s0; c0 < s1; c0 += kChunk) {
@@ -145,46 +146,64 @@ __global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, in
     }
     if (hist || biased) __syncthreads();
 
-    auto rule = [&](float v, int i, uint32_t open) -> float {     // id c0 + i
-      if (hist) {
-        const uint32_t c = cnt[i];
-        if (c) {                           // in the prompt or in the answer
-          v = v > 0.f ? v / rep : v * rep;
-          const uint32_t k = c & ~kSeen;
-          if (k) v -= freq * (float)k + pres;
-        }
+    // the penalties of an id with count word c, then its bias word
+    auto touch = [&](float v, uint32_t c, uint32_t w) -> float {
+      if (hist && c) {                     // in the prompt or in the answer
+        v = v > 0.f ? v / rep : v * rep;
+        const uint32_t k = c & ~kSeen;
+        if (k) v -= freq * (float)k + pres;
       }
-      if (biased) {
-        const uint32_t w = bias[i];
-        if (w != kNoBias) v += __uint_as_float(w);
-      }
-      return open & 1 ? v : -INFINITY;
+      if (biased && w != kNoBias) v += __uint_as_float(w);
+      return v;
     };
-    auto take = [&](float v, int i) {                              // v as it is returned
-      if (v != v) {
-        bad_x = true;
-        return;
+    // v as it is returned; ids come in ascending order, so the first of equals stays
+    auto take = [&](float v, int id) {
+      bad_x |= v != v;
+      if (v > best_v) {
+        best_v = v;
+        best_i = id;
       }
-      const unsigned long long k = token_key(v, c0 + i);
-      best = k > best ? k : best;
     };
     if (vec) {
       for (int i = tid * E; i < n; i += kThreads * E) {
         T e[E];
+        uint32_t c[E], w[E];
         *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(x + c0 + i);
         const uint32_t open = mask ? mask[(c0 + i) >> 5] >> ((c0 + i) & 31) : 0xffffffffu;
+        uint32_t any = 0;
+#pragma unroll
+        for (int q = 0; q < E; q += 4) {
+          if (hist) {
+            const uint4 u = *reinterpret_cast<const uint4*>(cnt + i + q);
+            c[q] = u.x; c[q + 1] = u.y; c[q + 2] = u.z; c[q + 3] = u.w;
+            any |= u.x | u.y | u.z | u.w;
+          }
+          if (biased) {
+            const uint4 u = *reinterpret_cast<const uint4*>(bias + i + q);
+            w[q] = u.x; w[q + 1] = u.y; w[q + 2] = u.z; w[q + 3] = u.w;
+            any |= ~(u.x & u.y & u.z & u.w);
+          }
+        }
+        float f[E];
+#pragma unroll
+        for (int q = 0; q < E; ++q) f[q] = to_f(e[q]);
+        if (any) {
+#pragma unroll
+          for (int q = 0; q < E; ++q) f[q] = touch(f[q], hist ? c[q] : 0u, biased ? w[q] : kNoBias);
+        }
 #pragma unroll
         for (int q = 0; q < E; ++q) {
-          e[q] = from_f<T>(rule(to_f(e[q]), i + q, open >> q));
-          take(to_f(e[q]), i + q);
+          e[q] = from_f<T>((open >> q) & 1 ? f[q] : -INFINITY);
+          take(to_f(e[q]), c0 + i + q);
         }
         if (y) *reinterpret_cast<uint4*>(y + c0 + i) = *reinterpret_cast<const uint4*>(e);
       }
     } else {
       for (int i = tid; i < n; i += kThreads) {
-        const uint32_t open = mask ? mask[(c0 + i) >> 5] >> ((c0 + i) & 31) : 1u;
-        const T v = from_f<T>(rule(to_f(x[c0 + i]), i, open));
-        take(to_f(v), i);
+        const bool open = mask ? (mask[(c0 + i) >> 5] >> ((c0 + i) & 31)) & 1 : true;
+        const float f = touch(to_f(x[c0 + i]), hist ? cnt[i] : 0u, biased ? bias[i] : kNoBias);
+        const T v = from_f<T>(open ? f : -INFINITY);
+        take(to_f(v), c0 + i);
         if (y) y[c0 + i] = v;
       }
     }
@@ -193,6 +212,7 @@ __global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, in
   if (bad_id) atomicOr(&g_err_logits, ERRBIT_INDEX);
   if (bad_x) atomicOr(&g_err_logits, ERRBIT_NONFINITE);
   if (!token) return;                      // uniform over the cluster
+  unsigned long long best = best_i >= 0 ? token_key(best_v, best_i) : 0ull;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const unsigned long long k = __shfl_xor_sync(0xffffffffu, best, o);
@@ -211,9 +231,7 @@ __global__ void __launch_bounds__(kThreads) k_logits(const T* logits, T* out, in
       asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(tc::mapa_shared(tc::smem_u32(&s_key), c)));
       best = k > best ? k : best;
     }
-    // only a value above -inf is chosen
-    const bool any = (uint32_t)(best >> 32) > ~0xff800000u;
-    token[row] = any ? (int32_t)~(uint32_t)best : -1;
+    token[row] = best ? (int32_t)~(uint32_t)best : -1;     // nothing: no value above -inf
   }
   tc::cluster_sync();                      // the key was read before its CTA ends
 }
