@@ -540,7 +540,7 @@ typedef struct {
     const float*    bias;         /* [n_rows, n_bias] added; an id listed twice gets both,
                                    * added up in list order                                   */
     const uint32_t* mask;         /* [n_rows, mask_ld] bit i % 32 of word i / 32: id i allowed */
-    int64_t         history_ld;
+    int64_t         history_ld;   /* at most 262143                                           */
     int64_t         mask_ld;      /* >= ceil(vocab / 32)                                      */
     int32_t         n_bias;       /* at most 4096                                             */
 } cb_logit_rules;

@@ -1334,8 +1334,9 @@ int cb_logits_process(const void* logits, int32_t n_rows, int32_t vocab, int32_t
   if (r.n_bias < 0 || r.n_bias > 4096) return fail(CB_ERR_SHAPE, "n_bias %d outside [0, 4096]", r.n_bias);
   if (n_rows == 0 || (!out && !token)) return CB_OK;
   if (!logits) return fail(CB_ERR_INVALID_ARG, "logits is NULL");
-  if (r.history && (!r.history_len || r.history_ld < 0 || r.history_ld > INT32_MAX))
-    return fail(CB_ERR_INVALID_ARG, "history needs history_len and 0 <= history_ld < 2^31");
+  if (r.history && (!r.history_len || r.history_ld < 0))
+    return fail(CB_ERR_INVALID_ARG, "history needs history_len and history_ld >= 0");
+  if (r.history_ld > (1 << 18) - 1) return fail(CB_ERR_UNSUPPORTED, "history_ld %lld exceeds 262143", (long long)r.history_ld);
   if (!r.history && r.history_ld != 0) return fail(CB_ERR_INVALID_ARG, "history is NULL with history_ld != 0");
   if (r.n_bias > 0 && (!r.bias_id || !r.bias)) return fail(CB_ERR_INVALID_ARG, "n_bias > 0 needs bias_id and bias");
   if (r.mask && r.mask_ld < (vocab + 31) / 32) return fail(CB_ERR_SHAPE, "mask_ld shorter than ceil(vocab / 32)");

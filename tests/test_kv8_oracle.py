@@ -178,6 +178,7 @@ def test_logits_process_refuses_bad_arguments(lib):
     assert lp(none, out=FAKE + 16) == 1                            # overlaps without being the same
     assert lp(rules(history=FAKE, history_ld=5)) == 1              # no lengths
     assert lp(rules(history=FAKE, history_len=FAKE, history_ld=-1)) == 1
+    assert lp(rules(history=FAKE, history_len=FAKE, history_ld=1 << 18)) == 8
     assert lp(rules(history_ld=4, repetition=FAKE)) == 1           # ids announced, none given
     assert lp(rules(n_bias=2)) == 1 and lp(rules(n_bias=-1)) == 2 and lp(rules(n_bias=4097, bias=FAKE, bias_id=FAKE)) == 2
     assert lp(rules(mask=FAKE, mask_ld=3)) == 2                    # 100 ids need 4 words
