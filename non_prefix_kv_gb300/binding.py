@@ -422,35 +422,72 @@ def cb_stream_wait(stream, event):
 
 
 # ---- 8-bit KV cache of an answer in progress, rules on the logits ---------------------------
-def _buf(what: str, t, dtype: str, n: Optional[int] = None) -> Optional[int]:
+# These calls come once per token and layer, so their marshalling is kept short: the current
+# device and stream are looked up once per call, torch's types once per process.
+class _Torch:
+    """torch and the types of the row dtypes, loaded at the first use."""
+
+    def __init__(self):
+        import torch
+        self.mod, self.i8, self.i32, self.f32 = torch, torch.int8, torch.int32, torch.float32
+        self.row = {CB_F32: torch.float32, CB_BF16: torch.bfloat16}
+        self.cb = {v: k for k, v in self.row.items()}
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+    def device(self) -> int:
+        cuda = self.mod.cuda
+        return cuda.current_device() if cuda.is_initialized() or cuda.is_available() else -2
+
+    def stream(self, stream, dev: int):
+        if stream is None and self.raw_stream is not None and dev >= 0:
+            return self.raw_stream(dev)
+        return _stream(stream)
+
+
+_TORCH = None
+
+
+def _torch() -> _Torch:
+    global _TORCH
+    if _TORCH is None:
+        _TORCH = _Torch()
+    return _TORCH
+
+
+def _buf(what: str, t, dtype, n: Optional[int], dev: int) -> Optional[int]:
     """The address of a buffer.  A tensor must be contiguous, on the current CUDA device, of
-    the element type and hold n elements; raw pointers pass unchecked."""
-    if t is None or isinstance(t, int):
+    the element type and hold n elements (None: any number); raw pointers pass unchecked."""
+    if t is None or type(t) is int:
         return t
-    import torch
-    if t.dtype is not getattr(torch, dtype):
+    if t.dtype is not dtype:
         raise ValueError(f"{what}: {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: not contiguous")
     if n is not None and t.numel() != n:
         raise ValueError(f"{what}: {tuple(t.shape)} holds {t.numel()} elements, expected {n}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{what}: on {t.device}, not on the current CUDA device")
     return t.data_ptr()
 
 
-_ROW_DTYPE = {CB_F32: "float32", CB_BF16: "bfloat16"}
+def _ws(t, dev: int):
+    """Address and size of a workspace tensor."""
+    if t is None:
+        return None, 0
+    return _buf("ws", t, t.dtype, None, dev), t.numel() * t.element_size()
 
 
 def kv8_cache(k_codes, v_codes, k_scale, v_scale, block: int) -> cb_kv8_cache:
     """The handle of a cache in these tensors: codes [n_seq, Hkv, capacity, head_dim] int8,
     scales [n_seq, Hkv, capacity / block] float32."""
+    T = _torch()
+    dev = T.device()
     n_seq, hkv, cap, hd = k_codes.shape
     if block not in (16, 32, 64, 128):
         raise ValueError(f"block {block} is not 16, 32, 64 or 128")
     ns = n_seq * hkv * (cap // block)
-    c = cb_kv8_cache(_buf("k_codes", k_codes, "int8"), _buf("v_codes", v_codes, "int8", k_codes.numel()),
-                     _buf("k_scale", k_scale, "float32", ns), _buf("v_scale", v_scale, "float32", ns), cap, n_seq, block)
+    c = cb_kv8_cache(_buf("k_codes", k_codes, T.i8, None, dev), _buf("v_codes", v_codes, T.i8, k_codes.numel(), dev),
+                     _buf("k_scale", k_scale, T.f32, ns, dev), _buf("v_scale", v_scale, T.f32, ns, dev), cap, n_seq, block)
     c.hkv, c.hd, c.tensors = hkv, hd, (k_codes, v_codes, k_scale, v_scale)
     return c
 
@@ -462,17 +499,21 @@ def _kv8(cache: cb_kv8_cache, dims: cb_dims):
 
 
 def cb_kv8_append(k, v, n_rows: int, start, count, cache: cb_kv8_cache, dims: cb_dims, stream=None):
-    dt, n = _ROW_DTYPE[dims.dtype], cache.n_seq * n_rows * cache.hkv * cache.hd
+    T = _torch()
+    dev, dt, ns = T.device(), T.row[dims.dtype], cache.n_seq
+    n = ns * n_rows * cache.hkv * cache.hd
     _check("cb_kv8_append", lib().cb_kv8_append(
-        _buf("k", k, dt, n), _buf("v", v, dt, n), n_rows, _buf("start", start, "int32", cache.n_seq),
-        _buf("count", count, "int32", cache.n_seq), _kv8(cache, dims), C.byref(dims), _stream(stream)))
+        _buf("k", k, dt, n, dev), _buf("v", v, dt, n, dev), n_rows, _buf("start", start, T.i32, ns, dev),
+        _buf("count", count, T.i32, ns, dev), _kv8(cache, dims), C.byref(dims), T.stream(stream, dev)))
 
 
 def cb_kv8_read(cache: cb_kv8_cache, start, count, n_rows: int, dims: cb_dims, k_out, v_out, stream=None):
-    dt, n = _ROW_DTYPE[dims.dtype], cache.n_seq * n_rows * cache.hkv * cache.hd
+    T = _torch()
+    dev, dt, ns = T.device(), T.row[dims.dtype], cache.n_seq
+    n = ns * n_rows * cache.hkv * cache.hd
     _check("cb_kv8_read", lib().cb_kv8_read(
-        _kv8(cache, dims), _buf("start", start, "int32", cache.n_seq), _buf("count", count, "int32", cache.n_seq),
-        n_rows, C.byref(dims), _buf("k_out", k_out, dt, n), _buf("v_out", v_out, dt, n), _stream(stream)))
+        _kv8(cache, dims), _buf("start", start, T.i32, ns, dev), _buf("count", count, T.i32, ns, dev), n_rows,
+        C.byref(dims), _buf("k_out", k_out, dt, n, dev), _buf("v_out", v_out, dt, n, dev), T.stream(stream, dev)))
 
 
 def cb_kv8_workspace_bytes(dims: cb_dims, n_seq: int, capacity: int, n_q: int, with_weights: bool = False) -> int:
@@ -483,21 +524,26 @@ def cb_kv8_workspace_bytes(dims: cb_dims, n_seq: int, capacity: int, n_q: int, w
 
 
 def cb_kv8_attention(q, last, n_q: int, cache: cb_kv8_cache, dims: cb_dims, out, weights=None, ws=None, stream=None):
-    dt, n = _ROW_DTYPE[dims.dtype], cache.n_seq * n_q * dims.n_heads * dims.head_dim
+    T = _torch()
+    dev, dt, ns = T.device(), T.row[dims.dtype], cache.n_seq
+    n = ns * n_q * dims.n_heads * dims.head_dim
+    w, wn = _ws(ws, dev)
     _check("cb_kv8_attention", lib().cb_kv8_attention(
-        _buf("q", q, dt, n), _buf("last", last, "int32", cache.n_seq * n_q), n_q, _kv8(cache, dims), C.byref(dims),
-        _buf("out", out, dt, n), _buf("weights", weights, "float32", cache.n_seq * cache.hkv * cache.capacity),
-        _ptr(ws), _nbytes(ws), _stream(stream)))
+        _buf("q", q, dt, n, dev), _buf("last", last, T.i32, ns * n_q, dev), n_q, _kv8(cache, dims), C.byref(dims),
+        _buf("out", out, dt, n, dev), _buf("weights", weights, T.f32, ns * cache.hkv * cache.capacity, dev), w, wn,
+        T.stream(stream, dev)))
 
 
 def cb_kv8_evict(src: cb_kv8_cache, length, weights, n_keep: int, n_sink: int, n_recent: int, dst: cb_kv8_cache,
                  dst_len, dst_weights, kept, dims: cb_dims, stream=None):
-    heads = src.n_seq * src.hkv
+    T = _torch()
+    dev, ns, heads = T.device(), src.n_seq, src.n_seq * src.hkv
     _check("cb_kv8_evict", lib().cb_kv8_evict(
-        _kv8(src, dims), _buf("length", length, "int32", src.n_seq),
-        _buf("weights", weights, "float32", heads * src.capacity), n_keep, n_sink, n_recent, _kv8(dst, dims),
-        _buf("dst_len", dst_len, "int32", src.n_seq), _buf("dst_weights", dst_weights, "float32", heads * dst.capacity),
-        _buf("kept", kept, "int32", heads * n_keep), C.byref(dims), _stream(stream)))
+        _kv8(src, dims), _buf("length", length, T.i32, ns, dev),
+        _buf("weights", weights, T.f32, heads * src.capacity, dev), n_keep, n_sink, n_recent, _kv8(dst, dims),
+        _buf("dst_len", dst_len, T.i32, ns, dev),
+        _buf("dst_weights", dst_weights, T.f32, heads * dst.capacity, dev),
+        _buf("kept", kept, T.i32, heads * n_keep, dev), C.byref(dims), T.stream(stream, dev)))
 
 
 def logit_rules(history=None, history_len=None, prompt_len=None, repetition=None, presence=None, frequency=None,
@@ -513,13 +559,15 @@ def logit_rules(history=None, history_len=None, prompt_len=None, repetition=None
         raise ValueError("bias and bias_id must have one shape")
     if history is None and any(t is not None for t in (history_len, prompt_len, repetition, presence, frequency)):
         raise ValueError("lengths and penalties need a history")
+    T = _torch()
+    dev, n = T.device(), rows[0] if rows else None
     r = cb_logit_rules(
-        _buf("history", history, "int32"), _buf("history_len", history_len, "int32"),
-        _buf("prompt_len", prompt_len, "int32"), _buf("repetition", repetition, "float32"),
-        _buf("presence", presence, "float32"), _buf("frequency", frequency, "float32"),
-        _buf("bias_id", bias_id, "int32"), _buf("bias", bias, "float32"), _buf("mask", mask, "int32"),
-        0 if history is None else history.shape[1], 0 if mask is None else mask.shape[1],
-        0 if bias_id is None else bias_id.shape[1])
+        _buf("history", history, T.i32, None, dev), _buf("history_len", history_len, T.i32, n, dev),
+        _buf("prompt_len", prompt_len, T.i32, n, dev), _buf("repetition", repetition, T.f32, n, dev),
+        _buf("presence", presence, T.f32, n, dev), _buf("frequency", frequency, T.f32, n, dev),
+        _buf("bias_id", bias_id, T.i32, None, dev), _buf("bias", bias, T.f32, None, dev),
+        _buf("mask", mask, T.i32, None, dev), 0 if history is None else history.shape[1],
+        0 if mask is None else mask.shape[1], 0 if bias_id is None else bias_id.shape[1])
     r.n_rows = rows[0] if rows else None
     r.tensors = (history, history_len, prompt_len, repetition, presence, frequency, bias_id, bias, mask)
     return r
@@ -527,12 +575,14 @@ def logit_rules(history=None, history_len=None, prompt_len=None, repetition=None
 
 def cb_logits_process(logits, rules: cb_logit_rules, out=None, token=None, stream=None):
     """logits [n_rows, vocab] float32 or bfloat16; out (may be logits) and token as in the header."""
+    T = _torch()
+    dev = T.device()
     n, vocab = logits.shape
     if rules.n_rows is not None and rules.n_rows != n:
         raise ValueError(f"rules for {rules.n_rows} rows, logits of {n}")
-    dt = {v: k for k, v in _ROW_DTYPE.items()}.get(str(logits.dtype).split(".")[-1])
+    dt = T.cb.get(logits.dtype)
     if dt is None:
         raise ValueError(f"logits: {logits.dtype}, expected float32 or bfloat16")
     _check("cb_logits_process", lib().cb_logits_process(
-        _buf("logits", logits, _ROW_DTYPE[dt]), n, vocab, dt, C.byref(rules), _buf("out", out, _ROW_DTYPE[dt], n * vocab),
-        _buf("token", token, "int32", n), _stream(stream)))
+        _buf("logits", logits, logits.dtype, None, dev), n, vocab, dt, C.byref(rules),
+        _buf("out", out, logits.dtype, n * vocab, dev), _buf("token", token, T.i32, n, dev), T.stream(stream, dev)))

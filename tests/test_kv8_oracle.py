@@ -190,7 +190,7 @@ def test_binding_refuses_wrong_tensors():
     s = torch.zeros(1, 2, 1)
     with pytest.raises(ValueError, match="current CUDA device"):
         B.kv8_cache(k, k.clone(), s, s.clone(), 32)
-    with pytest.raises(ValueError, match="expected int8"):
+    with pytest.raises(ValueError, match="expected torch.int8"):
         B.kv8_cache(k.float(), k, s, s, 32)
     with pytest.raises(ValueError, match="not contiguous"):
         B.kv8_cache(k.transpose(1, 2), k, s, s, 32)
