@@ -57,13 +57,18 @@ struct Kv8Tc {
   const bf16* q;
   const int32_t* last;      // [n_seq, n_q]
   bf16* out;
-  const uint8_t* kx;        // [n_seq * Hkv, tiles] key tiles in shared-memory order: bf16 codes
-  const uint8_t* vx;        // the same of V: fp16 codes
-  float* lse;               // [n_seq * Hkv, n_q * G] log2 of a row's sum, or null
+  uint8_t* kx;              // [n_seq * Hkv, tiles] key tiles in shared-memory order: bf16 codes
+  uint8_t* vx;              // the same of V: fp16 codes
+  int32_t* seq_max;         // [n_seq] the last row any query of the sequence sees
+  // for the weights (else null), per (sequence, KV head, query tile):
+  uint8_t* qx;              // the tile's query rows in shared-memory order
+  float* rows;              // [2][BM] log2 of each row's sum (+inf where there is none), last row it sees (int)
+  int32_t* tile_max;        // [n_seq, query tiles] the last row any query of the tile sees
   float* weights;           // [n_seq, Hkv, capacity]
   cb_kv8_cache c;
-  int n_q, H, Hkv, G, lg, tiles;
+  int n_q, H, Hkv, G, lg, tiles, q_tiles;
   int qpt;                  // queries per tile: 128 / G
+  int g_magic;              // ceil(2^16 / G): r / G = r g_magic >> 16 for r < 128
   float scale_log2;
 };
 
@@ -95,28 +100,47 @@ __global__ void __launch_bounds__(256) k_kv8_expand(const Kv8Tc p) {
   pdl_wait();
   pdl_trigger();
   const int tile = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
-  // some query sees the tile's first key?  (the newest rows usually come last)
-  bool need = false;
-  for (int j = p.n_q - 1 - (int)threadIdx.x; !need; j -= 256) {
-    const bool in = j >= 0 && last_of(p, s, j) >= tile * BN;
-    need = __syncthreads_or(in);
-    if (__syncthreads_and(j < 256)) break;
-  }
-  if (!need) return;
   const int64_t head = (int64_t)s * p.Hkv + h, row0 = (int64_t)tile * BN;
   const int64_t src = (head * p.c.capacity + row0) * HD, dst = (head * p.tiles + tile) * (int64_t)(BN * HD * 2);
   constexpr int PER = HD / 16;             // pieces of 16 codes in a row
+  constexpr int N = BN * PER / 256;        // pieces of a thread
+  // all loads first: they and the look for a query that sees the tile share one latency
+  uint4 k[N], v[N];
 #pragma unroll
-  for (int i = 0; i < BN * PER / 256; ++i) {
+  for (int i = 0; i < N; ++i) {
     const int idx = i * 256 + threadIdx.x, row = idx / PER, piece = idx % PER;
-    uint4 k = make_uint4(0, 0, 0, 0), v = k;
+    k[i] = v[i] = make_uint4(0, 0, 0, 0);
     if (row0 + row < p.c.capacity) {
-      k = *reinterpret_cast<const uint4*>(p.c.k_codes + src + row * HD + piece * 16);
-      v = *reinterpret_cast<const uint4*>(p.c.v_codes + src + row * HD + piece * 16);
+      k[i] = *reinterpret_cast<const uint4*>(p.c.k_codes + src + row * HD + piece * 16);
+      v[i] = *reinterpret_cast<const uint4*>(p.c.v_codes + src + row * HD + piece * 16);
     }
-    const uint32_t kw[4] = {k.x, k.y, k.z, k.w}, vw[4] = {v.x, v.y, v.z, v.w};
-    uint8_t* kd = const_cast<uint8_t*>(p.kx) + dst + (piece >> 2) * SLAB + row * 128;
-    uint8_t* vd = const_cast<uint8_t*>(p.vx) + dst + (piece >> 2) * SLAB + row * 128;
+  }
+  if (tile == 0 && h == 0) {               // the sequence's largest bound, for the kernels after this one
+    int mx = -1;
+    for (int j = threadIdx.x; j < p.n_q; j += 256) mx = max(mx, last_of(p, s, j));
+    __shared__ int sm[8];
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = mx;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int w = 0; w < 8; ++w) mx = max(mx, sm[w]);
+      p.seq_max[s] = mx;
+    }
+  }
+  // some query sees the tile's first key?  (the newest rows usually come last)
+  bool need = false;
+  for (int j = p.n_q - 1 - (int)threadIdx.x; !need; j -= 256) {
+    need = __syncthreads_or(j >= 0 && last_of(p, s, j) >= tile * BN);
+    if (__syncthreads_and(j < 256)) break;
+  }
+  if (!need) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int idx = i * 256 + threadIdx.x, row = idx / PER, piece = idx % PER;
+    const uint32_t kw[4] = {k[i].x, k[i].y, k[i].z, k[i].w}, vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint8_t* kd = p.kx + dst + (piece >> 2) * SLAB + row * 128;
+    uint8_t* vd = p.vx + dst + (piece >> 2) * SLAB + row * 128;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int at = ((2 * (piece & 3) + c) ^ (row & 7)) * 16;
@@ -138,7 +162,7 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const Kv8Tc& p, int j0, int r) {
   Row x;
-  const int jl = r / p.G;
+  const int jl = r * p.g_magic >> 16;
   x.j = j0 + jl;
   x.g = r - jl * p.G;
   x.on = jl < p.qpt && x.j >= 0;
@@ -149,11 +173,12 @@ __device__ __forceinline__ Row row_of(const Kv8Tc& p, int j0, int r) {
 // do not exist are zero); the caller waits for them and fences.
 template <int HD>
 __device__ __forceinline__ void gather_q(const Kv8Tc& p, int s, int h, int j0, uint8_t* dst, int tid, int n_thr) {
-  constexpr int PER = HD / 8;              // 16-byte pieces in a row
-  for (int i = tid; i < BM * PER; i += n_thr) {
-    const int r = i / PER, piece = i % PER;
+  constexpr int PER = HD / 8;              // 16-byte pieces in a row; n_thr is a multiple of it
+  const int piece = tid % PER;
+  const bf16* q = p.q + ((int64_t)s * p.n_q * p.H + (int64_t)h * p.G) * HD + piece * 8;
+  for (int r = tid / PER; r < BM; r += n_thr / PER) {
     const Row x = row_of(p, j0, r);
-    const bf16* src = p.q + (((int64_t)s * p.n_q + (x.on ? x.j : 0)) * p.H + (int64_t)h * p.G + (x.on ? x.g : 0)) * HD + piece * 8;
+    const bf16* src = q + ((int64_t)(x.on ? x.j : 0) * p.H + (x.on ? x.g : 0)) * HD;
     const uint32_t d = tc::smem_u32(dst + (piece >> 3) * SLAB + r * 128 + (((piece & 7) ^ (r & 7)) * 16));
     const int bytes = x.on ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
@@ -196,43 +221,93 @@ __device__ __forceinline__ Scales load_scales(const float* ks, const float* vs, 
   return r;
 }
 
-// One key tile of a softmax group; a thread owns one row of S_g and O_g in TMEM.  sc: the
-// tile's scale groups in the warp's own shared memory.
-template <int HD>
-__device__ __forceinline__ bool softmax_tile(uint64_t* s_full_g, uint64_t* p_full_g, uint64_t* pv_done_g, uint32_t u,
-                                             int key0, int last, uint32_t tS, uint32_t tO, const float4* sc,
-                                             float& m_used, float& l, int lane) {
-  if (!__all_sync(0xffffffffu, tc::mbar_wait(s_full_g, u & 1))) return false;
-  const bool none = __all_sync(0xffffffffu, key0 > last);
-  const bool full_row = key0 + BN - 1 <= last;
+// Pass 1 over a row's scores of one key tile: the largest t.  FULL: every row of the warp sees
+// every key (the common case, without a comparison per element).
+template <bool FULL>
+__device__ __forceinline__ float tile_max(uint32_t tS, int seen, const float4* sc) {
   float mt = -INFINITY;
-  if (!none) {
-    tc::tc_fence_after();
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t sr[64];
-      tc::tmem_ld32_nowait(tS + hf * 64, sr);
-      tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
-      tc::tmem_wait_ld();
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t sr[64];
+    tc::tmem_ld32_nowait(tS + hf * 64, sr);
+    tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
+    tc::tmem_wait_ld();
 #pragma unroll
-      for (int gg = 0; gg < 4; ++gg) {
-        float a = -INFINITY, b = -INFINITY;
-        if (full_row) {
+    for (int gg = 0; gg < 4; ++gg) {
+      float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            a = fmax3(a, __uint_as_float(sr[gg * 16 + i]), __uint_as_float(sr[gg * 16 + i + 1]));
-            b = fmax3(b, __uint_as_float(sr[gg * 16 + i + 2]), __uint_as_float(sr[gg * 16 + i + 3]));
-          }
-        } else {
+      for (int i = 0; i < 16; i += 4) {
+        float x[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (key0 + hf * 64 + gg * 16 + i <= last) a = fmaxf(a, __uint_as_float(sr[gg * 16 + i]));
+        for (int q = 0; q < 4; ++q) {
+          x[q] = __uint_as_float(sr[gg * 16 + i + q]);
+          if (!FULL && hf * 64 + gg * 16 + i + q > seen) x[q] = -INFINITY;
         }
-        const float4 c = sc[hf * 4 + gg];
-        mt = fmaxf(mt, fmaf(fmaxf(a, b), c.x, c.y));
+        a = fmax3(a, x[0], x[1]);
+        b = fmax3(b, x[2], x[3]);
       }
+      const float4 c = sc[hf * 4 + gg];
+      mt = fmaxf(mt, fmaf(fmaxf(a, b), c.x, c.y));
     }
   }
+  return mt;
+}
+// Pass 2: P = 2^(t - m + bias) over S as fp16 pairs (keys 2w, 2w + 1 to column w; the scores of
+// keys 0..63 are read before their columns are overwritten), and its sum with 1 / vs.
+template <bool FULL>
+__device__ __forceinline__ float tile_weights(uint32_t tS, int seen, const float4* sc, float off) {
+  float l = 0.f;
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t sr[64];
+    tc::tmem_ld32_nowait(tS + hf * 64, sr);
+    tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int gg = 0; gg < 2; ++gg) {
+        const float4 k = sc[hf * 4 + c * 2 + gg];
+        const uint64_t f2 = f2_pack(k.x, k.x), a2 = f2_pack(k.y + off, k.y + off);
+        uint64_t sum = 0ull;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const int k0 = c * 32 + gg * 16 + 2 * w;
+          const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, a2));
+          float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
+          if (!FULL) {
+            p0 = hf * 64 + k0 <= seen ? p0 : 0.f;
+            p1 = hf * 64 + k0 + 1 <= seen ? p1 : 0.f;
+          }
+          sum = f2_add(sum, f2_pack(p0, p1));
+          const __half2 h2 = __floats2half2_rn(p0, p1);
+          pk[gg * 8 + w] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        const float2 sm = f2_unpack(sum);
+        l = fmaf(sm.x + sm.y, k.z, l);
+      }
+      tc::tmem_st16u_nowait(tS + hf * 32 + c * 16, pk);
+    }
+  }
+  return l;
+}
+
+// One key tile of a softmax group; a thread owns one row of S_g and O_g in TMEM.  seen: the
+// last key of the tile that the row sees (may be negative or beyond it).  sc: the tile's scale
+// groups in the warp's own shared memory.
+template <int HD>
+__device__ __forceinline__ bool softmax_tile(uint64_t* s_full_g, uint64_t* p_full_g, uint64_t* pv_done_g, uint32_t u,
+                                             int seen, uint32_t tS, uint32_t tO, const float4* sc, float& m_used,
+                                             float& l, int lane) {
+  if (!__all_sync(0xffffffffu, tc::mbar_wait(s_full_g, u & 1))) return false;
+  const bool none = __all_sync(0xffffffffu, seen < 0), full = __all_sync(0xffffffffu, seen >= BN - 1);
+  float mt = -INFINITY;
+  tc::tc_fence_after();
+  if (full)
+    mt = tile_max<true>(tS, seen, sc);
+  else if (!none)
+    mt = tile_max<false>(tS, seen, sc);
   if (u == 0) {
     m_used = mt;               // O_g is written, not added to, by this tile's P.V
   } else {
@@ -255,45 +330,16 @@ __device__ __forceinline__ bool softmax_tile(uint64_t* s_full_g, uint64_t* p_ful
     }
   }
   const float off = kPBias - (m_used == -INFINITY ? 0.f : m_used);
+  if (full) {
+    l += tile_weights<true>(tS, seen, sc, off);
+  } else if (!none) {
+    l += tile_weights<false>(tS, seen, sc, off);
+  } else {
+    uint32_t pk[16];
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    uint32_t sr[64];
-    if (!none) {
-      tc::tmem_ld32_nowait(tS + hf * 64, sr);
-      tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
-      tc::tmem_wait_ld();
-    }
+    for (int w = 0; w < 16; ++w) pk[w] = 0u;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t pk[16];
-      if (none) {
-#pragma unroll
-        for (int w = 0; w < 16; ++w) pk[w] = 0u;
-      } else {
-#pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-          const float4 k = sc[hf * 4 + c * 2 + gg];
-          const uint64_t f2 = f2_pack(k.x, k.x), a2 = f2_pack(k.y + off, k.y + off);
-          uint64_t sum = 0ull;
-#pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            const int k0 = c * 32 + gg * 16 + 2 * w, key = key0 + hf * 64 + k0;
-            const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, a2));
-            float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
-            if (!full_row) {
-              p0 = key <= last ? p0 : 0.f;
-              p1 = key + 1 <= last ? p1 : 0.f;
-            }
-            sum = f2_add(sum, f2_pack(p0, p1));
-            const __half2 h2 = __floats2half2_rn(p0, p1);
-            pk[gg * 8 + w] = *reinterpret_cast<const uint32_t*>(&h2);
-          }
-          const float2 sm = f2_unpack(sum);
-          l = fmaf(sm.x + sm.y, k.z, l);
-        }
-      }
-      tc::tmem_st16u_nowait(tS + hf * 32 + c * 16, pk);
-    }
+    for (int c = 0; c < 4; ++c) tc::tmem_st16u_nowait(tS + c * 16, pk);
   }
   tc::tmem_wait_st();
   tc::tc_fence_before();
@@ -372,6 +418,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) mx = max(mx, wm[w]);
   __syncthreads();                 // wm's memory is the groups' row maxima later on
+  // for the weights: the tile's queries as they sit in shared memory, and its bound
+  const int64_t qt = head * p.q_tiles + blockIdx.y;
+  if (p.weights && rank == 0 && tid == 0) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p.qx + qt * L::T_BYTES),
+                 "r"(tc::smem_u32(sQ)), "r"((uint32_t)L::T_BYTES)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    if (h == 0) p.tile_max[s * p.q_tiles + blockIdx.y] = mx;
+  }
   const int64_t nk = (int64_t)mx + 1;
   const int all = (mx + BN) / BN;  // key tiles; 0 if no row sees a key
   const int ta = (int)((int64_t)all * rank / n_split), T = (int)((int64_t)all * (rank + 1) / n_split) - ta;
@@ -467,7 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
       }
       nx = load_scales(ks, vs, p.lg, ta + j + 2, nk, lane);
       __syncwarp();
-      ok = softmax_tile<HD>(&s_full[grp], &p_full[grp], &pv_done[grp], (uint32_t)u, (ta + j) * BN, last, trow + grp * BN,
+      ok = softmax_tile<HD>(&s_full[grp], &p_full[grp], &pv_done[grp], (uint32_t)u, last - (ta + j) * BN, trow + grp * BN,
                             trow + TM_O + grp * HD, sc, m_used, l, lane);
     }
     // the group's last P.V, then both groups' row statistics meet in shared memory
@@ -487,9 +542,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
       if (n_split > 1) {
         cm[r] = mm;
         cm[BM + r] = lt;
-      } else if (p.lse && x.on) {
-        p.lse[head * p.n_q * p.G + (int64_t)x.j * p.G + x.g] = lt > 0.f ? mm - kPBias + log2f(lt) : INFINITY;
+      } else if (p.weights) {
+        p.rows[qt * 2 * BM + r] = lt > 0.f ? mm - kPBias + log2f(lt) : INFINITY;
       }
+      if (p.weights && rank == 0) p.rows[qt * 2 * BM + BM + r] = __int_as_float(last);
     }
     // group g finalises columns [g HD/2, (g + 1) HD/2); O_g was never written with fewer than
     // g + 1 key tiles
@@ -538,7 +594,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
     for (int i = tid; i < per * W4; i += THREADS) {
       const int r = r0 + i / W4, w = i % W4;
       const Row x = row_of(p, j0, r);
-      if (!x.on) continue;
       float M = -INFINITY, sum = 0.f;
       for (int c = 0; c < n_split; ++c) M = fmaxf(M, tc::ld_cluster(tc::mapa_shared(cm_a + 4 * r, c)));
       float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -556,12 +611,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
       const float inv = sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[q] *= inv;
-      st4(p.out + (((int64_t)s * p.n_q + x.j) * p.H + (int64_t)h * p.G + x.g) * HD + 4 * w, o);
-      if (p.lse && w == 0)
-        p.lse[head * p.n_q * p.G + (int64_t)x.j * p.G + x.g] = sum > 0.f ? M - kPBias + log2f(sum) : INFINITY;
+      if (x.on) st4(p.out + (((int64_t)s * p.n_q + x.j) * p.H + (int64_t)h * p.G + x.g) * HD + 4 * w, o);
+      if (p.weights && w == 0) p.rows[qt * 2 * BM + r] = sum > 0.f ? M - kPBias + log2f(sum) : INFINITY;
     }
     tc::cluster_sync();            // the peers may still be reading this CTA's part
   }
+  if (p.weights && rank == 0 && tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   if (warp == 1) {
     __syncwarp();
     tc::tc_fence_after();
@@ -570,59 +625,77 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
 }
 
 // ---- weights --------------------------------------------------------------------------------
-// One CTA per (128 keys, KV head, sequence): S^T = C_K Q^T puts a key in each TMEM lane, so the
-// sum over the query rows stays inside a thread.  Row tiles go round four S buffers (TMEM 4 x
-// 128 columns); two softmax groups take alternate tiles, and their two sums per key meet at the
-// end.  Each Q tile is gathered by the softmax group that will read its scores, right after it
-// has finished the tile before.
+// S^T = C_K Q^T puts a key in each TMEM lane, so the sum over the query rows stays inside a
+// thread.  A resident CTA takes pairs of key tiles (of one KV head and sequence), one per
+// softmax group, and streams the query tiles that see them past both: a query tile is loaded
+// once for 256 keys, each group has two S buffers (TMEM 4 x 128 columns), and no sums have to
+// meet.  Warp roles as in the attention kernel.
+// Measured: 64 queries of 7 heads over 16384 rows of 8 KV heads, one CTA per key tile gathering
+// the queries itself 55 us (15 instructions per weight, and the start of 1024 CTAs).
 template <int HD>
 struct WLayout {
   static constexpr int T_BYTES = HD / 64 * SLAB;
-  static constexpr int QS = 4;                                // Q tiles: two per group
-  static constexpr int OFF_K = 0;
-  static constexpr int OFF_Q = T_BYTES;
-  static constexpr int OFF_L = OFF_Q + QS * T_BYTES;          // [QS][BM] float2 {log2 sum, last}
-  static constexpr int OFF_X = OFF_L + QS * BM * 8;           // [BM] the second group's sums
-  static constexpr int OFF_BAR = OFF_X + BM * 4;
+  static constexpr int QS = 4;                                // query tiles in flight
+  static constexpr int OFF_K = 0;                             // [2]
+  static constexpr int OFF_Q = 2 * T_BYTES;                   // [QS]
+  static constexpr int OFF_L = OFF_Q + QS * T_BYTES;          // [QS][2][BM] log2 sum, last
+  static constexpr int OFF_BAR = OFF_L + QS * 2 * BM * 4;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
 };
 
+// The query tiles that see a pair of key tiles, in ascending order, 32 bounds at a time; every
+// role of the CTA walks the same list.
+struct TileWalk {
+  const int32_t* bound;     // of the sequence's query tiles
+  int n, key0, base, lane;
+  unsigned mask;
+  __device__ __forceinline__ TileWalk(const int32_t* b, int n_, int key0_, int lane_)
+      : bound(b), n(n_), key0(key0_), base(-32), lane(lane_), mask(0) {}
+  // the next tile, -1 at the end
+  __device__ __forceinline__ int next() {
+    while (!mask) {
+      base += 32;
+      if (base >= n) return -1;
+      mask = __ballot_sync(0xffffffffu, base + lane < n && bound[base + lane] >= key0);
+    }
+    const int y = base + __ffs(mask) - 1;
+    mask &= mask - 1;
+    return y;
+  }
+};
+
 template <int HD>
 __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
-  pdl_wait();
-  pdl_trigger();
   using L = WLayout<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sK = base + L::OFF_K;
   uint8_t* sQ = base + L::OFF_Q;
-  float2* sL = reinterpret_cast<float2*>(base + L::OFF_L);
-  float* sx = reinterpret_cast<float*>(base + L::OFF_X);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
-  uint64_t* q_full = k_full + 1;     // [QS] the group's four warps gathered a Q tile
-  uint64_t* s_full = q_full + L::QS; // [QS]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + L::QS);
-
+  const float* sL = reinterpret_cast<const float*>(base + L::OFF_L);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);   // [2]
+  uint64_t* k_empty = k_full + 2;                                       // [2]
+  uint64_t* q_full = k_empty + 2;                                       // [QS]
+  uint64_t* q_empty = q_full + L::QS;                                   // [QS] the MMA and every softmax warp
+  uint64_t* s_full = q_empty + L::QS;                                   // [2 groups][2]
+  uint64_t* s_empty = s_full + 4;                                       // [2][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_empty + 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int key0 = blockIdx.x * BN, h = blockIdx.y, s = blockIdx.z;
-  const int64_t head = (int64_t)s * p.Hkv + h;
-  const int n_tiles = (p.n_q + p.qpt - 1) / p.qpt;
   if (tid == 0) {
-    tc::mbar_init(k_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&k_full[i], 1);
+      tc::mbar_init(&k_empty[i], 1);
+    }
     for (int i = 0; i < L::QS; ++i) {
-      tc::mbar_init(&q_full[i], 4);
+      tc::mbar_init(&q_full[i], 1);
+      tc::mbar_init(&q_empty[i], 1 + NSOFT);
+    }
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&s_empty[i], 4);
     }
     tc::fence_mbar_init();
   }
-  // does any query see the first key?
-  bool need = false;
-  for (int j = p.n_q - 1 - tid; !need; j -= THREADS) {
-    need = __syncthreads_or(j >= 0 && last_of(p, s, j) >= key0);
-    if (__syncthreads_and(j < THREADS)) break;
-  }
-  if (!need) return;
   if (warp == 1) {
     tc::tmem_alloc(tmem_slot, TMEM_COLS);
     tc::tmem_relinquish();
@@ -631,102 +704,168 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  const int pairs = (p.tiles + 1) / 2;
+  const int64_t items = (int64_t)p.c.n_seq * p.Hkv * pairs;
+  // calls f(head, sequence, first key tile, whether a query sees the second) for this CTA's pairs
+  auto each = [&](auto&& f) {
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+      const int64_t head = it / pairs;
+      const int s = (int)(head / p.Hkv), kt = 2 * (int)(it - head * pairs), mx = p.seq_max[s];
+      if (kt * BN > mx) continue;
+      if (!f(head, s, kt, kt + 1 < p.tiles && (kt + 1) * BN <= mx)) break;
+    }
+  };
 
   if (warp == 0) {
-    if (lane == 0) {
-      tc::mbar_expect_tx(k_full, L::T_BYTES);
-      tc::bulk_load(sK, p.kx + (head * p.tiles + blockIdx.x) * (int64_t)L::T_BYTES, L::T_BYTES, k_full);
-    }
+    // ------------------------------------------------------------------ copies
+    bool ok = true;
+    int n = 0, kn[2] = {0, 0};
+    each([&](int64_t head, int s, int kt, bool two) -> bool {
+      for (int g = 0; ok && g < (two ? 2 : 1); ++g) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&k_empty[g], (kn[g] & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          tc::mbar_expect_tx(&k_full[g], L::T_BYTES);
+          tc::bulk_load(sK + g * L::T_BYTES, p.kx + (head * p.tiles + kt + g) * (int64_t)L::T_BYTES, L::T_BYTES, &k_full[g]);
+        }
+        ++kn[g];
+      }
+      TileWalk walk(p.tile_max + s * p.q_tiles, p.q_tiles, kt * BN, lane);
+      for (int y; ok && (y = walk.next()) >= 0; ++n) {
+        const int b = n % L::QS;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[b], ((n / L::QS) & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          const int64_t qt = head * p.q_tiles + y;
+          tc::mbar_expect_tx(&q_full[b], L::T_BYTES + 2 * BM * 4);
+          tc::bulk_load(sQ + b * L::T_BYTES, p.qx + qt * L::T_BYTES, L::T_BYTES, &q_full[b]);
+          tc::bulk_load(base + L::OFF_L + b * 2 * BM * 4, p.rows + qt * 2 * BM, 2 * BM * 4, &q_full[b]);
+        }
+        __syncwarp();
+      }
+      return ok;
+    });
+    if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+    // no copy is in flight when the CTA ends, whoever gave up on what
+    for (int g = 0; g < 2; ++g)
+      if (kn[g] > 0) tc::mbar_wait(&k_full[g], (kn[g] - 1) & 1);
+    for (int i = n > L::QS ? n - L::QS : 0; i < n; ++i) tc::mbar_wait(&q_full[i % L::QS], (i / L::QS) & 1);
   } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issue
     constexpr uint32_t idesc = tc::idesc_bf16_f32(BN, BM);
     const uint64_t k_desc = tc::desc_sw128(tc::smem_u32(sK)), q_desc = tc::desc_sw128(tc::smem_u32(sQ));
-    bool ok = __all_sync(0xffffffffu, tc::mbar_wait(k_full, 0));
-    for (int y = 0; ok && y < n_tiles; ++y) {
-      // q_full also says that the group has read the scores this S buffer held four tiles ago
-      const int b = y % L::QS;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (y / L::QS) & 1));
-      if (!ok) break;
-      tc::tc_fence_after();
-      if (tc::elect_one()) {
-        const uint64_t qd = q_desc + (uint64_t)((b * L::T_BYTES) >> 4);
+    bool ok = true;
+    int n = 0, kn[2] = {0, 0}, sn[2] = {0, 0};
+    each([&](int64_t, int s, int kt, bool two) -> bool {
+      const int ng = two ? 2 : 1;
+      for (int g = 0; ok && g < ng; ++g) ok = __all_sync(0xffffffffu, tc::mbar_wait(&k_full[g], kn[g]++ & 1));
+      TileWalk walk(p.tile_max + s * p.q_tiles, p.q_tiles, kt * BN, lane);
+      for (int y = walk.next(); ok && y >= 0; ++n) {
+        const int b = n % L::QS, ahead = walk.next();
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (n / L::QS) & 1));
+        for (int g = 0; ok && g < ng; ++g) {
+          const int sb = sn[g] & 1;
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_empty[2 * g + sb], ((sn[g] >> 1) & 1) ^ 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+            const uint64_t kd = k_desc + (uint64_t)((g * L::T_BYTES) >> 4), qd = q_desc + (uint64_t)((b * L::T_BYTES) >> 4);
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + b * BM, k_desc + off, qd + off, idesc, k > 0);
+            for (int k = 0; k < HD / 16; ++k) {
+              const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+              tc::mma_bf16(tmem + (2 * g + sb) * BM, kd + off, qd + off, idesc, k > 0);
+            }
+            tc::mma_commit(&s_full[2 * g + sb]);
+            if (g == ng - 1) tc::mma_commit(&q_empty[b]);
+            if (ahead < 0) tc::mma_commit(&k_empty[g]);
+          }
+          __syncwarp();
+          ++sn[g];
         }
-        tc::mma_commit(&s_full[b]);
+        y = ahead;
       }
-      __syncwarp();
-    }
+      return ok;
+    });
     if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
   } else {
+    // ------------------------------------------------------------------ softmax
     const int grp = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const int gt = (warp - 2 - 4 * grp) * 32 + lane;       // thread of the group
-    const int key = key0 + r;
-    const bool live = key < p.c.capacity;
-    float f = 0.f;
-    if (live) f = fmaxf(p.c.k_scale[head * (p.c.capacity >> p.lg) + (key >> p.lg)], kKv8MinScale) * p.scale_log2;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const float* lse = p.lse + head * p.n_q * p.G;
-    // starts gathering Q tile y, with its rows' sums and bounds, into its buffer ...
-    auto gather = [&](int y) {
-      const int b = y % L::QS, j0 = p.n_q - (y + 1) * p.qpt;
-      gather_q<HD>(p, s, h, j0, sQ + b * L::T_BYTES, gt, 128);
-      const Row x = row_of(p, j0, gt);
-      float2 v = make_float2(INFINITY, __int_as_float(-1));
-      if (x.on) v = make_float2(lse[(int64_t)x.j * p.G + x.g], __int_as_float(last_of(p, s, x.j)));
-      sL[b * BM + gt] = v;
-    };
-    // ... and hands it to the tensor core
-    auto gathered = [&](int y) {
-      cp_async_wait_all();
-      tc::fence_proxy_async_smem();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&q_full[y % L::QS]);
-    };
-    float sum = 0.f;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + grp * 2 * BM;
     bool ok = true;
-    if (grp < n_tiles) {
-      gather(grp);
-      gathered(grp);
-    }
-    for (int y = grp; y < n_tiles; y += 2) {
-      const int b = y % L::QS;
-      // every warp of the group has gathered its part of tile y, and did so after reading the
-      // scores of tile y - 2: the buffers of tile y + 2, which are that tile's, are free
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (y / L::QS) & 1));
-      if (!ok) break;
-      if (y + 2 < n_tiles) gather(y + 2);
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[b], (y / L::QS) & 1));
-      if (!ok) break;
-      tc::tc_fence_after();
-      const float2* lb = sL + b * BM;
-#pragma unroll 1
-      for (int c = 0; c < BM / 32; ++c) {
-        uint32_t sr[32];
-        tc::tmem_ld32_nowait(trow + b * BM + c * 32, sr);
-        tc::tmem_wait_ld();
-        float acc[2] = {0.f, 0.f};
+    int n = 0, sn = 0;
+    each([&](int64_t head, int s, int kt, bool two) -> bool {
+      const bool mine = grp == 0 || two;
+      const int key = (kt + grp) * BN + r;
+      float f = 0.f;
+      if (mine && key < p.c.capacity)
+        f = fmaxf(p.c.k_scale[head * (p.c.capacity >> p.lg) + (key >> p.lg)], kKv8MinScale) * p.scale_log2;
+      const uint64_t f2 = f2_pack(f, f);
+      float sum = 0.f;
+      TileWalk walk(p.tile_max + s * p.q_tiles, p.q_tiles, kt * BN, lane);
+      while (ok && walk.next() >= 0) {
+        const int b = n % L::QS;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (n / L::QS) & 1));
+        if (!ok) break;
+        if (mine) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[2 * grp + (sn & 1)], (sn >> 1) & 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          const float* lse = sL + b * 2 * BM;
+          const int* last = reinterpret_cast<const int*>(lse + BM);
+          // the tile's rows either all see this warp's last key, or each is compared
+          int lo = 0x7fffffff;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 v = lb[c * 32 + i];
-          const float e = tc::ex2_approx(fmaf(__uint_as_float(sr[i]), f, -v.x));
-          acc[i & 1] += key <= __float_as_int(v.y) ? e : 0.f;
+          for (int i = 0; i < BM / 32; ++i) {
+            const int v = last[i * 32 + lane];
+            lo = min(lo, lse[i * 32 + lane] == INFINITY ? 0x7fffffff : v);      // a row without a sum weighs 0 anyway
+          }
+          const bool full = __reduce_min_sync(0xffffffffu, lo) >= (kt + grp) * BN + quad * 32 + 31;
+          const uint32_t tS = trow + (sn & 1) * BM;
+#pragma unroll 1
+          for (int c = 0; c < BM / 64; ++c) {
+            uint32_t sr[64];
+            tc::tmem_ld32_nowait(tS + c * 64, sr);
+            tc::tmem_ld32_nowait(tS + c * 64 + 32, sr + 32);
+            tc::tmem_wait_ld();
+            uint64_t acc[2] = {0ull, 0ull};
+            if (full) {
+#pragma unroll
+              for (int i = 0; i < 64; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(lse + c * 64 + i);
+                const float2 z0 = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), f2, f2_pack(-v.x, -v.y)));
+                const float2 z1 = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), f2, f2_pack(-v.z, -v.w)));
+                acc[0] = f2_add(acc[0], f2_pack(tc::ex2_approx(z0.x), tc::ex2_approx(z0.y)));
+                acc[1] = f2_add(acc[1], f2_pack(tc::ex2_approx(z1.x), tc::ex2_approx(z1.y)));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; i += 2) {
+                const float2 v = *reinterpret_cast<const float2*>(lse + c * 64 + i);
+                const int2 t = *reinterpret_cast<const int2*>(last + c * 64 + i);
+                const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), f2, f2_pack(-v.x, -v.y)));
+                const float e0 = key <= t.x ? tc::ex2_approx(z.x) : 0.f, e1 = key <= t.y ? tc::ex2_approx(z.y) : 0.f;
+                acc[(i >> 1) & 1] = f2_add(acc[(i >> 1) & 1], f2_pack(e0, e1));
+              }
+            }
+            const float2 x = f2_unpack(f2_add(acc[0], acc[1]));
+            sum += x.x + x.y;
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s_empty[2 * grp + (sn & 1)]);
+          ++sn;
         }
-        sum += acc[0] + acc[1];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&q_empty[b]);
+        ++n;
       }
-      if (y + 2 < n_tiles) gathered(y + 2);
-    }
-    cp_async_wait_all();
+      if (ok && mine && key < p.c.capacity && sum != 0.f) p.weights[head * p.c.capacity + key] += sum;
+      return ok;
+    });
     if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
-    if (grp == 1) sx[r] = sum;
-    asm volatile("bar.sync 3, %0;" ::"n"(NSOFT * 32) : "memory");
-    if (grp == 0 && live) {
-      sum += sx[r];
-      float* w = p.weights + head * p.c.capacity + key;
-      if (sum != 0.f) *w += sum;
-    }
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -771,13 +910,12 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (e = prepare_tc<HD>(dev, &sms)) != cudaSuccess) return e;
   if ((e = launch_k(k_kv8_expand<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
-  const int q_tiles = (p.n_q + p.qpt - 1) / p.qpt;
   // one CTA per SM: the keys are split while that gives more of them work
-  const int64_t units = (int64_t)q_tiles * p.Hkv * p.c.n_seq;
+  const int64_t units = (int64_t)p.q_tiles * p.Hkv * p.c.n_seq;
   int ns = 1;
   while (ns < 8 && units * ns * 2 <= sms && 2 * ns <= p.tiles) ns *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.Hkv * ns, q_tiles, p.c.n_seq);
+  cfg.gridDim = dim3(p.Hkv * ns, p.q_tiles, p.c.n_seq);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = Layout<HD>::SMEM;
   cfg.stream = s;
@@ -792,7 +930,8 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
   if ((e = cudaLaunchKernelEx(&cfg, k_kv8_attn_tc<HD>, p, ns)) != cudaSuccess) return e;
   if (!p.weights) return cudaSuccess;
-  return launch_k(k_kv8_weights_tc<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(THREADS), WLayout<HD>::SMEM, s, p);
+  const int64_t items = (int64_t)p.c.n_seq * p.Hkv * ((p.tiles + 1) / 2);
+  return launch_k(k_kv8_weights_tc<HD>, dim3((unsigned)(items < sms ? items : sms)), dim3(THREADS), WLayout<HD>::SMEM, s, p);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -813,9 +952,26 @@ bool kv8_tc_taken(int dt, int hd, int G, int n_q) {
   return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > 64 && (n_q + BM / G - 1) / (BM / G) <= 65535;
 }
 
+namespace {
+struct WsOff {
+  size_t vx, seq_max, qx, rows, tile_max, bytes;
+};
+WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+  const size_t tile = (size_t)BN * hd * 2, kt = (size_t)n_seq * Hkv * ((cap + BN - 1) / BN);
+  const size_t qt = (n_q + BM / G - 1) / (BM / G), all = (size_t)n_seq * Hkv * qt;
+  WsOff w;
+  w.vx = align256(kt * tile);
+  w.seq_max = w.vx + align256(kt * tile);
+  w.qx = w.seq_max + align256((size_t)n_seq * 4);
+  w.rows = w.qx + (weights ? align256(all * tile) : 0);
+  w.tile_max = w.rows + (weights ? align256(all * 2 * BM * 4) : 0);
+  w.bytes = w.tile_max + (weights ? align256((size_t)n_seq * qt * 4) : 0);
+  return w;
+}
+}  // namespace
+
 size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
-  const size_t tiles = (size_t)n_seq * Hkv * ((cap + BN - 1) / BN) * BN * hd * 2;
-  return 2 * align256(tiles) + (weights ? align256((size_t)n_seq * Hkv * n_q * G * 4) : 0);
+  return ws_of(n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
 }
 
 cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
@@ -833,12 +989,17 @@ cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_
   p.tiles = (int)((c.capacity + BN - 1) / BN);
   p.qpt = BM / p.G;
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)hd);
-  const size_t tiles = (size_t)c.n_seq * Hkv * p.tiles * BN * hd * 2;
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  p.kx = w;
-  p.vx = w + align256(tiles);
+  p.q_tiles = (n_q + p.qpt - 1) / p.qpt;
+  p.g_magic = ((1 << 16) + p.G - 1) / p.G;
+  const WsOff w = ws_of(c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  p.kx = b;
+  p.vx = b + w.vx;
+  p.seq_max = reinterpret_cast<int32_t*>(b + w.seq_max);
   if (weights) {
-    p.lse = reinterpret_cast<float*>(w + 2 * align256(tiles));
+    p.qx = b + w.qx;
+    p.rows = reinterpret_cast<float*>(b + w.rows);
+    p.tile_max = reinterpret_cast<int32_t*>(b + w.tile_max);
     p.weights = weights;
   }
   return hd == 128 ? launch_hd<128>(p, s) : launch_hd<64>(p, s);
