@@ -47,7 +47,8 @@ constexpr int BM = 128;              // query rows per tile
 constexpr int BN = 128;              // keys per tile
 constexpr int SLAB = 128 * 128;      // bytes of one [128 rows x 64 elements] swizzled slab
 constexpr int NSOFT = 8;             // softmax warps: two groups of one per TMEM lane quarter
-constexpr int THREADS = 32 * (2 + NSOFT);
+constexpr int ATTN_THREADS = 32 * NSOFT;           // of the attention kernel
+constexpr int THREADS = 32 * (2 + NSOFT);          // of the weights kernel
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NG = BN / 16;          // scale groups of a key tile
 constexpr float kPBias = 8.0f;       // as in cb_kv8_attn.cu: weights up to 2^8, 2^14 before m is raised
@@ -189,19 +190,16 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 // ---- attention ------------------------------------------------------------------------------
 template <int HD>
 struct Layout {
-  static constexpr int NSLAB = HD / 64;
-  static constexpr int T_BYTES = NSLAB * SLAB;               // a tile of Q, K or V
-  static constexpr int STAGES = HD == 128 ? 5 : 10;          // ring K_0, V_0, K_1, V_1, ...
+  static constexpr int T_BYTES = HD / 64 * SLAB;             // a tile of Q, K or V
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_KV = T_BYTES;
-  static constexpr int OFF_X = OFF_KV + STAGES * T_BYTES;    // [2 groups][2][BM] row max, row sum
+  static constexpr int OFF_K = T_BYTES;                      // [2 groups]
+  static constexpr int OFF_V = OFF_K + 2 * T_BYTES;          // [2]
+  static constexpr int OFF_X = OFF_V + 2 * T_BYTES;          // [2 groups][2][BM] row max, row sum
   static constexpr int OFF_ML = OFF_X + 4 * BM * 4;          // [2][BM] the CTA's row max and sum, read by the cluster
   static constexpr int OFF_SC = OFF_ML + 2 * BM * 4;         // [NSOFT][NG] float4 {ks, log2 vs, 1/vs, -}
   static constexpr int OFF_BAR = OFF_SC + NSOFT * NG * 16;
-  static constexpr int BYTES = OFF_BAR + 256;
-  static constexpr int SMEM = BYTES + 1024;
-  static_assert((6 + 2 * STAGES) * 8 + 8 <= 256, "barriers exceed their region");
-  static_assert(BM * HD * 4 <= STAGES * T_BYTES, "the merge buffer exceeds the ring");
+  static constexpr int SMEM = OFF_BAR + 128 + 1024;
+  static_assert(BM * HD * 4 <= 4 * T_BYTES, "the merge buffer exceeds K and V");
   static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
 };
 constexpr uint32_t TM_O = 2 * BN;    // O_0 at column 256, O_1 right after it
@@ -221,158 +219,81 @@ __device__ __forceinline__ Scales load_scales(const float* ks, const float* vs, 
   return r;
 }
 
-// Pass 1 over a row's scores of one key tile: the largest t.  FULL: every row of the warp sees
-// every key (the common case, without a comparison per element).
-template <bool FULL>
-__device__ __forceinline__ float tile_max(uint32_t tS, int seen, const float4* sc) {
+// The largest t of a row's 128 scores.
+__device__ __forceinline__ float row_max(const uint32_t* sr, const float4* sc) {
   float mt = -INFINITY;
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    uint32_t sr[64];
-    tc::tmem_ld32_nowait(tS + hf * 64, sr);
-    tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
-    tc::tmem_wait_ld();
+  for (int gg = 0; gg < NG; ++gg) {
+    float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-    for (int gg = 0; gg < 4; ++gg) {
-      float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        float x[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          x[q] = __uint_as_float(sr[gg * 16 + i + q]);
-          if (!FULL && hf * 64 + gg * 16 + i + q > seen) x[q] = -INFINITY;
-        }
-        a = fmax3(a, x[0], x[1]);
-        b = fmax3(b, x[2], x[3]);
-      }
-      const float4 c = sc[hf * 4 + gg];
-      mt = fmaxf(mt, fmaf(fmaxf(a, b), c.x, c.y));
+    for (int i = 0; i < 16; i += 4) {
+      const uint32_t* x = sr + gg * 16 + i;
+      a = fmax3(a, __uint_as_float(x[0]), __uint_as_float(x[1]));
+      b = fmax3(b, __uint_as_float(x[2]), __uint_as_float(x[3]));
     }
+    const float4 c = sc[gg];
+    mt = fmaxf(mt, fmaf(fmaxf(a, b), c.x, c.y));
   }
   return mt;
 }
-// Pass 2: P = 2^(t - m + bias) over S as fp16 pairs (keys 2w, 2w + 1 to column w; the scores of
-// keys 0..63 are read before their columns are overwritten), and its sum with 1 / vs.
-template <bool FULL>
-__device__ __forceinline__ float tile_weights(uint32_t tS, int seen, const float4* sc, float off) {
+// P = 2^(t - m + bias) over S as fp16 pairs (keys 2w, 2w + 1 to column w), and its sum with
+// 1 / vs; an unseen score of -inf gives 0.
+__device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, const float4* sc, float off) {
   float l = 0.f;
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    uint32_t sr[64];
-    tc::tmem_ld32_nowait(tS + hf * 64, sr);
-    tc::tmem_ld32_nowait(tS + hf * 64 + 32, sr + 32);
-    tc::tmem_wait_ld();
+  for (int c = 0; c < NG / 2; ++c) {
+    uint32_t pk[16];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t pk[16];
+    for (int gg = 0; gg < 2; ++gg) {
+      const float4 k = sc[2 * c + gg];
+      const uint64_t f2 = f2_pack(k.x, k.x), a2 = f2_pack(k.y + off, k.y + off);
+      uint64_t sum = 0ull;
 #pragma unroll
-      for (int gg = 0; gg < 2; ++gg) {
-        const float4 k = sc[hf * 4 + c * 2 + gg];
-        const uint64_t f2 = f2_pack(k.x, k.x), a2 = f2_pack(k.y + off, k.y + off);
-        uint64_t sum = 0ull;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-          const int k0 = c * 32 + gg * 16 + 2 * w;
-          const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, a2));
-          float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
-          if (!FULL) {
-            p0 = hf * 64 + k0 <= seen ? p0 : 0.f;
-            p1 = hf * 64 + k0 + 1 <= seen ? p1 : 0.f;
-          }
-          sum = f2_add(sum, f2_pack(p0, p1));
-          const __half2 h2 = __floats2half2_rn(p0, p1);
-          pk[gg * 8 + w] = *reinterpret_cast<const uint32_t*>(&h2);
-        }
-        const float2 sm = f2_unpack(sum);
-        l = fmaf(sm.x + sm.y, k.z, l);
+      for (int w = 0; w < 8; ++w) {
+        const int k0 = c * 32 + gg * 16 + 2 * w;
+        const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, a2));
+        const float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
+        sum = f2_add(sum, f2_pack(p0, p1));
+        const __half2 h2 = __floats2half2_rn(p0, p1);
+        pk[gg * 8 + w] = *reinterpret_cast<const uint32_t*>(&h2);
       }
-      tc::tmem_st16u_nowait(tS + hf * 32 + c * 16, pk);
+      const float2 sm = f2_unpack(sum);
+      l = fmaf(sm.x + sm.y, k.z, l);
     }
+    tc::tmem_st16u_nowait(tS + c * 16, pk);
   }
   return l;
 }
 
-// One key tile of a softmax group; a thread owns one row of S_g and O_g in TMEM.  seen: the
-// last key of the tile that the row sees (may be negative or beyond it).  sc: the tile's scale
-// groups in the warp's own shared memory.
+// Two groups of four warps take alternate key tiles (TMEM: S_0 | S_1 | O_0 | O_1), merged at
+// the end; a cluster's CTAs take consecutive runs of key tiles.  A group is a closed loop: its
+// first warp issues its copies and products between its share of the softmax, so a tile's chain
+// is S -> softmax -> P V -> S of the next tile with one hand-over each way, the other group
+// fills the gaps, and the eight warps (two per scheduler) may hold a row's 128 scores in
+// registers and read them once.  K's buffer is refilled as soon as S is there, V's once P V is
+// done: each load has most of a tile's chain to arrive, so one buffer per group suffices.
+// Measured (3328 rows of 56 heads over 16384 rows of 8, 973 GFLOP): with a copying and an
+// issuing warp, a ring of five tiles and the scores read twice for want of registers, 1045 us.
 template <int HD>
-__device__ __forceinline__ bool softmax_tile(uint64_t* s_full_g, uint64_t* p_full_g, uint64_t* pv_done_g, uint32_t u,
-                                             int seen, uint32_t tS, uint32_t tO, const float4* sc, float& m_used,
-                                             float& l, int lane) {
-  if (!__all_sync(0xffffffffu, tc::mbar_wait(s_full_g, u & 1))) return false;
-  const bool none = __all_sync(0xffffffffu, seen < 0), full = __all_sync(0xffffffffu, seen >= BN - 1);
-  float mt = -INFINITY;
-  tc::tc_fence_after();
-  if (full)
-    mt = tile_max<true>(tS, seen, sc);
-  else if (!none)
-    mt = tile_max<false>(tS, seen, sc);
-  if (u == 0) {
-    m_used = mt;               // O_g is written, not added to, by this tile's P.V
-  } else {
-    const bool need = mt > m_used + kLazy;
-    if (__any_sync(0xffffffffu, need)) {
-      // O_g must be stable: the group's previous P.V has completed
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(pv_done_g, (u - 1) & 1))) return false;
-      tc::tc_fence_after();
-      const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
-#pragma unroll 1
-      for (int c = 0; c < HD / 16; ++c) {
-        float o[16];
-        tc::tmem_ld16(tO + c * 16, o);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] *= alpha;
-        tc::tmem_st16(tO + c * 16, o);
-      }
-      l *= alpha;
-      if (need) m_used = mt;
-    }
-  }
-  const float off = kPBias - (m_used == -INFINITY ? 0.f : m_used);
-  if (full) {
-    l += tile_weights<true>(tS, seen, sc, off);
-  } else if (!none) {
-    l += tile_weights<false>(tS, seen, sc, off);
-  } else {
-    uint32_t pk[16];
-#pragma unroll
-    for (int w = 0; w < 16; ++w) pk[w] = 0u;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tc::tmem_st16u_nowait(tS + c * 16, pk);
-  }
-  tc::tmem_wait_st();
-  tc::tc_fence_before();
-  __syncwarp();
-  if (lane == 0) tc::mbar_arrive(p_full_g);
-  return true;
-}
-
-// Two softmax groups take alternate key tiles (TMEM: S_0 | S_1 | O_0 | O_1), merged at the
-// end; a cluster's CTAs take consecutive runs of key tiles.  Warp roles: 0 = copies, 1 = TMEM
-// allocation and MMA issue, 2..9 = softmax; all gather Q first.
-template <int HD>
-__global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n_split) {
+__global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n_split) {
   pdl_wait();
   pdl_trigger();
   using L = Layout<HD>;
-  constexpr int NST = L::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sQ = base + L::OFF_Q;
-  uint8_t* sKV = base + L::OFF_KV;
   float* xm = reinterpret_cast<float*>(base + L::OFF_X);   // [2][BM] row max, then [2][BM] row sum
   float* xl = xm + 2 * BM;
   float* cm = reinterpret_cast<float*>(base + L::OFF_ML);  // [BM] max, [BM] sum
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
-  uint64_t* s_full = bars;         // [2] per group: S_g holds a tile's scores
-  uint64_t* p_full = bars + 2;     // [2] the group's four warps wrote P
-  uint64_t* pv_done = bars + 4;    // [2] P V into O_g completed
-  uint64_t* kv_full = bars + 6;    // [NST]
-  uint64_t* kv_empty = kv_full + NST;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + NST);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+  uint64_t* k_full = bars + 4 * grp;       // a group's barriers: K and V have landed, S and P V are done
+  uint64_t* v_full = k_full + 1;
+  uint64_t* s_full = k_full + 2;
+  uint64_t* pv_done = k_full + 3;
   const int rank = blockIdx.x % n_split, h = blockIdx.x / n_split, s = blockIdx.z;
   // tiles are cut from the end of the queries: the longest rows come first, and the tile that
   // is cut short is the one with the lowest positions
@@ -380,25 +301,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
   const int64_t head = (int64_t)s * p.Hkv + h;
 
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&s_full[i], 1);
-      tc::mbar_init(&p_full[i], 4);
-      tc::mbar_init(&pv_done[i], 1);
-    }
-    for (int i = 0; i < NST; ++i) {
-      tc::mbar_init(&kv_full[i], 1);
-      tc::mbar_init(&kv_empty[i], 1);
-    }
+    for (int i = 0; i < 8; ++i) tc::mbar_init(&bars[i], 1);
     tc::fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 0) {
     tc::tmem_alloc(tmem_slot, TMEM_COLS);
     tc::tmem_relinquish();
   }
-  gather_q<HD>(p, s, h, j0, sQ, tid, THREADS);
+  gather_q<HD>(p, s, h, j0, sQ, tid, ATTN_THREADS);
   // keys that some row of the tile sees
   int mx = -1;
-  for (int i = tid; i < p.qpt; i += THREADS) {
+  for (int i = tid; i < p.qpt; i += ATTN_THREADS) {
     const int j = j0 + i;
     if (j >= 0) {
       const int l = p.last[(int64_t)s * p.n_q + j];
@@ -416,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 #pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) mx = max(mx, wm[w]);
+  for (int w = 0; w < ATTN_THREADS / 32; ++w) mx = max(mx, wm[w]);
   __syncthreads();                 // wm's memory is the groups' row maxima later on
   // for the weights: the tile's queries as they sit in shared memory, and its bound
   const int64_t qt = head * p.q_tiles + blockIdx.y;
@@ -430,108 +343,143 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
   const int64_t nk = (int64_t)mx + 1;
   const int all = (mx + BN) / BN;  // key tiles; 0 if no row sees a key
   const int ta = (int)((int64_t)all * rank / n_split), T = (int)((int64_t)all * (rank + 1) / n_split) - ta;
+  const int nt = T > grp ? (T - grp + 1) / 2 : 0;     // this group's: ta + grp, ta + grp + 2, ...
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ copies
-    if (lane == 0) {
-      const uint8_t* kx = p.kx + (head * p.tiles + ta) * (int64_t)L::T_BYTES;
-      const uint8_t* vx = p.vx + (head * p.tiles + ta) * (int64_t)L::T_BYTES;
-      int i = 0;
-      for (; i < 2 * T; ++i) {
-        const int st = i % NST;
-        if (!tc::mbar_wait(&kv_empty[st], ((i / NST) & 1) ^ 1)) {
-          atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
-          break;
-        }
-        tc::mbar_expect_tx(&kv_full[st], L::T_BYTES);
-        tc::bulk_load(sKV + st * L::T_BYTES, ((i & 1) ? vx : kx) + (int64_t)(i >> 1) * L::T_BYTES, L::T_BYTES, &kv_full[st]);
-      }
-      // no copy is in flight when the CTA ends, whoever gave up on what
-      for (int k = i > NST ? i - NST : 0; k < i; ++k) tc::mbar_wait(&kv_full[k % NST], (k / NST) & 1);
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issue
-    constexpr uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN);
-    constexpr uint32_t idesc_o = tc::idesc_f16_f32(BM, HD, true);
-    const uint64_t kv_desc = tc::desc_sw128(tc::smem_u32(sKV));
-    const uint64_t v_desc = tc::desc_sw128_mn(tc::smem_u32(sKV), SLAB);
-    const uint64_t q_desc = tc::desc_sw128(tc::smem_u32(sQ));
-    bool ok = true;
-    auto issue_s = [&](int jj) {
-      const int b = jj & 1, i = 2 * jj, st = i % NST;
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&kv_full[st], (i / NST) & 1) &&
-                                             (jj < 2 || tc::mbar_wait(&pv_done[b], ((jj - 2) >> 1) & 1)));
-      if (!ok) return;
+  const Row x = row_of(p, j0, r);
+  const int last = x.on ? last_of(p, s, x.j) : -1;
+  const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+  const uint32_t tS = trow + grp * BN, tO = trow + TM_O + grp * HD;
+  bool ok = true;                  // of this warp; one that gave up goes on meeting its group
+  {
+    const bool issuer = quad == 0;
+    const uint8_t* kx = p.kx + (head * p.tiles + ta + grp) * (int64_t)L::T_BYTES;
+    const uint8_t* vx = p.vx + (head * p.tiles + ta + grp) * (int64_t)L::T_BYTES;
+    uint8_t* sK = base + L::OFF_K + grp * L::T_BYTES;
+    uint8_t* sV = base + L::OFF_V + grp * L::T_BYTES;
+    int nk_loads = 0, nv_loads = 0;
+    auto load_k = [&](int u) {
+      ++nk_loads;
+      if (lane != 0) return;
+      tc::mbar_expect_tx(k_full, L::T_BYTES);
+      tc::bulk_load(sK, kx + (int64_t)(2 * u) * L::T_BYTES, L::T_BYTES, k_full);
+    };
+    auto load_v = [&](int u) {
+      ++nv_loads;
+      if (lane != 0) return;
+      tc::mbar_expect_tx(v_full, L::T_BYTES);
+      tc::bulk_load(sV, vx + (int64_t)(2 * u) * L::T_BYTES, L::T_BYTES, v_full);
+    };
+    auto issue_s = [&]() {
+      constexpr uint32_t idesc = tc::idesc_bf16_f32(BM, BN);
+      const uint64_t qd = tc::desc_sw128(tc::smem_u32(sQ)), kd = tc::desc_sw128(tc::smem_u32(sK));
       tc::tc_fence_after();
       if (tc::elect_one()) {
-        const uint64_t kd = kv_desc + (uint64_t)((st * L::T_BYTES) >> 4);
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
           const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + b * BN, q_desc + off, kd + off, idesc_s, k > 0);
+          tc::mma_bf16(tmem + grp * BN, qd + off, kd + off, idesc, k > 0);
         }
-        tc::mma_commit(&s_full[b]);
-        tc::mma_commit(&kv_empty[st]);
+        tc::mma_commit(s_full);
       }
       __syncwarp();
     };
-    auto issue_pv = [&](int jj) {
-      const int b = jj & 1, i = 2 * jj + 1, st = i % NST;
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&p_full[b], (jj >> 1) & 1) &&
-                                             tc::mbar_wait(&kv_full[st], (i / NST) & 1));
-      if (!ok) return;
+    auto issue_pv = [&](bool add) {
+      constexpr uint32_t idesc = tc::idesc_f16_f32(BM, HD, true);
+      const uint64_t vd = tc::desc_sw128_mn(tc::smem_u32(sV), SLAB);
       tc::tc_fence_after();
       if (tc::elect_one()) {
-        const uint64_t vd = v_desc + (uint64_t)((st * L::T_BYTES) >> 4);
 #pragma unroll
         for (int k = 0; k < BN / 16; ++k)
-          tc::mma_bf16_ts(tmem + TM_O + b * HD, tmem + b * BN + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc_o,
-                          (jj >= 2 || k > 0) ? 1u : 0u);
-        tc::mma_commit(&pv_done[b]);
-        tc::mma_commit(&kv_empty[st]);
+          tc::mma_bf16_ts(tmem + TM_O + grp * HD, tmem + grp * BN + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc,
+                          (add || k > 0) ? 1u : 0u);
+        tc::mma_commit(pv_done);
       }
       __syncwarp();
     };
-    if (T > 0) issue_s(0);
-    if (T > 1) issue_s(1);
-    for (int jj = 0; ok && jj < T; ++jj) {
-      issue_pv(jj);
-      if (jj + 2 < T) issue_s(jj + 2);
-    }
-    if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
-  } else {
-    // ------------------------------------------------------------------ softmax
-    const int grp = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const Row x = row_of(p, j0, r);
-    const int last = x.on ? last_of(p, s, x.j) : -1;
-    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     const int64_t nblk = p.c.capacity >> p.lg;
     const float* ks = p.c.k_scale + head * nblk;
     const float* vs = p.c.v_scale + head * nblk;
-    float4* sc = reinterpret_cast<float4*>(base + L::OFF_SC) + (warp - 2) * NG;
+    float4* sc = reinterpret_cast<float4*>(base + L::OFF_SC) + warp * NG;
     float m_used = -INFINITY, l = 0.f;
-    bool ok = true;
-    int u = 0;
+    if (issuer && nt > 0) {
+      load_k(0);
+      load_v(0);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(k_full, 0));
+      if (ok) issue_s();
+    }
     Scales nx = load_scales(ks, vs, p.lg, ta + grp, nk, lane);
-    for (int j = grp; j < T; j += 2, ++u) {
-      if (!ok) break;
+#pragma unroll 1
+    for (int u = 0; u < nt; ++u) {
+      const int tile = ta + grp + 2 * u;
       __syncwarp();
       if (lane < NG) {
         const float v = fmaxf(nx.v, kKv8MinScale);
         sc[lane] = make_float4(fmaxf(nx.k, kKv8MinScale) * p.scale_log2, log2f(v), 1.0f / v, 0.f);
       }
-      nx = load_scales(ks, vs, p.lg, ta + j + 2, nk, lane);
+      nx = load_scales(ks, vs, p.lg, tile + 2, nk, lane);
       __syncwarp();
-      ok = softmax_tile<HD>(&s_full[grp], &p_full[grp], &pv_done[grp], (uint32_t)u, last - (ta + j) * BN, trow + grp * BN,
-                            trow + TM_O + grp * HD, sc, m_used, l, lane);
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
+      if (ok) {
+        if (issuer && u + 1 < nt) load_k(u + 1);
+        uint32_t sr[BN];
+        tc::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
+        tc::tmem_wait_ld();
+        const int seen = last - tile * BN;     // the last key of the tile that the row sees
+        if (__any_sync(0xffffffffu, seen < BN - 1)) {      // most tiles are seen whole by all rows of the warp
+#pragma unroll
+          for (int i = 0; i < BN; ++i)
+            if (i > seen) sr[i] = 0xff800000u;
+        }
+        const float mt = row_max(sr, sc);
+        if (u == 0) {
+          m_used = mt;             // O_g is written, not added to, by this tile's P V
+        } else {
+          const bool need = mt > m_used + kLazy;
+          if (__any_sync(0xffffffffu, need)) {             // (S was issued after the last P V had completed)
+            const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              float o[16];
+              tc::tmem_ld16(tO + c * 16, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= alpha;
+              tc::tmem_st16(tO + c * 16, o);
+            }
+            l *= alpha;
+            if (need) m_used = mt;
+          }
+        }
+        l += row_weights(sr, tS, sc, kPBias - (m_used == -INFINITY ? 0.f : m_used));
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
+      if (issuer) {
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(v_full, u & 1));
+        if (ok) issue_pv(u > 0);
+        if (u + 1 < nt) {
+          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(k_full, (u + 1) & 1) && tc::mbar_wait(pv_done, u & 1));
+          if (ok) {
+            issue_s();
+            load_v(u + 1);
+          }
+        }
+      }
     }
-    // the group's last P.V, then both groups' row statistics meet in shared memory
-    const bool done = ok && (u == 0 || __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[grp], (u - 1) & 1)));
-    if (!done && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+    ok = ok && (nt == 0 || __all_sync(0xffffffffu, tc::mbar_wait(pv_done, (nt - 1) & 1)));
+    if (!ok) {
+      // report, and give the copies in flight as long again before the memory is given up
+      if (lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
+      if (nk_loads > 0) tc::mbar_wait(k_full, (nk_loads - 1) & 1);
+      if (nv_loads > 0) tc::mbar_wait(v_full, (nv_loads - 1) & 1);
+    }
+    // both groups' row statistics meet in shared memory
     xm[grp * BM + r] = m_used;
     xl[grp * BM + r] = l;
     tc::tc_fence_before();
-    asm volatile("bar.sync 1, %0;" ::"n"(NSOFT * 32) : "memory");
+    __syncthreads();
     tc::tc_fence_after();
     const float ma = xm[r], mb = xm[BM + r], mm = fmaxf(ma, mb);
     const float a0 = ma == -INFINITY ? 0.f : tc::ex2_approx(ma - mm);
@@ -549,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
     }
     // group g finalises columns [g HD/2, (g + 1) HD/2); O_g was never written with fewer than
     // g + 1 key tiles
-    float* om = reinterpret_cast<float*>(sKV) + r * HD;
+    float* om = reinterpret_cast<float*>(base + L::OFF_K) + r * HD;
     bf16* orow = p.out + (((int64_t)s * p.n_q + (x.on ? x.j : 0)) * p.H + (int64_t)h * p.G + (x.on ? x.g : 0)) * HD;
 #pragma unroll 1
     for (int c = 0; c < HD / 32; ++c) {
@@ -588,10 +536,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
   if (n_split > 1) {
     // ------------------------------------------------------------------ merge of the cluster
     tc::cluster_sync();
-    const uint32_t cm_a = tc::smem_u32(cm), om_a = tc::smem_u32(sKV);
+    const uint32_t cm_a = tc::smem_u32(cm), om_a = tc::smem_u32(base + L::OFF_K);
     const int per = BM / n_split, r0 = rank * per;        // this CTA's share of the rows
     constexpr int W4 = HD / 4;
-    for (int i = tid; i < per * W4; i += THREADS) {
+    for (int i = tid; i < per * W4; i += ATTN_THREADS) {
       const int r = r0 + i / W4, w = i % W4;
       const Row x = row_of(p, j0, r);
       float M = -INFINITY, sum = 0.f;
@@ -617,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
     tc::cluster_sync();            // the peers may still be reading this CTA's part
   }
   if (p.weights && rank == 0 && tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  if (warp == 1) {
+  if (warp == 0) {
     __syncwarp();
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, TMEM_COLS);
@@ -629,7 +577,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n
 // thread.  A resident CTA takes pairs of key tiles (of one KV head and sequence), one per
 // softmax group, and streams the query tiles that see them past both: a query tile is loaded
 // once for 256 keys, each group has two S buffers (TMEM 4 x 128 columns), and no sums have to
-// meet.  Warp roles as in the attention kernel.
+// meet.  Warp roles: 0 = copies,
+// 1 = TMEM allocation and MMA issue, 2..9 = softmax.
 // Measured: 64 queries of 7 heads over 16384 rows of 8 KV heads, one CTA per key tile gathering
 // the queries itself 55 us (15 instructions per weight, and the start of 1024 CTAs).
 template <int HD>
@@ -916,7 +865,7 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   while (ns < 8 && units * ns * 2 <= sms && 2 * ns <= p.tiles) ns *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.Hkv * ns, p.q_tiles, p.c.n_seq);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(ATTN_THREADS);
   cfg.dynamicSmemBytes = Layout<HD>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
