@@ -94,6 +94,19 @@ __device__ __forceinline__ uint32_t pair_bf16(uint32_t w, uint32_t sel) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// 32 bytes, the two halves exchanged if asked
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool swap) {
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = swap ? w[4 + i] : w[i];
+    b[i] = swap ? w[i] : w[4 + i];
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]),
+               "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
+               : "memory");
+}
+
 // One CTA per (key tile, KV head, sequence): 128 rows of K and V codes to bf16 / fp16 in
 // 128-byte-swizzled slabs.  Tiles no query sees are skipped.
 template <int HD>
@@ -140,18 +153,20 @@ __global__ void __launch_bounds__(256) k_kv8_expand(const Kv8Tc p) {
   for (int i = 0; i < N; ++i) {
     const int idx = i * 256 + threadIdx.x, row = idx / PER, piece = idx % PER;
     const uint32_t kw[4] = {k[i].x, k[i].y, k[i].z, k[i].w}, vw[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint8_t* kd = p.kx + dst + (piece >> 2) * SLAB + row * 128;
-    uint8_t* vd = p.vx + dst + (piece >> 2) * SLAB + row * 128;
+    // 16 codes are two neighbouring 16-byte chunks of the row, which the swizzle keeps in one
+    // 32-byte sector (odd rows in exchanged order): one store each
+    const int64_t at = dst + (piece >> 2) * SLAB + row * 128 + (((2 * (piece & 3)) ^ (row & 6)) * 16);
+    uint32_t ko[8], vo[8];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int at = ((2 * (piece & 3) + c) ^ (row & 7)) * 16;
-      const uint32_t u0 = vw[2 * c] ^ 0x80808080u, u1 = vw[2 * c + 1] ^ 0x80808080u;
-      *reinterpret_cast<uint4*>(kd + at) =
-          make_uint4(pair_bf16(kw[2 * c], 0x4140), pair_bf16(kw[2 * c], 0x4342), pair_bf16(kw[2 * c + 1], 0x4140),
-                     pair_bf16(kw[2 * c + 1], 0x4342));
-      *reinterpret_cast<uint4*>(vd + at) =
-          make_uint4(pair_f16(u0, 0x4140), pair_f16(u0, 0x4342), pair_f16(u1, 0x4140), pair_f16(u1, 0x4342));
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t u = vw[c] ^ 0x80808080u;
+      ko[2 * c] = pair_bf16(kw[c], 0x4140);
+      ko[2 * c + 1] = pair_bf16(kw[c], 0x4342);
+      vo[2 * c] = pair_f16(u, 0x4140);
+      vo[2 * c + 1] = pair_f16(u, 0x4342);
     }
+    store32(p.kx + at, ko, row & 1);
+    store32(p.vx + at, vo, row & 1);
   }
 }
 
@@ -414,7 +429,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
       __syncwarp();
       if (lane < NG) {
         const float v = fmaxf(nx.v, kKv8MinScale);
-        sc[lane] = make_float4(fmaxf(nx.k, kKv8MinScale) * p.scale_log2, log2f(v), 1.0f / v, 0.f);
+        // (approximate log and reciprocal: off by 2^-22 of a value beside P's own 2^-12; the exact
+        // forms cost 40 of 850 us at the Yi shape, by the few lanes that compute them)
+        sc[lane] = make_float4(fmaxf(nx.k, kKv8MinScale) * p.scale_log2, __log2f(v), __fdividef(1.0f, v), 0.f);
       }
       nx = load_scales(ks, vs, p.lg, tile + 2, nk, lane);
       __syncwarp();
@@ -425,7 +442,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
         tc::tc_fence_after();
 #pragma unroll
         for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
-        tc::tmem_wait_ld();
+        tc::tmem_wait_ld64(sr);
+        tc::tmem_wait_ld64(sr + 64);
         const int seen = last - tile * BN;     // the last key of the tile that the row sees
         if (__any_sync(0xffffffffu, seen < BN - 1)) {      // most tiles are seen whole by all rows of the warp
 #pragma unroll
@@ -778,7 +796,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
             uint32_t sr[64];
             tc::tmem_ld32_nowait(tS + c * 64, sr);
             tc::tmem_ld32_nowait(tS + c * 64 + 32, sr + 32);
-            tc::tmem_wait_ld();
+            tc::tmem_wait_ld64(sr);
             uint64_t acc[2] = {0ull, 0ull};
             if (full) {
 #pragma unroll
