@@ -27,8 +27,8 @@ cudaError_t launch_kv8_read(int dt, const cb_kv8_cache& c, const int32_t* start,
 cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const float* weights, int n_keep, int n_sink,
                               int n_recent, int64_t dcap, int32_t* dst_len, float* dst_weights, int32_t* kept, int Hkv,
                               cudaStream_t s);
-cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, const int32_t* dst_len, int n_keep,
-                            const int32_t* kept, int Hkv, int hd, cudaStream_t s);
+cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, int n_keep, const int32_t* kept, int Hkv,
+                            int hd, cudaStream_t s);
 bool kv8_attn_supported(int hd);
 size_t kv8_attn_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
 bool kv8_attn_weights_apart(int dt, int hd, int G, int n_q);
@@ -1320,7 +1320,7 @@ int cb_kv8_evict(const cb_kv8_cache* src, const int32_t* len, const float* weigh
             S(stream), launch_kv8_select(*src, len, weights, n_keep, n_sink, n_recent, dst->capacity, dst_len,
                                          dst_weights, kept, Hkv, S(stream)));
   CB_LAUNCH(CB_PROF_KV8_EVICT, 1, heads, n_keep, hd, 0.0, 4.0 * heads * n_keep * hd, S(stream),
-            launch_kv8_move(*src, *dst, dst_len, n_keep, kept, Hkv, hd, S(stream)));
+            launch_kv8_move(*src, *dst, n_keep, kept, Hkv, hd, S(stream)));
   return CB_OK;
 }
 
@@ -1381,7 +1381,6 @@ void cb_shutdown(void) {
   reset_mem_caches();
   reset_gemm_tc_caches();
   reset_attn_tc_caches();
-  reset_kv8_caches();
   reset_kv8_attn_caches();
   reset_kv8_tc_caches();
   reset_logits_caches();

@@ -7,8 +7,6 @@
 // rows be appended one at a time and lets attention apply it to a score or a probability: the
 // codes themselves enter the matrix instructions, exactly.  The layout is head-major, so a
 // head's block is one contiguous run of block * head_dim bytes.
-#include <mutex>
-
 #include "cb_kv8.cuh"
 
 namespace cb {
@@ -63,13 +61,10 @@ struct Chunk<bf16> {
     const uint32_t u = *reinterpret_cast<const uint32_t*>(&m) & 0x7fff7fffu;
     return max(u << 16, u & 0xffff0000u);
   }
-  __device__ __forceinline__ void values(float* f) const {
+  __device__ __forceinline__ void values(uint64_t* f) const {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 8; ++i) f[i] = tc::f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
 };
 template <>
@@ -86,34 +81,34 @@ struct Chunk<float> {
       m = max(max(max(m, w[i].x & 0x7fffffffu), max(w[i].y & 0x7fffffffu, w[i].z & 0x7fffffffu)), w[i].w & 0x7fffffffu);
     return m;
   }
-  __device__ __forceinline__ void values(float* f) const {
+  __device__ __forceinline__ void values(uint64_t* f) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      f[4 * i] = __uint_as_float(w[i].x);
-      f[4 * i + 1] = __uint_as_float(w[i].y);
-      f[4 * i + 2] = __uint_as_float(w[i].z);
-      f[4 * i + 3] = __uint_as_float(w[i].w);
+      f[2 * i] = tc::f2_pack(__uint_as_float(w[i].x), __uint_as_float(w[i].y));
+      f[2 * i + 1] = tc::f2_pack(__uint_as_float(w[i].z), __uint_as_float(w[i].w));
     }
   }
 };
 // not finite: 0
-__device__ __forceinline__ void zero_bad(float* f) {
+__device__ __forceinline__ void zero_bad(uint64_t* f) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (!isfinite(f[i])) f[i] = 0.f;
+  for (int i = 0; i < 8; ++i) {
+    const float2 v = tc::f2_unpack(f[i]);
+    f[i] = tc::f2_pack(isfinite(v.x) ? v.x : 0.f, isfinite(v.y) ? v.y : 0.f);
+  }
 }
 
 // One CTA per (touched block, K or V, head, sequence); a thread owns NCH chunks of 16 channels
 // of one row, held in registers between the maximum and the coding, so every new element is
 // read once.
 template <typename T, int NCH>
-__global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, const T* __restrict__ v, int n_rows,
+__global__ void __launch_bounds__(512) k_kv8_append(const T* __restrict__ k, const T* __restrict__ v, int n_rows,
                                                      const int32_t* __restrict__ start,
                                                      const int32_t* __restrict__ count, const cb_kv8_cache c, int lg,
-                                                     int Hkv, int hd) {
+                                                     int Hkv, int hd, uint32_t row_magic) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float sh[32];
+  __shared__ uint32_t sh[32];
   const int s = blockIdx.z, h = blockIdx.y, t = blockIdx.x >> 1;
   const bool is_v = blockIdx.x & 1;
   int64_t a, e;
@@ -127,10 +122,9 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
   int8_t* codes = (is_v ? c.v_codes : c.k_codes) + (head * c.capacity + r0) * hd;
   float* scale = (is_v ? c.v_scale : c.k_scale) + head * (c.capacity >> lg) + b;
   const float old = lo > 0 ? *scale : 0.f;
-  const int per_row = hd >> 4;
   const T* src = (is_v ? v : k) + (((int64_t)s * n_rows + (r0 - a)) * Hkv + h) * hd;
   // a thread's chunks lie whole rows apart
-  const int row0 = threadIdx.x / per_row, col = (threadIdx.x - row0 * per_row) << 4, step = block / NCH;
+  const int row0 = threadIdx.x * row_magic >> 16, col = (threadIdx.x << 4) - row0 * hd, step = block / NCH;
   Chunk<T> x[NCH];
   uint32_t top = 0;
   bool bad = false;
@@ -146,19 +140,21 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
       uint32_t m = x[i].amax_bits();
       if (m >= 0x7f800000u) {
         bad = true;
-        float f[16];
+        uint64_t f[8];
         x[i].values(f);
         zero_bad(f);
-        float a = 0.f;
+        m = 0;
 #pragma unroll
-        for (int q = 0; q < 16; ++q) a = fmaxf(a, fabsf(f[q]));
-        m = __float_as_uint(a);
+        for (int q = 0; q < 8; ++q) {
+          const float2 z = tc::f2_unpack(f[q]);
+          m = max(max(m, __float_as_uint(z.x) & 0x7fffffffu), __float_as_uint(z.y) & 0x7fffffffu);
+        }
       }
       top = max(top, m);
     }
   }
   if (bad) atomicOr(&g_err_kv8, ERRBIT_NONFINITE);
-  const float amax = kv8_block_max(__uint_as_float(top), sh);
+  const float amax = kv8_block_max(top, sh);
   const float sc = fmaxf(fmaxf(__fdiv_rn(amax, 127.0f), kKv8MinScale), old);
   const float inv = 1.0f / sc;
   const bool grow = sc > old;
@@ -167,18 +163,14 @@ __global__ void __launch_bounds__(1024) k_kv8_append(const T* __restrict__ k, co
     const int row = row0 + i * step;
     uint4* dst = reinterpret_cast<uint4*>(codes + row * hd + col);
     if (row >= lo && row < hi) {
-      float f[16];
+      uint64_t f[8];
       x[i].values(f);
       if (bad) zero_bad(f);
-      *dst = kv8_code16(f, sc, inv);
+      *dst = kv8_code16(f, inv, [&](float z, uint32_t q) { return kv8_code(z, sc, q); });
     } else if (row < lo && grow) {
-      float g[16];
-      uint32_t q[16];
+      uint64_t g[8];
       kv8_unpack16(*dst, g);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) q[c] = (uint32_t)(int)kv8_recode(g[c], old, sc, inv);
-      *dst = make_uint4(kv8_pack4(q[0], q[1], q[2], q[3]), kv8_pack4(q[4], q[5], q[6], q[7]),
-                        kv8_pack4(q[8], q[9], q[10], q[11]), kv8_pack4(q[12], q[13], q[14], q[15]));
+      *dst = kv8_code16(g, old * inv, [&](float z, uint32_t q) { return kv8_recode(z, old, sc, q); });
     }
   }
   if (threadIdx.x == 0 && grow) *scale = sc;
@@ -228,10 +220,15 @@ __global__ void __launch_bounds__(256) k_kv8_read(const cb_kv8_cache c, int lg, 
 #pragma unroll
   for (int i = 0; i < kReadUnroll; ++i)
     if (i * per < left) {
+      uint64_t g[8];
       float f[16];
-      kv8_unpack16(u[i], f);
+      kv8_unpack16(u[i], g);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) f[q] = __fmul_rn(f[q], sc[i]);
+      for (int q = 0; q < 8; ++q) {
+        const float2 z = tc::f2_unpack(g[q]);
+        f[2 * q] = __fmul_rn(z.x, sc[i]);
+        f[2 * q + 1] = __fmul_rn(z.y, sc[i]);
+      }
       T* o = out + (int64_t)i * per * Hkv * hd;
       put8(o, f, al32);
       put8(o + 8, f + 8, al32);
@@ -240,31 +237,31 @@ __global__ void __launch_bounds__(256) k_kv8_read(const cb_kv8_cache c, int lg, 
 
 // ---- eviction ---------------------------------------------------------------------------
 // A weight is a sum of probabilities (>= 0), so its bit pattern orders it; NaN and negative
-// values rank as 0.
-__device__ __forceinline__ uint32_t weight_key(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
+// values rank as 0.  One is added: 0 stands for a row that is not there.
+__device__ __forceinline__ uint32_t weight_key(float w) { return (w > 0.f ? __float_as_uint(w) : 0u) + 1u; }
 
 constexpr int kEvictThreads = 1024;
-constexpr int kEvictSmemKeys = 49152;    // keys staged in shared memory up to this many (192 KB)
 constexpr int kEvictBins = 2048;         // 11-bit digits: three passes over the 32 key bits
 
 // One CTA per (head, sequence): radix select of the k heaviest rows of [lo, hi), ties to the
-// lower row, then an ordered compaction: warp w owns a contiguous run of rows and ranks them
-// by ballots, so no lane strides through shared memory.
-template <bool SMEM>
+// lower row, then an ordered compaction.  Warp w owns a contiguous run of rows and ranks them
+// by ballots.  A thread holds its KPT keys in registers over all passes; with KPT = 0 (more
+// rows than 32 per thread) each pass reads the weights again, from L2.
+template <int KPT>
 __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __restrict__ weights,
                                                               const int32_t* __restrict__ len, int64_t cap, int n_keep,
                                                               int n_sink, int n_recent, int64_t dcap,
                                                               int32_t* __restrict__ dst_len,
                                                               float* __restrict__ dst_weights,
                                                               int32_t* __restrict__ kept) {
-  pdl_wait();
-  pdl_trigger();
-  extern __shared__ uint32_t skey[];
-  __shared__ int hist[kEvictBins];
+  __shared__ int hist[3][kEvictBins];
   __shared__ int s_gt[32], s_eq[32];
   __shared__ int s_digit, s_left;
   const int h = blockIdx.x, Hkv = gridDim.x, s = blockIdx.y, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
+  for (int i = tid; i < 3 * kEvictBins; i += kEvictThreads) hist[0][i] = 0;
+  pdl_wait();
+  pdl_trigger();
   const int64_t head = (int64_t)s * Hkv + h;
   int64_t n = len[s];
   if (n < 0 || n > cap) {
@@ -279,47 +276,66 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
   for (int64_t i = n_out + tid; i < n_keep; i += kEvictThreads) out[i] = -1;
   if (dw)
     for (int64_t i = n_out + tid; i < dcap; i += kEvictThreads) dw[i] = 0.f;
-  auto emit = [&](int pos, int row) {
-    out[pos] = row;
-    if (dw) dw[pos] = w[row];
-  };
   bool bad = false;
+  auto look = [&](float v) { bad = bad || !(v >= 0.f) || isinf(v); };
+  auto copy = [&](int pos, int row) {
+    const float v = w[row];
+    look(v);
+    out[pos] = row;
+    if (dw) dw[pos] = v;
+  };
   if (n <= n_keep) {
-    for (int i = tid; i < (int)n; i += kEvictThreads) {
-      if (!(w[i] >= 0.f) || isinf(w[i])) bad = true;
-      emit(i, i);
-    }
+    for (int i = tid; i < (int)n; i += kEvictThreads) copy(i, i);
     if (bad) atomicOr(&g_err_kv8, ERRBIT_NONFINITE);
     return;
   }
   const int lo = n_sink, hi = (int)n - n_recent, m = hi - lo;    // candidates; m > k because n > n_keep
   const int k = n_keep - n_sink - n_recent;
-  for (int i = tid; i < n_sink; i += kEvictThreads) emit(i, i);
-  for (int i = tid; i < n_recent; i += kEvictThreads) emit(n_keep - n_recent + i, hi + i);
-  for (int i = tid; i < (int)n; i += kEvictThreads) {
-    const float v = w[i];
-    if (!(v >= 0.f) || isinf(v)) bad = true;
-    if (SMEM && i >= lo && i < hi) skey[i - lo] = weight_key(v);
+  // this warp's candidates, lane by lane; KPT * 1024 >= m
+  const int seg = ((m + 31) / 32 + 31) & ~31;    // rows per warp, a multiple of 32
+  const int i0 = warp * seg, i1 = min(m, i0 + seg);
+  const float* wl = w + lo + i0 + lane;
+  uint32_t key[KPT > 0 ? KPT : 1];
+  auto each = [&](auto&& f) {                    // f(candidate, its key), whole warps; past the run the key is 0
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (j * 32 < seg) f(i0 + j * 32 + lane, key[j]);
+    } else {
+      for (int i = i0; i < i1; i += 32) f(i + lane, i + lane < i1 ? weight_key(wl[i - i0]) : 0u);
+    }
+  };
+  if constexpr (KPT > 0) {
+    float v[KPT];
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) v[j] = i0 + j * 32 + lane < i1 ? wl[j * 32] : 0.f;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      look(v[j]);
+      key[j] = i0 + j * 32 + lane < i1 ? weight_key(v[j]) : 0u;
+    }
+  } else {
+    for (int i = i0 + lane; i < i1; i += 32) look(wl[i - i0 - lane]);
   }
+  for (int i = tid; i < n_sink; i += kEvictThreads) copy(i, i);
+  for (int i = tid; i < n_recent; i += kEvictThreads) copy(n_keep - n_recent + i, hi + i);
   if (bad) atomicOr(&g_err_kv8, ERRBIT_NONFINITE);
   if (k == 0) return;
-  auto key_at = [&](int i) -> uint32_t { return SMEM ? skey[i] : weight_key(w[lo + i]); };
+  __syncthreads();
   uint32_t prefix = 0, mask = 0;
   int left = k;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t dmask = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kEvictBins; i += kEvictThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < m; i += kEvictThreads) {
-      const uint32_t key = key_at(i);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & dmask], 1);
-    }
+    int* hp = hist[pass];
+    each([&](int, uint32_t x) {
+      if (x != 0u && (x & mask) == prefix) atomicAdd(&hp[(x >> shift) & dmask], 1);
+    });
     __syncthreads();
     // thread t owns bins 2047 - 2t and 2046 - 2t: inclusive scan from the top
-    const int c0 = hist[kEvictBins - 1 - 2 * tid], c1 = hist[kEvictBins - 2 - 2 * tid];
-    int incl = c0 + c1;
+    const int2 c = *reinterpret_cast<const int2*>(&hp[kEvictBins - 2 - 2 * tid]);
+    int incl = c.x + c.y;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -327,127 +343,120 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
     }
     if (lane == 31) s_gt[warp] = incl;
     __syncthreads();
-    int base = 0;
-    for (int i = 0; i < warp; ++i) base += s_gt[i];
-    incl += base;
-    const int excl = incl - c0 - c1;
+    incl += __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+    const int excl = incl - c.x - c.y;
     if (excl < left && incl >= left) {     // exactly one thread
-      const bool second = excl + c0 < left;
+      const bool second = excl + c.y < left;
       s_digit = kEvictBins - 1 - 2 * tid - (second ? 1 : 0);
-      s_left = left - excl - (second ? c0 : 0);
+      s_left = left - excl - (second ? c.y : 0);
     }
     __syncthreads();
     prefix |= (uint32_t)s_digit << shift;
     mask |= dmask << shift;
     left = s_left;
-    __syncthreads();
   }
   // every key above the threshold, and the first `left` keys equal to it
-  const int seg = ((m + 31) / 32 + 31) & ~31;    // rows per warp, a multiple of 32
-  const int i0 = warp * seg, i1 = min(m, i0 + seg);
   int gt = 0, eq = 0;
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const uint32_t key = in ? key_at(i + lane) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, in && key > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, in && key == prefix));
-  }
+  each([&](int, uint32_t x) {
+    gt += __popc(__ballot_sync(0xffffffffu, x > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, x == prefix));
+  });
   if (lane == 0) {
     s_gt[warp] = gt;
     s_eq[warp] = eq;
   }
   __syncthreads();
-  int gt0 = 0, eq0 = 0;
-  for (int i = 0; i < warp; ++i) {
-    gt0 += s_gt[i];
-    eq0 += s_eq[i];
-  }
+  int gt0 = n_sink + __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+  int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
   const unsigned below = (1u << lane) - 1u;
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const uint32_t key = in ? key_at(i + lane) : 0u;
-    const unsigned bg = __ballot_sync(0xffffffffu, in && key > prefix);
-    const unsigned be = __ballot_sync(0xffffffffu, in && key == prefix);
-    const int g = gt0 + __popc(bg & below), q = eq0 + __popc(be & below);    // before this row
-    if (((bg >> lane) & 1) || (((be >> lane) & 1) && q < left)) emit(n_sink + g + min(q, left), lo + i + lane);
+  each([&](int i, uint32_t x) {
+    const unsigned bg = __ballot_sync(0xffffffffu, x > prefix), be = __ballot_sync(0xffffffffu, x == prefix);
+    const int q = eq0 + __popc(be & below);      // equal ones before this row
+    if (x > prefix || (x == prefix && q < left)) {
+      const int pos = gt0 + __popc(bg & below) + min(q, left);
+      out[pos] = lo + i;
+      if (dw) dw[pos] = w[lo + i];
+    }
     gt0 += __popc(bg);
     eq0 += __popc(be);
+  });
+}
+
+// the largest magnitude of 16 codes: bytes c + 128 as halves of words, their largest and smallest
+__device__ __forceinline__ int max_code(const uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t hi = 0x00800080u, lo = 0x00800080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = w[i] ^ 0x80808080u, a = u & 0x00ff00ffu, b = __byte_perm(u, 0, 0x4341);
+    hi = __vimax3_u16x2(hi, a, b);
+    lo = __vimin3_u16x2(lo, a, b);
   }
+  return max(max((int)(hi & 0xffffu), (int)(hi >> 16)) - 128, 128 - min((int)(lo & 0xffffu), (int)(lo >> 16)));
 }
 
 // One CTA per (destination block, K or V, head, sequence): gathers the block's kept rows,
-// takes their largest value, codes them afresh.  Rows past the last kept one are left alone.
+// takes their largest value, codes them afresh.  Rows past the last kept one (kept[] < 0 there)
+// are left alone.  A value is fl(code * its scale); its quotient by the new scale is coded from
+// the code times the scales' ratio (kv8_code16's three roundings).
 template <int NCH>
-__global__ void __launch_bounds__(1024) k_kv8_move(const cb_kv8_cache c, const cb_kv8_cache d, int lg, int Hkv, int hd,
-                                                   const int32_t* __restrict__ dst_len, int n_keep,
-                                                   const int32_t* __restrict__ kept) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ float sh[32];
+__global__ void __launch_bounds__(512) k_kv8_move(const cb_kv8_cache c, const cb_kv8_cache d, int lg, int Hkv, int hd,
+                                                  uint32_t row_magic, int n_keep, const int32_t* __restrict__ kept) {
+  __shared__ uint32_t sh[32];
   const int s = blockIdx.z, h = blockIdx.y, b = blockIdx.x >> 1;
   const bool is_v = blockIdx.x & 1;
-  const int r0 = b << lg, n = dst_len[s];
-  if (r0 >= n) return;
-  const int rows = min(1 << lg, n - r0);
+  const int r0 = b << lg;
   const int64_t head = (int64_t)s * Hkv + h;
   const int8_t* codes = (is_v ? c.v_codes : c.k_codes) + head * c.capacity * hd;
   const float* scale = (is_v ? c.v_scale : c.k_scale) + head * (c.capacity >> lg);
   int8_t* out = (is_v ? d.v_codes : d.k_codes) + (head * d.capacity + r0) * hd;
   const int32_t* kr = kept + head * n_keep + r0;
-  const int per_row = hd >> 4;
-  const int row0 = threadIdx.x / per_row, col = (threadIdx.x - row0 * per_row) << 4, step = (1 << lg) / NCH;
-  uint4 x[NCH];
-  float f[NCH][16], xs[NCH];
+  const int row0 = threadIdx.x * row_magic >> 16, col = (threadIdx.x << 4) - row0 * hd, step = (1 << lg) / NCH;
+  pdl_wait();
+  pdl_trigger();
+  int r[NCH];
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int row = row0 + i * step;
-    if (row < rows) {
-      const int64_t r = kr[row];
-      xs[i] = scale[r >> lg];
-      x[i] = *reinterpret_cast<const uint4*>(codes + r * hd + col);
-    }
-  }
-  float amax = 0.f;
+  for (int i = 0; i < NCH; ++i) r[i] = row0 + i * step < n_keep - r0 ? kr[row0 + i * step] : -1;
+  if (kr[0] < 0) return;
+  uint4 x[NCH];
+  float xs[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i)
-    if (row0 + i * step < rows) {
-      // the largest |code| times the scale is the largest |value|: products round monotonically
-      float m = 0.f;
-      kv8_unpack16(x[i], f[i]);
-#pragma unroll
-      for (int q = 0; q < 16; ++q) m = fmaxf(m, fabsf(f[i][q]));
-      amax = fmaxf(amax, __fmul_rn(m, xs[i]));
+    if (r[i] >= 0) {
+      xs[i] = scale[r[i] >> lg];
+      x[i] = *reinterpret_cast<const uint4*>(codes + (int64_t)r[i] * hd + col);
     }
-  amax = kv8_block_max(amax, sh);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i)
+    if (r[i] >= 0)       // the largest |code| times the scale is the largest |value|: products round monotonically
+      top = max(top, __float_as_uint(__fmul_rn((float)max_code(x[i]), xs[i])) & 0x7fffffffu);
+  const float amax = kv8_block_max(top, sh);
   const float sc = fmaxf(__fdiv_rn(amax, 127.0f), kKv8MinScale);
   const float inv = 1.0f / sc;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int row = row0 + i * step;
-    if (row < rows) {
-#pragma unroll
-      for (int q = 0; q < 16; ++q) f[i][q] = __fmul_rn(f[i][q], xs[i]);
-      *reinterpret_cast<uint4*>(out + row * hd + col) = kv8_code16(f[i], sc, inv);
+  for (int i = 0; i < NCH; ++i)
+    if (r[i] >= 0) {
+      uint64_t f[8];
+      kv8_unpack16(x[i], f);
+      *reinterpret_cast<uint4*>(out + (row0 + i * step) * hd + col) =
+          kv8_code16(f, xs[i] * inv, [&](float z, uint32_t q) { return kv8_code(__fmul_rn(z, xs[i]), sc, q); });
     }
-  }
   if (threadIdx.x == 0) (is_v ? d.v_scale : d.k_scale)[head * (d.capacity >> lg) + b] = sc;
 }
 
-// select's shared-memory limit set, per device
-std::mutex g_kv8_mem_mu;
-bool g_select_attr[64];
-
-// 16-channel chunks of a block (a multiple of 32, 32..2048) per thread, in whole warps
-int chunks_per_thread(int chunks) { return chunks > 128 && chunks % 64 == 0 ? 2 : 1; }
+// 16-channel chunks of a block (a multiple of 32, 32..2048) per thread, in whole warps and whole
+// rows apart
+int chunks_per_thread(int chunks) {
+  if (chunks >= 512 && chunks % 128 == 0) return 4;
+  return chunks > 128 && chunks % 64 == 0 ? 2 : 1;
+}
+// t / (hd / 16) of a thread index t < 512 as t * magic >> 16
+uint32_t row_magic(int hd) { return (65536 + hd / 16 - 1) / (hd / 16); }
 
 int log2_of(int block) { return 31 - __builtin_clz((unsigned)block); }
 
 }  // namespace
-
-void reset_kv8_caches() {
-  std::lock_guard<std::mutex> g(g_kv8_mem_mu);
-  for (int i = 0; i < 64; ++i) g_select_attr[i] = false;
-}
 
 cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, const int32_t* start,
                               const int32_t* count, const cb_kv8_cache& c, int Hkv, int hd, cudaStream_t s) {
@@ -458,11 +467,13 @@ cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, 
   const int lg = log2_of(c.block);
 #define CB_APPEND(T, N)                                                                                      \
   return launch_k(k_kv8_append<T, N>, grid, blk, 0, s, static_cast<const T*>(k), static_cast<const T*>(v), n_rows, \
-                  start, count, c, lg, Hkv, hd)
+                  start, count, c, lg, Hkv, hd, row_magic(hd))
   if (dt == DT_BF16) {
+    if (nch == 4) CB_APPEND(bf16, 4);
     if (nch == 2) CB_APPEND(bf16, 2);
     CB_APPEND(bf16, 1);
   }
+  if (nch == 4) CB_APPEND(float, 4);
   if (nch == 2) CB_APPEND(float, 2);
   CB_APPEND(float, 1);
 #undef CB_APPEND
@@ -485,32 +496,26 @@ cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const f
                               int n_recent, int64_t dcap, int32_t* dst_len, float* dst_weights, int32_t* kept, int Hkv,
                               cudaStream_t s) {
   const dim3 grid(Hkv, c.n_seq);
-  if (c.capacity > kEvictSmemKeys)
-    return launch_k(k_kv8_select<false>, grid, dim3(kEvictThreads), 0, s, weights, len, c.capacity, n_keep, n_sink,
-                    n_recent, dcap, dst_len, dst_weights, kept);
-  const size_t smem = (size_t)c.capacity * 4;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  {
-    std::lock_guard<std::mutex> g(g_kv8_mem_mu);
-    if (dev < 0 || dev >= 64 || !g_select_attr[dev]) {
-      e = cudaFuncSetAttribute(k_kv8_select<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictSmemKeys * 4);
-      if (e != cudaSuccess) return e;
-      if (dev >= 0 && dev < 64) g_select_attr[dev] = true;
-    }
-  }
-  return launch_k(k_kv8_select<true>, grid, dim3(kEvictThreads), smem, s, weights, len, c.capacity, n_keep, n_sink,
-                  n_recent, dcap, dst_len, dst_weights, kept);
+#define CB_SELECT(KPT)                                                                                              \
+  return launch_k(k_kv8_select<KPT>, grid, dim3(kEvictThreads), 0, s, weights, len, c.capacity, n_keep, n_sink, n_recent, \
+                  dcap, dst_len, dst_weights, kept)
+  if (c.capacity <= 4 * kEvictThreads) CB_SELECT(4);
+  if (c.capacity <= 16 * kEvictThreads) CB_SELECT(16);
+  if (c.capacity <= 32 * kEvictThreads) CB_SELECT(32);
+  CB_SELECT(0);
+#undef CB_SELECT
 }
 
-cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, const int32_t* dst_len, int n_keep,
-                            const int32_t* kept, int Hkv, int hd, cudaStream_t s) {
+cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, int n_keep, const int32_t* kept, int Hkv,
+                            int hd, cudaStream_t s) {
   const int chunks = c.block * hd / 16, nch = chunks_per_thread(chunks);
   const dim3 grid(2 * ((n_keep + c.block - 1) / c.block), Hkv, c.n_seq), blk(chunks / nch);
   const int lg = log2_of(c.block);
-  if (nch == 2) return launch_k(k_kv8_move<2>, grid, blk, 0, s, c, d, lg, Hkv, hd, dst_len, n_keep, kept);
-  return launch_k(k_kv8_move<1>, grid, blk, 0, s, c, d, lg, Hkv, hd, dst_len, n_keep, kept);
+#define CB_MOVE(N) return launch_k(k_kv8_move<N>, grid, blk, 0, s, c, d, lg, Hkv, hd, row_magic(hd), n_keep, kept)
+  if (nch == 4) CB_MOVE(4);
+  if (nch == 2) CB_MOVE(2);
+  CB_MOVE(1);
+#undef CB_MOVE
 }
 
 }  // namespace cb
