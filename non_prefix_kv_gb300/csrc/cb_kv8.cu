@@ -102,7 +102,7 @@ __device__ __forceinline__ void zero_bad(uint64_t* f) {
 // of one row, held in registers between the maximum and the coding, so every new element is
 // read once.
 template <typename T, int NCH>
-__global__ void __launch_bounds__(512) k_kv8_append(const T* __restrict__ k, const T* __restrict__ v, int n_rows,
+__global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1) k_kv8_append(const T* __restrict__ k, const T* __restrict__ v, int n_rows,
                                                      const int32_t* __restrict__ start,
                                                      const int32_t* __restrict__ count, const cb_kv8_cache c, int lg,
                                                      int Hkv, int hd, uint32_t row_magic) {
@@ -243,10 +243,13 @@ __device__ __forceinline__ uint32_t weight_key(float w) { return (w > 0.f ? __fl
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictBins = 2048;         // 11-bit digits: three passes over the 32 key bits
 
-// One CTA per (head, sequence): radix select of the k heaviest rows of [lo, hi), ties to the
-// lower row, then an ordered compaction.  Warp w owns a contiguous run of rows and ranks them
-// by ballots.  A thread holds its KPT keys in registers over all passes; with KPT = 0 (more
-// rows than 32 per thread) each pass reads the weights again, from L2.
+// One CTA per (head, sequence): radix select of the n_keep largest keys, where the first n_sink
+// and the last n_recent rows have the largest key of all, ties to the lower row, then an
+// ordered compaction.  A thread owns a run of consecutive rows, so it ranks its own keys by
+// counting and one scan over the threads places them; their keys stay in registers over all
+// passes (KPT of them: 4, 16 or 32 by the capacity; 8 heads of 16384 rows take 13 us with 16,
+// 34 us read again in each pass, 32 heads of 32768 rows 29 and 77 us).  With KPT = 0 (more rows
+// than 32 per thread) each pass reads the weights again.
 template <int KPT>
 __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __restrict__ weights,
                                                               const int32_t* __restrict__ len, int64_t cap, int n_keep,
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
                                                               float* __restrict__ dst_weights,
                                                               int32_t* __restrict__ kept) {
   __shared__ int hist[3][kEvictBins];
-  __shared__ int s_gt[32], s_eq[32];
+  __shared__ int s_sum[32], s_eq[32];
   __shared__ int s_digit, s_left;
   const int h = blockIdx.x, Hkv = gridDim.x, s = blockIdx.y, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -278,52 +281,66 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
     for (int64_t i = n_out + tid; i < dcap; i += kEvictThreads) dw[i] = 0.f;
   bool bad = false;
   auto look = [&](float v) { bad = bad || !(v >= 0.f) || isinf(v); };
-  auto copy = [&](int pos, int row) {
-    const float v = w[row];
-    look(v);
-    out[pos] = row;
-    if (dw) dw[pos] = v;
-  };
   if (n <= n_keep) {
-    for (int i = tid; i < (int)n; i += kEvictThreads) copy(i, i);
+    for (int i = tid; i < (int)n; i += kEvictThreads) {
+      const float v = w[i];
+      look(v);
+      out[i] = i;
+      if (dw) dw[i] = v;
+    }
     if (bad) atomicOr(&g_err_kv8, ERRBIT_NONFINITE);
     return;
   }
-  const int lo = n_sink, hi = (int)n - n_recent, m = hi - lo;    // candidates; m > k because n > n_keep
-  const int k = n_keep - n_sink - n_recent;
-  // this warp's candidates, lane by lane; KPT * 1024 >= m
-  const int seg = ((m + 31) / 32 + 31) & ~31;    // rows per warp, a multiple of 32
-  const int i0 = warp * seg, i1 = min(m, i0 + seg);
-  const float* wl = w + lo + i0 + lane;
+  const int hi = (int)n - n_recent;
+  auto key_of = [&](int i, float v) -> uint32_t {
+    return i >= (int)n ? 0u : i < n_sink || i >= hi ? ~0u : weight_key(v);
+  };
+  // this thread's rows: whole float4's, within the capacity (a multiple of 16)
+  const int run = KPT > 0 ? KPT : ((int)((n + kEvictThreads - 1) / kEvictThreads) + 3) & ~3, i0 = tid * run;
   uint32_t key[KPT > 0 ? KPT : 1];
-  auto each = [&](auto&& f) {                    // f(candidate, its key), whole warps; past the run the key is 0
+  auto load4 = [&](int i) -> float4 {
+    return i < (int)n ? *reinterpret_cast<const float4*>(w + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  auto look4 = [&](int i, float4 v) {
+    look(v.x);
+    if (i + 1 < (int)n) look(v.y);
+    if (i + 2 < (int)n) look(v.z);
+    if (i + 3 < (int)n) look(v.w);
+  };
+  auto each = [&](auto&& f) {                    // f(row, its key); rows past the last have key 0
     if constexpr (KPT > 0) {
 #pragma unroll
-      for (int j = 0; j < KPT; ++j)
-        if (j * 32 < seg) f(i0 + j * 32 + lane, key[j]);
+      for (int j = 0; j < KPT; ++j) f(i0 + j, key[j]);
     } else {
-      for (int i = i0; i < i1; i += 32) f(i + lane, i + lane < i1 ? weight_key(wl[i - i0]) : 0u);
+      for (int i = i0; i < i0 + run && i < (int)n; i += 4) {
+        const float4 v = load4(i);
+        f(i, key_of(i, v.x));
+        f(i + 1, key_of(i + 1, v.y));
+        f(i + 2, key_of(i + 2, v.z));
+        f(i + 3, key_of(i + 3, v.w));
+      }
     }
   };
   if constexpr (KPT > 0) {
-    float v[KPT];
+    float4 v[KPT / 4];
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) v[j] = i0 + j * 32 + lane < i1 ? wl[j * 32] : 0.f;
+    for (int j = 0; j < KPT / 4; ++j) v[j] = load4(i0 + 4 * j);
 #pragma unroll
-    for (int j = 0; j < KPT; ++j) {
-      look(v[j]);
-      key[j] = i0 + j * 32 + lane < i1 ? weight_key(v[j]) : 0u;
+    for (int j = 0; j < KPT / 4; ++j) {
+      const int i = i0 + 4 * j;
+      look4(i, v[j]);
+      key[4 * j] = key_of(i, v[j].x);
+      key[4 * j + 1] = key_of(i + 1, v[j].y);
+      key[4 * j + 2] = key_of(i + 2, v[j].z);
+      key[4 * j + 3] = key_of(i + 3, v[j].w);
     }
   } else {
-    for (int i = i0 + lane; i < i1; i += 32) look(wl[i - i0 - lane]);
+    for (int i = i0; i < i0 + run && i < (int)n; i += 4) look4(i, load4(i));
   }
-  for (int i = tid; i < n_sink; i += kEvictThreads) copy(i, i);
-  for (int i = tid; i < n_recent; i += kEvictThreads) copy(n_keep - n_recent + i, hi + i);
   if (bad) atomicOr(&g_err_kv8, ERRBIT_NONFINITE);
-  if (k == 0) return;
   __syncthreads();
   uint32_t prefix = 0, mask = 0;
-  int left = k;
+  int left = n_keep;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
@@ -341,9 +358,9 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) s_gt[warp] = incl;
+    if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-    incl += __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+    incl += __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
     const int excl = incl - c.x - c.y;
     if (excl < left && incl >= left) {     // exactly one thread
       const bool second = excl + c.y < left;
@@ -355,31 +372,62 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
     mask |= dmask << shift;
     left = s_left;
   }
-  // every key above the threshold, and the first `left` keys equal to it
+  // every key above the threshold (fewer than n_keep) and the first `left` keys equal to it: a
+  // thread's first place is the number of both before its rows
   int gt = 0, eq = 0;
   each([&](int, uint32_t x) {
-    gt += __popc(__ballot_sync(0xffffffffu, x > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, x == prefix));
+    gt += x > prefix;
+    eq += x == prefix;
   });
-  if (lane == 0) {
-    s_gt[warp] = gt;
-    s_eq[warp] = eq;
+  int gi = gt, ei = eq;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, gi, o), b = __shfl_up_sync(0xffffffffu, ei, o);
+    if (lane >= o) {
+      gi += a;
+      ei += b;
+    }
+  }
+  if (lane == 31) {
+    s_sum[warp] = gi;
+    s_eq[warp] = ei;
   }
   __syncthreads();
-  int gt0 = n_sink + __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
-  int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
-  const unsigned below = (1u << lane) - 1u;
-  each([&](int i, uint32_t x) {
-    const unsigned bg = __ballot_sync(0xffffffffu, x > prefix), be = __ballot_sync(0xffffffffu, x == prefix);
-    const int q = eq0 + __popc(be & below);      // equal ones before this row
-    if (x > prefix || (x == prefix && q < left)) {
-      const int pos = gt0 + __popc(bg & below) + min(q, left);
-      out[pos] = lo + i;
-      if (dw) dw[pos] = w[lo + i];
+  int g = gi - gt + __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
+  int q = ei - eq + __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
+  if constexpr (KPT > 0) {
+    // kept rows as bits; then the warp walks its rows 32 at a time, so that the writes are in order
+    const int at = g + min(q, left);
+    uint32_t keep = 0;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      const bool same = key[j] == prefix;
+      if (key[j] > prefix || (same && q < left)) keep |= 1u << j;
+      q += same;
     }
-    gt0 += __popc(bg);
-    eq0 += __popc(be);
-  });
+    const int bit = lane % KPT;
+#pragma unroll 4
+    for (int j = 0; j < KPT; ++j) {
+      const int from = j * (32 / KPT) + lane / KPT;
+      const uint32_t m = __shfl_sync(0xffffffffu, keep, from);
+      const int pos = __shfl_sync(0xffffffffu, at, from) + __popc(m & ((1u << bit) - 1u));
+      if (m >> bit & 1u) {
+        const int row = warp * 32 * KPT + j * 32 + lane;
+        out[pos] = row;
+        if (dw) dw[pos] = w[row];
+      }
+    }
+  } else {
+    each([&](int i, uint32_t x) {
+      if (x > prefix || (x == prefix && q < left)) {
+        const int pos = g + min(q, left);
+        out[pos] = i;
+        if (dw) dw[pos] = w[i];
+      }
+      g += x > prefix;
+      q += x == prefix;
+    });
+  }
 }
 
 // the largest magnitude of 16 codes: bytes c + 128 as halves of words, their largest and smallest
@@ -400,7 +448,7 @@ __device__ __forceinline__ int max_code(const uint4 v) {
 // are left alone.  A value is fl(code * its scale); its quotient by the new scale is coded from
 // the code times the scales' ratio (kv8_code16's three roundings).
 template <int NCH>
-__global__ void __launch_bounds__(512) k_kv8_move(const cb_kv8_cache c, const cb_kv8_cache d, int lg, int Hkv, int hd,
+__global__ void __launch_bounds__(512, 2) k_kv8_move(const cb_kv8_cache c, const cb_kv8_cache d, int lg, int Hkv, int hd,
                                                   uint32_t row_magic, int n_keep, const int32_t* __restrict__ kept) {
   __shared__ uint32_t sh[32];
   const int s = blockIdx.z, h = blockIdx.y, b = blockIdx.x >> 1;
@@ -446,9 +494,11 @@ __global__ void __launch_bounds__(512) k_kv8_move(const cb_kv8_cache c, const cb
 }
 
 // 16-channel chunks of a block (a multiple of 32, 32..2048) per thread, in whole warps and whole
-// rows apart
-int chunks_per_thread(int chunks) {
-  if (chunks >= 512 && chunks % 128 == 0) return 4;
+// rows apart.  Four of them from 512 on for append, from 256 on for the move, whose loads wait for
+// an index (blocks of 32 rows, hd 128: one token's append 4.1 us with two, 4.3 with four; halving
+// a 4096-row cache 31.4 us with two, 29.3 with four).
+int chunks_per_thread(int chunks, int four) {
+  if (chunks >= four && chunks % 128 == 0) return 4;
   return chunks > 128 && chunks % 64 == 0 ? 2 : 1;
 }
 // t / (hd / 16) of a thread index t < 512 as t * magic >> 16
@@ -460,7 +510,7 @@ int log2_of(int block) { return 31 - __builtin_clz((unsigned)block); }
 
 cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, const int32_t* start,
                               const int32_t* count, const cb_kv8_cache& c, int Hkv, int hd, cudaStream_t s) {
-  const int chunks = c.block * hd / 16, nch = chunks_per_thread(chunks);
+  const int chunks = c.block * hd / 16, nch = chunks_per_thread(chunks, 512);
   // a run of n_rows rows touches at most this many blocks, wherever it starts
   const unsigned nb = (unsigned)(((int64_t)n_rows + 2 * c.block - 2) / c.block);
   const dim3 grid(2 * nb, Hkv, c.n_seq), blk(chunks / nch);
@@ -508,7 +558,7 @@ cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const f
 
 cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, int n_keep, const int32_t* kept, int Hkv,
                             int hd, cudaStream_t s) {
-  const int chunks = c.block * hd / 16, nch = chunks_per_thread(chunks);
+  const int chunks = c.block * hd / 16, nch = chunks_per_thread(chunks, 256);
   const dim3 grid(2 * ((n_keep + c.block - 1) / c.block), Hkv, c.n_seq), blk(chunks / nch);
   const int lg = log2_of(c.block);
 #define CB_MOVE(N) return launch_k(k_kv8_move<N>, grid, blk, 0, s, c, d, lg, Hkv, hd, row_magic(hd), n_keep, kept)

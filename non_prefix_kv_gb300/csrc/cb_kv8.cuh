@@ -13,11 +13,11 @@ constexpr float kKv8MinScale = 1e-8f;
 
 // The integer nearest to x / s (ties to even), s > 0, as the low byte, from q = the bits of
 // c + 1.5 2^23 with c within one of it: the residual x - c s is exact in one fma (|r| <= s and
-// r is a multiple of the smaller of the two operands' last places), so comparing it with s/2
-// decides.
+// r is a multiple of the smaller of the two operands' last places).  Beyond s/2, or at s/2 and c
+// odd (the same as beyond the float before s/2), the neighbour is nearer.
 __device__ __forceinline__ uint32_t kv8_code(float x, float s, uint32_t q) {
-  const float r = fmaf(12582912.0f - __uint_as_float(q), s, x), h = 0.5f * s;
-  if (fabsf(r) > h || (fabsf(r) == h && (q & 1u))) q += r > 0.f ? 1u : ~0u;
+  const float r = fmaf(12582912.0f - __uint_as_float(q), s, x);
+  if (fabsf(r) > __uint_as_float(__float_as_uint(0.5f * s) - (q & 1u))) q += (__float_as_int(r) >> 31) | 1;
   return q;
 }
 
@@ -51,32 +51,31 @@ __device__ __forceinline__ uint32_t kv8_pack4(uint32_t a, uint32_t b, uint32_t c
 // x inv + 1.5 2^23 leaves the nearest integer in the low byte (a two's-complement byte, as the
 // 24 bits above it hold the offset's); its distance tells whether the roundings (at most
 // 127 * 3 * 2^-24 = 2.3e-5 in the quotient) could have chosen the other one.  Only then
-// exact(value, code) decides: for one value in 16000 by chance, but half the block's largest
-// value is a tie, which bf16 values hit often enough to send one warp in eight there.
+// exact(value, code) decides, for the 4 values of a word: one value in 16000 by chance, but
+// half a block's largest value is a tie, which bf16 values hit often, and re-coded rows of one
+// old block nearly always.
 template <typename F>
 __device__ __forceinline__ uint4 kv8_code16(const uint64_t* x, float inv, F&& exact) {
   constexpr float kMagic = 12582912.0f;
   const uint64_t inv2 = tc::f2_pack(inv, inv), magic = tc::f2_pack(kMagic, kMagic), minus = tc::f2_pack(-1.f, -1.f);
-  uint32_t q[16];
-  float far = 0.f;
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint64_t t = tc::f2_fma(x[i], inv2, magic);
-    const float2 d = tc::f2_unpack(tc::f2_fma(x[i], inv2, tc::f2_fma(t, minus, magic))), c = tc::f2_unpack(t);
-    far = fmaxf(fmaxf(far, fabsf(d.x)), fabsf(d.y));
-    q[2 * i] = __float_as_uint(c.x);
-    q[2 * i + 1] = __float_as_uint(c.y);
-  }
-  if (far > 0.5f - 3.1e-5f) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 v = tc::f2_unpack(x[i]);
-      q[2 * i] = exact(v.x, q[2 * i]);
-      q[2 * i + 1] = exact(v.y, q[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t0 = tc::f2_fma(x[2 * i], inv2, magic), t1 = tc::f2_fma(x[2 * i + 1], inv2, magic);
+    const float2 d0 = tc::f2_unpack(tc::f2_fma(x[2 * i], inv2, tc::f2_fma(t0, minus, magic)));
+    const float2 d1 = tc::f2_unpack(tc::f2_fma(x[2 * i + 1], inv2, tc::f2_fma(t1, minus, magic)));
+    const float2 c0 = tc::f2_unpack(t0), c1 = tc::f2_unpack(t1);
+    uint32_t q[4] = {__float_as_uint(c0.x), __float_as_uint(c0.y), __float_as_uint(c1.x), __float_as_uint(c1.y)};
+    if (fmaxf(fmaxf(fabsf(d0.x), fabsf(d0.y)), fmaxf(fabsf(d1.x), fabsf(d1.y))) > 0.5f - 3.1e-5f) {
+      const float2 v0 = tc::f2_unpack(x[2 * i]), v1 = tc::f2_unpack(x[2 * i + 1]);
+      q[0] = exact(v0.x, q[0]);
+      q[1] = exact(v0.y, q[1]);
+      q[2] = exact(v1.x, q[2]);
+      q[3] = exact(v1.y, q[3]);
     }
+    w[i] = kv8_pack4(q[0], q[1], q[2], q[3]);
   }
-  return make_uint4(kv8_pack4(q[0], q[1], q[2], q[3]), kv8_pack4(q[4], q[5], q[6], q[7]),
-                    kv8_pack4(q[8], q[9], q[10], q[11]), kv8_pack4(q[12], q[13], q[14], q[15]));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // block-wide maximum of non-negative values as their bits (whole warps); sh holds one word per warp
