@@ -30,13 +30,13 @@ cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const f
 cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, int n_keep, const int32_t* kept, int Hkv,
                             int hd, cudaStream_t s);
 bool kv8_attn_supported(int hd);
-size_t kv8_attn_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
-bool kv8_attn_weights_apart(int dt, int hd, int G, int n_q);
+size_t kv8_attn_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
+bool kv8_attn_weights_apart(int G, int n_q);
 cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
                             int hd, void* out, float* weights, void* ws, cudaStream_t s);
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
                                int Hkv, int hd, float* weights, void* ws, cudaStream_t s);
-bool kv8_tc_taken(int dt, int hd, int G, int n_q);
+bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights);
 size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
 cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
                           void* out, float* weights, void* ws, cudaStream_t s);
@@ -1250,9 +1250,9 @@ namespace {
 // scratch of an attention call: the tensor-core path's operands, or the small path's scores
 size_t kv8_ws(const cb_dims* d, int n_seq, int64_t cap, int n_q, bool weights) {
   const int G = d->n_heads / d->n_kv_heads;
-  if (kv8_tc_taken(d->dtype, d->head_dim, G, n_q))
+  if (kv8_tc_taken(d->dtype, d->head_dim, G, n_q, weights))
     return kv8_tc_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
-  return kv8_attn_ws_bytes(d->dtype, n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
+  return kv8_attn_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
 }
 }  // namespace
 
@@ -1261,7 +1261,9 @@ int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity,
   int st = check_dims(dims);
   if (st) return st;
   if (!out_host || n_seq < 1 || capacity < 1 || n_q < 0) return fail(CB_ERR_INVALID_ARG, "workspace query arguments");
-  *out_host = kv8_ws(dims, n_seq, capacity, n_q, with_weights != 0);
+  // what serves a call with the weights serves one without
+  *out_host = kv8_ws(dims, n_seq, capacity, n_q, false);
+  if (with_weights) *out_host = std::max(*out_host, kv8_ws(dims, n_seq, capacity, n_q, true));
   return CB_OK;
 }
 
@@ -1275,15 +1277,16 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   if (n_q == 0) return CB_OK;
   const int H = dims->n_heads, Hkv = dims->n_kv_heads, hd = dims->head_dim, G = H / Hkv;
   if ((int64_t)n_q * G > (1 << 27)) return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
-  // the line of work is counted in 32 bits: (row tile, sequence, head, 16 keys)
-  if ((double)(((int64_t)n_q * G + 7) / 8) * cache->n_seq * Hkv * ((double)cache->capacity / 16) > (double)INT32_MAX)
+  // the line of work (row tile, sequence, head, 16 keys) and the rows to join are counted in 32 bits
+  if ((double)(((int64_t)n_q * G + 7) / 8) * cache->n_seq * Hkv * std::max((double)cache->capacity / 16, 8.0) >
+      (double)INT32_MAX)
     return fail(CB_ERR_UNSUPPORTED, "kv8_attention: query rows, sequences, heads and capacity too many for one call");
   if (!q || !last || !out) return fail(CB_ERR_INVALID_ARG, "kv8_attention pointer is NULL");
   if ((st = check_al16({q, out, weights, ws}, "kv8_attention"))) return st;
   const size_t need = kv8_ws(dims, cache->n_seq, cache->capacity, n_q, weights != nullptr);
   if (need && (!ws || ws_bytes < need)) return fail(CB_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
   const int64_t m = (int64_t)cache->n_seq * n_q;
-  if (kv8_tc_taken(dims->dtype, hd, G, n_q)) {
+  if (kv8_tc_taken(dims->dtype, hd, G, n_q, weights != nullptr)) {
     CB_LAUNCH(CB_PROF_KV8_ATTN, 2, m, cache->capacity, H, 0.0, 0.0, S(stream),
               launch_kv8_tc(q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
     g_launches.fetch_add(weights ? 2 : 1, std::memory_order_relaxed);
@@ -1291,7 +1294,7 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   }
   CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),
             launch_kv8_attn(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
-  const bool apart = kv8_attn_weights_apart(dims->dtype, hd, G, n_q);
+  const bool apart = kv8_attn_weights_apart(G, n_q);
   g_launches.fetch_add(weights && !apart ? 2 : 1, std::memory_order_relaxed);    // the merge, and the account
   if (weights && apart)
     CB_LAUNCH(CB_PROF_KV8_ATTN, 1, m, cache->capacity, H, 0.0, 0.0, S(stream),

@@ -1,5 +1,5 @@
 // Attention over the 8-bit block-scaled KV cache (cb_kv8.cu), for a few query rows per KV head
-// (single tokens) and, in tiles of 8 or 16 rows, for any number.
+// (single tokens) and, in tiles of 8 rows, for any number.
 //
 // With ks, vs the scales of key i's block and c_k, c_v its codes:
 //   z_i = (q . c_k,i) * ks * log2(e) / sqrt(hd)                log2 of the unnormalised weight
@@ -41,6 +41,7 @@ constexpr int THREADS = 32 * WARPS;
 constexpr float kPBias = 8.0f;       // 2^(t - m) is held up to 2^8 ...
 constexpr float kLazy = 6.0f;        // ... and up to 2^14 before m is raised: fp16 ends at 2^16
 constexpr float kNone = -1e30f;      // m of a row that has seen no key
+constexpr int TILE = 8;              // query rows of a tile
 constexpr int MAX_WORKERS = 4096;    // warps of the largest grid (a workspace is sized without the device)
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -98,7 +99,7 @@ struct Kv8Attn {
   float* weights;           // [n_seq, Hkv, capacity], or null
   cb_kv8_cache c;
   int n_q, H, Hkv, G, lg;
-  int rt, row_tiles;        // query rows of a tile, tiles of a sequence
+  int row_tiles;            // tiles of a sequence's query rows
   float scale_log2;         // log2(e) / sqrt(hd)
 };
 
@@ -136,8 +137,8 @@ __device__ __forceinline__ void load4(const T* p, bool on, float* f) {
 // Row r of entry e (sequence e / row_tiles, row tile e % row_tiles): the last cache row it sees,
 // -1 where the row does not exist or its bound is bad (reported if asked).
 __device__ __forceinline__ int row_last(const Kv8Attn& p, int e, int r, bool report) {
-  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * p.rt + r;
-  if (r >= p.rt || row >= p.n_q * p.G) return -1;
+  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * TILE + r;
+  if (r >= TILE || row >= p.n_q * p.G) return -1;
   const int l = p.last[(int64_t)s * p.n_q + row / p.G];
   if (l < -1 || l >= p.c.capacity) {
     if (report) atomicOr(&g_err_kv8_attn, ERRBIT_INDEX);
@@ -153,8 +154,8 @@ __device__ __forceinline__ int row_last(const Kv8Attn& p, int e, int r, bool rep
 // new pair, so worker + unit numbers the pairs' slots without a gap wider than one.
 __device__ __forceinline__ int workers_of(int total, int workers) { return max(1, min(workers, total / 2)); }
 __device__ __forceinline__ float* slot(const Kv8Attn& p, int hd, int worker, int unit) {
-  const int rows = min(p.rt, p.n_q * p.G);
-  return p.part + ((int64_t)worker + unit) * (rows * hd + 2 * p.rt);     // [rt] max, [rt] sum, [rows][hd] O
+  const int rows = min(TILE, p.n_q * p.G);
+  return p.part + ((int64_t)worker + unit) * (rows * hd + 2 * TILE);     // [rt] max, [rt] sum, [rows][hd] O
 }
 
 // Single tokens are bound by the cache's bytes, and a grid of CTAs per (sequence, head) leaves
@@ -166,16 +167,15 @@ __device__ __forceinline__ float* slot(const Kv8Attn& p, int hd, int worker, int
 //
 // The products are taken transposed, S^T = C_K Q^T and O^T = C_V^T P^T, with the keys (then the
 // channels) as the 16 rows of mma.m16n8k16 and the query rows as its 8 columns: the few rows of
-// a token fill the instruction, and a thread's share of O is HD / 4 NT registers, so that 16
+// a token fill the instruction, and a thread's share of O is HD / 4 registers, so that 16
 // warps fit on an SM.  (With rows as M and 10 warps: 205 us at an issue rate of 0.33.)
-template <int HD, int NT, typename T>
+template <int HD, typename T>
 __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(const Kv8Attn p) {
   pdl_wait();
   pdl_trigger();
   using L = Lay<HD>;
   constexpr int NS = parts<T>();
   constexpr int KS = HD / 16;                    // k steps of a score; also channel tiles of O
-  constexpr int RT = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((128 - (tc::smem_u32(smem_raw) & 127)) & 127);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
   // entries, a scan over the threads places them (the first CTA writes the plan for the merge)
   auto steps_of = [&](int e, bool report) -> int {
     int mx = -1;
-    for (int r = 0; r < RT; ++r) mx = max(mx, row_last(p, e, r, report));
+    for (int r = 0; r < TILE; ++r) mx = max(mx, row_last(p, e, r, report));
     return (mx + L::KT) / L::KT;
   };
   const int share = (entries + THREADS - 1) / THREADS, e0 = min(entries, tid * share), e1 = min(entries, e0 + share);
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
   bool ok = true;
   for (int i = a; ok && i < b;) {
     // ------------------------------------------------------------------ a unit, or a part of one
-    const int s = cur.e / p.row_tiles, row0 = (cur.e - s * p.row_tiles) * RT, nrow = min(RT, R - row0), h = cur.h;
+    const int s = cur.e / p.row_tiles, row0 = (cur.e - s * p.row_tiles) * TILE, nrow = min(TILE, R - row0), h = cur.h;
     const int64_t head = (int64_t)s * p.Hkv + h;
     const int my_last = row_last(p, cur.e, lane, false);
     const int nk = __reduce_max_sync(0xffffffffu, my_last) + 1;       // keys some row sees
@@ -300,62 +300,56 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
       return r;
     };
     float2 next = scales_of(cur.k * L::KT);
-    // Q^T as the column operand: thread (g, t) holds row 8 n + g, channels [t HD/4, (t + 1) HD/4),
+    // Q^T as the column operand: thread (g, t) holds row g, channels [t HD/4, (t + 1) HD/4),
     // 4 per k step (the order of the channels inside a sum is free; K is read with the same one)
-    uint2 qb[NT][NS][KS];
-    float rf[NT][2];                             // score factor of rows 8 n + 2t, 2t + 1
-    int lastr[NT][2];
+    uint2 qb[NS][KS];
+    float rf[2];                             // score factor of rows 2t, 2t + 1
+    int lastr[2];
+    const int r = row0 + g;
+    const bool on = g < nrow;
+    const int j = on ? r / p.G : 0;
+    const T* qr = static_cast<const T*>(p.q) +
+                  (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (on ? r - j * p.G : 0)) * HD + t * (HD / 4);
+    float amax = 0.f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = row0 + 8 * n + g;
-      const bool on = 8 * n + g < nrow;
-      const int j = on ? r / p.G : 0;
-      const T* qr = static_cast<const T*>(p.q) +
-                    (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (on ? r - j * p.G : 0)) * HD + t * (HD / 4);
-      float amax = 0.f;
+    for (int ks = 0; ks < KS; ++ks) {
+      float f[4];
+      load4(qr + 4 * ks, on, f);
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    // 2^ex <= amax < 2^(ex + 1); both powers stay normal
+    int ex = amax > 0.f ? ilogbf(amax) : 0;
+    ex = ex < -120 ? -120 : (ex > 120 ? 120 : ex);
+    const float down = ldexpf(1.0f, -ex), up = ldexpf(p.scale_log2, ex);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        float f[4];
-        load4(qr + 4 * ks, on, f);
-        amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
-      }
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      // 2^ex <= amax < 2^(ex + 1); both powers stay normal
-      int ex = amax > 0.f ? ilogbf(amax) : 0;
-      ex = ex < -120 ? -120 : (ex > 120 ? 120 : ex);
-      const float down = ldexpf(1.0f, -ex), up = ldexpf(p.scale_log2, ex);
+    for (int ks = 0; ks < KS; ++ks) {
+      float f[4];
+      load4(qr + 4 * ks, on, f);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        float f[4];
-        load4(qr + 4 * ks, on, f);
+      for (int c = 0; c < 4; ++c) f[c] *= down;
+      qb[0][ks] = make_uint2(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]));
+      if constexpr (NS == 2)
+        qb[1][ks] = make_uint2(rest_h2(f[0], f[1], qb[0][ks].x), rest_h2(f[2], f[3], qb[0][ks].y));
+    }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) f[c] *= down;
-        qb[n][0][ks] = make_uint2(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]));
-        if constexpr (NS == 2)
-          qb[n][1][ks] = make_uint2(rest_h2(f[0], f[1], qb[n][0][ks].x), rest_h2(f[2], f[3], qb[n][0][ks].y));
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        rf[n][c] = __shfl_sync(0xffffffffu, up, (2 * t + c) * 4);
-        lastr[n][c] = __shfl_sync(0xffffffffu, my_last, 8 * n + 2 * t + c);
-      }
+    for (int c = 0; c < 2; ++c) {
+      rf[c] = __shfl_sync(0xffffffffu, up, (2 * t + c) * 4);
+      lastr[c] = __shfl_sync(0xffffffffu, my_last, 2 * t + c);
     }
     float* z = p.z ? p.z + (head * R + row0) * cap : nullptr;
-    float O[KS][NT][4];                          // channel tile, row tile: rows 2t, 2t + 1 of channels g, g + 8
-    float m_used[NT][2], l_sum[NT][2];           // of rows 8 n + 2t, 2t + 1 (l: this thread's keys)
+    float O[KS][4];                          // channel tile: rows 2t, 2t + 1 of channels g, g + 8
+    float m_used[2], l_sum[2];           // of rows 2t, 2t + 1 (l: this thread's keys)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        m_used[n][c] = kNone;
-        l_sum[n][c] = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) O[k][n][c] = 0.f;
+    for (int c = 0; c < 2; ++c) {
+      m_used[c] = kNone;
+      l_sum[c] = 0.f;
     }
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) O[k][c] = 0.f;
     const int end = min(b, i + cur.n - cur.k);   // line position after this unit's share
     const int unit = cur.e * p.Hkv + h;
     int k0 = cur.k * L::KT;
@@ -371,11 +365,9 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
         next = scales_of(key0 + 16);
         if (key0 >= nk) continue;
         // ---- scores of 16 keys: thread (g, t) reads keys g and g + 8
-        float S[NT][4];
+        float S[4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) S[n][c] = 0.f;
+        for (int c = 0; c < 4; ++c) S[c] = 0.f;
         const uint8_t* kr = sk + (w * 16 + g) * HD + t * (HD / 4);
         constexpr int KC = HD >= 64 ? 16 : 8;                 // bytes per load
 #pragma unroll
@@ -397,78 +389,67 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
             codes_to_h2(w0[q], x[0], x[2]);
             codes_to_h2(w1[q], x[1], x[3]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int part = 0; part < NS; ++part) mma_f16(S[n], x, qb[n][part][ks].x, qb[n][part][ks].y);
+            for (int part = 0; part < NS; ++part) mma_f16(S, x, qb[part][ks].x, qb[part][ks].y);
           }
         }
-        // ---- weights: element c of S[n] is key g + 8 (c / 2), row 8 n + 2t + c % 2
+        // ---- weights: element c of S is key g + 8 (c / 2), row 2t + c % 2
         const float vs = fmaxf(now.y, kKv8MinScale);
         const float3 sc = make_float3(fmaxf(now.x, kKv8MinScale), NS == 2 ? log2f(vs) : __log2f(vs), __fdividef(1.0f, vs));
         const bool whole = key0 + 15 <= mn;                   // every row sees every key
-        float f[NT][2], add[NT][2], ev[NT][4];
-        bool up = false;
+        float f[2], add[2], ev[4];
+        bool high = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int c = 0; c < 2; ++c) {
+          f[c] = rf[c] * sc.x;
+          add[c] = sc.y - m_used[c] + kPBias;
+        }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (key0 + g + 8 * (c >> 1) > lastr[c & 1]) S[c] = -INFINITY;
+        }
+        if (z) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (2 * t + (c & 1) < nrow)
+              z[(2 * t + (c & 1)) * cap + key0 + g + 8 * (c >> 1)] = S[c] * f[c & 1];
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) ev[c] = fmaf(S[c], f[c & 1], add[c & 1]);
+        high |= fmaxf(fmaxf(ev[0], ev[1]), fmaxf(ev[2], ev[3])) > kPBias + kLazy;
+        // m is raised when a weight would leave fp16's range (and at a row's first key)
+        if (__any_sync(0xffffffffu, high)) {
+          float al[2];
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            f[n][c] = rf[n][c] * sc.x;
-            add[n][c] = sc.y - m_used[n][c] + kPBias;
-          }
-          if (!whole) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (key0 + g + 8 * (c >> 1) > lastr[n][c & 1]) S[n][c] = -INFINITY;
-          }
-          if (z) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (8 * n + 2 * t + (c & 1) < nrow)
-                z[(8 * n + 2 * t + (c & 1)) * cap + key0 + g + 8 * (c >> 1)] = S[n][c] * f[n][c & 1];
+            float tt = fmaxf(S[c], S[c + 2]) * f[c];
+            tt = fmaxf(tt, __shfl_xor_sync(0xffffffffu, tt, 4));
+            tt = fmaxf(tt, __shfl_xor_sync(0xffffffffu, tt, 8));
+            tt = fmaxf(tt, __shfl_xor_sync(0xffffffffu, tt, 16)) + sc.y;
+            const bool raise = tt > m_used[c] + kLazy;
+            al[c] = raise ? tc::ex2_approx(m_used[c] - tt) : 1.0f;
+            if (raise) m_used[c] = tt;
+            l_sum[c] *= al[c];
+            add[c] = sc.y - m_used[c] + kPBias;
+            ev[c] = fmaf(S[c], f[c], add[c]);
+            ev[c + 2] = fmaf(S[c + 2], f[c], add[c]);
           }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) ev[n][c] = fmaf(S[n][c], f[n][c & 1], add[n][c & 1]);
-          up |= fmaxf(fmaxf(ev[n][0], ev[n][1]), fmaxf(ev[n][2], ev[n][3])) > kPBias + kLazy;
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) O[k][c] *= al[c & 1];
         }
-        // m is raised when a weight would leave fp16's range (and at a row's first key)
-        if (__any_sync(0xffffffffu, up)) {
+        uint32_t pb[NS][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float al[2];
+        for (int c = 0; c < 4; ++c) ev[c] = tc::ex2_approx(ev[c]);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float tt = fmaxf(S[n][c], S[n][c + 2]) * f[n][c];
-              tt = fmaxf(tt, __shfl_xor_sync(0xffffffffu, tt, 4));
-              tt = fmaxf(tt, __shfl_xor_sync(0xffffffffu, tt, 8));
-              tt = fmaxf(tt, __shfl_xor_sync(0xffffffffu, tt, 16)) + sc.y;
-              const bool raise = tt > m_used[n][c] + kLazy;
-              al[c] = raise ? tc::ex2_approx(m_used[n][c] - tt) : 1.0f;
-              if (raise) m_used[n][c] = tt;
-              l_sum[n][c] *= al[c];
-              add[n][c] = sc.y - m_used[n][c] + kPBias;
-              ev[n][c] = fmaf(S[n][c], f[n][c], add[n][c]);
-              ev[n][c + 2] = fmaf(S[n][c + 2], f[n][c], add[n][c]);
-            }
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) O[k][n][c] *= al[c & 1];
-          }
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t x = pack_h2(ev[2 * k], ev[2 * k + 1]);
+          pb[0][k] = transpose_h2(x);
+          if constexpr (NS == 2) pb[1][k] = transpose_h2(rest_h2(ev[2 * k], ev[2 * k + 1], x));
         }
-        uint32_t pb[NT][NS][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ev[n][c] = tc::ex2_approx(ev[n][c]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t x = pack_h2(ev[n][2 * k], ev[n][2 * k + 1]);
-            pb[n][0][k] = transpose_h2(x);
-            if constexpr (NS == 2) pb[n][1][k] = transpose_h2(rest_h2(ev[n][2 * k], ev[n][2 * k + 1], x));
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c) l_sum[n][c] = fmaf(ev[n][c] + ev[n][c + 2], sc.z, l_sum[n][c]);
-        }
+        for (int c = 0; c < 2; ++c) l_sum[c] = fmaf(ev[c] + ev[c + 2], sc.z, l_sum[c]);
         // ---- O^T += C_V^T P^T: this thread's V rows are keys 2t, 2t+1, 2t+8, 2t+9; rows g, g + 8
         // of channel tile k stand for channels (HD/8) g + 2 k, + 1
         const uint8_t* vr = sk + L::HALF + (w * 16 + 2 * t) * HD + g * (HD / 8);
@@ -497,12 +478,10 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
                                     codes_pair<2>(v[2][c], v[3][c]), codes_pair<3>(v[2][c], v[3][c])};
             const int k = c0 / 2 + 2 * c;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int part = 0; part < NS; ++part) {
-                mma_f16(O[k][n], x0, pb[n][part][0], pb[n][part][1]);
-                mma_f16(O[k + 1][n], x1, pb[n][part][0], pb[n][part][1]);
-              }
+            for (int part = 0; part < NS; ++part) {
+              mma_f16(O[k], x0, pb[part][0], pb[part][1]);
+              mma_f16(O[k + 1], x1, pb[part][0], pb[part][1]);
+            }
           }
         }
       }
@@ -517,25 +496,23 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
     // ------------------------------------------------------------------ the partial result
     float* dst = slot(p, HD, worker, unit);
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 8 * n + 2 * t + c;
-        float l = l_sum[n][c];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (g == 0) {
-          dst[r] = m_used[n][c];
-          dst[RT + r] = l;
-        }
-        if (r < nrow) {
-          float* o = dst + 2 * RT + r * HD + (HD / 8) * g;
-#pragma unroll
-          for (int k = 0; k < KS; k += 2)
-            *reinterpret_cast<float4*>(o + 2 * k) = make_float4(O[k][n][c], O[k][n][c + 2], O[k + 1][n][c], O[k + 1][n][c + 2]);
-        }
+    for (int c = 0; c < 2; ++c) {
+      const int r = 2 * t + c;
+      float l = l_sum[c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (g == 0) {
+        dst[r] = m_used[c];
+        dst[TILE + r] = l;
       }
+      if (r < nrow) {
+        float* o = dst + 2 * TILE + r * HD + (HD / 8) * g;
+#pragma unroll
+        for (int k = 0; k < KS; k += 2)
+          *reinterpret_cast<float4*>(o + 2 * k) = make_float4(O[k][c], O[k][c + 2], O[k + 1][c], O[k + 1][c + 2]);
+      }
+    }
     cur.k = 0;
     if (i < b) {                                 // the run goes on: the unit was finished
       if (++cur.h == p.Hkv) {
@@ -565,12 +542,11 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p,
   __shared__ float s_o[WPR > 1 ? MERGE_WARPS : 1][HD];
   __shared__ float s_m[MERGE_WARPS], s_l[MERGE_WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
-  const int rows = min(p.rt, p.n_q * p.G), entries = p.c.n_seq * p.row_tiles;
-  const int64_t item = (int64_t)blockIdx.x * (MERGE_WARPS / WPR) + warp / WPR;   // (entry, head, row of the tile)
-  const int64_t units = (int64_t)entries * p.Hkv;
-  if (item >= units * rows) return;    // whole CTAs when WPR = MERGE_WARPS
-  const int unit = (int)(item / rows), r = (int)(item - (int64_t)unit * rows), e = unit / p.Hkv, h = unit - e * p.Hkv;
-  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * p.rt + r, R = p.n_q * p.G;
+  const int rows = min(TILE, p.n_q * p.G), entries = p.c.n_seq * p.row_tiles;
+  const int item = blockIdx.x * (MERGE_WARPS / WPR) + warp / WPR;    // (entry, head, row of the tile)
+  if (item >= entries * p.Hkv * rows) return;    // whole CTAs when WPR = MERGE_WARPS
+  const int unit = item / rows, r = item - unit * rows, e = unit / p.Hkv, h = unit - e * p.Hkv;
+  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * TILE + r, R = p.n_q * p.G;
   const int start = p.plan[e], n = (p.plan[e + 1] - start) / p.Hkv, total = p.plan[entries];
   int w0 = 0, np = 0;                  // the unit's workers: the runs that meet [x0, x1)
   if (n > 0 && row < R) {
@@ -593,7 +569,7 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p,
     if (mine < np) {
       const float* src = slot(p, HD, w0 + mine, unit);
       m = src[r];
-      l = src[p.rt + r];
+      l = src[TILE + r];
     }
     const float top = fmaxf(mm, warp_max(m)), back = tc::ex2_approx(mm - top), f = tc::ex2_approx(m - top);
     mm = top;
@@ -603,7 +579,7 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p,
     const int cnt = min(32, (np - i0 + WPR - 1) / WPR);
 #pragma unroll 8
     for (int i = 0; i < cnt; ++i) {
-      const float* src = slot(p, HD, w0 + i0 + i * WPR, unit) + 2 * p.rt + r * HD + lane * PL;
+      const float* src = slot(p, HD, w0 + i0 + i * WPR, unit) + 2 * TILE + r * HD + lane * PL;
       const float fi = __shfl_sync(0xffffffffu, f, i);
       float v[PL];
       if constexpr (PL >= 4) {
@@ -826,13 +802,13 @@ std::mutex g_kv8_mu;
 uint32_t g_kv8_attr[64];
 int g_kv8_sms[64];
 
-template <int HD, int NT, typename T>
+template <int HD, typename T>
 cudaError_t prepare_attn(int dev) {
   constexpr int h = HD == 32 ? 0 : HD == 64 ? 1 : HD == 128 ? 2 : 3;
-  constexpr uint32_t bit = 1u << (h + (sizeof(T) == 4 ? 4 : 0) + (NT == 2 ? 8 : 0));
+  constexpr uint32_t bit = 1u << (h + (sizeof(T) == 4 ? 4 : 0));
   std::lock_guard<std::mutex> g(g_kv8_mu);
   if (dev >= 0 && dev < 64 && (g_kv8_attr[dev] & bit)) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, NT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<HD>::BYTES);
+  cudaError_t e = cudaFuncSetAttribute(k_kv8_attn<HD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<HD>::BYTES);
   if (e == cudaSuccess && dev >= 0 && dev < 64) g_kv8_attr[dev] |= bit;
   return e;
 }
@@ -849,22 +825,19 @@ int device_sms(int dev) {
   return n;
 }
 
-// rows of a tile of k_kv8_attn: 8 where they suffice, and where two parts of q or 256 channels
-// leave no registers for 16
-int tile_rows(int dt, int hd, int64_t R) { return dt == DT_F32 || hd == 256 || R <= 8 ? 8 : 16; }
-
-template <int HD, int NT, typename T>
-cudaError_t launch_attn_n(const Kv8Attn& p, cudaStream_t s) {
+template <int HD, typename T>
+cudaError_t launch_attn_t(const Kv8Attn& p, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if ((e = prepare_attn<HD, NT, T>(dev)) != cudaSuccess) return e;
+  if ((e = prepare_attn<HD, T>(dev)) != cudaSuccess) return e;
   const int ctas = std::min(ctas_per_sm<HD, T>() * device_sms(dev), MAX_WORKERS / WARPS);
-  if ((e = launch_k(k_kv8_attn<HD, NT, T>, dim3(ctas), dim3(THREADS), Lay<HD>::BYTES, s, p)) != cudaSuccess) return e;
-  // a unit has about workers / units partial results: one warp joins up to two dozen, more go
-  // over a CTA's eight
-  const int64_t units = (int64_t)p.c.n_seq * p.row_tiles * p.Hkv, items = units * std::min(p.rt, p.n_q * p.G);
-  if (units * 24 >= ctas * WARPS)
+  if ((e = launch_k(k_kv8_attn<HD, T>, dim3(ctas), dim3(THREADS), Lay<HD>::BYTES, s, p)) != cudaSuccess) return e;
+  const int64_t items = (int64_t)p.c.n_seq * p.row_tiles * p.Hkv * std::min(TILE, p.n_q * p.G);
+  // a warp per row where that alone fills the SMs, else a CTA (32 sequences of 8 x 7 heads, 1792
+  // rows whose units meet 10 workers each: 144 and 148 us; one of 32 heads, 32 rows and 75
+  // workers: 28 and 17 us; 8 of 32 heads, 256 rows and 10 workers: 48 and 46 us)
+  if (items >= (int64_t)MERGE_WARPS * device_sms(dev))
     e = launch_k(k_kv8_merge<HD, 1, T>, dim3((unsigned)((items + MERGE_WARPS - 1) / MERGE_WARPS)), dim3(32 * MERGE_WARPS), 0,
                  s, p, ctas * WARPS);
   else
@@ -872,13 +845,6 @@ cudaError_t launch_attn_n(const Kv8Attn& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   if (!p.z) return cudaSuccess;
   return launch_k(k_kv8_account, dim3((unsigned)((p.c.capacity + 1023) / 1024), p.Hkv, p.c.n_seq), dim3(256), 0, s, p);
-}
-
-template <int HD, typename T>
-cudaError_t launch_attn_t(const Kv8Attn& p, cudaStream_t s) {
-  if constexpr (HD < 256 && sizeof(T) == 2)
-    if (p.rt == 16) return launch_attn_n<HD, 2, T>(p, s);
-  return launch_attn_n<HD, 1, T>(p, s);
 }
 
 template <int HD, typename T>
@@ -900,10 +866,7 @@ void reset_kv8_attn_caches() {
 bool kv8_attn_supported(int hd) { return hd == 32 || hd == 64 || hd == 128 || hd == 256; }
 
 // whether the weights of several row tiles are taken by a kernel of their own, from the row sums
-bool kv8_attn_weights_apart(int dt, int hd, int G, int n_q) {
-  const int64_t R = (int64_t)n_q * G;
-  return R > tile_rows(dt, hd, R);
-}
+bool kv8_attn_weights_apart(int G, int n_q) { return (int64_t)n_q * G > TILE; }
 
 namespace {
 size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -911,22 +874,22 @@ size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 struct WsOff {
   size_t part, lse, z, bytes;
 };
-WsOff ws_of(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
-  const size_t R = (size_t)n_q * G, rt = tile_rows(dt, hd, (int64_t)R), tiles = (R + rt - 1) / rt;
+WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+  const size_t R = (size_t)n_q * G, tiles = (R + TILE - 1) / TILE;
   WsOff w;
   w.part = up256(((size_t)n_seq * tiles + 1) * 4);
-  w.lse = w.part + up256(((size_t)n_seq * tiles * Hkv + MAX_WORKERS) * (std::min(rt, R) * hd + 2 * rt) * 4);
+  w.lse = w.part + up256(((size_t)n_seq * tiles * Hkv + MAX_WORKERS) * (std::min((size_t)TILE, R) * hd + 2 * TILE) * 4);
   w.z = w.lse + (weights ? up256((size_t)n_seq * Hkv * R * 4) : 0);
-  w.bytes = w.z + (weights && !kv8_attn_weights_apart(dt, hd, G, n_q) ? (size_t)n_seq * Hkv * R * cap * 4 : 0);
+  w.bytes = w.z + (weights && !kv8_attn_weights_apart(G, n_q) ? (size_t)n_seq * Hkv * R * cap * 4 : 0);
   return w;
 }
 }  // namespace
 
-size_t kv8_attn_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
-  return ws_of(dt, n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
+size_t kv8_attn_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+  return ws_of(n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
 }
 
-static Kv8Attn make_params(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
+static Kv8Attn make_params(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
                            int hd, void* out, float* weights, void* ws) {
   Kv8Attn p{};
   p.q = q;
@@ -940,16 +903,15 @@ static Kv8Attn make_params(int dt, const void* q, const int32_t* last, int n_q, 
   p.lg = 31 - __builtin_clz((unsigned)c.block);
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)hd);
   const int64_t R = (int64_t)n_q * p.G;
-  p.rt = tile_rows(dt, hd, R);
-  p.row_tiles = (int)((R + p.rt - 1) / p.rt);
-  const WsOff w = ws_of(dt, c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
+  p.row_tiles = (int)((R + TILE - 1) / TILE);
+  const WsOff w = ws_of(c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
   char* b = static_cast<char*>(ws);
   p.plan = reinterpret_cast<int32_t*>(b);
   p.part = reinterpret_cast<float*>(b + w.part);
   if (weights) {
     p.lse = reinterpret_cast<float*>(b + w.lse);
     p.weights = weights;
-    if (!kv8_attn_weights_apart(dt, hd, p.G, n_q)) p.z = reinterpret_cast<float*>(b + w.z);
+    if (!kv8_attn_weights_apart(p.G, n_q)) p.z = reinterpret_cast<float*>(b + w.z);
   }
   return p;
 }
@@ -965,13 +927,13 @@ static Kv8Attn make_params(int dt, const void* q, const int32_t* last, int n_q, 
 
 cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
                             int hd, void* out, float* weights, void* ws, cudaStream_t s) {
-  const Kv8Attn p = make_params(dt, q, last, n_q, c, H, Hkv, hd, out, weights, ws);
+  const Kv8Attn p = make_params(q, last, n_q, c, H, Hkv, hd, out, weights, ws);
   CB_KV8_DISPATCH(launch_attn_t)
 }
 
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
                                int Hkv, int hd, float* weights, void* ws, cudaStream_t s) {
-  const Kv8Attn p = make_params(dt, q, last, n_q, c, H, Hkv, hd, nullptr, weights, ws);
+  const Kv8Attn p = make_params(q, last, n_q, c, H, Hkv, hd, nullptr, weights, ws);
   CB_KV8_DISPATCH(launch_weights_t)
 }
 

@@ -913,10 +913,14 @@ void reset_kv8_tc_caches() {
   }
 }
 
-// Which launches take the tensor cores: bf16, head_dim 64 or 128, and enough query rows per KV
-// head.
-bool kv8_tc_taken(int dt, int hd, int G, int n_q) {
-  return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > 64 && (n_q + BM / G - 1) / (BM / G) <= 65535;
+// Which calls take this path: bf16, head_dim 64 or 128, and enough query rows per KV head.  Its
+// time hardly depends on the rows (up to a tile), the other's grows with every 8 of them.
+// 32 / 40 / 48 rows, hd 128, others' time and this one's: 32 heads over 4096 keys 38, 43, 50 and
+// 33 us; 8 over 16384 35, 42, 47 and 42 us; 8 sequences of 8 over 8192 77, 94, 108 and 103 us.  With
+// the weights, 16 / 24 rows: 47, 62 and 48 us; 48, 59 and 56 us; 114, 143 and 140 us.
+bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights) {
+  return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > (weights ? 16 : 40) &&
+         (n_q + BM / G - 1) / (BM / G) <= 65535;
 }
 
 namespace {
