@@ -273,6 +273,31 @@ def test_attention(B, H, hkv, hd, block, cap, n_seq, n_q, dtype, weigh):
         assert torch.equal(acc, w0 + w)
 
 
+@pytest.mark.parametrize("weigh", [False, True])
+@pytest.mark.parametrize("H,hkv,hd,n_q", [
+    (2, 2, 128, 8), (2, 2, 64, 9), (2, 2, 128, 16), (2, 2, 128, 17), (2, 1, 64, 20), (2, 2, 128, 40), (2, 2, 64, 41),
+    (2, 2, 128, 41), (8, 1, 128, 5), (16, 1, 64, 1), (17, 1, 128, 1), (40, 1, 128, 1), (41, 1, 64, 1), (128, 1, 128, 1),
+    (130, 1, 128, 1), (43, 1, 64, 3), (127, 1, 128, 2)])
+def test_attention_where_the_paths_meet(B, H, hkv, hd, n_q, weigh):
+    """Query rows per KV head around the counts at which another kernel takes over."""
+    torch = torch_mod()
+    g = np.random.default_rng(H + 1000 * n_q)
+    cap, n_seq = 272, 2
+    lens = [cap, 130]
+    d, o = filled(B, g, n_seq, hkv, cap, hd, 16, lens)
+    q = rounded(g.standard_normal((n_seq, n_q, H, hd)), "bf16")
+    last = np.stack([g.integers(-1, n, n_q) for n in lens])
+    last[:, -1] = [cap - 1, 127]
+    w = torch.zeros(n_seq, hkv, cap, device="cuda") if weigh else None
+    dims = make_dims(B, H, hkv, hd, "bf16")
+    out = attend(B, d, q, last, dims, "bf16", w)
+    B.cb_sync(None)
+    check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, "bf16", hd)
+    if weigh:       # what serves a call with the weights serves one without
+        n = B.cb_kv8_workspace_bytes(dims, n_seq, cap, n_q, True)
+        assert n >= B.cb_kv8_workspace_bytes(dims, n_seq, cap, n_q, False)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n_q", [1, 3, 130])
 def test_attention_of_unlike_blocks(B, dtype, n_q):
@@ -415,10 +440,35 @@ def test_evict(B, hkv, hd, block, cap, keep, sink, recent, kind):
     check_cache(t, rd, rl)
 
 
+@pytest.mark.parametrize("cap", [4096, 4112, 16384, 16400, 32768, 32784])
+def test_evict_where_the_kernels_meet(B, cap):
+    """Capacities around those at which a thread holds more keys, or none."""
+    torch = torch_mod()
+    g = np.random.default_rng(cap)
+    hkv, hd, block, keep, sink, recent = 2, 32, 16, 1500, 5, 333
+    lens = [cap, cap - 7, keep + 1]
+    d, o = filled(B, g, 3, hkv, cap, hd, block, lens)
+    w = (g.uniform(0, 1, (3, hkv, cap)) ** 6).astype(np.float32)
+    w[0, 1] = g.integers(0, 3, cap)                     # ties across threads and warps
+    w[1, 0] = 0
+    t = Dev(B, 3, hkv, 1504, hd, block)
+    dl = torch.zeros(3, dtype=torch.int32, device="cuda")
+    dw = torch.full((3, hkv, 1504), 3.0, device="cuda")
+    kept = torch.zeros(3, hkv, keep, dtype=torch.int32, device="cuda")
+    B.cb_kv8_evict(d.c, dev_i32(lens), torch.from_numpy(w).cuda(), keep, sink, recent, t.c, dl, dw, kept,
+                   make_dims(B, hkv, hkv, hd, "bf16"))
+    B.cb_sync(None)
+    rd, rl, rw, rk = K8.evict(o, lens, w, keep, sink, recent, 1504)
+    np.testing.assert_array_equal(kept.cpu().numpy(), rk)
+    np.testing.assert_array_equal(dl.cpu().numpy(), rl)
+    np.testing.assert_array_equal(dw.cpu().numpy(), rw)
+    check_cache(t, rd, rl)
+
+
 def test_evict_of_a_long_cache_and_bad_weights(B):
     torch = torch_mod()
     g = np.random.default_rng(12)
-    hkv, hd, block, cap, keep = 2, 32, 128, 66560, 9000          # past the keys that fit in shared memory
+    hkv, hd, block, cap, keep = 2, 32, 128, 66560, 9000          # past the keys that threads hold
     d, o = filled(B, g, 1, hkv, cap, hd, block, [cap - 3])
     w = (g.uniform(0, 1, (1, hkv, cap)) ** 4).astype(np.float32)
     w[0, 1] = g.integers(0, 9, cap) / 8.0
@@ -612,3 +662,165 @@ def test_captured_graphs_streams_and_a_shared_workspace(B):
     for d, b in pairs:
         assert torch.equal(d.k, d0.k) and torch.equal(d.v, d0.v)
         assert torch.equal(b["out"], b0["out"]) and torch.equal(b["w"], b0["w"]) and torch.equal(b["start"], b0["start"])
+
+
+class Answer:
+    """One request over 8-bit caches: the prompt's rows, then a token per step, all lengths and
+    positions on the device; the caches are thinned out in between.  see(cache, layer, q, k, v,
+    out, weights before) is called after each attention, said() after each token."""
+    KEEP, SINK, RECENT, T = 40, 4, 12, 128
+
+    def __init__(self, B, shape, prompt):
+        from non_prefix_kv_gb300 import engine, synth
+        torch = torch_mod()
+        self.B, self.L, self.s = B, shape.n_layers, shape
+        self.dm = engine.DeviceModel.from_host(synth.make_model(shape, seed=3))
+        self.eng = engine.BlendEngine(self.dm, len(prompt), max_pos=256)
+        self.prompt = dev_i32(prompt)
+        n, hkv, hd, dt = len(prompt), shape.n_kv_heads, shape.head_dim, tdt(shape.dtype)
+        self.caches = [[Dev(B, 1, hkv, cap, hd, 16) for _ in range(self.L)] for cap in (96, 64)]
+        self.acc = [[torch.zeros(1, hkv, cap, device="cuda") for _ in range(self.L)] for cap in (96, 64)]
+        self.len = [torch.full((1,), m, dtype=torch.int32, device="cuda") for m in (n, 0)]
+        self.kept = torch.empty(1, hkv, self.KEEP, dtype=torch.int32, device="cuda")
+        self.pos, self.tok = dev_i32([n]), dev_i32([0])
+        self.hist, self.hl = dev_i32(np.pad(prompt, (0, self.T - n))[None]), dev_i32([n])
+        mask = np.ones((1, shape.vocab), bool)
+        mask[0, ::5] = False
+        self.rules = B.logit_rules(history=self.hist, history_len=self.hl, prompt_len=dev_i32([n]),
+                                   repetition=dev(np.array([1.3], np.float32)), presence=dev(np.array([0.4], np.float32)),
+                                   frequency=dev(np.array([0.2], np.float32)), bias_id=dev_i32([[7, 11, 7]]),
+                                   bias=dev(np.array([[0.5, -1.0, 0.25]], np.float32)), mask=mask_words(mask))
+        self.mask = mask[0]
+        size = max(B.cb_kv8_workspace_bytes(self.dm.dims, 1, 96, m, True) for m in (1, n))
+        self.ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+        row = lambda w, m=1: torch.empty(m, w, dtype=dt, device="cuda")  # noqa: E731
+        self.bufs = {m: [row(shape.d_model, m), row(shape.q_width, m), row(shape.kv_width, m), row(shape.kv_width, m),
+                         row(shape.q_width, m)] for m in (1, n)}
+        self.logits = torch.empty(1, shape.vocab, device="cuda")
+        self.out = torch.empty_like(self.logits)
+        self.see = self.said = lambda *a: None
+
+    def rows(self, m, tokens, pos, start, last, which):
+        """m rows through the layers; their hidden rows are bufs[m][0]."""
+        B, dm, e, s = self.B, self.dm, self.eng, self.s
+        x, q, k, v, o = self.bufs[m]
+        B.cb_gather_rows(x, dm.embed, tokens, m, s.d_model * x.element_size())
+        for l in range(self.L):
+            before = self.acc[which][l].clone()
+            B.cb_selective_qkv(x, None, pos, m, dm.dims, dm.layers_c[l], e.cos_sin, e.max_pos, q, k, v, e.ws)
+            B.cb_kv8_append(k, v, m, start, None, self.caches[which][l].c, dm.dims)
+            B.cb_kv8_attention(q, last, m, self.caches[which][l].c, dm.dims, o, self.acc[which][l], self.ws)
+            self.see(which, l, q, k, v, o, before)
+            B.cb_o_proj_ffn(o, x, m, dm.dims, dm.layers_c[l], x, e.ws)
+
+    def token(self, m):
+        B, dm = self.B, self.dm
+        B.cb_lmhead_argmax(self.bufs[m][0][m - 1], dm.final_norm, dm.w_lm, dm.dims, self.logits, self.tok, self.eng.ws)
+        B.cb_logits_process(self.logits, self.rules, self.out, self.tok)
+        self.said()
+        self.hist.scatter_(1, self.hl.long()[None], self.tok[None])
+        self.hl += 1
+
+    def prefill(self):
+        n = len(self.prompt)
+        last = torch_mod().arange(n, dtype=torch_mod().int32, device="cuda")
+        self.rows(n, self.prompt, last, dev_i32([0]), last, 0)
+        self.token(n)
+
+    def step(self, which):
+        self.rows(1, self.tok, self.pos, self.len[which], self.len[which], which)
+        self.token(1)
+        self.pos += 1
+        self.len[which] += 1
+
+    def thin(self):
+        for l in range(self.L):
+            self.B.cb_kv8_evict(self.caches[0][l].c, self.len[0], self.acc[0][l], self.KEEP, self.SINK, self.RECENT,
+                                self.caches[1][l].c, self.len[1], self.acc[1][l], self.kept, self.dm.dims)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_answer_from_its_prompt_to_its_last_token(B, dtype):
+    """The operators as they are used: a prompt's rows appended and attended (their weights
+    accounted), eight tokens one by one, the caches thinned out, eight more.  Every operator's
+    result is checked against the oracle's from the same inputs; then the same answer with each
+    token's step captured once and replayed gives the same bits."""
+    from non_prefix_kv_gb300 import synth
+    torch = torch_mod()
+    shape = synth.ModelShape(n_layers=2, d_model=512, n_heads=8, n_kv_heads=2, head_dim=64, d_ff=1024, vocab=512,
+                             dtype=dtype, w_std=0.05)
+    prompt = np.random.default_rng(40).integers(0, shape.vocab, 60).astype(np.int32)
+    hkv, hd, H = shape.n_kv_heads, shape.head_dim, shape.n_heads
+
+    a = Answer(B, shape, prompt)
+    twins = [[K8.empty(1, hkv, cap, hd, 16) for _ in range(a.L)] for cap in (96, 64)]
+    used = [0]
+
+    def see(which, l, q, k, v, o, before):
+        m = q.shape[0]
+        n0 = used[0]
+        kv = lambda t: host(t).reshape(1, m, hkv, hd).astype(np.float32)  # noqa: E731
+        K8.append(twins[which][l], kv(k), kv(v), [n0])
+        last = np.arange(n0, n0 + m)[None]
+        ref = K8.attention(twins[which][l], host(q).reshape(1, m, H, hd), last)
+        after = a.acc[which][l]
+        check_attention(o.view(1, m, H, hd), None, ref, last, dtype, hd)
+        # the account: the oracle's weights with the relative error of a weight (above), and one
+        # rounding of the sum
+        w, zmag = ref[1], ref[3]
+        rel = (2 * (zmag.max() * ((hd + 4) * 2.0 ** -24 + (2.0 ** -21 if dtype == "f32" else 0)) + 2.0 ** -21)
+               + (n0 + m) * 2.0 ** -24 + (m * H + 8) * 2.0 ** -24)
+        assert np.all(np.abs(host(after) - (host(before) + w)) <= w * rel + host(after) * 2.0 ** -23 + 1e-30)
+        if l == a.L - 1:
+            used[0] += m
+
+    def said():
+        h = a.hist[0, :int(a.hl[0])].cpu().numpy()
+        ref = K8.logits(host(a.logits)[0], h, len(prompt), float(np.float32(1.3)), float(np.float32(0.4)),
+                        float(np.float32(0.2)), [(7, 0.5), (11, -1.0), (7, 0.25)], a.mask)
+        got, fin = host(a.out)[0], np.isfinite(ref)
+        np.testing.assert_array_equal(np.isneginf(got), ~fin)
+        # at most 8 roundings of the largest magnitude met
+        size = 2 * np.abs(host(a.logits)[0]) + 0.2 * len(h) + 0.4 + 1.75
+        assert np.all(np.abs(got[fin] - ref[fin]) <= 8 * 2.0 ** -24 * size[fin])
+        assert int(a.tok[0]) == K8.token(got)
+
+    a.see, a.said = see, said
+    a.prefill()
+    for _ in range(8):
+        a.step(0)
+    a.thin()
+    B.cb_sync(None)
+    for l in range(a.L):
+        check_cache(a.caches[0][l], twins[0][l], [used[0]])
+        twins[1][l], dl, dw, _ = K8.evict(twins[0][l], [used[0]], a.acc[0][l].cpu().numpy(), a.KEEP, a.SINK, a.RECENT, 64)
+        check_cache(a.caches[1][l], twins[1][l], dl)
+        np.testing.assert_array_equal(a.acc[1][l].cpu().numpy(), dw)
+    used[0] = a.KEEP
+    for _ in range(8):
+        a.step(1)
+    B.cb_sync(None)
+    for l in range(a.L):
+        check_cache(a.caches[1][l], twins[1][l], [a.KEEP + 8])
+
+    b = Answer(B, shape, prompt)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b.prefill()
+        for which in (0, 1):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                b.step(which)
+            for _ in range(8):
+                g.replay()
+            if which == 0:
+                b.thin()
+    torch.cuda.current_stream().wait_stream(s)
+    B.cb_sync(None)
+    assert torch.equal(a.hist, b.hist) and torch.equal(a.hl, b.hl) and torch.equal(a.pos, b.pos)
+    for which in (0, 1):
+        for l in range(a.L):
+            x, y = a.caches[which][l], b.caches[which][l]
+            assert torch.equal(x.k, y.k) and torch.equal(x.v, y.v)
+            assert torch.equal(a.acc[which][l], b.acc[which][l])
