@@ -151,7 +151,9 @@ __device__ __forceinline__ int row_last(const Kv8Attn& p, int e, int r, bool rep
 // units follow one another by entry, then head, and the line is cut into equal runs, one per
 // worker (a warp).  A run may end inside a unit and hold several; each (worker, unit) pair
 // leaves one partial result.  Along the line either the worker or the unit goes up at every
-// new pair, so worker + unit numbers the pairs' slots without a gap wider than one.
+// new pair, so worker + unit numbers the pairs' slots without a gap wider than one.  A run has two
+// steps at least (a token of 32 heads over 512 / 2048 rows: 11.8 and 13.1 us; with one step 11.0 and
+// 14.0, with four 12.1 and 13.8, with eight 15.0 and 17.3).
 __device__ __forceinline__ int workers_of(int total, int workers) { return max(1, min(workers, total / 2)); }
 __device__ __forceinline__ float* slot(const Kv8Attn& p, int hd, int worker, int unit) {
   const int rows = min(TILE, p.n_q * p.G);
@@ -168,7 +170,11 @@ __device__ __forceinline__ float* slot(const Kv8Attn& p, int hd, int worker, int
 // The products are taken transposed, S^T = C_K Q^T and O^T = C_V^T P^T, with the keys (then the
 // channels) as the 16 rows of mma.m16n8k16 and the query rows as its 8 columns: the few rows of
 // a token fill the instruction, and a thread's share of O is HD / 4 registers, so that 16
-// warps fit on an SM.  (With rows as M and 10 warps: 205 us at an issue rate of 0.33.)
+// warps fit on an SM.  (With rows as M and 10 warps: 205 us at an issue rate of 0.33; with two row
+// tiles per instruction stream where there are more than 8 rows, 32 rows of 32 heads over 4096
+// keys 48 us instead of 38.)  Now 144 us for the 841 MB, 5.85 TB/s, merge included; bound by the
+// bytes and, at a busy issue slot in two cycles, by the conversion of the codes.  One token of 32
+// heads over 4096 rows (34 MB): 11.5 us and 5 more for the merge, bound by start and latency.
 template <int HD, typename T>
 __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(const Kv8Attn p) {
   pdl_wait();
@@ -639,7 +645,8 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p,
   }
 }
 
-// weights[key] += sum over the rows of 2^(z - log2 of the row's sum); four keys per thread
+// weights[key] += sum over the rows of 2^(z - log2 of the row's sum); four keys per thread.  Bound
+// by latency after a merge (8 sequences of 40 heads over 8192 rows: 12 us with the wait for it).
 __global__ void __launch_bounds__(256) k_kv8_account(const Kv8Attn p) {
   pdl_wait();
   pdl_trigger();

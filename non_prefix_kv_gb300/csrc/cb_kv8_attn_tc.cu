@@ -108,7 +108,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool swap) {
 }
 
 // One CTA per (key tile, KV head, sequence): 128 rows of K and V codes to bf16 / fp16 in
-// 128-byte-swizzled slabs.  Tiles no query sees are skipped.
+// 128-byte-swizzled slabs.  Tiles no query sees are skipped.  Bound by latency and L2 (34 MB of
+// codes read, 67 MB written that the next kernel reads from L2): 15 us for 8 heads of 16384 rows,
+// 19 us with 16-byte stores.
 template <int HD>
 __global__ void __launch_bounds__(256) k_kv8_expand(const Kv8Tc p) {
   pdl_wait();
@@ -287,8 +289,12 @@ __device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, co
 // fills the gaps, and the eight warps (two per scheduler) may hold a row's 128 scores in
 // registers and read them once.  K's buffer is refilled as soon as S is there, V's once P V is
 // done: each load has most of a tile's chain to arrive, so one buffer per group suffices.
-// Measured (3328 rows of 56 heads over 16384 rows of 8, 973 GFLOP): with a copying and an
-// issuing warp, a ring of five tiles and the scores read twice for want of registers, 1045 us.
+// Measured (3328 rows of 56 heads over 16384 rows of 8, 973 GFLOP): 813 us, 1.20 PFLOP/s, bound
+// by the loop's hand-overs and products (without any softmax 698 us).  With a copying and an
+// issuing warp, a ring of five tiles and the scores read twice for want of registers 1023 us; with
+// one accumulator, S two tiles ahead and the maximum handed on from tile to tile 883 us; with half
+// tiles and two score buffers per group 949 us; with two query tiles per CTA on shared key tiles
+// 879 us.
 template <int HD>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n_split) {
   pdl_wait();
@@ -595,10 +601,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
 // thread.  A resident CTA takes pairs of key tiles (of one KV head and sequence), one per
 // softmax group, and streams the query tiles that see them past both: a query tile is loaded
 // once for 256 keys, each group has two S buffers (TMEM 4 x 128 columns), and no sums have to
-// meet.  Warp roles: 0 = copies,
-// 1 = TMEM allocation and MMA issue, 2..9 = softmax.
-// Measured: 64 queries of 7 heads over 16384 rows of 8 KV heads, one CTA per key tile gathering
-// the queries itself 55 us (15 instructions per weight, and the start of 1024 CTAs).
+// meet.  Warp roles: 0 = copies, 1 = TMEM allocation and MMA issue, 2..9 = softmax.
+// Measured: 64 queries of 7 heads over 16384 rows of 8 KV heads (58.7 M weights) 21 us, bound by
+// the exponentials' chain from TMEM (33% of the issue slots, 32% of the special functions' rate);
+// one CTA per key tile gathering the queries itself 55 us.
 template <int HD>
 struct WLayout {
   static constexpr int T_BYTES = HD / 64 * SLAB;
@@ -877,7 +883,9 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (e = prepare_tc<HD>(dev, &sms)) != cudaSuccess) return e;
   if ((e = launch_k(k_kv8_expand<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
-  // one CTA per SM: the keys are split while that gives more of them work
+  // one CTA per SM: the keys are split while that gives more of them work (64 queries of 8 x 7
+  // heads over 16384 keys, 32 units, in 1 / 2 / 4 / 8 parts: 170, 102, 62, 94 us; 100 queries of 32
+  // heads over 4096: 58, 45, 34, 55 us)
   const int64_t units = (int64_t)p.q_tiles * p.Hkv * p.c.n_seq;
   int ns = 1;
   while (ns < 8 && units * ns * 2 <= sms && 2 * ns <= p.tiles) ns *= 2;
