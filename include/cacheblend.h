@@ -252,7 +252,8 @@ int cb_kv8_append(const void* k, const void* v, int32_t n_rows, const int32_t* s
 int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* count,
                 int32_t n_rows, const cb_dims* dims, void* k_out, void* v_out, void* stream);
 
-/* Device workspace (bytes) of cb_kv8_attention at these sizes.  Host-only. */
+/* Device workspace (bytes) of cb_kv8_attention at these sizes (16-byte aligned; what serves a
+ * call with the weights serves one without).  Host-only. */
 int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q,
                            int32_t with_weights, size_t* out_host);
 
@@ -260,15 +261,17 @@ int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity,
  * for the selected rows of a blend:
  *   out[s, j, h] = sum_{i <= last[s, j]} p_i v[i],  p = softmax_i(q[s, j, h] . k[i] / sqrt(hd)),
  * k, v of KV head h / (H / Hkv).
- *   q, out : [n_seq, n_q, H hd] of dims->dtype
+ *   q, out : [n_seq, n_q, H hd] of dims->dtype, apart from one another
  *   last   : [n_seq, n_q] int32, the last cache row each query sees (a token appended at row
  *            r sees itself: last = r); -1: none, its output row is 0 (padding).  A value
  *            outside [-1, capacity) is reported by cb_sync and counts as -1.
  *   weights: [n_seq, Hkv, capacity] fp32 or NULL; every row's entry grows by the sum of its p
  *            over the sequence's queries and the query heads of its KV head (the account that
  *            cb_kv8_evict goes by).  Rows no query sees are left as they were.
+ *            A query with a NaN makes its own output and the entries of the rows it sees NaN.
  * Queries need no order, but launches of many queries run faster when last ascends.
- * The results are the same from run to run (no floating-point atomics).
+ * The results are the same from run to run (no floating-point atomics).  Calls that use one
+ * workspace or add to the same weights must be ordered by their stream.
  * head_dim 32, 64, 128 or 256. */
 int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_kv8_cache* cache,
                      const cb_dims* dims, void* out, float* weights, void* ws, size_t ws_bytes,

@@ -1260,7 +1260,10 @@ int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity,
                            size_t* out_host) {
   int st = check_dims(dims);
   if (st) return st;
-  if (!out_host || n_seq < 1 || capacity < 1 || n_q < 0) return fail(CB_ERR_INVALID_ARG, "workspace query arguments");
+  if (!out_host || n_seq < 1 || n_seq > 65535 || capacity < 1 || capacity > (1 << 30) || n_q < 0)
+    return fail(CB_ERR_INVALID_ARG, "workspace query arguments");
+  if ((int64_t)n_q * (dims->n_heads / dims->n_kv_heads) > (1 << 27))
+    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
   // what serves a call with the weights serves one without
   *out_host = kv8_ws(dims, n_seq, capacity, n_q, false);
   if (with_weights) *out_host = std::max(*out_host, kv8_ws(dims, n_seq, capacity, n_q, true));
@@ -1279,12 +1282,16 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   if ((int64_t)n_q * G > (1 << 27)) return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
   // the line of work (row tile, sequence, head, 16 keys) and the rows to join are counted in 32 bits
   if ((double)(((int64_t)n_q * G + 7) / 8) * cache->n_seq * Hkv * std::max((double)cache->capacity / 16, 8.0) >
-      (double)INT32_MAX)
+      (double)(INT32_MAX - 65536))
     return fail(CB_ERR_UNSUPPORTED, "kv8_attention: query rows, sequences, heads and capacity too many for one call");
   if (!q || !last || !out) return fail(CB_ERR_INVALID_ARG, "kv8_attention pointer is NULL");
   if ((st = check_al16({q, out, weights, ws}, "kv8_attention"))) return st;
   const size_t need = kv8_ws(dims, cache->n_seq, cache->capacity, n_q, weights != nullptr);
   if (need && (!ws || ws_bytes < need)) return fail(CB_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
+  const size_t bytes = (size_t)cache->n_seq * n_q * H * hd * esize(dims->dtype);
+  if (static_cast<const char*>(q) < static_cast<char*>(out) + bytes &&
+      static_cast<char*>(out) < static_cast<const char*>(q) + bytes)
+    return fail(CB_ERR_INVALID_ARG, "kv8_attention: out overlaps q");
   const int64_t m = (int64_t)cache->n_seq * n_q;
   if (kv8_tc_taken(dims->dtype, hd, G, n_q, weights != nullptr)) {
     CB_LAUNCH(CB_PROF_KV8_ATTN, 2, m, cache->capacity, H, 0.0, 0.0, S(stream),

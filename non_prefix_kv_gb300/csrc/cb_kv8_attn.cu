@@ -662,10 +662,10 @@ __global__ void __launch_bounds__(256) k_kv8_account(const Kv8Attn p) {
   for (int r = 0; r < R; ++r) {
     const float4 v = *reinterpret_cast<const float4*>(z + r * cap);     // an unseen key's z is -inf
     const float l = lse[r];
-    a[0] += tc::ex2_approx(v.x - l);
-    a[1] += tc::ex2_approx(v.y - l);
-    a[2] += tc::ex2_approx(v.z - l);
-    a[3] += tc::ex2_approx(v.w - l);
+    a[0] += v.x == -INFINITY ? 0.f : tc::ex2_approx(v.x - l);           // (l of a NaN query is NaN)
+    a[1] += v.y == -INFINITY ? 0.f : tc::ex2_approx(v.y - l);
+    a[2] += v.z == -INFINITY ? 0.f : tc::ex2_approx(v.z - l);
+    a[3] += v.w == -INFINITY ? 0.f : tc::ex2_approx(v.w - l);
   }
   float* w = p.weights + head * cap + key;
 #pragma unroll

@@ -512,10 +512,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
     const float inv = lt > 0.f ? 1.0f / lt : 0.f;
     if (grp == 0) {
       if (n_split > 1) {
-        cm[r] = mm;
+        cm[r] = isnan(lt) ? lt : mm;       // (a NaN's scores leave no maximum; the row is not to look empty)
         cm[BM + r] = lt;
       } else if (p.weights) {
-        p.rows[qt * 2 * BM + r] = lt > 0.f ? mm - kPBias + log2f(lt) : INFINITY;
+        p.rows[qt * 2 * BM + r] = lt == 0.f ? INFINITY : mm - kPBias + log2f(lt);
       }
       if (p.weights && rank == 0) p.rows[qt * 2 * BM + BM + r] = __int_as_float(last);
     }
@@ -949,8 +949,9 @@ WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weight
 }
 }  // namespace
 
+// (the operands are written in 32-byte words: room to start on a boundary of those)
 size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
-  return ws_of(n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
+  return ws_of(n_seq, Hkv, G, n_q, cap, hd, weights).bytes + 32;
 }
 
 cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
@@ -971,7 +972,7 @@ cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_
   p.q_tiles = (n_q + p.qpt - 1) / p.qpt;
   p.g_magic = ((1 << 16) + p.G - 1) / p.G;
   const WsOff w = ws_of(c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
-  uint8_t* b = static_cast<uint8_t*>(ws);
+  uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
   p.kx = b;
   p.vx = b + w.vx;
   p.seq_max = reinterpret_cast<int32_t*>(b + w.seq_max);

@@ -348,6 +348,53 @@ def test_attention_is_the_same_from_run_to_run_and_per_sequence(B):
         assert torch.all(a[torch.from_numpy(last < 0).cuda()] == 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n_q", [1, 4, 11, 60])
+def test_a_query_with_a_nan_spoils_only_its_own_rows(B, n_q, dtype):
+    torch = torch_mod()
+    g = np.random.default_rng(n_q)
+    H, hkv, hd, cap, n_seq = 4, 2, 64, 288, 2
+    d, o = filled(B, g, n_seq, hkv, cap, hd, 32, [cap, cap])
+    q = rounded(g.standard_normal((n_seq, n_q, H, hd)), dtype)
+    last = g.integers(100, cap, (n_seq, n_q))
+    last[0, 0] = 90
+    bad = q.copy()
+    bad[0, 0, 3, 17] = np.nan                       # head 3: KV head 1
+    w = torch.zeros(n_seq, hkv, cap, device="cuda")
+    dims = make_dims(B, H, hkv, hd, dtype)
+    out = attend(B, d, bad, last, dims, dtype, w)
+    B.cb_sync(None)
+    assert torch.all(torch.isnan(out[0, 0, 3])) and torch.all(torch.isnan(w[0, 1, :91]))
+    out[0, 0, 3] = 0
+    w[0, 1, :91] = 0
+    q[0, 0, 3] = 0
+    ref = list(K8.attention(o, q.astype(np.float64), last))
+    ref[0][0, 0, 3] = 0
+    ref[1][0, 1, :91] = 0
+    check_attention(out, host(w), ref, last, dtype, hd)
+
+
+@pytest.mark.parametrize("n_q", [1, 20, 70])
+def test_attention_with_a_workspace_off_any_wider_boundary(B, n_q):
+    """The header asks for 16 bytes."""
+    torch = torch_mod()
+    g = np.random.default_rng(n_q)
+    H, hkv, hd, cap = 2, 2, 128, 160
+    d, o = filled(B, g, 1, hkv, cap, hd, 16, [cap])
+    q = rounded(g.standard_normal((1, n_q, H, hd)), "bf16")
+    last = g.integers(0, cap, (1, n_q))
+    dims = make_dims(B, H, hkv, hd, "bf16")
+    n = B.cb_kv8_workspace_bytes(dims, 1, cap, n_q, True)
+    whole = torch.full((n + 256,), 77, dtype=torch.uint8, device="cuda")
+    off = -whole.data_ptr() % 256 + 16 if whole.data_ptr() % 256 else 16
+    w, qd = torch.zeros(1, hkv, cap, device="cuda"), dev(q, "bf16")
+    out = torch.empty_like(qd)
+    B.cb_kv8_attention(qd, dev_i32(last), n_q, d.c, dims, out, w, whole[off:off + n])
+    B.cb_sync(None)
+    check_attention(out, host(w), K8.attention(o, q.astype(np.float64), last), last, "bf16", hd)
+    assert torch.all(whole[:off] == 77) and torch.all(whole[off + n:] == 77)
+
+
 def test_attention_reports_a_row_past_the_capacity(B):
     torch = torch_mod()
     g = np.random.default_rng(10)

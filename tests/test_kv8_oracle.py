@@ -148,6 +148,18 @@ def test_kv8_calls_refuse_bad_arguments(lib):
         B.cb_kv8_workspace_bytes(d, 0, 256, 1, True)
 
 
+def test_attention_refuses_an_output_over_its_queries_and_sizes_past_the_counters(lib):
+    d, c, r = _dims(), _cache(), ctypes.byref
+    need = B.cb_kv8_workspace_bytes(d, 2, 256, 4, True)
+    row = 2 * 4 * d.n_heads * d.head_dim * 2
+    for out in (FAKE, FAKE + 16, FAKE + row - 16, FAKE - row + 16):          # two sequences of 4 bf16 rows
+        assert lib.cb_kv8_attention(FAKE, FAKE, 4, r(c), r(d), out, None, FAKE, need, None) == 1
+        assert b"overlaps" in lib.cb_last_error_message()
+    for args in ((65536, 256, 1), (1, (1 << 30) + 1, 1), (1, 256, (1 << 31) - 1)):
+        with pytest.raises(B.CBError):
+            B.cb_kv8_workspace_bytes(d, *args)
+
+
 def test_evict_refuses_bad_arguments(lib):
     d, r = _dims(), ctypes.byref
     src = _cache()
