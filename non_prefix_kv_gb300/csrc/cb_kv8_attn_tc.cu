@@ -205,17 +205,21 @@ __device__ __forceinline__ void gather_q(const Kv8Tc& p, int s, int h, int j0, u
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ---- attention ------------------------------------------------------------------------------
-template <int HD>
+template <int HD, bool FUSED>
 struct Layout {
   static constexpr int T_BYTES = HD / 64 * SLAB;             // a tile of Q, K or V
+  static constexpr int C_BYTES = FUSED ? BN * HD : 0;        // a tile of codes
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = T_BYTES;                      // [2 groups]
   static constexpr int OFF_V = OFF_K + 2 * T_BYTES;          // [2]
-  static constexpr int OFF_X = OFF_V + 2 * T_BYTES;          // [2 groups][2][BM] row max, row sum
+  static constexpr int OFF_C = OFF_V + 2 * T_BYTES;          // [2 groups][K, V] codes; the row statistics come there
+                                                             // after the last ones are used up
+  static constexpr int OFF_X = OFF_C;                        // [2 groups][2][BM] row max, row sum
   static constexpr int OFF_ML = OFF_X + 4 * BM * 4;          // [2][BM] the CTA's row max and sum, read by the cluster
-  static constexpr int OFF_SC = OFF_ML + 2 * BM * 4;         // [NSOFT][NG] float4 {ks, log2 vs, 1/vs, -}
+  static constexpr int OFF_SC = FUSED ? OFF_C + 4 * C_BYTES : OFF_ML + 2 * BM * 4;   // [NSOFT][NG] float4 {ks, log2 vs, 1/vs, -}
   static constexpr int OFF_BAR = OFF_SC + NSOFT * NG * 16;
   static constexpr int SMEM = OFF_BAR + 128 + 1024;
+  static_assert(OFF_ML + 2 * BM * 4 <= OFF_SC, "the row statistics exceed the codes");
   static_assert(BM * HD * 4 <= 4 * T_BYTES, "the merge buffer exceeds K and V");
   static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
 };
@@ -234,6 +238,35 @@ __device__ __forceinline__ Scales load_scales(const float* ks, const float* vs, 
     r.v = vs[key >> lg];
   }
   return r;
+}
+
+// A tile's codes as an operand tile, by a group's 128 threads: 16 codes at a time, read in order,
+// to two 16-byte words of the swizzled row (the second slab's lanes write theirs the other way
+// round, so that eight lanes meet all banks).
+template <int HD, bool IS_V>
+__device__ __forceinline__ void convert_tile(const uint8_t* codes, uint8_t* dst, int t) {
+  constexpr int PER = HD / 16;
+#pragma unroll 4
+  for (int i = 0; i < PER; ++i) {
+    const int idx = i * 128 + t, row = idx / PER, piece = idx % PER;
+    const uint4 u = *reinterpret_cast<const uint4*>(codes + idx * 16);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint4 o[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      if (IS_V) {
+        const uint32_t u0 = w[2 * c] ^ 0x80808080u, u1 = w[2 * c + 1] ^ 0x80808080u;
+        o[c] = make_uint4(pair_f16(u0, 0x4140), pair_f16(u0, 0x4342), pair_f16(u1, 0x4140), pair_f16(u1, 0x4342));
+      } else {
+        o[c] = make_uint4(pair_bf16(w[2 * c], 0x4140), pair_bf16(w[2 * c], 0x4342), pair_bf16(w[2 * c + 1], 0x4140),
+                          pair_bf16(w[2 * c + 1], 0x4342));
+      }
+    }
+    uint8_t* d = dst + (piece >> 2) * SLAB + row * 128;
+    const int at = 2 * (piece & 3), sw = row & 7, first = (piece >> 2) & 1;
+    *reinterpret_cast<uint4*>(d + (((at + first) ^ sw) * 16)) = first ? o[1] : o[0];
+    *reinterpret_cast<uint4*>(d + (((at + (first ^ 1)) ^ sw) * 16)) = first ? o[0] : o[1];
+  }
 }
 
 // The largest t of a row's 128 scores.
@@ -295,11 +328,18 @@ __device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, co
 // one accumulator, S two tiles ahead and the maximum handed on from tile to tile 883 us; with half
 // tiles and two score buffers per group 949 us; with two query tiles per CTA on shared key tiles
 // 879 us.
-template <int HD>
+//
+// FUSED: the operands do not come ready from k_kv8_expand; the group that uses a tile converts it
+// itself, K while P V of the tile before runs, V while S runs.  That lengthens the loop by a half,
+// but where only one query tile reads the keys it saves writing and reading four bytes per code:
+// 85 rows of 40 heads over 6 x 16064 keys (987 MB of codes) 400 us instead of 651, 118 of 32 heads
+// over 1664 keys 16.5 instead of 21; with three query tiles (299 rows, 32 heads, 13440 keys) 182
+// instead of 163.
+template <int HD, bool FUSED>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n_split) {
   pdl_wait();
   pdl_trigger();
-  using L = Layout<HD>;
+  using L = Layout<HD, FUSED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sQ = base + L::OFF_Q;
@@ -307,14 +347,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
   float* xl = xm + 2 * BM;
   float* cm = reinterpret_cast<float*>(base + L::OFF_ML);  // [BM] max, [BM] sum
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-  uint64_t* k_full = bars + 4 * grp;       // a group's barriers: K and V have landed, S and P V are done
+  uint64_t* k_full = bars + 5 * grp;       // a group's barriers: K and V have landed, S and P V are done,
   uint64_t* v_full = k_full + 1;
   uint64_t* s_full = k_full + 2;
   uint64_t* pv_done = k_full + 3;
+  uint64_t* v_empty = k_full + 4;          // the four warps have read V's codes
   const int rank = blockIdx.x % n_split, h = blockIdx.x / n_split, s = blockIdx.z;
   // tiles are cut from the end of the queries: the longest rows come first, and the tile that
   // is cut short is the one with the lowest positions
@@ -322,7 +363,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
   const int64_t head = (int64_t)s * p.Hkv + h;
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) tc::mbar_init(&bars[i], 1);
+    for (int i = 0; i < 10; ++i) tc::mbar_init(&bars[i], i % 5 == 4 ? 4 : 1);
     tc::fence_mbar_init();
   }
   if (warp == 0) {
@@ -373,23 +414,33 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
   bool ok = true;                  // of this warp; one that gave up goes on meeting its group
   {
     const bool issuer = quad == 0;
-    const uint8_t* kx = p.kx + (head * p.tiles + ta + grp) * (int64_t)L::T_BYTES;
-    const uint8_t* vx = p.vx + (head * p.tiles + ta + grp) * (int64_t)L::T_BYTES;
     uint8_t* sK = base + L::OFF_K + grp * L::T_BYTES;
     uint8_t* sV = base + L::OFF_V + grp * L::T_BYTES;
+    uint8_t* cK = base + L::OFF_C + grp * 2 * L::C_BYTES;
+    uint8_t* cV = cK + L::C_BYTES;
     int nk_loads = 0, nv_loads = 0;
+    auto load = [&](const uint8_t* tiles, const int8_t* codes, uint8_t* dst, uint8_t* cdst, uint64_t* bar, int u) {
+      if (lane != 0) return;
+      const int tile = ta + grp + 2 * u;
+      if constexpr (FUSED) {
+        const int64_t key = (int64_t)tile * BN;
+        const uint32_t bytes = (uint32_t)(p.c.capacity - key < BN ? p.c.capacity - key : BN) * HD;
+        tc::mbar_expect_tx(bar, bytes);
+        tc::bulk_load(cdst, codes + (head * p.c.capacity + key) * HD, bytes, bar);
+      } else {
+        tc::mbar_expect_tx(bar, L::T_BYTES);
+        tc::bulk_load(dst, tiles + (head * p.tiles + tile) * (int64_t)L::T_BYTES, L::T_BYTES, bar);
+      }
+    };
     auto load_k = [&](int u) {
       ++nk_loads;
-      if (lane != 0) return;
-      tc::mbar_expect_tx(k_full, L::T_BYTES);
-      tc::bulk_load(sK, kx + (int64_t)(2 * u) * L::T_BYTES, L::T_BYTES, k_full);
+      load(p.kx, p.c.k_codes, sK, cK, k_full, u);
     };
     auto load_v = [&](int u) {
       ++nv_loads;
-      if (lane != 0) return;
-      tc::mbar_expect_tx(v_full, L::T_BYTES);
-      tc::bulk_load(sV, vx + (int64_t)(2 * u) * L::T_BYTES, L::T_BYTES, v_full);
+      load(p.vx, p.c.v_codes, sV, cV, v_full, u);
     };
+    auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); };
     auto issue_s = [&]() {
       constexpr uint32_t idesc = tc::idesc_bf16_f32(BM, BN);
       const uint64_t qd = tc::desc_sw128(tc::smem_u32(sQ)), kd = tc::desc_sw128(tc::smem_u32(sK));
@@ -422,15 +473,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
     const float* vs = p.c.v_scale + head * nblk;
     float4* sc = reinterpret_cast<float4*>(base + L::OFF_SC) + warp * NG;
     float m_used = -INFINITY, l = 0.f;
-    if (issuer && nt > 0) {
-      load_k(0);
-      load_v(0);
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(k_full, 0));
-      if (ok) issue_s();
-    }
     Scales nx = load_scales(ks, vs, p.lg, ta + grp, nk, lane);
-#pragma unroll 1
-    for (int u = 0; u < nt; ++u) {
+    // softmax of the group's tile u: scores to P, in place; on_scores() runs once they are there
+    auto softmax = [&](int u, auto&& on_scores) {
       const int tile = ta + grp + 2 * u;
       __syncwarp();
       if (lane < NG) {
@@ -442,52 +487,98 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
       nx = load_scales(ks, vs, p.lg, tile + 2, nk, lane);
       __syncwarp();
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
-      if (ok) {
-        if (issuer && u + 1 < nt) load_k(u + 1);
-        uint32_t sr[BN];
-        tc::tc_fence_after();
+      if (!ok) return;
+      on_scores();
+      uint32_t sr[BN];
+      tc::tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
-        tc::tmem_wait_ld64(sr);
-        tc::tmem_wait_ld64(sr + 64);
-        const int seen = last - tile * BN;     // the last key of the tile that the row sees
-        if (__any_sync(0xffffffffu, seen < BN - 1)) {      // most tiles are seen whole by all rows of the warp
+      for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
+      tc::tmem_wait_ld64(sr);
+      tc::tmem_wait_ld64(sr + 64);
+      const int seen = last - tile * BN;     // the last key of the tile that the row sees
+      if (__any_sync(0xffffffffu, seen < BN - 1)) {          // most tiles are seen whole by all rows of the warp
 #pragma unroll
-          for (int i = 0; i < BN; ++i)
-            if (i > seen) sr[i] = 0xff800000u;
-        }
-        const float mt = row_max(sr, sc);
-        if (u == 0) {
-          m_used = mt;             // O_g is written, not added to, by this tile's P V
-        } else {
-          const bool need = mt > m_used + kLazy;
-          if (__any_sync(0xffffffffu, need)) {             // (S was issued after the last P V had completed)
-            const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
-#pragma unroll 1
-            for (int c = 0; c < HD / 16; ++c) {
-              float o[16];
-              tc::tmem_ld16(tO + c * 16, o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= alpha;
-              tc::tmem_st16(tO + c * 16, o);
-            }
-            l *= alpha;
-            if (need) m_used = mt;
-          }
-        }
-        l += row_weights(sr, tS, sc, kPBias - (m_used == -INFINITY ? 0.f : m_used));
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
+        for (int i = 0; i < BN; ++i)
+          if (i > seen) sr[i] = 0xff800000u;
       }
-      asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory");
-      if (issuer) {
-        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(v_full, u & 1));
-        if (ok) issue_pv(u > 0);
-        if (u + 1 < nt) {
-          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(k_full, (u + 1) & 1) && tc::mbar_wait(pv_done, u & 1));
-          if (ok) {
-            issue_s();
-            load_v(u + 1);
+      const float mt = row_max(sr, sc);
+      if (u == 0) {
+        m_used = mt;             // O_g is written, not added to, by this tile's P V
+      } else {
+        const bool need = mt > m_used + kLazy;
+        if (__any_sync(0xffffffffu, need)) {                 // (S was issued after the last P V had completed)
+          const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            float o[16];
+            tc::tmem_ld16(tO + c * 16, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tc::tmem_st16(tO + c * 16, o);
+          }
+          l *= alpha;
+          if (need) m_used = mt;
+        }
+      }
+      l += row_weights(sr, tS, sc, kPBias - (m_used == -INFINITY ? 0.f : m_used));
+      tc::tmem_wait_st();
+      tc::tc_fence_before();
+    };
+    if (issuer && nt > 0) {
+      load_k(0);
+      load_v(0);
+    }
+    if constexpr (FUSED) {
+#pragma unroll 1
+      for (int u = -1; u < nt; ++u) {
+        if (u >= 0) {
+          softmax(u, [] {});
+          group_sync();            // P is there, and V, converted while S was on its way
+          if (issuer && ok) issue_pv(u > 0);
+        }
+        if (u + 1 >= nt) break;
+        // K of the next tile while P V runs: S of this tile is done with its buffer
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(k_full, (u + 1) & 1));
+        if (ok) convert_tile<HD, false>(cK, sK, r);
+        tc::fence_proxy_async_smem();
+        group_sync();
+        // S goes where P is, and V's buffer is free, once P V is done
+        ok = ok && (u < 0 || __all_sync(0xffffffffu, tc::mbar_wait(pv_done, u & 1)));
+        if (issuer && ok) {
+          issue_s();
+          if (u + 2 < nt) load_k(u + 2);
+        }
+        // V of the next tile while S runs
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(v_full, (u + 1) & 1));
+        if (ok) convert_tile<HD, true>(cV, sV, r);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(v_empty);
+        if (issuer && u + 2 < nt) {
+          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(v_empty, (u + 1) & 1));
+          if (ok) load_v(u + 2);
+        }
+      }
+    } else {
+      if (issuer && nt > 0) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(k_full, 0));
+        if (ok) issue_s();
+      }
+#pragma unroll 1
+      for (int u = 0; u < nt; ++u) {
+        softmax(u, [&] {
+          if (issuer && u + 1 < nt) load_k(u + 1);
+        });
+        group_sync();
+        if (issuer) {
+          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(v_full, u & 1));
+          if (ok) issue_pv(u > 0);
+          if (u + 1 < nt) {
+            ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(k_full, (u + 1) & 1) && tc::mbar_wait(pv_done, u & 1));
+            if (ok) {
+              issue_s();
+              load_v(u + 1);
+            }
           }
         }
       }
@@ -499,6 +590,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
       if (nk_loads > 0) tc::mbar_wait(k_full, (nk_loads - 1) & 1);
       if (nv_loads > 0) tc::mbar_wait(v_full, (nv_loads - 1) & 1);
     }
+    if (FUSED) __syncthreads();    // the statistics go where the other group's codes may still be
     // both groups' row statistics meet in shared memory
     xm[grp * BM + r] = m_used;
     xl[grp * BM + r] = l;
@@ -860,7 +952,9 @@ cudaError_t prepare_tc(int dev, int* sms) {
   std::lock_guard<std::mutex> g(g_tc_mu);
   const bool cached = dev >= 0 && dev < 64;
   if (!cached || !(g_tc_attr[dev] & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tc<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, true>::SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_kv8_attn_tc<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, false>::SMEM);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k_kv8_weights_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WLayout<HD>::SMEM);
     int n = 0;
@@ -882,7 +976,8 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (e = prepare_tc<HD>(dev, &sms)) != cudaSuccess) return e;
-  if ((e = launch_k(k_kv8_expand<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
+  const bool fused = !p.kx;
+  if (!fused && (e = launch_k(k_kv8_expand<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
   // one CTA per SM: the keys are split while that gives more of them work (64 queries of 8 x 7
   // heads over 16384 keys, 32 units, in 1 / 2 / 4 / 8 parts: 170, 102, 62, 94 us; 100 queries of 32
   // heads over 4096: 58, 45, 34, 55 us)
@@ -892,7 +987,7 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.Hkv * ns, p.q_tiles, p.c.n_seq);
   cfg.blockDim = dim3(ATTN_THREADS);
-  cfg.dynamicSmemBytes = Layout<HD>::SMEM;
+  cfg.dynamicSmemBytes = fused ? Layout<HD, true>::SMEM : Layout<HD, false>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -903,7 +998,7 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  if ((e = cudaLaunchKernelEx(&cfg, k_kv8_attn_tc<HD>, p, ns)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&cfg, fused ? k_kv8_attn_tc<HD, true> : k_kv8_attn_tc<HD, false>, p, ns)) != cudaSuccess) return e;
   if (!p.weights) return cudaSuccess;
   const int64_t items = (int64_t)p.c.n_seq * p.Hkv * ((p.tiles + 1) / 2);
   return launch_k(k_kv8_weights_tc<HD>, dim3((unsigned)(items < sms ? items : sms)), dim3(THREADS), WLayout<HD>::SMEM, s, p);
@@ -923,13 +1018,18 @@ void reset_kv8_tc_caches() {
 
 // Which calls take this path: bf16, head_dim 64 or 128, and enough query rows per KV head.  Its
 // time hardly depends on the rows (up to a tile), the other's grows with every 8 of them.
-// 32 / 40 / 48 rows, hd 128, others' time and this one's: 32 heads over 4096 keys 38, 43, 50 and
-// 33 us; 8 over 16384 35, 42, 47 and 42 us; 8 sequences of 8 over 8192 77, 94, 108 and 103 us.  With
+// 24 / 32 / 40 rows, hd 128, other's times and this one's: 32 heads over 4096 keys 33, 38, 41 and
+// 24 us; 8 over 16384 32, 35, 42 and 39 us; 8 sequences of 8 over 8192 61, 73, 87 and 71 us.  With
 // the weights, 16 / 24 rows: 47, 62 and 48 us; 48, 59 and 56 us; 114, 143 and 140 us.
 bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights) {
-  return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > (weights ? 16 : 40) &&
+  return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > (weights ? 16 : 24) &&
          (n_q + BM / G - 1) / (BM / G) <= 65535;
 }
+
+// One query tile and no weights (whose kernel reads K's operands): the attention converts the
+// codes itself.
+static bool is_fused(int G, int n_q, bool weights) { return !weights && n_q <= BM / G; }
+bool kv8_tc_expands(int G, int n_q, bool weights) { return !is_fused(G, n_q, weights); }
 
 namespace {
 struct WsOff {
@@ -938,7 +1038,8 @@ struct WsOff {
 WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
   const size_t tile = (size_t)BN * hd * 2, kt = (size_t)n_seq * Hkv * ((cap + BN - 1) / BN);
   const size_t qt = (n_q + BM / G - 1) / (BM / G), all = (size_t)n_seq * Hkv * qt;
-  WsOff w;
+  WsOff w{};
+  if (is_fused(G, n_q, weights)) return w;
   w.vx = align256(kt * tile);
   w.seq_max = w.vx + align256(kt * tile);
   w.qx = w.seq_max + align256((size_t)n_seq * 4);
@@ -951,7 +1052,8 @@ WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weight
 
 // (the operands are written in 32-byte words: room to start on a boundary of those)
 size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
-  return ws_of(n_seq, Hkv, G, n_q, cap, hd, weights).bytes + 32;
+  const size_t n = ws_of(n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
+  return n ? n + 32 : 0;
 }
 
 cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
@@ -973,9 +1075,11 @@ cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_
   p.g_magic = ((1 << 16) + p.G - 1) / p.G;
   const WsOff w = ws_of(c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
   uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
-  p.kx = b;
-  p.vx = b + w.vx;
-  p.seq_max = reinterpret_cast<int32_t*>(b + w.seq_max);
+  if (!is_fused(p.G, n_q, weights != nullptr)) {
+    p.kx = b;
+    p.vx = b + w.vx;
+    p.seq_max = reinterpret_cast<int32_t*>(b + w.seq_max);
+  }
   if (weights) {
     p.qx = b + w.qx;
     p.rows = reinterpret_cast<float*>(b + w.rows);
