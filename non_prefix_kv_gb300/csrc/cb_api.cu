@@ -37,7 +37,7 @@ cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q,
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
                                int Hkv, int hd, float* weights, void* ws, cudaStream_t s);
 bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights);
-bool kv8_tc_expands(int G, int n_q, bool weights);
+bool kv8_tc_expands(int G, int n_q);
 size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
 cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
                           void* out, float* weights, void* ws, cudaStream_t s);
@@ -1297,7 +1297,7 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   if (kv8_tc_taken(dims->dtype, hd, G, n_q, weights != nullptr)) {
     CB_LAUNCH(CB_PROF_KV8_ATTN, 2, m, cache->capacity, H, 0.0, 0.0, S(stream),
               launch_kv8_tc(q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
-    if (kv8_tc_expands(G, n_q, weights != nullptr)) g_launches.fetch_add(weights ? 2 : 1, std::memory_order_relaxed);
+    g_launches.fetch_add((kv8_tc_expands(G, n_q) ? 1 : 0) + (weights ? 1 : 0), std::memory_order_relaxed);
     return CB_OK;
   }
   CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),

@@ -60,7 +60,7 @@ struct Kv8Tc {
   bf16* out;
   uint8_t* kx;              // [n_seq * Hkv, tiles] key tiles in shared-memory order: bf16 codes
   uint8_t* vx;              // the same of V: fp16 codes
-  int32_t* seq_max;         // [n_seq] the last row any query of the sequence sees
+  int32_t* seq_max;         // [n_seq] the last row any query of the sequence sees (for the weights)
   // for the weights (else null), per (sequence, KV head, query tile):
   uint8_t* qx;              // the tile's query rows in shared-memory order
   float* rows;              // [2][BM] log2 of each row's sum (+inf where there is none), last row it sees (int)
@@ -697,13 +697,18 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
 // Measured: 64 queries of 7 heads over 16384 rows of 8 KV heads (58.7 M weights) 21 us, bound by
 // the exponentials' chain from TMEM (33% of the issue slots, 32% of the special functions' rate);
 // one CTA per key tile gathering the queries itself 55 us.
-template <int HD>
+//
+// FUSED (one query tile): K comes as codes, and a group converts its tile before it weighs it (85
+// rows of 40 heads over 6 x 16064 keys, attention and weights 701 us, 842 with the expansion).
+template <int HD, bool FUSED>
 struct WLayout {
   static constexpr int T_BYTES = HD / 64 * SLAB;
-  static constexpr int QS = 4;                                // query tiles in flight
+  static constexpr int C_BYTES = FUSED ? BN * HD : 0;
+  static constexpr int QS = FUSED ? 2 : 4;                    // query tiles in flight
   static constexpr int OFF_K = 0;                             // [2]
   static constexpr int OFF_Q = 2 * T_BYTES;                   // [QS]
-  static constexpr int OFF_L = OFF_Q + QS * T_BYTES;          // [QS][2][BM] log2 sum, last
+  static constexpr int OFF_C = OFF_Q + QS * T_BYTES;          // [2] codes
+  static constexpr int OFF_L = OFF_C + 2 * C_BYTES;           // [QS][2][BM] log2 sum, last
   static constexpr int OFF_BAR = OFF_L + QS * 2 * BM * 4;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
@@ -730,17 +735,18 @@ struct TileWalk {
   }
 };
 
-template <int HD>
+template <int HD, bool FUSED>
 __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
-  using L = WLayout<HD>;
+  using L = WLayout<HD, FUSED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sK = base + L::OFF_K;
   uint8_t* sQ = base + L::OFF_Q;
   const float* sL = reinterpret_cast<const float*>(base + L::OFF_L);
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);   // [2]
-  uint64_t* k_empty = k_full + 2;                                       // [2]
-  uint64_t* q_full = k_empty + 2;                                       // [QS]
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);   // [2] K (its codes) has landed
+  uint64_t* k_empty = k_full + 2;                                       // [2] the products (the four warps) have read it
+  uint64_t* k_conv = k_empty + 2;                                       // [2] the four warps have converted it
+  uint64_t* q_full = k_conv + 2;                                        // [QS]
   uint64_t* q_empty = q_full + L::QS;                                   // [QS] the MMA and every softmax warp
   uint64_t* s_full = q_empty + L::QS;                                   // [2 groups][2]
   uint64_t* s_empty = s_full + 4;                                       // [2][2]
@@ -749,7 +755,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&k_full[i], 1);
-      tc::mbar_init(&k_empty[i], 1);
+      tc::mbar_init(&k_empty[i], FUSED ? 4 : 1);
+      tc::mbar_init(&k_conv[i], 4);
     }
     for (int i = 0; i < L::QS; ++i) {
       tc::mbar_init(&q_full[i], 1);
@@ -793,8 +800,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&k_empty[g], (kn[g] & 1) ^ 1));
         if (!ok) break;
         if (lane == 0) {
-          tc::mbar_expect_tx(&k_full[g], L::T_BYTES);
-          tc::bulk_load(sK + g * L::T_BYTES, p.kx + (head * p.tiles + kt + g) * (int64_t)L::T_BYTES, L::T_BYTES, &k_full[g]);
+          if constexpr (FUSED) {
+            const int64_t key = (int64_t)(kt + g) * BN;
+            const uint32_t bytes = (uint32_t)(p.c.capacity - key < BN ? p.c.capacity - key : BN) * HD;
+            tc::mbar_expect_tx(&k_full[g], bytes);
+            tc::bulk_load(base + L::OFF_C + g * L::C_BYTES, p.c.k_codes + (head * p.c.capacity + key) * HD, bytes, &k_full[g]);
+          } else {
+            tc::mbar_expect_tx(&k_full[g], L::T_BYTES);
+            tc::bulk_load(sK + g * L::T_BYTES, p.kx + (head * p.tiles + kt + g) * (int64_t)L::T_BYTES, L::T_BYTES, &k_full[g]);
+          }
         }
         ++kn[g];
       }
@@ -826,7 +840,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
     int n = 0, kn[2] = {0, 0}, sn[2] = {0, 0};
     each([&](int64_t, int s, int kt, bool two) -> bool {
       const int ng = two ? 2 : 1;
-      for (int g = 0; ok && g < ng; ++g) ok = __all_sync(0xffffffffu, tc::mbar_wait(&k_full[g], kn[g]++ & 1));
+      for (int g = 0; ok && g < ng; ++g) ok = __all_sync(0xffffffffu, tc::mbar_wait(FUSED ? &k_conv[g] : &k_full[g], kn[g]++ & 1));
       TileWalk walk(p.tile_max + s * p.q_tiles, p.q_tiles, kt * BN, lane);
       for (int y = walk.next(); ok && y >= 0; ++n) {
         const int b = n % L::QS, ahead = walk.next();
@@ -845,7 +859,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
             }
             tc::mma_commit(&s_full[2 * g + sb]);
             if (g == ng - 1) tc::mma_commit(&q_empty[b]);
-            if (ahead < 0) tc::mma_commit(&k_empty[g]);
+            if (!FUSED && ahead < 0) tc::mma_commit(&k_empty[g]);
           }
           __syncwarp();
           ++sn[g];
@@ -860,9 +874,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
     const int grp = (warp - 2) >> 2, quad = warp & 3, r = quad * 32 + lane;
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + grp * 2 * BM;
     bool ok = true;
-    int n = 0, sn = 0;
+    int n = 0, sn = 0, kn = 0;
     each([&](int64_t head, int s, int kt, bool two) -> bool {
       const bool mine = grp == 0 || two;
+      if (FUSED && mine) {                       // (the products of the pair before are done with K: its last S was waited for)
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&k_full[grp], kn & 1));
+        if (!ok) return false;
+        ++kn;
+        convert_tile<HD, false>(base + L::OFF_C + grp * L::C_BYTES, sK + grp * L::T_BYTES, r);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&k_empty[grp]);
+          tc::mbar_arrive(&k_conv[grp]);
+        }
+      }
       const int key = (kt + grp) * BN + r;
       float f = 0.f;
       if (mine && key < p.c.capacity)
@@ -956,7 +982,9 @@ cudaError_t prepare_tc(int dev, int* sms) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k_kv8_attn_tc<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, false>::SMEM);
     if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_kv8_weights_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WLayout<HD>::SMEM);
+      e = cudaFuncSetAttribute(k_kv8_weights_tc<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, WLayout<HD, true>::SMEM);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k_kv8_weights_tc<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, WLayout<HD, false>::SMEM);
     int n = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -1001,7 +1029,9 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   if ((e = cudaLaunchKernelEx(&cfg, fused ? k_kv8_attn_tc<HD, true> : k_kv8_attn_tc<HD, false>, p, ns)) != cudaSuccess) return e;
   if (!p.weights) return cudaSuccess;
   const int64_t items = (int64_t)p.c.n_seq * p.Hkv * ((p.tiles + 1) / 2);
-  return launch_k(k_kv8_weights_tc<HD>, dim3((unsigned)(items < sms ? items : sms)), dim3(THREADS), WLayout<HD>::SMEM, s, p);
+  const dim3 grid((unsigned)(items < sms ? items : sms));
+  if (fused) return launch_k(k_kv8_weights_tc<HD, true>, grid, dim3(THREADS), WLayout<HD, true>::SMEM, s, p);
+  return launch_k(k_kv8_weights_tc<HD, false>, grid, dim3(THREADS), WLayout<HD, false>::SMEM, s, p);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -1020,16 +1050,15 @@ void reset_kv8_tc_caches() {
 // time hardly depends on the rows (up to a tile), the other's grows with every 8 of them.
 // 24 / 32 / 40 rows, hd 128, other's times and this one's: 32 heads over 4096 keys 33, 38, 41 and
 // 24 us; 8 over 16384 32, 35, 42 and 39 us; 8 sequences of 8 over 8192 61, 73, 87 and 71 us.  With
-// the weights, 16 / 24 rows: 47, 62 and 48 us; 48, 59 and 56 us; 114, 143 and 140 us.
+// the weights, 16 / 24 rows: 46, 61 and 41 us; 48, 59 and 56 us; 115, 141 and 124 us.
 bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights) {
   return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > (weights ? 16 : 24) &&
          (n_q + BM / G - 1) / (BM / G) <= 65535;
 }
 
-// One query tile and no weights (whose kernel reads K's operands): the attention converts the
-// codes itself.
-static bool is_fused(int G, int n_q, bool weights) { return !weights && n_q <= BM / G; }
-bool kv8_tc_expands(int G, int n_q, bool weights) { return !is_fused(G, n_q, weights); }
+// One query tile: the codes are converted where they are used.
+static bool is_fused(int G, int n_q) { return n_q <= BM / G; }
+bool kv8_tc_expands(int G, int n_q) { return !is_fused(G, n_q); }
 
 namespace {
 struct WsOff {
@@ -1039,10 +1068,11 @@ WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weight
   const size_t tile = (size_t)BN * hd * 2, kt = (size_t)n_seq * Hkv * ((cap + BN - 1) / BN);
   const size_t qt = (n_q + BM / G - 1) / (BM / G), all = (size_t)n_seq * Hkv * qt;
   WsOff w{};
-  if (is_fused(G, n_q, weights)) return w;
-  w.vx = align256(kt * tile);
-  w.seq_max = w.vx + align256(kt * tile);
-  w.qx = w.seq_max + align256((size_t)n_seq * 4);
+  if (!is_fused(G, n_q)) {
+    w.vx = align256(kt * tile);
+    w.seq_max = w.vx + align256(kt * tile);
+    w.qx = w.seq_max + align256((size_t)n_seq * 4);
+  }
   w.rows = w.qx + (weights ? align256(all * tile) : 0);
   w.tile_max = w.rows + (weights ? align256(all * 2 * BM * 4) : 0);
   w.bytes = w.tile_max + (weights ? align256((size_t)n_seq * qt * 4) : 0);
@@ -1075,7 +1105,7 @@ cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_
   p.g_magic = ((1 << 16) + p.G - 1) / p.G;
   const WsOff w = ws_of(c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
   uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
-  if (!is_fused(p.G, n_q, weights != nullptr)) {
+  if (!is_fused(p.G, n_q)) {
     p.kx = b;
     p.vx = b + w.vx;
     p.seq_max = reinterpret_cast<int32_t*>(b + w.seq_max);
@@ -1084,6 +1114,7 @@ cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_
     p.qx = b + w.qx;
     p.rows = reinterpret_cast<float*>(b + w.rows);
     p.tile_max = reinterpret_cast<int32_t*>(b + w.tile_max);
+    if (!p.seq_max) p.seq_max = p.tile_max;      // one tile per sequence
     p.weights = weights;
   }
   return hd == 128 ? launch_hd<128>(p, s) : launch_hd<64>(p, s);
