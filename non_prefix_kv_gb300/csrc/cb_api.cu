@@ -1303,7 +1303,7 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),
             launch_kv8_attn(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
   const bool apart = kv8_attn_weights_apart(G, n_q);
-  g_launches.fetch_add(weights && !apart ? 2 : 1, std::memory_order_relaxed);    // the merge, and the account
+  g_launches.fetch_add(1, std::memory_order_relaxed);    // the merge (with the account)
   if (weights && apart)
     CB_LAUNCH(CB_PROF_KV8_ATTN, 1, m, cache->capacity, H, 0.0, 0.0, S(stream),
               launch_kv8_weights(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, weights, ws, S(stream)));

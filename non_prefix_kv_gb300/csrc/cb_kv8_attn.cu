@@ -95,7 +95,7 @@ struct Kv8Attn {
   int32_t* plan;            // [entries + 1] steps before each (sequence, row tile), times Hkv
   float* part;              // partial results, see slot()
   float* z;                 // [n_seq * Hkv, n_q * G, capacity] scores z_i for the weights, or null
-  float* lse;               // [n_seq * Hkv, n_q * G] log2 of a row's sum, or null
+  float* lse;               // [n_seq * Hkv, n_q * G] log2 of a row's sum for k_kv8_weights, or null
   float* weights;           // [n_seq, Hkv, capacity], or null
   cb_kv8_cache c;
   int n_q, H, Hkv, G, lg;
@@ -134,17 +134,20 @@ __device__ __forceinline__ void load4(const T* p, bool on, float* f) {
   }
 }
 
-// Row r of entry e (sequence e / row_tiles, row tile e % row_tiles): the last cache row it sees,
-// -1 where the row does not exist or its bound is bad (reported if asked).
-__device__ __forceinline__ int row_last(const Kv8Attn& p, int e, int r, bool report) {
-  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * TILE + r;
-  if (r >= TILE || row >= p.n_q * p.G) return -1;
-  const int l = p.last[(int64_t)s * p.n_q + row / p.G];
+// The last cache row that query j of sequence s sees; -1 where its bound is bad (reported if asked).
+__device__ __forceinline__ int query_last(const Kv8Attn& p, int s, int j, bool report) {
+  const int l = p.last[(int64_t)s * p.n_q + j];
   if (l < -1 || l >= p.c.capacity) {
     if (report) atomicOr(&g_err_kv8_attn, ERRBIT_INDEX);
     return -1;
   }
   return l;
+}
+// The same for row r of entry e (sequence e / row_tiles, row tile e % row_tiles), -1 where the row
+// does not exist.
+__device__ __forceinline__ int row_last(const Kv8Attn& p, int e, int r) {
+  const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * TILE + r;
+  return r >= TILE || row >= p.n_q * p.G ? -1 : query_last(p, s, row / p.G, false);
 }
 
 // The line of work: unit (entry e, KV head h) holds the steps of the entry's visible keys;
@@ -155,6 +158,20 @@ __device__ __forceinline__ int row_last(const Kv8Attn& p, int e, int r, bool rep
 // steps at least (a token of 32 heads over 512 / 2048 rows: 11.8 and 13.1 us; with one step 11.0 and
 // 14.0, with four 12.1 and 13.8, with eight 15.0 and 17.3).
 __device__ __forceinline__ int workers_of(int total, int workers) { return max(1, min(workers, total / 2)); }
+// the first step of worker w's run: floor(total w / n), w <= n <= 2^12, without a 64-bit division
+__device__ __forceinline__ int run_start(int total, int w, int n) {
+  const unsigned each = (unsigned)total / (unsigned)n, rest = (unsigned)total - each * n;
+  return (int)(each * w + rest * w / n);
+}
+// the worker whose run holds step x: floor(((x + 1) n - 1) / total) (run_start(w + 1) > x says
+// (w + 1) total >= (x + 1) n); the fp32 quotient is off by less than one
+__device__ __forceinline__ int worker_of(int total, int x, int n) {
+  const int64_t a = ((int64_t)x + 1) * n - 1;
+  int w = (int)__fdividef((float)a, (float)total);
+  if ((int64_t)w * total > a) --w;
+  if ((int64_t)(w + 1) * total <= a) ++w;
+  return w;
+}
 __device__ __forceinline__ float* slot(const Kv8Attn& p, int hd, int worker, int unit) {
   const int rows = min(TILE, p.n_q * p.G);
   return p.part + ((int64_t)worker + unit) * (rows * hd + 2 * TILE);     // [rt] max, [rt] sum, [rows][hd] O
@@ -197,8 +214,9 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
   // ---- where this worker's run lies: thread i sums the steps of a contiguous share of the
   // entries, a scan over the threads places them (the first CTA writes the plan for the merge)
   auto steps_of = [&](int e, bool report) -> int {
+    const int s = e / p.row_tiles, row0 = (e - s * p.row_tiles) * TILE;
     int mx = -1;
-    for (int r = 0; r < TILE; ++r) mx = max(mx, row_last(p, e, r, report));
+    for (int j = row0 / p.G; j <= (min(R, row0 + TILE) - 1) / p.G; ++j) mx = max(mx, query_last(p, s, j, report));
     return (mx + L::KT) / L::KT;
   };
   const int share = (entries + THREADS - 1) / THREADS, e0 = min(entries, tid * share), e1 = min(entries, e0 + share);
@@ -232,12 +250,12 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
   // consecutive workers sit in different CTAs, so that few of them still spread over the SMs
   const int n_work = workers_of(total, gridDim.x * WARPS), worker = warp * gridDim.x + blockIdx.x;
   if (worker >= n_work) return;                  // no barrier of the CTA follows
-  const int a = (int)((int64_t)total * worker / n_work), b = (int)((int64_t)total * (worker + 1) / n_work);
+  const int a = run_start(total, worker, n_work), b = run_start(total, worker + 1, n_work);
   if (a >= b) return;
 
   // steps of entry e, by the whole warp
   auto warp_steps = [&](int e) -> int {
-    return (__reduce_max_sync(0xffffffffu, row_last(p, e, lane, false)) + L::KT) / L::KT;
+    return (__reduce_max_sync(0xffffffffu, row_last(p, e, lane)) + L::KT) / L::KT;
   };
   struct Pos {
     int e, h, k, n;       // entry, head, step of the unit, steps in a unit of the entry
@@ -290,7 +308,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
     // ------------------------------------------------------------------ a unit, or a part of one
     const int s = cur.e / p.row_tiles, row0 = (cur.e - s * p.row_tiles) * TILE, nrow = min(TILE, R - row0), h = cur.h;
     const int64_t head = (int64_t)s * p.Hkv + h;
-    const int my_last = row_last(p, cur.e, lane, false);
+    const int my_last = row_last(p, cur.e, lane);
     const int nk = __reduce_max_sync(0xffffffffu, my_last) + 1;       // keys some row sees
     const int mn = __reduce_min_sync(0xffffffffu, lane < nrow ? my_last : 0x7fffffff);
     const float* ksc = p.c.k_scale + head * (cap >> p.lg);
@@ -535,15 +553,76 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
   }
 }
 
+// The workers whose runs meet unit (entry e, head h): the first one, and how many.
+__device__ __forceinline__ int unit_workers(const Kv8Attn& p, int e, int h, int max_workers, int* first) {
+  const int start = p.plan[e], n = (p.plan[e + 1] - start) / p.Hkv, total = p.plan[p.c.n_seq * p.row_tiles];
+  if (n <= 0) return 0;
+  const int nw = workers_of(total, max_workers), x0 = start + h * n;
+  *first = worker_of(total, x0, nw);
+  return worker_of(total, x0 + n - 1, nw) - *first + 1;
+}
+
+// The account of the weights, one row tile: weights[key] += sum over the rows of 2^(z - log2 of the
+// row's sum), four keys per thread.  A CTA takes a (sequence, head)'s next 1024 keys and joins the
+// rows' sums itself, a warp per row, so that it need not wait for the merge: it is launched with it
+// (a token with weights, 32 heads over 1024 rows: 10.4 us, 13.8 as a launch of its own).
+__device__ __forceinline__ void account(const Kv8Attn& p, int hd, int block, int max_workers) {
+  __shared__ float s_lse[TILE];
+  const int64_t cap = p.c.capacity;
+  const int chunks = (int)((cap + 1023) / 1024), head = block / chunks, s = head / p.Hkv, h = head - s * p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, R = p.n_q * p.G;
+  const int64_t key = ((int64_t)(block - head * chunks) * 256 + threadIdx.x) * 4;
+  int mx = -1;
+  for (int r = 0; r < R; r += p.G) mx = max(mx, query_last(p, s, r / p.G, false));
+  if (key - threadIdx.x * 4 > mx) return;          // whole CTAs
+  if (warp < R) {
+    int w0 = 0;
+    const int np = unit_workers(p, s, h, max_workers, &w0);
+    float mm = kNone, sum = 0.f;
+    for (int i = lane; i < np + lane; i += 32) {   // whole warps
+      float m = kNone, l = 0.f;
+      if (i < np) {
+        const float* src = slot(p, hd, w0 + i, head);
+        m = src[warp];
+        l = src[TILE + warp];
+      }
+      const float top = fmaxf(mm, warp_max(m));
+      sum = fmaf(sum, tc::ex2_approx(mm - top), warp_sum(l * tc::ex2_approx(m - top)));
+      mm = top;
+    }
+    if (lane == 0) s_lse[warp] = sum == 0.f ? INFINITY : mm - kPBias + log2f(sum);
+  }
+  __syncthreads();
+  if (key > mx) return;
+  const float* z = p.z + head * R * cap + key;
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < R; ++r) {
+    const float4 v = *reinterpret_cast<const float4*>(z + r * cap);     // an unseen key's z is -inf
+    const float l = s_lse[r];
+    a[0] += v.x == -INFINITY ? 0.f : tc::ex2_approx(v.x - l);           // (l of a NaN query is NaN)
+    a[1] += v.y == -INFINITY ? 0.f : tc::ex2_approx(v.y - l);
+    a[2] += v.z == -INFINITY ? 0.f : tc::ex2_approx(v.z - l);
+    a[3] += v.w == -INFINITY ? 0.f : tc::ex2_approx(v.w - l);
+  }
+  float* w = p.weights + (int64_t)head * cap + key;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (key + k <= mx) w[k] += a[k];
+}
+
 // Joins the partial results of one query row: the workers whose runs meet its unit, their
 // maxima and sums, then the weighted sum of their O.  WPR warps per (row, unit), each taking
 // every WPR-th worker, 32 at a time (a lane per worker for the statistics, a lane per HD / 32
 // channels for O); with several warps their results meet in shared memory.
 constexpr int MERGE_WARPS = 8;
 template <int HD, int WPR, typename T>
-__global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p, int max_workers) {
+__global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p, int max_workers, int merge_ctas) {
   pdl_wait();
   pdl_trigger();
+  if ((int)blockIdx.x >= merge_ctas) {             // CTAs past the merge's: the account
+    account(p, HD, blockIdx.x - merge_ctas, max_workers);
+    return;
+  }
   constexpr int PL = HD / 32;          // channels of a lane
   __shared__ float s_o[WPR > 1 ? MERGE_WARPS : 1][HD];
   __shared__ float s_m[MERGE_WARPS], s_l[MERGE_WARPS];
@@ -553,19 +632,8 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p,
   if (item >= entries * p.Hkv * rows) return;    // whole CTAs when WPR = MERGE_WARPS
   const int unit = item / rows, r = item - unit * rows, e = unit / p.Hkv, h = unit - e * p.Hkv;
   const int s = e / p.row_tiles, row = (e - s * p.row_tiles) * TILE + r, R = p.n_q * p.G;
-  const int start = p.plan[e], n = (p.plan[e + 1] - start) / p.Hkv, total = p.plan[entries];
-  int w0 = 0, np = 0;                  // the unit's workers: the runs that meet [x0, x1)
-  if (n > 0 && row < R) {
-    const int nw = workers_of(total, max_workers);
-    const int64_t x0 = start + (int64_t)h * n, x1 = x0 + n - 1;
-    w0 = (int)(x0 * nw / total);
-    while ((int64_t)total * w0 / nw > x0) --w0;
-    while ((int64_t)total * (w0 + 1) / nw <= x0) ++w0;
-    int w1 = (int)(x1 * nw / total);
-    while ((int64_t)total * w1 / nw > x1) --w1;
-    while ((int64_t)total * (w1 + 1) / nw <= x1) ++w1;
-    np = w1 - w0 + 1;
-  }
+  int w0 = 0;
+  const int np = row < R ? unit_workers(p, e, h, max_workers, &w0) : 0;
   float mm = kNone, sum = 0.f, o[PL];
 #pragma unroll
   for (int k = 0; k < PL; ++k) o[k] = 0.f;
@@ -643,34 +711,6 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) k_kv8_merge(const Kv8Attn p,
 #pragma unroll
     for (int k = 0; k < PL; ++k) out[k] = from_f<T>(o[k]);
   }
-}
-
-// weights[key] += sum over the rows of 2^(z - log2 of the row's sum); four keys per thread.  Bound
-// by latency after a merge (8 sequences of 40 heads over 8192 rows: 12 us with the wait for it).
-__global__ void __launch_bounds__(256) k_kv8_account(const Kv8Attn p) {
-  pdl_wait();
-  pdl_trigger();
-  const int h = blockIdx.y, s = blockIdx.z, R = p.n_q * p.G;
-  const int64_t cap = p.c.capacity, head = (int64_t)s * p.Hkv + h;
-  int mx = -1;
-  for (int r = 0; r < R; r += p.G) mx = max(mx, row_last(p, s, r, false));
-  const int64_t key = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (key > mx) return;
-  const float* z = p.z + head * R * cap + key;
-  const float* lse = p.lse + head * R;
-  float a[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int r = 0; r < R; ++r) {
-    const float4 v = *reinterpret_cast<const float4*>(z + r * cap);     // an unseen key's z is -inf
-    const float l = lse[r];
-    a[0] += v.x == -INFINITY ? 0.f : tc::ex2_approx(v.x - l);           // (l of a NaN query is NaN)
-    a[1] += v.y == -INFINITY ? 0.f : tc::ex2_approx(v.y - l);
-    a[2] += v.z == -INFINITY ? 0.f : tc::ex2_approx(v.z - l);
-    a[3] += v.w == -INFINITY ? 0.f : tc::ex2_approx(v.w - l);
-  }
-  float* w = p.weights + head * cap + key;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (key + k <= mx) w[k] += a[k];
 }
 
 // The weights of more query rows than one tile holds: with log2 of every row's sum known, each
@@ -844,14 +884,13 @@ cudaError_t launch_attn_t(const Kv8Attn& p, cudaStream_t s) {
   // a warp per row where that alone fills the SMs, else a CTA (32 sequences of 8 x 7 heads, 1792
   // rows whose units meet 10 workers each: 144 and 148 us; one of 32 heads, 32 rows and 75
   // workers: 28 and 17 us; 8 of 32 heads, 256 rows and 10 workers: 48 and 46 us)
-  if (items >= (int64_t)MERGE_WARPS * device_sms(dev))
-    e = launch_k(k_kv8_merge<HD, 1, T>, dim3((unsigned)((items + MERGE_WARPS - 1) / MERGE_WARPS)), dim3(32 * MERGE_WARPS), 0,
-                 s, p, ctas * WARPS);
-  else
-    e = launch_k(k_kv8_merge<HD, MERGE_WARPS, T>, dim3((unsigned)items), dim3(32 * MERGE_WARPS), 0, s, p, ctas * WARPS);
-  if (e != cudaSuccess) return e;
-  if (!p.z) return cudaSuccess;
-  return launch_k(k_kv8_account, dim3((unsigned)((p.c.capacity + 1023) / 1024), p.Hkv, p.c.n_seq), dim3(256), 0, s, p);
+  const int64_t acc = p.z ? (p.c.capacity + 1023) / 1024 * p.Hkv * p.c.n_seq : 0;
+  if (items >= (int64_t)MERGE_WARPS * device_sms(dev)) {
+    const int n = (int)((items + MERGE_WARPS - 1) / MERGE_WARPS);
+    return launch_k(k_kv8_merge<HD, 1, T>, dim3((unsigned)(n + acc)), dim3(32 * MERGE_WARPS), 0, s, p, ctas * WARPS, n);
+  }
+  return launch_k(k_kv8_merge<HD, MERGE_WARPS, T>, dim3((unsigned)(items + acc)), dim3(32 * MERGE_WARPS), 0, s, p,
+                  ctas * WARPS, (int)items);
 }
 
 template <int HD, typename T>
@@ -886,8 +925,9 @@ WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weight
   WsOff w;
   w.part = up256(((size_t)n_seq * tiles + 1) * 4);
   w.lse = w.part + up256(((size_t)n_seq * tiles * Hkv + MAX_WORKERS) * (std::min((size_t)TILE, R) * hd + 2 * TILE) * 4);
-  w.z = w.lse + (weights ? up256((size_t)n_seq * Hkv * R * 4) : 0);
-  w.bytes = w.z + (weights && !kv8_attn_weights_apart(G, n_q) ? (size_t)n_seq * Hkv * R * cap * 4 : 0);
+  const bool apart = kv8_attn_weights_apart(G, n_q);
+  w.z = w.lse + (weights && apart ? up256((size_t)n_seq * Hkv * R * 4) : 0);
+  w.bytes = w.z + (weights && !apart ? (size_t)n_seq * Hkv * R * cap * 4 : 0);
   return w;
 }
 }  // namespace
@@ -916,9 +956,11 @@ static Kv8Attn make_params(const void* q, const int32_t* last, int n_q, const cb
   p.plan = reinterpret_cast<int32_t*>(b);
   p.part = reinterpret_cast<float*>(b + w.part);
   if (weights) {
-    p.lse = reinterpret_cast<float*>(b + w.lse);
     p.weights = weights;
-    if (!kv8_attn_weights_apart(p.G, n_q)) p.z = reinterpret_cast<float*>(b + w.z);
+    if (kv8_attn_weights_apart(p.G, n_q))
+      p.lse = reinterpret_cast<float*>(b + w.lse);
+    else
+      p.z = reinterpret_cast<float*>(b + w.z);
   }
   return p;
 }

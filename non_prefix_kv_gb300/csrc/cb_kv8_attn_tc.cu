@@ -11,7 +11,8 @@
 // order the tensor cores read, so that a tile is one bulk copy and no tensor map is needed:
 // every key tile is read by n_q G / 128 CTAs, and converting it in each of them would cost
 // more issue slots than the softmax itself (26 instructions per 16 codes, against one pass
-// over 5 bytes per code).
+// over 5 bytes per code).  With a single query tile each tile of the cache has one reader, which
+// converts it itself (FUSED).
 //
 // Rows of one KV head are packed into tiles: row r of a tile is query r / G, head r % G, so
 // a few queries of grouped heads fill a tile and a tile's rows share one narrow run of
