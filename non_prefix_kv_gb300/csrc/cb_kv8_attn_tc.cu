@@ -241,32 +241,35 @@ __device__ __forceinline__ Scales load_scales(const float* ks, const float* vs, 
   return r;
 }
 
-// A tile's codes as an operand tile, by a group's 128 threads: 16 codes at a time, read in order,
-// to two 16-byte words of the swizzled row (the second slab's lanes write theirs the other way
-// round, so that eight lanes meet all banks).
+// A tile's codes as an operand tile, by a group's 128 threads: 16 codes at a time to two 16-byte
+// words of the swizzled row.  Eight lanes take half a row of 64 channels each of two rows, so that
+// their writes meet all banks; a thread's rows lie a multiple of 8 apart, so its addresses differ
+// by constants.
 template <int HD, bool IS_V>
-__device__ __forceinline__ void convert_tile(const uint8_t* codes, uint8_t* dst, int t) {
-  constexpr int PER = HD / 16;
+__device__ __forceinline__ void convert_tile(const uint8_t* codes, uint8_t* dst, unsigned t) {
+  constexpr int ROWS_AT_ONCE = 128 * 16 / HD;
+  // lanes of a row pair: 4 of one row, 4 of the other, then (HD = 128) the same of the second slab
+  const unsigned slab = HD == 128 ? (t >> 3) & 1 : 0, pair = HD == 128 ? t >> 4 : t >> 3;
+  const unsigned row = 2 * pair + ((t >> 2) & 1), piece = t & 3, sw = row & 7;
+  const uint8_t* src = codes + row * HD + slab * 64 + piece * 16;
+  uint8_t* d0 = dst + slab * SLAB + row * 128 + ((2 * piece) ^ sw) * 16;
+  uint8_t* d1 = dst + slab * SLAB + row * 128 + ((2 * piece + 1) ^ sw) * 16;
 #pragma unroll 4
-  for (int i = 0; i < PER; ++i) {
-    const int idx = i * 128 + t, row = idx / PER, piece = idx % PER;
-    const uint4 u = *reinterpret_cast<const uint4*>(codes + idx * 16);
+  for (int i = 0; i < BN / ROWS_AT_ONCE; ++i) {
+    const uint4 u = *reinterpret_cast<const uint4*>(src + i * ROWS_AT_ONCE * HD);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint4 o[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
+      uint4 o;
       if (IS_V) {
         const uint32_t u0 = w[2 * c] ^ 0x80808080u, u1 = w[2 * c + 1] ^ 0x80808080u;
-        o[c] = make_uint4(pair_f16(u0, 0x4140), pair_f16(u0, 0x4342), pair_f16(u1, 0x4140), pair_f16(u1, 0x4342));
+        o = make_uint4(pair_f16(u0, 0x4140), pair_f16(u0, 0x4342), pair_f16(u1, 0x4140), pair_f16(u1, 0x4342));
       } else {
-        o[c] = make_uint4(pair_bf16(w[2 * c], 0x4140), pair_bf16(w[2 * c], 0x4342), pair_bf16(w[2 * c + 1], 0x4140),
-                          pair_bf16(w[2 * c + 1], 0x4342));
+        o = make_uint4(pair_bf16(w[2 * c], 0x4140), pair_bf16(w[2 * c], 0x4342), pair_bf16(w[2 * c + 1], 0x4140),
+                       pair_bf16(w[2 * c + 1], 0x4342));
       }
+      *reinterpret_cast<uint4*>((c ? d1 : d0) + i * ROWS_AT_ONCE * 128) = o;
     }
-    uint8_t* d = dst + (piece >> 2) * SLAB + row * 128;
-    const int at = 2 * (piece & 3), sw = row & 7, first = (piece >> 2) & 1;
-    *reinterpret_cast<uint4*>(d + (((at + first) ^ sw) * 16)) = first ? o[1] : o[0];
-    *reinterpret_cast<uint4*>(d + (((at + (first ^ 1)) ^ sw) * 16)) = first ? o[0] : o[1];
   }
 }
 
