@@ -37,9 +37,9 @@ cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q,
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
                                int Hkv, int hd, float* weights, void* ws, cudaStream_t s);
 bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights);
-bool kv8_tc_expands(int G, int n_q);
-size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
-cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
+bool kv8_tc_expands(int dt, int G, int n_q);
+size_t kv8_tc_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights);
+cudaError_t launch_kv8_tc(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
                           void* out, float* weights, void* ws, cudaStream_t s);
 cudaError_t launch_logits(int dt, const void* logits, int n_rows, int vocab, const cb_logit_rules& r, void* out,
                           int32_t* token, cudaStream_t s);
@@ -1252,7 +1252,7 @@ namespace {
 size_t kv8_ws(const cb_dims* d, int n_seq, int64_t cap, int n_q, bool weights) {
   const int G = d->n_heads / d->n_kv_heads;
   if (kv8_tc_taken(d->dtype, d->head_dim, G, n_q, weights))
-    return kv8_tc_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
+    return kv8_tc_ws_bytes(d->dtype, n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
   return kv8_attn_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
 }
 }  // namespace
@@ -1296,8 +1296,8 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   const int64_t m = (int64_t)cache->n_seq * n_q;
   if (kv8_tc_taken(dims->dtype, hd, G, n_q, weights != nullptr)) {
     CB_LAUNCH(CB_PROF_KV8_ATTN, 2, m, cache->capacity, H, 0.0, 0.0, S(stream),
-              launch_kv8_tc(q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
-    g_launches.fetch_add((kv8_tc_expands(G, n_q) ? 1 : 0) + (weights ? 1 : 0), std::memory_order_relaxed);
+              launch_kv8_tc(dims->dtype, q, last, n_q, *cache, H, Hkv, hd, out, weights, ws, S(stream)));
+    g_launches.fetch_add((kv8_tc_expands(dims->dtype, G, n_q) ? 1 : 0) + (weights ? 1 : 0), std::memory_order_relaxed);
     return CB_OK;
   }
   CB_LAUNCH(CB_PROF_KV8_ATTN, 0, m, cache->capacity, H, 0.0, 0.0, S(stream),

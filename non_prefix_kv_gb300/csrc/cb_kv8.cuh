@@ -29,6 +29,16 @@ __device__ __forceinline__ uint32_t kv8_recode(float c0, float old, float s, uin
   return q;
 }
 
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// the part of (a, b) that their fp16 rounding p leaves over, again as an fp16 pair
+__device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t p) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+  return pack_h2(a - f.x, b - f.y);
+}
+
 // 16 codes as 8 pairs of floats: byte ^ 0x80 = c + 128 under the exponent of 2^23 (no conversion
 // instruction: those run at a quarter of the rate)
 __device__ __forceinline__ void kv8_unpack16(const uint4 v, uint64_t* f) {

@@ -68,16 +68,6 @@ __device__ __forceinline__ uint32_t codes_pair(uint32_t a, uint32_t b) {
   const uint32_t x = __byte_perm(a, b, J | (J << 4) | ((4 + J) << 8) | ((4 + J) << 12));
   return h2_sub1152((x & 0x00ff00ffu) ^ 0x64806480u);
 }
-__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// the part of (a, b) that their fp16 rounding p leaves over, again as an fp16 pair
-__device__ __forceinline__ uint32_t rest_h2(float a, float b, uint32_t p) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
-  return pack_h2(a - f.x, b - f.y);
-}
-
 using tc::bulk_load;
 
 // 8 x 8 transposition of fp16 pairs across the warp: thread (g, t) gives elements (g, 2t..2t+1)

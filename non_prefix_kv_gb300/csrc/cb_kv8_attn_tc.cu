@@ -1,5 +1,5 @@
-// Attention of many query rows over the 8-bit block-scaled KV cache on the tensor cores (bf16,
-// head_dim 64 or 128), and the attention weight each cache row receives from them.
+// Attention of many query rows over the 8-bit block-scaled KV cache on the tensor cores
+// (head_dim 64 or 128), and the attention weight each cache row receives from them.
 //
 // The mathematics is cb_kv8_attn.cu's: the codes enter the matrix instructions exactly, K's
 // scale multiplies a score, V's scale sits in the exponent (t = z + log2 vs) and leaves the
@@ -7,6 +7,8 @@
 //   S_j = Q C_K,j^T    tcgen05.mma, bf16 x bf16 (an 8-bit code is exact in bf16), into TMEM
 //   P_j = 2^(t - m)    softmax warps, fp16, back into TMEM
 //   O  += P_j C_V,j    tcgen05.mma, fp16 x fp16, P from TMEM
+// fp32 queries come, as there, as two fp16 parts of the row divided by a power of two, and P as two
+// fp16 parts; the two products of each kind add up in the same accumulator.
 // k_kv8_expand turns the codes into those two forms once per call, already in the swizzled
 // order the tensor cores read, so that a tile is one bulk copy and no tensor map is needed:
 // every key tile is read by n_q G / 128 CTAs, and converting it in each of them would cost
@@ -52,19 +54,30 @@ constexpr int ATTN_THREADS = 32 * NSOFT;           // of the attention kernel
 constexpr int THREADS = 32 * (2 + NSOFT);          // of the weights kernel
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NG = BN / 16;          // scale groups of a key tile
+// fp16 parts of q and of the weights (bf16 queries enter as they are)
+template <typename T>
+constexpr int parts() {
+  return sizeof(T) == 4 ? 2 : 1;
+}
+// floats per query row that the weights' kernel reads
+template <typename T>
+constexpr int row_words() {
+  return sizeof(T) == 4 ? 3 : 2;
+}
 constexpr float kPBias = 8.0f;       // as in cb_kv8_attn.cu: weights up to 2^8, 2^14 before m is raised
 constexpr float kLazy = 6.0f;
 
 struct Kv8Tc {
-  const bf16* q;
+  const void* q;
   const int32_t* last;      // [n_seq, n_q]
-  bf16* out;
-  uint8_t* kx;              // [n_seq * Hkv, tiles] key tiles in shared-memory order: bf16 codes
+  void* out;
+  uint8_t* kx;              // [n_seq * Hkv, tiles] key tiles in shared-memory order: bf16 codes (fp32 queries: fp16)
   uint8_t* vx;              // the same of V: fp16 codes
   int32_t* seq_max;         // [n_seq] the last row any query of the sequence sees (for the weights)
   // for the weights (else null), per (sequence, KV head, query tile):
   uint8_t* qx;              // the tile's query rows in shared-memory order
-  float* rows;              // [2][BM] log2 of each row's sum (+inf where there is none), last row it sees (int)
+  float* rows;              // [BM] log2 of each row's sum (+inf where there is none), [BM] last row it sees (int),
+                            // fp32: [BM] the row's power of two
   int32_t* tile_max;        // [n_seq, query tiles] the last row any query of the tile sees
   float* weights;           // [n_seq, Hkv, capacity]
   cb_kv8_cache c;
@@ -112,7 +125,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool swap) {
 // 128-byte-swizzled slabs.  Tiles no query sees are skipped.  Bound by latency and L2 (34 MB of
 // codes read, 67 MB written that the next kernel reads from L2): 15 us for 8 heads of 16384 rows,
 // 19 us with 16-byte stores.
-template <int HD>
+template <int HD, typename T>
 __global__ void __launch_bounds__(256) k_kv8_expand(const Kv8Tc p) {
   pdl_wait();
   pdl_trigger();
@@ -163,8 +176,8 @@ __global__ void __launch_bounds__(256) k_kv8_expand(const Kv8Tc p) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint32_t u = vw[c] ^ 0x80808080u;
-      ko[2 * c] = pair_bf16(kw[c], 0x4140);
-      ko[2 * c + 1] = pair_bf16(kw[c], 0x4342);
+      ko[2 * c] = sizeof(T) == 4 ? pair_f16(kw[c] ^ 0x80808080u, 0x4140) : pair_bf16(kw[c], 0x4140);
+      ko[2 * c + 1] = sizeof(T) == 4 ? pair_f16(kw[c] ^ 0x80808080u, 0x4342) : pair_bf16(kw[c], 0x4342);
       vo[2 * c] = pair_f16(u, 0x4140);
       vo[2 * c + 1] = pair_f16(u, 0x4342);
     }
@@ -194,7 +207,7 @@ template <int HD>
 __device__ __forceinline__ void gather_q(const Kv8Tc& p, int s, int h, int j0, uint8_t* dst, int tid, int n_thr) {
   constexpr int PER = HD / 8;              // 16-byte pieces in a row; n_thr is a multiple of it
   const int piece = tid % PER;
-  const bf16* q = p.q + ((int64_t)s * p.n_q * p.H + (int64_t)h * p.G) * HD + piece * 8;
+  const bf16* q = static_cast<const bf16*>(p.q) + ((int64_t)s * p.n_q * p.H + (int64_t)h * p.G) * HD + piece * 8;
   for (int r = tid / PER; r < BM; r += n_thr / PER) {
     const Row x = row_of(p, j0, r);
     const bf16* src = q + ((int64_t)(x.on ? x.j : 0) * p.H + (x.on ? x.g : 0)) * HD;
@@ -203,15 +216,56 @@ __device__ __forceinline__ void gather_q(const Kv8Tc& p, int s, int h, int j0, u
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
   }
 }
+// The same for fp32 queries, two threads per row: the row divided by a power of two (to rf; its
+// largest magnitude is then in [1, 2)) as two fp16 parts, one tile after the other.
+template <int HD>
+__device__ __forceinline__ void split_q(const Kv8Tc& p, int s, int h, int j0, uint8_t* dst, float* rf, int tid) {
+  const int r = tid >> 1, half = tid & 1;
+  const Row x = row_of(p, j0, r);
+  const float* src = static_cast<const float*>(p.q) +
+                     (((int64_t)s * p.n_q + (x.on ? x.j : 0)) * p.H + (int64_t)h * p.G + (x.on ? x.g : 0)) * HD + half * (HD / 2);
+  float amax = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < HD / 2; c += 4) {
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    if (x.on) ld4(src + c, f);
+    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
+  }
+  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  int e = amax > 0.f ? ilogbf(amax) : 0;
+  e = e < -120 ? -120 : (e > 120 ? 120 : e);
+  const float down = ldexpf(1.0f, -e);
+  if (half == 0) rf[r] = ldexpf(1.0f, e);
+#pragma unroll 2
+  for (int c = 0; c < HD / 16; ++c) {
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (x.on) {
+      ld4(src + c * 8, f);
+      ld4(src + c * 8 + 4, f + 4);
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = f[2 * i] * down, b = f[2 * i + 1] * down;
+      hi[i] = pack_h2(a, b);
+      lo[i] = rest_h2(a, b, hi[i]);
+    }
+    const int chunk = half * (HD / 16) + c;
+    uint8_t* d = dst + (chunk >> 3) * SLAB + r * 128 + (((chunk & 7) ^ (r & 7)) * 16);
+    *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(d + HD / 64 * SLAB) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ---- attention ------------------------------------------------------------------------------
-template <int HD, bool FUSED>
+template <int HD, bool FUSED, typename T>
 struct Layout {
   static constexpr int T_BYTES = HD / 64 * SLAB;             // a tile of Q, K or V
+  static constexpr int Q_BYTES = parts<T>() * T_BYTES;
   static constexpr int C_BYTES = FUSED ? BN * HD : 0;        // a tile of codes
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = T_BYTES;                      // [2 groups]
+  static constexpr int OFF_K = Q_BYTES;                      // [2 groups]
   static constexpr int OFF_V = OFF_K + 2 * T_BYTES;          // [2]
   static constexpr int OFF_C = OFF_V + 2 * T_BYTES;          // [2 groups][K, V] codes; the row statistics come there
                                                              // after the last ones are used up
@@ -274,7 +328,8 @@ __device__ __forceinline__ void convert_tile(const uint8_t* codes, uint8_t* dst,
 }
 
 // The largest t of a row's 128 scores.
-__device__ __forceinline__ float row_max(const uint32_t* sr, const float4* sc) {
+template <typename T>
+__device__ __forceinline__ float row_max(const uint32_t* sr, const float4* sc, float rf) {
   float mt = -INFINITY;
 #pragma unroll
   for (int gg = 0; gg < NG; ++gg) {
@@ -286,21 +341,23 @@ __device__ __forceinline__ float row_max(const uint32_t* sr, const float4* sc) {
       b = fmax3(b, __uint_as_float(x[2]), __uint_as_float(x[3]));
     }
     const float4 c = sc[gg];
-    mt = fmaxf(mt, fmaf(fmaxf(a, b), c.x, c.y));
+    mt = fmaxf(mt, fmaf(fmaxf(a, b), sizeof(T) == 4 ? c.x * rf : c.x, c.y));
   }
   return mt;
 }
-// P = 2^(t - m + bias) over S as fp16 pairs (keys 2w, 2w + 1 to column w), and its sum with
-// 1 / vs; an unseen score of -inf gives 0.
-__device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, const float4* sc, float off) {
+// P = 2^(t - m + bias) over S as fp16 pairs (keys 2w, 2w + 1 to column w; fp32: the parts left over
+// by the rounding 64 columns on), and its sum with 1 / vs; an unseen score of -inf gives 0.
+template <typename T>
+__device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, const float4* sc, float off, float rf) {
   float l = 0.f;
 #pragma unroll
   for (int c = 0; c < NG / 2; ++c) {
-    uint32_t pk[16];
+    uint32_t pk[16], lo[16];
 #pragma unroll
     for (int gg = 0; gg < 2; ++gg) {
       const float4 k = sc[2 * c + gg];
-      const uint64_t f2 = f2_pack(k.x, k.x), a2 = f2_pack(k.y + off, k.y + off);
+      const float f = sizeof(T) == 4 ? k.x * rf : k.x;
+      const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(k.y + off, k.y + off);
       uint64_t sum = 0ull;
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
@@ -308,13 +365,14 @@ __device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, co
         const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, a2));
         const float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
         sum = f2_add(sum, f2_pack(p0, p1));
-        const __half2 h2 = __floats2half2_rn(p0, p1);
-        pk[gg * 8 + w] = *reinterpret_cast<const uint32_t*>(&h2);
+        pk[gg * 8 + w] = pack_h2(p0, p1);
+        if constexpr (sizeof(T) == 4) lo[gg * 8 + w] = rest_h2(p0, p1, pk[gg * 8 + w]);
       }
       const float2 sm = f2_unpack(sum);
       l = fmaf(sm.x + sm.y, k.z, l);
     }
     tc::tmem_st16u_nowait(tS + c * 16, pk);
+    if constexpr (sizeof(T) == 4) tc::tmem_st16u_nowait(tS + BN / 2 + c * 16, lo);
   }
   return l;
 }
@@ -339,11 +397,12 @@ __device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, co
 // 85 rows of 40 heads over 6 x 16064 keys (987 MB of codes) 400 us instead of 651, 118 of 32 heads
 // over 1664 keys 16.5 instead of 21; with three query tiles (299 rows, 32 heads, 13440 keys) 182
 // instead of 163.
-template <int HD, bool FUSED>
+template <int HD, bool FUSED, typename T>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, int n_split) {
   pdl_wait();
   pdl_trigger();
-  using L = Layout<HD, FUSED>;
+  using L = Layout<HD, FUSED, T>;
+  constexpr int NP = parts<T>(), RW = row_words<T>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sQ = base + L::OFF_Q;
@@ -374,7 +433,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
     tc::tmem_alloc(tmem_slot, TMEM_COLS);
     tc::tmem_relinquish();
   }
-  gather_q<HD>(p, s, h, j0, sQ, tid, ATTN_THREADS);
+  if constexpr (NP == 2)
+    split_q<HD>(p, s, h, j0, sQ, cm, tid);
+  else
+    gather_q<HD>(p, s, h, j0, sQ, tid, ATTN_THREADS);
   // keys that some row of the tile sees
   int mx = -1;
   for (int i = tid; i < p.qpt; i += ATTN_THREADS) {
@@ -396,20 +458,21 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
   const uint32_t tmem = *tmem_slot;
 #pragma unroll
   for (int w = 0; w < ATTN_THREADS / 32; ++w) mx = max(mx, wm[w]);
-  __syncthreads();                 // wm's memory is the groups' row maxima later on
+  const float rf = NP == 2 ? cm[r] : 1.0f;
+  __syncthreads();                 // wm's memory is the groups' row maxima later on, cm's the CTA's
   // for the weights: the tile's queries as they sit in shared memory, and its bound
   const int64_t qt = head * p.q_tiles + blockIdx.y;
   if (p.weights && rank == 0 && tid == 0) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p.qx + qt * L::T_BYTES),
-                 "r"(tc::smem_u32(sQ)), "r"((uint32_t)L::T_BYTES)
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p.qx + qt * L::Q_BYTES),
+                 "r"(tc::smem_u32(sQ)), "r"((uint32_t)L::Q_BYTES)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     if (h == 0) p.tile_max[s * p.q_tiles + blockIdx.y] = mx;
   }
   const int64_t nk = (int64_t)mx + 1;
   const int all = (mx + BN) / BN;  // key tiles; 0 if no row sees a key
-  const int ta = (int)((int64_t)all * rank / n_split), T = (int)((int64_t)all * (rank + 1) / n_split) - ta;
-  const int nt = T > grp ? (T - grp + 1) / 2 : 0;     // this group's: ta + grp, ta + grp + 2, ...
+  const int ta = (int)((int64_t)all * rank / n_split), n_kt = (int)((int64_t)all * (rank + 1) / n_split) - ta;
+  const int nt = n_kt > grp ? (n_kt - grp + 1) / 2 : 0;     // this group's: ta + grp, ta + grp + 2, ...
 
   const Row x = row_of(p, j0, r);
   const int last = x.on ? last_of(p, s, x.j) : -1;
@@ -446,15 +509,17 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
     };
     auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); };
     auto issue_s = [&]() {
-      constexpr uint32_t idesc = tc::idesc_bf16_f32(BM, BN);
+      constexpr uint32_t idesc = NP == 2 ? tc::idesc_f16_f32(BM, BN) : tc::idesc_bf16_f32(BM, BN);
       const uint64_t qd = tc::desc_sw128(tc::smem_u32(sQ)), kd = tc::desc_sw128(tc::smem_u32(sK));
       tc::tc_fence_after();
       if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + grp * BN, qd + off, kd + off, idesc, k > 0);
-        }
+        for (int part = 0; part < NP; ++part)
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+            tc::mma_bf16(tmem + grp * BN, qd + ((part * L::T_BYTES) >> 4) + off, kd + off, idesc, part + k > 0);
+          }
         tc::mma_commit(s_full);
       }
       __syncwarp();
@@ -465,9 +530,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
       tc::tc_fence_after();
       if (tc::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < BN / 16; ++k)
-          tc::mma_bf16_ts(tmem + TM_O + grp * HD, tmem + grp * BN + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc,
-                          (add || k > 0) ? 1u : 0u);
+        for (int part = 0; part < NP; ++part)
+#pragma unroll
+          for (int k = 0; k < BN / 16; ++k)
+            tc::mma_bf16_ts(tmem + TM_O + grp * HD, tmem + grp * BN + part * (BN / 2) + k * 8,
+                            vd + (uint64_t)((k * 16 * 128) >> 4), idesc, (add || part + k > 0) ? 1u : 0u);
         tc::mma_commit(pv_done);
       }
       __syncwarp();
@@ -486,7 +553,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
         const float v = fmaxf(nx.v, kKv8MinScale);
         // (approximate log and reciprocal: off by 2^-22 of a value beside P's own 2^-12; the exact
         // forms cost 40 of 850 us at the Yi shape, by the few lanes that compute them)
-        sc[lane] = make_float4(fmaxf(nx.k, kKv8MinScale) * p.scale_log2, __log2f(v), __fdividef(1.0f, v), 0.f);
+        sc[lane] = make_float4(fmaxf(nx.k, kKv8MinScale) * p.scale_log2, NP == 2 ? log2f(v) : __log2f(v), __fdividef(1.0f, v), 0.f);
       }
       nx = load_scales(ks, vs, p.lg, tile + 2, nk, lane);
       __syncwarp();
@@ -505,7 +572,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
         for (int i = 0; i < BN; ++i)
           if (i > seen) sr[i] = 0xff800000u;
       }
-      const float mt = row_max(sr, sc);
+      const float mt = row_max<T>(sr, sc, rf);
       if (u == 0) {
         m_used = mt;             // O_g is written, not added to, by this tile's P V
       } else {
@@ -524,7 +591,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
           if (need) m_used = mt;
         }
       }
-      l += row_weights(sr, tS, sc, kPBias - (m_used == -INFINITY ? 0.f : m_used));
+      l += row_weights<T>(sr, tS, sc, kPBias - (m_used == -INFINITY ? 0.f : m_used), rf);
       tc::tmem_wait_st();
       tc::tc_fence_before();
     };
@@ -611,25 +678,28 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
         cm[r] = isnan(lt) ? lt : mm;       // (a NaN's scores leave no maximum; the row is not to look empty)
         cm[BM + r] = lt;
       } else if (p.weights) {
-        p.rows[qt * 2 * BM + r] = lt == 0.f ? INFINITY : mm - kPBias + log2f(lt);
+        p.rows[qt * RW * BM + r] = lt == 0.f ? INFINITY : mm - kPBias + log2f(lt);
       }
-      if (p.weights && rank == 0) p.rows[qt * 2 * BM + BM + r] = __int_as_float(last);
+      if (p.weights && rank == 0) {
+        p.rows[qt * RW * BM + BM + r] = __int_as_float(last);
+        if (NP == 2) p.rows[qt * RW * BM + 2 * BM + r] = rf;
+      }
     }
     // group g finalises columns [g HD/2, (g + 1) HD/2); O_g was never written with fewer than
     // g + 1 key tiles
     float* om = reinterpret_cast<float*>(base + L::OFF_K) + r * HD;
-    bf16* orow = p.out + (((int64_t)s * p.n_q + (x.on ? x.j : 0)) * p.H + (int64_t)h * p.G + (x.on ? x.g : 0)) * HD;
+    T* orow = static_cast<T*>(p.out) + (((int64_t)s * p.n_q + (x.on ? x.j : 0)) * p.H + (int64_t)h * p.G + (x.on ? x.g : 0)) * HD;
 #pragma unroll 1
     for (int c = 0; c < HD / 32; ++c) {
       const int col = grp * (HD / 2) + c * 16;
       float o0[16], o1[16];
-      if (T > 0) {
+      if (n_kt > 0) {
         tc::tmem_ld16(trow + TM_O + col, o0);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o0[i] = 0.f;
       }
-      if (T > 1) {
+      if (n_kt > 1) {
         tc::tmem_ld16(trow + TM_O + HD + col, o1);
       } else {
 #pragma unroll
@@ -679,8 +749,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
       const float inv = sum > 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[q] *= inv;
-      if (x.on) st4(p.out + (((int64_t)s * p.n_q + x.j) * p.H + (int64_t)h * p.G + x.g) * HD + 4 * w, o);
-      if (p.weights && w == 0) p.rows[qt * 2 * BM + r] = sum > 0.f ? M - kPBias + log2f(sum) : INFINITY;
+      if (x.on) st4(static_cast<T*>(p.out) + (((int64_t)s * p.n_q + x.j) * p.H + (int64_t)h * p.G + x.g) * HD + 4 * w, o);
+      if (p.weights && w == 0) p.rows[qt * RW * BM + r] = sum > 0.f ? M - kPBias + log2f(sum) : INFINITY;
     }
     tc::cluster_sync();            // the peers may still be reading this CTA's part
   }
@@ -704,16 +774,18 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
 //
 // FUSED (one query tile): K comes as codes, and a group converts its tile before it weighs it (85
 // rows of 40 heads over 6 x 16064 keys, attention and weights 701 us, 842 with the expansion).
-template <int HD, bool FUSED>
+template <int HD, bool FUSED, typename T>
 struct WLayout {
   static constexpr int T_BYTES = HD / 64 * SLAB;
   static constexpr int C_BYTES = FUSED ? BN * HD : 0;
-  static constexpr int QS = FUSED ? 2 : 4;                    // query tiles in flight
+  static constexpr int Q_BYTES = parts<T>() * T_BYTES;
+  static constexpr int L_BYTES = row_words<T>() * BM * 4;
+  static constexpr int QS = FUSED || parts<T>() == 2 ? 2 : 4; // query tiles in flight
   static constexpr int OFF_K = 0;                             // [2]
   static constexpr int OFF_Q = 2 * T_BYTES;                   // [QS]
-  static constexpr int OFF_C = OFF_Q + QS * T_BYTES;          // [2] codes
-  static constexpr int OFF_L = OFF_C + 2 * C_BYTES;           // [QS][2][BM] log2 sum, last
-  static constexpr int OFF_BAR = OFF_L + QS * 2 * BM * 4;
+  static constexpr int OFF_C = OFF_Q + QS * Q_BYTES;          // [2] codes
+  static constexpr int OFF_L = OFF_C + 2 * C_BYTES;           // [QS][row_words][BM] log2 sum, last, power of two
+  static constexpr int OFF_BAR = OFF_L + QS * L_BYTES;
   static constexpr int SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
 };
@@ -739,9 +811,10 @@ struct TileWalk {
   }
 };
 
-template <int HD, bool FUSED>
+template <int HD, bool FUSED, typename T>
 __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
-  using L = WLayout<HD, FUSED>;
+  using L = WLayout<HD, FUSED, T>;
+  constexpr int NP = parts<T>(), RW = row_words<T>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* sK = base + L::OFF_K;
@@ -823,9 +896,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
         if (!ok) break;
         if (lane == 0) {
           const int64_t qt = head * p.q_tiles + y;
-          tc::mbar_expect_tx(&q_full[b], L::T_BYTES + 2 * BM * 4);
-          tc::bulk_load(sQ + b * L::T_BYTES, p.qx + qt * L::T_BYTES, L::T_BYTES, &q_full[b]);
-          tc::bulk_load(base + L::OFF_L + b * 2 * BM * 4, p.rows + qt * 2 * BM, 2 * BM * 4, &q_full[b]);
+          tc::mbar_expect_tx(&q_full[b], L::Q_BYTES + L::L_BYTES);
+          tc::bulk_load(sQ + b * L::Q_BYTES, p.qx + qt * L::Q_BYTES, L::Q_BYTES, &q_full[b]);
+          tc::bulk_load(base + L::OFF_L + b * L::L_BYTES, p.rows + qt * RW * BM, L::L_BYTES, &q_full[b]);
         }
         __syncwarp();
       }
@@ -838,7 +911,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
     for (int i = n > L::QS ? n - L::QS : 0; i < n; ++i) tc::mbar_wait(&q_full[i % L::QS], (i / L::QS) & 1);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issue
-    constexpr uint32_t idesc = tc::idesc_bf16_f32(BN, BM);
+    constexpr uint32_t idesc = NP == 2 ? tc::idesc_f16_f32(BN, BM) : tc::idesc_bf16_f32(BN, BM);
     const uint64_t k_desc = tc::desc_sw128(tc::smem_u32(sK)), q_desc = tc::desc_sw128(tc::smem_u32(sQ));
     bool ok = true;
     int n = 0, kn[2] = {0, 0}, sn[2] = {0, 0};
@@ -855,12 +928,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
           if (!ok) break;
           tc::tc_fence_after();
           if (tc::elect_one()) {
-            const uint64_t kd = k_desc + (uint64_t)((g * L::T_BYTES) >> 4), qd = q_desc + (uint64_t)((b * L::T_BYTES) >> 4);
+            const uint64_t kd = k_desc + (uint64_t)((g * L::T_BYTES) >> 4), qd = q_desc + (uint64_t)((b * L::Q_BYTES) >> 4);
 #pragma unroll
-            for (int k = 0; k < HD / 16; ++k) {
-              const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
-              tc::mma_bf16(tmem + (2 * g + sb) * BM, kd + off, qd + off, idesc, k > 0);
-            }
+            for (int part = 0; part < NP; ++part)
+#pragma unroll
+              for (int k = 0; k < HD / 16; ++k) {
+                const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+                tc::mma_bf16(tmem + (2 * g + sb) * BM, kd + off, qd + ((part * L::T_BYTES) >> 4) + off, idesc, part + k > 0);
+              }
             tc::mma_commit(&s_full[2 * g + sb]);
             if (g == ng - 1) tc::mma_commit(&q_empty[b]);
             if (!FUSED && ahead < 0) tc::mma_commit(&k_empty[g]);
@@ -908,7 +983,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
           ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[2 * grp + (sn & 1)], (sn >> 1) & 1));
           if (!ok) break;
           tc::tc_fence_after();
-          const float* lse = sL + b * 2 * BM;
+          const float* lse = sL + b * RW * BM;
           const int* last = reinterpret_cast<const int*>(lse + BM);
           // the tile's rows either all see this warp's last key, or each is compared
           int lo = 0x7fffffff;
@@ -926,12 +1001,21 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
             tc::tmem_ld32_nowait(tS + c * 64 + 32, sr + 32);
             tc::tmem_wait_ld64(sr);
             uint64_t acc[2] = {0ull, 0ull};
+            // scores of rows i, i + 1 (fp32: in the row's own power of two)
+            auto scores = [&](int i) -> uint64_t {
+              const uint64_t x = f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1]));
+              if constexpr (NP == 2) {
+                const float2 e = *reinterpret_cast<const float2*>(lse + 2 * BM + c * 64 + i);
+                return f2_fma(x, f2_pack(e.x, e.y), 0ull);
+              }
+              return x;
+            };
             if (full) {
 #pragma unroll
               for (int i = 0; i < 64; i += 4) {
                 const float4 v = *reinterpret_cast<const float4*>(lse + c * 64 + i);
-                const float2 z0 = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), f2, f2_pack(-v.x, -v.y)));
-                const float2 z1 = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])), f2, f2_pack(-v.z, -v.w)));
+                const float2 z0 = f2_unpack(f2_fma(scores(i), f2, f2_pack(-v.x, -v.y)));
+                const float2 z1 = f2_unpack(f2_fma(scores(i + 2), f2, f2_pack(-v.z, -v.w)));
                 acc[0] = f2_add(acc[0], f2_pack(tc::ex2_approx(z0.x), tc::ex2_approx(z0.y)));
                 acc[1] = f2_add(acc[1], f2_pack(tc::ex2_approx(z1.x), tc::ex2_approx(z1.y)));
               }
@@ -940,7 +1024,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
               for (int i = 0; i < 64; i += 2) {
                 const float2 v = *reinterpret_cast<const float2*>(lse + c * 64 + i);
                 const int2 t = *reinterpret_cast<const int2*>(last + c * 64 + i);
-                const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), f2, f2_pack(-v.x, -v.y)));
+                const float2 z = f2_unpack(f2_fma(scores(i), f2, f2_pack(-v.x, -v.y)));
                 const float e0 = key <= t.x ? tc::ex2_approx(z.x) : 0.f, e1 = key <= t.y ? tc::ex2_approx(z.y) : 0.f;
                 acc[(i >> 1) & 1] = f2_add(acc[(i >> 1) & 1], f2_pack(e0, e1));
               }
@@ -976,19 +1060,22 @@ std::mutex g_tc_mu;
 uint32_t g_tc_attr[64];
 int g_tc_sms[64];
 
-template <int HD>
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+template <int HD, typename T>
 cudaError_t prepare_tc(int dev, int* sms) {
-  constexpr uint32_t bit = HD == 128 ? 1u : 2u;
+  constexpr uint32_t bit = (HD == 128 ? 1u : 2u) << (sizeof(T) == 4 ? 2 : 0);
   std::lock_guard<std::mutex> g(g_tc_mu);
   const bool cached = dev >= 0 && dev < 64;
   if (!cached || !(g_tc_attr[dev] & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_tc<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, true>::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_kv8_attn_tc<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, false>::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_kv8_weights_tc<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, WLayout<HD, true>::SMEM);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(k_kv8_weights_tc<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, WLayout<HD, false>::SMEM);
+    cudaError_t e = allow_smem(k_kv8_attn_tc<HD, false, T>, Layout<HD, false, T>::SMEM);
+    if (e == cudaSuccess) e = allow_smem(k_kv8_weights_tc<HD, false, T>, WLayout<HD, false, T>::SMEM);
+    if constexpr (sizeof(T) == 2) {
+      if (e == cudaSuccess) e = allow_smem(k_kv8_attn_tc<HD, true, T>, Layout<HD, true, T>::SMEM);
+      if (e == cudaSuccess) e = allow_smem(k_kv8_weights_tc<HD, true, T>, WLayout<HD, true, T>::SMEM);
+    }
     int n = 0;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -1003,13 +1090,13 @@ cudaError_t prepare_tc(int dev, int* sms) {
   return cudaSuccess;
 }
 
-template <int HD>
+template <int HD, typename T>
 cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (e = prepare_tc<HD>(dev, &sms)) != cudaSuccess) return e;
+  if (e != cudaSuccess || (e = prepare_tc<HD, T>(dev, &sms)) != cudaSuccess) return e;
   const bool fused = !p.kx;
-  if (!fused && (e = launch_k(k_kv8_expand<HD>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
+  if (!fused && (e = launch_k(k_kv8_expand<HD, T>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
   // one CTA per SM: the keys are split while that gives more of them work (64 queries of 8 x 7
   // heads over 16384 keys, 32 units, in 1 / 2 / 4 / 8 parts: 170, 102, 62, 94 us; 100 queries of 32
   // heads over 4096: 58, 45, 34, 55 us)
@@ -1019,7 +1106,6 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.Hkv * ns, p.q_tiles, p.c.n_seq);
   cfg.blockDim = dim3(ATTN_THREADS);
-  cfg.dynamicSmemBytes = fused ? Layout<HD, true>::SMEM : Layout<HD, false>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1030,12 +1116,20 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  if ((e = cudaLaunchKernelEx(&cfg, fused ? k_kv8_attn_tc<HD, true> : k_kv8_attn_tc<HD, false>, p, ns)) != cudaSuccess) return e;
-  if (!p.weights) return cudaSuccess;
   const int64_t items = (int64_t)p.c.n_seq * p.Hkv * ((p.tiles + 1) / 2);
   const dim3 grid((unsigned)(items < sms ? items : sms));
-  if (fused) return launch_k(k_kv8_weights_tc<HD, true>, grid, dim3(THREADS), WLayout<HD, true>::SMEM, s, p);
-  return launch_k(k_kv8_weights_tc<HD, false>, grid, dim3(THREADS), WLayout<HD, false>::SMEM, s, p);
+  auto run = [&](auto* attn, int bytes, auto* weigh, int wbytes) -> cudaError_t {
+    cfg.dynamicSmemBytes = bytes;
+    const cudaError_t r = cudaLaunchKernelEx(&cfg, attn, p, ns);
+    if (r != cudaSuccess || !p.weights) return r;
+    return launch_k(weigh, grid, dim3(THREADS), wbytes, s, p);
+  };
+  if constexpr (sizeof(T) == 2)
+    if (fused)
+      return run(k_kv8_attn_tc<HD, true, T>, Layout<HD, true, T>::SMEM, k_kv8_weights_tc<HD, true, T>,
+                 WLayout<HD, true, T>::SMEM);
+  return run(k_kv8_attn_tc<HD, false, T>, Layout<HD, false, T>::SMEM, k_kv8_weights_tc<HD, false, T>,
+             WLayout<HD, false, T>::SMEM);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -1050,52 +1144,57 @@ void reset_kv8_tc_caches() {
   }
 }
 
-// Which calls take this path: bf16, head_dim 64 or 128, and enough query rows per KV head.  Its
+// Which calls take this path: head_dim 64 or 128, and enough query rows per KV head.  Its
 // time hardly depends on the rows (up to a tile), the other's grows with every 8 of them.
 // 24 / 32 / 40 rows, hd 128, other's times and this one's: 32 heads over 4096 keys 33, 38, 41 and
 // 24 us; 8 over 16384 32, 35, 42 and 39 us; 8 sequences of 8 over 8192 61, 73, 87 and 71 us.  With
-// the weights, 16 / 24 rows: 46, 61 and 41 us; 48, 59 and 56 us; 115, 141 and 124 us.
+// the weights, 16 / 24 rows: 46, 61 and 41 us; 48, 59 and 56 us; 115, 141 and 124 us.  fp32, 32 / 48 /
+// 96 rows: 32 heads over 4096 keys 43, 54, 88 and 42 us; 8 over 16384 40, 54, 89 and 52 us; 4 sequences
+// of 4 over 8192 34, 43, 69 and 54 us; with the weights, 16 / 24 rows: 62, 86 and 58 us; 65, 85 and 68
+// us; 59, 71 and 68 us.
 bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights) {
-  return dt == DT_BF16 && (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > (weights ? 16 : 24) &&
+  return (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > (weights ? 16 : dt == DT_F32 ? 48 : 24) &&
          (n_q + BM / G - 1) / (BM / G) <= 65535;
 }
 
-// One query tile: the codes are converted where they are used.
-static bool is_fused(int G, int n_q) { return n_q <= BM / G; }
-bool kv8_tc_expands(int G, int n_q) { return !is_fused(G, n_q); }
+// One query tile: the codes are converted where they are used (fp32's two parts of q leave no room
+// for them).
+static bool is_fused(int dt, int G, int n_q) { return dt == DT_BF16 && n_q <= BM / G; }
+bool kv8_tc_expands(int dt, int G, int n_q) { return !is_fused(dt, G, n_q); }
 
 namespace {
 struct WsOff {
   size_t vx, seq_max, qx, rows, tile_max, bytes;
 };
-WsOff ws_of(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+WsOff ws_of(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
   const size_t tile = (size_t)BN * hd * 2, kt = (size_t)n_seq * Hkv * ((cap + BN - 1) / BN);
   const size_t qt = (n_q + BM / G - 1) / (BM / G), all = (size_t)n_seq * Hkv * qt;
   WsOff w{};
-  if (!is_fused(G, n_q)) {
+  if (!is_fused(dt, G, n_q)) {
     w.vx = align256(kt * tile);
     w.seq_max = w.vx + align256(kt * tile);
     w.qx = w.seq_max + align256((size_t)n_seq * 4);
   }
-  w.rows = w.qx + (weights ? align256(all * tile) : 0);
-  w.tile_max = w.rows + (weights ? align256(all * 2 * BM * 4) : 0);
+  const int np = dt == DT_F32 ? 2 : 1;
+  w.rows = w.qx + (weights ? align256(all * tile * np) : 0);
+  w.tile_max = w.rows + (weights ? align256(all * (np + 1) * BM * 4) : 0);
   w.bytes = w.tile_max + (weights ? align256((size_t)n_seq * qt * 4) : 0);
   return w;
 }
 }  // namespace
 
 // (the operands are written in 32-byte words: room to start on a boundary of those)
-size_t kv8_tc_ws_bytes(int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
-  const size_t n = ws_of(n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
+size_t kv8_tc_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, int hd, bool weights) {
+  const size_t n = ws_of(dt, n_seq, Hkv, G, n_q, cap, hd, weights).bytes;
   return n ? n + 32 : 0;
 }
 
-cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
+cudaError_t launch_kv8_tc(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
                           void* out, float* weights, void* ws, cudaStream_t s) {
   Kv8Tc p{};
-  p.q = static_cast<const bf16*>(q);
+  p.q = q;
   p.last = last;
-  p.out = static_cast<bf16*>(out);
+  p.out = out;
   p.c = c;
   p.n_q = n_q;
   p.H = H;
@@ -1107,9 +1206,9 @@ cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)hd);
   p.q_tiles = (n_q + p.qpt - 1) / p.qpt;
   p.g_magic = ((1 << 16) + p.G - 1) / p.G;
-  const WsOff w = ws_of(c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
+  const WsOff w = ws_of(dt, c.n_seq, Hkv, p.G, n_q, c.capacity, hd, weights != nullptr);
   uint8_t* b = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
-  if (!is_fused(p.G, n_q)) {
+  if (!is_fused(dt, p.G, n_q)) {
     p.kx = b;
     p.vx = b + w.vx;
     p.seq_max = reinterpret_cast<int32_t*>(b + w.seq_max);
@@ -1121,7 +1220,8 @@ cudaError_t launch_kv8_tc(const void* q, const int32_t* last, int n_q, const cb_
     if (!p.seq_max) p.seq_max = p.tile_max;      // one tile per sequence
     p.weights = weights;
   }
-  return hd == 128 ? launch_hd<128>(p, s) : launch_hd<64>(p, s);
+  if (dt == DT_F32) return hd == 128 ? launch_hd<128, float>(p, s) : launch_hd<64, float>(p, s);
+  return hd == 128 ? launch_hd<128, bf16>(p, s) : launch_hd<64, bf16>(p, s);
 }
 
 }  // namespace cb

@@ -298,6 +298,26 @@ def test_attention_where_the_paths_meet(B, H, hkv, hd, n_q, weigh):
         assert n >= B.cb_kv8_workspace_bytes(dims, n_seq, cap, n_q, False)
 
 
+@pytest.mark.parametrize("weigh", [False, True])
+@pytest.mark.parametrize("H,hkv,hd,n_q", [(2, 2, 128, 16), (2, 2, 64, 17), (2, 2, 128, 17), (4, 1, 128, 12), (2, 2, 128, 49),
+                                          (7, 1, 64, 7), (7, 1, 128, 40), (2, 1, 64, 150)])
+def test_attention_in_fp32_where_the_paths_meet(B, H, hkv, hd, n_q, weigh):
+    """As above; rows of very different magnitudes share a tile."""
+    torch = torch_mod()
+    g = np.random.default_rng(H + 1000 * n_q + hd)
+    cap, n_seq = 272, 2
+    lens = [cap, 130]
+    d, o = filled(B, g, n_seq, hkv, cap, hd, 16, lens)
+    q = (g.standard_normal((n_seq, n_q, H, hd)) * 10.0 ** g.integers(-6, 1, (n_seq, n_q, H, 1))).astype(np.float32)
+    q[0, 0, 0] = 0
+    last = np.stack([g.integers(-1, n, n_q) for n in lens])
+    last[:, -1] = [cap - 1, 127]
+    w = torch.zeros(n_seq, hkv, cap, device="cuda") if weigh else None
+    out = attend(B, d, q, last, make_dims(B, H, hkv, hd, "f32"), "f32", w)
+    B.cb_sync(None)
+    check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, "f32", hd)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n_q", [1, 3, 130])
 def test_attention_of_unlike_blocks(B, dtype, n_q):
