@@ -727,9 +727,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
     // ------------------------------------------------------------------ merge of the cluster
     tc::cluster_sync();
     const uint32_t cm_a = tc::smem_u32(cm), om_a = tc::smem_u32(base + L::OFF_K);
-    const int per = BM / n_split, r0 = rank * per;        // this CTA's share of the rows
+    const int per = (BM + n_split - 1) / n_split, r0 = rank * per, nr = min(per, BM - r0);   // this CTA's share of the rows
     constexpr int W4 = HD / 4;
-    for (int i = tid; i < per * W4; i += ATTN_THREADS) {
+    for (int i = tid; i < nr * W4; i += ATTN_THREADS) {
       const int r = r0 + i / W4, w = i % W4;
       const Row x = row_of(p, j0, r);
       float M = -INFINITY, sum = 0.f;
@@ -1055,57 +1055,67 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
   }
 }
 
-// shared-memory limits set per device and kernel, and SM counts, guarded for calls from several threads
+// Per device and kernel, set once its shared-memory limit is: how many clusters of 1..8 of its CTAs
+// run at once, and the SM count.  Guarded for calls from several threads.
+struct TcDevice {
+  int clusters[9];
+  int sms;
+};
 std::mutex g_tc_mu;
-uint32_t g_tc_attr[64];
-int g_tc_sms[64];
+TcDevice g_tc[64][6];        // (HD, T, FUSED)
 
 template <typename F>
 cudaError_t allow_smem(F* kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
-template <int HD, typename T>
-cudaError_t prepare_tc(int dev, int* sms) {
-  constexpr uint32_t bit = (HD == 128 ? 1u : 2u) << (sizeof(T) == 4 ? 2 : 0);
+template <int HD, bool FUSED, typename T>
+cudaError_t prepare_tc(int dev, TcDevice* out) {
+  constexpr int which = (HD == 128 ? 0 : 3) + (sizeof(T) == 4 ? 2 : FUSED ? 1 : 0);
   std::lock_guard<std::mutex> g(g_tc_mu);
   const bool cached = dev >= 0 && dev < 64;
-  if (!cached || !(g_tc_attr[dev] & bit)) {
-    cudaError_t e = allow_smem(k_kv8_attn_tc<HD, false, T>, Layout<HD, false, T>::SMEM);
-    if (e == cudaSuccess) e = allow_smem(k_kv8_weights_tc<HD, false, T>, WLayout<HD, false, T>::SMEM);
-    if constexpr (sizeof(T) == 2) {
-      if (e == cudaSuccess) e = allow_smem(k_kv8_attn_tc<HD, true, T>, Layout<HD, true, T>::SMEM);
-      if (e == cudaSuccess) e = allow_smem(k_kv8_weights_tc<HD, true, T>, WLayout<HD, true, T>::SMEM);
-    }
-    int n = 0;
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    *sms = n;
-    if (cached) {
-      g_tc_attr[dev] |= bit;
-      g_tc_sms[dev] = n;
-    }
+  if (cached && g_tc[dev][which].sms) {
+    *out = g_tc[dev][which];
     return cudaSuccess;
   }
-  *sms = g_tc_sms[dev];
-  return cudaSuccess;
+  cudaError_t e = allow_smem(k_kv8_attn_tc<HD, FUSED, T>, Layout<HD, FUSED, T>::SMEM);
+  if (e == cudaSuccess) e = allow_smem(k_kv8_weights_tc<HD, FUSED, T>, WLayout<HD, FUSED, T>::SMEM);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&out->sms, cudaDevAttrMultiProcessorCount, dev);
+  for (int ns = 1; e == cudaSuccess && ns <= 8; ++ns) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ns);
+    cfg.blockDim = dim3(ATTN_THREADS);
+    cfg.dynamicSmemBytes = Layout<HD, FUSED, T>::SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ns;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&out->clusters[ns], k_kv8_attn_tc<HD, FUSED, T>, &cfg);
+  }
+  if (e == cudaSuccess && cached) g_tc[dev][which] = *out;
+  return e;
 }
 
-template <int HD, typename T>
-cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
-  int dev = 0, sms = 0;
+template <int HD, bool FUSED, typename T>
+cudaError_t launch_variant(const Kv8Tc& p, cudaStream_t s) {
+  int dev = 0;
+  TcDevice d{};
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (e = prepare_tc<HD, T>(dev, &sms)) != cudaSuccess) return e;
-  const bool fused = !p.kx;
-  if (!fused && (e = launch_k(k_kv8_expand<HD, T>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess) return e;
-  // one CTA per SM: the keys are split while that gives more of them work (64 queries of 8 x 7
-  // heads over 16384 keys, 32 units, in 1 / 2 / 4 / 8 parts: 170, 102, 62, 94 us; 100 queries of 32
-  // heads over 4096: 58, 45, 34, 55 us)
+  if (e != cudaSuccess || (e = prepare_tc<HD, FUSED, T>(dev, &d)) != cudaSuccess) return e;
+  if (!FUSED &&
+      (e = launch_k(k_kv8_expand<HD, T>, dim3(p.tiles, p.Hkv, p.c.n_seq), dim3(256), 0, s, p)) != cudaSuccess)
+    return e;
+  // the keys are split as far as all parts still run at once, and have two tiles each (64 queries of 8
+  // x 7 heads over 16384 keys, 32 units, in 1 / 2 / 4 / 8 parts: 170, 102, 62, 94 us; 85 queries of 40
+  // heads over 16064, 40 units, in 2 / 3: 124, 88 us; 48 of 8 x 4 over 4096, 16 units, in 4 / 8: 30, 24)
   const int64_t units = (int64_t)p.q_tiles * p.Hkv * p.c.n_seq;
-  int ns = 1;
-  while (ns < 8 && units * ns * 2 <= sms && 2 * ns <= p.tiles) ns *= 2;
+  int ns = 8;
+  while (ns > 1 && (units > d.clusters[ns] || 2 * ns > p.tiles)) --ns;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.Hkv * ns, p.q_tiles, p.c.n_seq);
   cfg.blockDim = dim3(ATTN_THREADS);
+  cfg.dynamicSmemBytes = Layout<HD, FUSED, T>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1116,20 +1126,17 @@ cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  if ((e = cudaLaunchKernelEx(&cfg, k_kv8_attn_tc<HD, FUSED, T>, p, ns)) != cudaSuccess || !p.weights) return e;
   const int64_t items = (int64_t)p.c.n_seq * p.Hkv * ((p.tiles + 1) / 2);
-  const dim3 grid((unsigned)(items < sms ? items : sms));
-  auto run = [&](auto* attn, int bytes, auto* weigh, int wbytes) -> cudaError_t {
-    cfg.dynamicSmemBytes = bytes;
-    const cudaError_t r = cudaLaunchKernelEx(&cfg, attn, p, ns);
-    if (r != cudaSuccess || !p.weights) return r;
-    return launch_k(weigh, grid, dim3(THREADS), wbytes, s, p);
-  };
+  return launch_k(k_kv8_weights_tc<HD, FUSED, T>, dim3((unsigned)(items < d.sms ? items : d.sms)), dim3(THREADS),
+                  WLayout<HD, FUSED, T>::SMEM, s, p);
+}
+
+template <int HD, typename T>
+cudaError_t launch_hd(const Kv8Tc& p, cudaStream_t s) {
   if constexpr (sizeof(T) == 2)
-    if (fused)
-      return run(k_kv8_attn_tc<HD, true, T>, Layout<HD, true, T>::SMEM, k_kv8_weights_tc<HD, true, T>,
-                 WLayout<HD, true, T>::SMEM);
-  return run(k_kv8_attn_tc<HD, false, T>, Layout<HD, false, T>::SMEM, k_kv8_weights_tc<HD, false, T>,
-             WLayout<HD, false, T>::SMEM);
+    if (!p.kx) return launch_variant<HD, true, T>(p, s);
+  return launch_variant<HD, false, T>(p, s);
 }
 
 size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -1138,10 +1145,8 @@ size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 void reset_kv8_tc_caches() {
   std::lock_guard<std::mutex> g(g_tc_mu);
-  for (int i = 0; i < 64; ++i) {
-    g_tc_attr[i] = 0;
-    g_tc_sms[i] = 0;
-  }
+  for (auto& dev : g_tc)
+    for (auto& d : dev) d = TcDevice{};
 }
 
 // Which calls take this path: head_dim 64 or 128, and enough query rows per KV head.  Its

@@ -415,6 +415,42 @@ def test_attention_with_a_workspace_off_any_wider_boundary(B, n_q):
     assert torch.all(whole[:off] == 77) and torch.all(whole[off + n:] == 77)
 
 
+@pytest.mark.parametrize("weigh", [False, True])
+@pytest.mark.parametrize("n_seq", [1, 15, 17, 19, 22, 26, 34, 45, 80])
+def test_attention_in_any_number_of_parts(B, n_seq, weigh):
+    """The keys of a (sequence, KV head) are split over as many CTAs as run at once: 8 down to 1."""
+    torch = torch_mod()
+    g = np.random.default_rng(n_seq)
+    H, hkv, hd, n_q, cap = 2, 1, 64, 13, 2064
+    lens = [cap] + [int(x) for x in g.integers(1, cap + 1, n_seq - 1)]
+    d, o = filled(B, g, n_seq, hkv, cap, hd, 16, lens)
+    q = rounded(g.standard_normal((n_seq, n_q, H, hd)), "bf16")
+    last = np.stack([g.integers(-1, n, n_q) for n in lens])
+    last[:, 5] = np.array(lens) - 1
+    w = torch.zeros(n_seq, hkv, cap, device="cuda") if weigh else None
+    out = attend(B, d, q, last, make_dims(B, H, hkv, hd, "bf16"), "bf16", w)
+    B.cb_sync(None)
+    check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, "bf16", hd)
+
+
+def test_attention_without_a_workspace_where_none_is_asked_for(B):
+    """One query tile of bf16 rows and no weights need none; a capacity that ends inside a key tile."""
+    torch = torch_mod()
+    g = np.random.default_rng(77)
+    for H, hkv, hd, n_q, cap in ((2, 2, 128, 30, 16), (2, 2, 64, 128, 144), (14, 2, 128, 18, 1040)):
+        dims = make_dims(B, H, hkv, hd, "bf16")
+        assert B.cb_kv8_workspace_bytes(dims, 2, cap, n_q) == 0
+        d, o = filled(B, g, 2, hkv, cap, hd, 16, [cap, cap - 1])
+        q = rounded(g.standard_normal((2, n_q, H, hd)), "bf16")
+        last = g.integers(-1, cap - 1, (2, n_q))
+        last[1] = -1                                # a sequence without a row to see
+        out = torch.full((2, n_q, H, hd), 7.5, dtype=torch.bfloat16, device="cuda")
+        B.cb_kv8_attention(dev(q, "bf16"), dev_i32(last), n_q, d.c, dims, out)
+        B.cb_sync(None)
+        check_attention(out, None, K8.attention(o, q.astype(np.float64), last), last, "bf16", hd)
+        assert torch.all(out[1] == 0)
+
+
 def test_attention_reports_a_row_past_the_capacity(B):
     torch = torch_mod()
     g = np.random.default_rng(10)
