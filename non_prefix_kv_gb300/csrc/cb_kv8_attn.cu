@@ -181,7 +181,7 @@ __device__ __forceinline__ float* slot(const Kv8Attn& p, int hd, int worker, int
 // tiles per instruction stream where there are more than 8 rows, 32 rows of 32 heads over 4096
 // keys 48 us instead of 38.)  Now 144 us for the 841 MB, 5.85 TB/s, merge included; bound by the
 // bytes and, at a busy issue slot in two cycles, by the conversion of the codes.  One token of 32
-// heads over 4096 rows (34 MB): 11.5 us and 5 more for the merge, bound by start and latency.
+// heads over 4096 rows (34 MB): 11.3 us and 4.6 more for the merge, bound by start and latency.
 template <int HD, typename T>
 __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(const Kv8Attn p) {
   pdl_wait();

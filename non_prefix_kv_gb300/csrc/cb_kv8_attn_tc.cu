@@ -384,8 +384,8 @@ __device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, co
 // fills the gaps, and the eight warps (two per scheduler) may hold a row's 128 scores in
 // registers and read them once.  K's buffer is refilled as soon as S is there, V's once P V is
 // done: each load has most of a tile's chain to arrive, so one buffer per group suffices.
-// Measured (3328 rows of 56 heads over 16384 rows of 8, 973 GFLOP): 813 us, 1.20 PFLOP/s, bound
-// by the loop's hand-overs and products (without any softmax 698 us).  With a copying and an
+// Measured (3328 rows of 56 heads over 16384 rows of 8, 973 GFLOP): 801 us, 1.21 PFLOP/s, bound
+// by the loop's hand-overs and products (without any softmax 698 us), at 1370 of 1400 W.  With a copying and an
 // issuing warp, a ring of five tiles and the scores read twice for want of registers 1023 us; with
 // one accumulator, S two tiles ahead and the maximum handed on from tile to tile 883 us; with half
 // tiles and two score buffers per group 949 us; with two query tiles per CTA on shared key tiles
@@ -394,7 +394,7 @@ __device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, co
 // FUSED: the operands do not come ready from k_kv8_expand; the group that uses a tile converts it
 // itself, K while P V of the tile before runs, V while S runs.  That lengthens the loop by a half,
 // but where only one query tile reads the keys it saves writing and reading four bytes per code:
-// 85 rows of 40 heads over 6 x 16064 keys (987 MB of codes) 400 us instead of 651, 118 of 32 heads
+// 85 rows of 40 heads over 6 x 16064 keys (987 MB of codes) 388 us instead of 651, 118 of 32 heads
 // over 1664 keys 16.5 instead of 21; with three query tiles (299 rows, 32 heads, 13440 keys) 182
 // instead of 163.
 template <int HD, bool FUSED, typename T>
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
 // one CTA per key tile gathering the queries itself 55 us.
 //
 // FUSED (one query tile): K comes as codes, and a group converts its tile before it weighs it (85
-// rows of 40 heads over 6 x 16064 keys, attention and weights 701 us, 842 with the expansion).
+// rows of 40 heads over 6 x 16064 keys, attention and weights 681 us, 842 with the expansion).
 template <int HD, bool FUSED, typename T>
 struct WLayout {
   static constexpr int T_BYTES = HD / 64 * SLAB;

@@ -767,6 +767,29 @@ def test_captured_graphs_streams_and_a_shared_workspace(B):
         assert torch.equal(b["out"], b0["out"]) and torch.equal(b["w"], b0["w"]) and torch.equal(b["start"], b0["start"])
 
 
+@pytest.mark.parametrize("n_q", [1, 30, 150])
+def test_the_first_call_may_be_captured(B, n_q):
+    """What the library looks up once per device, it may look up while a graph is captured."""
+    torch = torch_mod()
+    g = np.random.default_rng(n_q)
+    H, hkv, hd, cap = 4, 2, 64, 528
+    d, o = filled(B, g, 1, hkv, cap, hd, 16, [cap])
+    q = rounded(g.standard_normal((1, n_q, H, hd)), "bf16")
+    last = g.integers(0, cap, (1, n_q))
+    dims = make_dims(B, H, hkv, hd, "bf16")
+    qd, ld, w = dev(q, "bf16"), dev_i32(last), torch.zeros(1, hkv, cap, device="cuda")
+    out = torch.zeros_like(qd)
+    ws = torch.empty(B.cb_kv8_workspace_bytes(dims, 1, cap, n_q, True), dtype=torch.uint8, device="cuda")
+    B.cb_sync(None)
+    B.cb_shutdown()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        B.cb_kv8_attention(qd, ld, n_q, d.c, dims, out, w, ws)
+    gr.replay()
+    B.cb_sync(None)
+    check_attention(out, host(w), K8.attention(o, q.astype(np.float64), last), last, "bf16", hd)
+
+
 class Answer:
     """One request over 8-bit caches: the prompt's rows, then a token per step, all lengths and
     positions on the device; the caches are thinned out in between.  see(cache, layer, q, k, v,
