@@ -252,8 +252,8 @@ int cb_kv8_append(const void* k, const void* v, int32_t n_rows, const int32_t* s
 int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* count,
                 int32_t n_rows, const cb_dims* dims, void* k_out, void* v_out, void* stream);
 
-/* Device workspace (bytes) of cb_kv8_attention at these sizes (16-byte aligned; what serves a
- * call with the weights serves one without).  Host-only. */
+/* Device workspace (bytes) of cb_kv8_attention at these sizes (16-byte aligned; 0: none is
+ * needed; what serves a call with the weights serves one without).  Host-only. */
 int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q,
                            int32_t with_weights, size_t* out_host);
 

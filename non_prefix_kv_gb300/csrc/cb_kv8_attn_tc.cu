@@ -385,11 +385,11 @@ __device__ __forceinline__ float row_weights(const uint32_t* sr, uint32_t tS, co
 // registers and read them once.  K's buffer is refilled as soon as S is there, V's once P V is
 // done: each load has most of a tile's chain to arrive, so one buffer per group suffices.
 // Measured (3328 rows of 56 heads over 16384 rows of 8, 973 GFLOP): 801 us, 1.21 PFLOP/s, bound
-// by the loop's hand-overs and products (without any softmax 698 us), at 1370 of 1400 W.  With a copying and an
-// issuing warp, a ring of five tiles and the scores read twice for want of registers 1023 us; with
-// one accumulator, S two tiles ahead and the maximum handed on from tile to tile 883 us; with half
-// tiles and two score buffers per group 949 us; with two query tiles per CTA on shared key tiles
-// 879 us.
+// by the loop's hand-overs and products (without any softmax 698 us), at 1370 of 1400 W.  With a
+// copying and an issuing warp, a ring of five tiles and the scores read twice for want of
+// registers 1023 us; with one accumulator, S two tiles ahead and the maximum handed on from tile to
+// tile 883 us; with half tiles and two score buffers per group 949 us; with two query tiles per CTA
+// on shared key tiles 879 us.
 //
 // FUSED: the operands do not come ready from k_kv8_expand; the group that uses a tile converts it
 // itself, K while P V of the tile before runs, V while S runs.  That lengthens the loop by a half,
