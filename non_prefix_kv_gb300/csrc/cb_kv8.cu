@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(256) k_kv8_read(const cb_kv8_cache c, int lg, 
 // values rank as 0.  One is added: 0 stands for a row that is not there.
 __device__ __forceinline__ uint32_t weight_key(float w) { return (w > 0.f ? __float_as_uint(w) : 0u) + 1u; }
 
-constexpr int kEvictThreads = 1024;
 constexpr int kEvictBins = 2048;         // 11-bit digits: three passes over the 32 key bits
 
 // One CTA per (head, sequence): radix select of the n_keep largest keys, where the first n_sink
@@ -253,20 +252,23 @@ constexpr int kEvictBins = 2048;         // 11-bit digits: three passes over the
 // counting and one scan over the threads places them; their keys stay in registers over all
 // passes (KPT of them: 4, 16 or 32 by the capacity; 8 heads of 16384 rows take 13 us with 16,
 // 34 us read again in each pass, 32 heads of 32768 rows 29 and 77 us).  With KPT = 0 (more rows
-// than 32 per thread) each pass reads the weights again.
-template <int KPT>
-__global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __restrict__ weights,
+// than 32 per thread) each pass reads the weights again.  Up to 1024 rows 256 threads do
+// (eviction and read-back of 512 rows of 32 heads 10.4 us, 12.2 with 1024 threads, of 208 rows of 8 x 40
+// heads 14.6 and 17.3; of 4096 rows of 32 heads 28.7 with 1024 threads, 31.2 with 256).
+template <int NT, int KPT>
+__global__ void __launch_bounds__(NT) k_kv8_select(const float* __restrict__ weights,
                                                               const int32_t* __restrict__ len, int64_t cap, int n_keep,
                                                               int n_sink, int n_recent, int64_t dcap,
                                                               int32_t* __restrict__ dst_len,
                                                               float* __restrict__ dst_weights,
                                                               int32_t* __restrict__ kept) {
+  constexpr int BPT = kEvictBins / NT;           // bins of a thread
   __shared__ int hist[3][kEvictBins];
   __shared__ int s_sum[32], s_eq[32];
   __shared__ int s_digit, s_left;
   const int h = blockIdx.x, Hkv = gridDim.x, s = blockIdx.y, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
-  for (int i = tid; i < 3 * kEvictBins; i += kEvictThreads) hist[0][i] = 0;
+  for (int i = tid; i < 3 * kEvictBins; i += NT) hist[0][i] = 0;
   pdl_wait();
   pdl_trigger();
   const int64_t head = (int64_t)s * Hkv + h;
@@ -280,13 +282,13 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
   float* dw = dst_weights ? dst_weights + head * dcap : nullptr;
   const int n_out = n < n_keep ? (int)n : n_keep;
   if (tid == 0 && h == 0) dst_len[s] = n_out;
-  for (int64_t i = n_out + tid; i < n_keep; i += kEvictThreads) out[i] = -1;
+  for (int64_t i = n_out + tid; i < n_keep; i += NT) out[i] = -1;
   if (dw)
-    for (int64_t i = n_out + tid; i < dcap; i += kEvictThreads) dw[i] = 0.f;
+    for (int64_t i = n_out + tid; i < dcap; i += NT) dw[i] = 0.f;
   bool bad = false;
   auto look = [&](float v) { bad = bad || !(v >= 0.f) || isinf(v); };
   if (n <= n_keep) {
-    for (int i = tid; i < (int)n; i += kEvictThreads) {
+    for (int i = tid; i < (int)n; i += NT) {
       const float v = w[i];
       look(v);
       out[i] = i;
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
     return i >= (int)n ? 0u : i < n_sink || i >= hi ? ~0u : weight_key(v);
   };
   // this thread's rows: whole float4's, within the capacity (a multiple of 16)
-  const int run = KPT > 0 ? KPT : ((int)((n + kEvictThreads - 1) / kEvictThreads) + 3) & ~3, i0 = tid * run;
+  const int run = KPT > 0 ? KPT : ((int)((n + NT - 1) / NT) + 3) & ~3, i0 = tid * run;
   uint32_t key[KPT > 0 ? KPT : 1];
   auto load4 = [&](int i) -> float4 {
     return i < (int)n ? *reinterpret_cast<const float4*>(w + i) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -354,9 +356,17 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
       if (x != 0u && (x & mask) == prefix) atomicAdd(&hp[(x >> shift) & dmask], 1);
     });
     __syncthreads();
-    // thread t owns bins 2047 - 2t and 2046 - 2t: inclusive scan from the top
-    const int2 c = *reinterpret_cast<const int2*>(&hp[kEvictBins - 2 - 2 * tid]);
-    int incl = c.x + c.y;
+    // thread t owns the BPT bins below 2048 - BPT t: inclusive scan from the top
+    const int top = kEvictBins - 1 - BPT * tid;
+    int c[BPT], own = 0;
+#pragma unroll
+    for (int i = 0; i < BPT; i += 2) {
+      const int2 v = *reinterpret_cast<const int2*>(&hp[top - 1 - i]);
+      c[i] = v.y;
+      c[i + 1] = v.x;
+      own += v.x + v.y;
+    }
+    int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -365,11 +375,17 @@ __global__ void __launch_bounds__(kEvictThreads) k_kv8_select(const float* __res
     if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
     incl += __reduce_add_sync(0xffffffffu, lane < warp ? s_sum[lane] : 0);
-    const int excl = incl - c.x - c.y;
+    int excl = incl - own;
     if (excl < left && incl >= left) {     // exactly one thread
-      const bool second = excl + c.y < left;
-      s_digit = kEvictBins - 1 - 2 * tid - (second ? 1 : 0);
-      s_left = left - excl - (second ? c.y : 0);
+      int i = 0;
+#pragma unroll
+      for (int q = 0; q < BPT - 1; ++q)
+        if (i == q && excl + c[q] < left) {
+          excl += c[q];
+          ++i;
+        }
+      s_digit = top - i;
+      s_left = left - excl;
     }
     __syncthreads();
     prefix |= (uint32_t)s_digit << shift;
@@ -553,13 +569,14 @@ cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const f
                               int n_recent, int64_t dcap, int32_t* dst_len, float* dst_weights, int32_t* kept, int Hkv,
                               cudaStream_t s) {
   const dim3 grid(Hkv, c.n_seq);
-#define CB_SELECT(KPT)                                                                                              \
-  return launch_k(k_kv8_select<KPT>, grid, dim3(kEvictThreads), 0, s, weights, len, c.capacity, n_keep, n_sink, n_recent, \
-                  dcap, dst_len, dst_weights, kept)
-  if (c.capacity <= 4 * kEvictThreads) CB_SELECT(4);
-  if (c.capacity <= 16 * kEvictThreads) CB_SELECT(16);
-  if (c.capacity <= 32 * kEvictThreads) CB_SELECT(32);
-  CB_SELECT(0);
+#define CB_SELECT(NT, KPT)                                                                                          \
+  return launch_k(k_kv8_select<NT, KPT>, grid, dim3(NT), 0, s, weights, len, c.capacity, n_keep, n_sink, n_recent, dcap, \
+                  dst_len, dst_weights, kept)
+  if (c.capacity <= 4 * 256) CB_SELECT(256, 4);
+  if (c.capacity <= 4 * 1024) CB_SELECT(1024, 4);
+  if (c.capacity <= 16 * 1024) CB_SELECT(1024, 16);
+  if (c.capacity <= 32 * 1024) CB_SELECT(1024, 32);
+  CB_SELECT(1024, 0);
 #undef CB_SELECT
 }
 

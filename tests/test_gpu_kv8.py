@@ -568,6 +568,29 @@ def test_evict_where_the_kernels_meet(B, cap):
     check_cache(t, rd, rl)
 
 
+@pytest.mark.parametrize("cap", [16, 112, 1008, 1024, 1040])
+def test_evict_of_short_caches(B, cap):
+    torch = torch_mod()
+    g = np.random.default_rng(cap)
+    hkv, hd, block, keep = 3, 64, 16, max(2, cap // 3)
+    sink, recent = min(3, keep - 1), keep // 4
+    lens = [cap, cap - 1, keep + 1, keep]
+    d, o = filled(B, g, 4, hkv, cap, hd, block, lens)
+    w = (g.uniform(0, 1, (4, hkv, cap)) ** 8).astype(np.float32)
+    w[:, 1] = g.integers(0, 2, (4, cap))
+    w[0, 2] = np.exp(-np.arange(cap) % 7 * 11.0)          # many digits of the keys in use
+    t = Dev(B, 4, hkv, -(-keep // block) * block, hd, block)
+    dl = torch.zeros(4, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(4, hkv, keep, dtype=torch.int32, device="cuda")
+    B.cb_kv8_evict(d.c, dev_i32(lens), torch.from_numpy(w).cuda(), keep, sink, recent, t.c, dl, None, kept,
+                   make_dims(B, hkv, hkv, hd, "bf16"))
+    B.cb_sync(None)
+    rd, rl, _, rk = K8.evict(o, lens, w, keep, sink, recent, -(-keep // block) * block)
+    np.testing.assert_array_equal(kept.cpu().numpy(), rk)
+    np.testing.assert_array_equal(dl.cpu().numpy(), rl)
+    check_cache(t, rd, rl)
+
+
 def test_evict_of_a_long_cache_and_bad_weights(B):
     torch = torch_mod()
     g = np.random.default_rng(12)
