@@ -433,10 +433,13 @@ class _Torch:
         self.row = {CB_F32: torch.float32, CB_BF16: torch.bfloat16}
         self.cb = {v: k for k, v in self.row.items()}
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_device = getattr(torch._C, "_cuda_getDevice", None)
 
     def device(self) -> int:
         cuda = self.mod.cuda
-        return cuda.current_device() if cuda.is_initialized() or cuda.is_available() else -2
+        if cuda.is_initialized() and self.raw_device is not None:
+            return self.raw_device()
+        return cuda.current_device() if cuda.is_available() else -2
 
     def stream(self, stream, dev: int):
         if stream is None and self.raw_stream is not None and dev >= 0:
