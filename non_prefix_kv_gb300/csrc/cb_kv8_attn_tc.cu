@@ -772,8 +772,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
 // the exponentials' chain from TMEM (33% of the issue slots, 32% of the special functions' rate);
 // one CTA per key tile gathering the queries itself 55 us.
 //
-// FUSED (one query tile): K comes as codes, and a group converts its tile before it weighs it (85
-// rows of 40 heads over 6 x 16064 keys, attention and weights 681 us, 842 with the expansion).
+// FUSED (one query tile): K comes as codes, and a group converts the next pair's tile as soon as S of
+// this one's has come, before it weighs (85 rows of 40 heads over 6 x 16064 keys, attention and
+// weights 650 us; converting after weighing 681, with the expansion 842).
 template <int HD, bool FUSED, typename T>
 struct WLayout {
   static constexpr int T_BYTES = HD / 64 * SLAB;
@@ -858,14 +859,29 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
 
   const int pairs = (p.tiles + 1) / 2;
   const int64_t items = (int64_t)p.c.n_seq * p.Hkv * pairs;
-  // calls f(head, sequence, first key tile, whether a query sees the second) for this CTA's pairs
-  auto each = [&](auto&& f) {
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-      const int64_t head = it / pairs;
-      const int s = (int)(head / p.Hkv), kt = 2 * (int)(it - head * pairs), mx = p.seq_max[s];
-      if (kt * BN > mx) continue;
-      if (!f(head, s, kt, kt + 1 < p.tiles && (kt + 1) * BN <= mx)) break;
+  struct Pair {
+    int64_t it, head;
+    int s, kt;            // sequence, first key tile
+    bool two;             // a query sees the second
+  };
+  // this CTA's first pair from `it` on that a query sees
+  auto find = [&](int64_t it, Pair& x) -> bool {
+    for (; it < items; it += gridDim.x) {
+      x.it = it;
+      x.head = it / pairs;
+      x.s = (int)(x.head / p.Hkv);
+      x.kt = 2 * (int)(it - x.head * pairs);
+      const int mx = p.seq_max[x.s];
+      if (x.kt * BN > mx) continue;
+      x.two = x.kt + 1 < p.tiles && (x.kt + 1) * BN <= mx;
+      return true;
     }
+    return false;
+  };
+  auto each = [&](auto&& f) {
+    Pair x;
+    for (bool more = find(blockIdx.x, x); more; more = find(x.it + gridDim.x, x))
+      if (!f(x.head, x.s, x.kt, x.two)) break;
   };
 
   if (warp == 0) {
@@ -954,20 +970,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
     const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16) + grp * 2 * BM;
     bool ok = true;
     int n = 0, sn = 0, kn = 0;
-    each([&](int64_t head, int s, int kt, bool two) -> bool {
-      const bool mine = grp == 0 || two;
-      if (FUSED && mine) {                       // (the products of the pair before are done with K: its last S was waited for)
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&k_full[grp], kn & 1));
-        if (!ok) return false;
-        ++kn;
-        convert_tile<HD, false>(base + L::OFF_C + grp * L::C_BYTES, sK + grp * L::T_BYTES, r);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&k_empty[grp]);
-          tc::mbar_arrive(&k_conv[grp]);
-        }
+    // K of a pair from its codes; the products of the pair before are done with it
+    auto convert = [&](const Pair& x) {
+      if (grp == 1 && !x.two) return;
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&k_full[grp], kn & 1));
+      if (!ok) return;
+      ++kn;
+      convert_tile<HD, false>(base + L::OFF_C + grp * L::C_BYTES, sK + grp * L::T_BYTES, r);
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&k_empty[grp]);
+        tc::mbar_arrive(&k_conv[grp]);
       }
+    };
+    // on_scores() runs each time S of this group's tile has come
+    auto weigh = [&](int64_t head, int s, int kt, bool two, auto&& on_scores) -> bool {
+      const bool mine = grp == 0 || two;
       const int key = (kt + grp) * BN + r;
       float f = 0.f;
       if (mine && key < p.c.capacity)
@@ -981,6 +1000,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
         if (!ok) break;
         if (mine) {
           ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[2 * grp + (sn & 1)], (sn >> 1) & 1));
+          if (!ok) break;
+          on_scores();
           if (!ok) break;
           tc::tc_fence_after();
           const float* lse = sL + b * RW * BM;
@@ -1043,7 +1064,26 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
       }
       if (ok && mine && key < p.c.capacity && sum != 0.f) p.weights[head * p.c.capacity + key] += sum;
       return ok;
-    });
+    };
+    if constexpr (FUSED) {
+      // one query tile, so S comes once per pair: then K is free for the next pair's, whose S
+      // runs while this pair is weighed
+      Pair x, nx;
+      bool more = find(blockIdx.x, x);
+      if (more) convert(x);
+      while (ok && more) {
+        const bool next = find(x.it + gridDim.x, nx);
+        auto ahead = [&] {
+          if (next) convert(nx);
+        };
+        if (grp == 1 && !x.two) ahead();
+        if (!weigh(x.head, x.s, x.kt, x.two, ahead)) break;
+        more = next;
+        if (more) x = nx;
+      }
+    } else {
+      each([&](int64_t head, int s, int kt, bool two) { return weigh(head, s, kt, two, [] {}); });
+    }
     if (!ok && lane == 0) atomicOr(&g_err_kv8_tc, ERRBIT_TIMEOUT);
   }
   tc::tc_fence_before();
