@@ -750,7 +750,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[q] *= inv;
       if (x.on) st4(static_cast<T*>(p.out) + (((int64_t)s * p.n_q + x.j) * p.H + (int64_t)h * p.G + x.g) * HD + 4 * w, o);
-      if (p.weights && w == 0) p.rows[qt * RW * BM + r] = sum > 0.f ? M - kPBias + log2f(sum) : INFINITY;
+      // (as without a split: +inf only for a row that sees nothing, a NaN row's is NaN)
+      if (p.weights && w == 0) p.rows[qt * RW * BM + r] = sum == 0.f ? INFINITY : M - kPBias + log2f(sum);
     }
     tc::cluster_sync();            // the peers may still be reading this CTA's part
   }

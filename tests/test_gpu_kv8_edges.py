@@ -1,0 +1,51 @@
+"""The 8-bit cache's attention, its account of weights and the logit rules where they are easily
+wrong: queries that are not finite, padding, keys split over CTAs, tiny queries, very long
+caches, one buffer for calls of different sizes.  Oracle and tolerances as in test_gpu_kv8.py."""
+import numpy as np
+import pytest
+
+import oracle.kv8_oracle as K8
+from tests.gpu_util import dev, dev_i32, ensure_lib, host, tdt, torch_mod
+from tests.test_gpu_kv8 import (Dev, attend, check_attention, check_cache, filled, make_dims, rounded, run_logits)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    torch_mod()
+    ensure_lib()
+    from non_prefix_kv_gb300 import binding
+    return binding
+
+
+# Which kernels take the call: few rows in one tile and in more; one query tile (bf16 converts the
+# codes itself), several.  One sequence over 9 key tiles: the keys are split over a cluster.
+WAYS = [(2, 2, 64, 3), (4, 2, 64, 7), (2, 2, 64, 30), (2, 2, 128, 60), (4, 2, 64, 90), (2, 2, 128, 140)]   # H, hkv, hd, n_q
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,hkv,hd,n_q", WAYS)
+def test_a_nan_query_leaves_rows_it_does_not_see_alone_when_the_keys_are_split(B, H, hkv, hd, n_q, dtype):
+    """One query with a NaN sees the first 91 rows, all others the first 700 at least: several whole
+    key tiles lie in between."""
+    torch = torch_mod()
+    g = np.random.default_rng(n_q + 1)
+    cap = 1152
+    d, o = filled(B, g, 1, hkv, cap, hd, 32, [cap])
+    q = rounded(g.standard_normal((1, n_q, H, hd)), dtype)
+    last = g.integers(700, cap, (1, n_q))
+    last[0, 1] = 90
+    bad = q.copy()
+    bad[0, 1, H - 1, 17] = np.nan                   # a head of the last KV head
+    w = torch.zeros(1, hkv, cap, device="cuda")
+    out = attend(B, d, bad, last, make_dims(B, H, hkv, hd, dtype), dtype, w)
+    B.cb_sync(None)
+    assert torch.all(torch.isnan(out[0, 1, H - 1])) and torch.all(torch.isnan(w[0, hkv - 1, :91]))
+    out[0, 1, H - 1] = 0
+    w[0, hkv - 1, :91] = 0
+    q[0, 1, H - 1] = 0
+    ref = list(K8.attention(o, q.astype(np.float64), last))
+    ref[0][0, 1, H - 1] = 0
+    ref[1][0, hkv - 1, :91] = 0
+    check_attention(out, host(w), ref, last, dtype, hd)
