@@ -76,7 +76,7 @@ struct Kv8Tc {
   int32_t* seq_max;         // [n_seq] the last row any query of the sequence sees (for the weights)
   // for the weights (else null), per (sequence, KV head, query tile):
   uint8_t* qx;              // the tile's query rows in shared-memory order
-  float* rows;              // [BM] log2 of each row's sum (+inf where there is none), [BM] last row it sees (int),
+  float* rows;              // [BM] log2 of each row's sum (+inf where there is none), [BM] last row it sees (int; -1: none),
                             // fp32: [BM] the row's power of two
   int32_t* tile_max;        // [n_seq, query tiles] the last row any query of the tile sees
   float* weights;           // [n_seq, Hkv, capacity]
@@ -460,6 +460,18 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
   for (int w = 0; w < ATTN_THREADS / 32; ++w) mx = max(mx, wm[w]);
   const float rf = NP == 2 ? cm[r] : 1.0f;
   __syncthreads();                 // wm's memory is the groups' row maxima later on, cm's the CTA's
+  // For the weights a query that sees nothing is a row of zeros like one that does not exist: it may
+  // hold a NaN or an infinity, whose scores the weights' mask-free sum could not tell from others.
+  // (Comparing every key with -1 there instead: 85 padded rows x 6, 40 heads, 661 us instead of 650.)
+  if (p.weights) {
+    const Row y = row_of(p, j0, tid >> 1);
+    if (y.on && last_of(p, s, y.j) < 0)
+#pragma unroll 1
+      for (int i = tid & 1; i < L::Q_BYTES / SLAB * 8; i += 2)
+        *reinterpret_cast<uint4*>(sQ + (i >> 3) * SLAB + (tid >> 1) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+    tc::fence_proxy_async_smem();
+    __syncthreads();
+  }
   // for the weights: the tile's queries as they sit in shared memory, and its bound
   const int64_t qt = head * p.q_tiles + blockIdx.y;
   if (p.weights && rank == 0 && tid == 0) {
@@ -1007,12 +1019,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
           tc::tc_fence_after();
           const float* lse = sL + b * RW * BM;
           const int* last = reinterpret_cast<const int*>(lse + BM);
-          // the tile's rows either all see this warp's last key, or each is compared
+          // the tile's queries either all see this warp's last key, or each is compared, whatever its
+          // sum (a NaN's score stays one beside +inf).  Rows that see nothing are zeros: they weigh 0.
           int lo = 0x7fffffff;
 #pragma unroll
           for (int i = 0; i < BM / 32; ++i) {
             const int v = last[i * 32 + lane];
-            lo = min(lo, lse[i * 32 + lane] == INFINITY ? 0x7fffffff : v);      // a row without a sum weighs 0 anyway
+            lo = min(lo, v < 0 ? 0x7fffffff : v);
           }
           const bool full = __reduce_min_sync(0xffffffffu, lo) >= (kt + grp) * BN + quad * 32 + 31;
           const uint32_t tS = trow + (sn & 1) * BM;

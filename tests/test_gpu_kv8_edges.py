@@ -24,6 +24,29 @@ def B():
 WAYS = [(2, 2, 64, 3), (4, 2, 64, 7), (2, 2, 64, 30), (2, 2, 128, 60), (4, 2, 64, 90), (2, 2, 128, 140)]   # H, hkv, hd, n_q
 
 
+# ------------------------------------------------------------------ queries that are not finite
+@pytest.mark.parametrize("what", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,hkv,hd,n_q", WAYS)
+def test_padding_weighs_nothing_whatever_it_holds(B, H, hkv, hd, n_q, dtype, what):
+    """Queries that see nothing (last = -1) may hold anything; the others see whole key tiles."""
+    torch = torch_mod()
+    g = np.random.default_rng(n_q)
+    cap = 1152
+    d, o = filled(B, g, 1, hkv, cap, hd, 32, [cap])
+    q = rounded(g.standard_normal((1, n_q, H, hd)), dtype)
+    last = np.sort(g.integers(cap - 100, cap, (1, n_q)))
+    pad = [0, n_q // 2, n_q - 1]
+    last[0, pad] = -1
+    bad = q.copy()
+    bad[0, pad] = what
+    w = torch.zeros(1, hkv, cap, device="cuda")
+    out = attend(B, d, bad, last, make_dims(B, H, hkv, hd, dtype), dtype, w)
+    B.cb_sync(None)
+    assert torch.all(out[0, pad] == 0)
+    check_attention(out, host(w), K8.attention(o, q.astype(np.float64), last), last, dtype, hd)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("H,hkv,hd,n_q", WAYS)
 def test_a_nan_query_leaves_rows_it_does_not_see_alone_when_the_keys_are_split(B, H, hkv, hd, n_q, dtype):
@@ -48,4 +71,29 @@ def test_a_nan_query_leaves_rows_it_does_not_see_alone_when_the_keys_are_split(B
     ref = list(K8.attention(o, q.astype(np.float64), last))
     ref[0][0, 1, H - 1] = 0
     ref[1][0, hkv - 1, :91] = 0
+    check_attention(out, host(w), ref, last, dtype, hd)
+
+
+@pytest.mark.parametrize("what", [np.inf, -np.inf])
+@pytest.mark.parametrize("cap", [160, 1152])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,hkv,hd,n_q", WAYS)
+def test_an_infinite_query_spoils_only_its_own_rows(B, H, hkv, hd, n_q, dtype, cap, what):
+    torch = torch_mod()
+    g = np.random.default_rng(n_q + 2)
+    d, o = filled(B, g, 1, hkv, cap, hd, 32, [cap])
+    q = rounded(g.standard_normal((1, n_q, H, hd)), dtype)
+    last = g.integers(cap * 2 // 3, cap, (1, n_q))
+    last[0, 1] = 50
+    bad = q.copy()
+    bad[0, 1, H - 1, 5] = what
+    w = torch.zeros(1, hkv, cap, device="cuda")
+    out = attend(B, d, bad, last, make_dims(B, H, hkv, hd, dtype), dtype, w)
+    B.cb_sync(None)
+    out[0, 1, H - 1] = 0
+    w[0, hkv - 1, :51] = 0
+    q[0, 1, H - 1] = 0
+    ref = list(K8.attention(o, q.astype(np.float64), last))
+    ref[0][0, 1, H - 1] = 0
+    ref[1][0, hkv - 1, :51] = 0
     check_attention(out, host(w), ref, last, dtype, hd)
