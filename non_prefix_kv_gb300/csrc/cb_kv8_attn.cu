@@ -41,6 +41,7 @@ constexpr int THREADS = 32 * WARPS;
 constexpr float kPBias = 8.0f;       // 2^(t - m) is held up to 2^8 ...
 constexpr float kLazy = 6.0f;        // ... and up to 2^14 before m is raised: fp16 ends at 2^16
 constexpr float kNone = -1e30f;      // m of a row that has seen no key
+constexpr float kMinFactor = 1.17549435e-38f;   // a score's factor is no smaller: times an unseen score of -inf, 0 is NaN
 constexpr int TILE = 8;              // query rows of a tile
 constexpr int MAX_WORKERS = 4096;    // warps of the largest grid (a workspace is sized without the device)
 
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<HD, T>()) k_kv8_attn(cons
         bool high = false;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          f[c] = rf[c] * sc.x;
+          f[c] = fmaxf(rf[c] * sc.x, kMinFactor);             // (below it no score reaches 2^-100)
           add[c] = sc.y - m_used[c] + kPBias;
         }
         if (!whole) {

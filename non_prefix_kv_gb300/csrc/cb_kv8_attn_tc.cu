@@ -217,7 +217,9 @@ __device__ __forceinline__ void gather_q(const Kv8Tc& p, int s, int h, int j0, u
   }
 }
 // The same for fp32 queries, two threads per row: the row divided by a power of two (to rf; its
-// largest magnitude is then in [1, 2)) as two fp16 parts, one tile after the other.
+// largest magnitude is then in [1, 2)) as two fp16 parts, one tile after the other.  rf >= 2^-120
+// keeps a score's factor rf ks log2(e) / sqrt(hd) above 0 (2^-149.55 at the least, hd 128 and ks
+// 1e-8, which rounds up to 2^-149): an unseen score of -inf times 0 would be NaN.
 template <int HD>
 __device__ __forceinline__ void split_q(const Kv8Tc& p, int s, int h, int j0, uint8_t* dst, float* rf, int tid) {
   const int r = tid >> 1, half = tid & 1;

@@ -97,3 +97,27 @@ def test_an_infinite_query_spoils_only_its_own_rows(B, H, hkv, hd, n_q, dtype, c
     ref[0][0, 1, H - 1] = 0
     ref[1][0, hkv - 1, :51] = 0
     check_attention(out, host(w), ref, last, dtype, hd)
+
+
+# ------------------------------------------------------------------ scores next to zero
+@pytest.mark.parametrize("weigh", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [2.0 ** -121, 2.0 ** -126, 2.0 ** -133])
+@pytest.mark.parametrize("hd,n_q", [(32, 1), (64, 1), (128, 3), (256, 1), (256, 3), (256, 12), (64, 20), (128, 60), (64, 140)])
+def test_tiny_queries_over_keys_of_zero(B, hd, n_q, size, dtype, weigh):
+    """The score's factor (query's magnitude times the smallest scale) lies below fp32's range; keys
+    past `last` share groups of 16 with visible ones.  Every visible row weighs the same."""
+    torch = torch_mod()
+    g = np.random.default_rng(hd + n_q)
+    hkv, cap, dims = 2, 48, make_dims(B, 2, 2, hd, dtype)
+    d, o = Dev(B, 1, hkv, cap, hd, 16), K8.empty(1, hkv, cap, hd, 16)
+    k, v = np.zeros((1, cap, hkv, hd), np.float32), g.standard_normal((1, cap, hkv, hd)).astype(np.float32)
+    B.cb_kv8_append(dev(k), dev(v), cap, dev_i32([0]), None, d.c, make_dims(B, 2, 2, hd, "f32"))
+    K8.append(o, k, v, [0])
+    q = rounded(g.uniform(-1, 1, (1, n_q, 2, hd)) * size, dtype)
+    last = g.integers(0, cap, (1, n_q))
+    last[0, 0] = 20
+    w = torch.zeros(1, hkv, cap, device="cuda") if weigh else None
+    out = attend(B, d, q, last, dims, dtype, w)
+    B.cb_sync(None)
+    check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, dtype, hd)
