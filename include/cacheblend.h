@@ -253,7 +253,8 @@ int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* 
                 int32_t n_rows, const cb_dims* dims, void* k_out, void* v_out, void* stream);
 
 /* Device workspace (bytes) of cb_kv8_attention at these sizes (16-byte aligned; 0: none is
- * needed; what serves a call with the weights serves one without).  Host-only. */
+ * needed; what serves a call with the weights serves one without).  Refuses the sizes that
+ * the call refuses.  Host-only. */
 int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q,
                            int32_t with_weights, size_t* out_host);
 
@@ -272,7 +273,10 @@ int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity,
  * Queries need no order, but launches of many queries run faster when last ascends.
  * The results are the same from run to run (no floating-point atomics).  Calls that use one
  * workspace or add to the same weights must be ordered by their stream.
- * head_dim 32, 64, 128 or 256. */
+ * head_dim 32, 64, 128 or 256.  At most 2^27 query rows per KV head (n_q H / Hkv) and, where the
+ * tensor cores do not take the call, ceil(n_q H / Hkv / 8) n_seq Hkv max(capacity / 16, 8) below
+ * 2^31 - 2^16.  They take head_dim 64 and 128 with at most 128 query heads per KV head, from 25
+ * query rows per KV head on (fp32 49; with the weights 17), up to 65535 tiles of 128 rows. */
 int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_kv8_cache* cache,
                      const cb_dims* dims, void* out, float* weights, void* ws, size_t ws_bytes,
                      void* stream);

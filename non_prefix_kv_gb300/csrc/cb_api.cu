@@ -1255,6 +1255,21 @@ size_t kv8_ws(const cb_dims* d, int n_seq, int64_t cap, int n_q, bool weights) {
     return kv8_tc_ws_bytes(d->dtype, n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
   return kv8_attn_ws_bytes(n_seq, d->n_kv_heads, G, n_q, cap, d->head_dim, weights);
 }
+
+// what the attention's kernels do not take, whoever asks: the call or the query for its workspace
+int check_kv8_attn(const cb_dims* d, int n_seq, int64_t cap, int n_q, bool weights) {
+  if (!kv8_attn_supported(d->head_dim))
+    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: head_dim %d is not 32, 64, 128 or 256", d->head_dim);
+  const int G = d->n_heads / d->n_kv_heads;
+  if ((int64_t)n_q * G > (1 << 27)) return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
+  // the few-row kernels count the line of work (row tile, sequence, head, 16 keys) and the rows to
+  // join in 32 bits; the tensor-core kernels have no such counter
+  if (!kv8_tc_taken(d->dtype, d->head_dim, G, n_q, weights) &&
+      (double)(((int64_t)n_q * G + 7) / 8) * n_seq * d->n_kv_heads * std::max((double)cap / 16, 8.0) >
+          (double)(INT32_MAX - 65536))
+    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: query rows, sequences, heads and capacity too many for one call");
+  return CB_OK;
+}
 }  // namespace
 
 int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q, int32_t with_weights,
@@ -1263,8 +1278,7 @@ int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity,
   if (st) return st;
   if (!out_host || n_seq < 1 || n_seq > 65535 || capacity < 1 || capacity > (1 << 30) || n_q < 0)
     return fail(CB_ERR_INVALID_ARG, "workspace query arguments");
-  if ((int64_t)n_q * (dims->n_heads / dims->n_kv_heads) > (1 << 27))
-    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
+  if ((st = check_kv8_attn(dims, n_seq, capacity, n_q, with_weights != 0))) return st;
   // what serves a call with the weights serves one without
   *out_host = kv8_ws(dims, n_seq, capacity, n_q, false);
   if (with_weights) *out_host = std::max(*out_host, kv8_ws(dims, n_seq, capacity, n_q, true));
@@ -1275,16 +1289,10 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
                      void* out, float* weights, void* ws, size_t ws_bytes, void* stream) {
   int st = check_dims(dims);
   if (st || (st = check_cache(cache, dims, "kv8_attention"))) return st;
-  if (!kv8_attn_supported(dims->head_dim))
-    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: head_dim %d is not 32, 64, 128 or 256", dims->head_dim);
   if (n_q < 0) return fail(CB_ERR_SHAPE, "n_q < 0");
+  if ((st = check_kv8_attn(dims, cache->n_seq, cache->capacity, n_q, weights != nullptr))) return st;
   if (n_q == 0) return CB_OK;
   const int H = dims->n_heads, Hkv = dims->n_kv_heads, hd = dims->head_dim, G = H / Hkv;
-  if ((int64_t)n_q * G > (1 << 27)) return fail(CB_ERR_UNSUPPORTED, "kv8_attention: more than 2^27 query rows per KV head");
-  // the line of work (row tile, sequence, head, 16 keys) and the rows to join are counted in 32 bits
-  if ((double)(((int64_t)n_q * G + 7) / 8) * cache->n_seq * Hkv * std::max((double)cache->capacity / 16, 8.0) >
-      (double)(INT32_MAX - 65536))
-    return fail(CB_ERR_UNSUPPORTED, "kv8_attention: query rows, sequences, heads and capacity too many for one call");
   if (!q || !last || !out) return fail(CB_ERR_INVALID_ARG, "kv8_attention pointer is NULL");
   if ((st = check_al16({q, out, weights, ws}, "kv8_attention"))) return st;
   const size_t need = kv8_ws(dims, cache->n_seq, cache->capacity, n_q, weights != nullptr);

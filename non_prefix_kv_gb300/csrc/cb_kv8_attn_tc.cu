@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
                  "r"(tc::smem_u32(sQ)), "r"((uint32_t)L::Q_BYTES)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    if (h == 0) p.tile_max[s * p.q_tiles + blockIdx.y] = mx;
+    if (h == 0) p.tile_max[(int64_t)s * p.q_tiles + blockIdx.y] = mx;
   }
   const int64_t nk = (int64_t)mx + 1;
   const int all = (mx + BN) / BN;  // key tiles; 0 if no row sees a key
@@ -920,7 +920,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
         }
         ++kn[g];
       }
-      TileWalk walk(p.tile_max + s * p.q_tiles, p.q_tiles, kt * BN, lane);
+      TileWalk walk(p.tile_max + (int64_t)s * p.q_tiles, p.q_tiles, kt * BN, lane);
       for (int y; ok && (y = walk.next()) >= 0; ++n) {
         const int b = n % L::QS;
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[b], ((n / L::QS) & 1) ^ 1));
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
     each([&](int64_t, int s, int kt, bool two) -> bool {
       const int ng = two ? 2 : 1;
       for (int g = 0; ok && g < ng; ++g) ok = __all_sync(0xffffffffu, tc::mbar_wait(FUSED ? &k_conv[g] : &k_full[g], kn[g]++ & 1));
-      TileWalk walk(p.tile_max + s * p.q_tiles, p.q_tiles, kt * BN, lane);
+      TileWalk walk(p.tile_max + (int64_t)s * p.q_tiles, p.q_tiles, kt * BN, lane);
       for (int y = walk.next(); ok && y >= 0; ++n) {
         const int b = n % L::QS, ahead = walk.next();
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (n / L::QS) & 1));
@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_kv8_weights_tc(const Kv8Tc p) {
         f = fmaxf(p.c.k_scale[head * (p.c.capacity >> p.lg) + (key >> p.lg)], kKv8MinScale) * p.scale_log2;
       const uint64_t f2 = f2_pack(f, f);
       float sum = 0.f;
-      TileWalk walk(p.tile_max + s * p.q_tiles, p.q_tiles, kt * BN, lane);
+      TileWalk walk(p.tile_max + (int64_t)s * p.q_tiles, p.q_tiles, kt * BN, lane);
       while (ok && walk.next() >= 0) {
         const int b = n % L::QS;
         ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[b], (n / L::QS) & 1));

@@ -121,3 +121,41 @@ def test_tiny_queries_over_keys_of_zero(B, hd, n_q, size, dtype, weigh):
     out = attend(B, d, q, last, dims, dtype, w)
     B.cb_sync(None)
     check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, dtype, hd)
+
+
+# ------------------------------------------------------------------ sizes
+@pytest.mark.parametrize("weigh", [False, True])
+def test_many_queries_over_many_rows(B, weigh):
+    """The few-row kernels count ceil(n_q G / 8) n_seq Hkv capacity / 16 in 32 bits; this call's 2^31
+    are no business of the tensor-core kernels."""
+    torch = torch_mod()
+    g = np.random.default_rng(0)
+    H, hkv, hd, n_q, cap, held = 8, 1, 64, 65536, 1 << 19, 96
+    c = [torch.zeros(1, hkv, cap, hd, dtype=torch.int8, device="cuda") for _ in range(2)]
+    sc = [torch.full((1, hkv, cap // 128), float("nan"), device="cuda") for _ in range(2)]
+    cache = B.kv8_cache(*c, *sc, 128)
+    o = K8.empty(1, hkv, 128, hd, 128)
+    k, v = (rounded(g.standard_normal((1, held, hkv, hd)), "bf16") for _ in range(2))
+    dims = make_dims(B, H, hkv, hd, "bf16")
+    B.cb_kv8_append(dev(k, "bf16"), dev(v, "bf16"), held, dev_i32([0]), None, cache, dims)
+    K8.append(o, k, v, [0])
+    q = torch.randn(1, n_q, H, hd, device="cuda").to(torch.bfloat16)
+    last = torch.full((1, n_q), -1, dtype=torch.int32, device="cuda")
+    rows = np.array([0, 1, 30000, n_q - 2, n_q - 1])
+    at = np.array([0, 50, 95, 31, 95])
+    last[0, torch.from_numpy(rows).cuda()] = dev_i32(at)
+    out = torch.full_like(q, 7.5)
+    w = torch.zeros(1, hkv, cap, device="cuda") if weigh else None
+    ws = torch.empty(B.cb_kv8_workspace_bytes(dims, 1, cap, n_q, weigh), dtype=torch.uint8, device="cuda")
+    B.cb_kv8_attention(q, last, n_q, cache, dims, out, w, ws)
+    B.cb_sync(None)
+    ref = K8.attention(o, host(q[:, rows]), at[None])
+    check_attention(out[:, rows], None, ref, at[None], "bf16", hd)
+    rest = torch.ones(n_q, dtype=torch.bool, device="cuda")
+    rest[torch.from_numpy(rows).cuda()] = False
+    assert torch.all(out[0, rest] == 0)
+    if weigh:
+        assert torch.all(w[..., held:] == 0)
+        # as in check_attention: exp's argument and ex2 twice, sums over 96 keys and 40 rows
+        r = 2 * (ref[3].max() * (hd + 4) * 2.0 ** -24 + 2.0 ** -21) + (held + 5 * H + 8) * 2.0 ** -24
+        assert np.all(np.abs(host(w[..., :held]) - ref[1][..., :held]) <= ref[1][..., :held] * r + 1e-30)

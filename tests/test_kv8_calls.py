@@ -1,0 +1,60 @@
+"""What the calls of the 8-bit cache and the logit rules take and refuse, on the host (no GPU is
+touched: every call here is refused before anything is launched)."""
+import ctypes
+
+import pytest
+
+from non_prefix_kv_gb300 import binding as B
+from non_prefix_kv_gb300 import build as nb
+
+FAKE = 0x10000
+
+
+@pytest.fixture(scope="module")
+def lib():
+    nb.build()
+    return B.lib()
+
+
+def _dims(**kw):
+    base = dict(d_model=256, n_heads=4, n_kv_heads=2, head_dim=64, d_ff=512, vocab=1024, rope_base=1e4,
+                rms_eps=1e-5, dtype=B.CB_BF16)
+    base.update(kw)
+    return B.cb_dims(**base)
+
+
+def _cache(**kw):
+    base = dict(k_codes=1 << 40, v_codes=1 << 42, k_scale=1 << 44, v_scale=1 << 45, capacity=256, n_seq=2, block=32)
+    base.update(kw)
+    return B.cb_kv8_cache(**base)
+
+
+def attention_status(lib, d, c, n_q, weights=None):
+    """Of a call without a workspace: 4 where only that is wrong with it."""
+    return lib.cb_kv8_attention(1 << 46, 1 << 47, n_q, ctypes.byref(c), ctypes.byref(d), 1 << 48, weights, None, 0, None)
+
+
+@pytest.mark.parametrize("kw,n_seq,cap,n_q,weights,ok", [
+    # beyond 2^31 steps of the few-row kernels, but on the tensor cores
+    (dict(n_heads=32, n_kv_heads=32, head_dim=128), 1, 131072, 131072, False, True),
+    (dict(n_heads=56, n_kv_heads=8, head_dim=128), 32, 16384, 16384, False, True),
+    (dict(n_heads=56, n_kv_heads=8, head_dim=128), 32, 16384, 16384, True, True),
+    (dict(n_heads=56, n_kv_heads=8, head_dim=128, dtype=B.CB_F32), 32, 16384, 16384, True, True),
+    # the same on the few-row kernels
+    (dict(n_heads=32, n_kv_heads=32, head_dim=256), 1, 131072, 131072, False, False),
+    (dict(n_heads=32, n_kv_heads=32, head_dim=32), 1, 131072, 131072, True, False),
+    (dict(n_heads=8, n_kv_heads=8, head_dim=128), 65535, 131072, 1, False, False),
+    (dict(n_heads=8, n_kv_heads=8, head_dim=128), 65535, 1024, 1, True, True),
+    # no kernel at all
+    (dict(n_heads=4, n_kv_heads=2, head_dim=96), 1, 256, 1, False, False),
+    (dict(n_heads=128, n_kv_heads=1, head_dim=128), 1, 256, (1 << 20) + 1, False, False)])
+def test_the_workspace_query_refuses_what_the_call_refuses(lib, kw, n_seq, cap, n_q, weights, ok):
+    d, c = _dims(**kw), _cache(n_seq=n_seq, capacity=cap)
+    w = 1 << 50 if weights else None
+    assert attention_status(lib, d, c, n_q, w) == (4 if ok else 8)
+    if ok:
+        assert B.cb_kv8_workspace_bytes(d, n_seq, cap, n_q, weights) > 0
+    else:
+        with pytest.raises(B.CBError) as e:
+            B.cb_kv8_workspace_bytes(d, n_seq, cap, n_q, weights)
+        assert e.value.status == 8
