@@ -254,7 +254,12 @@ int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* 
 
 /* Device workspace (bytes) of cb_kv8_attention at these sizes (16-byte aligned; 0: none is
  * needed; what serves a call with the weights serves one without).  Refuses the sizes that
- * the call refuses.  Host-only. */
+ * the call refuses.  Host-only.
+ * Fewer queries may need more (bf16, 32 heads of 128 over 4096 rows: 2.4 MB for 1, 17.4 MB for 24,
+ * none for 25 to 128, 67 MB for 129): a buffer for calls of several n_q is the largest of what
+ * each of them asks for.  A larger capacity or n_seq never needs less.
+ * With more than one tile of 128 query rows per KV head (fp32: always) the tensor-core path
+ * expands the codes to 16 bits here, over the whole capacity: twice the cache's own bytes. */
 int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity, int32_t n_q,
                            int32_t with_weights, size_t* out_host);
 

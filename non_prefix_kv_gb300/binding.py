@@ -520,6 +520,8 @@ def cb_kv8_read(cache: cb_kv8_cache, start, count, n_rows: int, dims: cb_dims, k
 
 
 def cb_kv8_workspace_bytes(dims: cb_dims, n_seq: int, capacity: int, n_q: int, with_weights: bool = False) -> int:
+    """Bytes for one call of these sizes.  Fewer queries may need more: for calls of several n_q on
+    one buffer take the largest of what each asks for."""
     out = _SZ(0)
     _check("cb_kv8_workspace_bytes", lib().cb_kv8_workspace_bytes(C.byref(dims), n_seq, capacity, n_q,
                                                                   1 if with_weights else 0, C.byref(out)))

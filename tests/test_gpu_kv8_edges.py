@@ -159,3 +159,28 @@ def test_many_queries_over_many_rows(B, weigh):
         # as in check_attention: exp's argument and ex2 twice, sums over 96 keys and 40 rows
         r = 2 * (ref[3].max() * (hd + 4) * 2.0 ** -24 + 2.0 ** -21) + (held + 5 * H + 8) * 2.0 ** -24
         assert np.all(np.abs(host(w[..., :held]) - ref[1][..., :held]) <= ref[1][..., :held] * r + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_one_workspace_for_calls_of_different_sizes(B, dtype):
+    """Fewer queries may ask for more: a buffer for several n_q is the largest of what each asks for."""
+    torch = torch_mod()
+    g = np.random.default_rng(1)
+    H, hkv, hd, cap = 8, 4, 128, 528
+    dims = make_dims(B, H, hkv, hd, dtype)
+    d, o = filled(B, g, 1, hkv, cap, hd, 16, [cap])
+    counts = [64, 1, 24, 4, 12, 65, 8, 30]
+    ask = [B.cb_kv8_workspace_bytes(dims, 1, cap, n, w) for n in counts for w in (False, True)]
+    ws = torch.full((max(ask),), 255, dtype=torch.uint8, device="cuda")
+    if dtype == "bf16":
+        assert B.cb_kv8_workspace_bytes(dims, 1, cap, 64) == 0 < B.cb_kv8_workspace_bytes(dims, 1, cap, 1)
+    for n in counts:
+        for weigh in (False, True):
+            q = rounded(g.standard_normal((1, n, H, hd)), dtype)
+            last = g.integers(-1, cap, (1, n))
+            qd = dev(q, dtype)
+            out = torch.full_like(qd, 7.5)
+            w = torch.zeros(1, hkv, cap, device="cuda") if weigh else None
+            B.cb_kv8_attention(qd, dev_i32(last), n, d.c, dims, out, w, ws)
+            B.cb_sync(None)
+            check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, dtype, hd)

@@ -58,3 +58,20 @@ def test_the_workspace_query_refuses_what_the_call_refuses(lib, kw, n_seq, cap, 
         with pytest.raises(B.CBError) as e:
             B.cb_kv8_workspace_bytes(d, n_seq, cap, n_q, weights)
         assert e.value.status == 8
+
+
+def test_what_a_workspace_for_several_query_counts_has_to_hold(lib):
+    """As the header says: not monotone in n_q (its figures), but in capacity and sequences; with the
+    weights at least what it is without."""
+    d = _dims(n_heads=32, n_kv_heads=32, head_dim=128)
+    ask = lambda n, cap=4096, ns=1, w=False, dd=d: B.cb_kv8_workspace_bytes(dd, ns, cap, n, w)  # noqa: E731
+    assert [round(ask(n) / 1e6, 1) for n in (1, 24, 25, 128, 129)] == [2.4, 17.4, 0, 0, 67.1]
+    for dt in (B.CB_BF16, B.CB_F32):
+        for hd in (32, 64, 128, 256):
+            dd = _dims(n_heads=8, n_kv_heads=2, head_dim=hd, dtype=dt)
+            for n in (1, 2, 3, 5, 12, 13, 32, 33, 100, 1000):
+                assert ask(n, w=True, dd=dd) >= ask(n, dd=dd)
+                for w in (False, True):
+                    assert ask(n, 4112, 1, w, dd) >= ask(n, 4096, 1, w, dd) and ask(n, 4096, 3, w, dd) >= ask(n, 4096, 2, w, dd)
+    # the expanded codes: 2 bytes for each of K's and V's
+    assert 0 <= ask(129) - 2 * 2 * 32 * 4096 * 128 < 4096
