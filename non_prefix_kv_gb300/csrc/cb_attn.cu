@@ -17,12 +17,7 @@ namespace cb {
 
 static __device__ uint32_t g_err_attn;
 
-uint32_t take_error_attn() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_attn, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_attn, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_attn() { return take_word(g_err_attn); }
 
 template <typename T, int DPL>
 __global__ void __launch_bounds__(128) k_attn_simt(const T* __restrict__ q, const int32_t* __restrict__ q_pos,

@@ -29,12 +29,7 @@ namespace cb {
 
 static __device__ uint32_t g_err_attn_tc;
 
-uint32_t take_error_attn_tc() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_attn_tc, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_attn_tc, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_attn_tc() { return take_word(g_err_attn_tc); }
 
 namespace {
 

@@ -136,6 +136,17 @@ inline bool pdl_enabled() {
   return on;
 }
 
+// Host side: the bits of an error word of the current device, cleared if there are any (a blocking
+// copy, and only then a second one).  cb_sync takes every file's word: the ones of files whose
+// kernels no call has launched are not asked for.  (Nine words copied and cleared: 120 us.)
+template <typename W>
+inline uint32_t take_word(W& word) {
+  uint32_t v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, word, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
+  if (v) cudaMemcpyToSymbol(word, &z, sizeof(z));
+  return v;
+}
+
 // Host side: launch with the programmatic-stream-serialization attribute.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,

@@ -9,12 +9,7 @@ namespace cb {
 
 static __device__ uint32_t g_err_gemm;
 
-uint32_t take_error_gemm() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_gemm, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_gemm, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_gemm() { return take_word(g_err_gemm); }
 
 // acc[m][n] = sum_k A[m][k] B[n][k]; 64x64 tile per 256-thread block, 4x4 per thread.
 // EPI_SWIGLU: the 64 tile columns are 32 gate rows (j) and their 32 up partners

@@ -7,18 +7,16 @@
 // rows be appended one at a time and lets attention apply it to a score or a probability: the
 // codes themselves enter the matrix instructions, exactly.  The layout is head-major, so a
 // head's block is one contiguous run of block * head_dim bytes.
+#include <atomic>
+
 #include "cb_kv8.cuh"
 
 namespace cb {
 
 static __device__ uint32_t g_err_kv8;
+static std::atomic<bool> g_used_kv8{false};   // a kernel of this file was launched (or captured)
 
-uint32_t take_error_kv8() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_kv8, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_kv8, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_kv8() { return g_used_kv8 ? take_word(g_err_kv8) : 0u; }
 
 namespace {
 
@@ -533,6 +531,7 @@ int log2_of(int block) { return 31 - __builtin_clz((unsigned)block); }
 
 cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, const int32_t* start,
                               const int32_t* count, const cb_kv8_cache& c, int Hkv, int hd, cudaStream_t s) {
+  g_used_kv8 = true;
   const int chunks = c.block * hd / 16, nch = chunks_per_thread(chunks, 512);
   // a run of n_rows rows touches at most this many blocks, wherever it starts
   const unsigned nb = (unsigned)(((int64_t)n_rows + 2 * c.block - 2) / c.block);
@@ -554,6 +553,7 @@ cudaError_t launch_kv8_append(int dt, const void* k, const void* v, int n_rows, 
 
 cudaError_t launch_kv8_read(int dt, const cb_kv8_cache& c, const int32_t* start, const int32_t* count, int n_rows,
                             int Hkv, int hd, void* k_out, void* v_out, cudaStream_t s) {
+  g_used_kv8 = true;
   const int per = 256 / (hd / 16) * kReadUnroll;
   const bool al32 = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   const dim3 grid((unsigned)(((int64_t)n_rows + per - 1) / per), k_out && v_out ? 2 * Hkv : Hkv, c.n_seq);
@@ -568,6 +568,7 @@ cudaError_t launch_kv8_read(int dt, const cb_kv8_cache& c, const int32_t* start,
 cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const float* weights, int n_keep, int n_sink,
                               int n_recent, int64_t dcap, int32_t* dst_len, float* dst_weights, int32_t* kept, int Hkv,
                               cudaStream_t s) {
+  g_used_kv8 = true;
   const dim3 grid(Hkv, c.n_seq);
 #define CB_SELECT(NT, KPT)                                                                                          \
   return launch_k(k_kv8_select<NT, KPT>, grid, dim3(NT), 0, s, weights, len, c.capacity, n_keep, n_sink, n_recent, dcap, \
@@ -582,6 +583,7 @@ cudaError_t launch_kv8_select(const cb_kv8_cache& c, const int32_t* len, const f
 
 cudaError_t launch_kv8_move(const cb_kv8_cache& c, const cb_kv8_cache& d, int n_keep, const int32_t* kept, int Hkv,
                             int hd, cudaStream_t s) {
+  g_used_kv8 = true;
   const int chunks = c.block * hd / 16, nch = chunks_per_thread(chunks, 256);
   const dim3 grid(2 * ((n_keep + c.block - 1) / c.block), Hkv, c.n_seq), blk(chunks / nch);
   const int lg = log2_of(c.block);

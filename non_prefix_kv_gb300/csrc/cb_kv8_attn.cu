@@ -18,6 +18,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "cb_kv8.cuh"
@@ -26,13 +27,9 @@
 namespace cb {
 
 static __device__ uint32_t g_err_kv8_attn;
+static std::atomic<bool> g_used_kv8_attn{false};   // a kernel of this file was launched (or captured)
 
-uint32_t take_error_kv8_attn() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_kv8_attn, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_kv8_attn, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_kv8_attn() { return g_used_kv8_attn ? take_word(g_err_kv8_attn) : 0u; }
 
 namespace {
 
@@ -967,12 +964,14 @@ static Kv8Attn make_params(const void* q, const int32_t* last, int n_q, const cb
 
 cudaError_t launch_kv8_attn(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv,
                             int hd, void* out, float* weights, void* ws, cudaStream_t s) {
+  g_used_kv8_attn = true;
   const Kv8Attn p = make_params(q, last, n_q, c, H, Hkv, hd, out, weights, ws);
   CB_KV8_DISPATCH(launch_attn_t)
 }
 
 cudaError_t launch_kv8_weights(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H,
                                int Hkv, int hd, float* weights, void* ws, cudaStream_t s) {
+  g_used_kv8_attn = true;
   const Kv8Attn p = make_params(q, last, n_q, c, H, Hkv, hd, nullptr, weights, ws);
   CB_KV8_DISPATCH(launch_weights_t)
 }

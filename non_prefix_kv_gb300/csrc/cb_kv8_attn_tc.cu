@@ -22,6 +22,7 @@
 // shared memory.
 #include <math.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "cb_kv8.cuh"
@@ -30,13 +31,9 @@
 namespace cb {
 
 static __device__ uint32_t g_err_kv8_tc;
+static std::atomic<bool> g_used_kv8_tc{false};   // a kernel of this file was launched (or captured)
 
-uint32_t take_error_kv8_tc() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_kv8_tc, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_kv8_tc, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_kv8_tc() { return g_used_kv8_tc ? take_word(g_err_kv8_tc) : 0u; }
 
 namespace {
 
@@ -1254,6 +1251,7 @@ size_t kv8_tc_ws_bytes(int dt, int n_seq, int Hkv, int G, int n_q, int64_t cap, 
 
 cudaError_t launch_kv8_tc(int dt, const void* q, const int32_t* last, int n_q, const cb_kv8_cache& c, int H, int Hkv, int hd,
                           void* out, float* weights, void* ws, cudaStream_t s) {
+  g_used_kv8_tc = true;
   Kv8Tc p{};
   p.q = q;
   p.last = last;

@@ -19,6 +19,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "../../include/cacheblend.h"
@@ -29,13 +30,9 @@
 namespace cb {
 
 static __device__ uint32_t g_err_logits;
+static std::atomic<bool> g_used_logits{false};   // a kernel of this file was launched (or captured)
 
-uint32_t take_error_logits() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_logits, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_logits, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_logits() { return g_used_logits ? take_word(g_err_logits) : 0u; }
 
 namespace {
 
@@ -334,6 +331,7 @@ void reset_logits_caches() {
 
 cudaError_t launch_logits(int dt, const void* logits, int n_rows, int vocab, const cb_logit_rules& r, void* out,
                           int32_t* token, cudaStream_t s) {
+  g_used_logits = true;
   if (dt == DT_BF16) return launch_t<bf16>(logits, n_rows, vocab, r, out, token, s);
   return launch_t<float>(logits, n_rows, vocab, r, out, token, s);
 }

@@ -92,12 +92,7 @@ static unsigned grid_for(K* kernel, int64_t work_items, int threads) {
   return (unsigned)b;
 }
 
-uint32_t take_error_mem() {
-  uint32_t v = 0, z = 0;
-  if (cudaMemcpyFromSymbol(&v, g_err_mem, sizeof(v)) != cudaSuccess) return ERRBIT_INDEX;
-  cudaMemcpyToSymbol(g_err_mem, &z, sizeof(z));
-  return v;
-}
+uint32_t take_error_mem() { return take_word(g_err_mem); }
 
 // ------------------------------------------------------------------------ RoPE table
 // tab[p][i] = (cos(p theta_i), sin(p theta_i)), theta_i = base^(-2i/hd); angle in fp64.

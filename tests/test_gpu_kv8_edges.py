@@ -184,3 +184,41 @@ def test_one_workspace_for_calls_of_different_sizes(B, dtype):
             B.cb_kv8_attention(qd, dev_i32(last), n, d.c, dims, out, w, ws)
             B.cb_sync(None)
             check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, dtype, hd)
+
+
+# ------------------------------------------------------------------ cb_sync
+SYNC = """
+import sys
+import torch
+from torch.profiler import ProfilerActivity, profile
+from non_prefix_kv_gb300 import binding as B
+
+def copies():
+    B.cb_sync(None)
+    with profile(activities=[ProfilerActivity.CUDA]) as p:
+        B.cb_sync(None)
+        torch.cuda.synchronize()
+    names = [e.name for e in p.events() if e.name.startswith("Memcpy")]
+    return sum("DtoH" in n for n in names), sum("HtoD" in n for n in names)
+
+x = torch.zeros(1, 64, device="cuda")
+torch.cuda.synchronize()
+copies()          # (the profiler's first session may miss its copies)
+print(*copies())
+t = torch.zeros(1, dtype=torch.int32, device="cuda")
+B.cb_logits_process(x, B.logit_rules(), None, t)
+print(*copies())
+"""
+
+
+def test_sync_asks_only_for_what_was_launched(B):
+    """cb_sync's blocking copies in a process of its own: none for operators that nobody called, and
+    none to clear a word that holds nothing."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SYNC], capture_output=True, text=True, cwd=root, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    first, later = (tuple(map(int, line.split())) for line in r.stdout.strip().splitlines()[-2:])
+    assert (first, later) == ((5, 0), (6, 0))
