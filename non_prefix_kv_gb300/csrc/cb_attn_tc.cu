@@ -191,6 +191,7 @@ struct Layout {
   static constexpr int BYTES = OFF_BAR + 256;
   static constexpr int SMEM = BYTES + 1024;
   static_assert((1 + 6 + 2 * KV_STAGES) * 8 + 8 <= 256, "barriers exceed their region");
+  static_assert(SMEM >= tc::kWholeSm, "two CTAs could meet over TMEM columns");
 };
 constexpr uint32_t TM2_O = 2 * BN;   // O_0 at column 256, O_1 right after it
 
@@ -442,6 +443,7 @@ struct Layout2 {
   static constexpr int SMEM = BYTES + 1024;
   static_assert((1 + 6 + 2 * KV_STAGES) * 8 + 16 <= 256, "barriers exceed their region");
   static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
+  static_assert(SMEM >= tc::kWholeSm, "two CTAs could meet over TMEM columns");
 };
 
 template <int HD>

@@ -49,6 +49,7 @@ struct TileCfg {
   static constexpr int B_BYTES = BN * BK * 2;
   static constexpr int STAGES = BN == 256 ? 4 : 5;
   static constexpr int SMEM_BYTES = STAGES * (A_BYTES + B_BYTES) + 1024 /*align slack*/ + 256 /*barriers*/;
+  static_assert(SMEM_BYTES >= tc::kWholeSm, "two CTAs could meet over TMEM columns");
 };
 
 // Fused RMSNorm: row m's scale 1/rms from the partial sums of squares its producer left
@@ -510,6 +511,7 @@ struct PairCfg {
   static constexpr int B_BYTES = (BN / 2) * BK * 2;   // this CTA's half of the B tile
   static constexpr int STAGES = BN == 256 ? 6 : 7;
   static constexpr int SMEM_BYTES = STAGES * (A_BYTES + B_BYTES) + 1024 /*align slack*/ + 256 /*barriers*/;
+  static_assert(SMEM_BYTES >= tc::kWholeSm, "two CTAs could meet over TMEM columns");
 };
 constexpr int PAIR_BM = 2 * BM;
 

@@ -12,6 +12,13 @@ namespace tc {
 // try_wait iterations before a wait is declared lost (each try may suspend briefly)
 constexpr uint32_t kWaitLimit = 1u << 24;
 
+// A kernel that allocates all 512 TMEM columns asks for this much dynamic shared memory at least, so
+// that no two of their CTAs fit on an SM (228 KB, 1 KB reserved per CTA).  tcgen05.alloc waits without
+// a limit for columns that another CTA holds: of two clusters that share two SMs each could hold one
+// SM's columns and wait for the other's, and so could a kernel that is released before it allocates
+// and its dependent, which allocates before it waits for that kernel.
+constexpr int kWholeSm = 114 * 1024;
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -222,3 +222,39 @@ def test_sync_asks_only_for_what_was_launched(B):
     assert r.returncode == 0, r.stderr[-2000:]
     first, later = (tuple(map(int, line.split())) for line in r.stdout.strip().splitlines()[-2:])
     assert (first, later) == ((5, 0), (6, 0))
+
+
+# ------------------------------------------------------------------ calls at once
+@pytest.mark.parametrize("hd,n_q", [(64, 30), (64, 150), (128, 30)])
+def test_two_streams_at_once(B, hd, n_q):
+    """Attention with the keys split over clusters, and its weights, on two streams at once (a cache
+    and a workspace each): the same bits as one after the other."""
+    torch = torch_mod()
+    g = np.random.default_rng(hd)
+    hkv, cap, dims = 2, 2064, make_dims(B, 2, 2, hd, "bf16")
+    n = B.cb_kv8_workspace_bytes(dims, 1, cap, n_q, True)
+    sets = []
+    for _ in range(2):
+        d, _ = filled(B, g, 1, hkv, cap, hd, 16, [cap])
+        q = dev(rounded(g.standard_normal((1, n_q, 2, hd)), "bf16"), "bf16")
+        last = dev_i32(g.integers(0, cap, (1, n_q)))
+        sets.append((d, q, last, torch.empty_like(q), torch.zeros(1, hkv, cap, device="cuda"),
+                     torch.empty(n, dtype=torch.uint8, device="cuda")))
+    call = lambda s: B.cb_kv8_attention(s[1], s[2], n_q, s[0].c, dims, s[3], s[4], s[5])  # noqa: E731
+    ref = []
+    for s in sets:
+        for _ in range(20):
+            call(s)
+        B.cb_sync(None)
+        ref.append((s[3].clone(), s[4].clone()))
+        s[3].zero_(), s[4].zero_()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, s in zip(streams, sets):
+            with torch.cuda.stream(st):
+                call(s)
+    for st in streams:
+        B.cb_sync(st)
+    for s, (o, w) in zip(sets, ref):
+        assert torch.equal(s[3], o) and torch.equal(s[4], w)
