@@ -295,7 +295,8 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
  *   weights     : [n_seq, Hkv, src->capacity] fp32 as cb_kv8_attention accumulates them.  A NaN
  *                 or negative weight among [0, len) ranks as 0, infinity highest; all three
  *                 are reported (CB_ERR_NONFINITE).
- *   dst         : same n_seq and block, n_keep <= dst->capacity, no buffer shared with src
+ *   dst         : same n_seq and block, n_keep <= dst->capacity, no buffer shared with src (nor
+ *                 does any other output overlap an input or another output)
  *   dst_len     : [n_seq] int32, min(len[s], n_keep)
  *   dst_weights : [n_seq, Hkv, dst->capacity] fp32 or NULL: the kept rows' weights, then 0
  *   kept        : [n_seq, Hkv, n_keep] int32: the source row of each kept row, then -1

@@ -1195,24 +1195,36 @@ int check_cache(const cb_kv8_cache* c, const cb_dims* d, const char* what) {
   return CB_OK;
 }
 
-// codes and scales of a cache as address ranges, for the check that two caches share none
-bool caches_overlap(const cb_kv8_cache* a, const cb_kv8_cache* b, const cb_dims* d) {
-  auto ranges = [&](const cb_kv8_cache* c, uintptr_t (*r)[2]) {
-    const size_t rows = (size_t)c->n_seq * d->n_kv_heads * (size_t)c->capacity;
-    const void* p[4] = {c->k_codes, c->v_codes, c->k_scale, c->v_scale};
-    for (int i = 0; i < 4; ++i) {
-      r[i][0] = reinterpret_cast<uintptr_t>(p[i]);
-      r[i][1] = r[i][0] + (i < 2 ? rows * d->head_dim : rows / c->block * 4);
-    }
-  };
-  uintptr_t x[4][2], y[4][2];
-  ranges(a, x);
-  ranges(b, y);
-  for (auto& i : x)
-    for (auto& j : y)
-      if (i[0] < j[1] && j[0] < i[1]) return true;
+// memory that a call reads or writes
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+bool meet(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+}
+// whether something written (w) lies in something read (r) or in another written one
+bool writes_meet(std::initializer_list<Range> w, std::initializer_list<Range> r) {
+  for (auto i = w.begin(); i != w.end(); ++i) {
+    for (auto j = i + 1; j != w.end(); ++j)
+      if (meet(*i, *j)) return true;
+    for (const Range& x : r)
+      if (meet(*i, x)) return true;
+  }
   return false;
 }
+// codes and scales of a cache
+struct CacheRanges {
+  Range k, v, ks, vs;
+  CacheRanges(const cb_kv8_cache* c, const cb_dims* d) {
+    const size_t rows = (size_t)c->n_seq * d->n_kv_heads * (size_t)c->capacity, codes = rows * d->head_dim;
+    k = {c->k_codes, codes};
+    v = {c->v_codes, codes};
+    ks = {c->k_scale, rows / c->block * 4};
+    vs = {c->v_scale, rows / c->block * 4};
+  }
+};
 
 }  // namespace
 
@@ -1330,11 +1342,15 @@ int cb_kv8_evict(const cb_kv8_cache* src, const int32_t* len, const float* weigh
     return fail(CB_ERR_SHAPE, "need n_sink, n_recent >= 0 and n_sink + n_recent <= n_keep");
   if (!len || !weights || !dst_len || !kept) return fail(CB_ERR_INVALID_ARG, "kv8_evict pointer is NULL");
   if ((st = check_al16({weights, dst_weights, kept}, "kv8_evict"))) return st;
-  if (caches_overlap(src, dst, dims)) return fail(CB_ERR_INVALID_ARG, "kv8_evict: src and dst share memory");
-  if (len == dst_len || weights == dst_weights)
-    return fail(CB_ERR_INVALID_ARG, "kv8_evict: dst_len and dst_weights must not be the source's");
   const int Hkv = dims->n_kv_heads, hd = dims->head_dim;
   const int64_t heads = (int64_t)src->n_seq * Hkv;
+  const CacheRanges a(src, dims), b(dst, dims);
+  if (writes_meet({b.k, b.v, b.ks, b.vs}, {a.k, a.v, a.ks, a.vs}))
+    return fail(CB_ERR_INVALID_ARG, "kv8_evict: src and dst share memory, or two arrays of dst do");
+  const Range n{len, (size_t)src->n_seq * 4}, w{weights, (size_t)heads * src->capacity * 4}, dn{dst_len, (size_t)src->n_seq * 4},
+      dw{dst_weights, (size_t)heads * dst->capacity * 4}, kp{kept, (size_t)heads * n_keep * 4};
+  if (writes_meet({dn, dw, kp, b.k, b.v, b.ks, b.vs}, {n, w, a.k, a.v, a.ks, a.vs}))
+    return fail(CB_ERR_INVALID_ARG, "kv8_evict: an output overlaps an input or another output");
   CB_LAUNCH(CB_PROF_KV8_EVICT, 0, heads, src->capacity, n_keep, 0.0, (double)heads * (4.0 * src->capacity + 8.0 * n_keep),
             S(stream), launch_kv8_select(*src, len, weights, n_keep, n_sink, n_recent, dst->capacity, dst_len,
                                          dst_weights, kept, Hkv, S(stream)));

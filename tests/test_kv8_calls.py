@@ -75,3 +75,28 @@ def test_what_a_workspace_for_several_query_counts_has_to_hold(lib):
                     assert ask(n, 4112, 1, w, dd) >= ask(n, 4096, 1, w, dd) and ask(n, 4096, 3, w, dd) >= ask(n, 4096, 2, w, dd)
     # the expanded codes: 2 bytes for each of K's and V's
     assert 0 <= ask(129) - 2 * 2 * 32 * 4096 * 128 < 4096
+
+
+def test_evict_refuses_outputs_that_overlap(lib):
+    """Every output against every input and every other output, by a few bytes or by all."""
+    d = _dims()
+    src, dst = _cache(), _cache(k_codes=1 << 50, v_codes=1 << 51, k_scale=1 << 52, v_scale=1 << 53, capacity=128)
+    heads, n_keep = 2 * 2, 100
+    at = dict(len=1 << 30, weights=1 << 31, dst_len=1 << 32, dst_weights=1 << 33, kept=1 << 34)
+    size = dict(len=8, weights=heads * 256 * 4, dst_len=8, dst_weights=heads * 128 * 4, kept=heads * n_keep * 4)
+
+    def status(**kw):
+        a = {**at, **kw}
+        return lib.cb_kv8_evict(ctypes.byref(src), a["len"], a["weights"], n_keep, 1, 2, ctypes.byref(dst), a["dst_len"],
+                                a["dst_weights"], a["kept"], ctypes.byref(d), None)
+
+    arrays = [(at[k], size[k], k) for k in at]
+    arrays += [(src.k_codes, 2 * 2 * 256 * 64, ""), (src.v_scale, heads * 8 * 4, ""), (dst.v_codes, 2 * 2 * 128 * 64, ""),
+               (dst.k_scale, heads * 4 * 4, "")]
+    for out in ("dst_len", "dst_weights", "kept"):
+        for base, n, name in arrays:
+            if name == out:
+                continue
+            for p in (base, base + (n - 1) // 16 * 16, base - (size[out] - 1) // 16 * 16):
+                assert status(**{out: p}) == 1, (out, name, p - base)
+                assert b"overlaps" in lib.cb_last_error_message()
