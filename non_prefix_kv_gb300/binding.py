@@ -488,9 +488,15 @@ def kv8_cache(k_codes, v_codes, k_scale, v_scale, block: int) -> cb_kv8_cache:
     n_seq, hkv, cap, hd = k_codes.shape
     if block not in (16, 32, 64, 128):
         raise ValueError(f"block {block} is not 16, 32, 64 or 128")
-    ns = n_seq * hkv * (cap // block)
-    c = cb_kv8_cache(_buf("k_codes", k_codes, T.i8, None, dev), _buf("v_codes", v_codes, T.i8, k_codes.numel(), dev),
-                     _buf("k_scale", k_scale, T.f32, ns, dev), _buf("v_scale", v_scale, T.f32, ns, dev), cap, n_seq, block)
+    ptr = _buf("k_codes", k_codes, T.i8, None, dev)
+    if cap % block:
+        raise ValueError(f"capacity {cap} is not a multiple of block {block}")
+    scales = (n_seq, hkv, cap // block)
+    for what, t, shape in (("v_codes", v_codes, k_codes.shape), ("k_scale", k_scale, scales), ("v_scale", v_scale, scales)):
+        if tuple(t.shape) != tuple(shape):       # (the right number of elements in another layout would give wrong values)
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    c = cb_kv8_cache(ptr, _buf("v_codes", v_codes, T.i8, None, dev), _buf("k_scale", k_scale, T.f32, None, dev),
+                     _buf("v_scale", v_scale, T.f32, None, dev), cap, n_seq, block)
     c.hkv, c.hd, c.tensors = hkv, hd, (k_codes, v_codes, k_scale, v_scale)
     return c
 

@@ -100,3 +100,63 @@ def test_evict_refuses_outputs_that_overlap(lib):
             for p in (base, base + (n - 1) // 16 * 16, base - (size[out] - 1) // 16 * 16):
                 assert status(**{out: p}) == 1, (out, name, p - base)
                 assert b"overlaps" in lib.cb_last_error_message()
+
+
+# ---- the binding's checks, with stand-ins for torch's device and tensors ----------------------
+class Tensor:
+    def __init__(self, dtype, *shape, dev=0):
+        self.dtype, self.shape, self.dev, self.device = dtype, shape, dev, f"cuda:{dev}"
+
+    def numel(self):
+        n = 1
+        for x in self.shape:
+            n *= x
+        return n
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.dev
+
+    def data_ptr(self):
+        return FAKE
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """The current device as the binding sees it: fake.dev."""
+    torch = pytest.importorskip("torch")
+
+    class Fake(B._Torch):
+        dev = 0
+
+        def device(self):
+            return self.dev
+
+        def stream(self, stream, dev):
+            return None
+
+    f = Fake()
+    f.t = torch
+    monkeypatch.setattr(B, "_TORCH", f)
+    return f
+
+
+def handle(t, dev=0, **kw):
+    a = dict(k=(2, 3, 64, 64), v=(2, 3, 64, 64), ks=(2, 3, 4), vs=(2, 3, 4))
+    a.update(kw)
+    return B.kv8_cache(Tensor(t.int8, *a["k"], dev=dev), Tensor(t.int8, *a["v"], dev=dev),
+                       Tensor(t.float32, *a["ks"], dev=dev), Tensor(t.float32, *a["vs"], dev=dev), 16)
+
+
+def test_a_cache_is_made_of_tensors_of_the_right_shapes(fake):
+    t = fake.t
+    c = handle(t)
+    assert (c.n_seq, c.capacity, c.block, c.hkv, c.hd) == (2, 64, 16, 3, 64)
+    for kw in (dict(ks=(2, 4, 3)), dict(vs=(2, 4, 3)), dict(ks=(24,)), dict(v=(2, 64, 3, 64)), dict(v=(2, 3, 32, 128)),
+               dict(ks=(3, 2, 4))):
+        with pytest.raises(ValueError, match="shape"):
+            handle(t, **kw)
+    with pytest.raises(ValueError, match="multiple of block"):
+        handle(t, k=(2, 3, 72, 64), v=(2, 3, 72, 64))
