@@ -497,11 +497,13 @@ def kv8_cache(k_codes, v_codes, k_scale, v_scale, block: int) -> cb_kv8_cache:
             raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     c = cb_kv8_cache(ptr, _buf("v_codes", v_codes, T.i8, None, dev), _buf("k_scale", k_scale, T.f32, None, dev),
                      _buf("v_scale", v_scale, T.f32, None, dev), cap, n_seq, block)
-    c.hkv, c.hd, c.tensors = hkv, hd, (k_codes, v_codes, k_scale, v_scale)
+    c.hkv, c.hd, c.dev, c.tensors = hkv, hd, dev, (k_codes, v_codes, k_scale, v_scale)
     return c
 
 
-def _kv8(cache: cb_kv8_cache, dims: cb_dims):
+def _kv8(cache: cb_kv8_cache, dims: cb_dims, dev: int):
+    if cache.dev != dev:
+        raise ValueError(f"cache: on cuda:{cache.dev}, not on the current CUDA device")
     if cache.hkv != dims.n_kv_heads or cache.hd != dims.head_dim:
         raise ValueError(f"cache of {cache.hkv} heads of {cache.hd}, dims of {dims.n_kv_heads} heads of {dims.head_dim}")
     return C.byref(cache)
@@ -513,7 +515,7 @@ def cb_kv8_append(k, v, n_rows: int, start, count, cache: cb_kv8_cache, dims: cb
     n = ns * n_rows * cache.hkv * cache.hd
     _check("cb_kv8_append", lib().cb_kv8_append(
         _buf("k", k, dt, n, dev), _buf("v", v, dt, n, dev), n_rows, _buf("start", start, T.i32, ns, dev),
-        _buf("count", count, T.i32, ns, dev), _kv8(cache, dims), C.byref(dims), T.stream(stream, dev)))
+        _buf("count", count, T.i32, ns, dev), _kv8(cache, dims, dev), C.byref(dims), T.stream(stream, dev)))
 
 
 def cb_kv8_read(cache: cb_kv8_cache, start, count, n_rows: int, dims: cb_dims, k_out, v_out, stream=None):
@@ -521,7 +523,7 @@ def cb_kv8_read(cache: cb_kv8_cache, start, count, n_rows: int, dims: cb_dims, k
     dev, dt, ns = T.device(), T.row[dims.dtype], cache.n_seq
     n = ns * n_rows * cache.hkv * cache.hd
     _check("cb_kv8_read", lib().cb_kv8_read(
-        _kv8(cache, dims), _buf("start", start, T.i32, ns, dev), _buf("count", count, T.i32, ns, dev), n_rows,
+        _kv8(cache, dims, dev), _buf("start", start, T.i32, ns, dev), _buf("count", count, T.i32, ns, dev), n_rows,
         C.byref(dims), _buf("k_out", k_out, dt, n, dev), _buf("v_out", v_out, dt, n, dev), T.stream(stream, dev)))
 
 
@@ -540,7 +542,7 @@ def cb_kv8_attention(q, last, n_q: int, cache: cb_kv8_cache, dims: cb_dims, out,
     n = ns * n_q * dims.n_heads * dims.head_dim
     w, wn = _ws(ws, dev)
     _check("cb_kv8_attention", lib().cb_kv8_attention(
-        _buf("q", q, dt, n, dev), _buf("last", last, T.i32, ns * n_q, dev), n_q, _kv8(cache, dims), C.byref(dims),
+        _buf("q", q, dt, n, dev), _buf("last", last, T.i32, ns * n_q, dev), n_q, _kv8(cache, dims, dev), C.byref(dims),
         _buf("out", out, dt, n, dev), _buf("weights", weights, T.f32, ns * cache.hkv * cache.capacity, dev), w, wn,
         T.stream(stream, dev)))
 
@@ -550,8 +552,8 @@ def cb_kv8_evict(src: cb_kv8_cache, length, weights, n_keep: int, n_sink: int, n
     T = _torch()
     dev, ns, heads = T.device(), src.n_seq, src.n_seq * src.hkv
     _check("cb_kv8_evict", lib().cb_kv8_evict(
-        _kv8(src, dims), _buf("length", length, T.i32, ns, dev),
-        _buf("weights", weights, T.f32, heads * src.capacity, dev), n_keep, n_sink, n_recent, _kv8(dst, dims),
+        _kv8(src, dims, dev), _buf("length", length, T.i32, ns, dev),
+        _buf("weights", weights, T.f32, heads * src.capacity, dev), n_keep, n_sink, n_recent, _kv8(dst, dims, dev),
         _buf("dst_len", dst_len, T.i32, ns, dev),
         _buf("dst_weights", dst_weights, T.f32, heads * dst.capacity, dev),
         _buf("kept", kept, T.i32, heads * n_keep, dev), C.byref(dims), T.stream(stream, dev)))
@@ -580,6 +582,7 @@ def logit_rules(history=None, history_len=None, prompt_len=None, repetition=None
         _buf("mask", mask, T.i32, None, dev), 0 if history is None else history.shape[1],
         0 if mask is None else mask.shape[1], 0 if bias_id is None else bias_id.shape[1])
     r.n_rows = rows[0] if rows else None
+    r.dev = dev if rows else None
     r.tensors = (history, history_len, prompt_len, repetition, presence, frequency, bias_id, bias, mask)
     return r
 
@@ -591,6 +594,8 @@ def cb_logits_process(logits, rules: cb_logit_rules, out=None, token=None, strea
     n, vocab = logits.shape
     if rules.n_rows is not None and rules.n_rows != n:
         raise ValueError(f"rules for {rules.n_rows} rows, logits of {n}")
+    if rules.dev is not None and rules.dev != dev:
+        raise ValueError(f"rules: on cuda:{rules.dev}, not on the current CUDA device")
     dt = T.cb.get(logits.dtype)
     if dt is None:
         raise ValueError(f"logits: {logits.dtype}, expected float32 or bfloat16")

@@ -160,3 +160,22 @@ def test_a_cache_is_made_of_tensors_of_the_right_shapes(fake):
             handle(t, **kw)
     with pytest.raises(ValueError, match="multiple of block"):
         handle(t, k=(2, 3, 72, 64), v=(2, 3, 72, 64))
+
+
+def test_a_handle_is_refused_on_another_device(fake):
+    """The other arguments may well be on the current device: the handle's memory is not."""
+    t, d = fake.t, _dims(n_heads=6, n_kv_heads=3, head_dim=64)
+    fake.dev = 1
+    c, c2 = handle(t, dev=1), handle(t, dev=1)
+    rules = B.logit_rules(mask=Tensor(t.int32, 2, 4, dev=1))
+    fake.dev = 0
+    row = lambda *shape, dt=t.bfloat16: Tensor(dt, *shape)  # noqa: E731
+    i32 = lambda n: Tensor(t.int32, n)  # noqa: E731
+    calls = [lambda: B.cb_kv8_append(row(2, 5, 192), row(2, 5, 192), 5, i32(2), None, c, d),
+             lambda: B.cb_kv8_read(c, i32(2), None, 5, d, row(2, 5, 192), None),
+             lambda: B.cb_kv8_attention(row(2, 1, 384), i32(2), 1, c, d, row(2, 1, 384)),
+             lambda: B.cb_kv8_evict(c, i32(2), row(2, 3, 64, dt=t.float32), 8, 0, 0, c2, i32(2), None, i32(48), d),
+             lambda: B.cb_logits_process(row(2, 128, dt=t.float32), rules, None, i32(2))]
+    for call in calls:
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()
