@@ -562,7 +562,7 @@ typedef struct {
  *   x > 0 ? x / repetition : x * repetition   if the id is in the history,
  *   x - (frequency * count + presence)        if it is count > 0 times in the answer,
  *   x + bias,                                 then -inf where the mask does not allow the id;
- * fp32 arithmetic, rounded once to `dtype`.
+ * fp32 arithmetic, each operation rounded (none contracted), the result once more to `dtype`.
  *   logits, out : [n_rows, vocab] of `dtype` (CB_F32 or CB_BF16); out may be logits itself or
  *                 NULL
  *   token       : [n_rows] int32 or NULL: the lowest id with the largest value of out; -1 if

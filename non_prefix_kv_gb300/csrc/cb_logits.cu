@@ -201,13 +201,14 @@ __global__ void __launch_bounds__(kThreads, 4) k_logits(const T* logits, T* out,
     }
     if (hist || biased) __syncthreads();
 
-    // the rules of an id with a word that is not 0
+    // the rules of an id with a word that is not 0, every operation rounded (none joined to a
+    // multiply-add: the token goes by these values, and a last bit decides between near ones)
     auto touch = [&](float v, uint32_t w) -> float {
       if (w & (kPrompt | kCount)) {
-        v = v > 0.f ? v / rep : v * rep;
-        if (w & kCount) v -= freq * (float)(w & kCount) + pres;
+        v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+        if (w & kCount) v = __fsub_rn(v, __fadd_rn(__fmul_rn(freq, (float)(w & kCount)), pres));
       }
-      if (w & kOwner) v += sums[r.n_bias - (int)((w & kOwner) >> 18)];
+      if (w & kOwner) v = __fadd_rn(v, sums[r.n_bias - (int)((w & kOwner) >> 18)]);
       return v;
     };
     // v as it is returned; ids come in ascending order, so the first of equals stays

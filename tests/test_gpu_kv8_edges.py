@@ -186,6 +186,45 @@ def test_one_workspace_for_calls_of_different_sizes(B, dtype):
             check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, dtype, hd)
 
 
+# ------------------------------------------------------------------ logits
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,V,T,nb", [(3, 5000, 4000, 0), (2, 32000, 9000, 600), (4, 1027, 3000, 64)])
+def test_every_step_of_the_logit_rules_is_rounded_to_fp32(B, n, V, T, nb, dtype):
+    """The rules one after the other, each operation rounded: the same bits as numpy's fp32."""
+    torch = torch_mod()
+    g = np.random.default_rng(V)
+    f = np.float32
+    x = rounded(g.standard_normal((n, V)) * 3, dtype)
+    hist = (g.uniform(0, 1, (n, T)) ** 2 * V).astype(np.int32).clip(0, V - 1)
+    pl = g.integers(0, T // 2, n)
+    rep, pres, freq = (g.uniform(a, b, n).astype(f) for a, b in ((0.5, 2), (-1, 1), (0, 0.5)))
+    bid = g.integers(0, V, (n, nb)).astype(np.int32)
+    if nb:
+        bid[:, nb // 2:] = bid[:, :nb - nb // 2]           # each id twice at least
+    bias = g.standard_normal((n, nb)).astype(f)
+    rules = dict(history=dev_i32(hist), history_len=dev_i32([T] * n), prompt_len=dev_i32(pl), repetition=dev(rep),
+                 presence=dev(pres), frequency=dev(freq))
+    if nb:
+        rules.update(bias_id=dev_i32(bid), bias=dev(bias))
+    y, tok = run_logits(B, x, dtype, **rules)
+    B.cb_sync(None)
+    for b in range(n):
+        v = x[b].astype(f)
+        seen = np.bincount(hist[b], minlength=V) > 0
+        v = np.where(seen, np.where(v > 0, v / rep[b], v * rep[b]), v).astype(f)
+        made = np.bincount(hist[b, pl[b]:], minlength=V)
+        take = (freq[b] * made.astype(f)).astype(f) + pres[b]
+        v = np.where(made > 0, v - take.astype(f), v).astype(f)
+        total = {}
+        for i, z in zip(bid[b], bias[b]):
+            total[i] = f(total[i] + z) if i in total else z
+        for i, z in total.items():
+            v[i] = f(v[i] + z)
+        ref = rounded(v, dtype)
+        np.testing.assert_array_equal(y[b].float().cpu().numpy(), ref)
+        assert int(tok[b]) == K8.token(ref.astype(np.float64))
+
+
 # ------------------------------------------------------------------ cb_sync
 SYNC = """
 import sys
