@@ -213,7 +213,9 @@ int cb_rope_shift_q8(void* k_dst, void* v_dst, const uint8_t* k_codes, const uin
  * KV head h, row i sits at ((s * Hkv + h) * capacity + i) * head_dim (head-major: a head's
  * rows are contiguous), its scale at (s * Hkv + h) * (capacity / block) + i / block.
  * A row index counts the rows a sequence holds; after an eviction it is no longer the token's
- * position (keys keep the rotation they were stored with). */
+ * position (keys keep the rotation they were stored with).  No buffer that a call writes (for
+ * cb_kv8_append the cache, for cb_kv8_attention out, weights and workspace) may overlap another
+ * of its arguments: refused. */
 typedef struct {
     int8_t* k_codes;    /* [n_seq, Hkv, capacity, head_dim], 16-byte aligned (all four)     */
     int8_t* v_codes;

@@ -1237,6 +1237,10 @@ int cb_kv8_append(const void* k, const void* v, int32_t n_rows, const int32_t* s
   if (n_rows > cache->capacity) return fail(CB_ERR_SHAPE, "n_rows %d exceeds the capacity", n_rows);
   if (!k || !v || !start) return fail(CB_ERR_INVALID_ARG, "kv8_append pointer is NULL");
   if ((st = check_al16({k, v}, "kv8_append"))) return st;
+  const CacheRanges a(cache, dims);
+  const size_t in = (size_t)cache->n_seq * n_rows * dims->n_kv_heads * dims->head_dim * esize(dims->dtype), ns = (size_t)cache->n_seq * 4;
+  if (writes_meet({a.k, a.v, a.ks, a.vs}, {{k, in}, {v, in}, {start, ns}, {count, ns}}))
+    return fail(CB_ERR_INVALID_ARG, "kv8_append: an array of the cache overlaps another argument");
   const double W = 2.0 * dims->n_kv_heads * dims->head_dim, n = (double)cache->n_seq * n_rows;
   CB_LAUNCH(CB_PROF_KV8_APPEND, 0, (int64_t)cache->n_seq * n_rows, (int64_t)W, 0, 0.0, n * W * (1.0 + esize(dims->dtype)),
             S(stream), launch_kv8_append(dims->dtype, k, v, n_rows, start, count, *cache, dims->n_kv_heads,
@@ -1252,6 +1256,10 @@ int cb_kv8_read(const cb_kv8_cache* cache, const int32_t* start, const int32_t* 
   if (n_rows == 0 || (!k_out && !v_out)) return CB_OK;
   if (!start) return fail(CB_ERR_INVALID_ARG, "kv8_read: start is NULL");
   if ((st = check_al16({k_out, v_out}, "kv8_read"))) return st;
+  const CacheRanges a(cache, dims);
+  const size_t bytes = (size_t)cache->n_seq * n_rows * dims->n_kv_heads * dims->head_dim * esize(dims->dtype), ns = (size_t)cache->n_seq * 4;
+  if (writes_meet({{k_out, bytes}, {v_out, bytes}}, {a.k, a.v, a.ks, a.vs, {start, ns}, {count, ns}}))
+    return fail(CB_ERR_INVALID_ARG, "kv8_read: an output overlaps another argument");
   const double W = (k_out && v_out ? 2.0 : 1.0) * dims->n_kv_heads * dims->head_dim, n = (double)cache->n_seq * n_rows;
   CB_LAUNCH(CB_PROF_KV8_READ, 0, (int64_t)cache->n_seq * n_rows, (int64_t)W, 0, 0.0, n * W * (1.0 + esize(dims->dtype)),
             S(stream), launch_kv8_read(dims->dtype, *cache, start, count, n_rows, dims->n_kv_heads, dims->head_dim,
@@ -1313,6 +1321,10 @@ int cb_kv8_attention(const void* q, const int32_t* last, int32_t n_q, const cb_k
   if (static_cast<const char*>(q) < static_cast<char*>(out) + bytes &&
       static_cast<char*>(out) < static_cast<const char*>(q) + bytes)
     return fail(CB_ERR_INVALID_ARG, "kv8_attention: out overlaps q");
+  const CacheRanges a(cache, dims);
+  if (writes_meet({{out, bytes}, {weights, (size_t)cache->n_seq * Hkv * cache->capacity * 4}, {ws, need}},
+                  {{q, bytes}, {last, (size_t)cache->n_seq * n_q * 4}, a.k, a.v, a.ks, a.vs}))
+    return fail(CB_ERR_INVALID_ARG, "kv8_attention: out, the weights or the workspace overlaps another argument");
   const int64_t m = (int64_t)cache->n_seq * n_q;
   if (kv8_tc_taken(dims->dtype, hd, G, n_q, weights != nullptr)) {
     CB_LAUNCH(CB_PROF_KV8_ATTN, 2, m, cache->capacity, H, 0.0, 0.0, S(stream),

@@ -102,6 +102,38 @@ def test_evict_refuses_outputs_that_overlap(lib):
                 assert b"overlaps" in lib.cb_last_error_message()
 
 
+def test_append_read_and_attention_refuse_what_they_write_over_another_argument(lib):
+    d, c, r = _dims(), _cache(), ctypes.byref
+    codes, scales = 2 * 2 * 256 * 64, 2 * 2 * 8 * 4
+    cache = [(c.k_codes, codes), (c.v_codes, codes), (c.k_scale, scales), (c.v_scale, scales)]
+    k, v, start, count, n = 1 << 30, 1 << 31, 1 << 32, 1 << 33, 5
+    rows = 2 * n * 2 * 64 * 2                                  # bytes of k or v
+    append = lambda k=k, v=v, start=start, count=count, cc=c: lib.cb_kv8_append(k, v, n, start, count, r(cc), r(d), None)  # noqa: E731
+    read = lambda k=k, v=v, start=start, count=count: lib.cb_kv8_read(r(c), start, count, n, r(d), k, v, None)  # noqa: E731
+
+    def refused(status):
+        return status == 1 and b"overlaps" in lib.cb_last_error_message()
+
+    for base, size in cache:
+        for p in (base, base + size - 16, base - 16):
+            assert refused(append(k=p)) and refused(append(v=p)) and refused(read(k=p)) and refused(read(v=p))
+        assert refused(append(start=base)) and refused(append(count=base + size - 4))
+    assert refused(append(cc=_cache(v_codes=c.k_codes + codes - 16))) and refused(append(cc=_cache(k_scale=c.v_scale)))
+    assert refused(read(k=k, v=k + rows - 16)) and refused(read(start=k)) and refused(read(count=v + rows - 4))
+    # attention
+    q, last, out, w, ws = 1 << 30, 1 << 31, 1 << 32, 1 << 33, 1 << 34
+    need = B.cb_kv8_workspace_bytes(d, 2, 256, 4, True)
+    row, acc = 2 * 4 * 4 * 64 * 2, 2 * 2 * 256 * 4
+
+    def att(q=q, last=last, out=out, w=w, ws=ws):
+        return lib.cb_kv8_attention(q, last, 4, r(c), r(d), out, w, ws, need, None)
+
+    for base, size in cache + [(q, row), (last, 32)]:
+        for p in (base, base + (size - 1) // 16 * 16):
+            assert refused(att(out=p)) and refused(att(w=p)) and refused(att(ws=p))
+    assert refused(att(out=w + acc - 16)) and refused(att(w=ws + need - need % 16 - 16)) and refused(att(ws=out - 16))
+
+
 # ---- the binding's checks, with stand-ins for torch's device and tensors ----------------------
 class Tensor:
     def __init__(self, dtype, *shape, dev=0):
