@@ -186,6 +186,102 @@ def test_one_workspace_for_calls_of_different_sizes(B, dtype):
             check_attention(out, host(w) if weigh else None, K8.attention(o, q.astype(np.float64), last), last, dtype, hd)
 
 
+class Long:
+    """A cache of 3 sequences x 2 heads x 2^22 rows x 128: the last sequence starts 2^31 bytes into the
+    codes.  Its keys are 0 but for a few marked rows near both ends and in the middle, each with a
+    channel of its own; its values are distinct there, and elsewhere 50 (first half) or 110 in units
+    of 0.01.  A query points at a marked row (its score is 60, the others' 0: they weigh e^-60) or at
+    none (every visible row weighs the same)."""
+    HKV, HD, CAP, NSEQ, BLOCK = 2, 128, 1 << 22, 3, 128
+    MARKED = [0, 5, 127, 128, (1 << 21) + 77, (1 << 22) - 4097, (1 << 22) - 130, (1 << 22) - 2, (1 << 22) - 1]
+
+    def __init__(self, B):
+        torch = torch_mod()
+        n, h, c, d = self.NSEQ, self.HKV, self.CAP, self.HD
+        mk = lambda: torch.empty(n, h, c, d, dtype=torch.int8, device="cuda")  # noqa: E731
+        sc = lambda: torch.full((n, h, c // self.BLOCK), float("nan"), device="cuda")  # noqa: E731
+        self.k, self.v, self.ks, self.vs = mk(), mk(), sc(), sc()
+        self.cache = B.kv8_cache(self.k, self.v, self.ks, self.vs, self.BLOCK)
+        self.k[2] = 0
+        self.v[2, :, :c // 2] = 50
+        self.v[2, :, c // 2:] = 110
+        self.ks[2] = 1.0 / 128
+        self.vs[2] = 0.01
+        self.row = np.random.default_rng(6).integers(-127, 128, (h, len(self.MARKED), d))
+        for i, r in enumerate(self.MARKED):
+            self.k[2, :, r, 3 * i] = 64                 # 0.5
+            self.v[2, :, r] = torch.from_numpy(self.row[:, i].astype(np.int8)).cuda()
+
+    def query(self, i):
+        """The query that points at marked row i; None: at none."""
+        q = np.zeros(self.HD, np.float32)
+        if i is not None:
+            q[3 * i] = 2 * 60 * np.sqrt(np.float64(self.HD))
+        return q
+
+
+@pytest.fixture(scope="module")
+def long_cache(B):
+    x = Long(B)
+    yield x
+
+
+@pytest.mark.parametrize("dtype,n_q", [("bf16", 1), ("f32", 1), ("bf16", 12), ("bf16", 40), ("bf16", 150), ("f32", 60)])
+def test_attention_and_weights_over_a_long_cache(B, long_cache, dtype, n_q):
+    """Every path past 2^31 bytes of codes: rows near the end told apart by their values, the account
+    of each of the 2^22 rows."""
+    torch = torch_mod()
+    L = long_cache
+    h, cap, hd, marks = L.HKV, L.CAP, L.HD, L.MARKED
+    dims = make_dims(B, h, h, hd, dtype)
+    # per query and head: the marked row it points at; the last row it sees
+    point = [[(j + 4 * hh) % (len(marks) + 1) for hh in range(h)] for j in range(n_q)]
+    point = [[None if p == len(marks) else p for p in r] for r in point]
+    if n_q == 1:
+        point = [[len(marks) - 2, None]]
+    last = np.full((L.NSEQ, n_q), -1)
+    last[2] = cap - 1
+    if n_q > 1:
+        last[2, 1] = marks[7]              # the last row of all is not seen
+        last[2, 2] = cap // 2 - 1          # only values of 50 and marked ones
+    q = np.zeros((L.NSEQ, n_q, h, hd), np.float32)
+    for j in range(n_q):
+        for hh in range(h):
+            q[2, j, hh] = L.query(point[j][hh])
+    q = rounded(q, dtype)
+    w = torch.zeros(L.NSEQ, h, cap, device="cuda")
+    qd = dev(q, dtype)
+    out = torch.full_like(qd, 7.5)
+    ws = torch.empty(B.cb_kv8_workspace_bytes(dims, L.NSEQ, cap, n_q, True), dtype=torch.uint8, device="cuda")
+    B.cb_kv8_attention(qd, dev_i32(last), n_q, L.cache, dims, out, w, ws)
+    B.cb_sync(None)
+    assert torch.all(out[:2] == 0) and torch.all(w[:2] == 0)
+    got, acc = host(out[2]), host(w[2])
+    eps = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    want = np.zeros((h, cap))
+    for hh in range(h):
+        v = np.where(np.arange(cap) < cap // 2, 50.0, 110.0)
+        for j in range(n_q):
+            n, p = last[2, j] + 1, point[j][hh]
+            if p is not None and marks[p] < n:
+                # one row has all the weight but 2^22 e^-60; its own is rounded once on both sides of
+                # the fraction line (fp16: 2^-11, fp32: 2^-21)
+                ref = L.row[hh, p] * np.float64(np.float32(0.01))
+                tol = np.abs(ref) * (eps * 1.01 + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21) * 2) + 1e-12
+                assert np.all(np.abs(got[j, hh] - ref) <= tol), (j, hh)
+                want[hh, marks[p]] += 1
+            else:
+                # n equal weights, added 16 keys at a time: at most n / 16 sums, each cut to 24 bits
+                seen = [m for m in marks if m < n]
+                tot = v[:n].sum() - v[seen].sum() + L.row[hh, :len(seen)].sum(0)
+                ref = tot / n * np.float64(np.float32(0.01))
+                bound = (n / 16) * 2.0 ** -23 + 2.0 ** -10
+                assert np.all(np.abs(got[j, hh] - ref) <= np.abs(ref) * (bound + eps)), (j, hh)
+                want[hh, :n] += 1.0 / n
+    bound = cap / 16 * 2.0 ** -23 + 2.0 ** -18 + n_q * 2.0 ** -23
+    assert np.all(np.abs(acc - want) <= want * bound + n_q * np.exp(-59.0))
+
+
 # ------------------------------------------------------------------ logits
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,V,T,nb", [(3, 5000, 4000, 0), (2, 32000, 9000, 600), (4, 1027, 3000, 64)])
@@ -223,6 +319,66 @@ def test_every_step_of_the_logit_rules_is_rounded_to_fp32(B, n, V, T, nb, dtype)
         ref = rounded(v, dtype)
         np.testing.assert_array_equal(y[b].float().cpu().numpy(), ref)
         assert int(tok[b]) == K8.token(ref.astype(np.float64))
+
+
+# ------------------------------------------------------------------ from a blend to its answer
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_blends_rows_become_the_cache_that_answers(B, dtype):
+    """run_blend's K and V of every layer appended as they are; the next tokens attend over them."""
+    from non_prefix_kv_gb300 import engine as E, synth
+    torch = torch_mod()
+    s = synth.ModelShape(n_layers=2, d_model=256, n_heads=4, n_kv_heads=2, head_dim=64, d_ff=512, vocab=512, dtype=dtype,
+                         w_std=0.06)
+    g = np.random.default_rng(50)
+    pool = [g.integers(0, s.vocab, 96).astype(np.int32) for _ in range(3)]
+    tokens = np.concatenate(pool + [g.integers(0, s.vocab, 30).astype(np.int32)])
+    n, hkv, hd, H, cap = len(tokens), s.n_kv_heads, s.head_dim, s.n_heads, 384
+    dm = E.DeviceModel.from_host(synth.make_model(s, seed=4))
+    eng = E.BlendEngine(dm, n, max_pos=512)
+    req = E.Request(eng, eng.precompute_pool(pool), [0, 1, 2], tokens)
+    E.run_blend(req, E.layer_plan(s, req.N, req.n_cached, [1.0, 0.3]))
+    caches = [Dev(B, 1, hkv, cap, hd, 32) for _ in range(s.n_layers)]
+    twins = [K8.empty(1, hkv, cap, hd, 32) for _ in range(s.n_layers)]
+    for l in range(s.n_layers):
+        B.cb_kv8_append(req.K[l], req.V[l], n, dev_i32([0]), None, caches[l].c, dm.dims)
+    B.cb_sync(None)
+    rows = lambda t: host(t).reshape(1, -1, hkv, hd).astype(np.float32)  # noqa: E731
+    for l in range(s.n_layers):
+        K8.append(twins[l], rows(req.K[l]), rows(req.V[l]), [0])
+        check_cache(caches[l], twins[l], [n])
+    x, q, k, v, o = (torch.empty(1, w, dtype=tdt(dtype), device="cuda")
+                     for w in (s.d_model, s.q_width, s.kv_width, s.kv_width, s.q_width))
+    ws = torch.empty(B.cb_kv8_workspace_bytes(dm.dims, 1, cap, 1, True), dtype=torch.uint8, device="cuda")
+    acc = [torch.zeros(1, hkv, cap, device="cuda") for _ in range(s.n_layers)]
+    total, rel = [np.zeros((1, hkv, cap)) for _ in range(s.n_layers)], 0.0
+    tok, logits = req.token, torch.empty(1, s.vocab, device="cuda")
+    hist, rules = list(tokens), None
+    for step in range(5):
+        at = n + step
+        hist.append(int(tok))
+        B.cb_gather_rows(x, dm.embed, tok, 1, s.d_model * x.element_size())
+        for l in range(s.n_layers):
+            B.cb_selective_qkv(x, None, dev_i32([at]), 1, dm.dims, dm.layers_c[l], eng.cos_sin, eng.max_pos, q, k, v, eng.ws)
+            B.cb_kv8_append(k, v, 1, dev_i32([at]), None, caches[l].c, dm.dims)
+            B.cb_kv8_attention(q, dev_i32([at]), 1, caches[l].c, dm.dims, o, acc[l], ws)
+            B.cb_sync(None)
+            K8.append(twins[l], rows(k), rows(v), [at])
+            check_cache(caches[l], twins[l], [at + 1])
+            ref = K8.attention(twins[l], host(q).reshape(1, 1, H, hd), np.array([[at]]))
+            check_attention(o.view(1, 1, H, hd), None, ref, np.array([[at]]), dtype, hd)
+            total[l] += ref[1]
+            # of a weight, as in check_attention; one rounding of each of the account's five sums
+            rel = max(rel, 2 * (ref[3].max() * ((hd + 4) * 2.0 ** -24 + (2.0 ** -21 if dtype == "f32" else 0)) + 2.0 ** -21)
+                      + (at + 1 + H + 8 + 5) * 2.0 ** -24)
+            B.cb_o_proj_ffn(o, x, 1, dm.dims, dm.layers_c[l], x, eng.ws)
+        B.cb_lmhead_argmax(x[0], dm.final_norm, dm.w_lm, dm.dims, logits, tok, eng.ws)
+        rules = B.logit_rules(history=dev_i32([hist]), history_len=dev_i32([len(hist)]), prompt_len=dev_i32([n]),
+                              repetition=dev(np.array([1.2], np.float32)))
+        B.cb_logits_process(logits, rules, logits, tok)
+        B.cb_sync(None)
+        assert int(tok) == K8.token(host(logits)[0])
+    for l in range(s.n_layers):
+        assert np.all(np.abs(host(acc[l]) - total[l]) <= total[l] * rel + 1e-30)
 
 
 # ------------------------------------------------------------------ cb_sync
