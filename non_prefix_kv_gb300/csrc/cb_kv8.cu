@@ -100,8 +100,8 @@ __device__ __forceinline__ void zero_bad(uint64_t* f) {
 // held in registers between the maximum and the coding, so every new element is read once and
 // every code written once.  Bound by HBM for a prompt: 4 x 16001 rows of 8 heads of 128 (262 MB
 // of bf16 in, 131 MB of codes out) take about 65 us, 6 TB/s, in a replayed graph (two chunks per
-// thread and 64-bit conversions where a tie shows: 110 us; conversions everywhere: 121 us).  By
-// latency for a token: one row of 4 sequences of 32 heads 4.1 us.
+// thread and 64-bit conversions where a tie shows: 110 us; conversions everywhere: 121 us); of fp32
+// 107 us, 6.1 TB/s.  By latency for a token: one row of 4 sequences of 32 heads 4.1 us.
 template <typename T, int NCH>
 __global__ void __launch_bounds__(512, sizeof(T) == 2 ? 2 : 1) k_kv8_append(const T* __restrict__ k, const T* __restrict__ v, int n_rows,
                                                      const int32_t* __restrict__ start,
@@ -190,8 +190,8 @@ __device__ __forceinline__ void put8(float* p, const float* f, bool al32) {
 
 // A thread turns 16 codes into 16 values, a few rows of them at once.  A CTA takes a run of
 // rows of one head: the codes it reads are contiguous, each row it writes is a contiguous run
-// of hd values.  Bound by HBM, mostly by what it writes: 655 MB in 100 us (fp32 out), 6.5 TB/s,
-// with 32-byte stores.
+// of hd values.  Bound by HBM, mostly by what it writes: 655 MB in 97 us (fp32 out), 6.8 TB/s,
+// with 32-byte stores; bf16 out, in 16-byte ones, 393 MB in 78 us, 5.1 TB/s.
 constexpr int kReadUnroll = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) k_kv8_read(const cb_kv8_cache c, int lg, const int32_t* __restrict__ start,

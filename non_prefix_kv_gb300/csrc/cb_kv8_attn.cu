@@ -13,8 +13,10 @@
 // Rounding: q goes to fp16 after a division by a power of two per row (its 8 bf16 bits fit in
 // fp16's 11; an element 2^14 below the row's largest loses bits that are 2^-25 of that
 // largest), fp32 q as two such parts (22 bits).  2^(t - m) is rounded to fp16 (2^-11) beside
-// the rounding of the bf16 output (2^-8), for fp32 output split in two parts.  Sums, maxima
-// and accumulators are fp32.
+// the rounding of the bf16 output (2^-8), for fp32 output split in two parts.  bf16 rows take
+// log2 vs and 1 / vs by the approximate instructions, each off by 2 ulp: of log2 vs, which goes into
+// the exponent, that is 2^-20 at vs = 0.03 and 2^-18 at the smallest scale, still below fp16's 2^-11;
+// fp32 rows take log2f.  Sums, maxima and accumulators are fp32.
 #include <math.h>
 
 #include <algorithm>

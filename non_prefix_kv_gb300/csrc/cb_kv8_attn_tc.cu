@@ -121,7 +121,9 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool swap) {
 // One CTA per (key tile, KV head, sequence): 128 rows of K and V codes to bf16 / fp16 in
 // 128-byte-swizzled slabs.  Tiles no query sees are skipped.  Bound by latency and L2 (34 MB of
 // codes read, 67 MB written that the next kernel reads from L2): 15 us for 8 heads of 16384 rows,
-// 19 us with 16-byte stores.
+// 19 us with 16-byte stores.  The loads come before it is known whether a query sees the tile, so a
+// cache that is mostly empty is read whole: 832 rows of 32 heads over 1638 held rows 50 us in a cache
+// for 16384 rows, 28 us in one for 1664 (at 16384 held rows 194 us).
 template <int HD, typename T>
 __global__ void __launch_bounds__(256) k_kv8_expand(const Kv8Tc p) {
   pdl_wait();
@@ -562,8 +564,9 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) k_kv8_attn_tc(const Kv8Tc p, 
       __syncwarp();
       if (lane < NG) {
         const float v = fmaxf(nx.v, kKv8MinScale);
-        // (approximate log and reciprocal: off by 2^-22 of a value beside P's own 2^-12; the exact
-        // forms cost 40 of 850 us at the Yi shape, by the few lanes that compute them)
+        // (approximate log and reciprocal: off by 2 ulp, which for the log is 2^-20 at vs = 0.03 and
+        // 2^-18 at the smallest scale, absolute in P's exponent, beside P's own rounding of 2^-12; the
+        // exact forms cost 40 of 850 us at the Yi shape, by the few lanes that compute them)
         sc[lane] = make_float4(fmaxf(nx.k, kKv8MinScale) * p.scale_log2, NP == 2 ? log2f(v) : __log2f(v), __fdividef(1.0f, v), 0.f);
       }
       nx = load_scales(ks, vs, p.lg, tile + 2, nk, lane);
@@ -1209,7 +1212,9 @@ void reset_kv8_tc_caches() {
 // the weights, 16 / 24 rows: 46, 61 and 41 us; 48, 59 and 56 us; 115, 141 and 124 us.  fp32, 32 / 48 /
 // 96 rows: 32 heads over 4096 keys 43, 54, 88 and 42 us; 8 over 16384 40, 54, 89 and 52 us; 4 sequences
 // of 4 over 8192 34, 43, 69 and 54 us; with the weights, 16 / 24 rows: 62, 86 and 58 us; 65, 85 and 68
-// us; 59, 71 and 68 us.
+// us; 59, 71 and 68 us.  The rule goes by rows alone; where the (sequence, KV head) units are few
+// and the rows just past the bound the other path would still be faster, by a quarter at the most
+// (8 heads over 16384 keys at 32 rows 35 and 39 us, fp32 4 x 4 over 8192 at 49 rows 43 and 54).
 bool kv8_tc_taken(int dt, int hd, int G, int n_q, bool weights) {
   return (hd == 64 || hd == 128) && G <= BM && (int64_t)n_q * G > (weights ? 16 : dt == DT_F32 ? 48 : 24) &&
          (n_q + BM / G - 1) / (BM / G) <= 65535;

@@ -11,9 +11,9 @@
 // launch, no workspace.  Everything that does not depend on the launch before (the cluster's
 // meeting, the clearing of the words) comes before the wait for it.
 //
-// Measured, 64 rows of 64000 bf16 ids, a history of 2048, 300 biases, a mask: 15.3 us (17 MB; all
+// Measured, 64 rows of 64000 bf16 ids, a history of 2048, 300 biases, a mask: 15.4 us (17 MB; all
 // 512 CTAs in one wave, bound by the chain history -> owners -> stream -> keys), one row of 32000
-// fp32 ids with a history of 4352 7.4 us.  With a word for the count and one for the bias, sixteen
+// fp32 ids with a history of 4352 7.5 us.  With a word for the count and one for the bias, sixteen
 // CTAs of 256 threads per row and the keys read back through two cluster barriers, 31.7 us (two
 // waves; 5.3 us of it the stream itself, 5.5 the keys).
 #include <math.h>
