@@ -280,12 +280,12 @@ int cb_kv8_workspace_bytes(const cb_dims* dims, int32_t n_seq, int64_t capacity,
  *            with an infinity it leaves those undefined, and only those.  A query that sees nothing
  *            may hold anything.
  * Queries need no order, but launches of many queries run faster when last ascends.
- * Scores (up to 1e30 in magnitude), maxima and all sums are held in fp32, codes enter the products
+ * Scores (up to 1e29 in magnitude), maxima and all sums are held in fp32, codes enter the products
  * exactly.  Rounded to fewer bits are: each weight p before it multiplies V, to fp16 (2^-11 of it; for
  * fp32 rows to two fp16 parts, 2^-22), and by at most 2^-33 of the row's largest p times V scale;
- * fp32 queries, to two fp16 parts (2^-22 of the row's largest element), bf16 ones lose only
- * bits below 2^-25 of it.  Exponentials and, for bf16 rows, log2 of V's scale are the approximate ones (2^-18 at the
- * most).  The entries of `weights` are not rounded to fp16.
+ * fp32 queries, to two fp16 parts (2^-22 of the row's largest element); bf16 ones lose only bits
+ * below 2^-25 of it.  Exponentials and, for bf16 rows, log2 of V's scale are the approximate ones
+ * (off by 2^-18 at the most).  The entries of `weights` are not rounded to fp16.
  * The results are the same from run to run (no floating-point atomics).  Calls that use one
  * workspace or add to the same weights must be ordered by their stream.
  * head_dim 32, 64, 128 or 256.  At most 2^27 query rows per KV head (n_q H / Hkv) and, where the
