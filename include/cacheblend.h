@@ -20,7 +20,7 @@
  *    allocator return 256-byte aligned blocks); the kernels move rows in 16- and 32-byte
  *    vectors.  A misaligned buffer is refused with CB_ERR_INVALID_ARG before any launch.
  *    Exceptions: cb_gather_rows and cb_scatter_kv need 4 bytes, 8-bit codes 8 bytes, and
- *    arrays of row indices, positions or scores 4 bytes.
+ *    arrays of row indices, positions or scores 4 bytes; cb_rope_rows takes element alignment.
  *  - Streams: every call takes a cudaStream_t (passed as void*, NULL = legacy default
  *    stream), enqueues its kernels on it and returns without synchronising, unless the
  *    description says otherwise.
@@ -179,6 +179,88 @@ int cb_rope_shift(void* k_dst, void* v_dst, const void* k_src, const void* v_src
                   const int32_t* src_row, int64_t n_src_rows, const int32_t* delta,
                   int64_t n_rows, const cb_dims* dims, const float* cos_sin, int32_t max_pos,
                   void* stream);
+
+/* ---- rotary positions in other forms --------------------------------------------------- */
+
+/* How a head's first rot_dim channels are paired and by what angle pair i turns per position.
+ * theta_i = base^(-2i / rot_dim), and for contexts longer than the model was trained on, with
+ * f = factor and L = original_len:
+ *   CB_ROPE_PLAIN   theta_i
+ *   CB_ROPE_LINEAR  theta_i / f                                  (positions interpolated)
+ *   CB_ROPE_BASE    with base f^(rot_dim / (rot_dim - 2)) for base
+ *   CB_ROPE_WAVES   by the wavelength w = 2 pi / theta_i: theta_i where w < L / high, theta_i / f
+ *                   where w > L / low, between them g theta_i + (1 - g) theta_i / f with
+ *                   g = (L / w - low) / (high - low)
+ *   CB_ROPE_RAMP    by the pair's index: (1 - r) theta_i + r theta_i / f, r = (i - lo) / (hi - lo)
+ *                   clamped to [0, 1], lo = max(floor(D(high)), 0), hi = min(ceil(D(low)),
+ *                   rot_dim - 1) (hi = lo: hi - lo counts as 0.001), D(b) = rot_dim
+ *                   ln(L / (2 pi b)) / (2 ln base): the index of the pair that turns b times in L */
+#define CB_ROPE_INTERLEAVED 0   /* pairs (x[2i], x[2i + 1])                              */
+#define CB_ROPE_HALF        1   /* pairs (x[i], x[i + rot_dim / 2])                       */
+
+#define CB_ROPE_PLAIN  0
+#define CB_ROPE_LINEAR 1
+#define CB_ROPE_BASE   2
+#define CB_ROPE_WAVES  3
+#define CB_ROPE_RAMP   4
+
+typedef struct {
+    int32_t layout;        /* CB_ROPE_INTERLEAVED or CB_ROPE_HALF                          */
+    int32_t rot_dim;       /* rotated channels: even, 2..256 (CB_ROPE_BASE: from 4 on)     */
+    int32_t scaling;       /* CB_ROPE_PLAIN .. CB_ROPE_RAMP                                */
+    double  base;          /* > 1                                                          */
+    double  factor;        /* f >= 1 (PLAIN: not used)                                     */
+    double  original_len;  /* L > 0 (WAVES, RAMP)                                          */
+    double  low, high;     /* 0 < low < high (WAVES, RAMP)                                 */
+    double  amplitude;     /* > 0: multiplies the table's cos and sin (and so q and k)     */
+} cb_rope_spec;
+
+/* theta_i of every pair: theta_host [rot_dim / 2].  Host-only. */
+int cb_rope_theta(const cb_rope_spec* spec, double* theta_host);
+
+/* Fills cos_sin [max_pos][rot_dim / 2][2] (fp32) with amplitude * cos and sin(p theta_i), the
+ * angle formed in fp64 and rounded once.  With rot_dim = head_dim and CB_ROPE_INTERLEAVED the
+ * table serves every call of this library that takes one; cached keys are re-positioned
+ * (cb_rope_shift, cb_rope_rows with offsets) with a table of amplitude 1. */
+int cb_rope_table_scaled(float* cos_sin, int32_t max_pos, const cb_rope_spec* spec, void* stream);
+
+/* The rows of one cb_rope_rows call.  Row strides are in elements; 0 stands for rows without
+ * gaps.  The three inputs may be parts of one projection's rows (q | k | v). */
+typedef struct {
+    const void* q;            /* [n, H hd], or NULL (with q_out): none                     */
+    void*       q_out;
+    int64_t     q_ld, q_out_ld;
+    const void* k;            /* rows of [Hkv hd], or NULL (with v, k_out and v_out): none */
+    const void* v;            /* NULL (with v_out): keys only                              */
+    int64_t     k_ld, v_ld;
+    const int32_t* src_row;   /* [n] rows of k and v, each in [0, n_src_rows); NULL: i     */
+    int64_t     n_src_rows;
+    void*       k_out;        /* rows of [Hkv hd], e.g. of a cache                         */
+    void*       v_out;
+    int64_t     kv_out_ld;    /* of both                                                   */
+    const int32_t* kv_row;    /* [n] rows of k_out and v_out, each in [0, n_out_rows), or -1:
+                               * an idle row, its k and v are not stored; NULL: i          */
+    int64_t     n_out_rows;
+} cb_rope_rows_io;
+
+/* Rotates rows, in one launch:
+ *   q_out[i] = R(pos[i]) q[i],  k_out[kv_row[i]] = R(pos[i]) k[src_row[i]],
+ *   v_out[kv_row[i]] = v[src_row[i]],
+ * every head alike, its channels from rot_dim on copied.  For a decoding step: q, k, v of the new
+ * tokens, k and v straight into the answers' caches.  With offsets for pos it re-positions cached
+ * keys as cb_rope_shift does.
+ *   pos     : [n] int32, |pos| < max_pos; a negative one turns back
+ *   inverse : nonzero turns every row back: R(-pos), which is also the gradient of the rotation
+ *   cos_sin : cb_rope_table_scaled's (or cb_rope_table's) of spec->rot_dim
+ * Of spec only layout and rot_dim (at most head_dim) are used.  An output may be its own input
+ * (same address and stride, k and v without row indices) and lies apart from everything else.
+ * Two rows with the same kv_row leave one of them.  Element alignment suffices; rows on 16 bytes
+ * with rot_dim a multiple of 16 are moved in vectors.  A position or row index outside its range
+ * is reported by cb_sync (CB_ERR_DEVICE): a bad position leaves the row's outputs as they were,
+ * a bad row index those of its k and v. */
+int cb_rope_rows(const cb_rope_rows_io* io, const int32_t* pos, int32_t n, int32_t inverse,
+                 const cb_dims* dims, const cb_rope_spec* spec, const float* cos_sin,
+                 int32_t max_pos, void* stream);
 
 /* ---- 8-bit chunk KV ([CG] §Step 1 per-channel quantization; entropy coding is not done) */
 
@@ -584,6 +666,35 @@ typedef struct {
 int cb_logits_process(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype,
                       const cb_logit_rules* rules, void* out, int32_t* token, void* stream);
 
+/* How the next token of each row is drawn; a NULL pointer leaves a rule off. */
+typedef struct {
+    const float*   temperature;  /* [n_rows] T >= 0; 0: the lowest id of the largest logit   */
+    const int32_t* top_k;        /* [n_rows] keep the k largest; <= 0: all                   */
+    const float*   top_p;        /* [n_rows] keep the fewest that hold this share; >= 1: all,
+                                  * <= 0: the first                                          */
+    const float*   min_p;        /* [n_rows] keep w >= min_p; <= 0: all, above 1 as 1        */
+} cb_sample_rules;
+
+/* Draws a token per row from the given numbers:
+ *   w_i = exp((l_i - max l) / T), in order of falling logit, then rising id;
+ *   kept: the first top_k; of these the fewest whose weight reaches top_p of theirs; of these
+ *   the ones with w_i >= min_p;
+ *   token: the first kept id, by id, whose running weight exceeds u times the kept weight.
+ *   logits  : [n_rows, vocab] of `dtype` (CB_F32 or CB_BF16), e.g. cb_logits_process's out
+ *   u       : [n_rows] fp32 in [0, 1)
+ *   token   : [n_rows] int32; -1 if no logit is above -inf
+ *   logprob : [n_rows] fp32 or NULL: ln of the token's share of the kept weight (token -1: -inf)
+ *   n_kept  : [n_rows] int32 or NULL: how many ids were kept
+ * Weights are exact to 2^-29 and their sums exact, so a decision is the one of the formulas above
+ * but where they differ by less than that; results do not depend on the row's place or company.
+ * Ids at -inf are never kept, at +inf they share all the weight.  Reported by cb_sync
+ * (CB_ERR_NONFINITE): a NaN logit (never kept), a temperature that is not a finite number >= 0
+ * (counts as 1), a NaN share (off), a u outside [0, 1) (the nearest in it; NaN: 0).
+ * vocab up to 2^20. */
+int cb_sample_token(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype, const float* u,
+                    const cb_sample_rules* rules, int32_t* token, float* logprob, int32_t* n_kept,
+                    void* stream);
+
 /* ---- layer-ahead loading ------------------------------------------------------------ */
 
 /* Starts the copy of one layer's cached chunk KV from pinned host memory to the device on
@@ -624,6 +735,10 @@ int cb_stream_wait(void* stream, void* event);
                                  * the tensor cores (three launches at most, one record)  */
 #define CB_PROF_KV8_EVICT  15   /* aux: 0 selection, 1 move                                */
 #define CB_PROF_LOGITS     16
+#define CB_PROF_ROPE_ROWS  17
+#define CB_PROF_SHARED     18   /* shared-prefix attention; aux: 0 prefixes, 1 own rows, 2 the
+                                 * join of both                                            */
+#define CB_PROF_SAMPLE     19
 
 typedef struct {
     int32_t kind;      /* CB_PROF_*                                                     */

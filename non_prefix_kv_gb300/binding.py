@@ -14,6 +14,8 @@ CB_OK = 0
 CB_F32, CB_BF16 = 0, 1
 CB_DEV_KV, CB_DEV_K = 0, 1
 CB_LAYER_PRECHECK, CB_LAYER_CHECK, CB_LAYER_STEADY, CB_LAYER_GRADUAL = 0, 1, 2, 3
+CB_ROPE_INTERLEAVED, CB_ROPE_HALF = 0, 1
+CB_ROPE_PLAIN, CB_ROPE_LINEAR, CB_ROPE_BASE, CB_ROPE_WAVES, CB_ROPE_RAMP = 0, 1, 2, 3, 4
 STATUS_NAMES = {0: "CB_OK", 1: "CB_ERR_INVALID_ARG", 2: "CB_ERR_SHAPE", 3: "CB_ERR_DTYPE",
                 4: "CB_ERR_WORKSPACE", 5: "CB_ERR_NONFINITE", 6: "CB_ERR_CUDA", 7: "CB_ERR_TIMEOUT",
                 8: "CB_ERR_UNSUPPORTED", 9: "CB_ERR_DEVICE", 10: "CB_ERR_IO"}
@@ -64,9 +66,29 @@ class cb_logit_rules(C.Structure):
                 ("mask_ld", C.c_int64), ("n_bias", C.c_int32)]
 
 
+class cb_rope_spec(C.Structure):
+    """A form of rotary positions (see cacheblend.h); made by rope_spec()."""
+    _fields_ = [("layout", C.c_int32), ("rot_dim", C.c_int32), ("scaling", C.c_int32), ("base", C.c_double),
+                ("factor", C.c_double), ("original_len", C.c_double), ("low", C.c_double), ("high", C.c_double),
+                ("amplitude", C.c_double)]
+
+
+class cb_rope_rows_io(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_out", C.c_void_p), ("q_ld", C.c_int64), ("q_out_ld", C.c_int64),
+                ("k", C.c_void_p), ("v", C.c_void_p), ("k_ld", C.c_int64), ("v_ld", C.c_int64),
+                ("src_row", C.c_void_p), ("n_src_rows", C.c_int64), ("k_out", C.c_void_p), ("v_out", C.c_void_p),
+                ("kv_out_ld", C.c_int64), ("kv_row", C.c_void_p), ("n_out_rows", C.c_int64)]
+
+
+class cb_sample_rules(C.Structure):
+    """The rules of cb_sample_token (see cacheblend.h); made by sample_rules()."""
+    _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p)]
+
+
 PROF_KINDS = {0: "rope_shift", 1: "copy_rows", 2: "rmsnorm", 3: "gemm", 4: "attention", 5: "deviation",
               6: "topk", 7: "index", 8: "lmhead_gemv", 9: "argmax", 10: "rope_table", 11: "kv_quantize", 12: "kv8_append",
-              13: "kv8_read", 14: "kv8_attention", 15: "kv8_evict", 16: "logits"}
+              13: "kv8_read", 14: "kv8_attention", 15: "kv8_evict", 16: "logits", 17: "rope_rows",
+              18: "shared_attention", 19: "sample"}
 
 _P = C.c_void_p
 _I32 = C.c_int32
@@ -119,6 +141,11 @@ _PROTOS = {
     "cb_kv8_evict": (C.c_int, [C.POINTER(cb_kv8_cache), _P, _P, _I32, _I32, _I32, C.POINTER(cb_kv8_cache), _P, _P, _P,
                                C.POINTER(cb_dims), _P]),
     "cb_logits_process": (C.c_int, [_P, _I32, _I32, _I32, C.POINTER(cb_logit_rules), _P, _P, _P]),
+    "cb_rope_theta": (C.c_int, [C.POINTER(cb_rope_spec), C.POINTER(C.c_double)]),
+    "cb_rope_table_scaled": (C.c_int, [_P, _I32, C.POINTER(cb_rope_spec), _P]),
+    "cb_rope_rows": (C.c_int, [C.POINTER(cb_rope_rows_io), _P, _I32, _I32, C.POINTER(cb_dims), C.POINTER(cb_rope_spec), _P,
+                               _I32, _P]),
+    "cb_sample_token": (C.c_int, [_P, _I32, _I32, _I32, _P, C.POINTER(cb_sample_rules), _P, _P, _P, _P]),
     "cb_prefetch_layer": (C.c_int, [_P, _P, _SZ, _P, _P]),
     "cb_stream_wait": (C.c_int, [_P, _P]),
     "cb_kernel_launch_count": (_I64, []),
@@ -602,3 +629,100 @@ def cb_logits_process(logits, rules: cb_logit_rules, out=None, token=None, strea
     _check("cb_logits_process", lib().cb_logits_process(
         _buf("logits", logits, logits.dtype, None, dev), n, vocab, dt, C.byref(rules),
         _buf("out", out, logits.dtype, n * vocab, dev), _buf("token", token, T.i32, n, dev), T.stream(stream, dev)))
+
+
+# ---- rotary positions in other forms, sampling ----------------------------------------------
+def rope_spec(layout: int, rot_dim: int, base: float, scaling: int = CB_ROPE_PLAIN, factor: float = 1.0,
+              original_len: float = 0.0, low: float = 0.0, high: float = 0.0, amplitude: float = 1.0) -> cb_rope_spec:
+    """A form of rotary positions; refused if the header's ranges are not kept."""
+    s = cb_rope_spec(layout, rot_dim, scaling, base, factor, original_len, low, high, amplitude)
+    cb_rope_theta(s)
+    return s
+
+
+def cb_rope_theta(spec: cb_rope_spec) -> list:
+    """The angle each pair turns per position."""
+    out = (C.c_double * 128)()
+    _check("cb_rope_theta", lib().cb_rope_theta(C.byref(spec), out))
+    return list(out[:spec.rot_dim // 2])
+
+
+def cb_rope_table_scaled(cos_sin, max_pos: int, spec: cb_rope_spec, stream=None):
+    T = _torch()
+    dev = T.device()
+    _check("cb_rope_table_scaled", lib().cb_rope_table_scaled(
+        _buf("cos_sin", cos_sin, T.f32, max_pos * spec.rot_dim, dev), max_pos, C.byref(spec), T.stream(stream, dev)))
+
+
+def _strided(what: str, t, dtype, width: int, dev: int):
+    """Address and row stride of rows [n, width] whose channels are contiguous (a part of wider rows)."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {t.dtype}, expected {dtype}")
+    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()}, expected rows of {width} contiguous elements")
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, not on the current CUDA device")
+    # (one row has no stride; of none nothing is read)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def cb_rope_rows(q, k, v, pos, q_out, k_out, v_out, dims: cb_dims, spec: cb_rope_spec, cos_sin, max_pos: int, src_row=None,
+                 kv_row=None, inverse: bool = False, stream=None):
+    """q, q_out [n, H hd]; k, v rows of [Hkv hd] (row src_row[i]), k_out, v_out rows of [Hkv hd]
+    (row kv_row[i], -1: none): 2-D tensors, their rows may be parts of wider ones.  q or k, v may be
+    None with their outputs.  cos_sin: cb_rope_table_scaled's for at least max_pos positions."""
+    T = _torch()
+    dev, dt = T.device(), T.row[dims.dtype]
+    n, qw, w = pos.numel(), dims.n_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
+    for what, t in (("q", q), ("q_out", q_out)):
+        if t is not None and t.shape[0] != n:
+            raise ValueError(f"{what}: {t.shape[0]} rows, {n} positions")
+    for what, t, ref in (("v", v, k), ("v_out", v_out, k_out)):
+        if t is not None and (ref is None or t.shape[0] != ref.shape[0]):
+            raise ValueError(f"{what}: not the rows of {'k' if what == 'v' else 'k_out'}")
+    if cos_sin.numel() < max_pos * spec.rot_dim:
+        raise ValueError(f"cos_sin holds {cos_sin.numel()} values, {max_pos} positions of {spec.rot_dim} channels need more")
+    (pq, lq), (pqo, lqo) = _strided("q", q, dt, qw, dev), _strided("q_out", q_out, dt, qw, dev)
+    (pk, lk), (pv, lv) = _strided("k", k, dt, w, dev), _strided("v", v, dt, w, dev)
+    (pko, lko), (pvo, lvo) = _strided("k_out", k_out, dt, w, dev), _strided("v_out", v_out, dt, w, dev)
+    if pvo is not None and lvo != lko:
+        raise ValueError("k_out and v_out differ in their row stride")
+    io = cb_rope_rows_io(pq, pqo, lq, lqo, pk, pv, lk, lv, _buf("src_row", src_row, T.i32, n, dev),
+                         0 if k is None else k.shape[0], pko, pvo, lko, _buf("kv_row", kv_row, T.i32, n, dev),
+                         0 if k_out is None else k_out.shape[0])
+    _check("cb_rope_rows", lib().cb_rope_rows(
+        C.byref(io), _buf("pos", pos, T.i32, n, dev), n, 1 if inverse else 0, C.byref(dims), C.byref(spec),
+        _buf("cos_sin", cos_sin, T.f32, None, dev), max_pos, T.stream(stream, dev)))
+
+
+def sample_rules(temperature=None, top_k=None, top_p=None, min_p=None) -> cb_sample_rules:
+    """The rules of one batch: [n_rows] float32, top_k int32.  None leaves a rule off."""
+    T = _torch()
+    dev = T.device()
+    given = [t for t in (temperature, top_k, top_p, min_p) if t is not None]
+    n = given[0].numel() if given else None
+    r = cb_sample_rules(_buf("temperature", temperature, T.f32, n, dev), _buf("top_k", top_k, T.i32, n, dev),
+                        _buf("top_p", top_p, T.f32, n, dev), _buf("min_p", min_p, T.f32, n, dev))
+    r.n_rows, r.dev, r.tensors = n, dev if given else None, (temperature, top_k, top_p, min_p)
+    return r
+
+
+def cb_sample_token(logits, u, rules: cb_sample_rules, token, logprob=None, n_kept=None, stream=None):
+    """logits [n_rows, vocab] float32 or bfloat16, u [n_rows] float32; token, logprob and n_kept as in
+    the header."""
+    T = _torch()
+    dev = T.device()
+    n, vocab = logits.shape
+    if rules.n_rows is not None and rules.n_rows != n:
+        raise ValueError(f"rules for {rules.n_rows} rows, logits of {n}")
+    if rules.dev is not None and rules.dev != dev:
+        raise ValueError(f"rules: on cuda:{rules.dev}, not on the current CUDA device")
+    dt = T.cb.get(logits.dtype)
+    if dt is None:
+        raise ValueError(f"logits: {logits.dtype}, expected float32 or bfloat16")
+    _check("cb_sample_token", lib().cb_sample_token(
+        _buf("logits", logits, logits.dtype, None, dev), n, vocab, dt, _buf("u", u, T.f32, n, dev), C.byref(rules),
+        _buf("token", token, T.i32, n, dev), _buf("logprob", logprob, T.f32, n, dev),
+        _buf("n_kept", n_kept, T.i32, n, dev), T.stream(stream, dev)))

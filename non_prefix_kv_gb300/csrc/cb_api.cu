@@ -43,6 +43,13 @@ cudaError_t launch_kv8_tc(int dt, const void* q, const int32_t* last, int n_q, c
                           void* out, float* weights, void* ws, cudaStream_t s);
 cudaError_t launch_logits(int dt, const void* logits, int n_rows, int vocab, const cb_logit_rules& r, void* out,
                           int32_t* token, cudaStream_t s);
+// rotary positions (cb_rope.cu) and sampling (cb_sample.cu)
+cudaError_t launch_rope_table_scaled(float* tab, int max_pos, int rot, const double* theta, double amplitude,
+                                     cudaStream_t s);
+cudaError_t launch_rope_rows(int dt, const cb_rope_rows_io& io, const int32_t* pos, int n, int H, int Hkv, int hd, int rot,
+                             bool half, bool vec, const float* tab, int max_pos, bool inverse, cudaStream_t s);
+cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, const float* u, const cb_sample_rules& r,
+                          int32_t* token, float* logprob, int32_t* kept, cudaStream_t s);
 }  // namespace cb
 
 using namespace cb;
@@ -525,7 +532,7 @@ int cb_sync(void* stream, double timeout_s) {
   }
   const uint32_t bits = take_error_mem() | take_error_gemm() | take_error_gemm_tc() | take_error_attn() |
                         take_error_attn_tc() | take_error_kv8() | take_error_kv8_attn() | take_error_kv8_tc() |
-                        take_error_logits();
+                        take_error_logits() | take_error_rope() | take_error_sample();
   if (bits & ERRBIT_NONFINITE)
     return fail(CB_ERR_NONFINITE, "a deviation score, cache row, weight or logit was NaN/Inf (or out of its range)");
   if (bits & ERRBIT_INDEX) return fail(CB_ERR_DEVICE, "a kernel met an out-of-range index");
@@ -1395,6 +1402,170 @@ int cb_logits_process(const void* logits, int32_t n_rows, int32_t vocab, int32_t
     return fail(CB_ERR_INVALID_ARG, "out overlaps logits without being the same buffer");
   CB_LAUNCH(CB_PROF_LOGITS, 0, n_rows, vocab, 0, 0.0, (double)bytes * (out ? 2.0 : 1.0), S(stream),
             launch_logits(dtype, logits, n_rows, vocab, r, out, token, S(stream)));
+  return CB_OK;
+}
+
+// ---- rotary positions in other forms --------------------------------------------------------
+namespace {
+
+// theta_i of every pair, or why there is none
+int rope_theta(const cb_rope_spec* s, double* t) {
+  if (!s) return fail(CB_ERR_INVALID_ARG, "rope spec is NULL");
+  if (s->layout != CB_ROPE_INTERLEAVED && s->layout != CB_ROPE_HALF)
+    return fail(CB_ERR_INVALID_ARG, "rope layout %d", s->layout);
+  if (s->scaling < CB_ROPE_PLAIN || s->scaling > CB_ROPE_RAMP) return fail(CB_ERR_INVALID_ARG, "rope scaling %d", s->scaling);
+  const int rot = s->rot_dim, half = rot / 2;
+  if (rot < 2 || rot > 256 || rot % 2) return fail(CB_ERR_SHAPE, "rot_dim %d is not even in [2, 256]", rot);
+  if (!(s->base > 1.0) || !isfinite(s->base)) return fail(CB_ERR_INVALID_ARG, "rope base");
+  if (!(s->amplitude > 0.0) || !isfinite(s->amplitude)) return fail(CB_ERR_INVALID_ARG, "rope amplitude");
+  const double f = s->scaling == CB_ROPE_PLAIN ? 1.0 : s->factor, L = s->original_len, pi = 3.14159265358979323846;
+  if (!(f >= 1.0) || !isfinite(f)) return fail(CB_ERR_INVALID_ARG, "rope factor below 1");
+  const bool parts = s->scaling == CB_ROPE_WAVES || s->scaling == CB_ROPE_RAMP;
+  if (parts && (!(L > 0.0) || !isfinite(L))) return fail(CB_ERR_INVALID_ARG, "rope original_len");
+  if (parts && (!(s->low > 0.0) || !(s->high > s->low) || !isfinite(s->high)))
+    return fail(CB_ERR_INVALID_ARG, "rope needs 0 < low < high");
+  if (s->scaling == CB_ROPE_BASE && rot < 4) return fail(CB_ERR_SHAPE, "CB_ROPE_BASE needs rot_dim >= 4");
+  if (!t) return CB_OK;
+  const double base = s->scaling == CB_ROPE_BASE ? s->base * pow(f, (double)rot / (rot - 2)) : s->base;
+  auto dim = [&](double b) { return rot * log(L / (2 * pi * b)) / (2 * log(s->base)); };
+  double lo = 0, hi = 1;
+  if (s->scaling == CB_ROPE_RAMP) {
+    lo = std::max(floor(dim(s->high)), 0.0);
+    hi = std::min(ceil(dim(s->low)), rot - 1.0);
+  }
+  for (int i = 0; i < half; ++i) {
+    const double th = pow(base, -2.0 * i / rot);
+    t[i] = th;
+    if (s->scaling == CB_ROPE_LINEAR) {
+      t[i] = th / f;
+    } else if (s->scaling == CB_ROPE_WAVES) {
+      const double w = 2 * pi / th;
+      if (w > L / s->low) {
+        t[i] = th / f;
+      } else if (w >= L / s->high) {
+        const double g = (L / w - s->low) / (s->high - s->low);
+        t[i] = g * th + (1 - g) * th / f;
+      }
+    } else if (s->scaling == CB_ROPE_RAMP) {
+      const double r = std::min(std::max((i - lo) / (hi == lo ? 0.001 : hi - lo), 0.0), 1.0);
+      t[i] = (1 - r) * th + r * th / f;
+    }
+  }
+  return CB_OK;
+}
+
+// rows of `width` bytes, `ld` bytes apart
+struct Strided {
+  const void* p;
+  int64_t rows, width, ld;
+  bool same(const Strided& o) const { return p == o.p && ld == o.ld; }
+};
+bool rows_meet(const Strided& a, const Strided& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  const size_t na = (size_t)((a.rows - 1) * a.ld + a.width), nb = (size_t)((b.rows - 1) * b.ld + b.width);
+  if (!meet(Range{a.p, na}, Range{b.p, nb})) return false;
+  if (a.ld != b.ld) return true;
+  // columns of one row pitch: apart if neither reaches into the other's, once round the pitch
+  const int64_t ld = a.ld;
+  const int64_t d = (((reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) % ld) + ld) % ld;
+  return !(d >= a.width && d + b.width <= ld);
+}
+
+}  // namespace
+
+int cb_rope_theta(const cb_rope_spec* spec, double* theta_host) {
+  if (!theta_host) return fail(CB_ERR_INVALID_ARG, "theta_host is NULL");
+  return rope_theta(spec, theta_host);
+}
+
+int cb_rope_table_scaled(float* cos_sin, int32_t max_pos, const cb_rope_spec* spec, void* stream) {
+  double theta[128];
+  if (int st = rope_theta(spec, theta)) return st;
+  if (max_pos < 0) return fail(CB_ERR_SHAPE, "max_pos < 0");
+  if (max_pos == 0) return CB_OK;
+  if (!cos_sin) return fail(CB_ERR_INVALID_ARG, "cos_sin is NULL");
+  if (int st = check_al16({cos_sin}, "rope_table_scaled")) return st;
+  const double n = (double)max_pos * (spec->rot_dim / 2);
+  CB_LAUNCH(CB_PROF_ROPE_TABLE, 1, (int64_t)n, spec->rot_dim, 0, 0.0, 8.0 * n, S(stream),
+            launch_rope_table_scaled(cos_sin, max_pos, spec->rot_dim, theta, spec->amplitude, S(stream)));
+  return CB_OK;
+}
+
+int cb_rope_rows(const cb_rope_rows_io* io, const int32_t* pos, int32_t n, int32_t inverse, const cb_dims* dims,
+                 const cb_rope_spec* spec, const float* cos_sin, int32_t max_pos, void* stream) {
+  int st = check_dims(dims);
+  if (st || (st = rope_theta(spec, nullptr))) return st;
+  const int H = dims->n_heads, Hkv = dims->n_kv_heads, hd = dims->head_dim, rot = spec->rot_dim;
+  if (rot > hd) return fail(CB_ERR_SHAPE, "rot_dim %d exceeds head_dim %d", rot, hd);
+  if (n < 0 || max_pos < 1) return fail(CB_ERR_SHAPE, "need n >= 0 and max_pos >= 1");
+  if (!io) return fail(CB_ERR_INVALID_ARG, "rope_rows: io is NULL");
+  if (n == 0) return CB_OK;
+  cb_rope_rows_io a = *io;
+  if ((!a.q && !a.k) || !pos || !cos_sin) return fail(CB_ERR_INVALID_ARG, "rope_rows pointer is NULL");
+  if (!a.q != !a.q_out || !a.k != !a.k_out || !a.v != !a.v_out || (a.v && !a.k))
+    return fail(CB_ERR_INVALID_ARG, "rope_rows: every input needs its output, and v needs k");
+  const int64_t qw = (int64_t)H * hd, W = (int64_t)Hkv * hd, e = (int64_t)esize(dims->dtype);
+  for (int64_t* ld : {&a.q_ld, &a.q_out_ld})
+    if (!*ld) *ld = qw;
+  for (int64_t* ld : {&a.k_ld, &a.v_ld, &a.kv_out_ld})
+    if (!*ld) *ld = W;
+  const int64_t most = (int64_t)1 << 40;      // (keeps every product with a row index in 64 bits)
+  if ((a.q && (a.q_ld < qw || a.q_out_ld < qw || a.q_ld > most || a.q_out_ld > most)) ||
+      (a.k && (a.k_ld < W || a.kv_out_ld < W || a.k_ld > most || a.kv_out_ld > most)) ||
+      (a.v && (a.v_ld < W || a.v_ld > most)))
+    return fail(CB_ERR_SHAPE, "rope_rows: a row stride is shorter than its row (or beyond 2^40)");
+  if (a.k) {
+    if (a.n_src_rows < 0 || a.n_out_rows < 0 || a.n_src_rows > INT32_MAX || a.n_out_rows > INT32_MAX ||
+        (!a.src_row && a.n_src_rows < n) || (!a.kv_row && a.n_out_rows < n))
+      return fail(CB_ERR_SHAPE, "rope_rows: without row indices the buffers hold at least n rows (at most 2^31 - 1)");
+  }
+  const uintptr_t elems = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.q_out) |
+                          reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                          reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out);
+  const uintptr_t words = reinterpret_cast<uintptr_t>(pos) | reinterpret_cast<uintptr_t>(a.src_row) | reinterpret_cast<uintptr_t>(a.kv_row);
+  if (elems % (uintptr_t)e || words % 4) return fail(CB_ERR_INVALID_ARG, "rope_rows: buffer not aligned to its elements");
+  if ((st = check_al16({cos_sin}, "rope_rows"))) return st;
+  const Strided q{a.q, n, qw * e, a.q_ld * e}, qo{a.q_out, n, qw * e, a.q_out_ld * e},
+      k{a.k, a.src_row ? a.n_src_rows : n, W * e, a.k_ld * e}, v{a.v, a.src_row ? a.n_src_rows : n, W * e, a.v_ld * e},
+      ko{a.k_out, a.kv_row ? a.n_out_rows : n, W * e, a.kv_out_ld * e}, vo{a.v_out, a.kv_row ? a.n_out_rows : n, W * e, a.kv_out_ld * e};
+  const bool rows = !a.src_row && !a.kv_row;
+  const Strided ps{pos, 1, (int64_t)n * 4, (int64_t)n * 4}, ss{a.src_row, 1, (int64_t)n * 4, (int64_t)n * 4},
+      ds{a.kv_row, 1, (int64_t)n * 4, (int64_t)n * 4}, tb{cos_sin, 1, (int64_t)max_pos * rot * 4, (int64_t)max_pos * rot * 4};
+  bool bad = rows_meet(qo, ko) || rows_meet(qo, vo) || rows_meet(ko, vo) || rows_meet(qo, k) || rows_meet(qo, v) || rows_meet(ko, q) || rows_meet(ko, v) ||
+             rows_meet(vo, q) || rows_meet(vo, k) || (rows_meet(qo, q) && !qo.same(q)) || (rows_meet(ko, k) && !(rows && ko.same(k))) ||
+             (rows_meet(vo, v) && !(rows && vo.same(v)));
+  for (const Strided& o : {qo, ko, vo})
+    for (const Strided& i : {ps, ss, ds, tb}) bad = bad || rows_meet(o, i);
+  if (bad) return fail(CB_ERR_INVALID_ARG, "rope_rows: an output overlaps another argument");
+  const bool half = spec->layout == CB_ROPE_HALF;
+  const bool vec = rot % 16 == 0 && elems % 16 == 0 &&
+                   ((a.q ? a.q_ld | a.q_out_ld : 0) | (a.k ? a.k_ld | a.kv_out_ld : 0) | (a.v ? a.v_ld : 0)) * e % 16 == 0;
+  const double w = (a.q ? qw : 0) + (a.v ? 2.0 : a.k ? 1.0 : 0.0) * W;
+  CB_LAUNCH(CB_PROF_ROPE_ROWS, 0, n, (int64_t)w, rot, 3.0 * n * rot * ((a.q ? H : 0) + (a.k ? Hkv : 0)), 2.0 * e * n * w,
+            S(stream), launch_rope_rows(dims->dtype, a, pos, n, H, Hkv, hd, rot, half, vec, cos_sin, max_pos, inverse != 0,
+                                        S(stream)));
+  return CB_OK;
+}
+
+int cb_sample_token(const void* logits, int32_t n_rows, int32_t vocab, int32_t dtype, const float* u,
+                    const cb_sample_rules* rules, int32_t* token, float* logprob, int32_t* n_kept, void* stream) {
+  if (dtype != CB_F32 && dtype != CB_BF16) return fail(CB_ERR_DTYPE, "dtype %d", dtype);
+  if (n_rows < 0 || n_rows > 65535 || vocab < 1) return fail(CB_ERR_SHAPE, "need 0 <= n_rows <= 65535, vocab >= 1");
+  if (vocab > (1 << 20)) return fail(CB_ERR_UNSUPPORTED, "vocab %d exceeds 2^20", vocab);
+  if (!rules) return fail(CB_ERR_INVALID_ARG, "rules is NULL");
+  if (n_rows == 0) return CB_OK;
+  if (!logits || !u || !token) return fail(CB_ERR_INVALID_ARG, "sample_token pointer is NULL");
+  const cb_sample_rules& r = *rules;
+  if (int st = check_al16({logits}, "sample_token")) return st;
+  for (const void* q : {(const void*)u, (const void*)token, (const void*)logprob, (const void*)n_kept, (const void*)r.temperature,
+                        (const void*)r.top_k, (const void*)r.top_p, (const void*)r.min_p})
+    if (reinterpret_cast<uintptr_t>(q) & 3) return fail(CB_ERR_INVALID_ARG, "sample_token: array not 4-byte aligned");
+  const size_t bytes = (size_t)n_rows * vocab * esize(dtype), n4 = (size_t)n_rows * 4;
+  if (writes_meet({{token, n4}, {logprob, n4}, {n_kept, n4}},
+                  {{logits, bytes}, {u, n4}, {r.temperature, n4}, {r.top_k, n4}, {r.top_p, n4}, {r.min_p, n4}}))
+    return fail(CB_ERR_INVALID_ARG, "sample_token: an output overlaps another argument");
+  CB_LAUNCH(CB_PROF_SAMPLE, 0, n_rows, vocab, 0, 0.0, (double)bytes, S(stream),
+            launch_sample(dtype, logits, n_rows, vocab, u, r, token, logprob, n_kept, S(stream)));
   return CB_OK;
 }
 

@@ -195,6 +195,8 @@ uint32_t take_error_kv8();
 uint32_t take_error_kv8_attn();
 uint32_t take_error_kv8_tc();
 uint32_t take_error_logits();
+uint32_t take_error_rope();
+uint32_t take_error_sample();
 void reset_kv8_attn_caches();
 void reset_kv8_tc_caches();
 void reset_logits_caches();
