@@ -398,6 +398,51 @@ int cb_kv8_evict(const cb_kv8_cache* src, const int32_t* len, const float* weigh
                  int32_t* dst_len, float* dst_weights, int32_t* kept, const cb_dims* dims,
                  void* stream);
 
+/* ---- attention over a shared prefix ------------------------------------------------------ */
+
+/* Keys and values of one layer for a batch of sequences that share prefixes: answers to one
+ * blended prompt, or questions about the same documents.  The batch's sequences come group by
+ * group: those of group g are [seq0[g], seq0[g + 1]), and all of them see the rows
+ * [row0[g], row0[g] + len[g]) of k and v, and each its own rows behind them. */
+typedef struct {
+    const void*    k;          /* [n_rows, Hkv hd] the prefixes' rows, e.g. a request's blended cache */
+    const void*    v;
+    int64_t        n_rows;     /* at most 2^31 - 1                                        */
+    const int32_t* row0_host;  /* [n_groups]                                              */
+    const int32_t* len_host;   /* [n_groups] >= 0, row0 + len <= n_rows                   */
+    const int32_t* seq0_host;  /* [n_groups + 1] ascending, from 0 to n_seq               */
+    int32_t        n_groups;   /* 1..64                                                   */
+    int32_t        n_seq;      /* 1..65535                                                */
+    const void*    own_k;      /* [n_seq, capacity, Hkv hd]; NULL with capacity 0         */
+    const void*    own_v;
+    int64_t        capacity;   /* rows of a sequence's own cache; n_seq * capacity below 2^31 */
+} cb_shared_kv;
+
+/* Device workspace (bytes) of cb_shared_attention for n_q queries per sequence.  Host-only.
+ * Refuses what the call refuses.  It grows with n_q, n_seq, the prefixes and the capacity, but not
+ * evenly: a buffer for several calls is the largest of what each of them asks for. */
+int cb_shared_workspace_bytes(const cb_shared_kv* kv, const cb_dims* dims, int32_t n_q, size_t* out_host);
+
+/* Attention of n_q queries per sequence over its group's prefix and its own rows:
+ *   out[s, j, h] = sum_i p_i v[i],  p = softmax_i(q[s, j, h] . k[i] / sqrt(hd)),
+ * i over the prefix rows and the own rows 0..last[s, j], k and v of KV head h / (H / Hkv).  The
+ * prefix is read once for all sequences of its group.
+ *   q, out : [n_seq, n_q, H hd] of dims->dtype
+ *   last   : [n_seq, n_q] int32: the last own row that the query sees (a token stored at row r sees
+ *            itself: last = r); -1: the prefix only; -2: nothing, its output row is 0 (padding), as
+ *            is that of a query that sees no row at all.  A value outside [-2, capacity) is reported
+ *            by cb_sync (CB_ERR_DEVICE) and counts as -2.
+ * Own rows that no query of the sequence sees, and rows of k and v outside the prefixes, may hold
+ * anything; a row of V that some query of a sequence sees must be finite for the others as well.  A
+ * query that is not finite spoils its own output row only.
+ * Scores, maxima and sums are fp32; for bf16 the weights p are rounded to bf16 (2^-8 of each at most)
+ * before they multiply V, where the tensor cores take them (head_dim 64 and 128); fp32 is exact
+ * arithmetic.  Results are the same from run to run.  Calls that share a workspace must be ordered
+ * by their stream, two graphs that do by their replays.
+ * out and the workspace overlap no other argument.  At most 2^31 - 1 pieces of work. */
+int cb_shared_attention(const void* q, const int32_t* last, int32_t n_q, const cb_shared_kv* kv,
+                        const cb_dims* dims, void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- HKVD selection ----------------------------------------------------------------- */
 
 /* Per-candidate deviation and top-k ([CB-A] §KV deviation; §HKVD selection code):

@@ -80,6 +80,13 @@ class cb_rope_rows_io(C.Structure):
                 ("kv_out_ld", C.c_int64), ("kv_row", C.c_void_p), ("n_out_rows", C.c_int64)]
 
 
+class cb_shared_kv(C.Structure):
+    """A layer's keys and values of sequences that share prefixes (see cacheblend.h); made by shared_kv()."""
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("n_rows", C.c_int64), ("row0_host", C.POINTER(C.c_int32)),
+                ("len_host", C.POINTER(C.c_int32)), ("seq0_host", C.POINTER(C.c_int32)), ("n_groups", C.c_int32),
+                ("n_seq", C.c_int32), ("own_k", C.c_void_p), ("own_v", C.c_void_p), ("capacity", C.c_int64)]
+
+
 class cb_sample_rules(C.Structure):
     """The rules of cb_sample_token (see cacheblend.h); made by sample_rules()."""
     _fields_ = [("temperature", C.c_void_p), ("top_k", C.c_void_p), ("top_p", C.c_void_p), ("min_p", C.c_void_p)]
@@ -145,6 +152,8 @@ _PROTOS = {
     "cb_rope_table_scaled": (C.c_int, [_P, _I32, C.POINTER(cb_rope_spec), _P]),
     "cb_rope_rows": (C.c_int, [C.POINTER(cb_rope_rows_io), _P, _I32, _I32, C.POINTER(cb_dims), C.POINTER(cb_rope_spec), _P,
                                _I32, _P]),
+    "cb_shared_workspace_bytes": (C.c_int, [C.POINTER(cb_shared_kv), C.POINTER(cb_dims), _I32, C.POINTER(_SZ)]),
+    "cb_shared_attention": (C.c_int, [_P, _P, _I32, C.POINTER(cb_shared_kv), C.POINTER(cb_dims), _P, _P, _SZ, _P]),
     "cb_sample_token": (C.c_int, [_P, _I32, _I32, _I32, _P, C.POINTER(cb_sample_rules), _P, _P, _P, _P]),
     "cb_prefetch_layer": (C.c_int, [_P, _P, _SZ, _P, _P]),
     "cb_stream_wait": (C.c_int, [_P, _P]),
@@ -695,6 +704,62 @@ def cb_rope_rows(q, k, v, pos, q_out, k_out, v_out, dims: cb_dims, spec: cb_rope
     _check("cb_rope_rows", lib().cb_rope_rows(
         C.byref(io), _buf("pos", pos, T.i32, n, dev), n, 1 if inverse else 0, C.byref(dims), C.byref(spec),
         _buf("cos_sin", cos_sin, T.f32, None, dev), max_pos, T.stream(stream, dev)))
+
+
+def shared_kv(k, v, row0, length, seq0, own_k, own_v) -> cb_shared_kv:
+    """The handle of prefixes in k, v [n_rows, Hkv hd] (group g: rows [row0[g], row0[g] + length[g])) and
+    the own rows own_k, own_v [n_seq, capacity, Hkv hd] of the sequences (group g: [seq0[g], seq0[g + 1])).
+    The prefixes' rows or the own ones may be None."""
+    T = _torch()
+    dev = T.device()
+    n = len(row0)
+    if len(length) != n or len(seq0) != n + 1:
+        raise ValueError(f"{n} row0, {len(length)} lengths and {len(seq0)} seq0: expected n, n and n + 1")
+    if (k is None) != (v is None) or (own_k is None) != (own_v is None) or (k is None and own_k is None):
+        raise ValueError("k and v, own_k and own_v come in pairs")
+    some = k if k is not None else own_k
+    for what, t, ref in (("v", v, k), ("own_v", own_v, own_k)):
+        if t is not None and t.shape != ref.shape:
+            raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(ref.shape)}")
+    for what, t, nd in (("k", k, 2), ("own_k", own_k, 3)):
+        if t is not None and (t.dim() != nd or t.shape[-1] != some.shape[-1]):
+            raise ValueError(f"{what}: shape {tuple(t.shape)} is not rows of {some.shape[-1]} in {nd} dimensions")
+    if own_k is not None and own_k.shape[0] != seq0[-1]:
+        raise ValueError(f"own_k: {own_k.shape[0]} sequences, seq0 ends with {seq0[-1]}")
+    i32 = lambda a: (C.c_int32 * len(a))(*[int(x) for x in a])  # noqa: E731
+    host = i32(row0), i32(length), i32(seq0)
+    dt = some.dtype
+    c = cb_shared_kv(_buf("k", k, dt, None, dev), _buf("v", v, dt, None, dev), 0 if k is None else k.shape[0], *host, n, int(seq0[-1]),
+                     _buf("own_k", own_k, dt, None, dev), _buf("own_v", own_v, dt, None, dev), 0 if own_k is None else own_k.shape[1])
+    c.width, c.dtype, c.dev, c.tensors, c.host = some.shape[-1], dt, dev, (k, v, own_k, own_v), host
+    return c
+
+
+def _shared(kv: cb_shared_kv, dims: cb_dims, T: _Torch):
+    if kv.width != dims.n_kv_heads * dims.head_dim:
+        raise ValueError(f"rows of {kv.width}, dims of {dims.n_kv_heads} heads of {dims.head_dim}")
+    if kv.dtype is not T.row[dims.dtype]:
+        raise ValueError(f"rows of {kv.dtype}, dims of {T.row[dims.dtype]}")
+    return C.byref(kv)
+
+
+def cb_shared_workspace_bytes(kv: cb_shared_kv, dims: cb_dims, n_q: int) -> int:
+    out = _SZ(0)
+    _check("cb_shared_workspace_bytes",
+           lib().cb_shared_workspace_bytes(_shared(kv, dims, _torch()), C.byref(dims), n_q, C.byref(out)))
+    return int(out.value)
+
+
+def cb_shared_attention(q, last, n_q: int, kv: cb_shared_kv, dims: cb_dims, out, ws, stream=None):
+    T = _torch()
+    dev, dt, ns = T.device(), T.row[dims.dtype], kv.n_seq
+    if kv.dev != dev:
+        raise ValueError(f"shared_kv: on cuda:{kv.dev}, not on the current CUDA device")
+    n = ns * n_q * dims.n_heads * dims.head_dim
+    w, wn = _ws(ws, dev)
+    _check("cb_shared_attention", lib().cb_shared_attention(
+        _buf("q", q, dt, n, dev), _buf("last", last, T.i32, ns * n_q, dev), n_q, _shared(kv, dims, T), C.byref(dims),
+        _buf("out", out, dt, n, dev), w, wn, T.stream(stream, dev)))
 
 
 def sample_rules(temperature=None, top_k=None, top_p=None, min_p=None) -> cb_sample_rules:

@@ -14,6 +14,7 @@
 
 #include "../../include/cacheblend.h"
 #include "cb_internal.h"
+#include "cb_shared.cuh"
 
 namespace cb {
 uint32_t take_error_gemm_tc();
@@ -48,6 +49,8 @@ cudaError_t launch_rope_table_scaled(float* tab, int max_pos, int rot, const dou
                                      cudaStream_t s);
 cudaError_t launch_rope_rows(int dt, const cb_rope_rows_io& io, const int32_t* pos, int n, int H, int Hkv, int hd, int rot,
                              bool half, bool vec, const float* tab, int max_pos, bool inverse, cudaStream_t s);
+size_t shared_simt_ws_bytes(const Shared& p);
+cudaError_t launch_shared_simt(int dt, const Shared& p, void* ws, cudaStream_t s);
 cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, const float* u, const cb_sample_rules& r,
                           int32_t* token, float* logprob, int32_t* kept, cudaStream_t s);
 }  // namespace cb
@@ -532,7 +535,7 @@ int cb_sync(void* stream, double timeout_s) {
   }
   const uint32_t bits = take_error_mem() | take_error_gemm() | take_error_gemm_tc() | take_error_attn() |
                         take_error_attn_tc() | take_error_kv8() | take_error_kv8_attn() | take_error_kv8_tc() |
-                        take_error_logits() | take_error_rope() | take_error_sample();
+                        take_error_logits() | take_error_rope() | take_error_shared() | take_error_sample();
   if (bits & ERRBIT_NONFINITE)
     return fail(CB_ERR_NONFINITE, "a deviation score, cache row, weight or logit was NaN/Inf (or out of its range)");
   if (bits & ERRBIT_INDEX) return fail(CB_ERR_DEVICE, "a kernel met an out-of-range index");
@@ -1544,6 +1547,98 @@ int cb_rope_rows(const cb_rope_rows_io* io, const int32_t* pos, int32_t n, int32
   CB_LAUNCH(CB_PROF_ROPE_ROWS, 0, n, (int64_t)w, rot, 3.0 * n * rot * ((a.q ? H : 0) + (a.k ? Hkv : 0)), 2.0 * e * n * w,
             S(stream), launch_rope_rows(dims->dtype, a, pos, n, H, Hkv, hd, rot, half, vec, cos_sin, max_pos, inverse != 0,
                                         S(stream)));
+  return CB_OK;
+}
+
+// ---- attention over a shared prefix -----------------------------------------------------------
+namespace {
+
+// what the call is made of, checked but for the tensors of this call
+int make_shared(const cb_shared_kv* kv, const cb_dims* d, int n_q, Shared* p) {
+  if (!kv) return fail(CB_ERR_INVALID_ARG, "shared_kv is NULL");
+  if (n_q < 0) return fail(CB_ERR_SHAPE, "n_q < 0");
+  if (kv->n_groups < 1 || kv->n_groups > kMaxGroups) return fail(CB_ERR_SHAPE, "n_groups %d outside [1, 64]", kv->n_groups);
+  if (kv->n_seq < 1 || kv->n_seq > 65535) return fail(CB_ERR_SHAPE, "n_seq %d outside [1, 65535]", kv->n_seq);
+  if (!kv->row0_host || !kv->len_host || !kv->seq0_host) return fail(CB_ERR_INVALID_ARG, "shared_kv: array is NULL");
+  if (kv->n_rows < 0 || kv->n_rows > INT32_MAX) return fail(CB_ERR_SHAPE, "shared_kv: n_rows");
+  if (kv->capacity < 0 || kv->capacity * kv->n_seq > INT32_MAX || kv->capacity > INT32_MAX)
+    return fail(CB_ERR_SHAPE, "shared_kv: capacity %lld of %d sequences", (long long)kv->capacity, kv->n_seq);
+  if (kv->seq0_host[0] != 0 || kv->seq0_host[kv->n_groups] != kv->n_seq)
+    return fail(CB_ERR_SHAPE, "shared_kv: seq0 does not run from 0 to n_seq");
+  p->n_groups = kv->n_groups;
+  int64_t held = 0;
+  for (int g = 0; g < kv->n_groups; ++g) {
+    if (kv->seq0_host[g + 1] < kv->seq0_host[g]) return fail(CB_ERR_SHAPE, "shared_kv: seq0 descends");
+    const int64_t a = kv->row0_host[g], n = kv->len_host[g];
+    if (a < 0 || n < 0 || a + n > kv->n_rows) return fail(CB_ERR_SHAPE, "shared_kv: prefix %d outside its rows", g);
+    p->row0[g] = (int32_t)a;
+    p->len[g] = (int32_t)n;
+    p->seq0[g] = kv->seq0_host[g];
+    held = std::max(held, n);
+  }
+  p->seq0[kv->n_groups] = kv->n_seq;
+  if (held > 0 && (!kv->k || !kv->v)) return fail(CB_ERR_INVALID_ARG, "shared_kv: k or v is NULL");
+  if (kv->capacity > 0 && (!kv->own_k || !kv->own_v)) return fail(CB_ERR_INVALID_ARG, "shared_kv: own_k or own_v is NULL");
+  if (int st = check_al16({kv->k, kv->v, kv->own_k, kv->own_v}, "shared_kv")) return st;
+  p->k = kv->k;
+  p->v = kv->v;
+  p->own_k = kv->own_k;
+  p->own_v = kv->own_v;
+  p->capacity = kv->capacity;
+  p->n_seq = kv->n_seq;
+  p->n_q = n_q;
+  p->H = d->n_heads;
+  p->Hkv = d->n_kv_heads;
+  p->G = d->n_heads / d->n_kv_heads;
+  p->hd = d->head_dim;
+  p->scale_log2 = 1.4426950408889634f / sqrtf((float)d->head_dim);
+  // rows per KV head are counted in 32 bits
+  if ((double)kv->n_seq * n_q * p->G > (double)(1 << 30)) return fail(CB_ERR_UNSUPPORTED, "shared_attention: more than 2^30 query rows per KV head");
+  return CB_OK;
+}
+
+int shared_ws(const Shared& p, int dtype, size_t* need) {
+  *need = 0;
+  if (p.n_q == 0) return CB_OK;
+  *need = shared_simt_ws_bytes(p);
+  if (!*need) return fail(CB_ERR_UNSUPPORTED, "shared_attention: rows, heads and keys too many for one call");
+  return CB_OK;
+}
+
+}  // namespace
+
+int cb_shared_workspace_bytes(const cb_shared_kv* kv, const cb_dims* dims, int32_t n_q, size_t* out_host) {
+  int st = check_dims(dims);
+  if (st) return st;
+  if (!out_host) return fail(CB_ERR_INVALID_ARG, "out_host is NULL");
+  Shared p;
+  if ((st = make_shared(kv, dims, n_q, &p))) return st;
+  return shared_ws(p, dims->dtype, out_host);
+}
+
+int cb_shared_attention(const void* q, const int32_t* last, int32_t n_q, const cb_shared_kv* kv, const cb_dims* dims,
+                        void* out, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_dims(dims);
+  if (st) return st;
+  Shared p;
+  if ((st = make_shared(kv, dims, n_q, &p))) return st;
+  if (n_q == 0) return CB_OK;
+  if (!q || !last || !out) return fail(CB_ERR_INVALID_ARG, "shared_attention pointer is NULL");
+  if ((st = check_al16({q, out, ws}, "shared_attention"))) return st;
+  if (reinterpret_cast<uintptr_t>(last) & 3) return fail(CB_ERR_INVALID_ARG, "shared_attention: last not 4-byte aligned");
+  size_t need;
+  if ((st = shared_ws(p, dims->dtype, &need))) return st;
+  if (need && (!ws || ws_bytes < need)) return fail(CB_ERR_WORKSPACE, "workspace %zu < %zu", ws_bytes, need);
+  const size_t e = esize(dims->dtype), rows = (size_t)p.n_seq * n_q, bytes = rows * p.H * p.hd * e,
+               W = (size_t)p.Hkv * p.hd * e, pre = (size_t)kv->n_rows * W, own = (size_t)p.n_seq * p.capacity * W;
+  if (writes_meet({{out, bytes}, {ws, need}}, {{q, bytes}, {last, rows * 4}, {p.k, pre}, {p.v, pre}, {p.own_k, own}, {p.own_v, own}}))
+    return fail(CB_ERR_INVALID_ARG, "shared_attention: out or the workspace overlaps another argument");
+  p.q = q;
+  p.last = last;
+  p.out = out;
+  CB_LAUNCH(CB_PROF_SHARED, 0, (int64_t)rows, kv->n_rows, p.H, 0.0, 0.0, S(stream),
+            launch_shared_simt(dims->dtype, p, ws, S(stream)));
+  g_launches.fetch_add(1, std::memory_order_relaxed);    // the join
   return CB_OK;
 }
 

@@ -197,6 +197,7 @@ uint32_t take_error_kv8_tc();
 uint32_t take_error_logits();
 uint32_t take_error_rope();
 uint32_t take_error_sample();
+uint32_t take_error_shared();
 void reset_kv8_attn_caches();
 void reset_kv8_tc_caches();
 void reset_logits_caches();
