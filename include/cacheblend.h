@@ -781,8 +781,8 @@ int cb_stream_wait(void* stream, void* event);
 #define CB_PROF_KV8_EVICT  15   /* aux: 0 selection, 1 move                                */
 #define CB_PROF_LOGITS     16
 #define CB_PROF_ROPE_ROWS  17
-#define CB_PROF_SHARED     18   /* shared-prefix attention; aux: 0 prefixes, 1 own rows, 2 the
-                                 * join of both                                            */
+#define CB_PROF_SHARED     18   /* shared-prefix attention, its two or three launches as one
+                                 * record; aux: 1 on the tensor cores                      */
 #define CB_PROF_SAMPLE     19
 
 typedef struct {

@@ -49,8 +49,6 @@ cudaError_t launch_rope_table_scaled(float* tab, int max_pos, int rot, const dou
                                      cudaStream_t s);
 cudaError_t launch_rope_rows(int dt, const cb_rope_rows_io& io, const int32_t* pos, int n, int H, int Hkv, int hd, int rot,
                              bool half, bool vec, const float* tab, int max_pos, bool inverse, cudaStream_t s);
-size_t shared_simt_ws_bytes(const Shared& p);
-cudaError_t launch_shared_simt(int dt, const Shared& p, void* ws, cudaStream_t s);
 cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, const float* u, const cb_sample_rules& r,
                           int32_t* token, float* logprob, int32_t* kept, cudaStream_t s);
 }  // namespace cb
@@ -535,7 +533,7 @@ int cb_sync(void* stream, double timeout_s) {
   }
   const uint32_t bits = take_error_mem() | take_error_gemm() | take_error_gemm_tc() | take_error_attn() |
                         take_error_attn_tc() | take_error_kv8() | take_error_kv8_attn() | take_error_kv8_tc() |
-                        take_error_logits() | take_error_rope() | take_error_shared() | take_error_sample();
+                        take_error_logits() | take_error_rope() | take_error_shared() | take_error_shared_tc() | take_error_sample();
   if (bits & ERRBIT_NONFINITE)
     return fail(CB_ERR_NONFINITE, "a deviation score, cache row, weight or logit was NaN/Inf (or out of its range)");
   if (bits & ERRBIT_INDEX) return fail(CB_ERR_DEVICE, "a kernel met an out-of-range index");
@@ -1585,6 +1583,7 @@ int make_shared(const cb_shared_kv* kv, const cb_dims* d, int n_q, Shared* p) {
   p->own_k = kv->own_k;
   p->own_v = kv->own_v;
   p->capacity = kv->capacity;
+  p->n_rows = kv->n_rows;
   p->n_seq = kv->n_seq;
   p->n_q = n_q;
   p->H = d->n_heads;
@@ -1600,7 +1599,7 @@ int make_shared(const cb_shared_kv* kv, const cb_dims* d, int n_q, Shared* p) {
 int shared_ws(const Shared& p, int dtype, size_t* need) {
   *need = 0;
   if (p.n_q == 0) return CB_OK;
-  *need = shared_simt_ws_bytes(p);
+  *need = shared_tc_taken(dtype, p) ? shared_tc_ws_bytes(p) : shared_simt_ws_bytes(p);
   if (!*need) return fail(CB_ERR_UNSUPPORTED, "shared_attention: rows, heads and keys too many for one call");
   return CB_OK;
 }
@@ -1636,9 +1635,10 @@ int cb_shared_attention(const void* q, const int32_t* last, int32_t n_q, const c
   p.q = q;
   p.last = last;
   p.out = out;
-  CB_LAUNCH(CB_PROF_SHARED, 0, (int64_t)rows, kv->n_rows, p.H, 0.0, 0.0, S(stream),
-            launch_shared_simt(dims->dtype, p, ws, S(stream)));
-  g_launches.fetch_add(1, std::memory_order_relaxed);    // the join
+  const bool tc = shared_tc_taken(dims->dtype, p);
+  CB_LAUNCH(CB_PROF_SHARED, tc ? 1 : 0, (int64_t)rows, kv->n_rows, p.H, 0.0, 0.0, S(stream),
+            tc ? launch_shared_tc(p, ws, S(stream)) : launch_shared_simt(dims->dtype, p, ws, S(stream)));
+  g_launches.fetch_add(tc ? shared_tc_launches(p) - 1 : 1, std::memory_order_relaxed);    // the others of the call
   return CB_OK;
 }
 
@@ -1697,6 +1697,7 @@ void cb_shutdown(void) {
   reset_kv8_attn_caches();
   reset_kv8_tc_caches();
   reset_logits_caches();
+  reset_shared_tc_caches();
   ProfState& P = g_prof;
   bool failed = false;
   for (cudaEvent_t e : P.ev) failed = cudaEventDestroy(e) != cudaSuccess || failed;

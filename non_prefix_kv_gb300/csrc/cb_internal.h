@@ -198,8 +198,10 @@ uint32_t take_error_logits();
 uint32_t take_error_rope();
 uint32_t take_error_sample();
 uint32_t take_error_shared();
+uint32_t take_error_shared_tc();
 void reset_kv8_attn_caches();
 void reset_kv8_tc_caches();
 void reset_logits_caches();
+void reset_shared_tc_caches();
 
 }  // namespace cb

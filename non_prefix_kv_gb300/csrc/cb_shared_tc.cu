@@ -1,0 +1,930 @@
+// Attention of a batch over a shared prefix on the tensor cores (bf16, head_dim 64 or 128); the mathematics
+// is cb_shared.cu's: pieces with a running softmax, joined at the end.  Three kernels:
+//
+//   k_shared_prefix  the prefixes.  All rows (query, head) of a group's batch that share a KV head are rows of
+//                    one matrix: S = Q K^T and O = P V by tcgen05.mma over 128-row and 128-key tiles, so that
+//                    a prefix is read once per 128 rows.
+//   k_shared_own     each sequence's own rows: few rows, few keys, bound by the caches' bytes.
+//   k_shared_join    joins a row's pieces.
+//
+// Both of the first cut their work as one line of equal steps (key tiles of a (KV head, row tile); 16 keys of
+// a (sequence, head)) into equal runs, one per worker, wherever a tile's end falls: with whole tiles per CTA a
+// 4096-row prefix of 32 heads leaves a third of the 152 SMs idle.  A worker leaves one piece for every tile
+// that its run touches, in slot worker + tile (along the line one of the two goes up at every new pair).
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "cb_shared.cuh"
+#include "cb_tc.cuh"
+
+namespace cb {
+
+static __device__ uint32_t g_err_shared_tc;
+static std::atomic<bool> g_used_shared_tc{false};   // a kernel of this file was launched (or captured)
+
+uint32_t take_error_shared_tc() { return g_used_shared_tc ? take_word(g_err_shared_tc) : 0u; }
+
+namespace {
+
+using tc::f2_add;
+using tc::f2_fma;
+using tc::f2_pack;
+using tc::f2_unpack;
+using tc::fmax3;
+
+constexpr int BM = 128;              // rows of a tile
+constexpr int BN = 128;              // keys of a tile
+constexpr int SLAB = 128 * 128;      // bytes of one [128 rows x 64 elements] swizzled slab
+constexpr int THREADS = 256;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_O = 2 * BN;    // TMEM: S_0 | S_1 | O_0 | O_1
+constexpr float kLazy = 8.0f;        // weights up to 2^8 before a row's maximum is raised
+constexpr int kWorkers = 152;        // of the prefix kernel, one CTA per SM
+constexpr int kOwnWarps = 4, kOwnThreads = 32 * kOwnWarps, kOwnCtas = 304;   // of the own rows' kernel
+constexpr int TILE = 8;              // rows of its tiles
+
+struct Tc {
+  Shared s;
+  int total, workers;            // key tiles of all prefixes, CTAs that share them
+  int first[kMaxGroups + 1];     // key tiles before group g
+  int prob[kMaxGroups + 1];      // (KV head, row tile) pairs before group g
+  int qpt;                       // queries of a row tile: 128 / G
+  int slot_rows;                 // rows that a slot holds
+  float* part;                   // [workers + pairs][slot_rows][hd], then m and l: see slot()
+  // own rows
+  int row_tiles;                 // of a sequence
+  int own_slot_rows;
+  bool alone;                    // no prefix kernel runs before
+  int32_t* plan;                 // [n_seq row_tiles + 1] steps before each, times Hkv
+  float* own_part;               // [workers + n_seq row_tiles Hkv][rows][hd], m, l
+};
+
+__device__ __forceinline__ int row_tiles_of(const Tc& w, int g) {
+  return ((w.s.seq0[g + 1] - w.s.seq0[g]) * w.s.n_q + w.qpt - 1) / w.qpt;
+}
+__device__ __forceinline__ float* slot(float* part, int rows, int hd, int worker, int pair) {
+  return part + ((int64_t)worker + pair) * (rows * (hd + 2));
+}
+
+// A run's part inside one (group, KV head, row tile).
+struct Seg {
+  int g, h, rt, pair;
+  int tile, n;                   // its first key tile, and how many there are
+  int end;                       // where it ends on the line
+};
+__device__ __forceinline__ Seg segment(const Tc& w, int i, int b) {
+  Seg x;
+  x.g = 0;
+  while (i >= w.first[x.g + 1]) ++x.g;
+  const int kt = (w.s.len[x.g] + BN - 1) / BN, rts = row_tiles_of(w, x.g), at = i - w.first[x.g], pl = at / kt;
+  x.tile = at - pl * kt;
+  x.h = pl / rts;
+  x.rt = pl - x.h * rts;
+  x.pair = w.prob[x.g] + pl;
+  x.end = min(b, i + kt - x.tile);
+  x.n = x.end - i;
+  return x;
+}
+
+template <int HD>
+struct Layout {
+  static constexpr int T_BYTES = HD / 64 * SLAB;             // a tile of Q, K or V
+  static constexpr int OFF_Q = 0;                            // [2], by turns
+  static constexpr int OFF_K = 2 * T_BYTES;                  // [2 groups]
+  static constexpr int OFF_V = OFF_K + 2 * T_BYTES;          // [2]
+  static constexpr int OFF_X = OFF_V + 2 * T_BYTES;          // [2 groups][BM] row max, row sum
+  static constexpr int OFF_BAR = OFF_X + 4 * BM * 4;
+  static constexpr int SMEM = OFF_BAR + 128 + 1024 > tc::kWholeSm ? OFF_BAR + 128 + 1024 : tc::kWholeSm;
+  static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
+};
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Two groups of four warps take a segment's key tiles by turns; each is a closed loop, its first warp issuing
+// the copies and products between its share of the softmax: S -> softmax -> P V -> S of the group's next tile,
+// with one thread per row of the tile and its 128 scores in registers.  K's buffer is refilled as soon as S is
+// there, V's once P V is done, with the next segment's first tile where a segment ends; Q alternates between two
+// buffers.  Warps whose 32 rows do not exist (few queries) leave the softmax to the others.
+template <int HD>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_shared_prefix(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Tc w) {
+  pdl_wait();
+  pdl_trigger();                   // (before TMEM is allocated: see tc::kWholeSm)
+  using L = Layout<HD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  float* xm = reinterpret_cast<float*>(base + L::OFF_X);     // [2][BM] row max, then [2][BM] row sum
+  float* xl = xm + 2 * BM;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
+  uint64_t* q_full = bars + 8;                               // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+  uint64_t* k_full = bars + 4 * grp;       // a group's barriers: K and V have landed, S and P V are done
+  uint64_t* v_full = k_full + 1;
+  uint64_t* s_full = k_full + 2;
+  uint64_t* pv_done = k_full + 3;
+  const Shared& p = w.s;
+  const int a = run_start(w.total, blockIdx.x, w.workers), b = run_start(w.total, blockIdx.x + 1, w.workers);
+
+  if (tid == 0) {
+    for (int i = 0; i < 10; ++i) tc::mbar_init(&bars[i], 1);
+    tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&tmQ);
+    tc::tma_prefetch_desc(&tmK);
+    tc::tma_prefetch_desc(&tmV);
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(tmem_slot, TMEM_COLS);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+  const uint32_t tS = trow + grp * BN, tO = trow + TM_O + grp * HD;
+  const bool issuer = quad == 0;
+  uint8_t* sK = base + L::OFF_K + grp * L::T_BYTES;
+  uint8_t* sV = base + L::OFF_V + grp * L::T_BYTES;
+  bool ok = true;                  // of this warp; one that gave up goes on meeting the others
+  int nk_loads = 0, nv_loads = 0, nq_loads = 0;
+
+  auto load_q = [&](const Seg& x, int turn) {          // by thread 0
+    ++nq_loads;
+    tc::mbar_expect_tx(&q_full[turn], HD * 2 * p.G * w.qpt);
+    for (int s = 0; s < HD / 64; ++s)
+      tma_load_3d(base + L::OFF_Q + turn * L::T_BYTES + s * SLAB, &tmQ, &q_full[turn], 64 * s, x.h * p.G,
+                  p.seq0[x.g] * p.n_q + x.rt * w.qpt);
+  };
+  auto load_kv = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, const Seg& x, int tile) {   // by lane 0
+    tc::mbar_expect_tx(bar, L::T_BYTES);
+    for (int s = 0; s < HD / 64; ++s)
+      tc::tma_load_2d(dst + s * SLAB, map, bar, x.h * HD + 64 * s, p.row0[x.g] + tile * BN);
+  };
+  auto load_k = [&](const Seg& x, int tile) {
+    ++nk_loads;
+    if (lane == 0) load_kv(&tmK, sK, k_full, x, tile);
+  };
+  auto load_v = [&](const Seg& x, int tile) {
+    ++nv_loads;
+    if (lane == 0) load_kv(&tmV, sV, v_full, x, tile);
+  };
+  auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); };
+  auto issue_s = [&](int turn) {
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(BM, BN);
+    const uint64_t qd = tc::desc_sw128(tc::smem_u32(base + L::OFF_Q + turn * L::T_BYTES)), kd = tc::desc_sw128(tc::smem_u32(sK));
+    tc::tc_fence_after();
+    if (tc::elect_one()) {
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+        tc::mma_bf16(tmem + grp * BN, qd + off, kd + off, idesc, k > 0);
+      }
+      tc::mma_commit(s_full);
+    }
+    __syncwarp();
+  };
+  auto issue_pv = [&](bool add) {
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(BM, HD, true);
+    const uint64_t vd = tc::desc_sw128_mn(tc::smem_u32(sV), SLAB);
+    tc::tc_fence_after();
+    if (tc::elect_one()) {
+#pragma unroll
+      for (int k = 0; k < BN / 16; ++k)
+        tc::mma_bf16_ts(tmem + TM_O + grp * HD, tmem + grp * BN + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc,
+                        (add || k > 0) ? 1u : 0u);
+      tc::mma_commit(pv_done);
+    }
+    __syncwarp();
+  };
+
+  // ---- the run's segments
+  Seg cur = segment(w, a, b), nxt = cur;
+  nxt.n = 0;
+  if (cur.end < b) nxt = segment(w, cur.end, b);
+  if (tid == 0) {
+    load_q(cur, 0);
+    if (nxt.n) load_q(nxt, 1);
+  }
+  if (issuer && grp < cur.n) {
+    load_k(cur, cur.tile + grp);
+    load_v(cur, cur.tile + grp);
+    ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[0], 0) && tc::mbar_wait(k_full, 0));
+    if (ok) issue_s(0);
+  }
+  int u = 0;                       // the group's tiles so far: the phase of its barriers
+  for (int nseg = 0;; ++nseg) {
+    const int turn = nseg & 1;     // Q's buffer
+    const int rows = min(w.qpt, (p.seq0[cur.g + 1] - p.seq0[cur.g]) * p.n_q - cur.rt * w.qpt) * p.G;
+    const bool work = quad * 32 < rows;
+    const int len = p.len[cur.g];
+    float m_used = -INFINITY, l = 0.f;
+    for (int t = grp; t < cur.n; t += 2, ++u) {
+      const int tile = cur.tile + t, keys = min(BN, len - tile * BN);
+      const bool more = t + 2 < cur.n;
+      if (work) ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
+      if (issuer && ok) {
+        if (more)
+          load_k(cur, tile + 2);
+        else if (grp < nxt.n)
+          load_k(nxt, nxt.tile + grp);
+      }
+      if (work && ok) {
+        uint32_t sr[BN];
+        tc::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
+        tc::tmem_wait_ld64(sr);
+        tc::tmem_wait_ld64(sr + 64);
+        if (keys < BN) {
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c >= keys) sr[c] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < BN; c += 8) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mx[q] = fmax3(mx[q], __uint_as_float(sr[c + 2 * q]), __uint_as_float(sr[c + 2 * q + 1]));
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if (t == grp) {
+          m_used = mt;             // O_g is written, not added to, by this tile's P V
+        } else {
+          const bool need = mt > m_used + kLazy;
+          if (__any_sync(0xffffffffu, need)) {               // (S was issued after the last P V had completed)
+            const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              float o[16];
+              tc::tmem_ld16(tO + c * 16, o);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o[q] *= alpha;
+              tc::tmem_st16(tO + c * 16, o);
+            }
+            l *= alpha;
+            if (need) m_used = mt;
+          }
+        }
+        const float off = m_used == -INFINITY ? 0.f : -m_used;
+        const uint64_t f2 = f2_pack(p.scale_log2, p.scale_log2), o2 = f2_pack(off, off);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const int k0 = c * 32 + 2 * q;
+            const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, o2));
+            const float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
+            sum[q & 1] = f2_add(sum[q & 1], f2_pack(p0, p1));
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+            pk[q] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+          tc::tmem_st16u_nowait(tS + c * 16, pk);
+        }
+        const float2 sm = f2_unpack(f2_add(sum[0], sum[1]));
+        l += sm.x + sm.y;
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+      }
+      group_sync();
+      if (issuer) {
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(v_full, u & 1));
+        if (ok && keys < BN) {
+          // what the copy brought from behind the prefix may be no number: times a weight of 0 it would stay none
+          for (int c = lane; c < (BN - keys) * 8; c += 32)
+#pragma unroll
+            for (int s = 0; s < HD / 64; ++s)
+              *reinterpret_cast<uint4*>(sV + s * SLAB + keys * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (ok) issue_pv(t != grp);
+        if (more) {
+          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(k_full, (u + 1) & 1) && tc::mbar_wait(pv_done, u & 1));
+          if (ok) {
+            issue_s(turn);
+            load_v(cur, tile + 2);
+          }
+        } else if (grp < nxt.n) {
+          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(pv_done, u & 1));
+          if (ok) load_v(nxt, nxt.tile + grp);
+        }
+      }
+    }
+    const bool had = grp < cur.n;
+    if (!had && issuer && ok && grp < nxt.n) {
+      load_k(nxt, nxt.tile + grp);
+      load_v(nxt, nxt.tile + grp);
+    }
+    // ---- the segment's piece: both groups' row statistics meet in shared memory
+    ok = ok && (!had || __all_sync(0xffffffffu, tc::mbar_wait(pv_done, (u - 1) & 1)));
+    xm[grp * BM + r] = m_used;
+    xl[grp * BM + r] = l;
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    Seg nn = nxt;                  // (Q's buffer is free: both groups' S of this segment are done)
+    nn.n = 0;
+    if (nxt.n && nxt.end < b) {
+      nn = segment(w, nxt.end, b);
+      if (tid == 0) load_q(nn, turn);
+    }
+    if (issuer && grp < nxt.n) {
+      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&q_full[turn ^ 1], ((nseg + 1) >> 1) & 1) && tc::mbar_wait(k_full, u & 1));
+      if (ok) issue_s(turn ^ 1);
+    }
+    if (ok && work) {              // (uniform over the warp: the loads from TMEM are the whole warp's)
+      const float ma = xm[r], mb = xm[BM + r], mm = fmaxf(ma, mb);
+      const float a0 = ma == -INFINITY ? 0.f : tc::ex2_approx(ma - mm);
+      const float a1 = mb == -INFINITY ? 0.f : tc::ex2_approx(mb - mm);
+      // (a sum that is no number counts even though no maximum was found beside it)
+      const float lt = (ma == -INFINITY ? xl[r] : xl[r] * a0) + (mb == -INFINITY ? xl[BM + r] : xl[BM + r] * a1);
+      float* out = slot(w.part, w.slot_rows, HD, blockIdx.x, cur.pair);
+      if (grp == 0 && r < rows) {
+        out[w.slot_rows * HD + r] = isnan(lt) ? lt : mm;
+        out[w.slot_rows * (HD + 1) + r] = lt;
+      }
+      out += (int64_t)r * HD + grp * (HD / 2);
+#pragma unroll 1
+      for (int c = 0; c < HD / 32; ++c) {
+        const uint32_t col = TM_O + grp * (HD / 2) + c * 16;
+        float o0[16], o1[16];
+        tc::tmem_ld16(trow + col, o0);
+        if (cur.n > 1) {           // (else O_1 was never written)
+          tc::tmem_ld16(trow + col + HD, o1);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) o1[q] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) o0[q] = o0[q] * a0 + o1[q] * a1;
+        if (r < rows) {
+          st8(out + c * 16, o0);
+          st8(out + c * 16 + 8, o0 + 8);
+        }
+      }
+    }
+    tc::tc_fence_before();
+    __syncthreads();               // O and the statistics are free
+    tc::tc_fence_after();
+    if (!nxt.n) break;             // (uniform)
+    cur = nxt;
+    nxt = nn;
+  }
+  if (!ok) {
+    // report, and give the copies in flight as long again before the memory is given up
+    if (lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_TIMEOUT);
+    if (nk_loads > 0) tc::mbar_wait(k_full, (nk_loads - 1) & 1);
+    if (nv_loads > 0) tc::mbar_wait(v_full, (nv_loads - 1) & 1);
+    if (tid == 0)
+      for (int i = max(0, nq_loads - 2); i < nq_loads; ++i) tc::mbar_wait(&q_full[i & 1], (i >> 1) & 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    __syncwarp();
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// ---- own rows ---------------------------------------------------------------------------------
+// A step is 16 KW keys of one (sequence, KV head): 8 KB of K and V, by TMA into the warp's own stages, three in
+// flight.  The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, with the keys (then the channels)
+// as the 16 rows of mma.m16n8k16 and up to 8 query rows as its columns: a token's few rows fill the
+// instruction.  Every warp is a worker with an equal run of the line of steps and meets no other.
+template <int HD>
+struct Own {
+  static constexpr int KW = 128 / HD, KT = 16 * KW;
+  static constexpr int HALF = KT * HD * 2;                   // bytes of K (or V) of a step
+  static constexpr int NST = 3;
+  static constexpr int OFF_BAR = kOwnWarps * NST * 2 * HALF;
+  static constexpr int SMEM = OFF_BAR + kOwnWarps * NST * 8 + kOwnThreads * 4 + 1024;
+};
+
+__device__ __forceinline__ void mma_bf16_16x8(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t* a, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t* a, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(addr)
+               : "memory");
+}
+// 8 x 8 transposition of 16-bit pairs across the warp
+__device__ __forceinline__ uint32_t transpose_pairs(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// how many workers share the line: a run has two steps at least
+__device__ __forceinline__ int own_workers(int total, int workers) { return max(1, min(workers, total / 2)); }
+
+template <int HD>
+__global__ void __launch_bounds__(kOwnThreads, 2)
+    k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Tc w) {
+  // Nothing here needs the prefix kernel's results, only that everything before it is done, which that
+  // kernel has seen before it let this one start; the wait at the end makes this one end after it.
+  if (w.alone) pdl_wait();
+  pdl_trigger();
+  using L = Own<HD>;
+  constexpr int KS = HD / 16, SLABS = HD / 64, SL = L::KT * 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  const Shared& p = w.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* stages = base + warp * L::NST * 2 * L::HALF;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR) + warp * L::NST;
+  int* before = reinterpret_cast<int*>(base + L::OFF_BAR + kOwnWarps * L::NST * 8);
+  const int R = p.n_q * p.G, entries = p.n_seq * w.row_tiles;
+  if (lane == 0) {
+    for (int i = 0; i < L::NST; ++i) tc::mbar_init(&full[i], 1);
+    tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&tmK);
+    tc::tma_prefetch_desc(&tmV);
+  }
+  // ---- where this worker's run lies: thread i sums the steps of a share of the entries (sequence, row tile),
+  // a scan places them; the first CTA writes the plan for the join
+  auto row_last = [&](int e, int r) -> int {             // -1: no own row
+    const int s = e / w.row_tiles, row = (e - s * w.row_tiles) * TILE + r;
+    return r >= TILE || row >= R ? -1 : max(-1, shared_last(p, (int64_t)s * p.n_q + row / p.G));
+  };
+  auto steps_of = [&](int e) -> int {
+    const int s = e / w.row_tiles, row0 = (e - s * w.row_tiles) * TILE;
+    int mx = -1;
+    for (int j = row0 / p.G; j <= (min(R, row0 + TILE) - 1) / p.G; ++j) mx = max(mx, shared_last(p, (int64_t)s * p.n_q + j));
+    return (mx + L::KT) / L::KT;
+  };
+  const int share = (entries + kOwnThreads - 1) / kOwnThreads, e0 = min(entries, tid * share), e1 = min(entries, e0 + share);
+  int mine = 0;
+  for (int e = e0; e < e1; ++e) mine += steps_of(e) * p.Hkv;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __shared__ int wsum[kOwnWarps];
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int x = 0; x < kOwnWarps; ++x) {
+    if (x < warp) incl += wsum[x];
+    total += wsum[x];
+  }
+  before[tid] = incl - mine;
+  if (blockIdx.x == 0) {
+    int at = incl - mine;
+    for (int e = e0; e < e1; ++e) {
+      w.plan[e] = at;
+      at += steps_of(e) * p.Hkv;
+    }
+    if (tid == 0) w.plan[entries] = total;
+  }
+  __syncthreads();
+  const int n_work = own_workers(total, gridDim.x * kOwnWarps), worker = warp * gridDim.x + blockIdx.x;
+  const int a = worker < n_work ? run_start(total, worker, n_work) : 0, b = worker < n_work ? run_start(total, worker + 1, n_work) : 0;
+  if (a < b) {
+    auto warp_steps = [&](int e) -> int {
+      return (__reduce_max_sync(0xffffffffu, row_last(e, lane)) + L::KT) / L::KT;
+    };
+    struct Pos {
+      int e, h, k, n;       // entry, head, step of the unit, steps in a unit of the entry
+    };
+    auto advance = [&](Pos& x) {
+      if (++x.k < x.n) return;
+      x.k = 0;
+      if (++x.h < p.Hkv) return;
+      x.h = 0;
+      ++x.e;
+      while (x.e < entries && (x.n = warp_steps(x.e)) == 0) ++x.e;
+    };
+    Pos cur;
+    {
+      // the last thread whose share starts at or before the run
+      int c = 0;
+      for (int i = lane; i < kOwnThreads; i += 32)
+        if (before[i] <= a && i * share < entries) c = i;
+      c = __reduce_max_sync(0xffffffffu, c);
+      cur.e = c * share;
+      int left = a - before[c];
+      for (;; ++cur.e) {
+        cur.n = warp_steps(cur.e);
+        if (left < cur.n * p.Hkv) break;
+        left -= cur.n * p.Hkv;
+      }
+      cur.h = left / cur.n;
+      cur.k = left - cur.h * cur.n;
+    }
+    auto fill = [&](const Pos& x, int st) {
+      if (lane != 0) return;
+      const int row = (int)((int64_t)(x.e / w.row_tiles) * p.capacity) + x.k * L::KT;
+      tc::mbar_expect_tx(&full[st], 2 * L::HALF);
+#pragma unroll
+      for (int i = 0; i < SLABS; ++i) {
+        tc::tma_load_2d(stages + st * 2 * L::HALF + i * SL, &tmK, &full[st], x.h * HD + 64 * i, row);
+        tc::tma_load_2d(stages + st * 2 * L::HALF + L::HALF + i * SL, &tmV, &full[st], x.h * HD + 64 * i, row);
+      }
+    };
+    Pos pre = cur;                                 // the next step to load
+    int loaded = 0;
+    for (; loaded < L::NST && a + loaded < b; ++loaded) {
+      fill(pre, loaded);
+      if (a + loaded + 1 < b) advance(pre);
+    }
+    // a lane's row and 16-byte chunk in the matrices that ldmatrix reads: of K keys by channels, of V^T
+    // channels by keys
+    const int k_row = (lane & 7) + (lane & 8), k_chunk = lane >> 4;
+    const int v_row = (lane & 7) + ((lane >> 4) << 3), v_chunk = (lane >> 3) & 1;
+    bool ok = true;
+    int done = 0;                                  // steps of the run
+    while (ok && a + done < b) {
+      // ---------------------------------------------------------------- a unit, or a part of one
+      const int s = cur.e / w.row_tiles, row0 = (cur.e - s * w.row_tiles) * TILE, nrow = min(TILE, R - row0), h = cur.h;
+      const int e = cur.e, nk = __reduce_max_sync(0xffffffffu, row_last(e, lane)) + 1;
+      int lastr[2];
+      lastr[0] = row_last(e, 2 * t);
+      lastr[1] = row_last(e, 2 * t + 1);
+      uint32_t qb[KS][2];
+      {
+        const int row = row0 + g;
+        const bool on = g < nrow;
+        const int j = on ? row / p.G : 0;
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(
+            static_cast<const bf16*>(p.q) + (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (on ? row - j * p.G : 0)) * HD + 2 * t);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          qb[k][0] = on ? q[k * 8] : 0u;
+          qb[k][1] = on ? q[k * 8 + 4] : 0u;
+        }
+      }
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[KS][4];
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      const int n = min(cur.n - cur.k, b - a - done);
+      for (int x = 0; x < n; ++x, ++done) {
+        const int st = done % L::NST, key0 = (cur.k + x) * L::KT;
+        if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[st], (done / L::NST) & 1)))) break;
+        uint8_t* sk = stages + st * 2 * L::HALF;
+        uint8_t* sv = sk + L::HALF;
+        if (nk - key0 < L::KT) {
+          // rows behind the last one that is seen may hold anything
+          for (int c = lane; c < (L::KT - (nk - key0)) * 8; c += 32)
+#pragma unroll
+            for (int i = 0; i < SLABS; ++i)
+              *reinterpret_cast<uint4*>(sv + i * SL + (nk - key0) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+          tc::fence_proxy_async_smem();          // (before a copy into the same place)
+          __syncwarp();
+        }
+#pragma unroll
+        for (int kw = 0; kw < L::KW; ++kw) {
+          float z[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint32_t ka = tc::smem_u32(sk) + (kw * 16 + k_row) * 128;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            uint32_t f[4];
+            const int c = 2 * k + k_chunk;
+            ldmatrix4(f, ka + (c >> 3) * SL + (((c & 7) ^ (k_row & 7)) << 4));
+            mma_bf16_16x8(z, f, qb[k][0], qb[k][1]);
+          }
+          const int key = key0 + kw * 16 + g;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = key + (i >> 1) * 8 <= lastr[i & 1] ? z[i] * p.scale_log2 : -INFINITY;
+          float mx0 = fmaxf(z[0], z[2]), mx1 = fmaxf(z[1], z[3]);
+          if (__any_sync(0xffffffffu, mx0 > m[0] + kLazy || mx1 > m[1] + kLazy)) {
+#pragma unroll
+            for (int q = 4; q < 32; q <<= 1) {
+              mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, q));
+              mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, q));
+            }
+            mx0 = fmaxf(mx0, m[0]);
+            mx1 = fmaxf(mx1, m[1]);
+            const float f0 = m[0] == -INFINITY ? 0.f : tc::ex2_approx(m[0] - mx0);
+            const float f1 = m[1] == -INFINITY ? 0.f : tc::ex2_approx(m[1] - mx1);
+            if (m[0] != -INFINITY) l[0] *= f0;     // (a NaN stays)
+            if (m[1] != -INFINITY) l[1] *= f1;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              o[i][0] *= f0;
+              o[i][1] *= f1;
+              o[i][2] *= f0;
+              o[i][3] *= f1;
+            }
+            m[0] = mx0;
+            m[1] = mx1;
+          }
+          const float r0 = m[0] == -INFINITY ? 0.f : m[0], r1 = m[1] == -INFINITY ? 0.f : m[1];
+          const float p0 = tc::ex2_approx(z[0] - r0), p1 = tc::ex2_approx(z[1] - r1), p2 = tc::ex2_approx(z[2] - r0),
+                      p3 = tc::ex2_approx(z[3] - r1);
+          l[0] += p0 + p2;
+          l[1] += p1 + p3;
+          const uint32_t b0 = transpose_pairs(pack_bf16(p0, p1)), b1 = transpose_pairs(pack_bf16(p2, p3));
+          const uint32_t va = tc::smem_u32(sv) + (kw * 16 + v_row) * 128;
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            uint32_t f[4];
+            const int c = 2 * i + v_chunk;
+            ldmatrix4_trans(f, va + (c >> 3) * SL + (((c & 7) ^ (v_row & 7)) << 4));
+            mma_bf16_16x8(o[i], f, b0, b1);
+          }
+        }
+        __syncwarp();
+        if (a + loaded < b) {
+          fill(pre, loaded % L::NST);
+          ++loaded;
+          if (a + loaded < b) advance(pre);
+        }
+      }
+#pragma unroll
+      for (int q = 4; q < 32; q <<= 1) {
+        l[0] += __shfl_xor_sync(0xffffffffu, l[0], q);
+        l[1] += __shfl_xor_sync(0xffffffffu, l[1], q);
+      }
+      float* out = slot(w.own_part, w.own_slot_rows, HD, worker, e * p.Hkv + h);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = 2 * t + c;
+        if (r >= nrow || !ok) continue;
+        if (g == 0) {
+          out[w.own_slot_rows * HD + r] = isnan(l[c]) ? l[c] : m[c];
+          out[w.own_slot_rows * (HD + 1) + r] = l[c];
+        }
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          out[r * HD + i * 16 + g] = o[i][c];
+          out[r * HD + i * 16 + 8 + g] = o[i][2 + c];
+        }
+      }
+      cur.k += n - 1;
+      if (a + done < b) advance(cur);
+    }
+    if (!ok) {
+      // report, and give the copies in flight as long again
+      if (lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_TIMEOUT);
+      for (int i = max(0, loaded - L::NST); i < loaded; ++i) tc::mbar_wait(&full[i % L::NST], (i / L::NST) & 1);
+    }
+  }
+  if (!w.alone) pdl_wait();
+}
+
+// ---- join: one warp per (query, head) ------------------------------------------------------------
+template <int HD>
+__global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc w, int own_grid) {
+  const Shared& p = w.s;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  if (row >= (int64_t)p.n_seq * p.n_q * p.H) return;
+  const int64_t t = row / p.H;
+  const int hh = (int)(row - t * p.H), h = hh / p.G, gh = hh - h * p.G, s = (int)(t / p.n_q), j = (int)(t - (int64_t)s * p.n_q);
+  const int raw = p.last[t], last = shared_last(p, t);
+  if (raw != last && hh == 0 && lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_INDEX);
+  // pieces of the prefix, then the own ones: slots are one worker apart
+  int n_pre = 0, n_own = 0, r = 0, r_own = 0;
+  const float *pre = nullptr, *own = nullptr;
+  const int64_t pre_step = (int64_t)w.slot_rows * (HD + 2), own_step = (int64_t)w.own_slot_rows * (HD + 2);
+  if (last >= -1 && w.total > 0) {
+    int g = 0;
+    while (s >= p.seq0[g + 1]) ++g;
+    const int kt = (p.len[g] + BN - 1) / BN;
+    if (kt > 0) {
+      const int tl = (int)(t - (int64_t)p.seq0[g] * p.n_q), rt = tl / w.qpt, pl = h * row_tiles_of(w, g) + rt;
+      const int x0 = w.first[g] + pl * kt, w0 = worker_of(w.total, x0, w.workers);
+      n_pre = worker_of(w.total, x0 + kt - 1, w.workers) - w0 + 1;
+      pre = slot(w.part, w.slot_rows, HD, w0, w.prob[g] + pl);
+      r = (tl - rt * w.qpt) * p.G + gh;
+    }
+  }
+  if (last >= 0) {
+    const int rr = j * p.G + gh, e = s * w.row_tiles + rr / TILE, total = w.plan[p.n_seq * w.row_tiles];
+    const int at = w.plan[e], n = (w.plan[e + 1] - at) / p.Hkv, x0 = at + h * n;
+    const int workers = own_workers(total, own_grid * kOwnWarps), w0 = worker_of(total, x0, workers);
+    n_own = worker_of(total, x0 + n - 1, workers) - w0 + 1;
+    own = slot(w.own_part, w.own_slot_rows, HD, w0, e * p.Hkv + h);
+    r_own = rr % TILE;
+  }
+  const int n = n_pre + n_own;
+  auto piece = [&](int i) { return i < n_pre ? pre + i * pre_step : own + (i - n_pre) * own_step; };
+  auto stat = [&](int i, int which) {
+    return i < n_pre ? piece(i)[w.slot_rows * (HD + which) + r] : piece(i)[w.own_slot_rows * (HD + which) + r_own];
+  };
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, stat(i, 0));
+  M = warp_max(M);
+  constexpr int PER = HD / 32;
+  float L = 0.f, o[PER];
+#pragma unroll
+  for (int c = 0; c < PER; ++c) o[c] = 0.f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float f = 0.f;
+    if (i0 + lane < n) {
+      const float m = stat(i0 + lane, 0);
+      f = m == -INFINITY ? 0.f : tc::ex2_approx(m - M);      // (a NaN is no infinity)
+      L = fmaf(stat(i0 + lane, 1), f, L);
+    }
+    for (int i = 0; i < min(32, n - i0); ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+      if (fi == 0.f) continue;
+      const float* x = piece(i0 + i) + (i0 + i < n_pre ? r : r_own) * HD + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(x);
+        o[0] = fmaf(v.x, fi, o[0]);
+        o[1] = fmaf(v.y, fi, o[1]);
+        o[2] = fmaf(v.z, fi, o[2]);
+        o[3] = fmaf(v.w, fi, o[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(x);
+        o[0] = fmaf(v.x, fi, o[0]);
+        o[1] = fmaf(v.y, fi, o[1]);
+      }
+    }
+  }
+  L = warp_sum(L);
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  bf16* out = static_cast<bf16*>(p.out) + row * HD + lane * PER;
+  if constexpr (PER == 4) {
+#pragma unroll
+    for (int c = 0; c < PER; ++c) o[c] *= inv;
+    st4(out, o);
+  } else {
+    *reinterpret_cast<uint32_t*>(out) = pack_bf16(o[0] * inv, o[1] * inv);
+  }
+}
+
+// ---- host --------------------------------------------------------------------------------------
+// what the kernels need beside the call itself; false: too much for one call
+bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
+  w->s = s;
+  w->qpt = BM / s.G;
+  int64_t at = 0, pairs = 0, rows = 0;
+  for (int g = 0; g < s.n_groups; ++g) {
+    w->first[g] = (int)at;
+    w->prob[g] = (int)pairs;
+    const int64_t queries = (int64_t)(s.seq0[g + 1] - s.seq0[g]) * s.n_q, kt = (s.len[g] + BN - 1) / BN;
+    const int64_t n = kt ? (queries + w->qpt - 1) / w->qpt * s.Hkv : 0;
+    at += n * kt;
+    pairs += n;
+    if (n) rows = std::max(rows, std::min<int64_t>(queries, w->qpt) * s.G);
+    if (at > INT32_MAX / 2) return false;
+  }
+  w->first[s.n_groups] = (int)at;
+  w->prob[s.n_groups] = (int)pairs;
+  w->total = (int)at;
+  w->workers = (int)std::min<int64_t>(kWorkers, at);
+  w->slot_rows = (int)((rows + 3) & ~3);
+  w->row_tiles = (s.n_q * s.G + TILE - 1) / TILE;
+  w->own_slot_rows = (std::min(TILE, s.n_q * s.G) + 3) & ~3;
+  w->alone = at == 0;
+  const double units = (double)s.n_seq * w->row_tiles * s.Hkv;
+  if (s.capacity > 0 && units * ((s.capacity + 15) / 16) > (double)(INT32_MAX / 2)) return false;
+  if ((double)s.n_seq * s.n_q * s.H / 8 > (double)INT32_MAX) return false;
+  const size_t slot = sizeof(float) * (s.hd + 2);
+  const size_t pre = at ? (size_t)(w->workers + pairs) * w->slot_rows * slot : 0;
+  const size_t plan = s.capacity ? ((size_t)s.n_seq * w->row_tiles + 1) * 4 : 0;
+  const size_t own = s.capacity ? (size_t)(kOwnCtas * kOwnWarps + units) * w->own_slot_rows * slot : 0;
+  const size_t a = 0, b = (a + pre + 255) & ~size_t(255), c = (b + own + 255) & ~size_t(255);
+  w->part = reinterpret_cast<float*>(a);
+  w->own_part = reinterpret_cast<float*>(b);
+  w->plan = reinterpret_cast<int32_t*>(c);
+  *bytes = c + plan + 16;
+  return true;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+    if (e == cudaSuccess && q == cudaDriverEntryPointSuccess) return reinterpret_cast<EncodeTiledFn>(p);
+    if (e != cudaSuccess) cudaGetLastError();   // clears the error of this lookup only
+    return static_cast<EncodeTiledFn>(nullptr);
+  }();
+  return fn;
+}
+// bf16, dims from the inside out without gaps, boxes of 64 elements, 128-byte swizzle
+bool make_map(CUtensorMap* map, const void* ptr, std::initializer_list<int64_t> dims, std::initializer_list<int> box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t d[3], st[2];
+  cuuint32_t bx[3], one[3] = {1, 1, 1};
+  int n = 0;
+  for (int64_t x : dims) d[n++] = (cuuint64_t)x;
+  n = 0;
+  for (int x : box) bx[n++] = (cuuint32_t)x;
+  st[0] = d[0] * 2;
+  if (n == 3) st[1] = st[0] * d[1];
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(ptr), d, st, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+std::mutex g_shared_mu;
+uint32_t g_shared_attr[64];
+
+template <int HD>
+cudaError_t set_attrs() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> g(g_shared_mu);
+  const uint32_t bit = HD == 128 ? 1u : 2u;
+  if (dev >= 0 && dev < 64 && (g_shared_attr[dev] & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(k_shared_prefix<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_shared_own<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Own<HD>::SMEM);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) g_shared_attr[dev] |= bit;
+  return e;
+}
+
+template <int HD>
+cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
+  const Shared& s = w.s;
+  cudaError_t e = set_attrs<HD>();
+  if (e != cudaSuccess) return e;
+  const int64_t W = (int64_t)s.Hkv * HD;
+  if (w.total > 0) {
+    CUtensorMap q, k, v;
+    if (!make_map(&q, s.q, {HD, s.H, (int64_t)s.n_seq * s.n_q}, {64, s.G, w.qpt}) ||
+        !make_map(&k, s.k, {W, s.n_rows}, {64, BN}) || !make_map(&v, s.v, {W, s.n_rows}, {64, BN}))
+      return cudaErrorInvalidValue;
+    e = launch_k(k_shared_prefix<HD>, dim3(w.workers), dim3(THREADS), Layout<HD>::SMEM, st, q, k, v, w);
+    if (e != cudaSuccess) return e;
+  }
+  if (s.capacity > 0) {
+    CUtensorMap k, v;
+    const int64_t rows = s.n_seq * s.capacity;
+    if (!make_map(&k, s.own_k, {W, rows}, {64, Own<HD>::KT}) || !make_map(&v, s.own_v, {W, rows}, {64, Own<HD>::KT}))
+      return cudaErrorInvalidValue;
+    e = launch_k(k_shared_own<HD>, dim3(kOwnCtas), dim3(kOwnThreads), Own<HD>::SMEM, st, k, v, w);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t rows = (int64_t)s.n_seq * s.n_q * s.H;
+  return launch_k(k_shared_join<HD>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, w, kOwnCtas);
+}
+
+}  // namespace
+
+bool shared_tc_taken(int dt, const Shared& p) { return dt == DT_BF16 && (p.hd == 64 || p.hd == 128) && p.G <= BM; }
+
+size_t shared_tc_ws_bytes(const Shared& p) {
+  Tc w;
+  size_t n;
+  return plan_tc(p, &w, &n) ? n : 0;
+}
+
+int shared_tc_launches(const Shared& p) {
+  bool prefix = false;
+  for (int g = 0; g < p.n_groups; ++g) prefix = prefix || (p.len[g] > 0 && p.seq0[g + 1] > p.seq0[g]);
+  return 1 + (prefix ? 1 : 0) + (p.capacity > 0 ? 1 : 0);
+}
+
+void reset_shared_tc_caches() {
+  std::lock_guard<std::mutex> g(g_shared_mu);
+  for (int i = 0; i < 64; ++i) g_shared_attr[i] = 0;
+}
+
+cudaError_t launch_shared_tc(const Shared& p, void* ws, cudaStream_t s) {
+  g_used_shared_tc = true;
+  Tc w;
+  size_t n;
+  if (!plan_tc(p, &w, &n)) return cudaErrorInvalidValue;
+  char* base = static_cast<char*>(ws);
+  w.part = reinterpret_cast<float*>(base + reinterpret_cast<size_t>(w.part));
+  w.own_part = reinterpret_cast<float*>(base + reinterpret_cast<size_t>(w.own_part));
+  w.plan = reinterpret_cast<int32_t*>(base + reinterpret_cast<size_t>(w.plan));
+  return p.hd == 128 ? launch_hd<128>(w, s) : launch_hd<64>(w, s);
+}
+
+}  // namespace cb
