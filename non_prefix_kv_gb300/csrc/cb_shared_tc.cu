@@ -45,6 +45,7 @@ constexpr float kLazy = 8.0f;        // weights up to 2^8 before a row's maximum
 constexpr int kWorkers = 152;        // of the prefix kernel, one CTA per SM
 constexpr int kOwnWarps = 4, kOwnThreads = 32 * kOwnWarps, kOwnCtas = 304;   // of the own rows' kernel
 constexpr int TILE = 8;              // rows of its tiles
+constexpr int kHeld = 2048;          // (sequence, row tile) pairs whose steps a CTA keeps in shared memory
 
 struct Tc {
   Shared s;
@@ -118,8 +119,6 @@ template <int HD>
 __global__ void __launch_bounds__(THREADS, 1)
     k_shared_prefix(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Tc w) {
-  pdl_wait();
-  pdl_trigger();                   // (before TMEM is allocated: see tc::kWholeSm)
   using L = Layout<HD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
@@ -144,6 +143,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
+  Seg cur = segment(w, a, b), nxt = cur;
+  nxt.n = 0;
+  if (cur.end < b) nxt = segment(w, cur.end, b);
+  pdl_wait();
+  pdl_trigger();                   // (before TMEM is allocated: see tc::kWholeSm)
   if (warp == 0) {
     tc::tmem_alloc(tmem_slot, TMEM_COLS);
     tc::tmem_relinquish();
@@ -210,9 +214,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   // ---- the run's segments
-  Seg cur = segment(w, a, b), nxt = cur;
-  nxt.n = 0;
-  if (cur.end < b) nxt = segment(w, cur.end, b);
   if (tid == 0) {
     load_q(cur, 0);
     if (nxt.n) load_q(nxt, 1);
@@ -339,12 +340,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    Seg nn = nxt;                  // (Q's buffer is free: both groups' S of this segment are done)
-    nn.n = 0;
-    if (nxt.n && nxt.end < b) {
-      nn = segment(w, nxt.end, b);
-      if (tid == 0) load_q(nn, turn);
-    }
     if (issuer && grp < nxt.n) {
       ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&q_full[turn ^ 1], ((nseg + 1) >> 1) & 1) && tc::mbar_wait(k_full, u & 1));
       if (ok) issue_s(turn ^ 1);
@@ -360,32 +355,52 @@ __global__ void __launch_bounds__(THREADS, 1)
         out[w.slot_rows * HD + r] = isnan(lt) ? lt : mm;
         out[w.slot_rows * (HD + 1) + r] = lt;
       }
-      out += (int64_t)r * HD + grp * (HD / 2);
+      // The rows leave through Q's buffer, HD / 4 columns of the warp's 32 rows at a time, so that a store
+      // covers whole lines (each thread storing its own row took 2.1 us for 126 rows).
+      constexpr int C4 = HD / 16;  // 16-byte words of a row's part
+      uint8_t* st = base + L::OFF_Q + turn * L::T_BYTES + warp * (32 * C4 * 16);
 #pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
-        const uint32_t col = TM_O + grp * (HD / 2) + c * 16;
-        float o0[16], o1[16];
-        tc::tmem_ld16(trow + col, o0);
-        if (cur.n > 1) {           // (else O_1 was never written)
-          tc::tmem_ld16(trow + col + HD, o1);
-        } else {
+      for (int c = 0; c < 2; ++c) {
+        const int col = grp * (HD / 2) + c * (HD / 4);
 #pragma unroll
-          for (int q = 0; q < 16; ++q) o1[q] = 0.f;
-        }
+        for (int h = 0; h < C4 / 4; ++h) {
+          float o0[16], o1[16];
+          tc::tmem_ld16(trow + TM_O + col + h * 16, o0);
+          if (cur.n > 1) {         // (else O_1 was never written)
+            tc::tmem_ld16(trow + TM_O + HD + col + h * 16, o1);
+          } else {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) o0[q] = o0[q] * a0 + o1[q] * a1;
-        if (r < rows) {
-          st8(out + c * 16, o0);
-          st8(out + c * 16 + 8, o0 + 8);
+            for (int q = 0; q < 16; ++q) o1[q] = 0.f;
+          }
+#pragma unroll
+          for (int q = 0; q < 16; ++q) o0[q] = o0[q] * a0 + o1[q] * a1;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<float4*>(st + lane * (C4 * 16) + (((h * 4 + q) ^ (lane & (C4 - 1))) << 4)) =
+                make_float4(o0[4 * q], o0[4 * q + 1], o0[4 * q + 2], o0[4 * q + 3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C4; ++i) {
+          const int rr = i * (32 / C4) + lane / C4, q = lane & (C4 - 1), row = quad * 32 + rr;
+          if (row < rows)
+            *reinterpret_cast<float4*>(out + (int64_t)row * HD + col + q * 4) =
+                *reinterpret_cast<const float4*>(st + rr * (C4 * 16) + ((q ^ (rr & (C4 - 1))) << 4));
+        }
+        __syncwarp();
       }
+      tc::fence_proxy_async_smem();              // (before Q comes into the same place)
     }
     tc::tc_fence_before();
     __syncthreads();               // O and the statistics are free
     tc::tc_fence_after();
     if (!nxt.n) break;             // (uniform)
     cur = nxt;
-    nxt = nn;
+    nxt.n = 0;
+    if (cur.end < b) {
+      nxt = segment(w, cur.end, b);
+      if (tid == 0) load_q(nxt, turn);           // (both groups' S of the segment before are done with the buffer)
+    }
   }
   if (!ok) {
     // report, and give the copies in flight as long again before the memory is given up
@@ -414,7 +429,7 @@ struct Own {
   static constexpr int HALF = KT * HD * 2;                   // bytes of K (or V) of a step
   static constexpr int NST = 3;
   static constexpr int OFF_BAR = kOwnWarps * NST * 2 * HALF;
-  static constexpr int SMEM = OFF_BAR + kOwnWarps * NST * 8 + kOwnThreads * 4 + 1024;
+  static constexpr int SMEM = OFF_BAR + kOwnWarps * NST * 8 + kOwnThreads * 8 + kHeld * 4 + 1024;
 };
 
 __device__ __forceinline__ void mma_bf16_16x8(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -446,16 +461,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A (sequence, row tile, head) counts this many steps more on the line than it has: its start and its piece cost
+// a worker about as much.
+constexpr int kUnitCost = 1;
 // how many workers share the line: a run has two steps at least
 __device__ __forceinline__ int own_workers(int total, int workers) { return max(1, min(workers, total / 2)); }
 
 template <int HD>
 __global__ void __launch_bounds__(kOwnThreads, 2)
     k_shared_own(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Tc w) {
-  // Nothing here needs the prefix kernel's results, only that everything before it is done, which that
-  // kernel has seen before it let this one start; the wait at the end makes this one end after it.
-  if (w.alone) pdl_wait();
-  pdl_trigger();
   using L = Own<HD>;
   constexpr int KS = HD / 16, SLABS = HD / 64, SL = L::KT * 128;
   extern __shared__ uint8_t smem_raw[];
@@ -464,7 +478,8 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint8_t* stages = base + warp * L::NST * 2 * L::HALF;
   uint64_t* full = reinterpret_cast<uint64_t*>(base + L::OFF_BAR) + warp * L::NST;
-  int* before = reinterpret_cast<int*>(base + L::OFF_BAR + kOwnWarps * L::NST * 8);
+  int2* before = reinterpret_cast<int2*>(base + L::OFF_BAR + kOwnWarps * L::NST * 8);
+  int* held = reinterpret_cast<int*>(before + kOwnThreads);      // [min(entries, kHeld)] steps
   const int R = p.n_q * p.G, entries = p.n_seq * w.row_tiles;
   if (lane == 0) {
     for (int i = 0; i < L::NST; ++i) tc::mbar_init(&full[i], 1);
@@ -472,80 +487,125 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
+  // Nothing here needs the prefix kernel's results, only that everything before it is done, which that
+  // kernel has seen before it let this one start; the wait at the end makes this one end after it.
+  if (w.alone) pdl_wait();
+  pdl_trigger();
   // ---- where this worker's run lies: thread i sums the steps of a share of the entries (sequence, row tile),
   // a scan places them; the first CTA writes the plan for the join
   auto row_last = [&](int e, int r) -> int {             // -1: no own row
     const int s = e / w.row_tiles, row = (e - s * w.row_tiles) * TILE + r;
     return r >= TILE || row >= R ? -1 : max(-1, shared_last(p, (int64_t)s * p.n_q + row / p.G));
   };
-  auto steps_of = [&](int e) -> int {
+  auto count_steps = [&](int e) -> int {
     const int s = e / w.row_tiles, row0 = (e - s * w.row_tiles) * TILE;
     int mx = -1;
     for (int j = row0 / p.G; j <= (min(R, row0 + TILE) - 1) / p.G; ++j) mx = max(mx, shared_last(p, (int64_t)s * p.n_q + j));
     return (mx + L::KT) / L::KT;
   };
+  auto steps_of = [&](int e) -> int { return e < kHeld ? held[e] : count_steps(e); };
+  auto on_line = [&](int n) -> int { return n > 0 ? (n + kUnitCost) * p.Hkv : 0; };
   const int share = (entries + kOwnThreads - 1) / kOwnThreads, e0 = min(entries, tid * share), e1 = min(entries, e0 + share);
-  int mine = 0;
-  for (int e = e0; e < e1; ++e) mine += steps_of(e) * p.Hkv;
-  int incl = mine;
+  int mine = 0, steps = 0;                               // on the line, and steps
+  for (int e = e0; e < e1; ++e) {
+    const int n = count_steps(e);
+    if (e < kHeld) held[e] = n;
+    mine += on_line(n);
+    steps += n * p.Hkv;
+  }
+  int incl = mine, incl_steps = steps;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int y = __shfl_up_sync(0xffffffffu, incl, o), z = __shfl_up_sync(0xffffffffu, incl_steps, o);
+    if (lane >= o) {
+      incl += y;
+      incl_steps += z;
+    }
   }
-  __shared__ int wsum[kOwnWarps];
-  if (lane == 31) wsum[warp] = incl;
+  __shared__ int2 wsum[kOwnWarps];
+  if (lane == 31) wsum[warp] = make_int2(incl, incl_steps);
   __syncthreads();
   int total = 0;
 #pragma unroll
   for (int x = 0; x < kOwnWarps; ++x) {
-    if (x < warp) incl += wsum[x];
-    total += wsum[x];
+    if (x < warp) {
+      incl += wsum[x].x;
+      incl_steps += wsum[x].y;
+    }
+    total += wsum[x].x;
   }
-  before[tid] = incl - mine;
+  before[tid] = make_int2(incl - mine, incl_steps - steps);
   if (blockIdx.x == 0) {
     int at = incl - mine;
     for (int e = e0; e < e1; ++e) {
       w.plan[e] = at;
-      at += steps_of(e) * p.Hkv;
+      at += on_line(steps_of(e));
     }
     if (tid == 0) w.plan[entries] = total;
   }
   __syncthreads();
+  struct Pos {
+    int e, h, k, n;       // entry, head, step of the unit, steps in a unit of the entry
+    int step;             // the step's number among all
+  };
+  // place x of the line: the first step at or behind it (x < total)
+  auto place = [&](int x) -> Pos {
+    // the last thread whose share starts at or before it and is not empty
+    int c = 0;
+    for (int i = lane; i < kOwnThreads; i += 32)
+      if (before[i].x <= x && i * share < entries) c = i;
+    c = __reduce_max_sync(0xffffffffu, c);
+    int left = x - before[c].x, step = before[c].y;
+    Pos r;
+    for (int f = c * share;; f += 32) {
+      const int n = f + lane < entries ? steps_of(f + lane) : 0, mine = on_line(n);
+      int in = mine, st = n * p.Hkv;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, in, o), z = __shfl_up_sync(0xffffffffu, st, o);
+        if (lane >= o) {
+          in += y;
+          st += z;
+        }
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, left < in);
+      if (hit || f + 32 >= entries) {
+        const int who = hit ? __ffs(hit) - 1 : 31;
+        r.e = f + who;
+        r.n = __shfl_sync(0xffffffffu, n, who);
+        left -= __shfl_sync(0xffffffffu, in - mine, who);
+        r.step = step + __shfl_sync(0xffffffffu, st - n * p.Hkv, who);
+        break;
+      }
+      left -= __shfl_sync(0xffffffffu, in, 31);
+      step += __shfl_sync(0xffffffffu, st, 31);
+    }
+    r.h = left / (r.n + kUnitCost);
+    r.k = max(0, left - r.h * (r.n + kUnitCost) - kUnitCost);
+    r.step += r.h * r.n + r.k;
+    return r;
+  };
   const int n_work = own_workers(total, gridDim.x * kOwnWarps), worker = warp * gridDim.x + blockIdx.x;
-  const int a = worker < n_work ? run_start(total, worker, n_work) : 0, b = worker < n_work ? run_start(total, worker + 1, n_work) : 0;
-  if (a < b) {
-    auto warp_steps = [&](int e) -> int {
-      return (__reduce_max_sync(0xffffffffu, row_last(e, lane)) + L::KT) / L::KT;
-    };
-    struct Pos {
-      int e, h, k, n;       // entry, head, step of the unit, steps in a unit of the entry
-    };
+  if (worker < n_work && total > 0) {
+    const int va = run_start(total, worker, n_work), vb = run_start(total, worker + 1, n_work);
+    Pos cur = place(va);
+    int b;
+    if (vb < total) {
+      b = place(vb).step;
+    } else {
+      b = 0;
+#pragma unroll
+      for (int x = 0; x < kOwnWarps; ++x) b += wsum[x].y;
+    }
+    const int a = cur.step;
     auto advance = [&](Pos& x) {
       if (++x.k < x.n) return;
       x.k = 0;
       if (++x.h < p.Hkv) return;
       x.h = 0;
-      ++x.e;
-      while (x.e < entries && (x.n = warp_steps(x.e)) == 0) ++x.e;
+      for (++x.e; x.e < entries; ++x.e)
+        if ((x.n = (__reduce_max_sync(0xffffffffu, row_last(x.e, lane)) + L::KT) / L::KT) > 0) return;
     };
-    Pos cur;
-    {
-      // the last thread whose share starts at or before the run
-      int c = 0;
-      for (int i = lane; i < kOwnThreads; i += 32)
-        if (before[i] <= a && i * share < entries) c = i;
-      c = __reduce_max_sync(0xffffffffu, c);
-      cur.e = c * share;
-      int left = a - before[c];
-      for (;; ++cur.e) {
-        cur.n = warp_steps(cur.e);
-        if (left < cur.n * p.Hkv) break;
-        left -= cur.n * p.Hkv;
-      }
-      cur.h = left / cur.n;
-      cur.k = left - cur.h * cur.n;
-    }
     auto fill = [&](const Pos& x, int st) {
       if (lane != 0) return;
       const int row = (int)((int64_t)(x.e / w.row_tiles) * p.capacity) + x.k * L::KT;
@@ -562,36 +622,44 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
       fill(pre, loaded);
       if (a + loaded + 1 < b) advance(pre);
     }
+    // Q^T as the column operand: thread (g, t) holds row g, channels 2t, 2t + 1 (and 8 on) of every 16
+    auto load_q = [&](const Pos& x, uint32_t (*qb)[2]) {
+      const int s = x.e / w.row_tiles, row = (x.e - s * w.row_tiles) * TILE + g;
+      const bool on = row < R;
+      const int j = on ? row / p.G : 0;
+      const uint32_t* q = reinterpret_cast<const uint32_t*>(
+          static_cast<const bf16*>(p.q) + (((int64_t)s * p.n_q + j) * p.H + (int64_t)x.h * p.G + (on ? row - j * p.G : 0)) * HD + 2 * t);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qb[k][0] = on ? q[k * 8] : 0u;
+        qb[k][1] = on ? q[k * 8 + 4] : 0u;
+      }
+    };
     // a lane's row and 16-byte chunk in the matrices that ldmatrix reads: of K keys by channels, of V^T
     // channels by keys
     const int k_row = (lane & 7) + (lane & 8), k_chunk = lane >> 4;
     const int v_row = (lane & 7) + ((lane >> 4) << 3), v_chunk = (lane >> 3) & 1;
     bool ok = true;
     int done = 0;                                  // steps of the run
+    uint32_t qb[KS][2], qn[KS][2];                 // this unit's queries, and the next one's
+    int lv = row_last(cur.e, lane), lvn = lv;      // the last key of the tile's row `lane`, here and in the next unit
+    if (a < b) load_q(cur, qb);
     while (ok && a + done < b) {
       // ---------------------------------------------------------------- a unit, or a part of one
-      const int s = cur.e / w.row_tiles, row0 = (cur.e - s * w.row_tiles) * TILE, nrow = min(TILE, R - row0), h = cur.h;
-      const int e = cur.e, nk = __reduce_max_sync(0xffffffffu, row_last(e, lane)) + 1;
-      int lastr[2];
-      lastr[0] = row_last(e, 2 * t);
-      lastr[1] = row_last(e, 2 * t + 1);
-      uint32_t qb[KS][2];
-      {
-        const int row = row0 + g;
-        const bool on = g < nrow;
-        const int j = on ? row / p.G : 0;
-        const uint32_t* q = reinterpret_cast<const uint32_t*>(
-            static_cast<const bf16*>(p.q) + (((int64_t)s * p.n_q + j) * p.H + (int64_t)h * p.G + (on ? row - j * p.G : 0)) * HD + 2 * t);
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          qb[k][0] = on ? q[k * 8] : 0u;
-          qb[k][1] = on ? q[k * 8 + 4] : 0u;
-        }
-      }
+      const int row0 = (cur.e % w.row_tiles) * TILE, nrow = min(TILE, R - row0);
+      const int nk = __reduce_max_sync(0xffffffffu, lv) + 1;
+      const int lastr[2] = {__shfl_sync(0xffffffffu, lv, 2 * t), __shfl_sync(0xffffffffu, lv, 2 * t + 1)};
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[KS][4];
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       const int n = min(cur.n - cur.k, b - a - done);
+      Pos nx = cur;
+      if (a + done + n < b) {
+        nx.k = nx.n - 1;
+        advance(nx);
+        if (nx.e != cur.e) lvn = row_last(nx.e, lane);
+        load_q(nx, qn);
+      }
       for (int x = 0; x < n; ++x, ++done) {
         const int st = done % L::NST, key0 = (cur.k + x) * L::KT;
         if (!(ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[st], (done / L::NST) & 1)))) break;
@@ -608,18 +676,21 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
         }
 #pragma unroll
         for (int kw = 0; kw < L::KW; ++kw) {
-          float z[4] = {0.f, 0.f, 0.f, 0.f};
+          float z[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
           const uint32_t ka = tc::smem_u32(sk) + (kw * 16 + k_row) * 128;
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
+          for (int k = 0; k < KS; k += 2) {        // two sums: the products of one wait for one another
             uint32_t f[4];
-            const int c = 2 * k + k_chunk;
+            int c = 2 * k + k_chunk;
             ldmatrix4(f, ka + (c >> 3) * SL + (((c & 7) ^ (k_row & 7)) << 4));
             mma_bf16_16x8(z, f, qb[k][0], qb[k][1]);
+            c += 2;
+            ldmatrix4(f, ka + (c >> 3) * SL + (((c & 7) ^ (k_row & 7)) << 4));
+            mma_bf16_16x8(y, f, qb[k + 1][0], qb[k + 1][1]);
           }
           const int key = key0 + kw * 16 + g;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] = key + (i >> 1) * 8 <= lastr[i & 1] ? z[i] * p.scale_log2 : -INFINITY;
+          for (int i = 0; i < 4; ++i) z[i] = key + (i >> 1) * 8 <= lastr[i & 1] ? (z[i] + y[i]) * p.scale_log2 : -INFINITY;
           float mx0 = fmaxf(z[0], z[2]), mx1 = fmaxf(z[1], z[3]);
           if (__any_sync(0xffffffffu, mx0 > m[0] + kLazy || mx1 > m[1] + kLazy)) {
 #pragma unroll
@@ -670,7 +741,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
         l[0] += __shfl_xor_sync(0xffffffffu, l[0], q);
         l[1] += __shfl_xor_sync(0xffffffffu, l[1], q);
       }
-      float* out = slot(w.own_part, w.own_slot_rows, HD, worker, e * p.Hkv + h);
+      float* out = slot(w.own_part, w.own_slot_rows, HD, worker, cur.e * p.Hkv + cur.h);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int r = 2 * t + c;
@@ -685,8 +756,13 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
           out[r * HD + i * 16 + 8 + g] = o[i][2 + c];
         }
       }
-      cur.k += n - 1;
-      if (a + done < b) advance(cur);
+      cur = nx;
+      lv = lvn;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qb[k][0] = qn[k][0];
+        qb[k][1] = qn[k][1];
+      }
     }
     if (!ok) {
       // report, and give the copies in flight as long again
@@ -698,81 +774,94 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
 }
 
 // ---- join: one warp per (query, head) ------------------------------------------------------------
+// What does not come from the two kernels before is worked out before the wait for them.
 template <int HD>
 __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc w, int own_grid) {
   const Shared& p = w.s;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_trigger();
-  if (row >= (int64_t)p.n_seq * p.n_q * p.H) return;
-  const int64_t t = row / p.H;
-  const int hh = (int)(row - t * p.H), h = hh / p.G, gh = hh - h * p.G, s = (int)(t / p.n_q), j = (int)(t - (int64_t)s * p.n_q);
-  const int raw = p.last[t], last = shared_last(p, t);
-  if (raw != last && hh == 0 && lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_INDEX);
+  const int t = blockIdx.x, hh = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int s = t / p.n_q, j = t - s * p.n_q, h = hh / p.G, gh = hh - h * p.G;
+  const bool on = hh < p.H;
   // pieces of the prefix, then the own ones: slots are one worker apart
-  int n_pre = 0, n_own = 0, r = 0, r_own = 0;
+  int n_pre = 0, n_own = 0, r = 0;
   const float *pre = nullptr, *own = nullptr;
   const int64_t pre_step = (int64_t)w.slot_rows * (HD + 2), own_step = (int64_t)w.own_slot_rows * (HD + 2);
-  if (last >= -1 && w.total > 0) {
+  if (on && w.total > 0) {
     int g = 0;
     while (s >= p.seq0[g + 1]) ++g;
     const int kt = (p.len[g] + BN - 1) / BN;
     if (kt > 0) {
-      const int tl = (int)(t - (int64_t)p.seq0[g] * p.n_q), rt = tl / w.qpt, pl = h * row_tiles_of(w, g) + rt;
+      const int tl = t - p.seq0[g] * p.n_q, rt = tl / w.qpt, pl = h * row_tiles_of(w, g) + rt;
       const int x0 = w.first[g] + pl * kt, w0 = worker_of(w.total, x0, w.workers);
       n_pre = worker_of(w.total, x0 + kt - 1, w.workers) - w0 + 1;
       pre = slot(w.part, w.slot_rows, HD, w0, w.prob[g] + pl);
       r = (tl - rt * w.qpt) * p.G + gh;
     }
   }
+  const int rr = j * p.G + gh, e = s * w.row_tiles + rr / TILE, r_own = rr % TILE;
+  // (the bounds were written before the call: the kernels that let this one start had waited for that)
+  const bool only = w.alone && p.capacity == 0;
+  if (only) pdl_wait();
+  const int raw = p.last[t], last = shared_last(p, t);
+  if (raw != last && hh == 0 && lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_INDEX);
+  if (!only) pdl_wait();
+  pdl_trigger();
+  if (!on) return;
+  if (last == -2) n_pre = 0;
   if (last >= 0) {
-    const int rr = j * p.G + gh, e = s * w.row_tiles + rr / TILE, total = w.plan[p.n_seq * w.row_tiles];
-    const int at = w.plan[e], n = (w.plan[e + 1] - at) / p.Hkv, x0 = at + h * n;
+    const int total = w.plan[p.n_seq * w.row_tiles], at = w.plan[e], n = (w.plan[e + 1] - at) / p.Hkv - kUnitCost;
+    const int x0 = at + h * (n + kUnitCost) + kUnitCost;       // the unit's first step
     const int workers = own_workers(total, own_grid * kOwnWarps), w0 = worker_of(total, x0, workers);
     n_own = worker_of(total, x0 + n - 1, workers) - w0 + 1;
     own = slot(w.own_part, w.own_slot_rows, HD, w0, e * p.Hkv + h);
-    r_own = rr % TILE;
   }
   const int n = n_pre + n_own;
-  auto piece = [&](int i) { return i < n_pre ? pre + i * pre_step : own + (i - n_pre) * own_step; };
-  auto stat = [&](int i, int which) {
-    return i < n_pre ? piece(i)[w.slot_rows * (HD + which) + r] : piece(i)[w.own_slot_rows * (HD + which) + r_own];
-  };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, stat(i, 0));
-  M = warp_max(M);
   constexpr int PER = HD / 32;
-  float L = 0.f, o[PER];
+  auto stat = [&](int i, int which) {
+    return i < n_pre ? pre[i * pre_step + w.slot_rows * (HD + which) + r]
+                     : own[(i - n_pre) * own_step + w.own_slot_rows * (HD + which) + r_own];
+  };
+  auto load = [&](int i, float* x) {
+    const float* y = (i < n_pre ? pre + i * pre_step + r * HD : own + (i - n_pre) * own_step + r_own * HD) + lane * PER;
+    if constexpr (PER == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(y);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(y);
+      x[0] = v.x, x[1] = v.y;
+    }
+  };
+  // Pieces come eight at a time, statistics and rows in one go (a row is mostly one batch, and the time of a
+  // small join is that of its chain of loads), each batch joined to what came before it.
+  constexpr int BATCH = 8;
+  float M = -INFINITY, L = 0.f, o[PER];
 #pragma unroll
   for (int c = 0; c < PER; ++c) o[c] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float f = 0.f;
-    if (i0 + lane < n) {
-      const float m = stat(i0 + lane, 0);
-      f = m == -INFINITY ? 0.f : tc::ex2_approx(m - M);      // (a NaN is no infinity)
-      L = fmaf(stat(i0 + lane, 1), f, L);
+  for (int i0 = 0; i0 < n; i0 += BATCH) {
+    float x[BATCH][PER], m = -INFINITY, l = 0.f;
+    if (lane < BATCH && i0 + lane < n) {
+      m = stat(i0 + lane, 0);
+      l = stat(i0 + lane, 1);
     }
-    for (int i = 0; i < min(32, n - i0); ++i) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (i0 + i < n) load(i0 + i, x[i]);
+    const float top = fmaxf(M, warp_max(m)), keep = M == -INFINITY ? 0.f : tc::ex2_approx(M - top);
+    const float f = m == -INFINITY ? 0.f : tc::ex2_approx(m - top);      // (a NaN is no infinity)
+    L = fmaf(l, f, L * keep);
+#pragma unroll
+    for (int c = 0; c < PER; ++c) o[c] *= keep;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
       const float fi = __shfl_sync(0xffffffffu, f, i);
-      if (fi == 0.f) continue;
-      const float* x = piece(i0 + i) + (i0 + i < n_pre ? r : r_own) * HD + lane * PER;
-      if constexpr (PER == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(x);
-        o[0] = fmaf(v.x, fi, o[0]);
-        o[1] = fmaf(v.y, fi, o[1]);
-        o[2] = fmaf(v.z, fi, o[2]);
-        o[3] = fmaf(v.w, fi, o[3]);
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(x);
-        o[0] = fmaf(v.x, fi, o[0]);
-        o[1] = fmaf(v.y, fi, o[1]);
-      }
+#pragma unroll
+      for (int c = 0; c < PER; ++c)
+        if (i0 + i < n && fi != 0.f) o[c] = fmaf(x[i][c], fi, o[c]);
     }
+    M = top;
   }
   L = warp_sum(L);
   const float inv = L == 0.f ? 0.f : 1.0f / L;
-  bf16* out = static_cast<bf16*>(p.out) + row * HD + lane * PER;
+  bf16* out = static_cast<bf16*>(p.out) + ((int64_t)t * p.H + hh) * HD + lane * PER;
   if constexpr (PER == 4) {
 #pragma unroll
     for (int c = 0; c < PER; ++c) o[c] *= inv;
@@ -801,14 +890,14 @@ bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
   w->first[s.n_groups] = (int)at;
   w->prob[s.n_groups] = (int)pairs;
   w->total = (int)at;
-  w->workers = (int)std::min<int64_t>(kWorkers, at);
+  w->workers = (int)std::min<int64_t>(kWorkers, (at + 1) / 2);          // (a tile for each group of warps)
   w->slot_rows = (int)((rows + 3) & ~3);
   w->row_tiles = (s.n_q * s.G + TILE - 1) / TILE;
   w->own_slot_rows = (std::min(TILE, s.n_q * s.G) + 3) & ~3;
   w->alone = at == 0;
   const double units = (double)s.n_seq * w->row_tiles * s.Hkv;
-  if (s.capacity > 0 && units * ((s.capacity + 15) / 16) > (double)(INT32_MAX / 2)) return false;
-  if ((double)s.n_seq * s.n_q * s.H / 8 > (double)INT32_MAX) return false;
+  if (s.capacity > 0 && units * ((s.capacity + 15) / 16 + kUnitCost) > (double)(INT32_MAX / 2)) return false;
+  if ((s.H + 7) / 8 > 65535) return false;
   const size_t slot = sizeof(float) * (s.hd + 2);
   const size_t pre = at ? (size_t)(w->workers + pairs) * w->slot_rows * slot : 0;
   const size_t plan = s.capacity ? ((size_t)s.n_seq * w->row_tiles + 1) * 4 : 0;
@@ -890,8 +979,7 @@ cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
     e = launch_k(k_shared_own<HD>, dim3(kOwnCtas), dim3(kOwnThreads), Own<HD>::SMEM, st, k, v, w);
     if (e != cudaSuccess) return e;
   }
-  const int64_t rows = (int64_t)s.n_seq * s.n_q * s.H;
-  return launch_k(k_shared_join<HD>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, w, kOwnCtas);
+  return launch_k(k_shared_join<HD>, dim3(s.n_seq * s.n_q, (s.H + 7) / 8), dim3(256), 0, st, w, kOwnCtas);
 }
 
 }  // namespace
