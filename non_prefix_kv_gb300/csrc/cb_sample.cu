@@ -11,10 +11,17 @@
 // 31 bits behind the point (relative error 2^-29 at most, mostly of random sign), and sums are exact in any
 // order: the result does not depend on how the row is split.
 //
-// One cluster per row, a CTA holds a run of 256-id tiles.  Passes over the row (from L2 after the first):
-// the largest logit; for k, counts of 2048 classes of the key's leading bits, then of the border class's next
-// bits; for p the same with weights; where equal logits straddle the border, the id up to which they are kept;
-// the kept weight of every tile; and the one tile that holds the draw once more.
+// One cluster per row, a CTA holds a run of 256-id tiles.  What a row's rules ask for decides its way:
+//   k = 1 (or T = 0)      the largest logit's lowest id, found in the pass that finds the largest logit
+//   k up to 1024          that pass keeps the largest of each of 4096 groups of ids; the k-th largest of those is
+//                         no larger than the k-th logit, and few logits above it are not among the k.  These come
+//                         together, in order of their ids, in the first CTA, which sorts them and finishes
+//   a least share         is a least logit (a comparison); if few ids reach it they are finished in the same way
+//   p alone               the weights of 2048 classes of (max - l) / T, the border class's ids sorted as above; then
+//                         the kept weight of every tile, and the one tile that holds the draw once more
+//   other k, many equals  the same with counts (weights) of the key's leading bits, then of the border class's next
+// Few rows are bound by the chain of passes and of the cluster's meetings, many by the weights (about 30
+// instructions) and the classes' atomics.
 #include <math.h>
 
 #include <algorithm>
@@ -44,6 +51,10 @@ constexpr int kMaxTiles = 512;               // of a CTA
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kScale = 42;                   // a weight of 1 is 2^42: 2^20 of them stay below 2^63
 constexpr int kPiece = 14;                   // bits of a weight's pieces in a class's sums: 2^17 of them fit 32 bits
+constexpr int kList = 2048;                  // ids that one CTA finishes
+constexpr int kSmallK = 1024;
+constexpr int kGroups = 4096;                // groups whose largest logits bound the k-th: eight a thread at most
+constexpr float kStep = 32.0f;               // classes of an octave of weight
 
 struct Find {           // where the order's prefix ends: in this class, after so much of the classes above it
   u64 mass;             // weight above it
@@ -53,8 +64,22 @@ struct Find {           // where the order's prefix ends: in this class, after s
   uint32_t bin;
 };
 struct Shared {
-  uint32_t cnt[kBins];                       // of this CTA's ids in a class, and the pieces of their weights' sum
-  uint32_t piece[3][kBins];
+  union {
+    struct {
+      uint32_t cnt[kBins];                   // of this CTA's ids in a class, and the pieces of their weights' sum
+      uint32_t piece[3][kBins];
+    };
+    struct {
+      u64 order[kList];                      // a list's sort keys, then its kept weights
+      union {
+        struct {
+          uint32_t key[kList];               // a list's keys and ids, in order of the ids
+          int32_t id[kList];
+        };
+        uint32_t group[kGroups];             // the largest key of each group of ids
+      };
+    };
+  };
   u64 tile_mass[kMaxTiles];                  // kept weight of a tile (ties: how many)
   uint2 table[32];                           // 2^31 2^(j / 32), and the same in fp32
   u64 warp_mass[kWarps];
@@ -64,7 +89,7 @@ struct Shared {
   uint32_t part_count[kMaxCluster];
   float part_max[kMaxCluster];
   Find found;
-  uint32_t cutoff;
+  uint32_t cutoff, border;
 };
 
 // order of values as order of unsigned integers; bf16 values use the upper half
@@ -120,23 +145,56 @@ __device__ __forceinline__ V* at_rank(V* p, int rank) {      // the same object 
   return reinterpret_cast<V*>(a);
 }
 
+// 2^x of a class: the class of a logit, larger for a larger one
+__device__ __forceinline__ uint32_t class_of(float v, const Heat& h) {
+  const float y = (v == h.mx ? 0.f : v - h.mx) * h.ch;                 // <= 0; -inf for what weighs nothing
+  return kBins - 1 - (uint32_t)fminf(-y * kStep, (float)(kBins - 1));
+}
+
+// ceil(a share of `of`), at least 1; the share as a fraction of 2^64
+__device__ __forceinline__ u64 share_of(u64 of, u64 share) {
+  const u64 t = __umul64hi(of, share) + (of * share != 0);
+  return t ? t : 1ull;
+}
+
+struct Rules {
+  uint32_t k;            // 1..; 0xffffffff: all
+  u64 p;                 // the share as a fraction of 2^64 (p_on)
+  bool p_on;
+  float least;           // the least logit kept
+  u64 u;
+  float heat;            // > 0
+};
+
+struct Args {
+  int32_t* token;
+  float* logprob;
+  int32_t* kept;
+  const float* u;
+  cb_sample_rules r;
+  int vocab, tpc;
+  bool vec;
+};
+
 // One row's work as its cluster sees it.
 template <typename T>
 struct Row {
+  static constexpr int kKey = sizeof(T) == 2 ? 16 : 32;
   const T* x;
   Shared* s;
   Heat heat;
   int vocab, tile0, tiles, nc, rank;
   bool vec;
 
-  __device__ void meet() const {             // everything written so far is seen by the whole cluster
+  __device__ __forceinline__ void meet() const {             // everything written so far is seen by the whole cluster
     if (nc > 1)
       tc::cluster_sync();
     else
       __syncthreads();
   }
+  __device__ __forceinline__ Shared* at(int q) const { return nc > 1 ? at_rank(s, q) : s; }
   // the lane's eight values of tile t of this CTA; past the end -inf
-  __device__ int load(int t, float* f) const {
+  __device__ __forceinline__ int load(int t, float* f) const {
     const int lane = threadIdx.x & 31, id = (tile0 + t) * kTile + lane * 8;
     if (vec && id + 8 <= vocab) {
       ld8(x + id, f);
@@ -146,14 +204,49 @@ struct Row {
     }
     return id;
   }
+  __device__ __forceinline__ u64 weigh(float v) const { return weight<T>(v, heat, s->table); }
 
-  // Counts (and weights) of the classes (key >> shift) & (kBins - 1) of the ids with key >> upto == prefix, and
-  // key >= floor; upto 32: of all.  Then, in falling order of classes, the one in which the running count
-  // (weight) reaches `target` behind what lies above the prefix.  want(total weight of the classes) gives the
-  // target where it is not known before.
-  template <bool MASS, typename Want>
-  __device__ Find find(int shift, int upto, uint32_t prefix, uint32_t floor, Find above, Want want) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // This CTA's exclusive sum over its threads, and the sum of all (every thread calls)
+  __device__ __forceinline__ void scan(uint32_t& c, u64& m, uint32_t& ct, u64& mt) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t ci = c;
+    u64 mi = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, ci, o);
+      const u64 d = __shfl_up_sync(0xffffffffu, mi, o);
+      if (lane >= o) {
+        ci += a;
+        mi += d;
+      }
+    }
+    __syncthreads();                         // (what was there is read)
+    if (lane == 31) {
+      s->warp_count[warp] = ci;
+      s->warp_mass[warp] = mi;
+    }
+    __syncthreads();
+    ct = 0;
+    mt = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) {
+        ci += s->warp_count[w];
+        mi += s->warp_mass[w];
+      }
+      ct += s->warp_count[w];
+      mt += s->warp_mass[w];
+    }
+    c = ci - c;
+    m = mi - m;
+  }
+
+  // Counts (and weights) of the ids' classes cls(value, key), -1: none.  Then, in falling order of classes, the
+  // one in which the running count (weight) reaches the target behind what lies above all of them;
+  // want(weight of all) gives the target.
+  template <bool MASS, typename Cls, typename Want>
+  __device__ __forceinline__ Find find(Find above, Cls cls, Want want) {
+    const int tid = threadIdx.x, warp = tid >> 5;
     for (int i = tid; i < kBins; i += kThreads) {
       s->cnt[i] = 0;
       if (MASS) s->piece[0][i] = s->piece[1][i] = s->piece[2][i] = 0;
@@ -164,12 +257,12 @@ struct Row {
       load(t, f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t key = key_of<T>(f[i]);
-        if (!(f[i] > -INFINITY) || key < floor || (upto < 32 && key >> upto != prefix)) continue;
-        const uint32_t b = key >> shift & (kBins - 1);
+        if (!(f[i] > -INFINITY)) continue;
+        const int b = cls(f[i], key_of<T>(f[i]));
+        if (b < 0) continue;
         atomicAdd(&s->cnt[b], 1u);
         if (MASS) {
-          const u64 w = weight<T>(f[i], heat, s->table);
+          const u64 w = weigh(f[i]);
           const uint32_t p0 = (uint32_t)w & ((1u << kPiece) - 1), p1 = (uint32_t)(w >> kPiece) & ((1u << kPiece) - 1),
                          p2 = (uint32_t)(w >> 2 * kPiece);
           if (p0) atomicAdd(&s->piece[0][b], p0);
@@ -182,10 +275,8 @@ struct Row {
     // this CTA's share of the classes, in falling order; a thread holds up to four neighbours
     constexpr int kPer = kBins / kThreads;
     const int share = kBins / nc, per = share > kThreads ? share / kThreads : 1;
-    uint32_t c[kPer];
-    u64 m[kPer];
-    uint32_t cs = 0;
-    u64 ms = 0;
+    uint32_t c[kPer], cs = 0, ct;
+    u64 m[kPer], ms = 0, mt;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       c[j] = 0;
@@ -194,7 +285,7 @@ struct Row {
       if (j < per && i < share) {
         const int b = kBins - 1 - (rank * share + i);
         for (int q = 0; q < nc; ++q) {
-          const Shared* o = nc > 1 ? at_rank(s, q) : s;
+          const Shared* o = at(q);
           c[j] += o->cnt[b];
           if (MASS)
             m[j] += (u64)o->piece[0][b] + ((u64)o->piece[1][b] << kPiece) + ((u64)o->piece[2][b] << 2 * kPiece);
@@ -203,43 +294,18 @@ struct Row {
       cs += c[j];
       ms += m[j];
     }
-    uint32_t ci = cs;
-    u64 mi = ms;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t a = __shfl_up_sync(0xffffffffu, ci, o);
-      const u64 d = __shfl_up_sync(0xffffffffu, mi, o);
-      if (lane >= o) {
-        ci += a;
-        mi += d;
-      }
-    }
-    if (lane == 31) {
-      s->warp_count[warp] = ci;
-      s->warp_mass[warp] = mi;
-    }
-    __syncthreads();
-    uint32_t ct = 0;
-    u64 mt = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        ci += s->warp_count[w];
-        mi += s->warp_mass[w];
-      }
-      ct += s->warp_count[w];
-      mt += s->warp_mass[w];
-    }
+    uint32_t cb = cs;
+    u64 mb = ms;
+    scan(cb, mb, ct, mt);
     if (tid < nc) {
-      Shared* o = nc > 1 ? at_rank(s, tid) : s;
-      o->part_count[rank] = ct;
-      o->part_mass[rank] = mt;
+      at(tid)->part_count[rank] = ct;
+      at(tid)->part_mass[rank] = mt;
     }
     meet();
     // what lies above this thread's classes
     u64 all = 0;
-    uint32_t cb = above.count + ci - cs;
-    u64 mb = above.mass + mi - ms;
+    cb += above.count;
+    mb += above.mass;
     for (int q = 0; q < nc; ++q) {
       all += s->part_mass[q];
       if (q < rank) {
@@ -253,7 +319,7 @@ struct Row {
       const u64 before = MASS ? mb : cb, behind = MASS ? mb + m[j] : cb + c[j];
       if (before < target && target <= behind) {
         const Find r{mb, cb, c[j], m[j], (uint32_t)(kBins - 1 - (rank * share + tid * per + j))};
-        for (int q = 0; q < nc; ++q) (nc > 1 ? at_rank(s, q) : s)->found = r;
+        for (int q = 0; q < nc; ++q) at(q)->found = r;
       }
       cb += c[j];
       mb += m[j];
@@ -261,23 +327,232 @@ struct Row {
     meet();
     return s->found;
   }
-};
 
-struct Args {
-  int32_t* token;
-  float* logprob;
-  int32_t* kept;
-  const float* u;
-  cb_sample_rules r;
-  int vocab, tpc;
-  bool vec;
+  // The ids with take(value, key), in order, to the first CTA's list, if there are kList at most; how many
+  // (the same in all CTAs), and the weight of all ids of the row where it is asked for.
+  template <bool MASS, typename Take>
+  __device__ __forceinline__ uint32_t gather(Take take, u64* weight_of_all) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tpw = (tiles + kWarps - 1) / kWarps, t0 = warp * tpw, t1 = min(tiles, t0 + tpw);
+    uint32_t n = 0;
+    u64 m = 0;
+    for (int t = t0; t < t1; ++t) {
+      float f[8];
+      load(t, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!(f[i] > -INFINITY)) continue;
+        n += take(f[i], key_of<T>(f[i]));
+        if (MASS) m += weigh(f[i]);
+      }
+    }
+    uint32_t ct;
+    u64 mt;
+    scan(n, m, ct, mt);
+    if (tid < nc) {
+      at(tid)->part_count[rank] = ct;
+      if (MASS) at(tid)->part_mass[rank] = mt;
+    }
+    meet();
+    uint32_t base = 0, total = 0;
+    u64 all = 0;
+    for (int q = 0; q < nc; ++q) {
+      if (q < rank) base += s->part_count[q];
+      total += s->part_count[q];
+      if (MASS) all += s->part_mass[q];
+    }
+    if (MASS) *weight_of_all = all;
+    if (total <= kList) {
+      Shared* o = at(0);
+      // (the warp's first lane has the sum of the warps before it)
+      base += __shfl_sync(0xffffffffu, n, 0);
+      for (int t = t0; t < t1; ++t) {
+        float f[8];
+        const int id = load(t, f);
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c += f[i] > -INFINITY && take(f[i], key_of<T>(f[i]));
+        uint32_t incl = c;
+        if (__any_sync(0xffffffffu, c)) {
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += y;
+          }
+          uint32_t to = base + incl - c;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (f[i] > -INFINITY && take(f[i], key_of<T>(f[i]))) {
+              o->key[to] = key_of<T>(f[i]);
+              o->id[to++] = id + i;
+            }
+          base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+      }
+    }
+    meet();
+    return total;
+  }
+
+  // Sorts a list of n: order[r] is (all bits of the key inverted, place in the list), rising.  A warp owns 64
+  // neighbours at a time, so that steps of up to 32 need no other warp.
+  __device__ __forceinline__ void sort(int n) const {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int N = 64;
+    while (N < n) N <<= 1;
+    for (int i = tid; i < N; i += kThreads) s->order[i] = i < n ? (u64)~s->key[i] << 32 | (uint32_t)i : ~0ull;
+    __syncthreads();
+    auto step = [&](int i, int j, int size) {      // the pair (i, i + j)
+      const u64 a = s->order[i], b = s->order[i + j];
+      if ((a > b) == ((i & size) == 0)) {
+        s->order[i] = b;
+        s->order[i + j] = a;
+      }
+    };
+    for (int size = 2; size <= N; size <<= 1) {
+      int j = size >> 1;
+      for (; j > 32; j >>= 1) {
+        for (int q = tid; q < N / 2; q += kThreads) step((q & ~(j - 1)) * 2 + (q & (j - 1)), j, size);
+        __syncthreads();
+      }
+      for (int w = warp * 64; w < N; w += kWarps * 64)
+        for (int d = j; d > 0; d >>= 1) {
+          step(w + (lane & ~(d - 1)) * 2 + (lane & (d - 1)), d, size);
+          __syncwarp();
+        }
+      if (size >= 64) __syncthreads();
+    }
+    __syncthreads();
+  }
+
+  // The first CTA's list of n to the row's token.  all: the weight that p is a share of; 0: of the k kept.
+  __device__ __forceinline__ void finish(int n, const Rules& r, u64 all, const Args& a, int row) {
+    constexpr int kPer = kList / kThreads;
+    const int tid = threadIdx.x;
+    const uint32_t k = min(r.k, (uint32_t)n);
+    const bool sorted = r.p_on || k < (uint32_t)n;
+    if (sorted) sort(n);
+    u64 w[kPer], m = 0, mt;
+    uint32_t at_[kPer], key[kPer], c = 0, ct;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t i = tid * kPer + j;
+      w[j] = 0;
+      at_[j] = i;
+      key[j] = 0;
+      if (i < k) {
+        if (sorted) {
+          at_[j] = (uint32_t)s->order[i];
+          key[j] = ~(uint32_t)(s->order[i] >> 32);
+        } else {
+          key[j] = s->key[i];
+        }
+        w[j] = weigh(value_of<T>(key[j]));
+      }
+      m += w[j];
+    }
+    u64 before = m;
+    scan(c, before, ct, mt);
+    const u64 target = r.p_on ? share_of(all ? all : mt, r.p) : ~0ull;
+    c = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t i = tid * kPer + j;
+      const bool keep = i < k && before < target && value_of<T>(key[j]) >= r.least;
+      before += w[j];
+      c += keep;
+      if (!keep) w[j] = 0;
+    }
+    // (sort keys have been read: scan's barriers lie between)
+    for (int i = tid; i < kList; i += kThreads) s->order[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (w[j]) s->order[at_[j]] = w[j];
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      w[j] = s->order[tid * kPer + j];
+      m += w[j];
+    }
+    uint32_t kept = c;
+    scan(kept, m, ct, mt);
+    draw(m, mt, w, [&](int j, float* v) {
+      *v = value_of<T>(s->key[tid * kPer + j]);
+      return s->id[tid * kPer + j];
+    }, r, a, row);
+    if (tid == 0 && a.kept) a.kept[row] = (int32_t)ct;
+  }
+
+  // The one of a thread's weights (of all threads' sum `total`, `before` of it before the thread's first) that the
+  // draw falls on, if it is here.
+  template <int N, typename Id>
+  __device__ __forceinline__ void draw(u64 before, u64 total, const u64 (&w)[N], Id id_of, const Rules& r, const Args& a, int row) {
+    const u64 target = __umul64hi(total, r.u);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (before <= target && target < before + w[j]) {
+        float v;
+        a.token[row] = id_of(j, &v);
+        if (a.logprob) {
+          const double d = v == heat.mx ? 0.0 : (double)v - (double)heat.mx;
+          a.logprob[row] = (float)(d / (double)r.heat - log((double)total / (double)(1ull << kScale)));
+        }
+      }
+      before += w[j];
+    }
+  }
+
+  // A key that is no larger than the k-th largest of the row's, from the largest of its groups (first CTA).
+  __device__ __forceinline__ uint32_t bound(uint32_t k) {
+    const int tid = threadIdx.x;
+    uint32_t prefix = 0, above = 0;
+    int upto = kKey, shift = kKey - kBits;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+      for (int i = tid; i < kBins; i += kThreads) s->cnt[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < kGroups; i += kThreads) {
+        const uint32_t g = s->group[i];
+        if (g && (level == 0 || g >> upto == prefix)) atomicAdd(&s->cnt[g >> shift & (kBins - 1)], 1u);
+      }
+      __syncthreads();
+      constexpr int kPer = kBins / kThreads;
+      uint32_t c[kPer], cs = 0, ct;
+      u64 m = 0, mt;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) cs += c[j] = s->cnt[kBins - 1 - (tid * kPer + j)];
+      uint32_t cb = cs;
+      scan(cb, m, ct, mt);
+      if (above + ct < k) return 0;          // fewer groups than k hold an id (uniform)
+      cb += above;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (cb < k && k <= cb + c[j]) {
+          s->found.bin = kBins - 1 - (tid * kPer + j);
+          s->found.count = cb;
+        }
+        cb += c[j];
+      }
+      __syncthreads();
+      const int bits = upto - shift;
+      prefix = prefix << bits | (s->found.bin & ((1u << bits) - 1));
+      above = s->found.count;
+      if (shift == 0) break;
+      upto = shift;
+      shift = max(0, shift - kBits);
+      __syncthreads();
+    }
+    return prefix << (kKey == 32 ? 10 : 0);
+  }
 };
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logits, const Args a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
-  constexpr int kKey = sizeof(T) == 2 ? 16 : 32;
+  constexpr int kKey = Row<T>::kKey;
   if (tid < 32) {
     const double t = exp2(tid / 32.0);
     const uint32_t w = (uint32_t)(t * 2147483648.0 + 0.5);
@@ -300,114 +575,218 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
 
   // ---- the row's settings
   float heat = a.r.temperature ? a.r.temperature[row] : 1.0f;
+  const int ask = a.r.top_k ? a.r.top_k[row] : 0;
+  float p = a.r.top_p ? a.r.top_p[row] : 1.0f, mp = a.r.min_p ? a.r.min_p[row] : 0.0f, u = a.u[row];
+  bool bad = isnan(p) || isnan(mp) || !(u >= 0.0f && u < 1.0f);
   if (!(heat >= 0.0f) || isinf(heat)) {
-    if (report) atomicOr(&g_err_sample, ERRBIT_NONFINITE);
+    bad = true;
     heat = 1.0f;
   }
-  const int ask = a.r.top_k ? a.r.top_k[row] : 0;
-  uint32_t k = heat == 0.0f ? 1u : (ask <= 0 ? 0xffffffffu : (uint32_t)ask);
-  float p = a.r.top_p ? a.r.top_p[row] : 1.0f, mp = a.r.min_p ? a.r.min_p[row] : 0.0f, u = a.u[row];
-  if (isnan(p) || isnan(mp) || !(u >= 0.0f && u < 1.0f)) {
-    if (report) atomicOr(&g_err_sample, ERRBIT_NONFINITE);
-    if (isnan(p)) p = 1.0f;
-    if (isnan(mp)) mp = 0.0f;
-    if (!(u >= 0.0f)) u = 0.0f;
-    if (u >= 1.0f) u = 0.99999994f;
-  }
-  const u64 least = mp > 0.0f ? (u64)ceil(fmin((double)mp, 1.0) * (double)(1ull << kScale)) : 0ull;
+  if (bad && report) atomicOr(&g_err_sample, ERRBIT_NONFINITE);
+  if (isnan(p)) p = 1.0f;
+  if (isnan(mp)) mp = 0.0f;
+  if (!(u >= 0.0f)) u = 0.0f;
+  if (u >= 1.0f) u = 0.99999994f;
+  Rules r;
+  r.k = heat == 0.0f ? 1u : (ask <= 0 ? 0xffffffffu : (uint32_t)ask);
+  r.p_on = p < 1.0f && r.k > 1;
+  r.p = p > 0.0f ? (u64)((double)fminf(p, 0.99999994f) * 18446744073709551616.0) : 0ull;
+  r.u = (u64)((double)u * 18446744073709551616.0);
+  r.heat = heat > 0.0f ? heat : 1.0f;
+  const bool grouped = r.k > 1 && r.k <= kSmallK;
 
-  // ---- the largest logit, and how many there are
-  float mx = -INFINITY;
+  // ---- the largest logit, how many there are, and the largest of each group
+  float top[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = -INFINITY;
   uint32_t n = 0;
+  int first = 0x7fffffff;                    // the lowest id of the largest one (k = 1)
   bool nan = false;
   for (int t = warp; t < R.tiles; t += kWarps) {
     float f[8];
-    R.load(t, f);
+    const int id = R.load(t, f);
+    if (r.k == 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      nan |= f[i] != f[i];
-      n += f[i] > -INFINITY;
-      mx = fmaxf(mx, f[i]);
+      for (int i = 0; i < 8; ++i) {
+        if (f[i] > top[0]) {                 // (ids rise from tile to tile and within a lane)
+          top[0] = f[i];
+          first = id + i;
+        }
+        nan |= f[i] != f[i];
+        n += f[i] > -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        nan |= f[i] != f[i];
+        n += f[i] > -INFINITY;
+        top[i] = fmaxf(top[i], f[i]);
+      }
     }
   }
   if (nan) atomicOr(&g_err_sample, ERRBIT_NONFINITE);
+  if (grouped) {
+    // eight groups a thread in a cluster of one, four in one of two, ...: kGroups in all
+    const int per = 8 / R.nc;
+    uint32_t* to = (R.nc > 1 ? at_rank(sh.group, 0) : sh.group) + (R.rank * kThreads + tid) * per;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= per) break;
+      float v = top[i];
+#pragma unroll
+      for (int j = 1; j < 8; ++j)
+        if (i + j * per < 8) v = fmaxf(v, top[i + j * per]);
+      to[i] = v > -INFINITY ? key_of<T>(v) : 0u;
+    }
+  }
+  float mx = fmaxf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), fmaxf(fmaxf(top[4], top[5]), fmaxf(top[6], top[7])));
+  u64 best = r.k == 1 && mx > -INFINITY ? (u64)ordered(mx) << 32 | (uint32_t)~first : 0ull;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const u64 y = __shfl_xor_sync(0xffffffffu, best, o);
+    best = y > best ? y : best;
+  }
   n = __reduce_add_sync(0xffffffffu, n);
   mx = warp_max(mx);
   if (lane == 0) {
     sh.warp_count[warp] = n;
-    sh.warp_mass[warp] = __float_as_uint(mx);
+    sh.warp_mass[warp] = r.k == 1 ? best : (u64)__float_as_uint(mx);
   }
   __syncthreads();
   if (tid < R.nc) {
     n = 0;
+    best = 0;
     for (int w = 0; w < kWarps; ++w) {
       n += sh.warp_count[w];
-      mx = fmaxf(mx, __uint_as_float((uint32_t)sh.warp_mass[w]));
+      if (r.k == 1)
+        best = sh.warp_mass[w] > best ? sh.warp_mass[w] : best;
+      else
+        mx = fmaxf(mx, __uint_as_float((uint32_t)sh.warp_mass[w]));
     }
-    Shared* o = R.nc > 1 ? at_rank(&sh, tid) : &sh;
+    Shared* o = R.at(tid);
     o->part_count[R.rank] = n;
     o->part_max[R.rank] = mx;
+    o->part_mass[R.rank] = best;
   }
   R.meet();
   n = 0;
+  best = 0;
   mx = -INFINITY;
   for (int q = 0; q < R.nc; ++q) {
     n += sh.part_count[q];
     mx = fmaxf(mx, sh.part_max[q]);
+    best = sh.part_mass[q] > best ? sh.part_mass[q] : best;
   }
-  if (n == 0) {                              // nothing above -inf (uniform over the cluster)
+  if (n == 0 || r.k == 1) {                  // (uniform over the cluster, whose memory no one reads any more)
     if (report) {
-      a.token[row] = -1;
-      if (a.logprob) a.logprob[row] = -INFINITY;
-      if (a.kept) a.kept[row] = 0;
+      a.token[row] = n ? (int32_t)~(uint32_t)best : -1;
+      if (a.logprob) a.logprob[row] = n ? 0.0f : -INFINITY;
+      if (a.kept) a.kept[row] = n ? 1 : 0;
     }
-    R.meet();
     return;
   }
-  const double c = 1.4426950408889634 / (double)(heat > 0.0f ? heat : 1.0f);
+  const double c = 1.4426950408889634 / (double)r.heat;
   R.heat = Heat{mx, (float)c, (float)(c - (double)(float)c)};
-  R.meet();                                  // part_count and warp_count are used again
+  r.least = mp > 0.0f ? __double2float_ru((double)mx + (double)r.heat * log(fmin((double)mp, 1.0))) : -INFINITY;
+  if (r.k >= n) r.k = 0xffffffffu;
+  R.meet();                                  // what the CTAs told one another has been read
 
-  // ---- where the order's kept prefix ends: at `border`, of whose equals the first `quota` by id count
-  uint32_t border = 0, quota = 0xffffffffu, ties = 0;
-  if (k == 1) {
-    border = key_of<T>(mx);
-    quota = 1;
-    ties = 2;                                // (perhaps)
-  } else {
-    auto descend = [&](auto mass, uint32_t floor, auto want) {
-      constexpr bool M = decltype(mass)::value;
-      Find f{};
-      uint32_t prefix = 0;
-      int upto = 32, shift = kKey - kBits;
-      u64 target = 0;
-      for (;;) {
-        f = R.template find<M>(shift, upto, prefix, floor, f, [&](u64 all) { return target ? target : target = want(all); });
-        // (bits above the key's are 0; the class index keeps kBits bits, fewer where fewer are left)
-        const int bits = (upto == 32 ? kKey : upto) - shift;
-        prefix = upto == 32 ? f.bin : prefix << bits | (f.bin & ((1u << bits) - 1));
-        if (shift == 0) break;
-        upto = shift;
-        shift = max(0, shift - kBits);
+  // ---- few ids: one CTA finishes
+  if (grouped && r.k < n) {
+    if (R.rank == 0) {
+      const uint32_t b = R.bound(r.k);
+      if (tid < R.nc) R.at(tid)->border = b;
+    }
+    R.meet();
+    const uint32_t b = sh.border;
+    const uint32_t held = R.template gather<false>([&](float, uint32_t key) { return key >= b; }, nullptr);
+    if (held <= kList) {
+      if (R.rank == 0) R.finish(held, r, 0ull, a, row);
+      return;
+    }
+  }
+  if (r.k > n && mp > 0.0f) {
+    u64 all = 0;
+    auto take = [&](float v, uint32_t) { return v >= r.least; };
+    const uint32_t held = r.p_on ? R.template gather<true>(take, &all) : R.template gather<false>(take, nullptr);
+    if (held <= kList) {
+      if (R.rank == 0) R.finish(held, r, all, a, row);
+      return;
+    }
+  }
+
+  // ---- where the order's kept prefix ends: at the key `border`, of whose equals those up to the id `cutoff`
+  uint32_t border = 0, cutoff = 0xffffffffu, quota = 0xffffffffu, ties = 0;
+  // by the key's bits, from the class that f describes (shift < 0: from all ids) down; pick: the ids of that class
+  auto descend = [&](auto mass, Find f, auto pick, auto want) {
+    constexpr bool M = decltype(mass)::value;
+    uint32_t prefix = 0;
+    int upto = 32, shift = kKey - kBits;
+    u64 target = 0;
+    for (;;) {
+      f = R.template find<M>(
+          f,
+          [&](float v, uint32_t key) -> int {
+            return pick(v, key) && (upto == 32 || key >> upto == prefix) ? (int)(key >> shift & (kBins - 1)) : -1;
+          },
+          [&](u64 all) { return target ? target : target = want(all); });
+      const int bits = (upto == 32 ? kKey : upto) - shift;
+      prefix = upto == 32 ? f.bin : prefix << bits | (f.bin & ((1u << bits) - 1));
+      if (shift == 0) break;
+      upto = shift;
+      shift = max(0, shift - kBits);
+    }
+    border = prefix;
+    ties = f.in;
+    // all of the last class are equal
+    quota = M ? (uint32_t)((target - f.mass + f.in_mass / f.in - 1) / (f.in_mass / f.in)) : (uint32_t)(target - f.count);
+  };
+  if (r.k < n) descend(std::false_type{}, Find{}, [](float, uint32_t) { return true; }, [&](u64) { return (u64)r.k; });
+  if (r.p_on) {
+    const uint32_t floor = border;
+    const u64 spare = quota < ties ? (u64)(ties - quota) * R.weigh(value_of<T>(border)) : 0ull;
+    u64 target = 0;
+    const Find f = R.template find<true>(
+        Find{}, [&](float v, uint32_t key) -> int { return key >= floor ? (int)class_of(v, R.heat) : -1; },
+        [&](u64 all) { return target = share_of(all - spare, r.p); });
+    auto in_class = [&](float v, uint32_t key) { return key >= floor && class_of(v, R.heat) == f.bin; };
+    if (f.in <= kList) {
+      R.template gather<false>(in_class, nullptr);
+      if (R.rank == 0) {
+        R.sort(f.in);
+        constexpr int kPer = kList / kThreads;
+        u64 w[kPer], before = 0, mt;
+        uint32_t z = 0, ct;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const uint32_t i = tid * kPer + j;
+          w[j] = i < f.in ? R.weigh(value_of<T>(~(uint32_t)(sh.order[i] >> 32))) : 0ull;
+          before += w[j];
+        }
+        R.scan(z, before, ct, mt);
+        before += f.mass;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          if (before < target && target <= before + w[j]) {
+            const u64 o = sh.order[tid * kPer + j];
+            for (int q = 0; q < R.nc; ++q) {
+              R.at(q)->border = ~(uint32_t)(o >> 32);
+              R.at(q)->cutoff = sh.id[(uint32_t)o];
+            }
+          }
+          before += w[j];
+        }
       }
-      border = prefix;
-      ties = f.in;
-      // all of the last class are equal
-      quota = M ? (uint32_t)((target - f.mass + f.in_mass / f.in - 1) / (f.in_mass / f.in)) : (uint32_t)(target - f.count);
-    };
-    if (k < n) descend(std::false_type{}, 0u, [&](u64) { return (u64)k; });
-    if (p < 1.0f) {
-      const u64 spare = quota < ties ? (u64)(ties - quota) * weight<T>(value_of<T>(border), R.heat, sh.table) : 0ull;
-      const u64 share = p > 0.0f ? (u64)((double)p * 18446744073709551616.0) : 0ull;
-      descend(std::true_type{}, border, [&](u64 all) -> u64 {
-        const u64 of = all - spare, t = __umul64hi(of, share) + (of * share != 0);
-        return t ? t : 1ull;
-      });
+      R.meet();
+      border = sh.border;
+      cutoff = sh.cutoff;
+      quota = ties = 0;
+    } else {
+      descend(std::true_type{}, Find{f.mass, f.count, 0, 0, 0}, in_class, [&](u64) { return target; });
     }
   }
 
   // ---- equals at the border: the id up to which they are kept
-  uint32_t cutoff = 0xffffffffu;
   if (quota < ties) {
     for (int t = warp; t < R.tiles; t += kWarps) {
       float f[8];
@@ -422,7 +801,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     uint32_t mine = 0;
     for (int t = lane; t < R.tiles; t += 32) mine += (uint32_t)sh.tile_mass[t];
     mine = __reduce_add_sync(0xffffffffu, mine);
-    if (tid < R.nc) (R.nc > 1 ? at_rank(&sh, tid) : &sh)->part_count[R.rank] = mine;
+    if (tid < R.nc) R.at(tid)->part_count[R.rank] = mine;
     R.meet();
     uint32_t before = 0;
     for (int q = 0; q < R.rank; ++q) before += sh.part_count[q];
@@ -445,7 +824,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (f[i] > -INFINITY && key_of<T>(f[i]) == border && ++at == quota)
-          for (int q = 0; q < R.nc; ++q) (R.nc > 1 ? at_rank(&sh, q) : &sh)->cutoff = id + i;
+          for (int q = 0; q < R.nc; ++q) R.at(q)->cutoff = id + i;
     }
     R.meet();
     cutoff = sh.cutoff;
@@ -454,8 +833,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
   // ---- the kept weight of every tile
   auto kept_weight = [&](float v, int id) -> u64 {
     const uint32_t key = key_of<T>(v);
-    if (!(v > -INFINITY) || key < border || (key == border && (uint32_t)id > cutoff)) return 0ull;
-    return weight<T>(v, R.heat, sh.table);
+    if (!(v > -INFINITY) || v < r.least || key < border || (key == border && (uint32_t)id > cutoff)) return 0ull;
+    return R.weigh(v);
   };
   uint32_t kept = 0;
   for (int t = warp; t < R.tiles; t += kWarps) {
@@ -465,10 +844,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t key = key_of<T>(f[i]);
-      if (!(f[i] > -INFINITY) || key < border || (key == border && (uint32_t)(id + i) > cutoff)) continue;
-      const u64 w = weight<T>(f[i], R.heat, sh.table);
-      if (w < least) continue;
-      m += w;
+      if (!(f[i] > -INFINITY) || f[i] < r.least || key < border || (key == border && (uint32_t)(id + i) > cutoff)) continue;
+      m += R.weigh(f[i]);
       ++kept;
     }
     m = warp_sum64(m);
@@ -483,7 +860,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
   if (tid < R.nc) {
     kept = 0;
     for (int w = 0; w < kWarps; ++w) kept += sh.warp_count[w];
-    Shared* o = R.nc > 1 ? at_rank(&sh, tid) : &sh;
+    Shared* o = R.at(tid);
     o->part_mass[R.rank] = mine;
     o->part_count[R.rank] = kept;
   }
@@ -496,7 +873,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     kept += sh.part_count[q];
   }
   if (report && a.kept) a.kept[row] = (int32_t)kept;
-  const u64 share = (u64)((double)u * 18446744073709551616.0), target = __umul64hi(total, share);
+  const u64 target = __umul64hi(total, r.u);
   if (warp == 0 && before <= target && target < before + mine) {
     int t = 0;
     u64 run = before;
@@ -505,29 +882,17 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     const int id = R.load(t, f);
     u64 w[8], m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      w[i] = kept_weight(f[i], id + i);
-      if (w[i] < least) w[i] = 0;
-      m += w[i];
-    }
+    for (int i = 0; i < 8; ++i) m += w[i] = kept_weight(f[i], id + i);
     u64 incl = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    u64 at = run + incl - m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (at <= target && target < at + w[i]) {
-        a.token[row] = id + i;
-        if (a.logprob) {
-          const double d = f[i] == mx ? 0.0 : (double)f[i] - (double)mx;
-          a.logprob[row] = (float)(d / (double)(heat > 0.0f ? heat : 1.0f) - log((double)total / (double)(1ull << kScale)));
-        }
-      }
-      at += w[i];
-    }
+    R.draw(run + incl - m, total, w, [&](int j, float* v) {
+      *v = f[j];
+      return id + j;
+    }, r, a, row);
   }
 }
 
