@@ -50,24 +50,21 @@ constexpr int kTile = 256;                   // ids a warp takes at once, eight 
 constexpr int kMaxTiles = 512;               // of a CTA
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kScale = 42;                   // a weight of 1 is 2^42: 2^20 of them stay below 2^63
-constexpr int kPiece = 14;                   // bits of a weight's pieces in a class's sums: 2^17 of them fit 32 bits
 constexpr int kList = 2048;                  // ids that one CTA finishes
 constexpr int kSmallK = 1024;
 constexpr int kGroups = 4096;                // groups whose largest logits bound the k-th: eight a thread at most
 constexpr float kStep = 32.0f;               // classes of an octave of weight
 
-struct Find {           // where the order's prefix ends: in this class, after so much of the classes above it
-  u64 mass;             // weight above it
-  uint32_t count;       // ids above it
-  uint32_t in;          // ids in it
-  u64 in_mass;          // their weight
+struct Find {           // where the order's prefix ends: in this class,
+  u64 above;            // after so many ids (so much weight) of the classes above it,
+  u64 in;               // with so much in it
   uint32_t bin;
 };
 struct Shared {
   union {
     struct {
-      uint32_t cnt[kBins];                   // of this CTA's ids in a class, and the pieces of their weights' sum
-      uint32_t piece[3][kBins];
+      uint32_t cnt[kBins];                   // of this CTA's ids in a class, or
+      u64 sum[kBins];                        // their weights
     };
     struct {
       u64 order[kList];                      // a list's sort keys, then its kept weights
@@ -90,6 +87,8 @@ struct Shared {
   float part_max[kMaxCluster];
   Find found;
   uint32_t cutoff, border;
+  float least;
+  double least_off;      // T ln of the least share
 };
 
 // order of values as order of unsigned integers; bf16 values use the upper half
@@ -110,27 +109,34 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 struct Heat {
   float mx, ch, cl;      // the largest logit; log2(e) / T as two fp32 parts
 };
-// 2^42 exp((v - mx) / T).  y = (v - mx) log2(e) / T comes as two parts, k / 32 nearest to it is taken out
-// exactly, and 2^r - 1 of the rest (at most 1/64) multiplies a table's 2^(k mod 32 / 32).
+// acc + 2^42 exp((v - mx) / T).  y = (v - mx) log2(e) / T comes as two parts, k / 32 nearest to it is taken out
+// exactly, and 2^r - 1 of the rest (at most 1/64) multiplies a table's 2^(k mod 32 / 32): w with 31 bits behind the
+// point.  What lies 2^-42 below the largest weighs nothing.
 template <typename T>
-__device__ __forceinline__ u64 weight(float v, const Heat& h, const uint2* table) {
-  const float d = v - h.mx;
-  float e = 0.f;                             // what the difference lost (of bf16 values: nothing that matters)
+__device__ __forceinline__ u64 add_weight(u64 acc, float v, const Heat& h, const uint2* table) {
+  const float d = v == h.mx ? 0.f : v - h.mx;          // (two infinities have no difference)
+  float lo;                                            // what the product loses, and the difference before it (of
+  const float y = d * h.ch;                            // bf16 values: nothing that matters)
   if (sizeof(T) == 4) {
-    const float b = d - v;
-    e = (v - (d - b)) + (-h.mx - b);
+    const float b = d - v, e = (v - (d - b)) + (-h.mx - b);
+    lo = fmaf(d, h.ch, -y) + fmaf(d, h.cl, e * h.ch);
+  } else {
+    lo = fmaf(d, h.cl, fmaf(d, h.ch, -y));
   }
-  const float y = d * h.ch;
-  const float lo = fmaf(d, h.ch, -y) + fmaf(d, h.cl, e * h.ch);
-  const float kf = fmaf(y, 32.0f, 12582912.0f);
-  const int k = __float_as_int(kf) - 0x4B400000;
-  const float r = fmaf(kf - 12582912.0f, -0.03125f, y) + lo;
+  const float yc = fmaxf(y, -60.0f);                   // (2^-60 is none; a lo that is no number then does not matter)
+  const float kf = fmaf(yc, 32.0f, 12582912.0f);
+  const uint32_t bits = __float_as_uint(kf);           // 0x4B400000 + k
+  const float r = fmaf(kf - 12582912.0f, -0.03125f, yc) + lo;
   // (ln 2)^n / n!
   const float E = r * fmaf(r, fmaf(r, fmaf(r, 9.6181291e-3f, 5.5504109e-2f), 2.4022651e-1f), 6.9314718e-1f);
-  const uint2 t = table[k & 31];
+  const uint2 t = table[bits & 31];
   const uint32_t w = t.x + (uint32_t)__float2int_rn(__uint_as_float(t.y) * E);
-  const u64 full = ((u64)w << (kScale - 31)) >> (-(k >> 5) & 63);
-  return v == h.mx ? 1ull << kScale : (y > -(kScale + 2.0f) ? full : 0ull);
+  const int up = ((int)(bits - 0x4B400000u) >> 5) + (kScale - 31);
+  return acc + (u64)(w >> max(-up, 0)) * (u64)(1u << max(up, 0));
+}
+template <typename T>
+__device__ __forceinline__ u64 weight(float v, const Heat& h, const uint2* table) {
+  return add_weight<T>(0ull, v, h, table);
 }
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -149,6 +155,20 @@ __device__ __forceinline__ V* at_rank(V* p, int rank) {      // the same object 
 __device__ __forceinline__ uint32_t class_of(float v, const Heat& h) {
   const float y = (v == h.mx ? 0.f : v - h.mx) * h.ch;                 // <= 0; -inf for what weighs nothing
   return kBins - 1 - (uint32_t)fminf(-y * kStep, (float)(kBins - 1));
+}
+
+// x in [0, 1) as a fraction of 2^64 (exact from 2^-40 on)
+__device__ __forceinline__ u64 fraction(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const int e = (int)(b >> 23) - 86;                                    // x = m 2^(e - 64)
+  const u64 m = b < 0x00800000u ? 0ull : (b & 0x7fffffu) | 0x800000u;
+  return e >= 0 ? m << e : (e > -24 ? m >> -e : 0ull);
+}
+// log2(e) / T as two fp32 parts (fp64 would do, at a sixtieth of the rate: 4 us for a CTA's threads)
+__device__ __forceinline__ void heat_parts(float T, Heat& h) {
+  const float hi = 1.44269502f, lo = 1.92596303e-8f;                    // log2(e)
+  h.ch = hi / T;
+  h.cl = isinf(h.ch) ? 0.f : (fmaf(-h.ch, T, hi) + lo) / T;
 }
 
 // ceil(a share of `of`), at least 1; the share as a fraction of 2^64
@@ -205,6 +225,7 @@ struct Row {
     return id;
   }
   __device__ __forceinline__ u64 weigh(float v) const { return weight<T>(v, heat, s->table); }
+  __device__ __forceinline__ u64 add(u64 acc, float v) const { return add_weight<T>(acc, v, heat, s->table); }
 
   // This CTA's exclusive sum over its threads, and the sum of all (every thread calls)
   __device__ __forceinline__ void scan(uint32_t& c, u64& m, uint32_t& ct, u64& mt) const {
@@ -241,15 +262,17 @@ struct Row {
     m = mi - m;
   }
 
-  // Counts (and weights) of the ids' classes cls(value, key), -1: none.  Then, in falling order of classes, the
+  // Counts (or weights) of the ids' classes cls(value, key), -1: none.  Then, in falling order of classes, the
   // one in which the running count (weight) reaches the target behind what lies above all of them;
-  // want(weight of all) gives the target.
+  // want(all of it) gives the target.
   template <bool MASS, typename Cls, typename Want>
-  __device__ __forceinline__ Find find(Find above, Cls cls, Want want) {
+  __device__ __forceinline__ Find find(u64 above, Cls cls, Want want) {
     const int tid = threadIdx.x, warp = tid >> 5;
     for (int i = tid; i < kBins; i += kThreads) {
-      s->cnt[i] = 0;
-      if (MASS) s->piece[0][i] = s->piece[1][i] = s->piece[2][i] = 0;
+      if (MASS)
+        s->sum[i] = 0;
+      else
+        s->cnt[i] = 0;
     }
     __syncthreads();
     for (int t = warp; t < tiles; t += kWarps) {
@@ -260,68 +283,46 @@ struct Row {
         if (!(f[i] > -INFINITY)) continue;
         const int b = cls(f[i], key_of<T>(f[i]));
         if (b < 0) continue;
-        atomicAdd(&s->cnt[b], 1u);
-        if (MASS) {
-          const u64 w = weigh(f[i]);
-          const uint32_t p0 = (uint32_t)w & ((1u << kPiece) - 1), p1 = (uint32_t)(w >> kPiece) & ((1u << kPiece) - 1),
-                         p2 = (uint32_t)(w >> 2 * kPiece);
-          if (p0) atomicAdd(&s->piece[0][b], p0);
-          if (p1) atomicAdd(&s->piece[1][b], p1);
-          if (p2) atomicAdd(&s->piece[2][b], p2);
-        }
+        if (MASS)
+          atomicAdd(&s->sum[b], weigh(f[i]));
+        else
+          atomicAdd(&s->cnt[b], 1u);
       }
     }
     meet();
     // this CTA's share of the classes, in falling order; a thread holds up to four neighbours
     constexpr int kPer = kBins / kThreads;
     const int share = kBins / nc, per = share > kThreads ? share / kThreads : 1;
-    uint32_t c[kPer], cs = 0, ct;
     u64 m[kPer], ms = 0, mt;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      c[j] = 0;
       m[j] = 0;
       const int i = tid * per + j;
       if (j < per && i < share) {
         const int b = kBins - 1 - (rank * share + i);
-        for (int q = 0; q < nc; ++q) {
-          const Shared* o = at(q);
-          c[j] += o->cnt[b];
-          if (MASS)
-            m[j] += (u64)o->piece[0][b] + ((u64)o->piece[1][b] << kPiece) + ((u64)o->piece[2][b] << 2 * kPiece);
-        }
+        for (int q = 0; q < nc; ++q) m[j] += MASS ? at(q)->sum[b] : (u64)at(q)->cnt[b];
       }
-      cs += c[j];
       ms += m[j];
     }
-    uint32_t cb = cs;
     u64 mb = ms;
-    scan(cb, mb, ct, mt);
-    if (tid < nc) {
-      at(tid)->part_count[rank] = ct;
-      at(tid)->part_mass[rank] = mt;
-    }
+    uint32_t none = 0, nt;
+    scan(none, mb, nt, mt);
+    if (tid < nc) at(tid)->part_mass[rank] = mt;
     meet();
     // what lies above this thread's classes
     u64 all = 0;
-    cb += above.count;
-    mb += above.mass;
+    mb += above;
     for (int q = 0; q < nc; ++q) {
       all += s->part_mass[q];
-      if (q < rank) {
-        cb += s->part_count[q];
-        mb += s->part_mass[q];
-      }
+      if (q < rank) mb += s->part_mass[q];
     }
     const u64 target = want(all);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const u64 before = MASS ? mb : cb, behind = MASS ? mb + m[j] : cb + c[j];
-      if (before < target && target <= behind) {
-        const Find r{mb, cb, c[j], m[j], (uint32_t)(kBins - 1 - (rank * share + tid * per + j))};
+      if (mb < target && target <= mb + m[j]) {
+        const Find r{mb, m[j], (uint32_t)(kBins - 1 - (rank * share + tid * per + j))};
         for (int q = 0; q < nc; ++q) at(q)->found = r;
       }
-      cb += c[j];
       mb += m[j];
     }
     meet();
@@ -343,7 +344,7 @@ struct Row {
       for (int i = 0; i < 8; ++i) {
         if (!(f[i] > -INFINITY)) continue;
         n += take(f[i], key_of<T>(f[i]));
-        if (MASS) m += weigh(f[i]);
+        if (MASS) m = add(m, f[i]);
       }
     }
     uint32_t ct;
@@ -531,14 +532,14 @@ struct Row {
       for (int j = 0; j < kPer; ++j) {
         if (cb < k && k <= cb + c[j]) {
           s->found.bin = kBins - 1 - (tid * kPer + j);
-          s->found.count = cb;
+          s->found.above = cb;
         }
         cb += c[j];
       }
       __syncthreads();
       const int bits = upto - shift;
       prefix = prefix << bits | (s->found.bin & ((1u << bits) - 1));
-      above = s->found.count;
+      above = (uint32_t)s->found.above;
       if (shift == 0) break;
       upto = shift;
       shift = max(0, shift - kBits);
@@ -549,7 +550,7 @@ struct Row {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logits, const Args a) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ logits, const Args a) {
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
   constexpr int kKey = Row<T>::kKey;
@@ -590,10 +591,11 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
   Rules r;
   r.k = heat == 0.0f ? 1u : (ask <= 0 ? 0xffffffffu : (uint32_t)ask);
   r.p_on = p < 1.0f && r.k > 1;
-  r.p = p > 0.0f ? (u64)((double)fminf(p, 0.99999994f) * 18446744073709551616.0) : 0ull;
-  r.u = (u64)((double)u * 18446744073709551616.0);
+  r.p = fraction(fminf(fmaxf(p, 0.0f), 0.99999994f));
+  r.u = fraction(u);
   r.heat = heat > 0.0f ? heat : 1.0f;
   const bool grouped = r.k > 1 && r.k <= kSmallK;
+  if (mp > 0.0f && tid == kThreads - 32) sh.least_off = (double)r.heat * log(fmin((double)mp, 1.0));
 
   // ---- the largest logit, how many there are, and the largest of each group
   float top[8];
@@ -685,11 +687,12 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     }
     return;
   }
-  const double c = 1.4426950408889634 / (double)r.heat;
-  R.heat = Heat{mx, (float)c, (float)(c - (double)(float)c)};
-  r.least = mp > 0.0f ? __double2float_ru((double)mx + (double)r.heat * log(fmin((double)mp, 1.0))) : -INFINITY;
+  R.heat.mx = mx;
+  heat_parts(r.heat, R.heat);
+  if (tid == 0) sh.least = mp > 0.0f ? __double2float_ru((double)mx + sh.least_off) : -INFINITY;
   if (r.k >= n) r.k = 0xffffffffu;
   R.meet();                                  // what the CTAs told one another has been read
+  r.least = sh.least;
 
   // ---- few ids: one CTA finishes
   if (grouped && r.k < n) {
@@ -717,15 +720,16 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
 
   // ---- where the order's kept prefix ends: at the key `border`, of whose equals those up to the id `cutoff`
   uint32_t border = 0, cutoff = 0xffffffffu, quota = 0xffffffffu, ties = 0;
-  // by the key's bits, from the class that f describes (shift < 0: from all ids) down; pick: the ids of that class
-  auto descend = [&](auto mass, Find f, auto pick, auto want) {
+  // by the key's bits, of the ids that pick takes, with `above` before them
+  auto descend = [&](auto mass, u64 above, auto pick, auto want) {
     constexpr bool M = decltype(mass)::value;
+    Find f{above, 0, 0};
     uint32_t prefix = 0;
     int upto = 32, shift = kKey - kBits;
     u64 target = 0;
     for (;;) {
       f = R.template find<M>(
-          f,
+          f.above,
           [&](float v, uint32_t key) -> int {
             return pick(v, key) && (upto == 32 || key >> upto == prefix) ? (int)(key >> shift & (kBins - 1)) : -1;
           },
@@ -737,34 +741,34 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
       shift = max(0, shift - kBits);
     }
     border = prefix;
-    ties = f.in;
-    // all of the last class are equal
-    quota = M ? (uint32_t)((target - f.mass + f.in_mass / f.in - 1) / (f.in_mass / f.in)) : (uint32_t)(target - f.count);
+    const u64 each = M ? R.weigh(value_of<T>(border)) : 1ull;            // all of the last class are equal
+    ties = (uint32_t)(f.in / each);
+    quota = (uint32_t)((target - f.above + each - 1) / each);
   };
-  if (r.k < n) descend(std::false_type{}, Find{}, [](float, uint32_t) { return true; }, [&](u64) { return (u64)r.k; });
+  if (r.k < n) descend(std::false_type{}, 0ull, [](float, uint32_t) { return true; }, [&](u64) { return (u64)r.k; });
   if (r.p_on) {
     const uint32_t floor = border;
     const u64 spare = quota < ties ? (u64)(ties - quota) * R.weigh(value_of<T>(border)) : 0ull;
     u64 target = 0;
     const Find f = R.template find<true>(
-        Find{}, [&](float v, uint32_t key) -> int { return key >= floor ? (int)class_of(v, R.heat) : -1; },
+        0ull, [&](float v, uint32_t key) -> int { return key >= floor ? (int)class_of(v, R.heat) : -1; },
         [&](u64 all) { return target = share_of(all - spare, r.p); });
     auto in_class = [&](float v, uint32_t key) { return key >= floor && class_of(v, R.heat) == f.bin; };
-    if (f.in <= kList) {
-      R.template gather<false>(in_class, nullptr);
+    const uint32_t held = R.template gather<false>(in_class, nullptr);
+    if (held <= kList) {
       if (R.rank == 0) {
-        R.sort(f.in);
+        R.sort(held);
         constexpr int kPer = kList / kThreads;
         u64 w[kPer], before = 0, mt;
         uint32_t z = 0, ct;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const uint32_t i = tid * kPer + j;
-          w[j] = i < f.in ? R.weigh(value_of<T>(~(uint32_t)(sh.order[i] >> 32))) : 0ull;
+          w[j] = i < held ? R.weigh(value_of<T>(~(uint32_t)(sh.order[i] >> 32))) : 0ull;
           before += w[j];
         }
         R.scan(z, before, ct, mt);
-        before += f.mass;
+        before += f.above;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           if (before < target && target <= before + w[j]) {
@@ -782,7 +786,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
       cutoff = sh.cutoff;
       quota = ties = 0;
     } else {
-      descend(std::true_type{}, Find{f.mass, f.count, 0, 0, 0}, in_class, [&](u64) { return target; });
+      descend(std::true_type{}, f.above, in_class, [&](u64) { return target; });
     }
   }
 
@@ -830,12 +834,13 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     cutoff = sh.cutoff;
   }
 
-  // ---- the kept weight of every tile
-  auto kept_weight = [&](float v, int id) -> u64 {
-    const uint32_t key = key_of<T>(v);
-    if (!(v > -INFINITY) || v < r.least || key < border || (key == border && (uint32_t)id > cutoff)) return 0ull;
-    return R.weigh(v);
-  };
+  // ---- the kept weight of every tile: of the logits above `low`, and of those equal to it up to the id `upto`
+  float low = border ? value_of<T>(border) : -INFINITY;
+  int upto = border ? (int)min(cutoff, 0x7fffffffu) : -1;
+  if (r.least > low) {
+    low = r.least;
+    upto = 0x7fffffff;
+  }
   uint32_t kept = 0;
   for (int t = warp; t < R.tiles; t += kWarps) {
     float f[8];
@@ -843,10 +848,10 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
     u64 m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t key = key_of<T>(f[i]);
-      if (!(f[i] > -INFINITY) || f[i] < r.least || key < border || (key == border && (uint32_t)(id + i) > cutoff)) continue;
-      m += R.weigh(f[i]);
-      ++kept;
+      if (f[i] > low || (f[i] == low && id + i <= upto)) {
+        m = R.add(m, f[i]);
+        ++kept;
+      }
     }
     m = warp_sum64(m);
     if (lane == 0) sh.tile_mass[t] = m;
@@ -875,14 +880,31 @@ __global__ void __launch_bounds__(kThreads) k_sample(const T* __restrict__ logit
   if (report && a.kept) a.kept[row] = (int32_t)kept;
   const u64 target = __umul64hi(total, r.u);
   if (warp == 0 && before <= target && target < before + mine) {
+    // the first tile whose end lies beyond the draw, 32 at a time
     int t = 0;
     u64 run = before;
-    for (; run + sh.tile_mass[t] <= target; ++t) run += sh.tile_mass[t];
+    for (int t0 = 0;; t0 += 32) {
+      const u64 w = t0 + lane < R.tiles ? sh.tile_mass[t0 + lane] : 0ull;
+      u64 incl = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, target < run + incl);
+      if (hit || t0 + 32 >= R.tiles) {
+        const int who = hit ? __ffs(hit) - 1 : 0;
+        t = t0 + who;
+        run += __shfl_sync(0xffffffffu, incl - w, who);
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
     float f[8];
     const int id = R.load(t, f);
     u64 w[8], m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m += w[i] = kept_weight(f[i], id + i);
+    for (int i = 0; i < 8; ++i) m += w[i] = f[i] > low || (f[i] == low && id + i <= upto) ? R.weigh(f[i]) : 0ull;
     u64 incl = m;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -921,8 +943,9 @@ cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, con
   g_used_sample = true;
   Args a{token, logprob, kept, u, r, vocab, 0, vocab % 8 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0};
   const int tiles = (vocab + kTile - 1) / kTile;
+  // as many CTAs as run at once (two an SM), a tile for every warp
   int nc = kMaxCluster;
-  while (nc > 1 && tiles <= nc / 2 * kMaxTiles && ((int64_t)nc * n_rows > 608 || tiles < nc * kWarps)) nc /= 2;
+  while (nc > 1 && tiles <= nc / 2 * kMaxTiles && ((int64_t)nc * n_rows > 304 || tiles < nc / 2 * kWarps)) nc /= 2;
   a.tpc = (tiles + nc - 1) / nc;
   return dt == DT_BF16 ? launch_t<bf16>(logits, n_rows, a, nc, s) : launch_t<float>(logits, n_rows, a, nc, s);
 }
