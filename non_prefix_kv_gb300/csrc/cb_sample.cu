@@ -53,7 +53,6 @@ constexpr int kScale = 42;                   // a weight of 1 is 2^42: 2^20 of t
 constexpr int kList = 2048;                  // ids that one CTA finishes
 constexpr int kSmallK = 1024;
 constexpr int kGroups = 4096;                // groups whose largest logits bound the k-th: eight a thread at most
-constexpr float kStep = 32.0f;               // classes of an octave of weight
 
 struct Find {           // where the order's prefix ends: in this class,
   u64 above;            // after so many ids (so much weight) of the classes above it,
@@ -64,7 +63,10 @@ struct Shared {
   union {
     struct {
       uint32_t cnt[kBins];                   // of this CTA's ids in a class, or
-      u64 sum[kBins];                        // their weights
+      union {
+        u64 sum[kBins];                      // their weights, or
+        uint32_t part[2][kBins];             // (beside the counts) the parts of these above their class's base
+      };
     };
     struct {
       u64 order[kList];                      // a list's sort keys, then its kept weights
@@ -112,8 +114,14 @@ struct Heat {
 // acc + 2^42 exp((v - mx) / T).  y = (v - mx) log2(e) / T comes as two parts, k / 32 nearest to it is taken out
 // exactly, and 2^r - 1 of the rest (at most 1/64) multiplies a table's 2^(k mod 32 / 32): w with 31 bits behind the
 // point.  What lies 2^-42 below the largest weighs nothing.
+__device__ __forceinline__ uint32_t shift_right(uint32_t x, int n) {      // n from 0 on; 32 and more give 0
+  uint32_t y;
+  asm("shr.u32 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(n));
+  return y;
+}
+// w = 2^(k mod 32 / 32) 2^r with 31 bits behind the point, and 0x4B400000 + k
 template <typename T>
-__device__ __forceinline__ u64 add_weight(u64 acc, float v, const Heat& h, const uint2* table) {
+__device__ __forceinline__ uint32_t mantissa(float v, const Heat& h, const uint2* table, uint32_t& bits) {
   const float d = v == h.mx ? 0.f : v - h.mx;          // (two infinities have no difference)
   float lo;                                            // what the product loses, and the difference before it (of
   const float y = d * h.ch;                            // bf16 values: nothing that matters)
@@ -125,18 +133,68 @@ __device__ __forceinline__ u64 add_weight(u64 acc, float v, const Heat& h, const
   }
   const float yc = fmaxf(y, -60.0f);                   // (2^-60 is none; a lo that is no number then does not matter)
   const float kf = fmaf(yc, 32.0f, 12582912.0f);
-  const uint32_t bits = __float_as_uint(kf);           // 0x4B400000 + k
+  bits = __float_as_uint(kf);
   const float r = fmaf(kf - 12582912.0f, -0.03125f, yc) + lo;
   // (ln 2)^n / n!
   const float E = r * fmaf(r, fmaf(r, fmaf(r, 9.6181291e-3f, 5.5504109e-2f), 2.4022651e-1f), 6.9314718e-1f);
   const uint2 t = table[bits & 31];
-  const uint32_t w = t.x + (uint32_t)__float2int_rn(__uint_as_float(t.y) * E);
-  const int up = ((int)(bits - 0x4B400000u) >> 5) + (kScale - 31);
-  return acc + (u64)(w >> max(-up, 0)) * (u64)(1u << max(up, 0));
+  return t.x + (uint32_t)__float2int_rn(__uint_as_float(t.y) * E);
+}
+// how far w is shifted up (down) to the scale of the sums
+__device__ __forceinline__ int shift_of(uint32_t bits) { return ((int)(bits - 0x4B400000u) >> 5) + (kScale - 31); }
+template <typename T>
+__device__ __forceinline__ u64 add_weight(u64 acc, float v, const Heat& h, const uint2* table) {
+  uint32_t bits;
+  const uint32_t w = mantissa<T>(v, h, table, bits);
+  const int up = shift_of(bits);
+  return acc + (u64)shift_right(w, max(-up, 0)) * (u64)(1u << max(up, 0));
 }
 template <typename T>
 __device__ __forceinline__ u64 weight(float v, const Heat& h, const uint2* table) {
   return add_weight<T>(0ull, v, h, table);
+}
+// The class of a logit by its k, larger for a larger one: 32 to an octave of weight.  In a class all w have one
+// shift and lie between t - t / 64 (t the table's) and 2^27 more: see find().
+__device__ __forceinline__ uint32_t class_at(uint32_t bits) { return kBins - 1 + (bits - 0x4B400000u); }
+__device__ __forceinline__ uint32_t class_of(float v, const Heat& h) {
+  const float d = v == h.mx ? 0.f : v - h.mx;
+  return class_at(__float_as_uint(fmaf(fmaxf(d * h.ch, -60.0f), 32.0f, 12582912.0f)));
+}
+__device__ __forceinline__ uint32_t class_base(uint32_t bits, const uint2* table) {
+  const uint32_t t = table[bits & 31].x;
+  return shift_right(t - (t >> 6), max(-shift_of(bits), 0));
+}
+
+// ln(exp((v - mx) / T) / total), total in units of 2^-42, rounded about once: q = (v - mx) / T and e ln 2 as two
+// parts, ln m of total = m 2^e as logf's value and what exp of that is off by.  (In fp64 the one thread that does
+// this took a microsecond.)
+__device__ __forceinline__ float log_share(float v, const Heat& h, float T, u64 total, const uint2* table) {
+  float d = 0.f, dl = 0.f;
+  if (v != h.mx) {
+    d = v - h.mx;
+    const float b = d - v;
+    dl = (v - (d - b)) + (-h.mx - b);
+  }
+  const float q = d / T, ql = (fmaf(-q, T, d) + dl) / T;
+  const int z = __clzll((long long)total), e = 63 - z - kScale;
+  const u64 m = total << z;                                            // m / 2^63 in [1, 2)
+  const float mf = (float)(uint32_t)(m >> 40) * 1.1920929e-7f, y = logf(mf);
+  // 2^x, x = -y log2(e), as above: w 2^(k >> 5)
+  const float x = -y * 1.44269502f, xl = fmaf(-y, 1.44269502f, -x) - y * 1.92596303e-8f;
+  const float kf = fmaf(x, 32.0f, 12582912.0f);
+  const uint32_t bits = __float_as_uint(kf);
+  const float r = fmaf(kf - 12582912.0f, -0.03125f, x) + xl;
+  const float E = r * fmaf(r, fmaf(r, fmaf(r, 9.6181291e-3f, 5.5504109e-2f), 2.4022651e-1f), 6.9314718e-1f);
+  const uint2 t = table[bits & 31];
+  const uint32_t w = t.x + (uint32_t)__float2int_rn(__uint_as_float(t.y) * E);
+  // m w 2^(k >> 5) is near 1 (2^62 as the upper half of the product counts, k >> 5 is 0 or -1): what it is off by
+  const u64 one = __umul64hi(m, (u64)w << 32) >> -((int)(bits - 0x4B400000u) >> 5);
+  const float off = (float)(int64_t)(one - (1ull << 62)) * 2.16840434e-19f;
+  const float eh = (float)e * 0.693145752f, el = (float)e * 1.42860677e-6f;    // ln 2: 16 bits, and the rest
+  // -(q + ql) + eh + el + y + off, all of one sign but the small ones
+  const float s1 = eh - q, b1 = s1 - eh, e1 = (eh - (s1 - b1)) + (-q - b1);
+  const float s2 = s1 + y, b2 = s2 - s1, e2 = (s1 - (s2 - b2)) + (y - b2);
+  return -(s2 + (e1 + e2 + el - ql + off));
 }
 
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
@@ -149,12 +207,6 @@ __device__ __forceinline__ V* at_rank(V* p, int rank) {      // the same object 
   u64 a;
   asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<u64>(p)), "r"(rank));
   return reinterpret_cast<V*>(a);
-}
-
-// 2^x of a class: the class of a logit, larger for a larger one
-__device__ __forceinline__ uint32_t class_of(float v, const Heat& h) {
-  const float y = (v == h.mx ? 0.f : v - h.mx) * h.ch;                 // <= 0; -inf for what weighs nothing
-  return kBins - 1 - (uint32_t)fminf(-y * kStep, (float)(kBins - 1));
 }
 
 // x in [0, 1) as a fraction of 2^64 (exact from 2^-40 on)
@@ -224,6 +276,38 @@ struct Row {
     }
     return id;
   }
+  // fn(first id of the lane's eight, the eight, tile) for tiles t0, t0 + step, ... below t1, four loads in flight
+  template <typename Fn>
+  __device__ __forceinline__ void each(int t0, int t1, int step, Fn fn) const {
+    constexpr int U = sizeof(T) == 2 ? 4 : 2, Q = sizeof(T) / 2;
+    const int lane = threadIdx.x & 31;
+    for (int t = t0; t < t1; t += U * step) {
+      uint4 raw[U][Q];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int tt = t + u * step, id = (tile0 + tt) * kTile + lane * 8;
+        if (vec && tt < t1 && id + 8 <= vocab)
+#pragma unroll
+          for (int q = 0; q < Q; ++q) raw[u][q] = reinterpret_cast<const uint4*>(x + id)[q];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int tt = t + u * step, id = (tile0 + tt) * kTile + lane * 8;
+        if (tt >= t1) break;
+        float f[8];
+        if (vec && id + 8 <= vocab) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(raw[u]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            f[i] = Q == 2 ? __uint_as_float(w[i]) : __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = id + i < vocab ? to_f(x[id + i]) : -INFINITY;
+        }
+        fn(id, f, tt);
+      }
+    }
+  }
   __device__ __forceinline__ u64 weigh(float v) const { return weight<T>(v, heat, s->table); }
   __device__ __forceinline__ u64 add(u64 acc, float v) const { return add_weight<T>(acc, v, heat, s->table); }
 
@@ -262,33 +346,38 @@ struct Row {
     m = mi - m;
   }
 
-  // Counts (or weights) of the ids' classes cls(value, key), -1: none.  Then, in falling order of classes, the
-  // one in which the running count (weight) reaches the target behind what lies above all of them;
-  // want(all of it) gives the target.
-  template <bool MASS, typename Cls, typename Want>
+  // The ids' classes cls(value, key), -1: none, and in them counts (KIND 0), sums of weights (1), or sums of weights
+  // in the classes of class_of (2).  Then, in falling order of classes, the one in which the running count (weight)
+  // reaches the target behind what lies `above` all of them; want(all of it) gives the target.
+  //
+  // 64-bit sums are slow atomics (37 cycles a warp); in the classes of KIND 2, whose weights have one shift and
+  // differ by less than 2^27 units, a count and two 32-bit sums of parts of 13 and 14 bits do (2^17 ids a CTA).
+  template <int KIND, typename Cls, typename Want>
   __device__ __forceinline__ Find find(u64 above, Cls cls, Want want) {
     const int tid = threadIdx.x, warp = tid >> 5;
     for (int i = tid; i < kBins; i += kThreads) {
-      if (MASS)
-        s->sum[i] = 0;
-      else
-        s->cnt[i] = 0;
+      if (KIND != 1) s->cnt[i] = 0;
+      if (KIND != 0) s->sum[i] = 0;
     }
     __syncthreads();
-    for (int t = warp; t < tiles; t += kWarps) {
-      float f[8];
-      load(t, f);
+    each(warp, tiles, kWarps, [&](int, const float* f, int) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (!(f[i] > -INFINITY)) continue;
         const int b = cls(f[i], key_of<T>(f[i]));
         if (b < 0) continue;
-        if (MASS)
-          atomicAdd(&s->sum[b], weigh(f[i]));
-        else
-          atomicAdd(&s->cnt[b], 1u);
+        if (KIND == 0) atomicAdd(&s->cnt[b], 1u);
+        if (KIND == 1) atomicAdd(&s->sum[b], weigh(f[i]));
+        if (KIND == 2) {
+          uint32_t bits;
+          const uint32_t w = mantissa<T>(f[i], heat, s->table, bits);
+          const uint32_t u = shift_right(w, max(-shift_of(bits), 0)) - class_base(bits, s->table), c = class_at(bits);
+          atomicAdd(&s->cnt[c], 1u);
+          atomicAdd(&s->part[0][c], u & 0x1fffu);
+          atomicAdd(&s->part[1][c], u >> 13);
+        }
       }
-    }
+    });
     meet();
     // this CTA's share of the classes, in falling order; a thread holds up to four neighbours
     constexpr int kPer = kBins / kThreads;
@@ -300,7 +389,18 @@ struct Row {
       const int i = tid * per + j;
       if (j < per && i < share) {
         const int b = kBins - 1 - (rank * share + i);
-        for (int q = 0; q < nc; ++q) m[j] += MASS ? at(q)->sum[b] : (u64)at(q)->cnt[b];
+        u64 c = 0;
+        for (int q = 0; q < nc; ++q) {
+          const Shared* o = at(q);
+          if (KIND != 1) c += o->cnt[b];
+          if (KIND == 1) m[j] += o->sum[b];
+          if (KIND == 2) m[j] += (u64)o->part[0][b] + ((u64)o->part[1][b] << 13);
+        }
+        if (KIND == 0) m[j] = c;
+        if (KIND == 2) {
+          const uint32_t bits = 0x4B400000u + (uint32_t)(b - (kBins - 1));
+          m[j] = c ? (m[j] + c * class_base(bits, s->table)) << max(shift_of(bits), 0) : 0ull;
+        }
       }
       ms += m[j];
     }
@@ -329,24 +429,21 @@ struct Row {
     return s->found;
   }
 
-  // The ids with take(value, key), in order, to the first CTA's list, if there are kList at most; how many
-  // (the same in all CTAs), and the weight of all ids of the row where it is asked for.
+  // The ids with take(value) (false for -inf), in order, to the first CTA's list, if there are kList at most; how
+  // many (the same in all CTAs), and the weight of all ids of the row where it is asked for.
   template <bool MASS, typename Take>
   __device__ __forceinline__ uint32_t gather(Take take, u64* weight_of_all) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tpw = (tiles + kWarps - 1) / kWarps, t0 = warp * tpw, t1 = min(tiles, t0 + tpw);
     uint32_t n = 0;
     u64 m = 0;
-    for (int t = t0; t < t1; ++t) {
-      float f[8];
-      load(t, f);
+    each(t0, t1, 1, [&](int, const float* f, int) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (!(f[i] > -INFINITY)) continue;
-        n += take(f[i], key_of<T>(f[i]));
-        if (MASS) m = add(m, f[i]);
+        n += take(f[i]);
+        if (MASS && f[i] > -INFINITY) m = add(m, f[i]);
       }
-    }
+    });
     uint32_t ct;
     u64 mt;
     scan(n, m, ct, mt);
@@ -367,29 +464,28 @@ struct Row {
       Shared* o = at(0);
       // (the warp's first lane has the sum of the warps before it)
       base += __shfl_sync(0xffffffffu, n, 0);
-      for (int t = t0; t < t1; ++t) {
-        float f[8];
-        const int id = load(t, f);
+      each(t0, t1, 1, [&](int id, const float* f, int) {
         uint32_t c = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) c += f[i] > -INFINITY && take(f[i], key_of<T>(f[i]));
+        for (int i = 0; i < 8; ++i) c += take(f[i]);
+        if (!__any_sync(0xffffffffu, c)) return;
         uint32_t incl = c;
-        if (__any_sync(0xffffffffu, c)) {
 #pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-          }
-          uint32_t to = base + incl - c;
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += y;
+        }
+        uint32_t to = base + incl - c;
+        if (c) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (f[i] > -INFINITY && take(f[i], key_of<T>(f[i]))) {
+            if (take(f[i])) {
               o->key[to] = key_of<T>(f[i]);
               o->id[to++] = id + i;
             }
-          base += __shfl_sync(0xffffffffu, incl, 31);
         }
-      }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      });
     }
     meet();
     return total;
@@ -496,10 +592,7 @@ struct Row {
       if (before <= target && target < before + w[j]) {
         float v;
         a.token[row] = id_of(j, &v);
-        if (a.logprob) {
-          const double d = v == heat.mx ? 0.0 : (double)v - (double)heat.mx;
-          a.logprob[row] = (float)(d / (double)r.heat - log((double)total / (double)(1ull << kScale)));
-        }
+        if (a.logprob) a.logprob[row] = log_share(v, heat, r.heat, total, s->table);
       }
       before += w[j];
     }
@@ -533,6 +626,7 @@ struct Row {
         if (cb < k && k <= cb + c[j]) {
           s->found.bin = kBins - 1 - (tid * kPer + j);
           s->found.above = cb;
+          s->found.in = c[j];
         }
         cb += c[j];
       }
@@ -540,12 +634,13 @@ struct Row {
       const int bits = upto - shift;
       prefix = prefix << bits | (s->found.bin & ((1u << bits) - 1));
       above = (uint32_t)s->found.above;
-      if (shift == 0) break;
+      // (a class's lower end will do if not many more than k groups reach it)
+      if (shift == 0 || above + (uint32_t)s->found.in <= max(256u, k + k / 4)) return prefix << shift;
       upto = shift;
       shift = max(0, shift - kBits);
       __syncthreads();
     }
-    return prefix << (kKey == 32 ? 10 : 0);
+    return prefix << (kKey == 32 ? 10 : 0);      // after two levels
   }
 };
 
@@ -604,10 +699,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
   uint32_t n = 0;
   int first = 0x7fffffff;                    // the lowest id of the largest one (k = 1)
   bool nan = false;
-  for (int t = warp; t < R.tiles; t += kWarps) {
-    float f[8];
-    const int id = R.load(t, f);
-    if (r.k == 1) {
+  if (r.k == 1) {
+    R.each(warp, R.tiles, kWarps, [&](int id, const float* f, int) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (f[i] > top[0]) {                 // (ids rise from tile to tile and within a lane)
@@ -615,16 +708,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
           first = id + i;
         }
         nan |= f[i] != f[i];
-        n += f[i] > -INFINITY;
       }
-    } else {
+    });
+    n = top[0] > -INFINITY;                  // (only whether there is one)
+  } else {
+    R.each(warp, R.tiles, kWarps, [&](int, const float* f, int) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         nan |= f[i] != f[i];
         n += f[i] > -INFINITY;
         top[i] = fmaxf(top[i], f[i]);
       }
-    }
+    });
   }
   if (nan) atomicOr(&g_err_sample, ERRBIT_NONFINITE);
   if (grouped) {
@@ -701,8 +796,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
       if (tid < R.nc) R.at(tid)->border = b;
     }
     R.meet();
-    const uint32_t b = sh.border;
-    const uint32_t held = R.template gather<false>([&](float, uint32_t key) { return key >= b; }, nullptr);
+    const float b = fmaxf(value_of<T>(sh.border), -3.40282347e38f);      // (key 0: all)
+    const uint32_t held = R.template gather<false>([&](float v) { return v >= b; }, nullptr);
     if (held <= kList) {
       if (R.rank == 0) R.finish(held, r, 0ull, a, row);
       return;
@@ -710,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
   }
   if (r.k > n && mp > 0.0f) {
     u64 all = 0;
-    auto take = [&](float v, uint32_t) { return v >= r.least; };
+    auto take = [&](float v) { return v >= r.least && v > -INFINITY; };
     const uint32_t held = r.p_on ? R.template gather<true>(take, &all) : R.template gather<false>(take, nullptr);
     if (held <= kList) {
       if (R.rank == 0) R.finish(held, r, all, a, row);
@@ -721,14 +816,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
   // ---- where the order's kept prefix ends: at the key `border`, of whose equals those up to the id `cutoff`
   uint32_t border = 0, cutoff = 0xffffffffu, quota = 0xffffffffu, ties = 0;
   // by the key's bits, of the ids that pick takes, with `above` before them
-  auto descend = [&](auto mass, u64 above, auto pick, auto want) {
-    constexpr bool M = decltype(mass)::value;
+  auto descend = [&](auto kind, u64 above, auto pick, auto want) {
+    constexpr bool M = decltype(kind)::value;
     Find f{above, 0, 0};
     uint32_t prefix = 0;
     int upto = 32, shift = kKey - kBits;
     u64 target = 0;
     for (;;) {
-      f = R.template find<M>(
+      f = R.template find<M ? 1 : 0>(
           f.above,
           [&](float v, uint32_t key) -> int {
             return pick(v, key) && (upto == 32 || key >> upto == prefix) ? (int)(key >> shift & (kBins - 1)) : -1;
@@ -750,10 +845,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
     const uint32_t floor = border;
     const u64 spare = quota < ties ? (u64)(ties - quota) * R.weigh(value_of<T>(border)) : 0ull;
     u64 target = 0;
-    const Find f = R.template find<true>(
-        0ull, [&](float v, uint32_t key) -> int { return key >= floor ? (int)class_of(v, R.heat) : -1; },
+    const float from = floor ? value_of<T>(floor) : -3.40282347e38f;
+    const Find f = R.template find<2>(
+        0ull, [&](float v, uint32_t) -> int { return v >= from ? 0 : -1; },
         [&](u64 all) { return target = share_of(all - spare, r.p); });
-    auto in_class = [&](float v, uint32_t key) { return key >= floor && class_of(v, R.heat) == f.bin; };
+    auto in_class = [&](float v) { return v >= from && class_of(v, R.heat) == f.bin; };
     const uint32_t held = R.template gather<false>(in_class, nullptr);
     if (held <= kList) {
       if (R.rank == 0) {
@@ -786,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
       cutoff = sh.cutoff;
       quota = ties = 0;
     } else {
-      descend(std::true_type{}, f.above, in_class, [&](u64) { return target; });
+      descend(std::true_type{}, f.above, [&](float v, uint32_t) { return in_class(v); }, [&](u64) { return target; });
     }
   }
 
@@ -842,9 +938,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
     upto = 0x7fffffff;
   }
   uint32_t kept = 0;
-  for (int t = warp; t < R.tiles; t += kWarps) {
-    float f[8];
-    const int id = R.load(t, f);
+  R.each(warp, R.tiles, kWarps, [&](int id, const float* f, int t) {
     u64 m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -855,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
     }
     m = warp_sum64(m);
     if (lane == 0) sh.tile_mass[t] = m;
-  }
+  });
   kept = __reduce_add_sync(0xffffffffu, kept);
   if (lane == 0) sh.warp_count[warp] = kept;
   __syncthreads();
