@@ -790,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
   r.least = sh.least;
 
   // ---- few ids: one CTA finishes
+  u64 whole = 0;                             // the weight of all ids, where it is known
   if (grouped && r.k < n) {
     if (R.rank == 0) {
       const uint32_t b = R.bound(r.k);
@@ -811,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
       if (R.rank == 0) R.finish(held, r, all, a, row);
       return;
     }
+    whole = all;
   }
 
   // ---- where the order's kept prefix ends: at the key `border`, of whose equals those up to the id `cutoff`
@@ -845,10 +847,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
     const uint32_t floor = border;
     const u64 spare = quota < ties ? (u64)(ties - quota) * R.weigh(value_of<T>(border)) : 0ull;
     u64 target = 0;
-    const float from = floor ? value_of<T>(floor) : -3.40282347e38f;
+    // (with the whole weight known the ids below the least share can be left out: a border among them is no border)
+    const float from = fmaxf(floor ? value_of<T>(floor) : -3.40282347e38f, whole ? r.least : -3.40282347e38f);
     const Find f = R.template find<2>(
         0ull, [&](float v, uint32_t) -> int { return v >= from ? 0 : -1; },
-        [&](u64 all) { return target = share_of(all - spare, r.p); });
+        [&](u64 all) { return target = min(share_of(whole ? whole : all - spare, r.p), all); });
     auto in_class = [&](float v) { return v >= from && class_of(v, R.heat) == f.bin; };
     const uint32_t held = R.template gather<false>(in_class, nullptr);
     if (held <= kList) {
@@ -1037,9 +1040,13 @@ cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, con
   g_used_sample = true;
   Args a{token, logprob, kept, u, r, vocab, 0, vocab % 8 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0};
   const int tiles = (vocab + kTile - 1) / kTile;
-  // as many CTAs as run at once (two an SM), a tile for every warp
+  // As many CTAs as run at once (two an SM) with a tile for every warp, but two a row up to 304 rows: rows differ in
+  // what they ask for (64 rows of 64000: 8, 4, 2 a row 49, 43, 58 us; 256 of 131072, some with a share alone: 4, 2, 1 a
+  // row 173, 175, 231 us; one of 32000: 8, 4, 1 a row 12.8, 13.8, 17.5 us).
   int nc = kMaxCluster;
-  while (nc > 1 && tiles <= nc / 2 * kMaxTiles && ((int64_t)nc * n_rows > 304 || tiles < nc / 2 * kWarps)) nc /= 2;
+  while (nc > 1 && tiles <= nc / 2 * kMaxTiles &&
+         ((int64_t)(nc > 2 ? nc : 1) * n_rows > 304 || tiles < nc / 2 * kWarps))
+    nc /= 2;
   a.tpc = (tiles + nc - 1) / nc;
   return dt == DT_BF16 ? launch_t<bf16>(logits, n_rows, a, nc, s) : launch_t<float>(logits, n_rows, a, nc, s);
 }
