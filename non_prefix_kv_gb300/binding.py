@@ -664,17 +664,18 @@ def cb_rope_table_scaled(cos_sin, max_pos: int, spec: cb_rope_spec, stream=None)
 
 
 def _strided(what: str, t, dtype, width: int, dev: int):
-    """Address and row stride of rows [n, width] whose channels are contiguous (a part of wider rows)."""
+    """Address, row stride and count of rows [n, width] whose channels are contiguous (a part of wider rows)."""
     if t is None:
-        return None, 0
+        return None, 0, 0
+    shape, stride = t.shape, t.stride()
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {t.dtype}, expected {dtype}")
-    if t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()}, expected rows of {width} contiguous elements")
+    if len(shape) != 2 or shape[1] != width or stride[1] != 1:
+        raise ValueError(f"{what}: shape {tuple(shape)}, strides {stride}, expected rows of {width} contiguous elements")
     if t.get_device() != dev:
         raise ValueError(f"{what}: on {t.device}, not on the current CUDA device")
-    # (one row has no stride; of none nothing is read)
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+    n = shape[0]
+    return t.data_ptr(), stride[0] if n > 1 else width, n      # (one row has no stride)
 
 
 def cb_rope_rows(q, k, v, pos, q_out, k_out, v_out, dims: cb_dims, spec: cb_rope_spec, cos_sin, max_pos: int, src_row=None,
@@ -683,26 +684,25 @@ def cb_rope_rows(q, k, v, pos, q_out, k_out, v_out, dims: cb_dims, spec: cb_rope
     (row kv_row[i], -1: none): 2-D tensors, their rows may be parts of wider ones.  q or k, v may be
     None with their outputs.  cos_sin: cb_rope_table_scaled's for at least max_pos positions."""
     T = _torch()
-    dev, dt = T.device(), T.row[dims.dtype]
-    n, qw, w = pos.numel(), dims.n_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
-    for what, t in (("q", q), ("q_out", q_out)):
-        if t is not None and t.shape[0] != n:
-            raise ValueError(f"{what}: {t.shape[0]} rows, {n} positions")
-    for what, t, ref in (("v", v, k), ("v_out", v_out, k_out)):
-        if t is not None and (ref is None or t.shape[0] != ref.shape[0]):
-            raise ValueError(f"{what}: not the rows of {'k' if what == 'v' else 'k_out'}")
+    hd, dt, dev = dims.head_dim, T.row[dims.dtype], T.device()
+    n, qw, w = pos.numel(), dims.n_heads * hd, dims.n_kv_heads * hd
+    pq, lq, nq = _strided("q", q, dt, qw, dev)
+    pqo, lqo, nqo = _strided("q_out", q_out, dt, qw, dev)
+    pk, lk, nk = _strided("k", k, dt, w, dev)
+    pv, lv, nv = _strided("v", v, dt, w, dev)
+    pko, lko, nko = _strided("k_out", k_out, dt, w, dev)
+    pvo, lvo, nvo = _strided("v_out", v_out, dt, w, dev)
+    if (pq and nq != n) or (pqo and nqo != n):
+        raise ValueError(f"q: {nq} rows, q_out: {nqo} rows, {n} positions")
+    if (pv and nv != nk) or (pvo and (nvo != nko or lvo != lko)):
+        raise ValueError("k and v, k_out and v_out differ in their rows or (the outputs) row strides")
     if cos_sin.numel() < max_pos * spec.rot_dim:
         raise ValueError(f"cos_sin holds {cos_sin.numel()} values, {max_pos} positions of {spec.rot_dim} channels need more")
-    (pq, lq), (pqo, lqo) = _strided("q", q, dt, qw, dev), _strided("q_out", q_out, dt, qw, dev)
-    (pk, lk), (pv, lv) = _strided("k", k, dt, w, dev), _strided("v", v, dt, w, dev)
-    (pko, lko), (pvo, lvo) = _strided("k_out", k_out, dt, w, dev), _strided("v_out", v_out, dt, w, dev)
-    if pvo is not None and lvo != lko:
-        raise ValueError("k_out and v_out differ in their row stride")
-    io = cb_rope_rows_io(pq, pqo, lq, lqo, pk, pv, lk, lv, _buf("src_row", src_row, T.i32, n, dev),
-                         0 if k is None else k.shape[0], pko, pvo, lko, _buf("kv_row", kv_row, T.i32, n, dev),
-                         0 if k_out is None else k_out.shape[0])
+    i32 = T.i32
+    io = cb_rope_rows_io(pq, pqo, lq, lqo, pk, pv, lk, lv, _buf("src_row", src_row, i32, n, dev), nk, pko, pvo, lko,
+                         _buf("kv_row", kv_row, i32, n, dev), nko)
     _check("cb_rope_rows", lib().cb_rope_rows(
-        C.byref(io), _buf("pos", pos, T.i32, n, dev), n, 1 if inverse else 0, C.byref(dims), C.byref(spec),
+        C.byref(io), _buf("pos", pos, i32, n, dev), n, inverse, C.byref(dims), C.byref(spec),
         _buf("cos_sin", cos_sin, T.f32, None, dev), max_pos, T.stream(stream, dev)))
 
 
