@@ -127,7 +127,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
   uint64_t* q_full = bars + 8;                               // [2]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the warp's number from one lane: the compiler then knows it to be one for the warp, and descriptors stay in
+  // uniform registers)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
   uint64_t* k_full = bars + 4 * grp;       // a group's barriers: K and V have landed, S and P V are done
   uint64_t* v_full = k_full + 1;
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
   const uint32_t tS = trow + grp * BN, tO = trow + TM_O + grp * HD;
-  const bool issuer = quad == 0;
+  const bool issuer = quad == 0, loader = quad == 3;     // a group's products, and its copies, by different warps
   uint8_t* sK = base + L::OFF_K + grp * L::T_BYTES;
   uint8_t* sV = base + L::OFF_V + grp * L::T_BYTES;
   bool ok = true;                  // of this warp; one that gave up goes on meeting the others
@@ -218,9 +220,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     load_q(cur, 0);
     if (nxt.n) load_q(nxt, 1);
   }
-  if (issuer && grp < cur.n) {
+  if (loader && grp < cur.n) {
     load_k(cur, cur.tile + grp);
     load_v(cur, cur.tile + grp);
+  }
+  if (issuer && grp < cur.n) {
     ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[0], 0) && tc::mbar_wait(k_full, 0));
     if (ok) issue_s(0);
   }
@@ -234,8 +238,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int t = grp; t < cur.n; t += 2, ++u) {
       const int tile = cur.tile + t, keys = min(BN, len - tile * BN);
       const bool more = t + 2 < cur.n;
-      if (work) ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
-      if (issuer && ok) {
+      if (work || loader) ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
+      if (loader && ok) {
         if (more)
           load_k(cur, tile + 2);
         else if (grp < nxt.n)
@@ -318,18 +322,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (ok) issue_pv(t != grp);
         if (more) {
           ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(k_full, (u + 1) & 1) && tc::mbar_wait(pv_done, u & 1));
-          if (ok) {
-            issue_s(turn);
+          if (ok) issue_s(turn);
+        }
+      }
+      if (loader && (more || grp < nxt.n)) {
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(pv_done, u & 1));
+        if (ok) {
+          if (more)
             load_v(cur, tile + 2);
-          }
-        } else if (grp < nxt.n) {
-          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(pv_done, u & 1));
-          if (ok) load_v(nxt, nxt.tile + grp);
+          else
+            load_v(nxt, nxt.tile + grp);
         }
       }
     }
     const bool had = grp < cur.n;
-    if (!had && issuer && ok && grp < nxt.n) {
+    if (!had && loader && ok && grp < nxt.n) {
       load_k(nxt, nxt.tile + grp);
       load_v(nxt, nxt.tile + grp);
     }
