@@ -38,7 +38,8 @@ using tc::fmax3;
 constexpr int BM = 128;              // rows of a tile
 constexpr int BN = 128;              // keys of a tile
 constexpr int SLAB = 128 * 128;      // bytes of one [128 rows x 64 elements] swizzled slab
-constexpr int THREADS = 256;
+constexpr int THREADS = 384;         // of the prefix kernel: copies and products, two groups of softmax
+constexpr int kRegsIssue = 40, kRegsSoftmax = 232;      // registers a thread after the split; 40 + 2 x 232 = 3 x 168 as launched
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_O = 2 * BN;    // TMEM: S_0 | S_1 | O_0 | O_1
 constexpr float kLazy = 8.0f;        // weights up to 2^8 before a row's maximum is raised
@@ -110,11 +111,25 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Two groups of four warps take a segment's key tiles by turns; each is a closed loop, its first warp issuing
-// the copies and products between its share of the softmax: S -> softmax -> P V -> S of the group's next tile,
-// with one thread per row of the tile and its 128 scores in registers.  K's buffer is refilled as soon as S is
-// there, V's once P V is done, with the next segment's first tile where a segment ends; Q alternates between two
-// buffers.  Warps whose 32 rows do not exist (few queries) leave the softmax to the others.
+// Two groups take a segment's key tiles by turns.  A group is four warps of softmax, one thread per row of the tile
+// with its 128 scores in registers, one warp that issues its copies and one that issues its products, so that the
+// chain S -> softmax -> P V -> S of the group's next tile holds no copy and no wait for one.  K's buffer is refilled
+// as soon as S is there, V's once P V is done, across the ends of segments; Q alternates between two buffers, which
+// are also the way out of a segment's rows.  Warps whose 32 rows do not exist (few queries) leave the softmax to
+// the others.
+//
+// Barriers of a group: K and V have landed, S and P V are done, P is written.  How far the segments' results have
+// been read (from TMEM, and out of Q's buffer) is a count that the issuing warps look at: they may be ahead by more
+// than a barrier's phase can tell.
+__device__ __forceinline__ bool wait_count(const int* count, int n) {
+  for (uint32_t i = 0; i < tc::kWaitLimit; ++i) {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(tc::smem_u32(count)) : "memory");
+    if (v >= n) return true;
+  }
+  return false;
+}
+
 template <int HD>
 __global__ void __launch_bounds__(THREADS, 1)
     k_shared_prefix(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -125,32 +140,34 @@ __global__ void __launch_bounds__(THREADS, 1)
   float* xm = reinterpret_cast<float*>(base + L::OFF_X);     // [2][BM] row max, then [2][BM] row sum
   float* xl = xm + 2 * BM;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
-  uint64_t* q_full = bars + 8;                               // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 10);
-  // (the warp's number from one lane: the compiler then knows it to be one for the warp, and descriptors stay in
-  // uniform registers)
+  uint64_t* q_full = bars + 10;                              // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
+  int* read_out = reinterpret_cast<int*>(bars + 12) + 1;     // warps that have read out their part of a segment
+  // (the warp's number from one lane: the compiler then knows it to be one for the warp)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int grp = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-  uint64_t* k_full = bars + 4 * grp;       // a group's barriers: K and V have landed, S and P V are done
+  const int wg = warp >> 2, quad = warp & 3;
+  // warps 0 and 3 copy, 1 and 2 issue products, for groups 0 and 1; then the groups' softmax
+  const int grp = wg == 0 ? warp >> 1 : wg - 1;
+  uint64_t* k_full = bars + 5 * grp;
   uint64_t* v_full = k_full + 1;
   uint64_t* s_full = k_full + 2;
   uint64_t* pv_done = k_full + 3;
+  uint64_t* p_full = k_full + 4;
   const Shared& p = w.s;
   const int a = run_start(w.total, blockIdx.x, w.workers), b = run_start(w.total, blockIdx.x + 1, w.workers);
 
   if (tid == 0) {
-    for (int i = 0; i < 10; ++i) tc::mbar_init(&bars[i], 1);
+    for (int i = 0; i < 12; ++i) tc::mbar_init(&bars[i], i < 10 && i % 5 == 4 ? 4 : 1);
+    *read_out = 0;
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&tmQ);
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
-  Seg cur = segment(w, a, b), nxt = cur;
-  nxt.n = 0;
-  if (cur.end < b) nxt = segment(w, cur.end, b);
+  Seg cur = segment(w, a, b);
   pdl_wait();
   pdl_trigger();                   // (before TMEM is allocated: see tc::kWholeSm)
-  if (warp == 0) {
+  if (warp == 4) {
     tc::tmem_alloc(tmem_slot, TMEM_COLS);
     tc::tmem_relinquish();
   }
@@ -158,267 +175,257 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-  const uint32_t tS = trow + grp * BN, tO = trow + TM_O + grp * HD;
-  const bool issuer = quad == 0, loader = quad == 3;     // a group's products, and its copies, by different warps
   uint8_t* sK = base + L::OFF_K + grp * L::T_BYTES;
   uint8_t* sV = base + L::OFF_V + grp * L::T_BYTES;
-  bool ok = true;                  // of this warp; one that gave up goes on meeting the others
-  int nk_loads = 0, nv_loads = 0, nq_loads = 0;
-
-  auto load_q = [&](const Seg& x, int turn) {          // by thread 0
-    ++nq_loads;
-    tc::mbar_expect_tx(&q_full[turn], HD * 2 * p.G * w.qpt);
-    for (int s = 0; s < HD / 64; ++s)
-      tma_load_3d(base + L::OFF_Q + turn * L::T_BYTES + s * SLAB, &tmQ, &q_full[turn], 64 * s, x.h * p.G,
-                  p.seq0[x.g] * p.n_q + x.rt * w.qpt);
-  };
-  auto load_kv = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, const Seg& x, int tile) {   // by lane 0
-    tc::mbar_expect_tx(bar, L::T_BYTES);
-    for (int s = 0; s < HD / 64; ++s)
-      tc::tma_load_2d(dst + s * SLAB, map, bar, x.h * HD + 64 * s, p.row0[x.g] + tile * BN);
-  };
-  auto load_k = [&](const Seg& x, int tile) {
-    ++nk_loads;
-    if (lane == 0) load_kv(&tmK, sK, k_full, x, tile);
-  };
-  auto load_v = [&](const Seg& x, int tile) {
-    ++nv_loads;
-    if (lane == 0) load_kv(&tmV, sV, v_full, x, tile);
-  };
-  auto group_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + grp) : "memory"); };
-  auto issue_s = [&](int turn) {
-    constexpr uint32_t idesc = tc::idesc_bf16_f32(BM, BN);
-    const uint64_t qd = tc::desc_sw128(tc::smem_u32(base + L::OFF_Q + turn * L::T_BYTES)), kd = tc::desc_sw128(tc::smem_u32(sK));
-    tc::tc_fence_after();
-    if (tc::elect_one()) {
-#pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
-        tc::mma_bf16(tmem + grp * BN, qd + off, kd + off, idesc, k > 0);
-      }
-      tc::mma_commit(s_full);
-    }
-    __syncwarp();
-  };
-  auto issue_pv = [&](bool add) {
-    constexpr uint32_t idesc = tc::idesc_bf16_f32(BM, HD, true);
-    const uint64_t vd = tc::desc_sw128_mn(tc::smem_u32(sV), SLAB);
-    tc::tc_fence_after();
-    if (tc::elect_one()) {
-#pragma unroll
-      for (int k = 0; k < BN / 16; ++k)
-        tc::mma_bf16_ts(tmem + TM_O + grp * HD, tmem + grp * BN + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc,
-                        (add || k > 0) ? 1u : 0u);
-      tc::mma_commit(pv_done);
-    }
-    __syncwarp();
-  };
-
-  // ---- the run's segments
-  if (tid == 0) {
-    load_q(cur, 0);
-    if (nxt.n) load_q(nxt, 1);
-  }
-  if (loader && grp < cur.n) {
-    load_k(cur, cur.tile + grp);
-    load_v(cur, cur.tile + grp);
-  }
-  if (issuer && grp < cur.n) {
-    ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_full[0], 0) && tc::mbar_wait(k_full, 0));
-    if (ok) issue_s(0);
-  }
+  bool ok = true;                  // of this warp; the others of a segment find out by their own waits
   int u = 0;                       // the group's tiles so far: the phase of its barriers
-  for (int nseg = 0;; ++nseg) {
-    const int turn = nseg & 1;     // Q's buffer
-    const int rows = min(w.qpt, (p.seq0[cur.g + 1] - p.seq0[cur.g]) * p.n_q - cur.rt * w.qpt) * p.G;
-    const bool work = quad * 32 < rows;
-    const int len = p.len[cur.g];
-    float m_used = -INFINITY, l = 0.f;
-    for (int t = grp; t < cur.n; t += 2, ++u) {
-      const int tile = cur.tile + t, keys = min(BN, len - tile * BN);
-      const bool more = t + 2 < cur.n;
-      if (work || loader) ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
-      if (loader && ok) {
-        if (more)
-          load_k(cur, tile + 2);
-        else if (grp < nxt.n)
-          load_k(nxt, nxt.tile + grp);
-      }
-      if (work && ok) {
-        uint32_t sr[BN];
-        tc::tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
-        tc::tmem_wait_ld64(sr);
-        tc::tmem_wait_ld64(sr + 64);
-        if (keys < BN) {
-#pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c >= keys) sr[c] = 0xff800000u;
-        }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < BN; c += 8) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mx[q] = fmax3(mx[q], __uint_as_float(sr[c + 2 * q]), __uint_as_float(sr[c + 2 * q + 1]));
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        if (t == grp) {
-          m_used = mt;             // O_g is written, not added to, by this tile's P V
-        } else {
-          const bool need = mt > m_used + kLazy;
-          if (__any_sync(0xffffffffu, need)) {               // (S was issued after the last P V had completed)
-            const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
-#pragma unroll 1
-            for (int c = 0; c < HD / 16; ++c) {
-              float o[16];
-              tc::tmem_ld16(tO + c * 16, o);
-#pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] *= alpha;
-              tc::tmem_st16(tO + c * 16, o);
-            }
-            l *= alpha;
-            if (need) m_used = mt;
-          }
-        }
-        const float off = m_used == -INFINITY ? 0.f : -m_used;
-        const uint64_t f2 = f2_pack(p.scale_log2, p.scale_log2), o2 = f2_pack(off, off);
-        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const int k0 = c * 32 + 2 * q;
-            const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, o2));
-            const float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
-            sum[q & 1] = f2_add(sum[q & 1], f2_pack(p0, p1));
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-            pk[q] = *reinterpret_cast<const uint32_t*>(&h2);
-          }
-          tc::tmem_st16u_nowait(tS + c * 16, pk);
-        }
-        const float2 sm = f2_unpack(f2_add(sum[0], sum[1]));
-        l += sm.x + sm.y;
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-      }
-      group_sync();
-      if (issuer) {
-        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(v_full, u & 1));
-        if (ok && keys < BN) {
-          // what the copy brought from behind the prefix may be no number: times a weight of 0 it would stay none
-          for (int c = lane; c < (BN - keys) * 8; c += 32)
-#pragma unroll
+
+  if (wg == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue));
+    if (quad == 0 || quad == 3) {
+      // -------------------------------------------------------------- copies
+      int nk = 0, nv = 0, nq = 0;
+      for (int nseg = 0; ok; ++nseg) {
+        if (grp == 0) {
+          ok = nseg < 2 || __all_sync(0xffffffffu, wait_count(read_out, 8 * (nseg - 1)));
+          if (!ok) break;
+          ++nq;
+          if (lane == 0) {
+            uint64_t* bar = &q_full[nseg & 1];
+            tc::mbar_expect_tx(bar, HD * 2 * p.G * w.qpt);
             for (int s = 0; s < HD / 64; ++s)
-              *reinterpret_cast<uint4*>(sV + s * SLAB + keys * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-          tc::fence_proxy_async_smem();
+              tma_load_3d(base + L::OFF_Q + (nseg & 1) * L::T_BYTES + s * SLAB, &tmQ, bar, 64 * s, cur.h * p.G,
+                          p.seq0[cur.g] * p.n_q + cur.rt * w.qpt);
+          }
           __syncwarp();
         }
-        if (ok) issue_pv(t != grp);
-        if (more) {
-          ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(k_full, (u + 1) & 1) && tc::mbar_wait(pv_done, u & 1));
-          if (ok) issue_s(turn);
-        }
-      }
-      if (loader && (more || grp < nxt.n)) {
-        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(pv_done, u & 1));
-        if (ok) {
-          if (more)
-            load_v(cur, tile + 2);
-          else
-            load_v(nxt, nxt.tile + grp);
-        }
-      }
-    }
-    const bool had = grp < cur.n;
-    if (!had && loader && ok && grp < nxt.n) {
-      load_k(nxt, nxt.tile + grp);
-      load_v(nxt, nxt.tile + grp);
-    }
-    // ---- the segment's piece: both groups' row statistics meet in shared memory
-    ok = ok && (!had || __all_sync(0xffffffffu, tc::mbar_wait(pv_done, (u - 1) & 1)));
-    xm[grp * BM + r] = m_used;
-    xl[grp * BM + r] = l;
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    if (issuer && grp < nxt.n) {
-      ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&q_full[turn ^ 1], ((nseg + 1) >> 1) & 1) && tc::mbar_wait(k_full, u & 1));
-      if (ok) issue_s(turn ^ 1);
-    }
-    if (ok && work) {              // (uniform over the warp: the loads from TMEM are the whole warp's)
-      const float ma = xm[r], mb = xm[BM + r], mm = fmaxf(ma, mb);
-      const float a0 = ma == -INFINITY ? 0.f : tc::ex2_approx(ma - mm);
-      const float a1 = mb == -INFINITY ? 0.f : tc::ex2_approx(mb - mm);
-      // (a sum that is no number counts even though no maximum was found beside it)
-      const float lt = (ma == -INFINITY ? xl[r] : xl[r] * a0) + (mb == -INFINITY ? xl[BM + r] : xl[BM + r] * a1);
-      float* out = slot(w.part, w.slot_rows, HD, blockIdx.x, cur.pair);
-      if (grp == 0 && r < rows) {
-        out[w.slot_rows * HD + r] = isnan(lt) ? lt : mm;
-        out[w.slot_rows * (HD + 1) + r] = lt;
-      }
-      // The rows leave through Q's buffer, HD / 4 columns of the warp's 32 rows at a time, so that a store
-      // covers whole lines (each thread storing its own row took 2.1 us for 126 rows).
-      constexpr int C4 = HD / 16;  // 16-byte words of a row's part
-      uint8_t* st = base + L::OFF_Q + turn * L::T_BYTES + warp * (32 * C4 * 16);
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        const int col = grp * (HD / 2) + c * (HD / 4);
-#pragma unroll
-        for (int h = 0; h < C4 / 4; ++h) {
-          float o0[16], o1[16];
-          tc::tmem_ld16(trow + TM_O + col + h * 16, o0);
-          if (cur.n > 1) {         // (else O_1 was never written)
-            tc::tmem_ld16(trow + TM_O + HD + col + h * 16, o1);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) o1[q] = 0.f;
+        const int col = cur.h * HD, row = p.row0[cur.g] + cur.tile * BN;
+        for (int t = grp; t < cur.n; t += 2, ++u) {
+          if (u > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(s_full, (u - 1) & 1));
+          if (!ok) break;
+          ++nk;
+          if (lane == 0) {
+            tc::mbar_expect_tx(k_full, L::T_BYTES);
+            for (int s = 0; s < HD / 64; ++s) tc::tma_load_2d(sK + s * SLAB, &tmK, k_full, col + 64 * s, row + t * BN);
           }
-#pragma unroll
-          for (int q = 0; q < 16; ++q) o0[q] = o0[q] * a0 + o1[q] * a1;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<float4*>(st + lane * (C4 * 16) + (((h * 4 + q) ^ (lane & (C4 - 1))) << 4)) =
-                make_float4(o0[4 * q], o0[4 * q + 1], o0[4 * q + 2], o0[4 * q + 3]);
+          __syncwarp();
+          if (u > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_done, (u - 1) & 1));
+          if (!ok) break;
+          ++nv;
+          if (lane == 0) {
+            tc::mbar_expect_tx(v_full, L::T_BYTES);
+            for (int s = 0; s < HD / 64; ++s) tc::tma_load_2d(sV + s * SLAB, &tmV, v_full, col + 64 * s, row + t * BN);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < C4; ++i) {
-          const int rr = i * (32 / C4) + lane / C4, q = lane & (C4 - 1), row = quad * 32 + rr;
-          if (row < rows)
-            *reinterpret_cast<float4*>(out + (int64_t)row * HD + col + q * 4) =
-                *reinterpret_cast<const float4*>(st + rr * (C4 * 16) + ((q ^ (rr & (C4 - 1))) << 4));
-        }
-        __syncwarp();
+        if (!ok || cur.end >= b) break;
+        cur = segment(w, cur.end, b);
       }
-      tc::fence_proxy_async_smem();              // (before Q comes into the same place)
+      if (!ok) {                   // give the copies in flight as long again before the memory is given up
+        if (nk > 0) tc::mbar_wait(k_full, (nk - 1) & 1);
+        if (nv > 0) tc::mbar_wait(v_full, (nv - 1) & 1);
+        for (int i = max(0, nq - 2); i < nq; ++i) tc::mbar_wait(&q_full[i & 1], (i >> 1) & 1);
+      }
+    } else {
+      // -------------------------------------------------------------- products
+      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(BM, BN), idesc_o = tc::idesc_bf16_f32(BM, HD, true);
+      const uint64_t kd = tc::desc_sw128(tc::smem_u32(sK)), vd = tc::desc_sw128_mn(tc::smem_u32(sV), SLAB);
+      const uint32_t tS = tmem + grp * BN, tO = tmem + TM_O + grp * HD;
+      for (int nseg = 0; ok; ++nseg) {
+        const uint64_t qd = tc::desc_sw128(tc::smem_u32(base + L::OFF_Q + (nseg & 1) * L::T_BYTES));
+        const int len = p.len[cur.g] - cur.tile * BN;
+        for (int t = grp; t < cur.n; t += 2, ++u) {
+          const int keys = len - t * BN;
+          // S goes where P is, until P V is done
+          ok = __all_sync(0xffffffffu, (t != grp || tc::mbar_wait(&q_full[nseg & 1], (nseg >> 1) & 1)) &&
+                                           tc::mbar_wait(k_full, u & 1) && (u == 0 || tc::mbar_wait(pv_done, (u - 1) & 1)));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < HD / 16; ++k) {
+              const uint32_t off = ((k >> 2) * SLAB + (k & 3) * 32) >> 4;
+              tc::mma_bf16(tS, qd + off, kd + off, idesc_s, k > 0);
+            }
+            tc::mma_commit(s_full);
+          }
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, tc::mbar_wait(v_full, u & 1));
+          if (ok && keys < BN) {
+            // what the copy brought from behind the prefix may be no number: times a weight of 0 it would stay none
+            for (int c = lane; c < (BN - keys) * 8; c += 32)
+#pragma unroll
+              for (int s = 0; s < HD / 64; ++s)
+                *reinterpret_cast<uint4*>(sV + s * SLAB + keys * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+          }
+          // the segment's first tile writes O, once the segment before has been read out
+          ok = ok && __all_sync(0xffffffffu, (t != grp || nseg == 0 || wait_count(read_out, 8 * nseg)) && tc::mbar_wait(p_full, u & 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              tc::mma_bf16_ts(tO, tS + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc_o, (t != grp || k > 0) ? 1u : 0u);
+            tc::mma_commit(pv_done);
+          }
+          __syncwarp();
+        }
+        if (!ok || cur.end >= b) break;
+        cur = segment(w, cur.end, b);
+      }
     }
-    tc::tc_fence_before();
-    __syncthreads();               // O and the statistics are free
-    tc::tc_fence_after();
-    if (!nxt.n) break;             // (uniform)
-    cur = nxt;
-    nxt.n = 0;
-    if (cur.end < b) {
-      nxt = segment(w, cur.end, b);
-      if (tid == 0) load_q(nxt, turn);           // (both groups' S of the segment before are done with the buffer)
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ---------------------------------------------------------------- softmax
+    const int r = quad * 32 + lane;
+    const uint32_t trow = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t tS = trow + grp * BN, tO = trow + TM_O + grp * HD;
+    auto softmax_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    for (int nseg = 0;; ++nseg) {
+      const int turn = nseg & 1;   // Q's buffer
+      const int rows = min(w.qpt, (p.seq0[cur.g + 1] - p.seq0[cur.g]) * p.n_q - cur.rt * w.qpt) * p.G;
+      const bool work = quad * 32 < rows;
+      const int len = p.len[cur.g] - cur.tile * BN;
+      float m_used = -INFINITY, l = 0.f;
+      for (int t = grp; t < cur.n; t += 2, ++u) {
+        const int keys = len - t * BN;
+        ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
+        if (work && ok) {
+          uint32_t sr[BN];
+          tc::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
+          tc::tmem_wait_ld64(sr);
+          tc::tmem_wait_ld64(sr + 64);
+          if (keys < BN) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if (c >= keys) sr[c] = 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < BN; c += 8) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mx[q] = fmax3(mx[q], __uint_as_float(sr[c + 2 * q]), __uint_as_float(sr[c + 2 * q + 1]));
+          }
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          if (t == grp) {
+            m_used = mt;           // O_g is written, not added to, by this tile's P V
+          } else {
+            const bool need = mt > m_used + kLazy;
+            if (__any_sync(0xffffffffu, need)) {               // (S was issued after the last P V had completed)
+              const float alpha = need ? tc::ex2_approx(m_used - mt) : 1.0f;
+#pragma unroll 1
+              for (int c = 0; c < HD / 16; ++c) {
+                float o[16];
+                tc::tmem_ld16(tO + c * 16, o);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] *= alpha;
+                tc::tmem_st16(tO + c * 16, o);
+              }
+              l *= alpha;
+              if (need) m_used = mt;
+            }
+          }
+          const float off = m_used == -INFINITY ? 0.f : -m_used;
+          const uint64_t f2 = f2_pack(p.scale_log2, p.scale_log2), o2 = f2_pack(off, off);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const int k0 = c * 32 + 2 * q;
+              const float2 z = f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[k0]), __uint_as_float(sr[k0 + 1])), f2, o2));
+              const float p0 = tc::ex2_approx(z.x), p1 = tc::ex2_approx(z.y);
+              sum[q & 1] = f2_add(sum[q & 1], f2_pack(p0, p1));
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+              pk[q] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            tc::tmem_st16u_nowait(tS + c * 16, pk);
+          }
+          const float2 sm = f2_unpack(f2_add(sum[0], sum[1]));
+          l += sm.x + sm.y;
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(p_full);
+      }
+      // -------------------------------------------------------------- the segment's piece
+      // both groups' row statistics meet in shared memory
+      ok = ok && (grp >= cur.n || __all_sync(0xffffffffu, tc::mbar_wait(pv_done, (u - 1) & 1)));
+      xm[grp * BM + r] = m_used;
+      xl[grp * BM + r] = l;
+      tc::tc_fence_before();
+      softmax_sync();
+      tc::tc_fence_after();
+      if (ok && work) {            // (uniform over the warp: the loads from TMEM are the whole warp's)
+        const float ma = xm[r], mb = xm[BM + r], mm = fmaxf(ma, mb);
+        const float a0 = ma == -INFINITY ? 0.f : tc::ex2_approx(ma - mm);
+        const float a1 = mb == -INFINITY ? 0.f : tc::ex2_approx(mb - mm);
+        // (a sum that is no number counts even though no maximum was found beside it)
+        const float lt = (ma == -INFINITY ? xl[r] : xl[r] * a0) + (mb == -INFINITY ? xl[BM + r] : xl[BM + r] * a1);
+        float* out = slot(w.part, w.slot_rows, HD, blockIdx.x, cur.pair);
+        if (grp == 0 && r < rows) {
+          out[w.slot_rows * HD + r] = isnan(lt) ? lt : mm;
+          out[w.slot_rows * (HD + 1) + r] = lt;
+        }
+        // The rows leave through Q's buffer, HD / 4 columns of the warp's 32 rows at a time, so that a store
+        // covers whole lines (each thread storing its own row took 2.1 us for 126 rows).
+        constexpr int C4 = HD / 16;  // 16-byte words of a row's part
+        uint8_t* st = base + L::OFF_Q + turn * L::T_BYTES + (grp * 4 + quad) * (32 * C4 * 16);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int col = grp * (HD / 2) + c * (HD / 4);
+#pragma unroll
+          for (int h = 0; h < C4 / 4; ++h) {
+            float o0[16], o1[16];
+            tc::tmem_ld16(trow + TM_O + col + h * 16, o0);
+            if (cur.n > 1) {       // (else O_1 was never written)
+              tc::tmem_ld16(trow + TM_O + HD + col + h * 16, o1);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) o1[q] = 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 16; ++q) o0[q] = o0[q] * a0 + o1[q] * a1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<float4*>(st + lane * (C4 * 16) + (((h * 4 + q) ^ (lane & (C4 - 1))) << 4)) =
+                  make_float4(o0[4 * q], o0[4 * q + 1], o0[4 * q + 2], o0[4 * q + 3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < C4; ++i) {
+            const int rr = i * (32 / C4) + lane / C4, q = lane & (C4 - 1), row = quad * 32 + rr;
+            if (row < rows)
+              *reinterpret_cast<float4*>(out + (int64_t)row * HD + col + q * 4) =
+                  *reinterpret_cast<const float4*>(st + rr * (C4 * 16) + ((q ^ (rr & (C4 - 1))) << 4));
+          }
+          __syncwarp();
+        }
+        tc::fence_proxy_async_smem();            // (before Q comes into the same place)
+      }
+      tc::tc_fence_before();
+      softmax_sync();              // the statistics are free
+      if (lane == 0) {
+        __threadfence_block();
+        atomicAdd(read_out, 1);
+      }
+      if (cur.end >= b) break;     // (uniform)
+      cur = segment(w, cur.end, b);
     }
   }
-  if (!ok) {
-    // report, and give the copies in flight as long again before the memory is given up
-    if (lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_TIMEOUT);
-    if (nk_loads > 0) tc::mbar_wait(k_full, (nk_loads - 1) & 1);
-    if (nv_loads > 0) tc::mbar_wait(v_full, (nv_loads - 1) & 1);
-    if (tid == 0)
-      for (int i = max(0, nq_loads - 2); i < nq_loads; ++i) tc::mbar_wait(&q_full[i & 1], (i >> 1) & 1);
-  }
+  if (!ok && lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_TIMEOUT);
+  tc::tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 4) {
     __syncwarp();
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, TMEM_COLS);
