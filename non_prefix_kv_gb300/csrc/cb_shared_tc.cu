@@ -140,24 +140,24 @@ __global__ void __launch_bounds__(THREADS, 1)
   float* xm = reinterpret_cast<float*>(base + L::OFF_X);     // [2][BM] row max, then [2][BM] row sum
   float* xl = xm + 2 * BM;
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + L::OFF_BAR);
-  uint64_t* q_full = bars + 10;                              // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 12);
-  int* read_out = reinterpret_cast<int*>(bars + 12) + 1;     // warps that have read out their part of a segment
+  uint64_t* q_full = bars + 12;                              // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 14);
+  int* read_out = reinterpret_cast<int*>(bars + 14) + 1;     // warps that have read out their part of a segment
   // (the warp's number from one lane: the compiler then knows it to be one for the warp)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int wg = warp >> 2, quad = warp & 3;
   // warps 0 and 3 copy, 1 and 2 issue products, for groups 0 and 1; then the groups' softmax
   const int grp = wg == 0 ? warp >> 1 : wg - 1;
-  uint64_t* k_full = bars + 5 * grp;
+  uint64_t* k_full = bars + 6 * grp;
   uint64_t* v_full = k_full + 1;
   uint64_t* s_full = k_full + 2;
   uint64_t* pv_done = k_full + 3;
-  uint64_t* p_full = k_full + 4;
+  uint64_t* p_full = k_full + 4;                             // [2]: of the tile's first 64 keys, and of the others
   const Shared& p = w.s;
   const int a = run_start(w.total, blockIdx.x, w.workers), b = run_start(w.total, blockIdx.x + 1, w.workers);
 
   if (tid == 0) {
-    for (int i = 0; i < 12; ++i) tc::mbar_init(&bars[i], i < 10 && i % 5 == 4 ? 4 : 1);
+    for (int i = 0; i < 14; ++i) tc::mbar_init(&bars[i], i < 12 && i % 6 >= 4 ? 4 : 1);
     *read_out = 0;
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&tmQ);
@@ -261,16 +261,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
           }
           // the segment's first tile writes O, once the segment before has been read out
-          ok = ok && __all_sync(0xffffffffu, (t != grp || nseg == 0 || wait_count(read_out, 8 * nseg)) && tc::mbar_wait(p_full, u & 1));
-          if (!ok) break;
-          tc::tc_fence_after();
-          if (tc::elect_one()) {
+          ok = ok && __all_sync(0xffffffffu, t != grp || nseg == 0 || wait_count(read_out, 8 * nseg));
 #pragma unroll
-            for (int k = 0; k < BN / 16; ++k)
-              tc::mma_bf16_ts(tO, tS + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc_o, (t != grp || k > 0) ? 1u : 0u);
-            tc::mma_commit(pv_done);
+          for (int h = 0; h < 2; ++h) {            // (the second half of P is written while the first multiplies)
+            ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(&p_full[h], u & 1));
+            if (!ok) break;
+            tc::tc_fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int k = h * (BN / 32); k < (h + 1) * (BN / 32); ++k)
+                tc::mma_bf16_ts(tO, tS + k * 8, vd + (uint64_t)((k * 16 * 128) >> 4), idesc_o, (t != grp || k > 0) ? 1u : 0u);
+              if (h) tc::mma_commit(pv_done);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (!ok) break;
         }
         if (!ok || cur.end >= b) break;
         cur = segment(w, cur.end, b);
@@ -348,14 +353,22 @@ __global__ void __launch_bounds__(THREADS, 1)
               pk[q] = *reinterpret_cast<const uint32_t*>(&h2);
             }
             tc::tmem_st16u_nowait(tS + c * 16, pk);
+            if (c == 1) {
+              tc::tmem_wait_st();
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(p_full);
+            }
           }
           const float2 sm = f2_unpack(f2_add(sum[0], sum[1]));
           l += sm.x + sm.y;
           tc::tmem_wait_st();
           tc::tc_fence_before();
+        } else if (lane == 0) {
+          tc::mbar_arrive(p_full);
         }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(p_full);
+        if (lane == 0) tc::mbar_arrive(p_full + 1);
       }
       // -------------------------------------------------------------- the segment's piece
       // both groups' row statistics meet in shared memory
