@@ -56,14 +56,21 @@ struct Tc {
   int qpt;                       // queries of a row tile: 128 / G
   int slot_rows;                 // rows that a slot holds
   float* part;                   // [workers + pairs][slot_rows][hd], then m and l: see slot()
-  // own rows
+  // wide: row tiles hold queries of one sequence, and their line goes on from the prefix to the sequence's own rows
+  bool wide;
+  int chunks;                    // row tiles of a sequence
+  // own rows, where they have a kernel of their own
   int row_tiles;                 // of a sequence
   int own_slot_rows;
   bool alone;                    // no prefix kernel runs before
-  int32_t* plan;                 // [n_seq row_tiles + 1] steps before each, times Hkv
+  int32_t* plan;                 // [n_seq row_tiles + 1] steps before each, times Hkv; wide: how many row tiles are
+                                 // live, their key tiles, [n_seq chunks] the place of each among them (-1: none of
+                                 // its queries sees anything), [live + 1] key tiles before each
   float* own_part;               // [workers + n_seq row_tiles Hkv][rows][hd], m, l
 };
 
+// the CTAs that share a wide call's key tiles: a tile for each group of warps
+__device__ __forceinline__ int wide_workers(int total, int workers) { return min(workers, (total + 1) / 2); }
 __device__ __forceinline__ int row_tiles_of(const Tc& w, int g) {
   return ((w.s.seq0[g + 1] - w.s.seq0[g]) * w.s.n_q + w.qpt - 1) / w.qpt;
 }
@@ -71,27 +78,130 @@ __device__ __forceinline__ float* slot(float* part, int rows, int hd, int worker
   return part + ((int64_t)worker + pair) * (rows * (hd + 2));
 }
 
-// A run's part inside one (group, KV head, row tile).
+// A run's part inside one (KV head, row tile).
 struct Seg {
-  int g, h, rt, pair;
+  int h, pair;
   int tile, n;                   // its first key tile, and how many there are
   int end;                       // where it ends on the line
+  int tok, queries;              // the row tile's first query, and how many there are
+  int row0, len;                 // the prefix
+  int own_tile, own_row, own_len;    // the first key tile of own rows, the first own row, how many are seen
 };
-__device__ __forceinline__ Seg segment(const Tc& w, int i, int b) {
+constexpr int kWideTiles = 1024;     // row tiles of a wide call
+struct Wide {                        // the live row tiles of a wide call, in order
+  int first[kWideTiles + 1];         // key tiles before each; at the end those of one head
+  int id[kWideTiles], last[kWideTiles];
+  int n;
+};
+template <bool WIDE>
+__device__ __forceinline__ Seg segment(const Tc& w, const Wide& wide, int i, int b) {
+  const Shared& p = w.s;
   Seg x;
-  x.g = 0;
-  while (i >= w.first[x.g + 1]) ++x.g;
-  const int kt = (w.s.len[x.g] + BN - 1) / BN, rts = row_tiles_of(w, x.g), at = i - w.first[x.g], pl = at / kt;
-  x.tile = at - pl * kt;
-  x.h = pl / rts;
-  x.rt = pl - x.h * rts;
-  x.pair = w.prob[x.g] + pl;
+  int kt;
+  if constexpr (WIDE) {
+    const int per = wide.first[wide.n];
+    x.h = i / per;
+    int at = i - x.h * per, lo = 0, hi = wide.n - 1;         // the last one that starts at or before it
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (wide.first[mid] <= at)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int id = wide.id[lo], s = id / w.chunks, c = id - s * w.chunks;
+    int g = 0;
+    while (s >= p.seq0[g + 1]) ++g;
+    kt = wide.first[lo + 1] - wide.first[lo];
+    x.tile = at - wide.first[lo];
+    x.pair = x.h * wide.n + lo;
+    x.tok = s * p.n_q + c * w.qpt;
+    x.queries = min(w.qpt, p.n_q - c * w.qpt);
+    x.row0 = p.row0[g];
+    x.len = p.len[g];
+    x.own_tile = (x.len + BN - 1) / BN;
+    x.own_row = (int)(s * p.capacity);
+    x.own_len = wide.last[lo] + 1;
+  } else {
+    int g = 0;
+    while (i >= w.first[g + 1]) ++g;
+    const int rts = row_tiles_of(w, g), at = i - w.first[g];
+    kt = (p.len[g] + BN - 1) / BN;
+    const int pl = at / kt;
+    x.tile = at - pl * kt;
+    x.h = pl / rts;
+    x.pair = w.prob[g] + pl;
+    const int q0 = (pl - x.h * rts) * w.qpt;
+    x.tok = p.seq0[g] * p.n_q + q0;
+    x.queries = min(w.qpt, (p.seq0[g + 1] - p.seq0[g]) * p.n_q - q0);
+    x.row0 = p.row0[g];
+    x.len = p.len[g];
+    x.own_tile = 0x7fffffff;
+    x.own_row = x.own_len = 0;
+  }
   x.end = min(b, i + kt - x.tile);
   x.n = x.end - i;
   return x;
 }
+// keys of the segment's tile j that are there
+template <bool WIDE>
+__device__ __forceinline__ int keys_of(const Seg& x, int j) {
+  return min(BN, WIDE && j >= x.own_tile ? x.own_len - (j - x.own_tile) * BN : x.len - j * BN);
+}
 
-template <int HD>
+// The row tiles of which some query sees something; the first CTA leaves them in the plan for the join.
+__device__ __forceinline__ void make_wide(const Tc& w, Wide& wide, int tid, int threads) {
+  const Shared& p = w.s;
+  const int tiles = p.n_seq * w.chunks;
+  for (int i = tid; i < tiles; i += threads) {
+    const int s = i / w.chunks, c = i - s * w.chunks;
+    int mx = -2, g = 0;
+    for (int j = c * w.qpt; j < min(p.n_q, (c + 1) * w.qpt); ++j) mx = max(mx, shared_last(p, (int64_t)s * p.n_q + j));
+    while (s >= p.seq0[g + 1]) ++g;
+    wide.id[i] = mx >= -1 ? (p.len[g] + BN - 1) / BN + (mx + BN) / BN : 0;
+    wide.last[i] = mx;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    const bool write = blockIdx.x == 0;
+    int at = 0, units = 0;
+    for (int i0 = 0; i0 < tiles; i0 += 32) {
+      const int i = i0 + tid, n = i < tiles ? wide.id[i] : 0, mx = i < tiles ? wide.last[i] : -2;
+      const unsigned live = __ballot_sync(0xffffffffu, n > 0);
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (tid >= o) incl += y;
+      }
+      const int to = at + __popc(live & ((1u << tid) - 1));
+      if (n > 0) {
+        wide.first[to] = units + incl - n;
+        wide.id[to] = i;
+        wide.last[to] = mx;
+      }
+      if (write) {
+        if (i < tiles) w.plan[2 + i] = n > 0 ? to : -1;
+        if (n > 0) w.plan[2 + tiles + to] = units + incl - n;
+      }
+      at += __popc(live);
+      units += __shfl_sync(0xffffffffu, incl, 31);
+      __syncwarp();
+    }
+    if (tid == 0) {
+      wide.first[at] = units;
+      wide.n = at;
+      if (write) {
+        w.plan[0] = at;
+        w.plan[1] = units;
+        w.plan[2 + tiles + at] = units;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+template <int HD, bool WIDE>
 struct Layout {
   static constexpr int T_BYTES = HD / 64 * SLAB;             // a tile of Q, K or V
   static constexpr int OFF_Q = 0;                            // [2], by turns
@@ -99,7 +209,9 @@ struct Layout {
   static constexpr int OFF_V = OFF_K + 2 * T_BYTES;          // [2]
   static constexpr int OFF_X = OFF_V + 2 * T_BYTES;          // [2 groups][BM] row max, row sum
   static constexpr int OFF_BAR = OFF_X + 4 * BM * 4;
-  static constexpr int SMEM = OFF_BAR + 128 + 1024 > tc::kWholeSm ? OFF_BAR + 128 + 1024 : tc::kWholeSm;
+  static constexpr int OFF_WIDE = OFF_BAR + 128;
+  static constexpr int END = OFF_WIDE + (WIDE ? (int)sizeof(Wide) : 0) + 1024;
+  static constexpr int SMEM = END > tc::kWholeSm ? END : tc::kWholeSm;
   static_assert(SMEM <= 227 * 1024, "shared memory exceeds the per-block limit");
 };
 
@@ -118,6 +230,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 // are also the way out of a segment's rows.  Warps whose 32 rows do not exist (few queries) leave the softmax to
 // the others.
 //
+// WIDE: the calls with many queries of each sequence.  A row tile's queries are of one sequence and its key tiles go
+// on from the prefix's to the sequence's own, under each row's bound, so that own rows need no kernel of their own;
+// row tiles of padding are left out.  (8 questions of 48 to 96 queries of 56 heads over 16000 rows: 299 us without.)
+//
 // Barriers of a group: K and V have landed, S and P V are done, P is written.  How far the segments' results have
 // been read (from TMEM, and out of Q's buffer) is a count that the issuing warps look at: they may be ahead by more
 // than a barrier's phase can tell.
@@ -130,11 +246,12 @@ __device__ __forceinline__ bool wait_count(const int* count, int n) {
   return false;
 }
 
-template <int HD>
+template <int HD, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1)
     k_shared_prefix(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Tc w) {
-  using L = Layout<HD>;
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmOwnK,
+                    const __grid_constant__ CUtensorMap tmOwnV, const __grid_constant__ Tc w) {
+  using L = Layout<HD, WIDE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   float* xm = reinterpret_cast<float*>(base + L::OFF_X);     // [2][BM] row max, then [2][BM] row sum
@@ -154,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* pv_done = k_full + 3;
   uint64_t* p_full = k_full + 4;                             // [2]: of the tile's first 64 keys, and of the others
   const Shared& p = w.s;
-  const int a = run_start(w.total, blockIdx.x, w.workers), b = run_start(w.total, blockIdx.x + 1, w.workers);
+  Wide& wide = *reinterpret_cast<Wide*>(base + L::OFF_WIDE);
 
   if (tid == 0) {
     for (int i = 0; i < 14; ++i) tc::mbar_init(&bars[i], i < 12 && i % 6 >= 4 ? 4 : 1);
@@ -164,9 +281,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
-  Seg cur = segment(w, a, b);
-  pdl_wait();
+  int total = w.total, workers = w.workers;
+  if (!WIDE) pdl_wait();
+  if (WIDE) {
+    pdl_wait();
+    make_wide(w, wide, tid, THREADS);
+    total = wide.first[wide.n] * p.Hkv;
+    workers = wide_workers(total, workers);
+  }
   pdl_trigger();                   // (before TMEM is allocated: see tc::kWholeSm)
+  if (WIDE && (int)blockIdx.x >= workers) return;
+  const int a = run_start(total, blockIdx.x, workers), b = run_start(total, blockIdx.x + 1, workers);
+  Seg cur = segment<WIDE>(w, wide, a, b);
   if (warp == 4) {
     tc::tmem_alloc(tmem_slot, TMEM_COLS);
     tc::tmem_relinquish();
@@ -195,18 +321,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::mbar_expect_tx(bar, HD * 2 * p.G * w.qpt);
             for (int s = 0; s < HD / 64; ++s)
               tma_load_3d(base + L::OFF_Q + (nseg & 1) * L::T_BYTES + s * SLAB, &tmQ, bar, 64 * s, cur.h * p.G,
-                          p.seq0[cur.g] * p.n_q + cur.rt * w.qpt);
+                          cur.tok);
           }
           __syncwarp();
         }
-        const int col = cur.h * HD, row = p.row0[cur.g] + cur.tile * BN;
+        const int col = cur.h * HD;
         for (int t = grp; t < cur.n; t += 2, ++u) {
+          const int j = cur.tile + t;
+          const bool own = WIDE && j >= cur.own_tile;
+          const int row = own ? cur.own_row + (j - cur.own_tile) * BN : cur.row0 + j * BN;
           if (u > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(s_full, (u - 1) & 1));
           if (!ok) break;
           ++nk;
           if (lane == 0) {
             tc::mbar_expect_tx(k_full, L::T_BYTES);
-            for (int s = 0; s < HD / 64; ++s) tc::tma_load_2d(sK + s * SLAB, &tmK, k_full, col + 64 * s, row + t * BN);
+            for (int s = 0; s < HD / 64; ++s) tc::tma_load_2d(sK + s * SLAB, own ? &tmOwnK : &tmK, k_full, col + 64 * s, row);
           }
           __syncwarp();
           if (u > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(pv_done, (u - 1) & 1));
@@ -214,12 +343,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           ++nv;
           if (lane == 0) {
             tc::mbar_expect_tx(v_full, L::T_BYTES);
-            for (int s = 0; s < HD / 64; ++s) tc::tma_load_2d(sV + s * SLAB, &tmV, v_full, col + 64 * s, row + t * BN);
+            for (int s = 0; s < HD / 64; ++s) tc::tma_load_2d(sV + s * SLAB, own ? &tmOwnV : &tmV, v_full, col + 64 * s, row);
           }
           __syncwarp();
         }
         if (!ok || cur.end >= b) break;
-        cur = segment(w, cur.end, b);
+        cur = segment<WIDE>(w, wide, cur.end, b);
       }
       if (!ok) {                   // give the copies in flight as long again before the memory is given up
         if (nk > 0) tc::mbar_wait(k_full, (nk - 1) & 1);
@@ -233,9 +362,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t tS = tmem + grp * BN, tO = tmem + TM_O + grp * HD;
       for (int nseg = 0; ok; ++nseg) {
         const uint64_t qd = tc::desc_sw128(tc::smem_u32(base + L::OFF_Q + (nseg & 1) * L::T_BYTES));
-        const int len = p.len[cur.g] - cur.tile * BN;
         for (int t = grp; t < cur.n; t += 2, ++u) {
-          const int keys = len - t * BN;
+          const int keys = keys_of<WIDE>(cur, cur.tile + t);
           // S goes where P is, until P V is done
           ok = __all_sync(0xffffffffu, (t != grp || tc::mbar_wait(&q_full[nseg & 1], (nseg >> 1) & 1)) &&
                                            tc::mbar_wait(k_full, u & 1) && (u == 0 || tc::mbar_wait(pv_done, (u - 1) & 1)));
@@ -278,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!ok) break;
         }
         if (!ok || cur.end >= b) break;
-        cur = segment(w, cur.end, b);
+        cur = segment<WIDE>(w, wide, cur.end, b);
       }
     }
   } else {
@@ -290,12 +418,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto softmax_sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     for (int nseg = 0;; ++nseg) {
       const int turn = nseg & 1;   // Q's buffer
-      const int rows = min(w.qpt, (p.seq0[cur.g + 1] - p.seq0[cur.g]) * p.n_q - cur.rt * w.qpt) * p.G;
+      const int rows = cur.queries * p.G;
       const bool work = quad * 32 < rows;
-      const int len = p.len[cur.g] - cur.tile * BN;
+      const int mine = WIDE && r < rows ? shared_last(p, cur.tok + r / p.G) + 1 : 0;       // own rows that the row sees
       float m_used = -INFINITY, l = 0.f;
       for (int t = grp; t < cur.n; t += 2, ++u) {
-        const int keys = len - t * BN;
+        const int j = cur.tile + t;
+        const int keys = WIDE && j >= cur.own_tile ? mine - (j - cur.own_tile) * BN : cur.len - j * BN;    // that the row sees
         ok = ok && __all_sync(0xffffffffu, tc::mbar_wait(s_full, u & 1));
         if (work && ok) {
           uint32_t sr[BN];
@@ -304,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int c = 0; c < BN; c += 32) tc::tmem_ld32_nowait(tS + c, sr + c);
           tc::tmem_wait_ld64(sr);
           tc::tmem_wait_ld64(sr + 64);
-          if (keys < BN) {
+          if (__any_sync(0xffffffffu, keys < BN)) {
 #pragma unroll
             for (int c = 0; c < BN; ++c)
               if (c >= keys) sr[c] = 0xff800000u;
@@ -432,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         atomicAdd(read_out, 1);
       }
       if (cur.end >= b) break;     // (uniform)
-      cur = segment(w, cur.end, b);
+      cur = segment<WIDE>(w, wide, cur.end, b);
     }
   }
   if (!ok && lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_TIMEOUT);
@@ -802,7 +931,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
 
 // ---- join: one warp per (query, head) ------------------------------------------------------------
 // What does not come from the two kernels before is worked out before the wait for them.
-template <int HD>
+template <int HD, bool WIDE>
 __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc w, int own_grid) {
   const Shared& p = w.s;
   const int t = blockIdx.x, hh = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -812,7 +941,7 @@ __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc 
   int n_pre = 0, n_own = 0, r = 0;
   const float *pre = nullptr, *own = nullptr;
   const int64_t pre_step = (int64_t)w.slot_rows * (HD + 2), own_step = (int64_t)w.own_slot_rows * (HD + 2);
-  if (on && w.total > 0) {
+  if (!WIDE && on && w.total > 0) {
     int g = 0;
     while (s >= p.seq0[g + 1]) ++g;
     const int kt = (p.len[g] + BN - 1) / BN;
@@ -826,15 +955,25 @@ __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc 
   }
   const int rr = j * p.G + gh, e = s * w.row_tiles + rr / TILE, r_own = rr % TILE;
   // (the bounds were written before the call: the kernels that let this one start had waited for that)
-  const bool only = w.alone && p.capacity == 0;
+  const bool only = !WIDE && w.alone && p.capacity == 0;
   if (only) pdl_wait();
   const int raw = p.last[t], last = shared_last(p, t);
   if (raw != last && hh == 0 && lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_INDEX);
   if (!only) pdl_wait();
   pdl_trigger();
   if (!on) return;
+  if (WIDE && last > -2) {
+    const int tiles = p.n_seq * w.chunks, c = j / w.qpt, li = w.plan[2 + s * w.chunks + c];
+    if (li >= 0) {
+      const int per = w.plan[1], total = per * p.Hkv, workers = wide_workers(total, w.workers), f = w.plan[2 + tiles + li],
+                x0 = h * per + f, kt = w.plan[2 + tiles + li + 1] - f, w0 = worker_of(total, x0, workers);
+      n_pre = worker_of(total, x0 + kt - 1, workers) - w0 + 1;
+      pre = slot(w.part, w.slot_rows, HD, w0, h * w.plan[0] + li);
+      r = (j - c * w.qpt) * p.G + gh;
+    }
+  }
   if (last == -2) n_pre = 0;
-  if (last >= 0) {
+  if (!WIDE && last >= 0) {
     const int total = w.plan[p.n_seq * w.row_tiles], at = w.plan[e], n = (w.plan[e + 1] - at) / p.Hkv - kUnitCost;
     const int x0 = at + h * (n + kUnitCost) + kUnitCost;       // the unit's first step
     const int workers = own_workers(total, own_grid * kOwnWarps), w0 = worker_of(total, x0, workers);
@@ -903,7 +1042,30 @@ __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc 
 bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
   w->s = s;
   w->qpt = BM / s.G;
+  w->chunks = (s.n_q + w->qpt - 1) / w->qpt;
   int64_t at = 0, pairs = 0, rows = 0;
+  // Row tiles of one sequence each where they are not many more than tiles of a whole group's queries.
+  int64_t packed = 0;
+  for (int g = 0; g < s.n_groups; ++g) packed += ((int64_t)(s.seq0[g + 1] - s.seq0[g]) * s.n_q + w->qpt - 1) / w->qpt;
+  const int64_t tiles = (int64_t)s.n_seq * w->chunks;
+  w->wide = tiles <= kWideTiles && 4 * tiles <= 5 * packed;
+  if (w->wide) {
+    int64_t longest = 0;
+    for (int g = 0; g < s.n_groups; ++g) longest = std::max<int64_t>(longest, s.len[g]);
+    const double most = (double)tiles * s.Hkv * ((longest + BN - 1) / BN + (s.capacity + BN - 1) / BN);
+    if (most > INT32_MAX / 2 || (s.H + 7) / 8 > 65535) return false;
+    w->total = 0;
+    w->workers = (int)std::min<double>(kWorkers, std::max(1.0, (most + 1) / 2));
+    w->slot_rows = (std::min(s.n_q, w->qpt) * s.G + 3) & ~3;
+    w->alone = false;
+    w->own_part = nullptr;
+    w->row_tiles = w->own_slot_rows = 0;
+    const size_t pre = (size_t)(w->workers + tiles * s.Hkv) * w->slot_rows * sizeof(float) * (s.hd + 2), at = (pre + 255) & ~size_t(255);
+    w->part = nullptr;
+    w->plan = reinterpret_cast<int32_t*>(at);
+    *bytes = at + (2 * tiles + 3) * 4 + 16;
+    return true;
+  }
   for (int g = 0; g < s.n_groups; ++g) {
     w->first[g] = (int)at;
     w->prob[g] = (int)pairs;
@@ -978,7 +1140,8 @@ cudaError_t set_attrs() {
   std::lock_guard<std::mutex> g(g_shared_mu);
   const uint32_t bit = HD == 128 ? 1u : 2u;
   if (dev >= 0 && dev < 64 && (g_shared_attr[dev] & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(k_shared_prefix<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD>::SMEM);
+  e = cudaFuncSetAttribute(k_shared_prefix<HD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, false>::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_shared_prefix<HD, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<HD, true>::SMEM);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_shared_own<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Own<HD>::SMEM);
   if (e == cudaSuccess && dev >= 0 && dev < 64) g_shared_attr[dev] |= bit;
   return e;
@@ -990,23 +1153,35 @@ cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
   cudaError_t e = set_attrs<HD>();
   if (e != cudaSuccess) return e;
   const int64_t W = (int64_t)s.Hkv * HD;
-  if (w.total > 0) {
-    CUtensorMap q, k, v;
-    if (!make_map(&q, s.q, {HD, s.H, (int64_t)s.n_seq * s.n_q}, {64, s.G, w.qpt}) ||
-        !make_map(&k, s.k, {W, s.n_rows}, {64, BN}) || !make_map(&v, s.v, {W, s.n_rows}, {64, BN}))
+  const dim3 join(s.n_seq * s.n_q, (s.H + 7) / 8);
+  CUtensorMap q, k, v, own_k, own_v;
+  if ((w.wide || w.total > 0) && !make_map(&q, s.q, {HD, s.H, (int64_t)s.n_seq * s.n_q}, {64, s.G, w.qpt})) return cudaErrorInvalidValue;
+  if (w.wide) {
+    // (what is not there is not read: any map will do)
+    const bool pre = s.n_rows > 0, own = s.capacity > 0;
+    const int64_t rows = s.n_seq * s.capacity;
+    if ((pre && (!make_map(&k, s.k, {W, s.n_rows}, {64, BN}) || !make_map(&v, s.v, {W, s.n_rows}, {64, BN}))) ||
+        (own && (!make_map(&own_k, s.own_k, {W, rows}, {64, BN}) || !make_map(&own_v, s.own_v, {W, rows}, {64, BN}))))
       return cudaErrorInvalidValue;
-    e = launch_k(k_shared_prefix<HD>, dim3(w.workers), dim3(THREADS), Layout<HD>::SMEM, st, q, k, v, w);
+    if (!pre) k = v = q;
+    if (!own) own_k = own_v = q;
+    e = launch_k(k_shared_prefix<HD, true>, dim3(w.workers), dim3(THREADS), Layout<HD, true>::SMEM, st, q, k, v, own_k, own_v, w);
+    if (e != cudaSuccess) return e;
+    return launch_k(k_shared_join<HD, true>, join, dim3(256), 0, st, w, kOwnCtas);
+  }
+  if (w.total > 0) {
+    if (!make_map(&k, s.k, {W, s.n_rows}, {64, BN}) || !make_map(&v, s.v, {W, s.n_rows}, {64, BN})) return cudaErrorInvalidValue;
+    e = launch_k(k_shared_prefix<HD, false>, dim3(w.workers), dim3(THREADS), Layout<HD, false>::SMEM, st, q, k, v, k, v, w);
     if (e != cudaSuccess) return e;
   }
   if (s.capacity > 0) {
-    CUtensorMap k, v;
     const int64_t rows = s.n_seq * s.capacity;
     if (!make_map(&k, s.own_k, {W, rows}, {64, Own<HD>::KT}) || !make_map(&v, s.own_v, {W, rows}, {64, Own<HD>::KT}))
       return cudaErrorInvalidValue;
     e = launch_k(k_shared_own<HD>, dim3(kOwnCtas), dim3(kOwnThreads), Own<HD>::SMEM, st, k, v, w);
     if (e != cudaSuccess) return e;
   }
-  return launch_k(k_shared_join<HD>, dim3(s.n_seq * s.n_q, (s.H + 7) / 8), dim3(256), 0, st, w, kOwnCtas);
+  return launch_k(k_shared_join<HD, false>, join, dim3(256), 0, st, w, kOwnCtas);
 }
 
 }  // namespace
@@ -1020,9 +1195,10 @@ size_t shared_tc_ws_bytes(const Shared& p) {
 }
 
 int shared_tc_launches(const Shared& p) {
-  bool prefix = false;
-  for (int g = 0; g < p.n_groups; ++g) prefix = prefix || (p.len[g] > 0 && p.seq0[g + 1] > p.seq0[g]);
-  return 1 + (prefix ? 1 : 0) + (p.capacity > 0 ? 1 : 0);
+  Tc w;
+  size_t n;
+  if (!plan_tc(p, &w, &n)) return 0;
+  return w.wide ? 2 : 1 + (w.total > 0 ? 1 : 0) + (p.capacity > 0 ? 1 : 0);
 }
 
 void reset_shared_tc_caches() {
