@@ -62,6 +62,7 @@ struct Tc {
   // own rows, where they have a kernel of their own
   int row_tiles;                 // of a sequence
   int own_slot_rows;
+  int own_ctas;                  // CTAs of its kernel
   bool alone;                    // no prefix kernel runs before
   int32_t* plan;                 // [n_seq row_tiles + 1] steps before each, times Hkv; wide: how many row tiles are
                                  // live, their key tiles, [n_seq chunks] the place of each among them (-1: none of
@@ -932,7 +933,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
 // ---- join: one warp per (query, head) ------------------------------------------------------------
 // What does not come from the two kernels before is worked out before the wait for them.
 template <int HD, bool WIDE>
-__global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc w, int own_grid) {
+__global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc w) {
   const Shared& p = w.s;
   const int t = blockIdx.x, hh = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int s = t / p.n_q, j = t - s * p.n_q, h = hh / p.G, gh = hh - h * p.G;
@@ -976,7 +977,7 @@ __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc 
   if (!WIDE && last >= 0) {
     const int total = w.plan[p.n_seq * w.row_tiles], at = w.plan[e], n = (w.plan[e + 1] - at) / p.Hkv - kUnitCost;
     const int x0 = at + h * (n + kUnitCost) + kUnitCost;       // the unit's first step
-    const int workers = own_workers(total, own_grid * kOwnWarps), w0 = worker_of(total, x0, workers);
+    const int workers = own_workers(total, w.own_ctas * kOwnWarps), w0 = worker_of(total, x0, workers);
     n_own = worker_of(total, x0 + n - 1, workers) - w0 + 1;
     own = slot(w.own_part, w.own_slot_rows, HD, w0, e * p.Hkv + h);
   }
@@ -1080,6 +1081,22 @@ bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
   w->prob[s.n_groups] = (int)pairs;
   w->total = (int)at;
   w->workers = (int)std::min<int64_t>(kWorkers, (at + 1) / 2);          // (a tile for each group of warps)
+  w->own_ctas = kOwnCtas;
+  if (at > 0 && s.capacity > 0) {
+    // The own rows' kernel starts beside the prefixes', on SMs that are left to it, so that one's products and start
+    // cover the other's bytes: as many as make both last alike, as far as the host can know (caches half full; a key
+    // tile takes an SM 0.95 us of products or 1.3 of bytes, a CTA of the other kernel reads 32 GB/s and starts in 4 us).
+    // 64 answers of 56 heads over 16384 rows 45.5 us, one kernel after the other 51.5; 4 of 32 over 4096 16.2 and 19.1.
+    const double unit = (rows > 64 ? 0.95 : 1.3) * s.hd / 128, bytes = 2.0 * s.n_seq * s.capacity * s.Hkv * s.hd;
+    double best = 1e30;
+    int left = 4;
+    for (int x = 4; x <= kWorkers / 2; x += 2) {
+      const double t = std::max((double)at / (kWorkers - x) * unit + 4.0, bytes / (2 * x * 32e3) + 4.0);
+      if (t < best) best = t, left = x;
+    }
+    w->workers = std::min(w->workers, kWorkers - left);
+    w->own_ctas = 2 * left;
+  }
   w->slot_rows = (int)((rows + 3) & ~3);
   w->row_tiles = (s.n_q * s.G + TILE - 1) / TILE;
   w->own_slot_rows = (std::min(TILE, s.n_q * s.G) + 3) & ~3;
@@ -1167,7 +1184,7 @@ cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
     if (!own) own_k = own_v = q;
     e = launch_k(k_shared_prefix<HD, true>, dim3(w.workers), dim3(THREADS), Layout<HD, true>::SMEM, st, q, k, v, own_k, own_v, w);
     if (e != cudaSuccess) return e;
-    return launch_k(k_shared_join<HD, true>, join, dim3(256), 0, st, w, kOwnCtas);
+    return launch_k(k_shared_join<HD, true>, join, dim3(256), 0, st, w);
   }
   if (w.total > 0) {
     if (!make_map(&k, s.k, {W, s.n_rows}, {64, BN}) || !make_map(&v, s.v, {W, s.n_rows}, {64, BN})) return cudaErrorInvalidValue;
@@ -1178,10 +1195,10 @@ cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
     const int64_t rows = s.n_seq * s.capacity;
     if (!make_map(&k, s.own_k, {W, rows}, {64, Own<HD>::KT}) || !make_map(&v, s.own_v, {W, rows}, {64, Own<HD>::KT}))
       return cudaErrorInvalidValue;
-    e = launch_k(k_shared_own<HD>, dim3(kOwnCtas), dim3(kOwnThreads), Own<HD>::SMEM, st, k, v, w);
+    e = launch_k(k_shared_own<HD>, dim3(w.own_ctas), dim3(kOwnThreads), Own<HD>::SMEM, st, k, v, w);
     if (e != cudaSuccess) return e;
   }
-  return launch_k(k_shared_join<HD, false>, join, dim3(256), 0, st, w, kOwnCtas);
+  return launch_k(k_shared_join<HD, false>, join, dim3(256), 0, st, w);
 }
 
 }  // namespace
