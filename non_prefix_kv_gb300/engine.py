@@ -141,13 +141,28 @@ class ChunkPoolQ8:
 
 
 class BlendEngine:
-    def __init__(self, dm: DeviceModel, n_tok_max: int, max_pos: Optional[int] = None, device="cuda"):
+    def __init__(self, dm: DeviceModel, n_tok_max: int, max_pos: Optional[int] = None, device="cuda",
+                 rope: Optional[B.cb_rope_spec] = None):
+        """rope: how the model's positions are scaled (binding.rope_spec, interleaved pairs of the whole
+        head); None: its plain rope_base."""
         self.dm = dm
         self.device = device
         s = dm.shape
         self.max_pos = int(max_pos or n_tok_max)
         self.cos_sin = torch.empty(self.max_pos * s.head_dim, dtype=torch.float32, device=device)
-        B.cb_rope_table(self.cos_sin, self.max_pos, s.head_dim, float(s.rope_base))
+        if rope is None:
+            B.cb_rope_table(self.cos_sin, self.max_pos, s.head_dim, float(s.rope_base))
+        else:
+            if rope.layout != B.CB_ROPE_INTERLEAVED or rope.rot_dim != s.head_dim:
+                raise ValueError("a blend rotates interleaved pairs of the whole head")
+            B.cb_rope_table_scaled(self.cos_sin, self.max_pos, rope)
+        # cached keys carry the scaling's amplitude already: they are re-positioned without it
+        self.cos_sin_shift = self.cos_sin
+        if rope is not None and rope.amplitude != 1.0:
+            self.cos_sin_shift = torch.empty_like(self.cos_sin)
+            plain = B.rope_spec(rope.layout, rope.rot_dim, rope.base, rope.scaling, rope.factor, rope.original_len,
+                                rope.low, rope.high)
+            B.cb_rope_table_scaled(self.cos_sin_shift, self.max_pos, plain)
         self.ws = torch.empty(B.cb_workspace_bytes(dm.dims, n_tok_max, n_tok_max), dtype=torch.uint8,
                               device=device)
         self.n_tok_max = n_tok_max
@@ -560,11 +575,11 @@ def run_blend(req: Request, plan, dev_mode: int = B.CB_DEV_KV, sel_override=None
             if isinstance(req.pool, ChunkPoolQ8):
                 p = req.pool
                 B.cb_rope_shift_q8(kd, vd, p.kq[l], p.vq[l], p.ks[l], p.kz[l], p.vs[l], p.vz[l], src,
-                                   req.n_pool_rows, req.qrow[c0:c0 + n], len(p.lens), dl, n, dims, eng.cos_sin,
+                                   req.n_pool_rows, req.qrow[c0:c0 + n], len(p.lens), dl, n, dims, eng.cos_sin_shift,
                                    eng.max_pos, st)
             else:
-                B.cb_rope_shift(kd, vd, req.pool.k[l], req.pool.v[l], src, dl, n, dims, eng.cos_sin, eng.max_pos,
-                                st)
+                B.cb_rope_shift(kd, vd, req.pool.k[l], req.pool.v[l], src, dl, n, dims, eng.cos_sin_shift,
+                                eng.max_pos, st)
 
     skip = set(pre) if recompute_precheck_kv else set()
     partial = {l: req.pool_ranges(split) for l in pre} if split is not None else {}
