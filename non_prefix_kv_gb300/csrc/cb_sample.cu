@@ -52,6 +52,9 @@ constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kScale = 42;                   // a weight of 1 is 2^42: 2^20 of them stay below 2^63
 constexpr int kList = 2048;                  // ids that one CTA finishes
 constexpr int kSmallK = 1024;
+constexpr int kPer = kList / kThreads;       // ids of a list that a thread holds, neighbours
+constexpr int kMembers = 256;                // ids of a class that are compared one by one
+constexpr int kStage = kList / kWarps;       // ids that a warp holds before it knows their places
 constexpr int kGroups = 4096;                // groups whose largest logits bound the k-th: eight a thread at most
 
 struct Find {           // where the order's prefix ends: in this class,
@@ -62,22 +65,23 @@ struct Find {           // where the order's prefix ends: in this class,
 struct Shared {
   union {
     struct {
-      uint32_t cnt[kBins];                   // of this CTA's ids in a class, or
+      uint32_t cnt[kBins];                   // ids in a class, and
       union {
         u64 sum[kBins];                      // their weights, or
-        uint32_t part[2][kBins];             // (beside the counts) the parts of these above their class's base
+        uint32_t part[2][kBins];             // the parts of these above their class's base
       };
     };
+    u64 order[kList];                        // ids on their way to a list; a list's sort keys
     struct {
-      u64 order[kList];                      // a list's sort keys, then its kept weights
-      union {
-        struct {
-          uint32_t key[kList];               // a list's keys and ids, in order of the ids
-          int32_t id[kList];
-        };
-        uint32_t group[kGroups];             // the largest key of each group of ids
-      };
+      u64 member[kMembers], member_weight[kMembers], before[kMembers];
     };
+  };
+  union {
+    struct {
+      uint32_t key[kList];                   // a list's keys and ids, in order of the ids
+      int32_t id[kList];
+    };
+    uint32_t group[kGroups];                 // the largest key of each group of ids
   };
   u64 tile_mass[kMaxTiles];                  // kept weight of a tile (ties: how many)
   uint2 table[32];                           // 2^31 2^(j / 32), and the same in fp32
@@ -88,6 +92,8 @@ struct Shared {
   uint32_t part_count[kMaxCluster];
   float part_max[kMaxCluster];
   Find found;
+  u64 mass;
+  uint32_t members[2];
   uint32_t cutoff, border;
   float least;
   double least_off;      // T ln of the least share
@@ -380,11 +386,11 @@ struct Row {
     });
     meet();
     // this CTA's share of the classes, in falling order; a thread holds up to four neighbours
-    constexpr int kPer = kBins / kThreads;
+    constexpr int kOwn = kBins / kThreads;
     const int share = kBins / nc, per = share > kThreads ? share / kThreads : 1;
-    u64 m[kPer], ms = 0, mt;
+    u64 m[kOwn], ms = 0, mt;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < kOwn; ++j) {
       m[j] = 0;
       const int i = tid * per + j;
       if (j < per && i < share) {
@@ -418,7 +424,7 @@ struct Row {
     }
     const u64 target = want(all);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
+    for (int j = 0; j < kOwn; ++j) {
       if (mb < target && target <= mb + m[j]) {
         const Find r{mb, m[j], (uint32_t)(kBins - 1 - (rank * share + tid * per + j))};
         for (int q = 0; q < nc; ++q) at(q)->found = r;
@@ -435,18 +441,41 @@ struct Row {
   __device__ __forceinline__ uint32_t gather(Take take, u64* weight_of_all) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tpw = (tiles + kWarps - 1) / kWarps, t0 = warp * tpw, t1 = min(tiles, t0 + tpw);
-    uint32_t n = 0;
+    u64* stage = s->order + warp * kStage;
+    uint32_t found = 0;                      // of this warp
     u64 m = 0;
-    each(t0, t1, 1, [&](int, const float* f, int) {
+    // put(place among the warp's, key, id) for those taken
+    auto walk = [&](auto put, bool mass) {
+      found = 0;
+      each(t0, t1, 1, [&](int id, const float* f, int) {
+        uint32_t c = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        n += take(f[i]);
-        if (MASS && f[i] > -INFINITY) m = add(m, f[i]);
-      }
-    });
-    uint32_t ct;
+        for (int i = 0; i < 8; ++i) {
+          c += take(f[i]);
+          if (MASS && mass && f[i] > -INFINITY) m = add(m, f[i]);
+        }
+        if (!__any_sync(0xffffffffu, c)) return;
+        uint32_t incl = c;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += y;
+        }
+        uint32_t to = found + incl - c;
+        if (c) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (take(f[i])) put(to++, key_of<T>(f[i]), id + i);
+        }
+        found += __shfl_sync(0xffffffffu, incl, 31);
+      });
+    };
+    walk([&](uint32_t to, uint32_t key, int id) {
+      if (to < kStage) stage[to] = (u64)key << 32 | (uint32_t)id;
+    }, true);
+    uint32_t before = lane ? 0 : found, ct;
     u64 mt;
-    scan(n, m, ct, mt);
+    scan(before, m, ct, mt);
     if (tid < nc) {
       at(tid)->part_count[rank] = ct;
       if (MASS) at(tid)->part_mass[rank] = mt;
@@ -462,30 +491,16 @@ struct Row {
     if (MASS) *weight_of_all = all;
     if (total <= kList) {
       Shared* o = at(0);
-      // (the warp's first lane has the sum of the warps before it)
-      base += __shfl_sync(0xffffffffu, n, 0);
-      each(t0, t1, 1, [&](int id, const float* f, int) {
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c += take(f[i]);
-        if (!__any_sync(0xffffffffu, c)) return;
-        uint32_t incl = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, d);
-          if (lane >= d) incl += y;
-        }
-        uint32_t to = base + incl - c;
-        if (c) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (take(f[i])) {
-              o->key[to] = key_of<T>(f[i]);
-              o->id[to++] = id + i;
-            }
-        }
-        base += __shfl_sync(0xffffffffu, incl, 31);
-      });
+      base += __shfl_sync(0xffffffffu, before, 0);
+      auto put = [&](uint32_t to, uint32_t key, int id) {
+        o->key[base + to] = key;
+        o->id[base + to] = id;
+      };
+      if (found <= kStage) {
+        for (uint32_t i = lane; i < found; i += 32) put(i, (uint32_t)(stage[i] >> 32), (int)(uint32_t)stage[i]);
+      } else {
+        walk(put, false);                    // more than there is room for: once more
+      }
     }
     meet();
     return total;
@@ -522,61 +537,235 @@ struct Row {
     __syncthreads();
   }
 
-  // The first CTA's list of n to the row's token.  all: the weight that p is a share of; 0: of the k kept.
-  __device__ __forceinline__ void finish(int n, const Rules& r, u64 all, const Args& a, int row) {
-    constexpr int kPer = kList / kThreads;
-    const int tid = threadIdx.x;
-    const uint32_t k = min(r.k, (uint32_t)n);
-    const bool sorted = r.p_on || k < (uint32_t)n;
-    if (sorted) sort(n);
-    u64 w[kPer], m = 0, mt;
-    uint32_t at_[kPer], key[kPer], c = 0, ct;
+  // A thread's part of a list of n: places tid kPer + j.
+  __device__ __forceinline__ void list(int n, uint32_t (&key)[kPer], u64 (&w)[kPer], bool (&keep)[kPer]) const {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t i = tid * kPer + j;
-      w[j] = 0;
-      at_[j] = i;
-      key[j] = 0;
-      if (i < k) {
-        if (sorted) {
-          at_[j] = (uint32_t)s->order[i];
-          key[j] = ~(uint32_t)(s->order[i] >> 32);
-        } else {
-          key[j] = s->key[i];
-        }
-        w[j] = weigh(value_of<T>(key[j]));
+      const int i = threadIdx.x * kPer + j;
+      keep[j] = i < n;
+      key[j] = i < n ? s->key[i] : 0u;
+      w[j] = i < n ? weigh(value_of<T>(key[j])) : 0ull;
+    }
+  }
+
+  // Which of a list (all of its ids kept when called) are among the first k of the order, and of those (p_on) come
+  // before want(the weight of all of them) of weight is reached, with `above` before the list; the id at which it is
+  // reached becomes border and cutoff.  The keys fall into classes, or the values into classes of one width, and only
+  // the ids of the class in which the order ends are compared with one another.  With more than kMembers of them that
+  // are not equal the list is sorted, which takes 12 us of a CTA for 2048 ids.
+  template <typename Want>
+  __device__ __forceinline__ void select(int n, uint32_t k, bool p_on, u64 above, Want want, const uint32_t (&key)[kPer],
+                                         const u64 (&w)[kPer], bool (&keep)[kPer]) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (keep[j]) {
+        lo = min(lo, key[j]);
+        hi = max(hi, key[j]);
       }
-      m += w[j];
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    __syncthreads();                         // (what was there is read)
+    if (lane == 0) {
+      s->warp_count[warp] = lo;
+      s->warp_mass[warp] = hi;
     }
-    u64 before = m;
-    scan(c, before, ct, mt);
-    const u64 target = r.p_on ? share_of(all ? all : mt, r.p) : ~0ull;
-    c = 0;
+    for (int i = tid; i < kBins; i += kThreads) {
+      s->cnt[i] = 0;
+      s->sum[i] = 0;
+    }
+    if (tid < 2) s->members[tid] = 0;
+    if (tid == 2) s->mass = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      lo = min(lo, s->warp_count[i]);
+      hi = max(hi, (uint32_t)s->warp_mass[i]);
+    }
+    const float vlo = value_of<T>(lo), scale = (float)(kBins - 1) / (value_of<T>(hi) - vlo);
+    const bool exact = hi - lo < kBins;      // a class for every key (bf16, mostly)
+    int bin[kPer];                           // (what is no number, with infinite ends, is class 0)
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      bin[j] = exact ? (int)(key[j] - lo) : min(kBins - 1, __float2int_rz((value_of<T>(key[j]) - vlo) * scale));
+      if (keep[j]) {
+        atomicAdd(&s->cnt[bin[j]], 1u);
+        atomicAdd(&s->sum[bin[j]], w[j]);
+      }
+    }
+    __syncthreads();
+    constexpr int kOwn = kBins / kThreads;   // classes of a thread, in falling order
+    uint32_t c[kOwn], cb = 0, ct;
+    u64 m[kOwn], mb = 0, mt;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+      cb += c[j] = s->cnt[kBins - 1 - (tid * kOwn + j)];
+      mb += m[j] = s->sum[kBins - 1 - (tid * kOwn + j)];
+    }
+    scan(cb, mb, ct, mt);
+    mb += above;
+    // how much (how many, or their weight) of a class lies before each of its ids
+    u64 ahead[kPer];
+    auto order_class = [&](auto weighted, int b) -> bool {
+      constexpr int which = decltype(weighted)::value ? 1 : 0;
+      if (exact) {                           // equals, in order of their ids
+        uint32_t x = 0, all;
+        u64 none = 0, no;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x += keep[j] && bin[j] == b;
+        scan(x, none, all, no);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          ahead[j] = which ? x * w[j] : x;
+          x += keep[j] && bin[j] == b;
+        }
+        return true;
+      }
+      uint32_t slot[kPer];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (keep[j] && bin[j] == b) {
+          slot[j] = atomicAdd(&s->members[which], 1u);
+          if (slot[j] < kMembers) {          // its place in the order: all bits of the key inverted, place in the list
+            s->member[slot[j]] = (u64)~key[j] << 32 | (uint32_t)(tid * kPer + j);
+            s->member_weight[slot[j]] = which ? w[j] : 1ull;
+            s->before[slot[j]] = 0;
+          }
+        }
+      __syncthreads();
+      const int many = (int)s->members[which], i = tid % kMembers;
+      if (many > kMembers) return false;
+      if (i < many) {
+        const u64 mine = s->member[i];
+        u64 sum = 0;
+#pragma unroll 4
+        for (int x = tid / kMembers; x < many; x += kThreads / kMembers) sum += s->member[x] < mine ? s->member_weight[x] : 0ull;
+        if (sum) atomicAdd(&s->before[i], sum);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (keep[j] && bin[j] == b) ahead[j] = s->before[slot[j]];
+      return true;
+    };
+    int kb = -1;                             // the class in which the first k end
+    u64 mk = above + mt, mk_above = 0, target = 0;       // weight up to the end of the first k, and before its class
+    bool few = true;
+    if (k < (uint32_t)n) {
+      u64 run = mb;
+#pragma unroll
+      for (int j = 0; j < kOwn; ++j) {
+        if (cb < k && k <= cb + c[j]) s->found = Find{run, cb, (uint32_t)(kBins - 1 - (tid * kOwn + j))};
+        cb += c[j];
+        run += m[j];
+      }
+      __syncthreads();
+      kb = (int)s->found.bin;
+      mk_above = s->found.above;
+      const uint32_t quota = k - (uint32_t)s->found.in;
+      few = order_class(std::false_type{}, kb);
+      if (few) {
+        u64 more = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (keep[j] && bin[j] <= kb) {
+            keep[j] = bin[j] == kb && ahead[j] < quota;
+            more += keep[j] ? w[j] : 0ull;
+          }
+        if (more) atomicAdd(&s->mass, more);
+        __syncthreads();
+        mk = mk_above + s->mass;
+      }
+    }
+    if (few && p_on) {
+      target = want(mk - above);
+      if (target <= mk) {                    // (else all of them come before it)
+        int pb = kb;
+        u64 before = mk_above;
+        if (kb < 0 || target <= mk_above) {
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            if (mb < target && target <= mb + m[j]) s->found = Find{mb, 0, (uint32_t)(kBins - 1 - (tid * kOwn + j))};
+            mb += m[j];
+          }
+          __syncthreads();
+          pb = (int)s->found.bin;
+          before = s->found.above;
+        }
+        few = order_class(std::true_type{}, pb);
+        if (few) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j)
+            if (keep[j] && bin[j] <= pb) {
+              const u64 run = bin[j] == pb ? before + ahead[j] : target;
+              keep[j] = run < target;
+              if (keep[j] && target <= run + w[j]) {
+                s->border = key[j];
+                s->cutoff = s->id[tid * kPer + j];
+              }
+            }
+        }
+      }
+    }
+    if (few) return;
+    __syncthreads();
+    sort(n);
+    u64 ws[kPer], run = 0;
+    uint32_t none = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const uint32_t i = tid * kPer + j;
-      const bool keep = i < k && before < target && value_of<T>(key[j]) >= r.least;
-      before += w[j];
-      c += keep;
-      if (!keep) w[j] = 0;
+      run += ws[j] = i < k && i < (uint32_t)n ? weigh(value_of<T>(~(uint32_t)(s->order[i] >> 32))) : 0ull;
     }
-    // (sort keys have been read: scan's barriers lie between)
-    for (int i = tid; i < kList; i += kThreads) s->order[i] = 0;
+    scan(none, run, ct, mt);
+    target = want(mt);
+    run += above;
+    uint32_t kept = 0;                       // bit j
+    int place[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t i = tid * kPer + j;
+      place[j] = i < (uint32_t)n ? (int)(uint32_t)s->order[i] : -1;
+      if (i < k && i < (uint32_t)n && (!p_on || run < target)) {
+        kept |= 1u << j;
+        if (p_on && target <= run + ws[j]) {
+          s->border = ~(uint32_t)(s->order[i] >> 32);
+          s->cutoff = s->id[place[j]];
+        }
+      }
+      run += ws[j];
+    }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPer; ++j)
-      if (w[j]) s->order[at_[j]] = w[j];
+      if (place[j] >= 0) s->order[place[j]] = kept >> j & 1;
     __syncthreads();
-    m = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) keep[j] = tid * kPer + j < n && s->order[tid * kPer + j] != 0;
+  }
+
+  // The first CTA's list of n to the row's token.  all: the weight that p is a share of; 0: of the k kept.
+  __device__ __forceinline__ void finish(int n, const Rules& r, u64 all, const Args& a, int row) {
+    const int tid = threadIdx.x;
+    const uint32_t k = min(r.k, (uint32_t)n);
+    uint32_t key[kPer], kept = 0, ct;
+    u64 w[kPer], m = 0, mt;
+    bool keep[kPer];
+    list(n, key, w, keep);
+    if (r.p_on || k < (uint32_t)n) select(n, k, r.p_on, 0ull, [&](u64 of) { return share_of(all ? all : of, r.p); }, key, w, keep);
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      w[j] = s->order[tid * kPer + j];
+      if (!keep[j] || value_of<T>(key[j]) < r.least) {
+        w[j] = 0;
+      } else {
+        ++kept;
+      }
       m += w[j];
     }
-    uint32_t kept = c;
     scan(kept, m, ct, mt);
     draw(m, mt, w, [&](int j, float* v) {
-      *v = value_of<T>(s->key[tid * kPer + j]);
+      *v = value_of<T>(key[j]);
       return s->id[tid * kPer + j];
     }, r, a, row);
     if (tid == 0 && a.kept) a.kept[row] = (int32_t)ct;
@@ -612,8 +801,8 @@ struct Row {
         if (g && (level == 0 || g >> upto == prefix)) atomicAdd(&s->cnt[g >> shift & (kBins - 1)], 1u);
       }
       __syncthreads();
-      constexpr int kPer = kBins / kThreads;
-      uint32_t c[kPer], cs = 0, ct;
+      constexpr int kOwn = kBins / kThreads;
+      uint32_t c[kOwn], cs = 0, ct;
       u64 m = 0, mt;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) cs += c[j] = s->cnt[kBins - 1 - (tid * kPer + j)];
@@ -856,28 +1045,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
     const uint32_t held = R.template gather<false>(in_class, nullptr);
     if (held <= kList) {
       if (R.rank == 0) {
-        R.sort(held);
-        constexpr int kPer = kList / kThreads;
-        u64 w[kPer], before = 0, mt;
-        uint32_t z = 0, ct;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const uint32_t i = tid * kPer + j;
-          w[j] = i < held ? R.weigh(value_of<T>(~(uint32_t)(sh.order[i] >> 32))) : 0ull;
-          before += w[j];
-        }
-        R.scan(z, before, ct, mt);
-        before += f.above;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          if (before < target && target <= before + w[j]) {
-            const u64 o = sh.order[tid * kPer + j];
-            for (int q = 0; q < R.nc; ++q) {
-              R.at(q)->border = ~(uint32_t)(o >> 32);
-              R.at(q)->cutoff = sh.id[(uint32_t)o];
-            }
-          }
-          before += w[j];
+        uint32_t key[kPer];
+        u64 w[kPer];
+        bool keep[kPer];
+        R.list(held, key, w, keep);
+        R.select(held, held, true, f.above, [&](u64) { return target; }, key, w, keep);
+        __syncthreads();
+        if (tid > 0 && tid < R.nc) {
+          R.at(tid)->border = sh.border;
+          R.at(tid)->cutoff = sh.cutoff;
         }
       }
       R.meet();
