@@ -52,7 +52,7 @@ constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kScale = 42;                   // a weight of 1 is 2^42: 2^20 of them stay below 2^63
 constexpr int kList = 2048;                  // ids that one CTA finishes
 constexpr int kSmallK = 1024;
-constexpr int kPer = kList / kThreads;       // ids of a list that a thread holds, neighbours
+constexpr int kClasses = kThreads;           // of a list
 constexpr int kMembers = 256;                // ids of a class that are compared one by one
 constexpr int kStage = kList / kWarps;       // ids that a warp holds before it knows their places
 constexpr int kGroups = 4096;                // groups whose largest logits bound the k-th: eight a thread at most
@@ -92,8 +92,7 @@ struct Shared {
   uint32_t part_count[kMaxCluster];
   float part_max[kMaxCluster];
   Find found;
-  u64 mass;
-  uint32_t members[2];
+  uint32_t members;
   uint32_t cutoff, border;
   float least;
   double least_off;      // T ln of the least share
@@ -337,16 +336,18 @@ struct Row {
       s->warp_mass[warp] = mi;
     }
     __syncthreads();
-    ct = 0;
+    // (a lane for each warp's sums; of 64 bits 21 at a time, and no carry is lost)
+    const uint32_t wc = lane < kWarps ? s->warp_count[lane] : 0u;
+    const u64 wm = lane < kWarps ? s->warp_mass[lane] : 0ull;
+    const bool before = lane < warp;
+    ct = __reduce_add_sync(0xffffffffu, wc);
+    ci += __reduce_add_sync(0xffffffffu, before ? wc : 0u);
     mt = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        ci += s->warp_count[w];
-        mi += s->warp_mass[w];
-      }
-      ct += s->warp_count[w];
-      mt += s->warp_mass[w];
+    for (int i = 0; i < 63; i += 21) {
+      const uint32_t part = (uint32_t)(wm >> i) & 0x1fffffu;
+      mt += (u64)__reduce_add_sync(0xffffffffu, part) << i;
+      mi += (u64)__reduce_add_sync(0xffffffffu, before ? part : 0u) << i;
     }
     c = ci - c;
     m = mi - m;
@@ -537,33 +538,23 @@ struct Row {
     __syncthreads();
   }
 
-  // A thread's part of a list of n: places tid kPer + j.
-  __device__ __forceinline__ void list(int n, uint32_t (&key)[kPer], u64 (&w)[kPer], bool (&keep)[kPer]) const {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int i = threadIdx.x * kPer + j;
-      keep[j] = i < n;
-      key[j] = i < n ? s->key[i] : 0u;
-      w[j] = i < n ? weigh(value_of<T>(key[j])) : 0ull;
-    }
-  }
-
-  // Which of a list (all of its ids kept when called) are among the first k of the order, and of those (p_on) come
-  // before want(the weight of all of them) of weight is reached, with `above` before the list; the id at which it is
-  // reached becomes border and cutoff.  The keys fall into classes, or the values into classes of one width, and only
-  // the ids of the class in which the order ends are compared with one another.  With more than kMembers of them that
-  // are not equal the list is sorted, which takes 12 us of a CTA for 2048 ids.
-  template <typename Want>
-  __device__ __forceinline__ void select(int n, uint32_t k, bool p_on, u64 above, Want want, const uint32_t (&key)[kPer],
-                                         const u64 (&w)[kPer], bool (&keep)[kPer]) {
+  // Which of a list are among the first k of the order, and of those (p_on) come before a target of weight is reached,
+  // with `above` before the list: `of`, or (above = 0) the share p of it, of the weight of the first k with of = 0.  The
+  // id at which it is reached becomes border and cutoff; the others' ids get their top bit set.
+  // Keys (bf16: there are few of them) or ranges of values are classes; only the ids of the class in which the order
+  // ends are compared with one another, equals by counting.  With more than kMembers of them that are not equal the
+  // list is sorted, which takes 12 us of a CTA for 2048 ids.
+  // One CTA runs through this once a row, and instructions that it meets for the first time cost it more than what
+  // they do: loops stay loops, and the first k and p go the same way (unrolled, k = 50 with p took 2 us more).
+  __device__ __forceinline__ void select(int n, uint32_t k, bool p_on, u64 above, u64 of, u64 share) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int per = (n + kThreads - 1) / kThreads, i0 = min(n, tid * per), i1 = min(n, i0 + per);
     uint32_t lo = 0xffffffffu, hi = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (keep[j]) {
-        lo = min(lo, key[j]);
-        hi = max(hi, key[j]);
-      }
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      lo = min(lo, s->key[i]);
+      hi = max(hi, s->key[i]);
+    }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     __syncthreads();                         // (what was there is read)
@@ -571,220 +562,149 @@ struct Row {
       s->warp_count[warp] = lo;
       s->warp_mass[warp] = hi;
     }
-    for (int i = tid; i < kBins; i += kThreads) {
-      s->cnt[i] = 0;
-      s->sum[i] = 0;
-    }
-    if (tid < 2) s->members[tid] = 0;
-    if (tid == 2) s->mass = 0;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      lo = min(lo, s->warp_count[i]);
-      hi = max(hi, (uint32_t)s->warp_mass[i]);
-    }
-    const float vlo = value_of<T>(lo), scale = (float)(kBins - 1) / (value_of<T>(hi) - vlo);
-    const bool exact = hi - lo < kBins;      // a class for every key (bf16, mostly)
-    int bin[kPer];                           // (what is no number, with infinite ends, is class 0)
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      bin[j] = exact ? (int)(key[j] - lo) : min(kBins - 1, __float2int_rz((value_of<T>(key[j]) - vlo) * scale));
-      if (keep[j]) {
-        atomicAdd(&s->cnt[bin[j]], 1u);
-        atomicAdd(&s->sum[bin[j]], w[j]);
-      }
-    }
-    __syncthreads();
-    constexpr int kOwn = kBins / kThreads;   // classes of a thread, in falling order
-    uint32_t c[kOwn], cb = 0, ct;
-    u64 m[kOwn], mb = 0, mt;
-#pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
-      cb += c[j] = s->cnt[kBins - 1 - (tid * kOwn + j)];
-      mb += m[j] = s->sum[kBins - 1 - (tid * kOwn + j)];
-    }
-    scan(cb, mb, ct, mt);
-    mb += above;
-    // how much (how many, or their weight) of a class lies before each of its ids
-    u64 ahead[kPer];
-    auto order_class = [&](auto weighted, int b) -> bool {
-      constexpr int which = decltype(weighted)::value ? 1 : 0;
-      if (exact) {                           // equals, in order of their ids
-        uint32_t x = 0, all;
-        u64 none = 0, no;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) x += keep[j] && bin[j] == b;
-        scan(x, none, all, no);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          ahead[j] = which ? x * w[j] : x;
-          x += keep[j] && bin[j] == b;
-        }
-        return true;
-      }
-      uint32_t slot[kPer];
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (keep[j] && bin[j] == b) {
-          slot[j] = atomicAdd(&s->members[which], 1u);
-          if (slot[j] < kMembers) {          // its place in the order: all bits of the key inverted, place in the list
-            s->member[slot[j]] = (u64)~key[j] << 32 | (uint32_t)(tid * kPer + j);
-            s->member_weight[slot[j]] = which ? w[j] : 1ull;
-            s->before[slot[j]] = 0;
-          }
-        }
-      __syncthreads();
-      const int many = (int)s->members[which], i = tid % kMembers;
-      if (many > kMembers) return false;
-      if (i < many) {
-        const u64 mine = s->member[i];
-        u64 sum = 0;
-#pragma unroll 4
-        for (int x = tid / kMembers; x < many; x += kThreads / kMembers) sum += s->member[x] < mine ? s->member_weight[x] : 0ull;
-        if (sum) atomicAdd(&s->before[i], sum);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (keep[j] && bin[j] == b) ahead[j] = s->before[slot[j]];
-      return true;
+    lo = __reduce_min_sync(0xffffffffu, s->warp_count[lane % kWarps]);
+    hi = __reduce_max_sync(0xffffffffu, (uint32_t)s->warp_mass[lane % kWarps]);
+    const bool exact = hi - lo < kClasses;   // a class for every key
+    const float vlo = value_of<T>(lo), scale = (float)(kClasses - 1) / (value_of<T>(hi) - vlo);
+    auto class_in = [&](uint32_t key) -> int {           // (what is no number, with infinite ends, is class 0)
+      return exact ? (int)(key - lo) : min(kClasses - 1, __float2int_rz((value_of<T>(key) - vlo) * scale));
     };
-    int kb = -1;                             // the class in which the first k end
-    u64 mk = above + mt, mk_above = 0, target = 0;       // weight up to the end of the first k, and before its class
     bool few = true;
-    if (k < (uint32_t)n) {
-      u64 run = mb;
-#pragma unroll
-      for (int j = 0; j < kOwn; ++j) {
-        if (cb < k && k <= cb + c[j]) s->found = Find{run, cb, (uint32_t)(kBins - 1 - (tid * kOwn + j))};
-        cb += c[j];
-        run += m[j];
+    uint32_t none = 0, no;
+    u64 mt;
+#pragma unroll 1
+    for (int by = k < (uint32_t)n ? 0 : 1; by < (p_on ? 2 : 1); ++by) {      // by number, by weight
+      auto amount = [&](uint32_t key) -> u64 { return by ? weigh(value_of<T>(key)) : 1ull; };
+      s->sum[tid] = 0;
+      if (tid == 0) s->members = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i)
+        if (s->id[i] >= 0) atomicAdd(&s->sum[class_in(s->key[i])], amount(s->key[i]));
+      __syncthreads();
+      const u64 m = s->sum[kClasses - 1 - tid], front = by ? above : 0ull;
+      u64 mb = m;
+      scan(none, mb, no, mt);
+      none = 0;
+      mb += front;
+      const u64 limit = by ? (above ? of : share_of(of ? of : mt, share)) : (u64)k;
+      if (limit > front + mt) break;         // all of them come before it
+      if (mb < limit && limit <= mb + m) {
+        s->found.bin = kClasses - 1 - tid;
+        s->found.above = mb;
       }
       __syncthreads();
-      kb = (int)s->found.bin;
-      mk_above = s->found.above;
-      const uint32_t quota = k - (uint32_t)s->found.in;
-      few = order_class(std::false_type{}, kb);
-      if (few) {
-        u64 more = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (keep[j] && bin[j] <= kb) {
-            keep[j] = bin[j] == kb && ahead[j] < quota;
-            more += keep[j] ? w[j] : 0ull;
-          }
-        if (more) atomicAdd(&s->mass, more);
-        __syncthreads();
-        mk = mk_above + s->mass;
+      const int b = (int)s->found.bin;
+      const u64 base = s->found.above;
+      auto decide = [&](int i, u64 at, u64 w) {          // `at` of the order lies before it
+        if (at >= limit) {
+          s->id[i] |= 0x80000000;
+        } else if (by && limit <= at + w) {
+          s->border = s->key[i];
+          s->cutoff = s->id[i];
+        }
+      };
+      uint32_t x = 0;
+      if (exact) {
+#pragma unroll 1
+        for (int i = i0; i < i1; ++i) x += s->id[i] >= 0 && class_in(s->key[i]) == b;
+        u64 zero = 0, z;
+        scan(x, zero, no, z);
       }
-    }
-    if (few && p_on) {
-      target = want(mk - above);
-      if (target <= mk) {                    // (else all of them come before it)
-        int pb = kb;
-        u64 before = mk_above;
-        if (kb < 0 || target <= mk_above) {
-#pragma unroll
-          for (int j = 0; j < kOwn; ++j) {
-            if (mb < target && target <= mb + m[j]) s->found = Find{mb, 0, (uint32_t)(kBins - 1 - (tid * kOwn + j))};
-            mb += m[j];
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) {
+        if (s->id[i] < 0) continue;
+        const uint32_t key = s->key[i];
+        const int c = class_in(key);
+        if (c < b) s->id[i] |= 0x80000000;
+        if (c != b) continue;
+        const u64 w = amount(key);
+        if (exact) {
+          decide(i, base + w * x++, w);
+        } else {
+          const uint32_t to = atomicAdd(&s->members, 1u);
+          if (to < kMembers) {               // its place in the order: all bits of the key inverted, place in the list
+            s->member[to] = (u64)~key << 32 | (uint32_t)i;
+            s->member_weight[to] = w;
+            s->before[to] = base;
           }
-          __syncthreads();
-          pb = (int)s->found.bin;
-          before = s->found.above;
         }
-        few = order_class(std::true_type{}, pb);
-        if (few) {
-#pragma unroll
-          for (int j = 0; j < kPer; ++j)
-            if (keep[j] && bin[j] <= pb) {
-              const u64 run = bin[j] == pb ? before + ahead[j] : target;
-              keep[j] = run < target;
-              if (keep[j] && target <= run + w[j]) {
-                s->border = key[j];
-                s->cutoff = s->id[tid * kPer + j];
-              }
-            }
+      }
+      __syncthreads();
+      if (!exact) {
+        const int many = (int)s->members, i = tid % kMembers;
+        if (many > kMembers) {
+          few = false;
+          break;
         }
+        if (i < many) {
+          const u64 mine = s->member[i];
+          u64 sum = 0;
+          for (int y = tid / kMembers; y < many; y += kThreads / kMembers) sum += s->member[y] < mine ? s->member_weight[y] : 0ull;
+          if (sum) atomicAdd(&s->before[i], sum);
+        }
+        __syncthreads();
+        if (tid < many) decide((int)(uint32_t)s->member[tid], s->before[tid], s->member_weight[tid]);
+        __syncthreads();
       }
     }
     if (few) return;
     __syncthreads();
     sort(n);
-    u64 ws[kPer], run = 0;
-    uint32_t none = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint32_t i = tid * kPer + j;
-      run += ws[j] = i < k && i < (uint32_t)n ? weigh(value_of<T>(~(uint32_t)(s->order[i] >> 32))) : 0ull;
+    u64 run = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      s->id[i] &= 0x7fffffff;
+      if (i < k) run += weigh(value_of<T>(~(uint32_t)(s->order[i] >> 32)));
     }
-    scan(none, run, ct, mt);
-    target = want(mt);
+    scan(none, run, no, mt);
+    const u64 limit = p_on ? (above ? of : share_of(of ? of : mt, share)) : ~0ull;
     run += above;
-    uint32_t kept = 0;                       // bit j
-    int place[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint32_t i = tid * kPer + j;
-      place[j] = i < (uint32_t)n ? (int)(uint32_t)s->order[i] : -1;
-      if (i < k && i < (uint32_t)n && (!p_on || run < target)) {
-        kept |= 1u << j;
-        if (p_on && target <= run + ws[j]) {
-          s->border = ~(uint32_t)(s->order[i] >> 32);
-          s->cutoff = s->id[place[j]];
-        }
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const int at = (int)(uint32_t)s->order[i];
+      if (i >= k || run >= limit) {
+        s->id[at] |= 0x80000000;
+        continue;
       }
-      run += ws[j];
+      const u64 w = weigh(value_of<T>(~(uint32_t)(s->order[i] >> 32)));
+      if (limit <= run + w) {
+        s->border = s->key[at];
+        s->cutoff = s->id[at];
+      }
+      run += w;
     }
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (place[j] >= 0) s->order[place[j]] = kept >> j & 1;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) keep[j] = tid * kPer + j < n && s->order[tid * kPer + j] != 0;
   }
 
   // The first CTA's list of n to the row's token.  all: the weight that p is a share of; 0: of the k kept.
   __device__ __forceinline__ void finish(int n, const Rules& r, u64 all, const Args& a, int row) {
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, per = (n + kThreads - 1) / kThreads, i0 = min(n, tid * per), i1 = min(n, i0 + per);
     const uint32_t k = min(r.k, (uint32_t)n);
-    uint32_t key[kPer], kept = 0, ct;
-    u64 w[kPer], m = 0, mt;
-    bool keep[kPer];
-    list(n, key, w, keep);
-    if (r.p_on || k < (uint32_t)n) select(n, k, r.p_on, 0ull, [&](u64 of) { return share_of(all ? all : of, r.p); }, key, w, keep);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (!keep[j] || value_of<T>(key[j]) < r.least) {
-        w[j] = 0;
-      } else {
-        ++kept;
-      }
-      m += w[j];
+    if (r.p_on || k < (uint32_t)n) select(n, k, r.p_on, 0ull, all, r.p);
+    uint32_t kept = 0, ct;
+    u64 m = 0, mt;
+    auto weight_at = [&](int i) -> u64 { return s->id[i] >= 0 && value_of<T>(s->key[i]) >= r.least ? weigh(value_of<T>(s->key[i])) : 0ull; };
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      kept += s->id[i] >= 0 && value_of<T>(s->key[i]) >= r.least;
+      m += weight_at(i);
     }
     scan(kept, m, ct, mt);
-    draw(m, mt, w, [&](int j, float* v) {
-      *v = value_of<T>(key[j]);
-      return s->id[tid * kPer + j];
-    }, r, a, row);
+    const u64 target = __umul64hi(mt, r.u);
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+      const u64 w = weight_at(i);
+      if (m <= target && target < m + w) emit(s->id[i], value_of<T>(s->key[i]), mt, r, a, row);
+      m += w;
+    }
     if (tid == 0 && a.kept) a.kept[row] = (int32_t)ct;
   }
 
-  // The one of a thread's weights (of all threads' sum `total`, `before` of it before the thread's first) that the
-  // draw falls on, if it is here.
-  template <int N, typename Id>
-  __device__ __forceinline__ void draw(u64 before, u64 total, const u64 (&w)[N], Id id_of, const Rules& r, const Args& a, int row) {
-    const u64 target = __umul64hi(total, r.u);
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (before <= target && target < before + w[j]) {
-        float v;
-        a.token[row] = id_of(j, &v);
-        if (a.logprob) a.logprob[row] = log_share(v, heat, r.heat, total, s->table);
-      }
-      before += w[j];
-    }
+  __device__ __forceinline__ void emit(int id, float v, u64 total, const Rules& r, const Args& a, int row) const {
+    a.token[row] = id;
+    if (a.logprob) a.logprob[row] = log_share(v, heat, r.heat, total, s->table);
   }
 
   // A key that is no larger than the k-th largest of the row's, from the largest of its groups (first CTA).
@@ -805,15 +725,15 @@ struct Row {
       uint32_t c[kOwn], cs = 0, ct;
       u64 m = 0, mt;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) cs += c[j] = s->cnt[kBins - 1 - (tid * kPer + j)];
+      for (int j = 0; j < kOwn; ++j) cs += c[j] = s->cnt[kBins - 1 - (tid * kOwn + j)];
       uint32_t cb = cs;
       scan(cb, m, ct, mt);
       if (above + ct < k) return 0;          // fewer groups than k hold an id (uniform)
       cb += above;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
+      for (int j = 0; j < kOwn; ++j) {
         if (cb < k && k <= cb + c[j]) {
-          s->found.bin = kBins - 1 - (tid * kPer + j);
+          s->found.bin = kBins - 1 - (tid * kOwn + j);
           s->found.above = cb;
           s->found.in = c[j];
         }
@@ -1045,11 +965,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
     const uint32_t held = R.template gather<false>(in_class, nullptr);
     if (held <= kList) {
       if (R.rank == 0) {
-        uint32_t key[kPer];
-        u64 w[kPer];
-        bool keep[kPer];
-        R.list(held, key, w, keep);
-        R.select(held, held, true, f.above, [&](u64) { return target; }, key, w, keep);
+        // (with nothing above the class the target is a share of 1 of it)
+        R.select(held, held, true, f.above, target, ~0ull);
         __syncthreads();
         if (tid > 0 && tid < R.nc) {
           R.at(tid)->border = sh.border;
@@ -1184,10 +1101,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
       const u64 y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    R.draw(run + incl - m, total, w, [&](int j, float* v) {
-      *v = f[j];
-      return id + j;
-    }, r, a, row);
+    run += incl - m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (run <= target && target < run + w[j]) R.emit(id + j, f[j], total, r, a, row);
+      run += w[j];
+    }
   }
 }
 
