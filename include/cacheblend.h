@@ -713,7 +713,8 @@ int cb_logits_process(const void* logits, int32_t n_rows, int32_t vocab, int32_t
 
 /* How the next token of each row is drawn; a NULL pointer leaves a rule off. */
 typedef struct {
-    const float*   temperature;  /* [n_rows] T >= 0; 0: the lowest id of the largest logit   */
+    const float*   temperature;  /* [n_rows] T >= 0; 0 (and what is below 2^-126): the lowest id
+                                  * of the largest logit                                     */
     const int32_t* top_k;        /* [n_rows] keep the k largest; <= 0: all                   */
     const float*   top_p;        /* [n_rows] keep the fewest that hold this share; >= 1: all,
                                   * <= 0: the first                                          */
@@ -730,7 +731,7 @@ typedef struct {
  *   token   : [n_rows] int32; -1 if no logit is above -inf
  *   logprob : [n_rows] fp32 or NULL: ln of the token's share of the kept weight (token -1: -inf)
  *   n_kept  : [n_rows] int32 or NULL: how many ids were kept
- * Weights are exact to 2^-29 and their sums exact, so a decision is the one of the formulas above
+ * Weights are exact to 2^-28 and their sums exact, so a decision is the one of the formulas above
  * but where they differ by less than that; results do not depend on the row's place or company.
  * Ids at -inf are never kept, at +inf they share all the weight.  Reported by cb_sync
  * (CB_ERR_NONFINITE): a NaN logit (never kept), a temperature that is not a finite number >= 0

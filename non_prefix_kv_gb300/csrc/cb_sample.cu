@@ -7,9 +7,9 @@
 //
 // Every decision compares sums of weights, and it should be the one that 64-bit arithmetic takes: with
 // fp32 weights a draw over 64000 near-equal ids would fall on another id in one row of fifty.  So a weight
-// is an integer, 2^42 w: 2^x by a table of 32 steps and a polynomial of degree 4 on a remainder that holds
-// 31 bits behind the point (relative error 2^-29 at most, mostly of random sign), and sums are exact in any
-// order: the result does not depend on how the row is split.
+// is an integer, 2^42 w: 2^x by a table of 32 steps and the first terms of the series on the rest (Tang's table-driven
+// method, ACM TOMS 15, 1989), with 31 bits behind the point and a relative error of 2^-28 at most, mostly of random
+// sign.  Sums are exact in any order: the result does not depend on how the row is split.
 //
 // One cluster per row, a CTA holds a run of 256-id tiles.  What a row's rules ask for decides its way:
 //   k = 1 (or T = 0)      the largest logit's lowest id, found in the pass that finds the largest logit
@@ -68,7 +68,7 @@ struct Shared {
       uint32_t cnt[kBins];                   // ids in a class, and
       union {
         u64 sum[kBins];                      // their weights, or
-        uint32_t part[2][kBins];             // the parts of these above their class's base
+        uint32_t part[2][kBins];             // of their lower and upper halves
       };
     };
     u64 order[kList];                        // ids on their way to a list; a list's sort keys
@@ -158,18 +158,12 @@ template <typename T>
 __device__ __forceinline__ u64 weight(float v, const Heat& h, const uint2* table) {
   return add_weight<T>(0ull, v, h, table);
 }
-// The class of a logit by its k, larger for a larger one: 32 to an octave of weight.  In a class all w have one
-// shift and lie between t - t / 64 (t the table's) and 2^27 more: see find().
+// The class of a logit by its k, larger for a larger one: 32 to an octave of weight.  In a class all w have one shift.
 __device__ __forceinline__ uint32_t class_at(uint32_t bits) { return kBins - 1 + (bits - 0x4B400000u); }
 __device__ __forceinline__ uint32_t class_of(float v, const Heat& h) {
   const float d = v == h.mx ? 0.f : v - h.mx;
   return class_at(__float_as_uint(fmaf(fmaxf(d * h.ch, -60.0f), 32.0f, 12582912.0f)));
 }
-__device__ __forceinline__ uint32_t class_base(uint32_t bits, const uint2* table) {
-  const uint32_t t = table[bits & 31].x;
-  return shift_right(t - (t >> 6), max(-shift_of(bits), 0));
-}
-
 // ln(exp((v - mx) / T) / total), total in units of 2^-42, rounded about once: q = (v - mx) / T and e ln 2 as two
 // parts, ln m of total = m 2^e as logf's value and what exp of that is off by.  (In fp64 the one thread that does
 // this took a microsecond.)
@@ -357,8 +351,8 @@ struct Row {
   // in the classes of class_of (2).  Then, in falling order of classes, the one in which the running count (weight)
   // reaches the target behind what lies `above` all of them; want(all of it) gives the target.
   //
-  // 64-bit sums are slow atomics (37 cycles a warp); in the classes of KIND 2, whose weights have one shift and
-  // differ by less than 2^27 units, a count and two 32-bit sums of parts of 13 and 14 bits do (2^17 ids a CTA).
+  // 64-bit sums are slow atomics (37 cycles a warp); the weights of a class of KIND 2 have one shift and 32 bits, and
+  // two 32-bit sums of their halves do for 2^16 ids a CTA.  Beyond, what these carry is counted.
   template <int KIND, typename Cls, typename Want>
   __device__ __forceinline__ Find find(u64 above, Cls cls, Want want) {
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -378,10 +372,14 @@ struct Row {
         if (KIND == 2) {
           uint32_t bits;
           const uint32_t w = mantissa<T>(f[i], heat, s->table, bits);
-          const uint32_t u = shift_right(w, max(-shift_of(bits), 0)) - class_base(bits, s->table), c = class_at(bits);
-          atomicAdd(&s->cnt[c], 1u);
-          atomicAdd(&s->part[0][c], u & 0x1fffu);
-          atomicAdd(&s->part[1][c], u >> 13);
+          const uint32_t u = shift_right(w, max(-shift_of(bits), 0)), c = class_at(bits);
+          if (tiles <= 65536 / kTile) {
+            atomicAdd(&s->part[0][c], u & 0xffffu);
+            atomicAdd(&s->part[1][c], u >> 16);
+          } else {
+            if (atomicAdd(&s->part[0][c], u & 0xffffu) > ~(u & 0xffffu)) atomicAdd(&s->cnt[c], 1u);
+            if (atomicAdd(&s->part[1][c], u >> 16) > ~(u >> 16)) atomicAdd(&s->cnt[c], 0x10000u);
+          }
         }
       }
     });
@@ -399,15 +397,15 @@ struct Row {
         u64 c = 0;
         for (int q = 0; q < nc; ++q) {
           const Shared* o = at(q);
-          if (KIND != 1) c += o->cnt[b];
+          if (KIND == 0) c += o->cnt[b];
           if (KIND == 1) m[j] += o->sum[b];
-          if (KIND == 2) m[j] += (u64)o->part[0][b] + ((u64)o->part[1][b] << 13);
+          if (KIND == 2) {
+            const uint32_t carry = o->cnt[b];
+            m[j] += ((u64)(carry >> 16) << 48) + ((u64)o->part[1][b] << 16) + ((u64)(carry & 0xffffu) << 32) + o->part[0][b];
+          }
         }
         if (KIND == 0) m[j] = c;
-        if (KIND == 2) {
-          const uint32_t bits = 0x4B400000u + (uint32_t)(b - (kBins - 1));
-          m[j] = c ? (m[j] + c * class_base(bits, s->table)) << max(shift_of(bits), 0) : 0ull;
-        }
+        if (KIND == 2) m[j] <<= max(shift_of(0x4B400000u + (uint32_t)(b - (kBins - 1))), 0);
       }
       ms += m[j];
     }
@@ -787,6 +785,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
     bad = true;
     heat = 1.0f;
   }
+  if (heat < 1.17549435e-38f) heat = 0.0f;             // (1 / T would be infinite)
   if (bad && report) atomicOr(&g_err_sample, ERRBIT_NONFINITE);
   if (isnan(p)) p = 1.0f;
   if (isnan(mp)) mp = 0.0f;

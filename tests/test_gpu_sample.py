@@ -1,6 +1,6 @@
 """Drawing tokens from given numbers, against the fp64 oracle: tokens and counts exactly (unless the oracle
-says that a decision is nearer than 2^-28 of the weight, where the weights' own 2^-29 may decide: no input here
-is), logprobs within their fp32 rounding and 2^-28 (the token's weight and the sum, 2^-29 each)."""
+says that a decision is nearer than 2^-28 of the weight, where the weights' own rounding may decide: no input
+here is), logprobs within their fp32 rounding and 2^-28 (the token's weight and the sum)."""
 import numpy as np
 import pytest
 
@@ -34,7 +34,7 @@ def draw(B, x, u, T=None, k=None, p=None, m=None, dtype="f32"):
     return logits, tok, lp, kept
 
 
-def check(B, x, u, T=None, k=None, p=None, m=None, dtype="f32"):
+def check(B, x, u, T=None, k=None, p=None, m=None, dtype="f32", least=2.0 ** -28):
     logits, tok, lp, kept = draw(B, x, u, T, k, p, m, dtype)
     B.cb_sync(None)
     logits, tok, lp, kept = (t.double().cpu().numpy() for t in (logits, tok, lp, kept))
@@ -42,7 +42,7 @@ def check(B, x, u, T=None, k=None, p=None, m=None, dtype="f32"):
     for b in range(len(x)):
         w_tok, w_lp, w_kept, near = A.sample(logits[b], float(np.float32(u[b])), one(T, b, 1.0), 0 if k is None else int(k[b]),
                                              one(p, b, 1.0), one(m, b, 0.0))
-        assert near > 2.0 ** -28, "an input too close to a border"
+        assert near > least, "an input too close to a border"
         assert tok[b] == w_tok and kept[b] == w_kept, (b, tok[b], w_tok, kept[b], w_kept)
         if w_tok >= 0:
             assert abs(lp[b] - w_lp) <= 2.0 ** -24 * abs(w_lp) + 2.0 ** -28
@@ -109,6 +109,53 @@ def test_large_vocabularies_and_many_rows(B, dtype):
     for s, t in zip(a[1:], b[1:]):
         assert bool((s == t).all())
     B.cb_sync(None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_flat_rows(B, dtype):
+    """All ids equal: one class holds the whole row, of up to 2^17 ids in a block.  Every weight is that
+    of the largest, exactly 1 (2^42 of the kernel's units), so that a decision has no error but u's and p's own
+    products': below 2^-44."""
+    u = [0.0, 0.123456789, 0.87654321, 0.99999994]
+    for V in (70000, 131072, 300001, 1 << 20):
+        x = np.full((4, V), 1.5)
+        for p in (0.3100001, 0.7700003):
+            check(B, x, u, p=np.full(4, p), dtype=dtype, least=2.0 ** -44)
+        check(B, x, u, k=np.full(4, V // 3), p=np.full(4, 0.56789), dtype=dtype, least=2.0 ** -44)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_lists_of_uneven_values(B, dtype):
+    """Ids that no classes of one width tell apart: one far above the others, infinities, most of them equal."""
+    g = np.random.default_rng(6)
+    n, V = 6, 3000
+    x = g.random((n, V))
+    x[:, 1234] = 1e6
+    x[1, 77] = 2e6
+    x[2:4, :1500] = 0.75
+    u = g.random(n)
+    T = np.full(n, 1e6)
+    for k in (1, 300, 900, 1024):
+        check(B, x, u, T=T, k=np.full(n, k), dtype=dtype)
+        check(B, x, u, T=T, k=np.full(n, k), p=np.linspace(0.2, 0.9, n), dtype=dtype)
+    check(B, x[:, :2000], u, T=T, m=np.full(n, 0.3), p=np.linspace(0.2, 0.9, n), dtype=dtype)
+    x[0, [5, 9, 2000]] = np.inf
+    x[1, 0] = np.inf
+    _, tok, lp, kept = draw(B, x[:2], [0.7, 0.2], k=[700, 700], p=[0.9, 0.9], dtype=dtype)
+    B.cb_sync(None)
+    assert tok.tolist() == [2000, 0] and kept.tolist() == [3, 1]
+
+
+def test_temperatures_of_no_weight(B):
+    """Below the smallest normal number a temperature counts as 0: the first of the largest."""
+    x = np.zeros((3, 700))
+    x[:, [300, 301]] = 1.0
+    for T in (0.0, 1e-45, 1.1e-38):
+        for kw in (dict(), dict(k=[5] * 3), dict(p=[0.9] * 3), dict(m=[0.1] * 3)):
+            _, tok, lp, kept = draw(B, x, [0.0, 0.6, 0.99], T=[T] * 3, **kw)
+            assert tok.tolist() == [300] * 3 and kept.tolist() == [1] * 3 and lp.tolist() == [0.0] * 3
+    B.cb_sync(None)
+    check(B, x, [0.1, 0.6, 0.9], T=[1.2e-38, 1e-30, 1e30])
 
 
 def test_extremes(B):
