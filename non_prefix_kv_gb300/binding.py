@@ -667,15 +667,18 @@ def _strided(what: str, t, dtype, width: int, dev: int):
     """Address, row stride and count of rows [n, width] whose channels are contiguous (a part of wider rows)."""
     if t is None:
         return None, 0, 0
-    shape, stride = t.shape, t.stride()
+    try:
+        n, w = t.shape
+        ld, one = t.stride()
+    except ValueError:
+        n, w, ld, one = 0, -1, 0, 0                            # not two dimensions
+    if w != width or one != 1:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()}, expected rows of {width} contiguous elements")
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {t.dtype}, expected {dtype}")
-    if len(shape) != 2 or shape[1] != width or stride[1] != 1:
-        raise ValueError(f"{what}: shape {tuple(shape)}, strides {stride}, expected rows of {width} contiguous elements")
     if t.get_device() != dev:
         raise ValueError(f"{what}: on {t.device}, not on the current CUDA device")
-    n = shape[0]
-    return t.data_ptr(), stride[0] if n > 1 else width, n      # (one row has no stride)
+    return t.data_ptr(), ld if n > 1 else width, n             # (one row has no stride)
 
 
 def cb_rope_rows(q, k, v, pos, q_out, k_out, v_out, dims: cb_dims, spec: cb_rope_spec, cos_sin, max_pos: int, src_row=None,

@@ -933,7 +933,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2)
 // ---- join: one warp per (query, head) ------------------------------------------------------------
 // What does not come from the two kernels before is worked out before the wait for them.
 template <int HD, bool WIDE>
-__global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc w) {
+__global__ void __launch_bounds__(256, WIDE ? 5 : 3) k_shared_join(const __grid_constant__ Tc w) {
   const Shared& p = w.s;
   const int t = blockIdx.x, hh = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int s = t / p.n_q, j = t - s * p.n_q, h = hh / p.G, gh = hh - h * p.G;
@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ Tc 
   };
   // Pieces come eight at a time, statistics and rows in one go (a row is mostly one batch, and the time of a
   // small join is that of its chain of loads), each batch joined to what came before it.
-  constexpr int BATCH = 8;
+  constexpr int BATCH = WIDE ? 4 : 8;
   float M = -INFINITY, L = 0.f, o[PER];
 #pragma unroll
   for (int c = 0; c < PER; ++c) o[c] = 0.f;
