@@ -1559,7 +1559,7 @@ int make_shared(const cb_shared_kv* kv, const cb_dims* d, int n_q, Shared* p) {
   if (kv->n_seq < 1 || kv->n_seq > 65535) return fail(CB_ERR_SHAPE, "n_seq %d outside [1, 65535]", kv->n_seq);
   if (!kv->row0_host || !kv->len_host || !kv->seq0_host) return fail(CB_ERR_INVALID_ARG, "shared_kv: array is NULL");
   if (kv->n_rows < 0 || kv->n_rows > INT32_MAX) return fail(CB_ERR_SHAPE, "shared_kv: n_rows");
-  if (kv->capacity < 0 || kv->capacity * kv->n_seq > INT32_MAX || kv->capacity > INT32_MAX)
+  if (kv->capacity < 0 || kv->capacity > INT32_MAX || kv->capacity * kv->n_seq > INT32_MAX)
     return fail(CB_ERR_SHAPE, "shared_kv: capacity %lld of %d sequences", (long long)kv->capacity, kv->n_seq);
   if (kv->seq0_host[0] != 0 || kv->seq0_host[kv->n_groups] != kv->n_seq)
     return fail(CB_ERR_SHAPE, "shared_kv: seq0 does not run from 0 to n_seq");

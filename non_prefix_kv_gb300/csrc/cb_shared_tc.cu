@@ -1175,7 +1175,7 @@ cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
   if ((w.wide || w.total > 0) && !make_map(&q, s.q, {HD, s.H, (int64_t)s.n_seq * s.n_q}, {64, s.G, w.qpt})) return cudaErrorInvalidValue;
   if (w.wide) {
     // (what is not there is not read: any map will do)
-    const bool pre = s.n_rows > 0, own = s.capacity > 0;
+    const bool pre = *std::max_element(s.len, s.len + s.n_groups) > 0, own = s.capacity > 0;
     const int64_t rows = s.n_seq * s.capacity;
     if ((pre && (!make_map(&k, s.k, {W, s.n_rows}, {64, BN}) || !make_map(&v, s.v, {W, s.n_rows}, {64, BN}))) ||
         (own && (!make_map(&own_k, s.own_k, {W, rows}, {64, BN}) || !make_map(&own_v, s.own_v, {W, rows}, {64, BN}))))

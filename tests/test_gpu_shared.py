@@ -243,3 +243,77 @@ def test_own_caches_past_2_to_the_31_elements(B):
         ref = torch.einsum("hi,ihc->hc", p, vals).reshape(-1)
         mag = torch.einsum("hi,ihc->hc", p, vals.abs()).reshape(-1)
         assert bool(((out[-1, 0].double() - ref).abs() <= 2.0 ** -7 * 1.1 * mag + (l + 200) * 2 * EPS * mag).all())
+
+
+@pytest.mark.parametrize("H,hkv,n_seq,n_q", [(2, 2, 1100, 1), (16, 1, 1024, 8), (16, 1, 1025, 8), (14, 2, 300, 1)])
+def test_many_sequences(B, H, hkv, n_seq, n_q):
+    """Row tiles of one sequence each up to 1024 of them, packed ones beyond; more sequences than a block keeps."""
+    c = Case(B, n_seq, "bf16", H, hkv, 64, [130, 200], [0, n_seq - 7, n_seq], n_q, 21)
+    c.run()
+    B.cb_sync(None)
+    c.check([0, 1, 2, n_seq // 2, n_seq - 8, n_seq - 7, n_seq - 1])
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("cap", [0, 50, 300])
+def test_many_queries_of_several_groups(B, hd, cap):
+    """Prefixes and groups that are empty, sequences of padding, of the prefix alone, of the last row alone."""
+    lens, seq0, n_q = [300, 64, 0, 129, 0], [0, 2, 2, 5, 6, 7], 36
+    g = np.random.default_rng(cap)
+    last = g.integers(-2, max(cap, 1), (7, n_q)) if cap else g.integers(-2, 0, (7, n_q))
+    last[1] = -2
+    last[3] = -1
+    last[4, :20] = -2
+    last[4, 20:] = cap - 1
+    last[6, 18:] = -2
+    c = Case(B, 3, "bf16", 14, 2, hd, lens, seq0, n_q, cap, last=last)
+    c.run()
+    B.cb_sync(None)
+    c.check()
+
+
+def test_absent_prefixes_have_no_address(B):
+    """Prefixes of no rows: their buffer may be missing whatever its count of rows says."""
+    for dtype in ("bf16", "f32"):
+        for n_q in (1, 64):
+            c = Case(B, 5, dtype, 4, 2, 64, [0, 0], [0, 2, 3], n_q, 40)
+            c.kv.k = c.kv.v = None
+            c.run()
+            B.cb_sync(None)
+            c.check()
+
+
+def test_two_streams_at_once(B):
+    """Calls of three kinds and a draw, on two streams with workspaces of their own, give what they give alone."""
+    torch = torch_mod()
+    cases = [[Case(B, s, "bf16", 14, 2, 128, [1500], [0, 9], 1, 200), Case(B, s + 1, "bf16", 14, 2, 128, [900], [0, 3], 40, 60),
+              Case(B, s + 2, "f32", 4, 4, 64, [500], [0, 3], 2, 40)] for s in (20, 30)]
+    logits = [torch.randn(40, 9001, device="cuda") for _ in range(2)]
+    u = torch.rand(40, device="cuda")
+    rules = B.sample_rules(top_p=torch.full((40,), 0.9, device="cuda"))
+    tokens = [torch.zeros(40, dtype=torch.int32, device="cuda") for _ in range(2)]
+
+    def all_of(i, stream=None):
+        for c in cases[i]:
+            B.cb_shared_attention(c.q, c.last, c.n_q, c.kv, c.dims, c.out, c.ws, stream=stream)
+        B.cb_sample_token(logits[i], u, rules, tokens[i], stream=stream)
+
+    alone = []
+    for i in range(2):
+        all_of(i)
+        B.cb_sync(None)
+        alone.append([c.out.clone() for c in cases[i]] + [tokens[i].clone()])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        for c in cases[i]:
+            c.out.fill_(5.0)
+        tokens[i].fill_(-9)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i, s in enumerate(streams):
+            all_of(i, s.cuda_stream)
+    torch.cuda.synchronize()
+    B.cb_sync(None)
+    for i in range(2):
+        for got, want in zip([c.out for c in cases[i]] + [tokens[i]], alone[i]):
+            assert bool((got == want).all())
