@@ -365,8 +365,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint64_t qd = tc::desc_sw128(tc::smem_u32(base + L::OFF_Q + (nseg & 1) * L::T_BYTES));
         for (int t = grp; t < cur.n; t += 2, ++u) {
           const int keys = keys_of<WIDE>(cur, cur.tile + t);
-          // S goes where P is, until P V is done
-          ok = __all_sync(0xffffffffu, (t != grp || tc::mbar_wait(&q_full[nseg & 1], (nseg >> 1) & 1)) &&
+          // Q: a group that had no tile in segments of one may be here while the buffer still holds the segment's before
+          // the last, and the barrier's phase cannot tell; once that has been read out it can.  S goes where P is, until
+          // P V is done.
+          ok = __all_sync(0xffffffffu, (t != grp || ((nseg < 2 || wait_count(read_out, 8 * (nseg - 1))) &&
+                                                     tc::mbar_wait(&q_full[nseg & 1], (nseg >> 1) & 1))) &&
                                            tc::mbar_wait(k_full, u & 1) && (u == 0 || tc::mbar_wait(pv_done, (u - 1) & 1)));
           if (!ok) break;
           tc::tc_fence_after();

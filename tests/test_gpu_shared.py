@@ -317,3 +317,23 @@ def test_two_streams_at_once(B):
     for i in range(2):
         for got, want in zip([c.out for c in cases[i]] + [tokens[i]], alone[i]):
             assert bool((got == want).all())
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n_q", [1, 3])
+def test_short_and_long_prefixes_by_turns(B, hd, n_q):
+    """Runs of work of one key tile each, in which only one of two groups has a share, before longer ones."""
+    lens, seq0 = [], [0]
+    for i in range(20):
+        lens += [60, 400 + 50 * i]
+        seq0 += [seq0[-1] + 90, seq0[-1] + 120]
+    c = Case(B, 12, "bf16", 8, 8, hd, lens, seq0, n_q, 0)
+    c.run()
+    B.cb_sync(None)
+    c.check([x + d for x in seq0[:-1] for d in (0, 17)])
+    first = c.out.clone()
+    for _ in range(5):
+        c.out.fill_(7.0)
+        c.run()
+        assert bool((c.out == first).all())
+    B.cb_sync(None)
