@@ -56,8 +56,9 @@ struct Tc {
   int qpt;                       // queries of a row tile: 128 / G
   int slot_rows;                 // rows that a slot holds
   float* part;                   // [workers + pairs][slot_rows][hd], then m and l: see slot()
-  // wide: row tiles hold queries of one sequence, and their line goes on from the prefix to the sequence's own rows
-  bool wide;
+  // wide: the line holds row tiles with queries of one sequence, which go on from the prefix to the sequence's own
+  // rows; or (split) to the own rows alone, and behind them the row tiles of the groups with the prefixes
+  bool wide, split;
   int chunks;                    // row tiles of a sequence
   // own rows, where they have a kernel of their own
   int row_tiles;                 // of a sequence
@@ -65,7 +66,7 @@ struct Tc {
   int own_ctas;                  // CTAs of its kernel
   bool alone;                    // no prefix kernel runs before
   int32_t* plan;                 // [n_seq row_tiles + 1] steps before each, times Hkv; wide: how many row tiles are
-                                 // live, their key tiles, [n_seq chunks] the place of each among them (-1: none of
+                                 // live, their key tiles, [row tiles] the place of each among them (-1: none of
                                  // its queries sees anything), [live + 1] key tiles before each
   float* own_part;               // [workers + n_seq row_tiles Hkv][rows][hd], m, l
 };
@@ -88,7 +89,11 @@ struct Seg {
   int row0, len;                 // the prefix
   int own_tile, own_row, own_len;    // the first key tile of own rows, the first own row, how many are seen
 };
-constexpr int kWideTiles = 1024;     // row tiles of a wide call
+constexpr int kWideTiles = 2048;     // row tiles of a wide call
+// Rows of a sequence and KV head from which its own keys go with the prefixes' (split) if they do not fill tiles: the
+// other kernel reads them once per 8 rows.  16 and 64 sequences over 4096 rows of 32 heads: 8 rows 38 and 97 us (27 and
+// 72 apart), 16 rows 51 and 131 (52 and 185), 88 rows 124 (649).
+constexpr int kSplitRows = 16;
 struct Wide {                        // the live row tiles of a wide call, in order
   int first[kWideTiles + 1];         // key tiles before each; at the end those of one head
   int id[kWideTiles], last[kWideTiles];
@@ -110,19 +115,30 @@ __device__ __forceinline__ Seg segment(const Tc& w, const Wide& wide, int i, int
       else
         hi = mid - 1;
     }
-    const int id = wide.id[lo], s = id / w.chunks, c = id - s * w.chunks;
-    int g = 0;
-    while (s >= p.seq0[g + 1]) ++g;
+    const int id = wide.id[lo], of_seq = p.n_seq * w.chunks;
     kt = wide.first[lo + 1] - wide.first[lo];
     x.tile = at - wide.first[lo];
     x.pair = x.h * wide.n + lo;
-    x.tok = s * p.n_q + c * w.qpt;
-    x.queries = min(w.qpt, p.n_q - c * w.qpt);
+    int g = 0;
+    if (id < of_seq) {
+      const int s = id / w.chunks, c = id - s * w.chunks;
+      while (s >= p.seq0[g + 1]) ++g;
+      x.tok = s * p.n_q + c * w.qpt;
+      x.queries = min(w.qpt, p.n_q - c * w.qpt);
+      x.len = w.split ? 0 : p.len[g];
+      x.own_tile = (x.len + BN - 1) / BN;
+      x.own_row = (int)(s * p.capacity);
+      x.own_len = wide.last[lo] + 1;
+    } else {
+      while (id - of_seq >= w.prob[g + 1]) ++g;
+      const int q0 = (id - of_seq - w.prob[g]) * w.qpt;
+      x.tok = p.seq0[g] * p.n_q + q0;
+      x.queries = min(w.qpt, (p.seq0[g + 1] - p.seq0[g]) * p.n_q - q0);
+      x.len = p.len[g];
+      x.own_tile = 0x7fffffff;
+      x.own_row = x.own_len = 0;
+    }
     x.row0 = p.row0[g];
-    x.len = p.len[g];
-    x.own_tile = (x.len + BN - 1) / BN;
-    x.own_row = (int)(s * p.capacity);
-    x.own_len = wide.last[lo] + 1;
   } else {
     int g = 0;
     while (i >= w.first[g + 1]) ++g;
@@ -153,14 +169,27 @@ __device__ __forceinline__ int keys_of(const Seg& x, int j) {
 // The row tiles of which some query sees something; the first CTA leaves them in the plan for the join.
 __device__ __forceinline__ void make_wide(const Tc& w, Wide& wide, int tid, int threads) {
   const Shared& p = w.s;
-  const int tiles = p.n_seq * w.chunks;
-  for (int i = tid; i < tiles; i += threads) {
-    const int s = i / w.chunks, c = i - s * w.chunks;
-    int mx = -2, g = 0;
-    for (int j = c * w.qpt; j < min(p.n_q, (c + 1) * w.qpt); ++j) mx = max(mx, shared_last(p, (int64_t)s * p.n_q + j));
-    while (s >= p.seq0[g + 1]) ++g;
-    wide.id[i] = mx >= -1 ? (p.len[g] + BN - 1) / BN + (mx + BN) / BN : 0;
-    wide.last[i] = mx;
+  const int of_seq = p.n_seq * w.chunks, shared = w.split ? w.prob[p.n_groups] : 0, tiles = of_seq + shared;
+  // The order of the row tiles.  Split: the groups' ones spread among the sequences', which are short and cost a start
+  // and a piece each (all of these first, the CTAs that got them took three times as long as the others).
+  auto id_at = [&](int i) -> int {
+    const int a = i * shared / tiles, b = (i + 1) * shared / tiles;
+    return b > a ? of_seq + a : i - a;
+  };
+  for (int pos = tid; pos < tiles; pos += threads) {
+    int mx = -2, g = 0, n;
+    const int i = id_at(pos);
+    if (i < of_seq) {
+      const int s = i / w.chunks, c = i - s * w.chunks;
+      for (int j = c * w.qpt; j < min(p.n_q, (c + 1) * w.qpt); ++j) mx = max(mx, shared_last(p, (int64_t)s * p.n_q + j));
+      while (s >= p.seq0[g + 1]) ++g;
+      n = mx >= -1 ? (w.split ? 0 : (p.len[g] + BN - 1) / BN) + (mx + BN) / BN : 0;
+    } else {
+      while (i - of_seq >= w.prob[g + 1]) ++g;
+      n = (p.len[g] + BN - 1) / BN;
+    }
+    wide.id[pos] = n;
+    wide.last[pos] = mx;
   }
   __syncthreads();
   if (tid < 32) {
@@ -178,11 +207,11 @@ __device__ __forceinline__ void make_wide(const Tc& w, Wide& wide, int tid, int 
       const int to = at + __popc(live & ((1u << tid) - 1));
       if (n > 0) {
         wide.first[to] = units + incl - n;
-        wide.id[to] = i;
+        wide.id[to] = id_at(i);
         wide.last[to] = mx;
       }
       if (write) {
-        if (i < tiles) w.plan[2 + i] = n > 0 ? to : -1;
+        if (i < tiles) w.plan[2 + id_at(i)] = n > 0 ? to : -1;
         if (n > 0) w.plan[2 + tiles + to] = units + incl - n;
       }
       at += __popc(live);
@@ -234,6 +263,8 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 // WIDE: the calls with many queries of each sequence.  A row tile's queries are of one sequence and its key tiles go
 // on from the prefix's to the sequence's own, under each row's bound, so that own rows need no kernel of their own;
 // row tiles of padding are left out.  (8 questions of 48 to 96 queries of 56 heads over 16000 rows: 299 us without.)
+// Where sequences do not fill their tiles the prefixes' tiles are packed from a whole group's queries and only the own
+// keys' are a sequence's own (split: 29 of 88 queries of 32 heads over 8204 rows 408 us, 1787 with the own rows' kernel).
 //
 // Barriers of a group: K and V have landed, S and P V are done, P is written.  How far the segments' results have
 // been read (from TMEM, and out of Q's buffer) is a count that the issuing warps look at: they may be ahead by more
@@ -957,7 +988,7 @@ __global__ void __launch_bounds__(256, WIDE ? 5 : 3) k_shared_join(const __grid_
       r = (tl - rt * w.qpt) * p.G + gh;
     }
   }
-  const int rr = j * p.G + gh, e = s * w.row_tiles + rr / TILE, r_own = rr % TILE;
+  const int rr = j * p.G + gh, e = s * w.row_tiles + rr / TILE;
   // (the bounds were written before the call: the kernels that let this one start had waited for that)
   const bool only = !WIDE && w.alone && p.capacity == 0;
   if (only) pdl_wait();
@@ -966,14 +997,30 @@ __global__ void __launch_bounds__(256, WIDE ? 5 : 3) k_shared_join(const __grid_
   if (!only) pdl_wait();
   pdl_trigger();
   if (!on) return;
+  int r_own = rr % TILE;
   if (WIDE && last > -2) {
-    const int tiles = p.n_seq * w.chunks, c = j / w.qpt, li = w.plan[2 + s * w.chunks + c];
-    if (li >= 0) {
-      const int per = w.plan[1], total = per * p.Hkv, workers = wide_workers(total, w.workers), f = w.plan[2 + tiles + li],
-                x0 = h * per + f, kt = w.plan[2 + tiles + li + 1] - f, w0 = worker_of(total, x0, workers);
-      n_pre = worker_of(total, x0 + kt - 1, workers) - w0 + 1;
-      pre = slot(w.part, w.slot_rows, HD, w0, h * w.plan[0] + li);
-      r = (j - c * w.qpt) * p.G + gh;
+    const int of_seq = p.n_seq * w.chunks, tiles = of_seq + (w.split ? w.prob[p.n_groups] : 0), per = w.plan[1],
+              total = per * p.Hkv, workers = wide_workers(total, w.workers);
+    auto pieces = [&](int id, const float*& from) -> int {             // of a row tile
+      const int li = w.plan[2 + id];
+      if (li < 0) return 0;
+      const int f = w.plan[2 + tiles + li], x0 = h * per + f, kt = w.plan[2 + tiles + li + 1] - f,
+                w0 = worker_of(total, x0, workers);
+      from = slot(w.part, w.slot_rows, HD, w0, h * w.plan[0] + li);
+      return worker_of(total, x0 + kt - 1, workers) - w0 + 1;
+    };
+    const int c = j / w.qpt, at = (j - c * w.qpt) * p.G + gh;
+    if (w.split) {
+      int g = 0;
+      while (s >= p.seq0[g + 1]) ++g;
+      const int tl = t - p.seq0[g] * p.n_q, rt = tl / w.qpt;
+      r = (tl - rt * w.qpt) * p.G + gh;
+      n_pre = pieces(of_seq + w.prob[g] + rt, pre);
+      r_own = at;
+      if (last >= 0) n_own = pieces(s * w.chunks + c, own);
+    } else {
+      r = at;
+      n_pre = pieces(s * w.chunks + c, pre);
     }
   }
   if (last == -2) n_pre = 0;
@@ -1052,18 +1099,28 @@ bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
   int64_t packed = 0;
   for (int g = 0; g < s.n_groups; ++g) packed += ((int64_t)(s.seq0[g + 1] - s.seq0[g]) * s.n_q + w->qpt - 1) / w->qpt;
   const int64_t tiles = (int64_t)s.n_seq * w->chunks;
-  w->wide = tiles <= kWideTiles && 4 * tiles <= 5 * packed;
+  // Where they are, own rows still go with the prefixes if a sequence's rows would read their keys several times over
+  // in the other kernel.
+  w->split = tiles + packed <= kWideTiles && 4 * tiles > 5 * packed && s.capacity > 0 && s.n_q * s.G >= kSplitRows;
+  w->wide = w->split || (tiles <= kWideTiles && 4 * tiles <= 5 * packed);
   if (w->wide) {
-    int64_t longest = 0;
-    for (int g = 0; g < s.n_groups; ++g) longest = std::max<int64_t>(longest, s.len[g]);
+    int64_t longest = 0, n = 0;
+    for (int g = 0; g < s.n_groups; ++g) {
+      longest = std::max<int64_t>(longest, s.len[g]);
+      w->prob[g] = (int)n;                   // (split: row tiles before group g)
+      if (w->split) n += ((int64_t)(s.seq0[g + 1] - s.seq0[g]) * s.n_q + w->qpt - 1) / w->qpt;
+    }
+    w->prob[s.n_groups] = (int)n;
+    const int64_t tiles = (int64_t)s.n_seq * w->chunks + n;
     const double most = (double)tiles * s.Hkv * ((longest + BN - 1) / BN + (s.capacity + BN - 1) / BN);
     if (most > INT32_MAX / 2 || (s.H + 7) / 8 > 65535) return false;
     w->total = 0;
     w->workers = (int)std::min<double>(kWorkers, std::max(1.0, (most + 1) / 2));
-    w->slot_rows = (std::min(s.n_q, w->qpt) * s.G + 3) & ~3;
+    w->slot_rows = ((w->split ? w->qpt : std::min(s.n_q, w->qpt)) * s.G + 3) & ~3;
+    w->own_slot_rows = w->slot_rows;
     w->alone = false;
     w->own_part = nullptr;
-    w->row_tiles = w->own_slot_rows = 0;
+    w->row_tiles = 0;
     const size_t pre = (size_t)(w->workers + tiles * s.Hkv) * w->slot_rows * sizeof(float) * (s.hd + 2), at = (pre + 255) & ~size_t(255);
     w->part = nullptr;
     w->plan = reinterpret_cast<int32_t*>(at);
@@ -1208,17 +1265,54 @@ cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
 
 bool shared_tc_taken(int dt, const Shared& p) { return dt == DT_BF16 && (p.hd == 64 || p.hd == 128) && p.G <= BM; }
 
+// fn(part of the call, its first query), one after the other: with as many row tiles as a wide call takes, where the own
+// keys are to go with the prefixes.
+template <typename Fn>
+static bool in_parts(const Shared& p, Fn fn) {
+  const int64_t qpt = BM / p.G, chunks = (p.n_q + qpt - 1) / qpt, tiles = chunks * p.n_seq;
+  int64_t packed = 0;
+  for (int g = 0; g < p.n_groups; ++g) packed += ((int64_t)(p.seq0[g + 1] - p.seq0[g]) * p.n_q + qpt - 1) / qpt;
+  if (p.capacity == 0 || (int64_t)p.n_q * p.G < kSplitRows ||
+      (tiles <= kWideTiles && (4 * tiles <= 5 * packed || tiles + packed <= kWideTiles)))
+    return fn(p, (int64_t)0);
+  // whole sequences, or parts of one (twice the row tiles: the groups' ones count too)
+  const int64_t seqs = std::max<int64_t>(1, kWideTiles / (2 * chunks)), queries = std::min<int64_t>(p.n_q, kWideTiles / 2 * qpt);
+  const int64_t own = p.capacity * p.Hkv * p.hd * 2;
+  for (int64_t s = 0; s < p.n_seq; s += seqs)
+    for (int64_t j = 0; j < p.n_q; j += queries) {
+      Shared x = p;
+      x.n_seq = (int)std::min(seqs, p.n_seq - s);
+      x.n_q = (int)std::min(queries, p.n_q - j);
+      for (int g = 0; g <= p.n_groups; ++g) x.seq0[g] = (int32_t)std::min<int64_t>(std::max<int64_t>(p.seq0[g] - s, 0), x.n_seq);
+      x.own_k = static_cast<const char*>(p.own_k) + s * own;
+      x.own_v = static_cast<const char*>(p.own_v) + s * own;
+      if (!fn(x, s * p.n_q + j)) return false;
+    }
+  return true;
+}
+
 size_t shared_tc_ws_bytes(const Shared& p) {
-  Tc w;
-  size_t n;
-  return plan_tc(p, &w, &n) ? n : 0;
+  size_t most = 0;
+  const bool ok = in_parts(p, [&](const Shared& x, int64_t) {
+    Tc w;
+    size_t n;
+    if (!plan_tc(x, &w, &n)) return false;
+    most = std::max(most, n);
+    return true;
+  });
+  return ok ? most : 0;
 }
 
 int shared_tc_launches(const Shared& p) {
-  Tc w;
-  size_t n;
-  if (!plan_tc(p, &w, &n)) return 0;
-  return w.wide ? 2 : 1 + (w.total > 0 ? 1 : 0) + (p.capacity > 0 ? 1 : 0);
+  int launches = 0;
+  in_parts(p, [&](const Shared& x, int64_t) {
+    Tc w;
+    size_t n;
+    if (!plan_tc(x, &w, &n)) return false;
+    launches += w.wide ? 2 : 1 + (w.total > 0 ? 1 : 0) + (x.capacity > 0 ? 1 : 0);
+    return true;
+  });
+  return launches;
 }
 
 void reset_shared_tc_caches() {
@@ -1228,14 +1322,26 @@ void reset_shared_tc_caches() {
 
 cudaError_t launch_shared_tc(const Shared& p, void* ws, cudaStream_t s) {
   g_used_shared_tc = true;
-  Tc w;
-  size_t n;
-  if (!plan_tc(p, &w, &n)) return cudaErrorInvalidValue;
-  char* base = static_cast<char*>(ws);
-  w.part = reinterpret_cast<float*>(base + reinterpret_cast<size_t>(w.part));
-  w.own_part = reinterpret_cast<float*>(base + reinterpret_cast<size_t>(w.own_part));
-  w.plan = reinterpret_cast<int32_t*>(base + reinterpret_cast<size_t>(w.plan));
-  return p.hd == 128 ? launch_hd<128>(w, s) : launch_hd<64>(w, s);
+  cudaError_t e = cudaSuccess;
+  in_parts(p, [&](const Shared& x, int64_t t0) {
+    Tc w;
+    size_t n;
+    if (!plan_tc(x, &w, &n)) {
+      e = cudaErrorInvalidValue;
+      return false;
+    }
+    char* base = static_cast<char*>(ws);
+    w.part = reinterpret_cast<float*>(base + reinterpret_cast<size_t>(w.part));
+    w.own_part = reinterpret_cast<float*>(base + reinterpret_cast<size_t>(w.own_part));
+    w.plan = reinterpret_cast<int32_t*>(base + reinterpret_cast<size_t>(w.plan));
+    const int64_t row = (int64_t)p.H * p.hd * 2;
+    w.s.q = static_cast<const char*>(p.q) + t0 * row;
+    w.s.out = static_cast<char*>(p.out) + t0 * row;
+    w.s.last = p.last + t0;
+    e = p.hd == 128 ? launch_hd<128>(w, s) : launch_hd<64>(w, s);
+    return e == cudaSuccess;
+  });
+  return e;
 }
 
 }  // namespace cb

@@ -245,13 +245,14 @@ def test_own_caches_past_2_to_the_31_elements(B):
         assert bool(((out[-1, 0].double() - ref).abs() <= 2.0 ** -7 * 1.1 * mag + (l + 200) * 2 * EPS * mag).all())
 
 
-@pytest.mark.parametrize("H,hkv,n_seq,n_q", [(2, 2, 1100, 1), (16, 1, 1024, 8), (16, 1, 1025, 8), (14, 2, 300, 1)])
+@pytest.mark.parametrize("H,hkv,n_seq,n_q", [(2, 2, 1100, 1), (16, 1, 1024, 8), (16, 1, 1025, 8), (14, 2, 300, 1),
+                                               (16, 1, 2100, 8), (16, 1, 2100, 3), (2, 2, 2500, 1), (64, 1, 2, 2060)])
 def test_many_sequences(B, H, hkv, n_seq, n_q):
-    """Row tiles of one sequence each up to 1024 of them, packed ones beyond; more sequences than a block keeps."""
-    c = Case(B, n_seq, "bf16", H, hkv, 64, [130, 200], [0, n_seq - 7, n_seq], n_q, 21)
+    """Row tiles up to as many as a call takes at once, and beyond; more sequences than a block keeps."""
+    c = Case(B, n_seq, "bf16", H, hkv, 64, [130, 200], [0, max(n_seq - 7, 1), n_seq], n_q, 21)
     c.run()
     B.cb_sync(None)
-    c.check([0, 1, 2, n_seq // 2, n_seq - 8, n_seq - 7, n_seq - 1])
+    c.check({0, 1, min(2, n_seq - 1), n_seq // 2, max(n_seq - 8, 0), max(n_seq - 7, 0), n_seq - 1})
 
 
 @pytest.mark.parametrize("hd", [64, 128])
@@ -317,6 +318,33 @@ def test_two_streams_at_once(B):
     for i in range(2):
         for got, want in zip([c.out for c in cases[i]] + [tokens[i]], alone[i]):
             assert bool((got == want).all())
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("H,hkv,lens,seq0,n_q,cap", [
+    (2, 2, [700], [0, 9], 50, 300),                      # 50 of a tile's 128 rows
+    (4, 2, [300, 0, 129], [0, 3, 7, 12], 17, 40),        # a group without a prefix
+    (7, 1, [1000, 64], [0, 5, 11], 5, 200),
+    (3, 3, [0], [0, 6], 70, 150),                        # no prefix at all
+    (32, 1, [513], [0, 20], 1, 33)])
+def test_questions_that_share_tiles(B, hd, H, hkv, lens, seq0, n_q, cap):
+    """Enough rows of a sequence for its own keys to go with the prefixes, too few to fill tiles."""
+    g = np.random.default_rng(n_q)
+    n = seq0[-1]
+    last = g.integers(-2, cap, (n, n_q))
+    last[0] = -2
+    last[1] = -1
+    last[2, : n_q // 2] = -2
+    last[n - 1] = cap - 1
+    c = Case(B, 8, "bf16", H, hkv, hd, lens, seq0, n_q, cap, last=last)
+    c.run()
+    B.cb_sync(None)
+    c.check()
+    first = c.out.clone()
+    c.ws.fill_(129)
+    c.run()
+    B.cb_sync(None)
+    assert bool((c.out == first).all())
 
 
 @pytest.mark.parametrize("hd", [64, 128])
