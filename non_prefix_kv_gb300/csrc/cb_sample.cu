@@ -15,10 +15,10 @@
 //   k = 1 (or T = 0)      the largest logit's lowest id, found in the pass that finds the largest logit
 //   k up to 1024          that pass keeps the largest of each of 4096 groups of ids; the k-th largest of those is
 //                         no larger than the k-th logit, and few logits above it are not among the k.  These come
-//                         together, in order of their ids, in the first CTA, which sorts them and finishes
+//                         together, in order of their ids, in the first CTA, which puts them into classes and finishes
 //   a least share         is a least logit (a comparison); if few ids reach it they are finished in the same way
-//   p alone               the weights of 2048 classes of (max - l) / T, the border class's ids sorted as above; then
-//                         the kept weight of every tile, and the one tile that holds the draw once more
+//   p alone               the weights of 2048 classes of (max - l) / T, the border class's ids as above; then the
+//                         kept weight of every tile, and the one tile that holds the draw once more
 //   other k, many equals  the same with counts (weights) of the key's leading bits, then of the border class's next
 // Few rows are bound by the chain of passes and of the cluster's meetings, many by the weights (about 30
 // instructions) and the classes' atomics.
