@@ -54,7 +54,8 @@ constexpr int kHeld = 2048;          // (sequence, row tile) pairs whose steps a
 
 struct Tc {
   Shared s;
-  int total, workers;            // key tiles of all prefixes, CTAs that share them
+  int total, workers;            // key tiles of all prefixes, the runs that they are cut into
+  int ctas;                      // that take these runs by turns
   int first[kMaxGroups + 1];     // key tiles before group g
   int prob[kMaxGroups + 1];      // (KV head, row tile) pairs before group g
   int qpt;                       // queries of a row tile: 128 / G
@@ -75,7 +76,7 @@ struct Tc {
   float* own_part;               // [workers + n_seq row_tiles Hkv][rows][hd], m, l
 };
 
-// the CTAs that share a wide call's key tiles: a tile for each group of warps
+// the runs of a wide call's key tiles: a tile for each group of warps
 __device__ __forceinline__ int wide_workers(int total, int workers) { return min(workers, (total + 1) / 2); }
 __device__ __forceinline__ int row_tiles_of(const Tc& w, int g) {
   return ((w.s.seq0[g + 1] - w.s.seq0[g]) * w.s.n_q + w.qpt - 1) / w.qpt;
@@ -268,7 +269,7 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
 // on from the prefix's to the sequence's own, under each row's bound, so that own rows need no kernel of their own;
 // row tiles of padding are left out.  (8 questions of 48 to 96 queries of 56 heads over 16000 rows: 299 us without.)
 // Where sequences do not fill their tiles the prefixes' tiles are packed from a whole group's queries and only the own
-// keys' are a sequence's own (split: 29 of 88 queries of 32 heads over 8204 rows 408 us, 1787 with the own rows' kernel).
+// keys' are a sequence's own (split: 29 of 88 queries of 32 heads over 8204 rows 332 us, 1787 with the own rows' kernel).
 //
 // Barriers of a group: K and V have landed, S and P V are done, P is written.  How far the segments' results have
 // been read (from TMEM, and out of Q's buffer) is a count that the issuing warps look at: they may be ahead by more
@@ -327,8 +328,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   pdl_trigger();                   // (before TMEM is allocated: see tc::kWholeSm)
   if (WIDE && (int)blockIdx.x >= workers) return;
-  const int a = run_start(total, blockIdx.x, workers), b = run_start(total, blockIdx.x + 1, workers);
-  Seg cur = segment<WIDE>(w, wide, a, b);
+  int run = blockIdx.x, b = run_start(total, run + 1, workers);
+  Seg cur = segment<WIDE>(w, wide, run_start(total, run, workers), b);
+  auto next = [&]() -> bool {      // the segment behind cur: of its run, or of the CTA's next one
+    int a = cur.end;
+    if (a >= b) {
+      run += gridDim.x;
+      if (run >= workers) return false;
+      a = run_start(total, run, workers);
+      b = run_start(total, run + 1, workers);
+    }
+    cur = segment<WIDE>(w, wide, a, b);
+    return true;
+  };
   if (warp == 4) {
     tc::tmem_alloc(tmem_slot, TMEM_COLS);
     tc::tmem_relinquish();
@@ -383,8 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
         }
-        if (!ok || cur.end >= b) break;
-        cur = segment<WIDE>(w, wide, cur.end, b);
+        if (!ok || !next()) break;
       }
       if (!ok) {                   // give the copies in flight as long again before the memory is given up
         if (nk > 0) tc::mbar_wait(k_full, (nk - 1) & 1);
@@ -444,8 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           if (!ok) break;
         }
-        if (!ok || cur.end >= b) break;
-        cur = segment<WIDE>(w, wide, cur.end, b);
+        if (!ok || !next()) break;
       }
     }
   } else {
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const float a1 = mb == -INFINITY ? 0.f : tc::ex2_approx(mb - mm);
         // (a sum that is no number counts even though no maximum was found beside it)
         const float lt = (ma == -INFINITY ? xl[r] : xl[r] * a0) + (mb == -INFINITY ? xl[BM + r] : xl[BM + r] * a1);
-        float* out = slot(w.part, w.slot_rows, HD, blockIdx.x, cur.pair);
+        float* out = slot(w.part, w.slot_rows, HD, run, cur.pair);
         if (grp == 0 && r < rows) {
           out[w.slot_rows * HD + r] = isnan(lt) ? lt : mm;
           out[w.slot_rows * (HD + 1) + r] = lt;
@@ -599,8 +609,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         __threadfence_block();
         atomicAdd(read_out, 1);
       }
-      if (cur.end >= b) break;     // (uniform)
-      cur = segment<WIDE>(w, wide, cur.end, b);
+      if (!next()) break;          // (uniform)
     }
   }
   if (!ok && lane == 0) atomicOr(&g_err_shared_tc, ERRBIT_TIMEOUT);
@@ -1093,6 +1102,17 @@ __global__ void __launch_bounds__(256, WIDE ? 5 : 3) k_shared_join(const __grid_
 }
 
 // ---- host --------------------------------------------------------------------------------------
+// How many runs of the line a CTA gets.  All CTAs' first runs come first on the line, so that the heads at work at one
+// time are a part of all, and prefixes that several row tiles read come from L2 after the first.  29 x 88 queries of 32
+// heads over 8204 rows 406 us with one run, 332 with two; 300 x 1 over 8192 180 and 171.  Two row tiles do not pay for
+// the pieces (150 x 1 of 40 heads over 12267 128 and 141), nor do runs of 26 tiles (64 x 24 over 4096 166 and 180).
+int slices(const Shared& s, const Tc& w, double tiles) {               // tiles of a CTA
+  double again = 0;
+  for (int g = 0; g < s.n_groups; ++g)
+    if ((int64_t)(s.seq0[g + 1] - s.seq0[g]) * s.n_q > 2 * w.qpt) again += 4.0 * s.len[g] * s.Hkv * s.hd;
+  return (int)std::max(1.0, std::min({ceil(again / 96e6), tiles / 40, 16.0}));
+}
+
 // what the kernels need beside the call itself; false: too much for one call
 bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
   w->s = s;
@@ -1119,7 +1139,8 @@ bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
     const double most = (double)tiles * s.Hkv * ((longest + BN - 1) / BN + (s.capacity + BN - 1) / BN);
     if (most > INT32_MAX / 2 || (s.H + 7) / 8 > 65535) return false;
     w->total = 0;
-    w->workers = (int)std::min<double>(kWorkers, std::max(1.0, (most + 1) / 2));
+    w->ctas = (int)std::min<double>(kWorkers, std::max(1.0, (most + 1) / 2));
+    w->workers = w->ctas * slices(s, *w, most / w->ctas);
     w->slot_rows = ((w->split ? w->qpt : std::min(s.n_q, w->qpt)) * s.G + 3) & ~3;
     w->own_slot_rows = w->slot_rows;
     w->alone = false;
@@ -1144,7 +1165,7 @@ bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
   w->first[s.n_groups] = (int)at;
   w->prob[s.n_groups] = (int)pairs;
   w->total = (int)at;
-  w->workers = (int)std::min<int64_t>(kWorkers, (at + 1) / 2);          // (a tile for each group of warps)
+  w->ctas = (int)std::min<int64_t>(kWorkers, (at + 1) / 2);             // (a tile for each group of warps)
   w->own_ctas = kOwnCtas;
   if (at > 0 && s.capacity > 0) {
     // The own rows' kernel starts beside the prefixes', on SMs that are left to it, so that one's products and start
@@ -1158,9 +1179,10 @@ bool plan_tc(const Shared& s, Tc* w, size_t* bytes) {
       const double t = std::max((double)at / (kWorkers - x) * unit + 4.0, bytes / (2 * x * 32e3) + 4.0);
       if (t < best) best = t, left = x;
     }
-    w->workers = std::min(w->workers, kWorkers - left);
+    w->ctas = std::min(w->ctas, kWorkers - left);
     w->own_ctas = 2 * left;
   }
+  w->workers = w->ctas * slices(s, *w, (double)at / std::max(1, w->ctas));
   w->slot_rows = (int)((rows + 3) & ~3);
   w->row_tiles = (s.n_q * s.G + TILE - 1) / TILE;
   w->own_slot_rows = (std::min(TILE, s.n_q * s.G) + 3) & ~3;
@@ -1246,13 +1268,13 @@ cudaError_t launch_hd(const Tc& w, cudaStream_t st) {
       return cudaErrorInvalidValue;
     if (!pre) k = v = q;
     if (!own) own_k = own_v = q;
-    e = launch_k(k_shared_prefix<HD, true>, dim3(w.workers), dim3(THREADS), Layout<HD, true>::SMEM, st, q, k, v, own_k, own_v, w);
+    e = launch_k(k_shared_prefix<HD, true>, dim3(w.ctas), dim3(THREADS), Layout<HD, true>::SMEM, st, q, k, v, own_k, own_v, w);
     if (e != cudaSuccess) return e;
     return launch_k(k_shared_join<HD, true>, join, dim3(256), 0, st, w);
   }
   if (w.total > 0) {
     if (!make_map(&k, s.k, {W, s.n_rows}, {64, BN}) || !make_map(&v, s.v, {W, s.n_rows}, {64, BN})) return cudaErrorInvalidValue;
-    e = launch_k(k_shared_prefix<HD, false>, dim3(w.workers), dim3(THREADS), Layout<HD, false>::SMEM, st, q, k, v, k, v, w);
+    e = launch_k(k_shared_prefix<HD, false>, dim3(w.ctas), dim3(THREADS), Layout<HD, false>::SMEM, st, q, k, v, k, v, w);
     if (e != cudaSuccess) return e;
   }
   if (s.capacity > 0) {

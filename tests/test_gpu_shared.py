@@ -365,3 +365,17 @@ def test_short_and_long_prefixes_by_turns(B, hd, n_q):
         c.run()
         assert bool((c.out == first).all())
     B.cb_sync(None)
+
+
+@pytest.mark.parametrize("n_seq,n_q,cap,rows", [(29, 88, 100, [5]), (700, 1, 4, [0, 333, 699])])
+def test_a_prefix_larger_than_the_cache(B, n_seq, n_q, cap, rows):
+    """Several row tiles over 134 MB of keys and values, a part of the heads at a time."""
+    c = Case(B, 14, "bf16", 32, 32, 128, [8204], [0, n_seq], n_q, cap)
+    c.run()
+    B.cb_sync(None)
+    c.check(rows)
+    first = c.out.clone()
+    c.ws.fill_(130)
+    c.run()
+    B.cb_sync(None)
+    assert bool((c.out == first).all())
