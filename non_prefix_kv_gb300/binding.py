@@ -672,7 +672,7 @@ def _strided(what: str, t, dtype, width: int, dev: int):
         ld, one = t.stride()
     except ValueError:
         n, w, ld, one = 0, -1, 0, 0                            # not two dimensions
-    if w != width or one != 1:
+    if w != width or one != 1 or (ld < width and n > 1):       # (expanded rows overlap one another)
         raise ValueError(f"{what}: shape {tuple(t.shape)}, strides {t.stride()}, expected rows of {width} contiguous elements")
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {t.dtype}, expected {dtype}")

@@ -244,7 +244,8 @@ def test_the_binding_refuses_tensors_of_another_kind(lib, fake):
     with pytest.raises(B.CBError, match="overlaps"):
         rows()                                                  # all at one address: that far it gets
     for kw in (dict(q=Tensor(f32, N, QW)), dict(q=Tensor(bf, N - 1, QW)), dict(q=Tensor(bf, N, QW + 1)), dict(q=Tensor(bf, N, QW, dev=1)),
-               dict(q_out=Tensor(bf, N, QW, stride=(QW * 2, 2))), dict(v=Tensor(bf, N + 1, W)), dict(v_out=Tensor(bf, N + 1, W)),
+               dict(q_out=Tensor(bf, N, QW, stride=(QW * 2, 2))), dict(q=Tensor(bf, N, QW, stride=(0, 1))),
+               dict(k_out=Tensor(bf, N, W, stride=(W - 8, 1))), dict(v=Tensor(bf, N + 1, W)), dict(v_out=Tensor(bf, N + 1, W)),
                dict(v_out=Tensor(bf, N, W, stride=(W * 2, 1))), dict(pos=Tensor(t.int64, N)), dict(cos_sin=Tensor(f32, 100 * 64 - 1)),
                dict(src_row=Tensor(i32, N + 1)), dict(kv_row=Tensor(i32, N, dev=1)), dict(k=Tensor(bf, N * W)), dict(k=Tensor(bf, 1, N, W))):
         with pytest.raises((ValueError, IndexError)):
