@@ -11,10 +11,11 @@
 //
 // This file: fp32 rows (exact arithmetic) and head sizes that the tensor-core kernels do not take.  4 rows of 8
 // lanes share a warp, K and then V of 32 keys in shared memory: 6 x 3 queries of 4 heads of 64 over 1000 rows take
-// 12.7 us, most of it two launches and the chain of loads of one piece; a call of many rows is bound by the fp32
+// 11.7 us, most of it two launches and the chain of loads of one piece; a call of many rows is bound by the fp32
 // products, which read a key's value from shared memory for every row.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "cb_shared.cuh"
 
@@ -29,6 +30,10 @@ namespace {
 
 constexpr int kRows = 16, kKeys = 32, kThreads = 128;
 constexpr float kNone = -INFINITY;
+// K and V in buffers of their own, loaded at once: 64 sequences of 8 heads over 4096 rows 97 us for heads of 128 (123
+// with one buffer, V after the scores); of 256, where fewer CTAs then fit an SM, 201 (194).
+template <int HD>
+constexpr bool kBoth = HD <= 128;
 
 // The pieces: first the prefix's (group, KV head, row tile, run of keys), then the own ones (sequence, KV
 // head, row tile, run of keys).  Rows of a tile are consecutive (query, head of the KV head) pairs.
@@ -45,8 +50,9 @@ __global__ void __launch_bounds__(kThreads) k_shared_simt(const __grid_constant_
   constexpr int PAD = 4, LD = HD + PAD, PER = HD / 8;
   extern __shared__ float smem[];
   float* sq = smem;                          // [kRows][LD]
-  float* sk = sq + kRows * LD;               // [kKeys][LD], K and then V
-  float* sp = sk + kKeys * LD;               // [kRows][kKeys + PAD]
+  float* sk = sq + kRows * LD;               // [kKeys][LD]
+  float* sv = kBoth<HD> ? sk + kKeys * LD : sk;          // [kKeys][LD]
+  float* sp = sv + kKeys * LD;               // [kRows][kKeys + PAD]
   __shared__ int s_last[kRows];
   const int tid = threadIdx.x, r = tid >> 3, c = tid & 7;
   pdl_wait();
@@ -124,16 +130,21 @@ __global__ void __launch_bounds__(kThreads) k_shared_simt(const __grid_constant_
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
   for (int j0 = 0; j0 < keys; j0 += kKeys) {
-    auto rows_of = [&](const T* x) {         // keys past the last one that is seen are not read
+    __syncthreads();
+    auto rows_of = [&](auto with_k, auto with_v) {       // keys past the last one that is seen are not read
       for (int i = tid; i < kKeys * (HD / 4); i += kThreads) {
         const int j = i / (HD / 4), at = i % (HD / 4) * 4;
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        if (j0 + j < keys) ld4(x + (int64_t)(key0 + j0 + j) * W + h * HD + at, f);
-        *reinterpret_cast<float4*>(sk + j * LD + at) = make_float4(f[0], f[1], f[2], f[3]);
+        float f[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
+        if (j0 + j < keys) {
+          const int64_t from = (int64_t)(key0 + j0 + j) * W + h * HD + at;
+          if (with_k) ld4(k + from, f);
+          if (with_v) ld4(v + from, e);
+        }
+        if (with_k) *reinterpret_cast<float4*>(sk + j * LD + at) = make_float4(f[0], f[1], f[2], f[3]);
+        if (with_v) *reinterpret_cast<float4*>(sv + j * LD + at) = make_float4(e[0], e[1], e[2], e[3]);
       }
     };
-    __syncthreads();
-    rows_of(k);
+    rows_of(std::true_type{}, std::bool_constant<kBoth<HD>>{});
     __syncthreads();
     // scores of keys c, c + 8, c + 16, c + 24
     float z[4] = {0.f, 0.f, 0.f, 0.f};
@@ -165,15 +176,18 @@ __global__ void __launch_bounds__(kThreads) k_shared_simt(const __grid_constant_
       l += e;
       sp[r * (kKeys + PAD) + c + 8 * q] = e;
     }
-    __syncthreads();
-    rows_of(v);
-    __syncthreads();
+    if (!kBoth<HD>) {
+      __syncthreads();
+      rows_of(std::false_type{}, std::true_type{});
+      __syncthreads();
+    }
+    __syncwarp();                            // (a row's weights are its warp's)
 #pragma unroll 4
     for (int j = 0; j < kKeys; ++j) {
       const float e = sp[r * (kKeys + PAD) + j];
 #pragma unroll
       for (int i = 0; i < PER; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(sk + j * LD + i * 8 + c * 4);
+        const float4 x = *reinterpret_cast<const float4*>(sv + j * LD + i * 8 + c * 4);
         o[i] = fmaf(e, x.x, o[i]);
         o[i + 1] = fmaf(e, x.y, o[i + 1]);
         o[i + 2] = fmaf(e, x.z, o[i + 2]);
@@ -207,9 +221,9 @@ __global__ void __launch_bounds__(256) k_shared_join_simt(const __grid_constant_
   const int a = last >= -1 ? (p.len[g] + w.chunk - 1) / w.chunk : 0, b = last >= 0 ? last / w.own_chunk + 1 : 0;
   const float* part = w.part + row * (w.n_chunk + w.n_own) * (HD + 2);
   auto piece = [&](int i) { return part + (int64_t)(i < a ? i : w.n_chunk + i - a) * (HD + 2); };
-  // eight pieces at a time, statistics and rows in one go, each batch joined to what came before it (one piece
-  // after the other 6 x 3 queries of 4 heads over 1000 rows took 29 us)
-  constexpr int BATCH = 8, PER = HD / 32;
+  // sixteen (eight) pieces at a time, statistics and rows in one go, each batch joined to what came before it (one
+  // piece after the other 6 x 3 queries of 4 heads over 1000 rows took 29 us)
+  constexpr int PER = HD / 32, BATCH = PER <= 4 ? 16 : 8;
   float M = kNone, L = 0.f, o[PER];
 #pragma unroll
   for (int q = 0; q < PER; ++q) o[q] = 0.f;
@@ -278,7 +292,7 @@ bool cut(const Shared& p, Pieces* w) {
 template <typename T, int HD>
 cudaError_t launch_hd(const Shared& p, const Pieces& w, cudaStream_t s) {
   const int64_t n = w.first[p.n_groups] + (int64_t)w.own_tiles * p.Hkv * p.n_seq * w.n_own;
-  const size_t smem = ((kRows + kKeys) * (HD + 4) + kRows * (kKeys + 4)) * sizeof(float);
+  const size_t smem = ((kRows + (kBoth<HD> ? 2 : 1) * kKeys) * (HD + 4) + kRows * (kKeys + 4)) * sizeof(float);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k_shared_simt<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
