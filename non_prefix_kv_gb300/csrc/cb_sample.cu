@@ -1134,13 +1134,13 @@ cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, con
   g_used_sample = true;
   Args a{token, logprob, kept, u, r, vocab, 0, vocab % 8 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0};
   const int tiles = (vocab + kTile - 1) / kTile;
-  // As many CTAs as run at once (two an SM) with a tile for every warp, but no more than 192 tiles for one of them (rows
-  // differ in what they ask for) unless that would be more than six rounds.  8, 4, 2, 1 a row: one row of 32000 ids 11.9,
-  // 12.4, 15.0, 15.6 us; 256 of them 108, 69, 55, 53; 64 of 64000 41.8, 40.1, 57, 79; 400 194, 129, 107, 123; 256 of
-  // 131072 192, 152, 158, 241; 800 534, 375, 327, 353.
+  // As many CTAs as run at once (two an SM) with a tile for every warp, but two a row up to 304 rows: rows differ in
+  // what they ask for, and the slowest counts.  8, 4, 2, 1 a row: one row of 32000 ids 11.9, 12.4, 15.0, 15.6 us; 64 of
+  // 64000, some with a share alone, 41.8, 40.1, 57, 79; 256 of 131072 by different rules 192, 152, 158, 241, but all by
+  // k = 50 and a share -, 68, 51, 36, and 400 of 64000 by these -, 85, 61, 40.
   int nc = kMaxCluster;
   while (nc > 1 && tiles <= nc / 2 * kMaxTiles &&
-         (((int64_t)nc * n_rows > 304 && (tiles <= nc / 2 * 192 || (int64_t)nc * n_rows > 6 * 304)) || tiles < nc / 2 * kWarps))
+         ((int64_t)(nc > 2 ? nc : 1) * n_rows > 304 || tiles < nc / 2 * kWarps))
     nc /= 2;
   a.tpc = (tiles + nc - 1) / nc;
   return dt == DT_BF16 ? launch_t<bf16>(logits, n_rows, a, nc, s) : launch_t<float>(logits, n_rows, a, nc, s);
