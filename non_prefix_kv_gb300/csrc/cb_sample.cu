@@ -96,6 +96,7 @@ struct Shared {
   uint32_t cutoff, border;
   float least;
   double least_off;      // T ln of the least share
+  float near_off;        // the same in fp32 (that conversion by all threads took 2 us)
 };
 
 // order of values as order of unsigned integers; bf16 values use the upper half
@@ -771,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
   const int all_tiles = (a.vocab + kTile - 1) / kTile;
   R.tile0 = R.rank * a.tpc;
   R.tiles = max(0, min(a.tpc, all_tiles - R.tile0));
+  if (tid == 0) sh.members = 0;
   R.meet();                                  // every CTA of the cluster runs before its memory is written
   pdl_wait();
   pdl_trigger();
@@ -798,7 +800,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
   r.u = fraction(u);
   r.heat = heat > 0.0f ? heat : 1.0f;
   const bool grouped = r.k > 1 && r.k <= kSmallK;
-  if (mp > 0.0f && tid == kThreads - 32) sh.least_off = (double)r.heat * log(fmin((double)mp, 1.0));
+  if (mp > 0.0f && tid == kThreads - 32) {
+    sh.least_off = (double)r.heat * log(fmin((double)mp, 1.0));
+    sh.near_off = (float)sh.least_off;
+  }
 
   // ---- the largest logit, how many there are, and the largest of each group
   float top[8];
@@ -894,6 +899,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
   heat_parts(r.heat, R.heat);
   if (tid == 0) sh.least = mp > 0.0f ? __double2float_ru((double)mx + sh.least_off) : -INFINITY;
   if (r.k >= n) r.k = 0xffffffffu;
+  if (r.k > n && mp > 0.0f && r.p_on) {      // how many groups reach the least share, about
+    const float near = mx + sh.near_off;
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c += top[i] >= near;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) atomicAdd(&sh.members, c);
+  }
   R.meet();                                  // what the CTAs told one another has been read
   r.least = sh.least;
 
@@ -912,7 +925,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const T* __restrict__ lo
       return;
     }
   }
-  if (r.k > n && mp > 0.0f) {
+  // (more groups than 1500 would be more ids than a list takes, and the weights of all ids are not worth the attempt: 256
+  // rows of 131072, some so, 159 us with it, 126 without)
+  uint32_t reach = 0;
+  if (r.k > n && mp > 0.0f && r.p_on)
+    for (int q = 0; q < R.nc; ++q) reach += R.at(q)->members;
+  if (r.k > n && mp > 0.0f && reach <= 1500) {
     u64 all = 0;
     auto take = [&](float v) { return v >= r.least && v > -INFINITY; };
     const uint32_t held = r.p_on ? R.template gather<true>(take, &all) : R.template gather<false>(take, nullptr);
@@ -1136,8 +1154,9 @@ cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, con
   const int tiles = (vocab + kTile - 1) / kTile;
   // As many CTAs as run at once (two an SM) with a tile for every warp, but two a row up to 304 rows: rows differ in
   // what they ask for, and the slowest counts.  8, 4, 2, 1 a row: one row of 32000 ids 11.9, 12.4, 15.0, 15.6 us; 64 of
-  // 64000, some with a share alone, 41.8, 40.1, 57, 79; 256 of 131072 by different rules 192, 152, 158, 241, but all by
-  // k = 50 and a share -, 68, 51, 36, and 400 of 64000 by these -, 85, 61, 40.
+  // 64000, some with a share alone, 41.8, 40.1, 57, 79; 256 of 131072 by different rules 192, 152, 158, 241 (the last
+  // three before some of them skipped the list of a least share), but all by k = 50 and a share -, 68, 51, 36, and 400 of
+  // 64000 by these -, 85, 61, 40.
   int nc = kMaxCluster;
   while (nc > 1 && tiles <= nc / 2 * kMaxTiles &&
          ((int64_t)(nc > 2 ? nc : 1) * n_rows > 304 || tiles < nc / 2 * kWarps))
