@@ -1153,10 +1153,9 @@ cudaError_t launch_sample(int dt, const void* logits, int n_rows, int vocab, con
   Args a{token, logprob, kept, u, r, vocab, 0, vocab % 8 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0};
   const int tiles = (vocab + kTile - 1) / kTile;
   // As many CTAs as run at once (two an SM) with a tile for every warp, but two a row up to 304 rows: rows differ in
-  // what they ask for, and the slowest counts.  8, 4, 2, 1 a row: one row of 32000 ids 11.9, 12.4, 15.0, 15.6 us; 64 of
-  // 64000, some with a share alone, 41.8, 40.1, 57, 79; 256 of 131072 by different rules 192, 152, 158, 241 (the last
-  // three before some of them skipped the list of a least share), but all by k = 50 and a share -, 68, 51, 36, and 400 of
-  // 64000 by these -, 85, 61, 40.
+  // what they ask for, and the slowest counts.  8, 4, 2, 1 a row: one row of 32000 ids 12.0, 12.6, 14.8, 15.3 us; 64 of
+  // 64000, some with a share alone, 42.9, 37.3, 48, 68; 256 of 131072 by different rules 173, 131, 126, 181, all by k = 50
+  // and a share -, 68, 51, 36; 400 of 64000 by these -, 85, 61, 40.
   int nc = kMaxCluster;
   while (nc > 1 && tiles <= nc / 2 * kMaxTiles &&
          ((int64_t)(nc > 2 ? nc : 1) * n_rows > 304 || tiles < nc / 2 * kWarps))
