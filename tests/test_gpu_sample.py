@@ -262,3 +262,18 @@ def test_captured_after_the_logit_rules(B):
         for b in range(n):
             w = A.sample(out[b].double().cpu().numpy(), float(u[b]), float(np.float32(0.8)), 0, float(np.float32(0.9)))
             assert (int(tok[b]), int(kept[b])) == (w[0], w[2]) and w[3] > 2.0 ** -28
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5000, 40000])
+def test_a_least_share_that_many_or_few_reach(B, dtype, V):
+    """With a share of the weight beside it, from a handful of ids to all of them, by way of about as many as a list takes.
+    (Of more ids than these some weight is always too near the least share for the oracle.)"""
+    g = np.random.default_rng(V)
+    n = 8
+    x = g.standard_normal((n, V)) * np.array([0.02, 0.2, 0.5, 0.8, 1.1, 1.4, 2.0, 3.0])[:, None]
+    x[::3, ::2] = -np.inf
+    u = g.random(n)
+    for m in (0.3, 0.05, 0.005):
+        check(B, x, u, p=np.full(n, 0.93), m=np.full(n, m), dtype=dtype)
+        check(B, x, u, T=np.linspace(0.6, 1.4, n), p=np.linspace(0.3, 0.99, n), m=np.full(n, m), dtype=dtype)
